@@ -126,6 +126,21 @@ int check_common(int type, const void* W, int64_t rows, int64_t K, Nvfp4View* nv
 
 }  // namespace
 
+int* device_error_word() { return error_word(); }
+
+cudaError_t opt_in_smem(const void* kernel, int bytes) {
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, int> done;
+    const int dev = current_device();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    int& have = done[{kernel, dev}];
+    if (have >= bytes) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) have = bytes;
+    return e;
+}
+
 int device_sm_count() {
     static std::atomic<int> counts[kMaxDevices];
     const int dev = current_device();
@@ -161,10 +176,15 @@ EncodeFn tensor_map_encoder() {
 
 bool encode_u32_map(CUtensorMap* map, const void* base, int64_t rows, int64_t row_u32, int box_x, int box_y,
                     bool swizzle_128b) {
+    return encode_u32_map_pitch(map, base, rows, row_u32, row_u32 * 4, box_x, box_y, swizzle_128b);
+}
+
+bool encode_u32_map_pitch(CUtensorMap* map, const void* base, int64_t rows, int64_t row_u32, int64_t pitch_bytes,
+                          int box_x, int box_y, bool swizzle_128b) {
     EncodeFn enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_u32), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_u32 * 4)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch_bytes)};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_y)};
     const cuuint32_t estr[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,

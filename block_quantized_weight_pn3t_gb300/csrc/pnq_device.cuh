@@ -278,6 +278,13 @@ __device__ __forceinline__ uint32_t f32x2_to_f16x2(float a, float b) {
     return d;
 }
 
+// Two floats -> bf16x2 (low half = a), rounded to nearest even.
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float a, float b) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+}
+
 // Packed fp32 pairs (two lanes in one 64-bit register; sm_100 family), round to nearest even;
 // explicit .rn operations are never contracted into fused multiply-adds.
 __device__ __forceinline__ uint64_t f32x2_pack(float lo, float hi) {

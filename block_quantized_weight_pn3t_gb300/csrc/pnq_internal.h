@@ -28,6 +28,12 @@ struct GroupedOut {
 
 int device_sm_count();
 
+// Device address of the library's error word on the current device (pnq_device_error reads it).
+int* device_error_word();
+
+// Raises a kernel's dynamic shared memory limit to `bytes`, once per (kernel, device).
+cudaError_t opt_in_smem(const void* kernel, int bytes);
+
 // 2-D tensor map over a row-major u32 matrix [rows][row_u32] (row pitch a multiple of 16
 // bytes) with box {box_x, box_y}; rows past the end read as zeros. swizzle_128b: the copy
 // stores 16-byte chunk c of box row r at chunk c ^ (r % 8) of that row (box rows of 128 bytes,
@@ -35,6 +41,10 @@ int device_sm_count();
 // encoder rejects the arguments.
 bool encode_u32_map(CUtensorMap* map, const void* base, int64_t rows, int64_t row_u32, int box_x, int box_y,
                     bool swizzle_128b = false);
+
+// The same for rows of row_u32 words that start every pitch_bytes bytes (a multiple of 16).
+bool encode_u32_map_pitch(CUtensorMap* map, const void* base, int64_t rows, int64_t row_u32, int64_t pitch_bytes,
+                          int box_x, int box_y, bool swizzle_128b);
 
 cudaError_t launch_pn_dequant(int type, const uint8_t* W, int64_t n_rows, int64_t K, float* out,
                               cudaStream_t stream);
@@ -94,5 +104,51 @@ cudaError_t launch_pn_gemv_mma(int type, const uint8_t* W, int64_t N, int64_t K,
 cudaError_t launch_nvfp4_gemv_mma(const Nvfp4View& w, int64_t N, int64_t K, const uint16_t* X, int M,
                                   float* Y, int* err, int cluster, int stages, bool static_weights,
                                   cudaStream_t stream);
+
+// ---- expert layer (pnq_experts.cu) ------------------------------------------------------------
+
+// pnq_expert_plan of the C ABI (all pointers device); no plan: tokens = rows, experts = 0.
+struct PlanView {
+    int32_t* offsets = nullptr;
+    int32_t* block_start = nullptr;
+    int32_t* order = nullptr;
+    int32_t* position = nullptr;
+    int32_t* scale_row = nullptr;
+    int64_t tokens = 0;
+    int slots = 1;
+    int experts = 0;
+};
+
+enum class ExpertOp { Gather, GatherBackward, Combine, CombineBackward };
+
+cudaError_t launch_expert_sort(const int32_t* ids, const PlanView& p, cudaStream_t stream);
+// a, b: input rows (b: CombineBackward's YS); weights, dweights where the operator has them.
+cudaError_t launch_expert_rows(ExpertOp op, bool bf16, const void* a, const void* b, int64_t D, const PlanView& p,
+                               const float* weights, void* out, float* dweights, cudaStream_t stream);
+
+// ---- 4-bit microscaled operands (layout: include/pnq.h) -----------------------------------------
+
+struct Fp4View {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int64_t rows;      // of one matrix
+    int64_t matrices;
+};
+
+inline int64_t fp4_pitch(int64_t K) { return (K / 2 + 15) / 16 * 16; }
+inline int64_t fp4_chunks(bool mx, int64_t K) { return mx ? (K + 127) / 128 : (K + 63) / 64; }
+
+cudaError_t launch_fp4_quantize(bool mx, bool bf16, const void* X, int64_t ldx, int64_t rows, int64_t K,
+                                int64_t matrices, float inv_g, const PlanView& p, uint8_t* codes, uint8_t* scales,
+                                cudaStream_t stream);
+cudaError_t launch_fp4_dequantize(bool mx, const Fp4View& v, int64_t K, float g, const PlanView& p, bool bf16, void* out,
+                                  cudaStream_t stream);
+cudaError_t launch_fp4_pack(bool mx, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
+                            int64_t matrices, uint8_t* codes_out, uint8_t* scales_out, cudaStream_t stream);
+
+// Y = alpha X W^T (p.experts == 0), or by experts with p (x: its sorted rows).
+cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t K, const PlanView& p, float alpha,
+                            const float* w_global, bool bf16, void* Y, int* err, bool static_weights,
+                            cudaStream_t stream);
 
 }  // namespace pnq

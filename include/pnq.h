@@ -48,6 +48,10 @@
  *       scales  [N][ceil(K / G)] binary16 words.
  *     Alignment: lo 8 bytes (W8) or 4 bytes, hi 2 bytes, scales 2 bytes (else PNQ_ERR_ALIGN).
  *
+ *   PNQ_MXFP4 (1006, a library id): E2M1 codes as in NVFP4 with one power-of-two scale per 32
+ *     weights along K (a biased exponent byte b: 2^(b - 127), 255 = NaN) and a global multiplier
+ *     (usually 1). Taken by the pnq_fp4_* calls only; their operand layout is described there.
+ *
  * Fast paths (taken automatically, never required)
  *   PN: W and X 16-byte aligned and (K/BLK) % 8 == 0.  NVFP4: codes, scales and X 16-byte
  *   aligned and K % 256 == 0. Other layouts run a slower (generic) path within the same
@@ -69,6 +73,7 @@ enum pnq_type {
     PNQ_PN4T = 125,
     PNQ_NVFP4 = 1004,
     PNQ_NVFP4_DIV = 1005,
+    PNQ_MXFP4 = 1006,
     PNQ_Q4G64_F16S = 1104,
     PNQ_Q5G64_F16S = 1105,
     PNQ_Q6G64_F16S = 1106,
@@ -281,6 +286,137 @@ int pnq_device_error(int32_t* code);
  * call.)
  */
 int pnq_selftest_wait(uint32_t limit_us, cudaStream_t stream);
+
+/* ---- 4-bit microscaled operands: quantisation and product --------------------------------------
+ *
+ * Operand layout (type PNQ_NVFP4: groups of G = 16; PNQ_MXFP4: G = 32; K % G == 0; pnq_fp4_layout
+ * gives the sizes). An operand holds `matrices` matrices of `rows` x K (activations: one; the
+ * weights of an expert layer: one per expert).
+ *   codes   [matrices * rows][pitch] bytes, two E2M1 codes per byte, low nibble = even k, pitch =
+ *           K / 2 rounded up to 16 (bytes past K / 2 are never read). 16-byte aligned.
+ *   scales  tiles of 128 rows x 4 groups, 512 bytes each: the word of row r (0..127), group j
+ *           (0..3) at byte 16 (r % 32) + 4 (r / 32) + j. Tiles of one 128-row block follow each
+ *           other along K (ceil(K / (4 G)) of them); every matrix starts a new block; words of
+ *           groups past K are zero. 16-byte aligned. NVFP4 words are E4M3FN, MXFP4 words biased
+ *           exponents.
+ *   global  one fp32 multiplier g: a value is e2m1 * scale * g.
+ * Operands made with an expert plan hold the plan's sorted rows: codes row i is sorted row i, its
+ * scales are at tiled row scale_row[i] (each expert's rows start a new 128-row block).
+ */
+
+/* Element types of activations, expert rows and products. */
+enum pnq_float { PNQ_F32 = 0, PNQ_BF16 = 1 };
+
+/* How the rows of an expert layer are sorted: device int32 arrays, filled by pnq_expert_sort. Passed
+ * by HOST pointer. n = tokens * slots is the number of (token, slot) choices; slot number t * slots
+ * + j is token t's j-th choice. */
+typedef struct pnq_expert_plan {
+    int32_t* offsets;      /* [experts + 1] first sorted row of each expert; the last: rows in use */
+    int32_t* block_start;  /* [experts + 1] first 128-row scale block of each expert */
+    int32_t* order;        /* [n] slot number of each sorted row, -1 past the rows in use */
+    int32_t* position;     /* [n] sorted row of each slot, -1 for a dropped one */
+    int32_t* scale_row;    /* [n] row of each sorted row in the tiled scales, -1 past the rows in use */
+    int64_t tokens;
+    int32_t slots;         /* choices per token, 1..64 */
+    int32_t experts;       /* 1..1024 */
+} pnq_expert_plan;
+
+/* Sizes of an operand: the codes' row pitch and the bytes of the tiled scales. With an expert plan,
+ * pass plan_experts = the plan's experts and rows = its tokens * slots (matrices = 1): the bytes
+ * then hold any distribution of the rows. plan_experts = 0 otherwise. Returns PNQ_OK, PNQ_ERR_TYPE,
+ * PNQ_ERR_SHAPE or PNQ_ERR_NULL. */
+int pnq_fp4_layout(int type, int64_t rows, int64_t K, int64_t matrices, int64_t plan_experts, uint64_t* pitch,
+                   uint64_t* scale_bytes);
+
+/*
+ * pnq_fp4_quantize -- encode matrices * rows rows of K values (X device, fp32 or bf16, row r at X + r *
+ * ldx elements) for the global multiplier g. Per element y = fp32(x * fp32(1 / g)); per group
+ *   NVFP4: scale = E4M3FN(fp32(amax |y| / 6)), nearest, ties to even, saturating at 448;
+ *   MXFP4: scale = 2^(floor(log2(amax |y|)) - 2), at least 2^-127 (also the scale of a zero group);
+ * code = the E2M1 value nearest to y / scale, ties to even, saturating at 6, sign of y; a zero scale has
+ * zero codes. A group with a NaN or an infinite y gets a NaN scale and zero codes: its values, and every
+ * product over it, are NaN. Rows of other groups and matrices are not touched.
+ *   plan  NULL, or an expert plan: X holds plan->tokens rows (rows = tokens, matrices = 1), each is
+ *         encoded once and written to the sorted rows of its slots.
+ * X element-aligned (16-byte aligned rows are faster); codes and scales 16-byte aligned. Errors:
+ * PNQ_ERR_TYPE (format or element type), PNQ_ERR_SHAPE, PNQ_ERR_NULL, PNQ_ERR_ALIGN, PNQ_ERR_VALUE (g not
+ * finite and > 0, or 1 / g not finite), PNQ_ERR_CUDA.
+ */
+int pnq_fp4_quantize(int type, int x_type, const void* X, int64_t ldx, int64_t rows, int64_t K, int64_t matrices,
+                     float global_scale, const pnq_expert_plan* plan, uint8_t* codes, uint8_t* scales,
+                     cudaStream_t stream);
+
+/*
+ * pnq_fp4_dequantize -- out[r][k] = fp32(e2m1 * scale * g) (the first product is exact), rounded once more
+ * to nearest even for a bf16 out. out: [matrices * rows][K] contiguous, element-aligned. With a plan:
+ * rows = tokens * slots sorted rows; rows past the rows in use are written as zeros.
+ */
+int pnq_fp4_dequantize(int type, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
+                       int64_t matrices, float global_scale, const pnq_expert_plan* plan, int out_type, void* out,
+                       cudaStream_t stream);
+
+/*
+ * pnq_fp4_pack -- lay out row-major weights (codes [matrices * rows][K / 2], scale words [matrices *
+ * rows][K / G], as pnq_gemv takes NVFP4) as an operand, once, when they are loaded. Words are copied
+ * as they are. codes_out == codes is allowed where K % 32 == 0 (the codes then stay in place).
+ */
+int pnq_fp4_pack(int type, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, int64_t matrices,
+                 uint8_t* codes_out, uint8_t* scales_out, cudaStream_t stream);
+
+/*
+ * pnq_fp4_gemm -- Y[m][n] = alpha * sum_k X[m][k] W[n][k] over the codes and scales (global multipliers
+ * go into alpha: g_x * g_w), on the 4-bit tensor cores with fp32 accumulation. X: M rows, W: N
+ * rows, one matrix each. Y: [M][N] fp32 or bf16 (one rounding), contiguous, element-aligned. flags:
+ * PNQ_GEMV_STATIC_WEIGHTS as for pnq_gemv_ex. M, N >= 0; a zero one launches nothing. The library
+ * allocates nothing. Accuracy (fp32 Y, finite inputs): |Y - Y_exact| <= 1e-5 * sum_k |X W| * |alpha| +
+ * 1e-6 * |alpha|.
+ */
+int pnq_fp4_gemm(int type, const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, const uint8_t* w_codes,
+                 const uint8_t* w_scales, int64_t N, int64_t K, float alpha, int y_type, void* Y, unsigned int flags,
+                 cudaStream_t stream);
+
+/*
+ * pnq_fp4_gemm_experts -- the product of an expert layer: Y[i] = alpha * w_global[e] * X[i] W_e^T for every
+ * sorted row i of expert e. X: the operand pnq_fp4_quantize made with the same plan; W: experts
+ * matrices of N x K; w_global: device fp32 [experts], or NULL (all 1). Y: [tokens * slots][N]; rows past
+ * the rows in use are written as zeros. An expert without rows is not read.
+ */
+int pnq_fp4_gemm_experts(int type, const uint8_t* x_codes, const uint8_t* x_scales, const pnq_expert_plan* plan,
+                         const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int64_t K, float alpha,
+                         const float* w_global, int y_type, void* Y, unsigned int flags, cudaStream_t stream);
+
+/* ---- tokens to their experts and back ----------------------------------------------------------- */
+
+/*
+ * pnq_expert_sort -- fill a plan from ids (device int32 [tokens][slots], the expert of each choice): the
+ * sorted rows run by expert, and by slot number within one (stable). A choice whose id is outside 0 ..
+ * experts - 1 is dropped. tokens may be 0. Errors: PNQ_ERR_SHAPE (slots, experts, or tokens * slots over
+ * 2^30), PNQ_ERR_NULL, PNQ_ERR_ALIGN (4 bytes), PNQ_ERR_CUDA.
+ */
+int pnq_expert_sort(const int32_t* ids, const pnq_expert_plan* plan, cudaStream_t stream);
+
+/*
+ * pnq_expert_gather -- XS[i] = X[token of sorted row i] (X [tokens][D], XS [tokens * slots][D], fp32 or bf16,
+ * contiguous, element-aligned; 16-byte aligned rows are faster); rows past the rows in use are zeros.
+ * pnq_expert_gather_backward -- its gradient: dX[t] = sum over t's slots of dXS[position], in fp32, in
+ * slot order, rounded once; a token without rows gets zeros.
+ */
+int pnq_expert_gather(int type, const void* X, int64_t D, const pnq_expert_plan* plan, void* XS, cudaStream_t stream);
+int pnq_expert_gather_backward(int type, const void* dXS, int64_t D, const pnq_expert_plan* plan, void* dX,
+                               cudaStream_t stream);
+
+/*
+ * pnq_expert_combine -- Y[t] = sum over t's slots j of weights[t][j] * YS[position] (weights device fp32
+ * [tokens][slots]; YS [tokens * slots][D], Y [tokens][D]), in fp32, in slot order, rounded once. The rows
+ * and weights of dropped slots are not read.
+ * pnq_expert_combine_backward -- its gradients: dYS[i] = weights * dY[token] for every sorted row (rows past the
+ * rows in use are zeros), dWeights[t][j] = <dY[t], YS[position]> in fp32 (0 for a dropped slot). dWeights
+ * may be NULL.
+ */
+int pnq_expert_combine(int type, const void* YS, int64_t D, const pnq_expert_plan* plan, const float* weights, void* Y,
+                       cudaStream_t stream);
+int pnq_expert_combine_backward(int type, const void* dY, const void* YS, int64_t D, const pnq_expert_plan* plan,
+                                const float* weights, void* dYS, float* dWeights, cudaStream_t stream);
 
 /* Library version string (static storage). */
 const char* pnq_version(void);
