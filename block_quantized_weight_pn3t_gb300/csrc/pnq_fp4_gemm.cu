@@ -22,6 +22,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 
 #include "pnq_device.cuh"
 #include "pnq_internal.h"
@@ -34,10 +35,12 @@ constexpr int kStageK = 256;                   // K per stage: 128 bytes of code
 constexpr int kStageWords = kStageK / 8;       // the same in u32 words
 constexpr int kCodesA = kRows * kStageK / 2;   // 16 KB
 constexpr int kScaleTile = 512;                // 128 rows x 4 groups
-constexpr int kThreads = 192;                  // producer, MMA, four epilogue warps
-constexpr int kEpilogueThreads = 128;
+constexpr int kEpilogueWarps = 8;              // two per lane quarter of tensor memory
+constexpr int kEpilogueThreads = 32 * kEpilogueWarps;
+constexpr int kThreads = 64 + kEpilogueThreads;  // producer, MMA, epilogue
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxStages = 10;
+constexpr int kScaleSets = 2;                  // sets of scale columns in tensor memory
 constexpr int kSmemLimit = 227 * 1024;
 
 struct GemmArgs {
@@ -49,6 +52,7 @@ struct GemmArgs {
     int M, N, K;             // activation rows, weight rows of a matrix, K
     int chunks;              // scale tiles along K per 128-row block
     int S;                   // stages
+    int ks;                  // CTAs of a cluster that share a tile's K (1: none)
 };
 
 template <bool MX, int BN>
@@ -61,8 +65,8 @@ struct Plan {
     static constexpr int kAcc = BN <= 128 ? 2 : 1;               // accumulators
     // tensor-memory columns: accumulators, then two sets of scale columns (A: 4 per tile, B: 4 per tile and block)
     static constexpr int kSetCols = 4 * kTiles * (1 + kBlocksB);
-    static constexpr int kUsed = kAcc * BN + 2 * kSetCols;
-    static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    static constexpr int kUsed = kAcc * BN + kScaleSets * kSetCols;
+    static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     // E2M1 operands, scale type, N, M = 128
     static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(BN >> 3) << 17) |
                                        ((MX ? 1u : 0u) << 23) | (static_cast<uint32_t>(kRows >> 4) << 24);
@@ -144,6 +148,13 @@ struct Walk {
     }
 };
 
+// f * scale of one accumulator column -> y, n consecutive across the warp.
+template <class T>
+__device__ __forceinline__ void store_y(T* y, float f) {
+    if constexpr (sizeof(T) == 4) *y = f;
+    else *y = __float2bfloat16_rn(f);
+}
+
 template <bool MX, int BN, class T>
 __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
                                                                const __grid_constant__ CUtensorMap map_ws,
@@ -164,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     auto acc_empty = [&](int i) { return b0 + 8u * (2 * kMaxStages + 2 + i); };
     const uint32_t finished = b0 + 8u * (2 * kMaxStages + 4);
     const int S = a.S, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto stage = [&](int s) { return smem_addr(base) + static_cast<uint32_t>(s * P::kStage); };
+    const uint32_t sbase = smem_addr(base);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -173,12 +184,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full(i), 1);
-            mbar_init(acc_empty(i), kEpilogueThreads / 32);
+            mbar_init(acc_empty(i), kEpilogueWarps);
         }
         mbar_init(finished, 1);
         mbar_fence_init();
     }
     if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), P::kCols);
+    griddep_wait();  // nothing above reads what an earlier kernel wrote
     if (a.p.experts > 0) {
         // tiles before each expert: a block scan, each thread over consecutive experts
         const int E = a.p.experts, nt = (a.N + kRows - 1) / kRows, per = (E + kThreads - 1) / kThreads;
@@ -204,28 +216,35 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    griddep_launch_dependents();
     const uint32_t tmem = tmem_slot;
-    const int nk = (a.K + kStageK - 1) / kStageK;
+    // this CTA's share of the stages along K: [kt0, kt1)
+    const int nk = (a.K + kStageK - 1) / kStageK, kz = static_cast<int>(blockIdx.y);
+    const int kt0 = kz * nk / a.ks, kt1 = (kz + 1) * nk / a.ks;
     Walk<BN> walk(a, starts);
-    Tile tile;
+    Tile tile{};
+    bool any = false;  // this CTA had a tile (the same in all its threads)
 
+    // Warps 0 and 1 run their loops converged, one elected lane issues: the waits are the whole warp's, and
+    // everything the asynchronous instructions take is warp-uniform.
     if (warp == 0) {
-        if (lane == 0) {
-            // one pass over the weights of a tile row: keep the activations in L2, let the weights go first
-            const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
-            const int blocks_w = (a.N + 127) / 128;
-            bool ok = true;
-            int i = 0;
-            while (ok && walk.next(tile)) {
-                const int wrow = tile.e * a.N + tile.n0;
-                const int wsc = (tile.e * blocks_w + tile.n0 / 128) * a.chunks, xsc = tile.sblock * a.chunks;
-                for (int kt = 0; kt < nk; ++kt, ++i) {
-                    const int s = i % S;
-                    if (i >= S && !mbar_wait_bounded(empty(s), ((i / S) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t st = stage(s), sc = st + kCodesA + P::kCodesB;
+        // one pass over the weights of a tile row: keep the activations in L2, let the weights go first
+        const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
+        const int blocks_w = (a.N + 127) / 128;
+        bool ok = true;
+        int s = 0, issued = 0;
+        uint32_t phase = 1;  // the first wait for each free stage passes
+        while (ok && walk.next(tile)) {
+            any = true;
+            const int wrow = tile.e * a.N + tile.n0;
+            const int wsc = (tile.e * blocks_w + tile.n0 / 128) * a.chunks, xsc = tile.sblock * a.chunks;
+            for (int kt = kt0; kt < kt1; ++kt) {
+                if (!__all_sync(0xffffffffu, mbar_wait_cycles(empty(s), phase))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage), sc = st + kCodesA + P::kCodesB;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(full(s), P::kStage);
                     tma_load_2d(st, &map_w, kt * kStageWords, wrow, full(s), pol_w);
                     tma_load_2d(sc, &map_ws, 0, wsc + kt * P::kTiles, full(s), pol_w);
@@ -234,112 +253,155 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                     for (int b = 0; b < P::kBlocksB; ++b)
                         tma_load_2d(sc + P::kScalesA * (1 + b), &map_xs, 0, xsc + b * a.chunks + kt * P::kTiles, full(s), pol_x);
                 }
+                ++issued;
+                if (++s == S) s = 0, phase ^= 1;
             }
-            if (!ok) record_error(a.err, kErrEmptyWait);
-            bool drained = true;  // every copy issued has landed before the CTA may exit
-            for (int g = max(0, i - S); drained && g < i; ++g) drained = mbar_wait_bounded(full(g % S), (g / S) & 1);
-            if (!drained) record_error(a.err, kErrDrainWait);
         }
+        if (!ok && lane == 0) record_error(a.err, kErrEmptyWait);
+        bool drained = true;  // every copy issued has landed before the CTA may exit
+        for (int g = max(0, issued - S); drained && g < issued; ++g) drained = mbar_wait_cycles(full(g % S), (g / S) & 1);
+        if (!drained && lane == 0) record_error(a.err, kErrDrainWait);
+        __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            bool ok = true;
-            int i = 0, n = 0;
-            while (ok && walk.next(tile)) {
-                const int buf = n % P::kAcc;
-                if (n >= P::kAcc && !mbar_wait_bounded(acc_empty(buf), ((n / P::kAcc) - 1) & 1)) {
+        bool ok = true;
+        int s = 0, set = 0, buf = 0, n = 0, done = 0;
+        uint32_t phase = 0, acc_phase = 1;
+        int ws = 0;               // the stage whose MMAs last read the scale columns in turn
+        uint32_t ws_phase = 0;
+        while (ok && walk.next(tile)) {
+            any = true;
+            if (!__all_sync(0xffffffffu, mbar_wait_cycles(acc_empty(buf), acc_phase))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN);
+            const uint32_t sfb_row = static_cast<uint32_t>(tile.srow >> 5);
+            for (int kt = kt0; kt < kt1; ++kt) {
+                bool ready = mbar_wait_cycles(full(s), phase);
+                // the set of scale columns is written again: the MMAs that read it have to be done
+                if (done >= kScaleSets) {
+                    ready = ready && mbar_wait_cycles(empty(ws), ws_phase);
+                    if (++ws == S) ws = 0, ws_phase ^= 1;
+                }
+                if (!__all_sync(0xffffffffu, ready)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN);
-                for (int kt = 0; kt < nk; ++kt, ++i) {
-                    const int s = i % S;
-                    if (!mbar_wait_bounded(full(s), (i / S) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    // the scale columns of stage i - 2 are written again: its MMAs have to be done
-                    if (i >= 2 && !mbar_wait_bounded(empty((i - 2) % S), ((i - 2) / S) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t st = stage(s), sc = st + kCodesA + P::kCodesB;
-                    const uint32_t sfa = tmem + P::kAcc * BN + static_cast<uint32_t>((i & 1) * P::kSetCols);
-                    const uint32_t sfb = sfa + 4 * P::kTiles;
+                const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage), sc = st + kCodesA + P::kCodesB;
+                const uint32_t sfa = tmem + P::kAcc * BN + static_cast<uint32_t>(set * P::kSetCols);
+                const uint32_t sfb = sfa + 4 * P::kTiles;
+                const uint64_t da = desc_codes(st), db = desc_codes(st + kCodesA), ds = desc_scales(sc);
+                const int steps = min(4, (a.K - kt * kStageK + 63) / 64);  // K past the end: no MMA
+                if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < P::kTiles; ++j) {
-                        tmem_copy_scales(sfa + 4 * j, desc_scales(sc + j * kScaleTile));
+                        tmem_copy_scales(sfa + 4 * j, ds + (j * kScaleTile >> 4));
 #pragma unroll
                         for (int b = 0; b < P::kBlocksB; ++b)
-                            tmem_copy_scales(sfb + 4 * (j * P::kBlocksB + b),
-                                             desc_scales(sc + P::kScalesA * (1 + b) + j * kScaleTile));
+                            tmem_copy_scales(sfb + 4 * (j * P::kBlocksB + b), ds + ((P::kScalesA * (1 + b) + j * kScaleTile) >> 4));
                     }
-                    const int steps = min(4, (a.K - kt * kStageK + 63) / 64);  // K past the end: no MMA
-                    for (int j = 0; j < steps; ++j) {
-                        const int q = MX ? j >> 1 : j;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        constexpr int kPerTile = MX ? 2 : 1;
+                        const int q = j / kPerTile;
                         // MXFP4: two K steps share a tile; the descriptor says which half of its words
                         const uint32_t half = MX ? 2u * (j & 1) : 0u;
-                        mma_fp4<MX>(acc, desc_codes(st + 32 * j), desc_codes(st + kCodesA + 32 * j),
-                                    P::kIdesc | (half << 4) | (half << 29), sfa + 4 * q,
-                                    sfb + 4 * q * P::kBlocksB + (tile.srow >> 5), (kt > 0 || j > 0) ? 1u : 0u);
+                        if (j < steps)
+                            mma_fp4<MX>(acc, da + 2 * j, db + 2 * j, P::kIdesc | (half << 4) | (half << 29), sfa + 4 * q,
+                                        sfb + 4 * q * P::kBlocksB + sfb_row, (kt > kt0 || j > 0) ? 1u : 0u);
                     }
                     tc_commit(empty(s));  // the stage and its scale columns are free once these MMAs have read them
+                    if (kt == kt1 - 1) tc_commit(acc_full(buf));
                 }
-                if (!ok) break;
-                tc_commit(acc_full(buf));
-                ++n;
+                __syncwarp();
+                ++done;
+                if (++s == S) s = 0, phase ^= 1;
+                if (++set == kScaleSets) set = 0;
             }
-            if (!ok) record_error(a.err, kErrFullWait);
-            tc_commit(finished);  // no MMA is in flight when tensor memory is released
-            if (!mbar_wait_bounded(finished, 0)) record_error(a.err, kErrDrainWait);
+            if (++buf == P::kAcc) buf = 0, acc_phase ^= 1;
+            ++n;
         }
+        if (!ok && lane == 0) record_error(a.err, kErrFullWait);
+        if (elect_one()) tc_commit(finished);  // no MMA is in flight when tensor memory is released
+        __syncwarp();
+        if (!mbar_wait_cycles(finished, 0) && lane == 0) record_error(a.err, kErrDrainWait);
         __syncwarp();
     } else {
-        const int q = warp & 3;  // lanes 32 q .. of tensor memory
+        const int q = warp & 3, half = (warp - 2) >> 2;  // lanes 32 q .. of tensor memory, half of the columns
+        constexpr int kHalf = BN / 2;
+        constexpr int kChunk = kHalf < 32 ? kHalf : 32;
         T* Y = static_cast<T*>(a.Y);
+        float* red = reinterpret_cast<float*>(base);
         bool ok = true;
-        int n = 0;
+        int buf = 0;
+        uint32_t acc_phase = 0;
         while (walk.next(tile)) {
-            const int buf = n % P::kAcc;
-            ok = mbar_wait_warp(acc_full(buf), (n / P::kAcc) & 1);  // warp-uniform: tcgen05.ld is .aligned
+            any = true;
+            ok = __all_sync(0xffffffffu, mbar_wait_cycles(acc_full(buf), acc_phase));  // tcgen05.ld is .aligned
             if (!ok) break;
             tc_fence_after();
-            const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN) + (static_cast<uint32_t>(32 * q) << 16);
-            const int r = tile.n0 + 32 * q + lane;
-            const float scale = a.w_global ? a.alpha * __ldg(a.w_global + tile.e) : a.alpha;
-            T* y = Y + static_cast<int64_t>(tile.row0) * a.N + r;
-#pragma unroll 1
-            for (int c0 = 0; c0 < BN && c0 < tile.rows; c0 += 16) {
-                uint32_t v[16];
-                tmem_ld<16>(acc + static_cast<uint32_t>(c0), v);
-                tmem_wait_ld();
-                if (r < a.N) {
+            const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN + half * kHalf) + (static_cast<uint32_t>(32 * q) << 16);
+            const int r = tile.n0 + 32 * q + lane, cols = tile.rows - half * kHalf;
+            // the accumulator goes to registers at once: the next tile's MMAs wait for nothing more
+            uint32_t v[kHalf / kChunk][kChunk];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c0 + j < tile.rows) {
-                            const float f = __uint_as_float(v[j]) * scale;
-                            if constexpr (sizeof(T) == 4) y[static_cast<int64_t>(c0 + j) * a.N] = f;
-                            else y[static_cast<int64_t>(c0 + j) * a.N] = __float2bfloat16_rn(f);
-                        }
-                }
-            }
+            for (int c = 0; c < kHalf / kChunk; ++c)
+                if (c * kChunk < cols) tmem_ld<kChunk>(acc + c * kChunk, v[c]);
+            tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(acc_empty(buf));
-            ++n;
+            if (a.ks > 1) {
+                // the partial tile to shared memory, [column][128 rows]; every copy and MMA of the one tile is done
+#pragma unroll
+                for (int c = 0; c < kHalf / kChunk; ++c)
+#pragma unroll
+                    for (int j = 0; j < kChunk; ++j)
+                        if (c * kChunk + j < cols)
+                            red[(half * kHalf + c * kChunk + j) * kRows + 32 * q + lane] = __uint_as_float(v[c][j]);
+            } else if (r < a.N) {
+                const float scale = a.w_global ? a.alpha * __ldg(a.w_global + tile.e) : a.alpha;
+                T* y = Y + static_cast<int64_t>(tile.row0 + half * kHalf) * a.N + r;
+#pragma unroll
+                for (int c = 0; c < kHalf / kChunk; ++c)
+#pragma unroll
+                    for (int j = 0; j < kChunk; ++j) {
+                        if (c * kChunk + j < cols) store_y(y, __uint_as_float(v[c][j]) * scale);
+                        y += a.N;
+                    }
+            }
+            if (++buf == P::kAcc) buf = 0, acc_phase ^= 1;
         }
         if (!ok && lane == 0) record_error(a.err, kErrFullWait);
         if (a.p.experts > 0) {  // rows past the rows in use
             const int64_t used = __ldg(a.p.offsets + a.p.experts), count = (static_cast<int64_t>(a.M) - used) * a.N;
-            const int tid = static_cast<int>(threadIdx.x) - (kThreads - kEpilogueThreads);
-            for (int64_t j = static_cast<int64_t>(blockIdx.x) * kEpilogueThreads + tid; j < count;
-                 j += static_cast<int64_t>(gridDim.x) * kEpilogueThreads)
+            const int64_t cta = blockIdx.y * static_cast<int64_t>(gridDim.x) + blockIdx.x;
+            const int64_t step = static_cast<int64_t>(gridDim.x) * gridDim.y * kEpilogueThreads;
+            for (int64_t j = cta * kEpilogueThreads + static_cast<int>(threadIdx.x) - 64; j < count; j += step)
                 Y[used * a.N + j] = T(0.0f);
         }
         tc_fence_before();
     }
     __syncthreads();
+    if (a.ks > 1) {
+        // CTA kz of the cluster sums its share of the tile's columns over the ks partial tiles, in CTA order
+        // (distributed shared memory), and writes them
+        cluster_sync();
+        if (any) {
+            T* Y = static_cast<T*>(a.Y);
+            const float scale = a.w_global ? a.alpha * __ldg(a.w_global + tile.e) : a.alpha;
+            const int c0 = kz * tile.rows / a.ks, c1 = (kz + 1) * tile.rows / a.ks;
+            for (int e = static_cast<int>(threadIdx.x); e < (c1 - c0) * kRows; e += kThreads) {
+                const int c = c0 + e / kRows, r = e % kRows;
+                float v = 0.0f;
+                for (int z = 0; z < a.ks; ++z) v += ld_dsmem_f32(sbase + 4u * static_cast<uint32_t>(c * kRows + r), static_cast<uint32_t>(z));
+                if (tile.n0 + r < a.N) store_y(Y + static_cast<int64_t>(tile.row0 + c) * a.N + tile.n0 + r, v * scale);
+            }
+        }
+        cluster_sync();  // no CTA leaves while another still reads its tile
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, P::kCols);
@@ -352,31 +414,45 @@ cudaError_t run_gemm(const CUtensorMap (&maps)[4], GemmArgs a, int64_t tiles, cu
     constexpr int kStatic = 8 * 1024;  // barriers, expert tiles (rounded up)
     a.S = std::min(kMaxStages, (kSmemLimit - 1024 - kStatic) / P::kStage);
     static_assert((kSmemLimit - 1024 - kStatic) / P::kStage >= 3, "three stages at least");
+    static_assert(3 * P::kStage >= BN * kRows * 4 || BN == 256, "a partial tile fits the stages");
     const int smem = a.S * P::kStage + 1024;
     auto kern = fp4_gemm_kernel<MX, BN, T>;
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
-    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles, device_sm_count())));
-    kern<<<grid, kThreads, smem, stream>>>(maps[0], maps[1], maps[2], maps[3], a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t lc{};
+    // K split: one tile per cluster; otherwise persistent CTAs
+    lc.gridDim = a.ks > 1 ? dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.ks))
+                          : dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(tiles, device_sm_count()))));
+    lc.blockDim = dim3(kThreads);
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = static_cast<unsigned>(a.ks);
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    return cudaLaunchKernelEx(&lc, kern, maps[0], maps[1], maps[2], maps[3], a);
 }
 
 template <bool MX, int BN>
-cudaError_t run_out(bool bf16, const Fp4View& x, const Fp4View& w, int64_t K, const GemmArgs& a, cudaStream_t stream) {
+cudaError_t run_out(bool bf16, const Fp4View& x, const Fp4View& w, int64_t K, const GemmArgs& a, int64_t tiles,
+                    cudaStream_t stream) {
     using P = Plan<MX, BN>;
     const int64_t nt = (w.rows + kRows - 1) / kRows;
     // 128-row scale blocks that a copy may touch: by experts the operand has room for any distribution
     const int64_t xblocks = a.p.experts ? (x.rows + 127 * std::min<int64_t>(a.p.experts, x.rows)) / 128 : (x.rows + 127) / 128;
-    const int64_t mt = a.p.experts ? std::min<int64_t>(x.rows, x.rows / BN + std::min<int64_t>(a.p.experts, x.rows))
-                                   : (x.rows + BN - 1) / BN;
     CUtensorMap maps[4];
     if (!encode_u32_map_pitch(&maps[0], w.codes, w.rows * w.matrices, K / 8, fp4_pitch(K), kStageWords, kRows, true) ||
         !encode_u32_map(&maps[1], w.scales, nt * w.matrices * a.chunks, 128, 128, P::kTiles) ||
         !encode_u32_map_pitch(&maps[2], x.codes, x.rows, K / 8, fp4_pitch(K), kStageWords, BN, true) ||
         !encode_u32_map(&maps[3], x.scales, xblocks * a.chunks, 128, 128, P::kTiles))
         return cudaErrorInvalidValue;
-    return bf16 ? run_gemm<MX, BN, __nv_bfloat16>(maps, a, nt * mt, stream)
-                : run_gemm<MX, BN, float>(maps, a, nt * mt, stream);
+    return bf16 ? run_gemm<MX, BN, __nv_bfloat16>(maps, a, tiles, stream)
+                : run_gemm<MX, BN, float>(maps, a, tiles, stream);
 }
 
 }  // namespace
@@ -396,11 +472,22 @@ cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t
     a.chunks = static_cast<int>(fp4_chunks(mx, K));
     // activation rows of a tile: of the matrix, or of an expert on average
     const int64_t rows = p.experts ? (x.rows + p.experts - 1) / p.experts : x.rows;
+    const int bn = rows <= 32 && !p.experts ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    const int64_t nt = (w.rows + kRows - 1) / kRows, nk = (K + kStageK - 1) / kStageK;
+    const int64_t tiles = nt * (p.experts ? std::min<int64_t>(x.rows, x.rows / bn + std::min<int64_t>(p.experts, x.rows))
+                                          : (x.rows + bn - 1) / bn);
+    a.ks = 1;
+    if (bn <= 128)
+        while (a.ks < 8 && tiles * (a.ks + 1) <= device_sm_count() && nk >= 4 * (a.ks + 1)) ++a.ks;
+    if (const char* s = std::getenv("PNQ_FP4_KS")) a.ks = std::atoi(s);
     auto go = [&](auto m) {
         constexpr bool MX = decltype(m)::value;
-        if (rows <= 64) return run_out<MX, 64>(bf16, x, w, K, a, stream);
-        if (rows <= 128) return run_out<MX, 128>(bf16, x, w, K, a, stream);
-        return run_out<MX, 256>(bf16, x, w, K, a, stream);
+        switch (bn) {
+            case 32: return run_out<MX, 32>(bf16, x, w, K, a, tiles, stream);
+            case 64: return run_out<MX, 64>(bf16, x, w, K, a, tiles, stream);
+            case 128: return run_out<MX, 128>(bf16, x, w, K, a, tiles, stream);
+            default: return run_out<MX, 256>(bf16, x, w, K, a, tiles, stream);
+        }
     };
     return mx ? go(std::true_type{}) : go(std::false_type{});
 }

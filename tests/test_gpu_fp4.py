@@ -275,7 +275,8 @@ def test_gemm_experts(kind, T, k, E, N, K, how, dtype):
 
 
 def test_long_rows_pass_32_bits():
-    """Operands whose code offsets pass 2^31: the last rows, against the same rows apart."""
+    """Operands whose code offsets pass 2^31: the last rows' codes against the same rows encoded apart, their products
+    (how K is split depends on the shape, so not bit for bit) against the sums in 64 bits."""
     kind, rows, K = pnq.NVFP4, 70_000, 65_536  # 2.3 GB of codes
     gen = torch.Generator(device="cuda").manual_seed(1)
     row = torch.randn(256, K, generator=gen, device="cuda", dtype=torch.bfloat16)
@@ -284,11 +285,10 @@ def test_long_rows_pass_32_bits():
     last = pnq.fp4_quantize(kind, x[-300:].contiguous())
     v = torch.randn(3, K, generator=gen, device="cuda")
     vm = pnq.fp4_quantize(kind, v)
-    y = pnq.fp4_gemm(vm, m)
-    assert torch.equal(y[:, -300:], pnq.fp4_gemm(vm, last))
     assert torch.equal(m.codes[-300:], last.codes)
-    z = pnq.fp4_gemm(m, vm)
-    assert torch.equal(z[-300:], pnq.fp4_gemm(last, vm))
+    vv, lv = (pnq.fp4_dequantize(t).double().cpu().numpy() for t in (vm, last))
+    check_product(pnq.fp4_gemm(vm, m)[:, -300:], vv, lv, 1.0, torch.float32)
+    check_product(pnq.fp4_gemm(m, vm)[-300:], lv, vv, 1.0, torch.float32)
 
 
 def test_streams_and_graph():
