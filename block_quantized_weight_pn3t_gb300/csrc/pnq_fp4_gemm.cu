@@ -22,7 +22,11 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdio>
 #include <cstdlib>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "pnq_device.cuh"
 #include "pnq_internal.h"
@@ -55,21 +59,21 @@ struct GemmArgs {
     int ks;                  // CTAs of a cluster that share a tile's K (1: none)
 };
 
-template <bool MX, int BN>
+template <bool MX, int BN, int CG>
 struct Plan {
     static constexpr int kTiles = MX ? 2 : 4;                    // scale tiles per stage and 128-row block
     static constexpr int kScalesA = kTiles * kScaleTile;
     static constexpr int kBlocksB = BN > 128 ? 2 : 1;            // 128-row blocks of activation scales
-    static constexpr int kCodesB = BN * kStageK / 2;
+    static constexpr int kCodesB = BN / CG * kStageK / 2;         // a pair's CTAs hold half of the activation rows each
     static constexpr int kStage = kCodesA + kCodesB + kScalesA * (1 + kBlocksB);
     static constexpr int kAcc = BN <= 128 ? 2 : 1;               // accumulators
     // tensor-memory columns: accumulators, then two sets of scale columns (A: 4 per tile, B: 4 per tile and block)
     static constexpr int kSetCols = 4 * kTiles * (1 + kBlocksB);
     static constexpr int kUsed = kAcc * BN + kScaleSets * kSetCols;
     static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-    // E2M1 operands, scale type, N, M = 128
+    // E2M1 operands, scale type, N, M = 128 per CTA
     static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(BN >> 3) << 17) |
-                                       ((MX ? 1u : 0u) << 23) | (static_cast<uint32_t>(kRows >> 4) << 24);
+                                       ((MX ? 1u : 0u) << 23) | (static_cast<uint32_t>(CG * kRows >> 4) << 24);
 };
 
 // Shared-memory descriptors: K-major 128-byte swizzled code rows (8-row groups 1024 bytes apart), and unswizzled
@@ -82,29 +86,34 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
     return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
 }
 
-// One scale tile (32 rows x 16 bytes) -> four columns of tensor memory, in all four lane quarters.
+// One scale tile (32 rows x 16 bytes) -> four columns of tensor memory, in all four lane quarters (a pair: in both
+// CTAs, each from its own shared memory).
+template <int CG>
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    if constexpr (CG == 2)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-template <bool MX>
+#define PNQ_MMA_FP4(GROUP, KIND)                                                                                   \
+    asm volatile(                                                                                                  \
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                          \
+        "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),          \
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                                            \
+        : "memory")
+
+template <bool MX, int CG>
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                         uint32_t accumulate) {
-    if constexpr (MX)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
+    if constexpr (MX && CG == 1) PNQ_MMA_FP4("1", "mxf4.block_scale.scale_vec::2X");
+    if constexpr (MX && CG == 2) PNQ_MMA_FP4("2", "mxf4.block_scale.scale_vec::2X");
+    if constexpr (!MX && CG == 1) PNQ_MMA_FP4("1", "mxf4nvf4.block_scale.scale_vec::4X");
+    if constexpr (!MX && CG == 2) PNQ_MMA_FP4("2", "mxf4nvf4.block_scale.scale_vec::4X");
 }
+#undef PNQ_MMA_FP4
 
-// A tile: 128 weight rows from n0 of matrix e, up to BN activation rows from m0 of the matrix's rows.
+// A tile: 128 weight rows (a pair: 256) from n0 of matrix e, up to BN activation rows from m0 of the matrix's rows.
 struct Tile {
     int e;        // matrix (0 when dense)
     int row0;     // first activation row (global)
@@ -116,14 +125,15 @@ struct Tile {
 
 // Walks the tiles t = first, first + step, ..: all roles of a CTA see the same sequence. By experts: `starts[e]`
 // (shared memory) is the number of tiles before expert e.
-template <int BN>
+template <int BN, int CG>
 struct Walk {
+    static constexpr int kTileN = CG * kRows;
     const GemmArgs& a;
     const int* starts;
     int t, step, nt, e;
     __device__ Walk(const GemmArgs& args, const int* tile_starts)
-        : a(args), starts(tile_starts), t(static_cast<int>(blockIdx.x)), step(static_cast<int>(gridDim.x)),
-          nt((args.N + kRows - 1) / kRows), e(0) {}
+        : a(args), starts(tile_starts), t(static_cast<int>(blockIdx.x) / CG), step(static_cast<int>(gridDim.x) / CG),
+          nt((args.N + kTileN - 1) / kTileN), e(0) {}
     __device__ bool next(Tile& o) {
         int m;
         if (a.p.experts == 0) {
@@ -133,14 +143,14 @@ struct Walk {
             const int band = t / (16 * mt), r = t - band * 16 * mt;
             const int width = min(16, nt - 16 * band);
             m = r / width;
-            o = Tile{0, m * BN, min(BN, a.M - m * BN), (16 * band + r - m * width) * kRows, m * BN / 128, m * BN % 128};
+            o = Tile{0, m * BN, min(BN, a.M - m * BN), (16 * band + r - m * width) * kTileN, m * BN / 128, m * BN % 128};
         } else {
             if (t >= starts[a.p.experts]) return false;
             while (t >= starts[e + 1]) ++e;
             const int first = __ldg(a.p.offsets + e), count = __ldg(a.p.offsets + e + 1) - first;
             const int mt = (count + BN - 1) / BN, r = t - starts[e];
             m = r % mt;
-            o = Tile{e, first + m * BN, min(BN, count - m * BN), r / mt * kRows,
+            o = Tile{e, first + m * BN, min(BN, count - m * BN), r / mt * kTileN,
                      __ldg(a.p.block_start + e) + m * BN / 128, m * BN % 128};
         }
         t += step;
@@ -155,13 +165,13 @@ __device__ __forceinline__ void store_y(T* y, float f) {
     else *y = __float2bfloat16_rn(f);
 }
 
-template <bool MX, int BN, class T>
+template <bool MX, int BN, int CG, class T>
 __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
                                                                const __grid_constant__ CUtensorMap map_ws,
                                                                const __grid_constant__ CUtensorMap map_x,
                                                                const __grid_constant__ CUtensorMap map_xs,
                                                                const GemmArgs a) {
-    using P = Plan<MX, BN>;
+    using P = Plan<MX, BN, CG>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
@@ -176,6 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     const uint32_t finished = b0 + 8u * (2 * kMaxStages + 4);
     const int S = a.S, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sbase = smem_addr(base);
+    // pair: CTA 0 leads (its barriers count both CTAs' copies, its thread issues the MMAs of both)
+    const uint32_t rank = CG == 2 ? blockIdx.x & 1u : 0u;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -184,16 +196,21 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full(i), 1);
-            mbar_init(acc_empty(i), kEpilogueWarps);
+            mbar_init(acc_empty(i), CG * kEpilogueWarps);
         }
         mbar_init(finished, 1);
         mbar_fence_init();
     }
-    if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), P::kCols);
+    if constexpr (CG == 2) {
+        cluster_sync();  // the pair's barriers exist before either CTA signals them
+        if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), P::kCols);
+    } else {
+        if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), P::kCols);
+    }
     griddep_wait();  // nothing above reads what an earlier kernel wrote
     if (a.p.experts > 0) {
         // tiles before each expert: a block scan, each thread over consecutive experts
-        const int E = a.p.experts, nt = (a.N + kRows - 1) / kRows, per = (E + kThreads - 1) / kThreads;
+        const int E = a.p.experts, nt = (a.N + CG * kRows - 1) / (CG * kRows), per = (E + kThreads - 1) / kThreads;
         const int e0 = min(E, static_cast<int>(threadIdx.x) * per), e1 = min(E, e0 + per);
         int sum = 0;
         for (int e = e0; e < e1; ++e) sum += (__ldg(a.p.offsets + e + 1) - __ldg(a.p.offsets + e) + BN - 1) / BN * nt;
@@ -221,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     // this CTA's share of the stages along K: [kt0, kt1)
     const int nk = (a.K + kStageK - 1) / kStageK, kz = static_cast<int>(blockIdx.y);
     const int kt0 = kz * nk / a.ks, kt1 = (kz + 1) * nk / a.ks;
-    Walk<BN> walk(a, starts);
+    Walk<BN, CG> walk(a, starts);
     Tile tile{};
     bool any = false;  // this CTA had a tile (the same in all its threads)
 
@@ -236,8 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         uint32_t phase = 1;  // the first wait for each free stage passes
         while (ok && walk.next(tile)) {
             any = true;
-            const int wrow = tile.e * a.N + tile.n0;
-            const int wsc = (tile.e * blocks_w + tile.n0 / 128) * a.chunks, xsc = tile.sblock * a.chunks;
+            const int n0 = tile.n0 + static_cast<int>(rank) * kRows, wrow = tile.e * a.N + n0;
+            const int xrow = tile.row0 + static_cast<int>(rank) * (BN / CG);
+            const int wsc = (tile.e * blocks_w + n0 / 128) * a.chunks, xsc = tile.sblock * a.chunks;
             for (int kt = kt0; kt < kt1; ++kt) {
                 if (!__all_sync(0xffffffffu, mbar_wait_cycles(empty(s), phase))) {
                     ok = false;
@@ -245,30 +263,42 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                 }
                 const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage), sc = st + kCodesA + P::kCodesB;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(full(s), P::kStage);
-                    tma_load_2d(st, &map_w, kt * kStageWords, wrow, full(s), pol_w);
-                    tma_load_2d(sc, &map_ws, 0, wsc + kt * P::kTiles, full(s), pol_w);
-                    tma_load_2d(st + kCodesA, &map_x, kt * kStageWords, tile.row0, full(s), pol_x);
+                    if (rank == 0) mbar_arrive_expect_tx(full(s), CG * P::kStage);
+                    const uint32_t bar = CG == 2 ? cluster_addr(full(s), 0) : full(s);
+                    auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t pol) {
+                        if constexpr (CG == 2) tma_load_2d_pair(dst, map, x, y, bar, pol);
+                        else tma_load_2d(dst, map, x, y, bar, pol);
+                    };
+                    load(st, &map_w, kt * kStageWords, wrow, pol_w);
+                    load(sc, &map_ws, 0, wsc + kt * P::kTiles, pol_w);
+                    load(st + kCodesA, &map_x, kt * kStageWords, xrow, pol_x);
 #pragma unroll
                     for (int b = 0; b < P::kBlocksB; ++b)
-                        tma_load_2d(sc + P::kScalesA * (1 + b), &map_xs, 0, xsc + b * a.chunks + kt * P::kTiles, full(s), pol_x);
+                        load(sc + P::kScalesA * (1 + b), &map_xs, 0, xsc + b * a.chunks + kt * P::kTiles, pol_x);
                 }
                 ++issued;
                 if (++s == S) s = 0, phase ^= 1;
             }
         }
         if (!ok && lane == 0) record_error(a.err, kErrEmptyWait);
-        bool drained = true;  // every copy issued has landed before the CTA may exit
-        for (int g = max(0, issued - S); drained && g < issued; ++g) drained = mbar_wait_cycles(full(g % S), (g / S) & 1);
+        // every copy issued has landed before the CTA may exit; a pair's are all counted in CTA 0, and CTA 1 waits until
+        // its last stages are reported free (no signal to its barriers is under way when it exits)
+        bool drained = true;
+        for (int g = max(0, issued - S); drained && g < issued; ++g)
+            drained = mbar_wait_cycles(rank == 0 ? full(g % S) : empty(g % S), (g / S) & 1);
         if (!drained && lane == 0) record_error(a.err, kErrDrainWait);
         __syncwarp();
     } else if (warp == 1) {
+        auto commit = [](uint32_t bar) {
+            if constexpr (CG == 2) tc_commit_pair(bar);
+            else tc_commit(bar);
+        };
         bool ok = true;
         int s = 0, set = 0, buf = 0, n = 0, done = 0;
         uint32_t phase = 0, acc_phase = 1;
         int ws = 0;               // the stage whose MMAs last read the scale columns in turn
         uint32_t ws_phase = 0;
-        while (ok && walk.next(tile)) {
+        while (ok && rank == 0 && walk.next(tile)) {
             any = true;
             if (!__all_sync(0xffffffffu, mbar_wait_cycles(acc_empty(buf), acc_phase))) {
                 ok = false;
@@ -297,10 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                 if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < P::kTiles; ++j) {
-                        tmem_copy_scales(sfa + 4 * j, ds + (j * kScaleTile >> 4));
+                        tmem_copy_scales<CG>(sfa + 4 * j, ds + (j * kScaleTile >> 4));
 #pragma unroll
                         for (int b = 0; b < P::kBlocksB; ++b)
-                            tmem_copy_scales(sfb + 4 * (j * P::kBlocksB + b), ds + ((P::kScalesA * (1 + b) + j * kScaleTile) >> 4));
+                            tmem_copy_scales<CG>(sfb + 4 * (j * P::kBlocksB + b), ds + ((P::kScalesA * (1 + b) + j * kScaleTile) >> 4));
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -309,11 +339,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                         // MXFP4: two K steps share a tile; the descriptor says which half of its words
                         const uint32_t half = MX ? 2u * (j & 1) : 0u;
                         if (j < steps)
-                            mma_fp4<MX>(acc, da + 2 * j, db + 2 * j, P::kIdesc | (half << 4) | (half << 29), sfa + 4 * q,
+                            mma_fp4<MX, CG>(acc, da + 2 * j, db + 2 * j, P::kIdesc | (half << 4) | (half << 29), sfa + 4 * q,
                                         sfb + 4 * q * P::kBlocksB + sfb_row, (kt > kt0 || j > 0) ? 1u : 0u);
                     }
-                    tc_commit(empty(s));  // the stage and its scale columns are free once these MMAs have read them
-                    if (kt == kt1 - 1) tc_commit(acc_full(buf));
+                    commit(empty(s));  // the stage and its scale columns are free once these MMAs have read them
+                    if (kt == kt1 - 1) commit(acc_full(buf));
                 }
                 __syncwarp();
                 ++done;
@@ -324,9 +354,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
             ++n;
         }
         if (!ok && lane == 0) record_error(a.err, kErrFullWait);
-        if (elect_one()) tc_commit(finished);  // no MMA is in flight when tensor memory is released
-        __syncwarp();
-        if (!mbar_wait_cycles(finished, 0) && lane == 0) record_error(a.err, kErrDrainWait);
+        if (rank == 0) {  // no MMA is in flight when tensor memory is released
+            if (elect_one()) {
+                if constexpr (CG == 2) tc_commit_pair_own(finished);
+                else tc_commit(finished);
+            }
+            __syncwarp();
+            if (!mbar_wait_cycles(finished, 0) && lane == 0) record_error(a.err, kErrDrainWait);
+        }
         __syncwarp();
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;  // lanes 32 q .. of tensor memory, half of the columns
@@ -343,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
             if (!ok) break;
             tc_fence_after();
             const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN + half * kHalf) + (static_cast<uint32_t>(32 * q) << 16);
-            const int r = tile.n0 + 32 * q + lane, cols = tile.rows - half * kHalf;
+            const int r = tile.n0 + static_cast<int>(rank) * kRows + 32 * q + lane, cols = tile.rows - half * kHalf;
             // the accumulator goes to registers at once: the next tile's MMAs wait for nothing more
             uint32_t v[kHalf / kChunk][kChunk];
 #pragma unroll
@@ -352,7 +387,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty(buf));
+            if (lane == 0) {
+                if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(acc_empty(buf), 0));
+                else mbar_arrive(acc_empty(buf));
+            }
             if (a.ks > 1) {
                 // the partial tile to shared memory, [column][128 rows]; every copy and MMA of the one tile is done
 #pragma unroll
@@ -385,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         tc_fence_before();
     }
     __syncthreads();
-    if (a.ks > 1) {
+    if constexpr (CG == 2) cluster_sync();  // both CTAs' copies have landed, both accumulators are read
+    if (CG == 1 && a.ks > 1) {
         // CTA kz of the cluster sums its share of the tile's columns over the ks partial tiles, in CTA order
         // (distributed shared memory), and writes them
         cluster_sync();
@@ -404,55 +443,84 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     }
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, P::kCols);
+        if constexpr (CG == 2) tmem_dealloc_pair(tmem, P::kCols);
+        else tmem_dealloc(tmem, P::kCols);
     }
 }
 
-template <bool MX, int BN, class T>
+// CTA pairs of a kernel that the current device holds at once (not every group of SMs is even).
+cudaError_t resident_pairs(const void* kernel, cudaLaunchConfig_t lc, int* pairs) {
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, int> known;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    int& n = known[{kernel, dev}];
+    if (n == 0) {
+        lc.gridDim = dim3(2 * static_cast<unsigned>(device_sm_count()));
+        lc.numAttrs = 1;  // the cluster alone
+        const cudaError_t q = cudaOccupancyMaxActiveClusters(&n, kernel, &lc);
+        if (q != cudaSuccess) return q;
+        n = std::max(n, 1);
+    }
+    *pairs = n;
+    return cudaSuccess;
+}
+
+template <bool MX, int BN, int CG, class T>
 cudaError_t run_gemm(const CUtensorMap (&maps)[4], GemmArgs a, int64_t tiles, cudaStream_t stream) {
-    using P = Plan<MX, BN>;
+    using P = Plan<MX, BN, CG>;
     constexpr int kStatic = 8 * 1024;  // barriers, expert tiles (rounded up)
     a.S = std::min(kMaxStages, (kSmemLimit - 1024 - kStatic) / P::kStage);
     static_assert((kSmemLimit - 1024 - kStatic) / P::kStage >= 3, "three stages at least");
     static_assert(3 * P::kStage >= BN * kRows * 4 || BN == 256, "a partial tile fits the stages");
     const int smem = a.S * P::kStage + 1024;
-    auto kern = fp4_gemm_kernel<MX, BN, T>;
+    auto kern = fp4_gemm_kernel<MX, BN, CG, T>;
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc{};
-    // K split: one tile per cluster; otherwise persistent CTAs
-    lc.gridDim = a.ks > 1 ? dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.ks))
-                          : dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(tiles, device_sm_count()))));
     lc.blockDim = dim3(kThreads);
     lc.dynamicSmemBytes = static_cast<size_t>(smem);
     lc.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.x = CG;
     attr[0].val.clusterDim.y = static_cast<unsigned>(a.ks);
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 2;
+    // K split: one tile per cluster; otherwise as many persistent CTAs (pairs) as the device holds at once
+    if (a.ks > 1) {
+        lc.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.ks));
+    } else if (CG == 1) {
+        lc.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, device_sm_count())));
+    } else {
+        int pairs = 0;
+        const cudaError_t q = resident_pairs(reinterpret_cast<const void*>(kern), lc, &pairs);
+        if (q != cudaSuccess) return q;
+        lc.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs)));
+    }
     return cudaLaunchKernelEx(&lc, kern, maps[0], maps[1], maps[2], maps[3], a);
 }
 
-template <bool MX, int BN>
+template <bool MX, int BN, int CG = 1>
 cudaError_t run_out(bool bf16, const Fp4View& x, const Fp4View& w, int64_t K, const GemmArgs& a, int64_t tiles,
                     cudaStream_t stream) {
-    using P = Plan<MX, BN>;
-    const int64_t nt = (w.rows + kRows - 1) / kRows;
+    using P = Plan<MX, BN, CG>;
+    const int64_t nt = (w.rows + kRows - 1) / kRows;  // 128-row scale blocks of a matrix
     // 128-row scale blocks that a copy may touch: by experts the operand has room for any distribution
     const int64_t xblocks = a.p.experts ? (x.rows + 127 * std::min<int64_t>(a.p.experts, x.rows)) / 128 : (x.rows + 127) / 128;
     CUtensorMap maps[4];
     if (!encode_u32_map_pitch(&maps[0], w.codes, w.rows * w.matrices, K / 8, fp4_pitch(K), kStageWords, kRows, true) ||
         !encode_u32_map(&maps[1], w.scales, nt * w.matrices * a.chunks, 128, 128, P::kTiles) ||
-        !encode_u32_map_pitch(&maps[2], x.codes, x.rows, K / 8, fp4_pitch(K), kStageWords, BN, true) ||
+        !encode_u32_map_pitch(&maps[2], x.codes, x.rows, K / 8, fp4_pitch(K), kStageWords, BN / CG, true) ||
         !encode_u32_map(&maps[3], x.scales, xblocks * a.chunks, 128, 128, P::kTiles))
         return cudaErrorInvalidValue;
-    return bf16 ? run_gemm<MX, BN, __nv_bfloat16>(maps, a, tiles, stream)
-                : run_gemm<MX, BN, float>(maps, a, tiles, stream);
+    return bf16 ? run_gemm<MX, BN, CG, __nv_bfloat16>(maps, a, tiles, stream)
+                : run_gemm<MX, BN, CG, float>(maps, a, tiles, stream);
 }
 
 }  // namespace
@@ -472,21 +540,31 @@ cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t
     a.chunks = static_cast<int>(fp4_chunks(mx, K));
     // activation rows of a tile: of the matrix, or of an expert on average
     const int64_t rows = p.experts ? (x.rows + p.experts - 1) / p.experts : x.rows;
-    const int bn = rows <= 32 && !p.experts ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
-    const int64_t nt = (w.rows + kRows - 1) / kRows, nk = (K + kStageK - 1) / kStageK;
-    const int64_t tiles = nt * (p.experts ? std::min<int64_t>(x.rows, x.rows / bn + std::min<int64_t>(p.experts, x.rows))
-                                          : (x.rows + bn - 1) / bn);
+    int bn = rows <= 32 && !p.experts ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    const int64_t nk = (K + kStageK - 1) / kStageK;
+    auto count = [&](int tile_n, int tile_m) {
+        const int64_t mt = p.experts ? std::min<int64_t>(x.rows, x.rows / tile_m + std::min<int64_t>(p.experts, x.rows))
+                                     : (x.rows + tile_m - 1) / tile_m;
+        return (w.rows + tile_n - 1) / tile_n * mt;
+    };
+    int pair = bn == 256;
+    if (const char* s = std::getenv("PNQ_FP4_CFG")) {
+        int b = 0, c = 0;
+        if (std::sscanf(s, "%d,%d", &b, &c) == 2) bn = b, pair = c;
+    }
+    const int64_t tiles = count(pair ? 2 * kRows : kRows, bn);
     a.ks = 1;
-    if (bn <= 128)
+    if (!pair && bn <= 128)
         while (a.ks < 8 && tiles * (a.ks + 1) <= device_sm_count() && nk >= 4 * (a.ks + 1)) ++a.ks;
-    if (const char* s = std::getenv("PNQ_FP4_KS")) a.ks = std::atoi(s);
     auto go = [&](auto m) {
         constexpr bool MX = decltype(m)::value;
         switch (bn) {
             case 32: return run_out<MX, 32>(bf16, x, w, K, a, tiles, stream);
             case 64: return run_out<MX, 64>(bf16, x, w, K, a, tiles, stream);
-            case 128: return run_out<MX, 128>(bf16, x, w, K, a, tiles, stream);
-            default: return run_out<MX, 256>(bf16, x, w, K, a, tiles, stream);
+            case 128: return pair ? run_out<MX, 128, 2>(bf16, x, w, K, a, tiles, stream)
+                                  : run_out<MX, 128>(bf16, x, w, K, a, tiles, stream);
+            default: return pair ? run_out<MX, 256, 2>(bf16, x, w, K, a, tiles, stream)
+                                 : run_out<MX, 256>(bf16, x, w, K, a, tiles, stream);
         }
     };
     return mx ? go(std::true_type{}) : go(std::false_type{});
