@@ -66,7 +66,7 @@ struct Plan {
     static constexpr int kBlocksB = BN > 128 ? 2 : 1;            // 128-row blocks of activation scales
     static constexpr int kCodesB = BN / CG * kStageK / 2;         // a pair's CTAs hold half of the activation rows each
     static constexpr int kStage = kCodesA + kCodesB + kScalesA * (1 + kBlocksB);
-    static constexpr int kAcc = BN <= 128 ? 2 : 1;               // accumulators
+    static constexpr int kAcc = BN <= 192 ? 2 : 1;               // accumulators
     // tensor-memory columns: accumulators, then two sets of scale columns (A: 4 per tile, B: 4 per tile and block)
     static constexpr int kSetCols = 4 * kTiles * (1 + kBlocksB);
     static constexpr int kUsed = kAcc * BN + kScaleSets * kSetCols;
@@ -240,29 +240,27 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     const int kt0 = kz * nk / a.ks, kt1 = (kz + 1) * nk / a.ks;
     Walk<BN, CG> walk(a, starts);
     Tile tile{};
-    bool any = false;  // this CTA had a tile (the same in all its threads)
 
-    // Warps 0 and 1 run their loops converged, one elected lane issues: the waits are the whole warp's, and
-    // everything the asynchronous instructions take is warp-uniform.
+    // Warps 0 and 1 run their loops in one elected lane: a wait by 32 lanes is 32 probes of the barrier, one after
+    // the other (a stage's turn took 0.25 us that way with nothing else in it).
     if (warp == 0) {
-        // one pass over the weights of a tile row: keep the activations in L2, let the weights go first
-        const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
-        const int blocks_w = (a.N + 127) / 128;
-        bool ok = true;
-        int s = 0, issued = 0;
-        uint32_t phase = 1;  // the first wait for each free stage passes
-        while (ok && walk.next(tile)) {
-            any = true;
-            const int n0 = tile.n0 + static_cast<int>(rank) * kRows, wrow = tile.e * a.N + n0;
-            const int xrow = tile.row0 + static_cast<int>(rank) * (BN / CG);
-            const int wsc = (tile.e * blocks_w + n0 / 128) * a.chunks, xsc = tile.sblock * a.chunks;
-            for (int kt = kt0; kt < kt1; ++kt) {
-                if (!__all_sync(0xffffffffu, mbar_wait_cycles(empty(s), phase))) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage), sc = st + kCodesA + P::kCodesB;
-                if (elect_one()) {
+        if (elect_one()) {
+            // one pass over the weights of a tile row: keep the activations in L2, let the weights go first
+            const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
+            const int blocks_w = (a.N + 127) / 128;
+            bool ok = true;
+            int s = 0, issued = 0;
+            uint32_t phase = 1;  // the first wait for each free stage passes
+            while (ok && walk.next(tile)) {
+                const int n0 = tile.n0 + static_cast<int>(rank) * kRows, wrow = tile.e * a.N + n0;
+                const int xrow = tile.row0 + static_cast<int>(rank) * (BN / CG);
+                const int wsc = (tile.e * blocks_w + n0 / 128) * a.chunks, xsc = tile.sblock * a.chunks;
+                for (int kt = kt0; kt < kt1; ++kt) {
+                    if (!mbar_wait_cycles(empty(s), phase)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage), sc = st + kCodesA + P::kCodesB;
                     if (rank == 0) mbar_arrive_expect_tx(full(s), CG * P::kStage);
                     const uint32_t bar = CG == 2 ? cluster_addr(full(s), 0) : full(s);
                     auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t pol) {
@@ -275,62 +273,61 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
 #pragma unroll
                     for (int b = 0; b < P::kBlocksB; ++b)
                         load(sc + P::kScalesA * (1 + b), &map_xs, 0, xsc + b * a.chunks + kt * P::kTiles, pol_x);
+                    ++issued;
+                    if (++s == S) s = 0, phase ^= 1;
                 }
-                ++issued;
-                if (++s == S) s = 0, phase ^= 1;
             }
+            if (!ok) record_error(a.err, kErrEmptyWait);
+            // every copy issued has landed before the CTA may exit; a pair's are all counted in CTA 0, and CTA 1 waits
+            // until its last stages are reported free (no signal to its barriers is under way when it exits)
+            bool drained = true;
+            for (int g = max(0, issued - S); drained && g < issued; ++g)
+                drained = mbar_wait_cycles(rank == 0 ? full(g % S) : empty(g % S), (g / S) & 1);
+            if (!drained) record_error(a.err, kErrDrainWait);
         }
-        if (!ok && lane == 0) record_error(a.err, kErrEmptyWait);
-        // every copy issued has landed before the CTA may exit; a pair's are all counted in CTA 0, and CTA 1 waits until
-        // its last stages are reported free (no signal to its barriers is under way when it exits)
-        bool drained = true;
-        for (int g = max(0, issued - S); drained && g < issued; ++g)
-            drained = mbar_wait_cycles(rank == 0 ? full(g % S) : empty(g % S), (g / S) & 1);
-        if (!drained && lane == 0) record_error(a.err, kErrDrainWait);
-        __syncwarp();
     } else if (warp == 1) {
-        auto commit = [](uint32_t bar) {
-            if constexpr (CG == 2) tc_commit_pair(bar);
-            else tc_commit(bar);
-        };
-        bool ok = true;
-        int s = 0, set = 0, buf = 0, n = 0, done = 0;
-        uint32_t phase = 0, acc_phase = 1;
-        int ws = 0;               // the stage whose MMAs last read the scale columns in turn
-        uint32_t ws_phase = 0;
-        while (ok && rank == 0 && walk.next(tile)) {
-            any = true;
-            if (!__all_sync(0xffffffffu, mbar_wait_cycles(acc_empty(buf), acc_phase))) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN);
-            const uint32_t sfb_row = static_cast<uint32_t>(tile.srow >> 5);
-            for (int kt = kt0; kt < kt1; ++kt) {
-                bool ready = mbar_wait_cycles(full(s), phase);
-                // the set of scale columns is written again: the MMAs that read it have to be done
-                if (done >= kScaleSets) {
-                    ready = ready && mbar_wait_cycles(empty(ws), ws_phase);
-                    if (++ws == S) ws = 0, ws_phase ^= 1;
-                }
-                if (!__all_sync(0xffffffffu, ready)) {
+        if (rank == 0 && elect_one()) {
+            auto commit = [](uint32_t bar) {
+                if constexpr (CG == 2) tc_commit_pair(bar);
+                else tc_commit(bar);
+            };
+            bool ok = true;
+            int s = 0, set = 0, buf = 0, done = 0;
+            uint32_t phase = 0, acc_phase = 1;
+            int ws = 0;  // the stage whose MMAs last read the scale columns in turn
+            uint32_t ws_phase = 0;
+            while (ok && walk.next(tile)) {
+                if (!mbar_wait_cycles(acc_empty(buf), acc_phase)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage), sc = st + kCodesA + P::kCodesB;
-                const uint32_t sfa = tmem + P::kAcc * BN + static_cast<uint32_t>(set * P::kSetCols);
-                const uint32_t sfb = sfa + 4 * P::kTiles;
-                const uint64_t da = desc_codes(st), db = desc_codes(st + kCodesA), ds = desc_scales(sc);
-                const int steps = min(4, (a.K - kt * kStageK + 63) / 64);  // K past the end: no MMA
-                if (elect_one()) {
+                const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN);
+                const uint32_t sfb_row = static_cast<uint32_t>(tile.srow >> 5);
+                for (int kt = kt0; kt < kt1; ++kt) {
+                    bool ready = mbar_wait_cycles(full(s), phase);
+                    // the set of scale columns is written again: the MMAs that read it have to be done
+                    if (done >= kScaleSets) {
+                        ready = ready && mbar_wait_cycles(empty(ws), ws_phase);
+                        if (++ws == S) ws = 0, ws_phase ^= 1;
+                    }
+                    if (!ready) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage), sc = st + kCodesA + P::kCodesB;
+                    const uint32_t sfa = tmem + P::kAcc * BN + static_cast<uint32_t>(set * P::kSetCols);
+                    const uint32_t sfb = sfa + 4 * P::kTiles;
+                    const uint64_t da = desc_codes(st), db = desc_codes(st + kCodesA), ds = desc_scales(sc);
+                    const int steps = min(4, (a.K - kt * kStageK + 63) / 64);  // K past the end: no MMA
 #pragma unroll
                     for (int j = 0; j < P::kTiles; ++j) {
                         tmem_copy_scales<CG>(sfa + 4 * j, ds + (j * kScaleTile >> 4));
 #pragma unroll
                         for (int b = 0; b < P::kBlocksB; ++b)
-                            tmem_copy_scales<CG>(sfb + 4 * (j * P::kBlocksB + b), ds + ((P::kScalesA * (1 + b) + j * kScaleTile) >> 4));
+                            tmem_copy_scales<CG>(sfb + 4 * (j * P::kBlocksB + b),
+                                                 ds + ((P::kScalesA * (1 + b) + j * kScaleTile) >> 4));
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -340,29 +337,22 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                         const uint32_t half = MX ? 2u * (j & 1) : 0u;
                         if (j < steps)
                             mma_fp4<MX, CG>(acc, da + 2 * j, db + 2 * j, P::kIdesc | (half << 4) | (half << 29), sfa + 4 * q,
-                                        sfb + 4 * q * P::kBlocksB + sfb_row, (kt > kt0 || j > 0) ? 1u : 0u);
+                                            sfb + 4 * q * P::kBlocksB + sfb_row, (kt > kt0 || j > 0) ? 1u : 0u);
                     }
                     commit(empty(s));  // the stage and its scale columns are free once these MMAs have read them
                     if (kt == kt1 - 1) commit(acc_full(buf));
+                    ++done;
+                    if (++s == S) s = 0, phase ^= 1;
+                    if (++set == kScaleSets) set = 0;
                 }
-                __syncwarp();
-                ++done;
-                if (++s == S) s = 0, phase ^= 1;
-                if (++set == kScaleSets) set = 0;
+                if (++buf == P::kAcc) buf = 0, acc_phase ^= 1;
             }
-            if (++buf == P::kAcc) buf = 0, acc_phase ^= 1;
-            ++n;
+            if (!ok) record_error(a.err, kErrFullWait);
+            // no MMA is in flight when tensor memory is released
+            if constexpr (CG == 2) tc_commit_pair_own(finished);
+            else tc_commit(finished);
+            if (!mbar_wait_cycles(finished, 0)) record_error(a.err, kErrDrainWait);
         }
-        if (!ok && lane == 0) record_error(a.err, kErrFullWait);
-        if (rank == 0) {  // no MMA is in flight when tensor memory is released
-            if (elect_one()) {
-                if constexpr (CG == 2) tc_commit_pair_own(finished);
-                else tc_commit(finished);
-            }
-            __syncwarp();
-            if (!mbar_wait_cycles(finished, 0) && lane == 0) record_error(a.err, kErrDrainWait);
-        }
-        __syncwarp();
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;  // lanes 32 q .. of tensor memory, half of the columns
         constexpr int kHalf = BN / 2;
@@ -373,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         int buf = 0;
         uint32_t acc_phase = 0;
         while (walk.next(tile)) {
-            any = true;
-            ok = __all_sync(0xffffffffu, mbar_wait_cycles(acc_full(buf), acc_phase));  // tcgen05.ld is .aligned
+            if (lane == 0) ok = mbar_wait_cycles(acc_full(buf), acc_phase);
+            ok = __shfl_sync(0xffffffffu, ok, 0);  // tcgen05.ld is .aligned: the warp goes on or stops as one
             if (!ok) break;
             tc_fence_after();
             const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN + half * kHalf) + (static_cast<uint32_t>(32 * q) << 16);
@@ -428,7 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         // CTA kz of the cluster sums its share of the tile's columns over the ks partial tiles, in CTA order
         // (distributed shared memory), and writes them
         cluster_sync();
-        if (any) {
+        Walk<BN, CG> again(a, starts);
+        if (again.next(tile)) {
             T* Y = static_cast<T*>(a.Y);
             const float scale = a.w_global ? a.alpha * __ldg(a.w_global + tile.e) : a.alpha;
             const int c0 = kz * tile.rows / a.ks, c1 = (kz + 1) * tile.rows / a.ks;
@@ -474,7 +465,7 @@ cudaError_t run_gemm(const CUtensorMap (&maps)[4], GemmArgs a, int64_t tiles, cu
     constexpr int kStatic = 8 * 1024;  // barriers, expert tiles (rounded up)
     a.S = std::min(kMaxStages, (kSmemLimit - 1024 - kStatic) / P::kStage);
     static_assert((kSmemLimit - 1024 - kStatic) / P::kStage >= 3, "three stages at least");
-    static_assert(3 * P::kStage >= BN * kRows * 4 || BN == 256, "a partial tile fits the stages");
+    static_assert(3 * P::kStage >= BN * kRows * 4 || BN >= 192, "a partial tile fits the stages");
     const int smem = a.S * P::kStage + 1024;
     auto kern = fp4_gemm_kernel<MX, BN, CG, T>;
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem);
@@ -563,6 +554,7 @@ cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t
             case 64: return run_out<MX, 64>(bf16, x, w, K, a, tiles, stream);
             case 128: return pair ? run_out<MX, 128, 2>(bf16, x, w, K, a, tiles, stream)
                                   : run_out<MX, 128>(bf16, x, w, K, a, tiles, stream);
+            case 192: return run_out<MX, 192, 2>(bf16, x, w, K, a, tiles, stream);
             default: return pair ? run_out<MX, 256, 2>(bf16, x, w, K, a, tiles, stream)
                                  : run_out<MX, 256>(bf16, x, w, K, a, tiles, stream);
         }
