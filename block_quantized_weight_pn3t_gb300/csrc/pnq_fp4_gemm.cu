@@ -44,8 +44,10 @@ constexpr int kEpilogueThreads = 32 * kEpilogueWarps;
 constexpr int kThreads = 64 + kEpilogueThreads;  // producer, MMA, epilogue
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxStages = 10;
-constexpr int kScaleSets = 2;                  // sets of scale columns in tensor memory
 constexpr int kSmemLimit = 227 * 1024;
+constexpr int kStaticSmem = 6 * 1024;          // barriers, expert tiles (rounded up)
+
+constexpr int imin(int a, int b) { return a < b ? a : b; }
 
 struct GemmArgs {
     void* Y;
@@ -55,7 +57,7 @@ struct GemmArgs {
     float alpha;
     int M, N, K;             // activation rows, weight rows of a matrix, K
     int chunks;              // scale tiles along K per 128-row block
-    int S;                   // stages
+    int weights_once;        // every weight row is read by one tile only
     int ks;                  // CTAs of a cluster that share a tile's K (1: none)
 };
 
@@ -66,10 +68,13 @@ struct Plan {
     static constexpr int kBlocksB = BN > 128 ? 2 : 1;            // 128-row blocks of activation scales
     static constexpr int kCodesB = BN / CG * kStageK / 2;         // a pair's CTAs hold half of the activation rows each
     static constexpr int kStage = kCodesA + kCodesB + kScalesA * (1 + kBlocksB);
-    static constexpr int kAcc = BN <= 192 ? 2 : 1;               // accumulators
-    // tensor-memory columns: accumulators, then two sets of scale columns (A: 4 per tile, B: 4 per tile and block)
+    static constexpr int kAcc = BN <= 128 ? 2 : 1;               // accumulators
+    // tensor-memory columns: accumulators, then a set of scale columns for every stage (A: 4 per tile, B: 4 per tile and
+    // block): a stage that is full again has its scale columns free too, so the MMA thread waits once per stage
     static constexpr int kSetCols = 4 * kTiles * (1 + kBlocksB);
-    static constexpr int kUsed = kAcc * BN + kScaleSets * kSetCols;
+    static constexpr int kStages = imin(kMaxStages, imin((kSmemLimit - 1024 - kStaticSmem) / kStage, (512 - kAcc * BN) / kSetCols));
+    static_assert(kStages >= 3, "three stages at least");
+    static constexpr int kUsed = kAcc * BN + kStages * kSetCols;
     static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     // E2M1 operands, scale type, N, M = 128 per CTA
     static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(BN >> 3) << 17) |
@@ -184,7 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     auto acc_full = [&](int i) { return b0 + 8u * (2 * kMaxStages + i); };
     auto acc_empty = [&](int i) { return b0 + 8u * (2 * kMaxStages + 2 + i); };
     const uint32_t finished = b0 + 8u * (2 * kMaxStages + 4);
-    const int S = a.S, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int S = P::kStages;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sbase = smem_addr(base);
     // pair: CTA 0 leads (its barriers count both CTAs' copies, its thread issues the MMAs of both)
     const uint32_t rank = CG == 2 ? blockIdx.x & 1u : 0u;
@@ -245,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     // the other (a stage's turn took 0.25 us that way with nothing else in it).
     if (warp == 0) {
         if (elect_one()) {
-            // one pass over the weights of a tile row: keep the activations in L2, let the weights go first
-            const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
+            // weights that no other tile reads leave L2 first
+            const uint64_t pol_x = l2_policy_evict_last(), pol_w = a.weights_once ? l2_policy_evict_first() : pol_x;
             const int blocks_w = (a.N + 127) / 128;
             bool ok = true;
             int s = 0, issued = 0;
@@ -292,35 +298,26 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                 else tc_commit(bar);
             };
             bool ok = true;
-            int s = 0, set = 0, buf = 0, done = 0;
+            int s = 0, buf = 0;
             uint32_t phase = 0, acc_phase = 1;
-            int ws = 0;  // the stage whose MMAs last read the scale columns in turn
-            uint32_t ws_phase = 0;
+            bool peek = false;  // the stage in turn was seen full
             while (ok && walk.next(tile)) {
-                if (!mbar_wait_cycles(acc_empty(buf), acc_phase)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
                 const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN);
                 const uint32_t sfb_row = static_cast<uint32_t>(tile.srow >> 5);
                 for (int kt = kt0; kt < kt1; ++kt) {
-                    bool ready = mbar_wait_cycles(full(s), phase);
-                    // the set of scale columns is written again: the MMAs that read it have to be done
-                    if (done >= kScaleSets) {
-                        ready = ready && mbar_wait_cycles(empty(ws), ws_phase);
-                        if (++ws == S) ws = 0, ws_phase ^= 1;
-                    }
-                    if (!ready) {
+                    if (!peek && !mbar_wait_cycles(full(s), phase)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage), sc = st + kCodesA + P::kCodesB;
-                    const uint32_t sfa = tmem + P::kAcc * BN + static_cast<uint32_t>(set * P::kSetCols);
+                    const uint32_t sfa = tmem + P::kAcc * BN + static_cast<uint32_t>(s * P::kSetCols);
                     const uint32_t sfb = sfa + 4 * P::kTiles;
                     const uint64_t da = desc_codes(st), db = desc_codes(st + kCodesA), ds = desc_scales(sc);
                     const int steps = min(4, (a.K - kt * kStageK + 63) / 64);  // K past the end: no MMA
+                    const int now = s;
+                    if (++s == S) s = 0, phase ^= 1;
+                    peek = mbar_try_wait(full(s), phase);  // a probe takes some 100 cycles: over before the next stage's turn
 #pragma unroll
                     for (int j = 0; j < P::kTiles; ++j) {
                         tmem_copy_scales<CG>(sfa + 4 * j, ds + (j * kScaleTile >> 4));
@@ -328,6 +325,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                         for (int b = 0; b < P::kBlocksB; ++b)
                             tmem_copy_scales<CG>(sfb + 4 * (j * P::kBlocksB + b),
                                                  ds + ((P::kScalesA * (1 + b) + j * kScaleTile) >> 4));
+                    }
+                    if (kt == kt0) {  // the accumulator: asked for once the first scales are on their way
+                        if (!mbar_wait_cycles(acc_empty(buf), acc_phase)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -339,11 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                             mma_fp4<MX, CG>(acc, da + 2 * j, db + 2 * j, P::kIdesc | (half << 4) | (half << 29), sfa + 4 * q,
                                             sfb + 4 * q * P::kBlocksB + sfb_row, (kt > kt0 || j > 0) ? 1u : 0u);
                     }
-                    commit(empty(s));  // the stage and its scale columns are free once these MMAs have read them
+                    commit(empty(now));  // the stage and its scale columns are free once these MMAs have read them
                     if (kt == kt1 - 1) commit(acc_full(buf));
-                    ++done;
-                    if (++s == S) s = 0, phase ^= 1;
-                    if (++set == kScaleSets) set = 0;
                 }
                 if (++buf == P::kAcc) buf = 0, acc_phase ^= 1;
             }
@@ -462,11 +463,8 @@ cudaError_t resident_pairs(const void* kernel, cudaLaunchConfig_t lc, int* pairs
 template <bool MX, int BN, int CG, class T>
 cudaError_t run_gemm(const CUtensorMap (&maps)[4], GemmArgs a, int64_t tiles, cudaStream_t stream) {
     using P = Plan<MX, BN, CG>;
-    constexpr int kStatic = 8 * 1024;  // barriers, expert tiles (rounded up)
-    a.S = std::min(kMaxStages, (kSmemLimit - 1024 - kStatic) / P::kStage);
-    static_assert((kSmemLimit - 1024 - kStatic) / P::kStage >= 3, "three stages at least");
-    static_assert(3 * P::kStage >= BN * kRows * 4 || BN >= 192, "a partial tile fits the stages");
-    const int smem = a.S * P::kStage + 1024;
+    static_assert(P::kStages * P::kStage >= BN * kRows * 4, "a partial tile fits the stages");
+    constexpr int smem = P::kStages * P::kStage + 1024;
     auto kern = fp4_gemm_kernel<MX, BN, CG, T>;
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
@@ -544,6 +542,7 @@ cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t
         if (std::sscanf(s, "%d,%d", &b, &c) == 2) bn = b, pair = c;
     }
     const int64_t tiles = count(pair ? 2 * kRows : kRows, bn);
+    a.weights_once = p.experts ? rows <= bn : x.rows <= bn;
     a.ks = 1;
     if (!pair && bn <= 128)
         while (a.ks < 8 && tiles * (a.ks + 1) <= device_sm_count() && nk >= 4 * (a.ks + 1)) ++a.ks;
@@ -554,7 +553,6 @@ cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t
             case 64: return run_out<MX, 64>(bf16, x, w, K, a, tiles, stream);
             case 128: return pair ? run_out<MX, 128, 2>(bf16, x, w, K, a, tiles, stream)
                                   : run_out<MX, 128>(bf16, x, w, K, a, tiles, stream);
-            case 192: return run_out<MX, 192, 2>(bf16, x, w, K, a, tiles, stream);
             default: return pair ? run_out<MX, 256, 2>(bf16, x, w, K, a, tiles, stream)
                                  : run_out<MX, 256>(bf16, x, w, K, a, tiles, stream);
         }
