@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 
 #include "pnq_device.cuh"
 #include "pnq_internal.h"
@@ -19,74 +20,81 @@ namespace {
 
 // ---- the plan -----------------------------------------------------------------------------------
 //
-// Counting sort of n expert ids by a cluster of C CTAs (C = 1..8), one launch:
+// Counting sort of n expert ids by a cluster of C CTAs (C = 1..8) of W warps each, one launch:
 //   1. every warp counts the experts of its own run of consecutive slots (shared-memory histogram per
 //      warp);
 //   2. a prefix over the CTA's warps, then over the cluster's CTAs (distributed shared memory), then
 //      over the experts, turns the counts into each warp's first sorted row per expert;
 //   3. every warp walks its run again, 32 slots at a time: lanes with the same expert rank themselves by
 //      lane (match), so equal experts keep the order of their slots.
+// The work is a chain of latencies, not bytes: a warp's ids are loaded kSortAhead batches at a time and, where one
+// such load holds its whole run, once for both passes.
 constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortAhead = 16;
 
 __device__ __forceinline__ int ld_dsmem_s32(uint32_t local_addr, uint32_t rank) {
     return __float_as_int(ld_dsmem_f32(local_addr, rank));
 }
 
-// Exclusive prefix sum of v over the block's threads (all kSortThreads take part).
-__device__ __forceinline__ int block_exclusive_scan(int v, int* warp_sums) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = v;
+// Exclusive prefix sum of v over the block's threads (all take part; warp_sums: one value per warp).
+__device__ __forceinline__ unsigned long long block_exclusive_scan(unsigned long long v, unsigned long long* warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    unsigned long long s = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, s, d);
+        const unsigned long long u = __shfl_up_sync(0xffffffffu, s, d);
         if (lane >= d) s += u;
     }
     if (lane == 31) warp_sums[warp] = s;
     __syncthreads();
-    if (warp == 0) {
-        const int own = warp_sums[lane];
-        int t = own;
+    unsigned long long before = lane < warp && lane < warps ? warp_sums[lane] : 0;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, t, d);
-            if (lane >= d) t += u;
-        }
-        warp_sums[lane] = t - own;
-    }
-    __syncthreads();
-    const int r = warp_sums[warp] + s - v;
-    __syncthreads();
-    return r;
+    for (int d = 16; d > 0; d >>= 1) before += __shfl_xor_sync(0xffffffffu, before, d);
+    return before + s - v;
 }
 
 __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int32_t* __restrict__ ids, int n, PlanView p,
-                                                                     int C) {
+                                                                     int C, int per) {
     extern __shared__ int sort_smem[];
-    const int E = p.experts;
-    int* hist = sort_smem;                 // [warps][E]
-    int* total = hist + kSortWarps * E;    // [E] counts of this CTA
-    int* first = total + E;                // [E] first sorted row of the expert
-    int* block0 = first + E;               // [E] first scale block of the expert
-    __shared__ int warp_sums[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int E = p.experts, W = static_cast<int>(blockDim.x) >> 5;
+    int* hist = sort_smem;        // [W][E]
+    int* total = hist + W * E;    // [E] counts of this CTA
+    int* first = total + E;       // [E] first sorted row of the expert
+    int* block0 = first + E;      // [E] first scale block of the expert
+    __shared__ unsigned long long warp_sums[32];
+    __shared__ int used_rows;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = static_cast<int>(blockDim.x);
     const int rank = static_cast<int>(blockIdx.x);
-    // this warp's run of slots: whole batches of 32, the same number for every warp of the cluster
-    const int batches = (n + 31) / 32, per = (batches + C * kSortWarps - 1) / (C * kSortWarps);
-    const int b0 = (rank * kSortWarps + warp) * per, b1 = min(batches, b0 + per);
+    // this warp's run of slots: `per` whole batches of 32
+    const int batches = (n + 31) / 32;
+    const int b0 = min(batches, (rank * W + warp) * per), b1 = min(batches, b0 + per);
 
-    for (int i = tid; i < kSortWarps * E; i += kSortThreads) hist[i] = 0;
+    int e[kSortAhead];
+    auto load = [&](int b) {  // the experts of batches b .. b + kSortAhead - 1, -1 where there is none
+#pragma unroll
+        for (int j = 0; j < kSortAhead; ++j) {
+            const int i = 32 * (b + j) + lane;
+            e[j] = b + j < b1 && i < n ? __ldg(ids + i) : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kSortAhead; ++j)
+            if (static_cast<unsigned>(e[j]) >= static_cast<unsigned>(E)) e[j] = -1;
+    };
+    load(b0);
+    for (int i = tid; i < W * E; i += threads) hist[i] = 0;
     __syncthreads();
     int* mine = hist + warp * E;
-    for (int b = b0; b < b1; ++b) {
-        const int i = 32 * b + lane;
-        const int e = i < n ? __ldg(ids + i) : -1;
-        if (e >= 0 && e < E) atomicAdd(mine + e, 1);
+    for (int b = b0; b < b1; b += kSortAhead) {
+        if (b > b0) load(b);
+#pragma unroll
+        for (int j = 0; j < kSortAhead; ++j)
+            if (e[j] >= 0) atomicAdd(mine + e[j], 1);
     }
     __syncthreads();
-    int count = 0;  // of expert `tid` in this CTA (E <= kSortThreads)
+    int count = 0;  // of expert `tid` in this CTA (E <= threads)
     if (tid < E) {
-        for (int w = 0; w < kSortWarps; ++w) {
+#pragma unroll 8
+        for (int w = 0; w < W; ++w) {
             const int c = hist[w * E + tid];
             hist[w * E + tid] = count;
             count += c;
@@ -105,12 +113,15 @@ __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int3
             }
         }
     }
-    const int off = block_exclusive_scan(all, warp_sums);
-    const int blk = block_exclusive_scan((all + 127) / 128, warp_sums);
+    if (C > 1) cluster_sync();  // every CTA has read the counts: they may be written over, and the CTAs may leave
+    // rows and 128-row blocks before expert tid, in one scan
+    const unsigned long long pre =
+        block_exclusive_scan((static_cast<unsigned long long>((all + 127) / 128) << 32) | static_cast<unsigned>(all), warp_sums);
+    const int off = static_cast<int>(pre & 0xffffffffu), blk = static_cast<int>(pre >> 32);
     if (tid < E) {
+        total[tid] = off + before;  // this CTA's first sorted row of the expert (no one reads the counts any more, below)
         first[tid] = off;
         block0[tid] = blk;
-        for (int w = 0; w < kSortWarps; ++w) hist[w * E + tid] += off + before;
         if (rank == 0) {
             p.offsets[tid] = off;
             p.block_start[tid] = blk;
@@ -119,31 +130,39 @@ __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int3
                 p.block_start[E] = blk + (all + 127) / 128;
             }
         }
-        if (tid == E - 1) warp_sums[0] = off + all;
+        if (tid == E - 1) used_rows = off + all;
     }
     __syncthreads();
-    const int used = warp_sums[0];
-    for (int b = b0; b < b1; ++b) {
-        const int i = 32 * b + lane;
-        int e = i < n ? __ldg(ids + i) : -1;
-        if (e < 0 || e >= E) e = -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        const int r = __popc(same & ((1u << lane) - 1u));
-        const int at = e >= 0 ? mine[e] + r : -1;
-        __syncwarp();
-        if (e >= 0 && r == 0) mine[e] += __popc(same);
-        __syncwarp();
-        if (i < n) p.position[i] = at;
-        if (at >= 0) {
-            p.order[at] = i;
-            p.scale_row[at] = 128 * block0[e] + at - first[e];
+    if (b1 - b0 > kSortAhead) load(b0);
+    for (int b = b0; b < b1; b += kSortAhead) {
+        if (b > b0) load(b);
+        const int most = min(kSortAhead, b1 - b);
+#pragma unroll
+        for (int j = 0; j < kSortAhead; ++j) {
+            if (j >= most) break;
+            const int i = 32 * (b + j) + lane;
+            const uint32_t same = __match_any_sync(0xffffffffu, e[j]);
+            const int r = __popc(same & ((1u << lane) - 1u));
+            int at = -1, within = 0;
+            if (e[j] >= 0) {
+                at = mine[e[j]] + r;
+                within = total[e[j]] - first[e[j]] + at;
+                at += total[e[j]];
+            }
+            __syncwarp();
+            if (e[j] >= 0 && r == 0) mine[e[j]] += __popc(same);
+            __syncwarp();
+            if (i < n) p.position[i] = at;
+            if (at >= 0) {
+                p.order[at] = i;
+                p.scale_row[at] = 128 * block0[e[j]] + within;
+            }
         }
     }
-    for (int i = used + rank * kSortThreads + tid; i < n; i += C * kSortThreads) {
+    for (int i = used_rows + rank * threads + tid; i < n; i += C * threads) {
         p.order[i] = -1;
         p.scale_row[i] = -1;
     }
-    if (C > 1) cluster_sync();  // no CTA leaves while another still reads its counts
 }
 
 // ---- rows ---------------------------------------------------------------------------------------
@@ -201,59 +220,85 @@ __device__ __forceinline__ void zero_tail(Raw* out, const PlanView& p, int64_t n
         out[used * vecs + i] = Raw{};
 }
 
+// A team of TEAM threads takes a token: a warp where there are many tokens (no block-wide step, and the loads of many
+// tokens in flight), a CTA where there are few.
 constexpr int kRowThreads = 256;
 constexpr int kSlotBatch = 8;  // slots whose rows are in flight together
 
+template <int TEAM>
+struct Team {
+    static constexpr int kPerCta = kRowThreads / TEAM;
+    static __device__ __forceinline__ int thread() { return static_cast<int>(threadIdx.x) % TEAM; }
+    static __device__ __forceinline__ int64_t first() {
+        return static_cast<int64_t>(blockIdx.x) * kPerCta + static_cast<int>(threadIdx.x) / TEAM;
+    }
+    static __device__ __forceinline__ int64_t step() { return static_cast<int64_t>(gridDim.x) * kPerCta; }
+};
+
+// Sorted rows (and weights) of slots j0 .. j0 + kSlotBatch - 1 of token t; -1 where there is none.
+template <bool WEIGHTED>
+__device__ __forceinline__ void load_slots(const PlanView& p, const float* weights, int64_t t, int j0, int (&at)[kSlotBatch],
+                                           float (&w)[kSlotBatch]) {
+    const int k = p.slots;
+#pragma unroll
+    for (int j = 0; j < kSlotBatch; ++j) at[j] = j0 + j < k ? __ldg(p.position + t * k + j0 + j) : -1;
+#pragma unroll
+    for (int j = 0; j < kSlotBatch; ++j) {
+        w[j] = 0.0f;
+        if (WEIGHTED && j0 + j < k) w[j] = __ldg(weights + t * k + j0 + j);
+    }
+}
+
 // XS[position of each slot of t] = X[t].
-template <class T, int V>
+template <class T, int V, int TEAM>
 __global__ void __launch_bounds__(kRowThreads) expert_gather_kernel(const typename Vec<T, V>::Raw* __restrict__ X,
                                                                     int64_t vecs, PlanView p,
                                                                     typename Vec<T, V>::Raw* __restrict__ XS) {
-    const int k = p.slots;
-    for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-        const int32_t* pos = p.position + t * k;
-        for (int64_t c = threadIdx.x; c < vecs; c += kRowThreads) {
-            const auto v = __ldg(X + t * vecs + c);
-            for (int j = 0; j < k; ++j) {
-                const int64_t at = __ldg(pos + j);
-                if (at >= 0) XS[at * vecs + c] = v;
+    for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
+        for (int j0 = 0; j0 < p.slots; j0 += kSlotBatch) {
+            int at[kSlotBatch];
+            float w[kSlotBatch];
+            load_slots<false>(p, nullptr, t, j0, at, w);
+            for (int64_t c = Team<TEAM>::thread(); c < vecs; c += TEAM) {
+                const auto v = __ldg(X + t * vecs + c);
+#pragma unroll
+                for (int j = 0; j < kSlotBatch; ++j)
+                    if (at[j] >= 0) XS[at[j] * vecs + c] = v;
             }
         }
     }
-    zero_tail(XS, p, p.tokens * k, vecs);
+    zero_tail(XS, p, p.tokens * p.slots, vecs);
 }
 
 // Y[t] = sum over slots of (weights or 1) * YS[position].
-template <class T, int V, bool WEIGHTED>
+template <class T, int V, int TEAM, bool WEIGHTED>
 __global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(const typename Vec<T, V>::Raw* __restrict__ YS,
                                                                      int64_t vecs, PlanView p,
                                                                      const float* __restrict__ weights,
                                                                      typename Vec<T, V>::Raw* __restrict__ Y) {
     using Raw = typename Vec<T, V>::Raw;
     const int k = p.slots;
-    for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-        const int32_t* pos = p.position + t * k;
-        const float* wt = weights + t * k;
-        for (int64_t c = threadIdx.x; c < vecs; c += kRowThreads) {
+    for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
+        int at[kSlotBatch];
+        float w[kSlotBatch];
+        load_slots<WEIGHTED>(p, weights, t, 0, at, w);
+        for (int64_t c = Team<TEAM>::thread(); c < vecs; c += TEAM) {
             float acc[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] = 0.0f;
             for (int j0 = 0; j0 < k; j0 += kSlotBatch) {
+                if (k > kSlotBatch) load_slots<WEIGHTED>(p, weights, t, j0, at, w);
                 Raw r[kSlotBatch];
-                int64_t at[kSlotBatch];
-#pragma unroll
-                for (int j = 0; j < kSlotBatch; ++j) at[j] = j0 + j < k ? __ldg(pos + j0 + j) : -1;
 #pragma unroll
                 for (int j = 0; j < kSlotBatch; ++j)
                     if (at[j] >= 0) r[j] = __ldg(YS + at[j] * vecs + c);
 #pragma unroll
                 for (int j = 0; j < kSlotBatch; ++j) {
                     if (at[j] < 0) continue;
-                    const float w = WEIGHTED ? __ldg(wt + j0 + j) : 1.0f;
                     float f[V];
                     Vec<T, V>::to_f32(r[j], f);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) acc[i] = WEIGHTED ? fmaf(w, f[i], acc[i]) : acc[i] + f[i];
+                    for (int i = 0; i < V; ++i) acc[i] = WEIGHTED ? fmaf(w[j], f[i], acc[i]) : acc[i] + f[i];
                 }
             }
             Y[t * vecs + c] = Vec<T, V>::from_f32(acc);
@@ -262,34 +307,31 @@ __global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(const typen
 }
 
 // dYS[position] = weights * dY[t], dWeights[t][j] = <dY[t], YS[position]>.
-template <class T, int V>
-__global__ void __launch_bounds__(kRowThreads) expert_combine_backward_kernel(
+template <class T, int V, int TEAM>
+__global__ void __launch_bounds__(kRowThreads, 2) expert_combine_backward_kernel(
     const typename Vec<T, V>::Raw* __restrict__ dY, const typename Vec<T, V>::Raw* __restrict__ YS, int64_t vecs,
     PlanView p, const float* __restrict__ weights, typename Vec<T, V>::Raw* __restrict__ dYS,
     float* __restrict__ dWeights) {
     using Raw = typename Vec<T, V>::Raw;
     __shared__ float part[kRowThreads / 32][kSlotBatch];
     const int k = p.slots, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-        const int32_t* pos = p.position + t * k;
+    for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
         for (int j0 = 0; j0 < k; j0 += kSlotBatch) {
-            int64_t at[kSlotBatch];
+            int at[kSlotBatch];
             float w[kSlotBatch], dot[kSlotBatch];
+            load_slots<true>(p, weights, t, j0, at, w);
 #pragma unroll
-            for (int j = 0; j < kSlotBatch; ++j) {
-                at[j] = j0 + j < k ? __ldg(pos + j0 + j) : -1;
-                w[j] = at[j] >= 0 ? __ldg(weights + t * k + j0 + j) : 0.0f;
-                dot[j] = 0.0f;
-            }
-            for (int64_t c = threadIdx.x; c < vecs; c += kRowThreads) {
-                float g[V];
-                Vec<T, V>::to_f32(__ldg(dY + t * vecs + c), g);
+            for (int j = 0; j < kSlotBatch; ++j) dot[j] = 0.0f;
+            for (int64_t c = Team<TEAM>::thread(); c < vecs; c += TEAM) {
+                const Raw gr = __ldg(dY + t * vecs + c);
                 Raw r[kSlotBatch];
                 if (dWeights) {
 #pragma unroll
                     for (int j = 0; j < kSlotBatch; ++j)
                         if (at[j] >= 0) r[j] = __ldg(YS + at[j] * vecs + c);
                 }
+                float g[V];
+                Vec<T, V>::to_f32(gr, g);
 #pragma unroll
                 for (int j = 0; j < kSlotBatch; ++j) {
                     if (at[j] < 0) continue;
@@ -305,28 +347,29 @@ __global__ void __launch_bounds__(kRowThreads) expert_combine_backward_kernel(
                 }
             }
             if (dWeights) {
+                float mine = 0.0f;  // lane j: the warp's sum of slot j0 + j
 #pragma unroll
                 for (int j = 0; j < kSlotBatch; ++j) {
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
-                    if (lane == 0) part[warp][j] = dot[j];
+                    if (lane == j) mine = dot[j];
                 }
-                __syncthreads();
-                if (threadIdx.x < kSlotBatch && j0 + static_cast<int>(threadIdx.x) < k) {
-                    float s = 0.0f;
-                    for (int q = 0; q < kRowThreads / 32; ++q) s += part[q][threadIdx.x];
-                    dWeights[t * k + j0 + threadIdx.x] = s;
+                if (TEAM == 32) {
+                    if (lane < kSlotBatch && j0 + lane < k) dWeights[t * k + j0 + lane] = mine;
+                } else {
+                    if (lane < kSlotBatch) part[warp][lane] = mine;
+                    __syncthreads();
+                    if (threadIdx.x < kSlotBatch && j0 + static_cast<int>(threadIdx.x) < k) {
+                        float s = 0.0f;
+                        for (int q = 0; q < kRowThreads / 32; ++q) s += part[q][threadIdx.x];
+                        dWeights[t * k + j0 + threadIdx.x] = s;
+                    }
+                    __syncthreads();
                 }
-                __syncthreads();
             }
         }
     }
     zero_tail(dYS, p, p.tokens * k, vecs);
-}
-
-int row_grid(int64_t tokens) {
-    // enough CTAs to fill the device several times over; each then walks tokens with that stride
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tokens, int64_t(device_sm_count()) * 32)));
 }
 
 bool vectorised(const void* a, const void* b, const void* c, int64_t row_bytes) {
@@ -343,29 +386,40 @@ typename Vec<T, V>::Raw* raw(void* p) {
     return static_cast<typename Vec<T, V>::Raw*>(p);
 }
 
-template <class T, int V>
+template <class T, int V, int TEAM>
 cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const PlanView& p, const float* weights,
                      void* out, float* dw, cudaStream_t stream) {
-    const int64_t vecs = D / V;
-    const int grid = row_grid(p.tokens);
+    const int64_t vecs = D / V, per = kRowThreads / TEAM;
+    // enough CTAs to fill the device several times over; each then walks tokens with that stride
+    const int grid = static_cast<int>(
+        std::max<int64_t>(1, std::min<int64_t>((p.tokens + per - 1) / per, int64_t(device_sm_count()) * 32)));
     switch (op) {
         case ExpertOp::Gather:
-            expert_gather_kernel<T, V><<<grid, kRowThreads, 0, stream>>>(raw<T, V>(a), vecs, p, raw<T, V>(out));
+            expert_gather_kernel<T, V, TEAM><<<grid, kRowThreads, 0, stream>>>(raw<T, V>(a), vecs, p, raw<T, V>(out));
             break;
         case ExpertOp::GatherBackward:
-            expert_combine_kernel<T, V, false><<<grid, kRowThreads, 0, stream>>>(raw<T, V>(a), vecs, p, nullptr,
-                                                                                 raw<T, V>(out));
+            expert_combine_kernel<T, V, TEAM, false><<<grid, kRowThreads, 0, stream>>>(raw<T, V>(a), vecs, p, nullptr,
+                                                                                       raw<T, V>(out));
             break;
         case ExpertOp::Combine:
-            expert_combine_kernel<T, V, true><<<grid, kRowThreads, 0, stream>>>(raw<T, V>(a), vecs, p, weights,
-                                                                                raw<T, V>(out));
+            expert_combine_kernel<T, V, TEAM, true><<<grid, kRowThreads, 0, stream>>>(raw<T, V>(a), vecs, p, weights,
+                                                                                      raw<T, V>(out));
             break;
         case ExpertOp::CombineBackward:
-            expert_combine_backward_kernel<T, V><<<grid, kRowThreads, 0, stream>>>(raw<T, V>(a), raw<T, V>(b), vecs, p,
-                                                                                   weights, raw<T, V>(out), dw);
+            expert_combine_backward_kernel<T, V, TEAM><<<grid, kRowThreads, 0, stream>>>(
+                raw<T, V>(a), raw<T, V>(b), vecs, p, weights, raw<T, V>(out), dw);
             break;
     }
     return cudaGetLastError();
+}
+
+template <class T, int V>
+cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const PlanView& p, const float* weights,
+                     void* out, float* dw, cudaStream_t stream) {
+    int team = p.tokens >= int64_t(device_sm_count()) * 16 ? 32 : kRowThreads;
+    if (const char* s = std::getenv("PNQ_TEAM")) team = std::atoi(s);
+    if (team == 32) return run_rows<T, V, 32>(op, a, b, D, p, weights, out, dw, stream);
+    return run_rows<T, V, kRowThreads>(op, a, b, D, p, weights, out, dw, stream);
 }
 
 }  // namespace
@@ -381,16 +435,19 @@ cudaError_t launch_expert_rows(ExpertOp op, bool bf16, const void* a, const void
 }
 
 cudaError_t launch_expert_sort(const int32_t* ids, const PlanView& p, cudaStream_t stream) {
-    const int n = static_cast<int>(p.tokens * p.slots);
-    const int smem = (kSortWarps + 3) * p.experts * static_cast<int>(sizeof(int));
+    const int n = static_cast<int>(p.tokens * p.slots), batches = (n + 31) / 32;
+    // Few slots: one warp per batch of 32 and a thread per expert. Many: CTAs of 32 warps, up to a portable cluster,
+    // before a warp takes a second batch.
+    const int C = std::max(1, std::min(8, (batches + 31) / 32));
+    const int warps = C > 1 ? 32 : std::max({1, batches, (p.experts + 31) / 32});
+    const int per = std::max(1, (batches + C * warps - 1) / (C * warps));
+    const int smem = (warps + 3) * p.experts * static_cast<int>(sizeof(int));
     // opt in to the most any number of experts needs (1024: 143,360 bytes), once per device
-    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(expert_sort_kernel), (kSortWarps + 3) * 1024 * 4);
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(expert_sort_kernel), (kSortThreads / 32 + 3) * 1024 * 4);
     if (e != cudaSuccess) return e;
-    // one CTA per 8192 slots, at most a portable cluster
-    const int C = std::max(1, std::min(8, (n + 8191) / 8192));
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3(C);
-    lc.blockDim = dim3(kSortThreads);
+    lc.blockDim = dim3(32 * warps);
     lc.dynamicSmemBytes = smem;
     lc.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -400,7 +457,7 @@ cudaError_t launch_expert_sort(const int32_t* ids, const PlanView& p, cudaStream
     attr[0].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, expert_sort_kernel, ids, n, p, C);
+    return cudaLaunchKernelEx(&lc, expert_sort_kernel, ids, n, p, C, per);
 }
 
 }  // namespace pnq

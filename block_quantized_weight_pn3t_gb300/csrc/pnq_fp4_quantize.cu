@@ -2,10 +2,14 @@
 // weights (NVFP4: groups of 16 with E4M3 scales, MXFP4: groups of 32 with power-of-two scales; layout and
 // definitions in include/pnq.h).
 //
-// All three are elementwise over K with a maximum per group: bound by HBM. A warp takes 256 consecutive
-// elements of a row, 8 per lane (one 16-byte load of bf16); the lanes of a group take its maximum by
-// shuffles, and each lane writes its 8 codes as one word. The scale words of four groups meet in one lane
-// and leave as one word (they are neighbours in the tiled layout).
+// All three are elementwise over K with a maximum per group: bound by HBM. A warp takes 1024 consecutive
+// elements of a row in four steps of 256, all four loads in flight at once (few rows: one step per warp, so
+// that more warps share them).
+//   encode: 8 elements per lane (one 16-byte load of bf16); the lanes of a group take its maximum by shuffles,
+//           each lane writes its 8 codes as one word; the scale words of four groups meet in one lane and leave
+//           as one word (they are neighbours in the tiled layout).
+//   decode: a lane loads the words of 8 codes and the warp exchanges them so that lane l writes elements 4 l ..
+//           4 l + 3 of 128: every store covers 512 contiguous bytes of fp32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -19,7 +23,6 @@ namespace pnq {
 namespace {
 
 constexpr int kQThreads = 256;
-constexpr int kItemElems = 256;  // elements of a row per warp and item
 
 // Byte offset of the word of four groups (chunk c) of tiled row r.
 __device__ __forceinline__ int64_t scale_word(int64_t r, int64_t c, int64_t chunks) {
@@ -54,6 +57,13 @@ __device__ __forceinline__ uint32_t f32_to_e4m3(float v) {
     return d & 0xFFu;
 }
 
+__device__ __forceinline__ __half2 u32_as_half2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+
+// Value of an E4M3FN word with its sign bit clear (a positive scale, or NaN).
+__device__ __forceinline__ float e4m3_bits_to_f32(uint32_t word) {
+    return __low2float(u32_as_half2(e4m3x2_to_f16x2(word)));
+}
+
 template <class T, bool VEC>
 __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
     if constexpr (sizeof(T) == 4) {
@@ -82,6 +92,15 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
     }
 }
 
+// x / s rounded to nearest, for s > 0 and r = 1 / s rounded to nearest: two fused steps after the first estimate
+// give the correctly rounded quotient (P. W. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990). Where the remainder underflows the quotient is far below the least nonzero
+// code's threshold. The sign is x's, of a zero too (the fused steps would make -0 a +0).
+__device__ __forceinline__ float divide(float x, float s, float r) {
+    const float q = x * r;
+    return copysignf(fmaf(fmaf(-q, s, x), r, q), x);
+}
+
 // Encodes this lane's 8 elements (live: the lane is inside the row): its scale word and its 8 codes. The
 // group's lanes (2 for NVFP4, 4 for MXFP4) are neighbours.
 template <bool MX>
@@ -106,101 +125,140 @@ __device__ __forceinline__ void encode8(float (&x)[8], bool live, float inv_g, u
 #pragma unroll
         for (int i = 0; i < 8; ++i) t[i] = x[i] * inv;
     } else {
-        word = finite ? f32_to_e4m3(__fdiv_rn(amax, 6.0f)) : 0x7Fu;
+        word = finite ? f32_to_e4m3(divide(amax, 6.0f, 1.0f / 6.0f)) : 0x7Fu;
         zero |= word == 0;
-        const float s = zero ? 1.0f : e4m3_to_f32(word);
+        const float s = zero ? 1.0f : e4m3_bits_to_f32(word), r = __frcp_rn(s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = __fdiv_rn(x[i], s);
+        for (int i = 0; i < 8; ++i) t[i] = divide(x[i], s, r);
     }
     codes = zero ? 0u : f32x8_to_e2m1(t);
     if (!live) word = 0;
 }
 
-template <bool MX, class T, bool VEC, bool PLAN>
+// STEPS steps of 256 elements per warp and item.
+template <bool MX, class T, bool VEC, bool PLAN, int STEPS>
 __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const T* __restrict__ X, int64_t ldx, int64_t rows,
                                                                  int64_t matrices, int K, float inv_g, PlanView p,
                                                                  uint8_t* __restrict__ codes, int64_t pitch,
-                                                                 uint8_t* __restrict__ scales, int64_t chunks) {
-    constexpr int kGroupLanes = MX ? 4 : 2;
+                                                                 uint8_t* __restrict__ scales, int chunks) {
+    constexpr int kGroupLanes = MX ? 4 : 2, kChunkElems = MX ? 128 : 64;
     const int lane = threadIdx.x & 31;
-    const int64_t per_row = (K + kItemElems - 1) / kItemElems, items = rows * matrices * per_row;
+    const int per_row = (K + STEPS * 256 - 1) / (STEPS * 256);
+    const int64_t items = rows * matrices * per_row;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kQThreads / 32);
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
-        const int64_t r = it / per_row;
-        const int k = static_cast<int>(it - r * per_row) * kItemElems + 8 * lane;
-        const bool live = k < K;
-        float x[8];
-        if (live) load8<T, VEC>(X + r * ldx + k, x);
-        uint32_t word, c;
-        encode8<MX>(x, live, inv_g, word, c);
-        // the words of four groups in one, in every lane of the four
-        word = lane % kGroupLanes == 0 ? word << (8 * (lane / kGroupLanes % 4)) : 0u;
-        word |= __shfl_xor_sync(0xffffffffu, word, kGroupLanes);
-        word |= __shfl_xor_sync(0xffffffffu, word, 2 * kGroupLanes);
-        const int64_t chunk = k / (MX ? 128 : 64);
-        const bool leads = lane % (4 * kGroupLanes) == 0 && chunk < chunks;
+        const int64_t r = items <= INT32_MAX ? static_cast<int32_t>(it) / per_row : it / per_row;
+        const int k0 = static_cast<int>(it - r * per_row) * (STEPS * 256) + 8 * lane;
+        float x[STEPS][8];
+#pragma unroll
+        for (int u = 0; u < STEPS; ++u)
+            if (k0 + 256 * u < K) load8<T, VEC>(X + r * ldx + k0 + 256 * u, x[u]);
+        // with a plan: where the row goes, lane j holding slot j's places
+        int at = -1, srow = 0;
+        if (PLAN && lane < p.slots) {
+            at = __ldg(p.position + r * p.slots + lane);
+            if (at >= 0) srow = __ldg(p.scale_row + at);
+        }
+        uint32_t word[STEPS], c[STEPS];
+#pragma unroll
+        for (int u = 0; u < STEPS; ++u) {
+            encode8<MX>(x[u], k0 + 256 * u < K, inv_g, word[u], c[u]);
+            // the words of four groups in one, in every lane of the four
+            word[u] = lane % kGroupLanes == 0 ? word[u] << (8 * (lane / kGroupLanes % 4)) : 0u;
+            word[u] |= __shfl_xor_sync(0xffffffffu, word[u], kGroupLanes);
+            word[u] |= __shfl_xor_sync(0xffffffffu, word[u], 2 * kGroupLanes);
+        }
+        auto put = [&](int64_t row, int64_t tiled) {
+            uint8_t* cp = codes + row * pitch + k0 / 2;
+            uint8_t* sp = scales + scale_word(tiled, 0, chunks);
+#pragma unroll
+            for (int u = 0; u < STEPS; ++u) {
+                const int k = k0 + 256 * u, chunk = k / kChunkElems;
+                if (k < K) *reinterpret_cast<uint32_t*>(cp + 128 * u) = c[u];
+                if (lane % (4 * kGroupLanes) == 0 && chunk < chunks) *reinterpret_cast<uint32_t*>(sp + chunk * 512) = word[u];
+            }
+        };
         if (!PLAN) {
-            if (live) *reinterpret_cast<uint32_t*>(codes + r * pitch + k / 2) = c;
-            if (leads) *reinterpret_cast<uint32_t*>(scales + scale_word(tiled_row(r, rows, matrices), chunk, chunks)) = word;
+            put(r, tiled_row(r, rows, matrices));
         } else {
-            for (int j = 0; j < p.slots; ++j) {
-                const int64_t at = __ldg(p.position + r * p.slots + j);
-                if (at < 0) continue;
-                if (live) *reinterpret_cast<uint32_t*>(codes + at * pitch + k / 2) = c;
-                if (leads)
-                    *reinterpret_cast<uint32_t*>(scales + scale_word(__ldg(p.scale_row + at), chunk, chunks)) = word;
+            for (int j0 = 0; j0 < p.slots; j0 += 32) {
+                if (j0) {
+                    at = -1;
+                    if (j0 + lane < p.slots) at = __ldg(p.position + r * p.slots + j0 + lane);
+                    if (at >= 0) srow = __ldg(p.scale_row + at);
+                }
+                for (int j = 0; j < min(32, p.slots - j0); ++j) {
+                    const int row = __shfl_sync(0xffffffffu, at, j), tiled = __shfl_sync(0xffffffffu, srow, j);
+                    if (row >= 0) put(row, tiled);
+                }
             }
         }
     }
 }
 
-// A lane decodes 8 codes: out = fp32(e2m1 * s * g), the first product exact.
-template <bool MX, class T, bool VEC>
+// Four elements -> out at o.
+template <class T, bool VEC>
+__device__ __forceinline__ void store4(T* o, float a, float b, float c, float d) {
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (VEC) *reinterpret_cast<float4*>(o) = make_float4(a, b, c, d);
+        else o[0] = a, o[1] = b, o[2] = c, o[3] = d;
+    } else {
+        const uint32_t lo = f32x2_to_bf16x2(a, b), hi = f32x2_to_bf16x2(c, d);
+        if constexpr (VEC) {
+            *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
+        } else {
+            uint16_t* h = reinterpret_cast<uint16_t*>(o);
+            h[0] = static_cast<uint16_t>(lo), h[1] = static_cast<uint16_t>(lo >> 16);
+            h[2] = static_cast<uint16_t>(hi), h[3] = static_cast<uint16_t>(hi >> 16);
+        }
+    }
+}
+
+// out = fp32(e2m1 * s * g), the first product exact.
+template <bool MX, class T, bool VEC, int STEPS>
 __global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const uint8_t* __restrict__ codes, int64_t pitch,
-                                                                   const uint8_t* __restrict__ scales, int64_t chunks,
+                                                                   const uint8_t* __restrict__ scales, int chunks,
                                                                    int64_t rows, int64_t matrices, int K, float g,
                                                                    const int32_t* __restrict__ scale_row,
                                                                    T* __restrict__ out) {
-    const int64_t per_row = K / 8, items = rows * matrices * per_row;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kQThreads;
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x; it < items; it += step) {
-        const int64_t r = it / per_row;
-        const int k = static_cast<int>(it - r * per_row) * 8;
-        const int64_t sr = scale_row ? __ldg(scale_row + r) : tiled_row(r, rows, matrices);
-        float v[8];
-        if (sr >= 0) {
-            const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(codes + r * pitch + k / 2));
-            const int group = k / (MX ? 32 : 16);
-            const uint32_t word = __ldg(scales + scale_word(sr, group >> 2, chunks) + (group & 3));
-            const float s = !MX ? e4m3_to_f32(word)
-                            : word == 255u ? __uint_as_float(0x7FC00000u)
-                            : word == 0u   ? __uint_as_float(0x00400000u)  // 2^-127
-                                           : __uint_as_float(word << 23);
+    constexpr int kChunkElems = MX ? 128 : 64, kChunksStep = 256 / kChunkElems;
+    const int lane = threadIdx.x & 31;
+    const int per_row = (K + STEPS * 256 - 1) / (STEPS * 256);
+    const int64_t items = rows * matrices * per_row;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kQThreads / 32);
+    for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
+        const int64_t r = items <= INT32_MAX ? static_cast<int32_t>(it) / per_row : it / per_row;
+        const int k0 = static_cast<int>(it - r * per_row) * (STEPS * 256);
+        const int64_t sr = scale_row ? __ldg(scale_row + r) : tiled_row(r, rows, matrices);  // -1: a row not in use
+        uint32_t c[STEPS], w = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(e2m1_to_f32((c >> (4 * i)) & 15u), s), g);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        for (int u = 0; u < STEPS; ++u) {
+            const int k = k0 + 256 * u + 8 * lane;
+            c[u] = sr >= 0 && k < K ? __ldg(reinterpret_cast<const uint32_t*>(codes + r * pitch + k / 2)) : 0u;
         }
-        T* o = out + r * static_cast<int64_t>(K) + k;
-        if constexpr (sizeof(T) == 4) {
-            if constexpr (VEC) {
-                reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
+        // lane j holds the scale words of the item's chunk j
+        const int chunk = k0 / kChunkElems + lane;
+        if (sr >= 0 && lane < STEPS * kChunksStep && chunk < chunks)
+            w = __ldg(reinterpret_cast<const uint32_t*>(scales + scale_word(sr, chunk, chunks)));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = v[i];
-            }
-        } else {
-            uint32_t w[4];
+        for (int u = 0; u < STEPS; ++u) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = f32x2_to_bf16x2(v[2 * i], v[2 * i + 1]);
-            if constexpr (VEC) {
-                *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-                uint16_t* h = reinterpret_cast<uint16_t*>(o);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+            for (int h = 0; h < 2; ++h) {  // lane l: elements 4 l .. 4 l + 3 of this half of the step
+                const uint32_t four = __shfl_sync(0xffffffffu, c[u], 16 * h + (lane >> 1)) >> (16 * (lane & 1));
+                const int group = (128 * h + 4 * lane) / (kChunkElems / 4);  // within the step
+                const uint32_t word = __shfl_sync(0xffffffffu, w, u * kChunksStep + (group >> 2)) >> (8 * (group & 3)) & 255u;
+                float s = MX ? (word == 255u ? __uint_as_float(0x7FC00000u)
+                                : word == 0u ? __uint_as_float(0x00400000u)  // 2^-127
+                                             : __uint_as_float(word << 23))
+                             : e4m3_bits_to_f32(word);
+                if (sr < 0) s = 0.0f;
+                const float2 a = __half22float2(u32_as_half2(e2m1x2_to_f16x2<0>(four)));
+                const float2 b = __half22float2(u32_as_half2(e2m1x2_to_f16x2<1>(four)));
+                const int k = k0 + 256 * u + 128 * h + 4 * lane;
+                if (k < K)
+                    store4<T, VEC>(out + r * static_cast<int64_t>(K) + k, __fmul_rn(__fmul_rn(a.x, s), g),
+                                   __fmul_rn(__fmul_rn(a.y, s), g), __fmul_rn(__fmul_rn(b.x, s), g),
+                                   __fmul_rn(__fmul_rn(b.y, s), g));
             }
         }
     }
@@ -252,34 +310,50 @@ int item_grid(int64_t items, int per_cta) {
         std::max<int64_t>(1, std::min<int64_t>((items + per_cta - 1) / per_cta, int64_t(device_sm_count()) * 8)));
 }
 
+// Whether the rows fill the device's warps with items of 1024 elements; otherwise items of 256.
+bool many_items(int64_t rows, int64_t K) { return rows * ((K + 1023) / 1024) >= int64_t(device_sm_count()) * 16; }
+
+template <bool MX, class T, bool VEC, bool PLAN, int STEPS>
+void run_quantize(const T* x, int64_t ldx, int64_t rows, int64_t K, int64_t matrices, float inv_g, const PlanView& p,
+                  uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
+    const int64_t items = rows * matrices * ((K + STEPS * 256 - 1) / (STEPS * 256));
+    fp4_quantize_kernel<MX, T, VEC, PLAN, STEPS><<<item_grid(items, kQThreads / 32), kQThreads, 0, stream>>>(
+        x, ldx, rows, matrices, static_cast<int>(K), inv_g, p, codes, fp4_pitch(K), scales, static_cast<int>(fp4_chunks(MX, K)));
+}
+
 template <bool MX, class T, bool VEC>
 void run_quantize(const void* X, int64_t ldx, int64_t rows, int64_t K, int64_t matrices, float inv_g, const PlanView& p,
                   uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
-    const int64_t items = rows * matrices * ((K + kItemElems - 1) / kItemElems);
-    const int grid = item_grid(items, kQThreads / 32);
-    const int64_t pitch = fp4_pitch(K), chunks = fp4_chunks(MX, K);
     const T* x = static_cast<const T*>(X);
-    if (p.experts)
-        fp4_quantize_kernel<MX, T, VEC, true><<<grid, kQThreads, 0, stream>>>(x, ldx, rows, matrices, static_cast<int>(K),
-                                                                              inv_g, p, codes, pitch, scales, chunks);
-    else
-        fp4_quantize_kernel<MX, T, VEC, false><<<grid, kQThreads, 0, stream>>>(x, ldx, rows, matrices, static_cast<int>(K),
-                                                                               inv_g, p, codes, pitch, scales, chunks);
+    const bool many = many_items(rows * matrices, K);
+    if (p.experts) {
+        if (many) run_quantize<MX, T, VEC, true, 4>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+        else run_quantize<MX, T, VEC, true, 1>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+    } else {
+        if (many) run_quantize<MX, T, VEC, false, 4>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+        else run_quantize<MX, T, VEC, false, 1>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+    }
+}
+
+template <bool MX, class T, bool VEC, int STEPS>
+void run_dequantize(const Fp4View& v, int64_t K, float g, const PlanView& p, T* out, cudaStream_t stream) {
+    const int64_t items = v.rows * v.matrices * ((K + STEPS * 256 - 1) / (STEPS * 256));
+    fp4_dequantize_kernel<MX, T, VEC, STEPS><<<item_grid(items, kQThreads / 32), kQThreads, 0, stream>>>(
+        v.codes, fp4_pitch(K), v.scales, static_cast<int>(fp4_chunks(MX, K)), v.rows, v.matrices, static_cast<int>(K), g,
+        p.experts ? p.scale_row : nullptr, out);
 }
 
 template <bool MX, class T>
 void run_dequantize(const Fp4View& v, int64_t K, float g, const PlanView& p, void* out, cudaStream_t stream) {
-    const int grid = item_grid(v.rows * v.matrices * (K / 8), kQThreads);
-    const int64_t pitch = fp4_pitch(K), chunks = fp4_chunks(MX, K);
-    const int32_t* sr = p.experts ? p.scale_row : nullptr;
     T* o = static_cast<T*>(out);
-    // rows of K elements (a multiple of 8) keep the base's 16-byte alignment
-    if (reinterpret_cast<uintptr_t>(out) % 16 == 0)
-        fp4_dequantize_kernel<MX, T, true><<<grid, kQThreads, 0, stream>>>(v.codes, pitch, v.scales, chunks, v.rows,
-                                                                           v.matrices, static_cast<int>(K), g, sr, o);
-    else
-        fp4_dequantize_kernel<MX, T, false><<<grid, kQThreads, 0, stream>>>(v.codes, pitch, v.scales, chunks, v.rows,
-                                                                            v.matrices, static_cast<int>(K), g, sr, o);
+    const bool many = many_items(v.rows * v.matrices, K);
+    // rows of K elements (a multiple of 16) keep the base's 16-byte alignment
+    if (reinterpret_cast<uintptr_t>(out) % 16 == 0) {
+        if (many) run_dequantize<MX, T, true, 4>(v, K, g, p, o, stream);
+        else run_dequantize<MX, T, true, 1>(v, K, g, p, o, stream);
+    } else {
+        run_dequantize<MX, T, false, 1>(v, K, g, p, o, stream);
+    }
 }
 
 }  // namespace
