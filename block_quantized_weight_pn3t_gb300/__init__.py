@@ -13,7 +13,7 @@ from ._binding import (PN3T, PN4T, NVFP4, NVFP4_DIV, Q4G64_F16S, Q5G64_F16S, Q6G
 
 # the 4-bit operands and the expert layer work on torch tensors throughout: their module (and torch) is
 # imported at the first use of one of its names
-_FP4_NAMES = ("MXFP4", "FP4_GROUP", "Fp4Matrix", "ExpertPlan", "pnq_expert_plan", "fp4_lib", "fp4_layout", "fp4_quantize",
+_FP4_NAMES = ("MXFP4", "FP4_GROUP", "Fp4Matrix", "ExpertPlan", "fp4_lib", "fp4_layout", "fp4_quantize",
               "fp4_dequantize", "fp4_pack", "fp4_gemm", "fp4_gemm_experts", "expert_sort", "expert_gather",
               "expert_gather_backward", "expert_combine", "expert_combine_backward")
 

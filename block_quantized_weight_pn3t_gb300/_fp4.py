@@ -13,6 +13,7 @@ the pnq_fp4_* and pnq_expert_* entry points (formats, layouts and rounding steps
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -24,10 +25,8 @@ FP4_GROUP = {NVFP4: 16, MXFP4: 32}
 _FLOAT = {torch.float32: 0, torch.bfloat16: 1}
 
 
-class pnq_expert_plan(ctypes.Structure):
-    _fields_ = [("offsets", ctypes.c_void_p), ("block_start", ctypes.c_void_p), ("order", ctypes.c_void_p),
-                ("position", ctypes.c_void_p), ("scale_row", ctypes.c_void_p), ("tokens", ctypes.c_int64),
-                ("slots", ctypes.c_int32), ("experts", ctypes.c_int32)]
+# struct pnq_expert_plan of include/pnq.h: five device addresses, tokens, slots, experts
+_PLAN = struct.Struct("@5Pqii")
 
 
 _P, _I64, _I, _F, _U = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_uint
@@ -183,23 +182,21 @@ class ExpertPlan:
     """How the (token, slot) choices of an expert layer are sorted by expert: one int32 CUDA buffer that holds, one
     after the other, offsets [experts + 1], block_start [experts + 1], order [n], position [n] and scale_row [n]
     (n = tokens * slots; meanings in ``include/pnq.h``, pnq_expert_plan)."""
-    __slots__ = ("tokens", "slots", "experts", "rows", "buffer", "device_index", "descriptor", "ref")
+    __slots__ = ("tokens", "slots", "experts", "rows", "buffer", "device_index", "ref")
 
     def __init__(self, tokens: int, slots: int, experts: int, buffer=None, device=None):
         n = tokens * slots
         size = 2 * (experts + 1) + 3 * n
         if buffer is None:
             buffer = torch.empty(size, dtype=torch.int32, device=device)
-        if not (isinstance(buffer, torch.Tensor) and buffer.dtype is torch.int32 and buffer.is_cuda and buffer.numel() >= size
+        elif not (isinstance(buffer, torch.Tensor) and buffer.dtype is torch.int32 and buffer.is_cuda and buffer.numel() >= size
                 and buffer.is_contiguous()):
             _refuse(buffer, "plan buffer", torch.int32, None, size)
         self.tokens, self.slots, self.experts, self.rows, self.buffer = tokens, slots, experts, n, buffer
         self.device_index = buffer.get_device()
         at = buffer.data_ptr()
         order = at + 8 * (experts + 1)
-        self.descriptor = pnq_expert_plan(at, at + 4 * (experts + 1), order, order + 4 * n, order + 8 * n, tokens, slots,
-                                          experts)
-        self.ref = ctypes.addressof(self.descriptor)
+        self.ref = _PLAN.pack(at, at + 4 * (experts + 1), order, order + 4 * n, order + 8 * n, tokens, slots, experts)
 
     def _part(self, first: int, count: int):
         return self.buffer.narrow(0, first, count)
@@ -417,7 +414,7 @@ def _rows(t, what: str, rows: int, plan: ExpertPlan):
 def _rows_out(out, like, rows: int, D: int, plan: ExpertPlan):
     """(out or a new one like `like`, address)."""
     if out is None:
-        out = torch.empty((rows, D), dtype=like.dtype, device=like.device)
+        out = like.new_empty((rows, D))
         return out, out.data_ptr()
     return out, _matrix(out, "out", like.dtype, rows, D, plan.device_index)
 

@@ -141,6 +141,19 @@ cudaError_t opt_in_smem(const void* kernel, int bytes) {
     return e;
 }
 
+cudaError_t opt_in_cluster(const void* kernel) {
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, bool> done;
+    const int dev = current_device();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    bool& have = done[{kernel, dev}];
+    if (have) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) have = true;
+    return e;
+}
+
 int device_sm_count() {
     static std::atomic<int> counts[kMaxDevices];
     const int dev = current_device();

@@ -10,7 +10,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <cstdlib>
 
 #include "pnq_device.cuh"
 #include "pnq_internal.h"
@@ -20,17 +19,23 @@ namespace {
 
 // ---- the plan -----------------------------------------------------------------------------------
 //
-// Counting sort of n expert ids by a cluster of C CTAs (C = 1..8) of W warps each, one launch:
+// Counting sort of n expert ids by a cluster of C CTAs (C = 1..16) of W warps each:
 //   1. every warp counts the experts of its own run of consecutive slots (shared-memory histogram per
 //      warp);
 //   2. a prefix over the CTA's warps, then over the cluster's CTAs (distributed shared memory), then
 //      over the experts, turns the counts into each warp's first sorted row per expert;
 //   3. every warp walks its run again, 32 slots at a time: lanes with the same expert rank themselves by
-//      lane (match), so equal experts keep the order of their slots.
+//      lane, so equal experts keep the order of their slots. The lanes with the same expert are found by a
+//      ballot for each bit of its number (a match instruction costs an SM some 64 cycles: 131072 slots over 128
+//      experts took 21 us with it).
+// Many slots (C > 1): the sorted side's words (order, scale_row) are written by a second kernel on the whole device,
+// from position: they scatter, one sector a word, and eight SMs would take longer over those stores than over all
+// the rest (131072 slots over 128 experts: 20.5 us in one launch).
 // The work is a chain of latencies, not bytes: a warp's ids are loaded kSortAhead batches at a time and, where one
 // such load holds its whole run, once for both passes.
 constexpr int kSortThreads = 1024;
-constexpr int kSortAhead = 16;
+constexpr int kSortAhead = 8;
+constexpr int kSortCluster = 16;  // the largest a device may run; not a portable size, this is one device's code
 
 __device__ __forceinline__ int ld_dsmem_s32(uint32_t local_addr, uint32_t rank) {
     return __float_as_int(ld_dsmem_f32(local_addr, rank));
@@ -53,8 +58,9 @@ __device__ __forceinline__ unsigned long long block_exclusive_scan(unsigned long
     return before + s - v;
 }
 
+template <bool MANY>
 __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int32_t* __restrict__ ids, int n, PlanView p,
-                                                                     int C, int per) {
+                                                                     int C, int per, int bits) {
     extern __shared__ int sort_smem[];
     const int E = p.experts, W = static_cast<int>(blockDim.x) >> 5;
     int* hist = sort_smem;        // [W][E]
@@ -102,7 +108,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int3
         total[tid] = count;
     }
     int before = 0, all = count;
-    if (C > 1) {
+    if (MANY) {
         cluster_sync();
         if (tid < E) {
             all = 0;
@@ -113,7 +119,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int3
             }
         }
     }
-    if (C > 1) cluster_sync();  // every CTA has read the counts: they may be written over, and the CTAs may leave
+    if (MANY) cluster_sync();  // every CTA has read the counts: they may be written over, and the CTAs may leave
     // rows and 128-row blocks before expert tid, in one scan
     const unsigned long long pre =
         block_exclusive_scan((static_cast<unsigned long long>((all + 127) / 128) << 32) | static_cast<unsigned>(all), warp_sums);
@@ -141,27 +147,46 @@ __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int3
         for (int j = 0; j < kSortAhead; ++j) {
             if (j >= most) break;
             const int i = 32 * (b + j) + lane;
-            const uint32_t same = __match_any_sync(0xffffffffu, e[j]);
-            const int r = __popc(same & ((1u << lane) - 1u));
-            int at = -1, within = 0;
-            if (e[j] >= 0) {
-                at = mine[e[j]] + r;
-                within = total[e[j]] - first[e[j]] + at;
-                at += total[e[j]];
+            const uint32_t key = e[j] >= 0 ? static_cast<uint32_t>(e[j]) : static_cast<uint32_t>(E);
+            uint32_t same = 0xffffffffu;
+            for (int q = 0; q < bits; ++q) {
+                const bool one = (key >> q) & 1u;
+                const uint32_t ones = __ballot_sync(0xffffffffu, one);
+                same &= one ? ones : ~ones;
             }
+            const int r = __popc(same & ((1u << lane) - 1u));
+            const int at = e[j] >= 0 ? mine[e[j]] + total[e[j]] + r : -1;
             __syncwarp();
             if (e[j] >= 0 && r == 0) mine[e[j]] += __popc(same);
             __syncwarp();
             if (i < n) p.position[i] = at;
-            if (at >= 0) {
+            if (!MANY && at >= 0) {
                 p.order[at] = i;
-                p.scale_row[at] = 128 * block0[e[j]] + within;
+                p.scale_row[at] = 128 * block0[e[j]] + at - first[e[j]];
             }
         }
     }
-    for (int i = used_rows + rank * threads + tid; i < n; i += C * threads) {
-        p.order[i] = -1;
-        p.scale_row[i] = -1;
+    if (!MANY)
+        for (int i = used_rows + tid; i < n; i += threads) {
+            p.order[i] = -1;
+            p.scale_row[i] = -1;
+        }
+}
+
+// order and scale_row from position (many slots).
+__global__ void __launch_bounds__(256) expert_order_kernel(const int32_t* __restrict__ ids, int n, PlanView p) {
+    const int used = __ldg(p.offsets + p.experts);
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
+        const int at = __ldg(p.position + i);
+        if (at >= 0) {
+            const int e = __ldg(ids + i);
+            p.order[at] = i;
+            p.scale_row[at] = 128 * __ldg(p.block_start + e) + at - __ldg(p.offsets + e);
+        }
+        if (i >= used) {
+            p.order[i] = -1;
+            p.scale_row[i] = -1;
+        }
     }
 }
 
@@ -416,9 +441,11 @@ cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const
 template <class T, int V>
 cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const PlanView& p, const float* weights,
                      void* out, float* dw, cudaStream_t stream) {
-    int team = p.tokens >= int64_t(device_sm_count()) * 16 ? 32 : kRowThreads;
-    if (const char* s = std::getenv("PNQ_TEAM")) team = std::atoi(s);
-    if (team == 32) return run_rows<T, V, 32>(op, a, b, D, p, weights, out, dw, stream);
+    // A warp per token where the tokens give every SM 16 warps (16384 tokens of 2048 bf16, 8 slots: combine 97 us against 112
+    // with a CTA per token, its gradients 178 against 204; 7 tokens of 1999 fp32 take 28 us by warps and 5 by CTAs). The
+    // gather of a row that a CTA takes in one step or more keeps the CTA (93 us against 96).
+    const bool warps = p.tokens >= int64_t(device_sm_count()) * 16 && (op != ExpertOp::Gather || D / V < kRowThreads);
+    if (warps) return run_rows<T, V, 32>(op, a, b, D, p, weights, out, dw, stream);
     return run_rows<T, V, kRowThreads>(op, a, b, D, p, weights, out, dw, stream);
 }
 
@@ -436,14 +463,16 @@ cudaError_t launch_expert_rows(ExpertOp op, bool bf16, const void* a, const void
 
 cudaError_t launch_expert_sort(const int32_t* ids, const PlanView& p, cudaStream_t stream) {
     const int n = static_cast<int>(p.tokens * p.slots), batches = (n + 31) / 32;
-    // Few slots: one warp per batch of 32 and a thread per expert. Many: CTAs of 32 warps, up to a portable cluster,
+    // Few slots: one warp per batch of 32 and a thread per expert. Many: CTAs of 32 warps, up to the largest cluster,
     // before a warp takes a second batch.
-    const int C = std::max(1, std::min(8, (batches + 31) / 32));
+    const int C = std::max(1, std::min(kSortCluster, (batches + 31) / 32));
     const int warps = C > 1 ? 32 : std::max({1, batches, (p.experts + 31) / 32});
     const int per = std::max(1, (batches + C * warps - 1) / (C * warps));
     const int smem = (warps + 3) * p.experts * static_cast<int>(sizeof(int));
+    const auto kern = C > 1 ? expert_sort_kernel<true> : expert_sort_kernel<false>;
     // opt in to the most any number of experts needs (1024: 143,360 bytes), once per device
-    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(expert_sort_kernel), (kSortThreads / 32 + 3) * 1024 * 4);
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), (kSortThreads / 32 + 3) * 1024 * 4);
+    if (e == cudaSuccess && C > 8) e = opt_in_cluster(reinterpret_cast<const void*>(kern));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3(C);
@@ -457,7 +486,13 @@ cudaError_t launch_expert_sort(const int32_t* ids, const PlanView& p, cudaStream
     attr[0].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, expert_sort_kernel, ids, n, p, C, per);
+    int bits = 1;  // of the numbers 0 .. experts (the last: a dropped slot)
+    while ((p.experts >> bits) != 0) ++bits;
+    e = cudaLaunchKernelEx(&lc, kern, ids, n, p, C, per, bits);
+    if (e != cudaSuccess || C == 1) return e;
+    const int grid = std::min((n + 255) / 256, device_sm_count() * 8);
+    expert_order_kernel<<<grid, 256, 0, stream>>>(ids, n, p);
+    return cudaGetLastError();
 }
 
 }  // namespace pnq

@@ -34,6 +34,9 @@ int* device_error_word();
 // Raises a kernel's dynamic shared memory limit to `bytes`, once per (kernel, device).
 cudaError_t opt_in_smem(const void* kernel, int bytes);
 
+// Allows a kernel clusters of more than 8 CTAs, once per (kernel, device).
+cudaError_t opt_in_cluster(const void* kernel);
+
 // 2-D tensor map over a row-major u32 matrix [rows][row_u32] (row pitch a multiple of 16
 // bytes) with box {box_x, box_y}; rows past the end read as zeros. swizzle_128b: the copy
 // stores 16-byte chunk c of box row r at chunk c ^ (r % 8) of that row (box rows of 128 bytes,

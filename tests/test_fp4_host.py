@@ -23,8 +23,14 @@ def lib():
     return pnq.fp4_lib()
 
 
+class Plan(ctypes.Structure):
+    """struct pnq_expert_plan of include/pnq.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("offsets", "block_start", "order", "position", "scale_row")] + \
+        [("tokens", ctypes.c_int64), ("slots", ctypes.c_int32), ("experts", ctypes.c_int32)]
+
+
 def plan(tokens=4, slots=2, experts=3, **other):
-    p = pnq.pnq_expert_plan(FAKE, FAKE, FAKE, FAKE, FAKE, tokens, slots, experts)
+    p = Plan(FAKE, FAKE, FAKE, FAKE, FAKE, tokens, slots, experts)
     for k, v in other.items():
         setattr(p, k, v)
     return p
