@@ -26,6 +26,7 @@
 #include <cstdlib>
 #include <map>
 #include <mutex>
+#include <tuple>
 #include <utility>
 
 #include "pnq_device.cuh"
@@ -44,6 +45,7 @@ constexpr int kEpilogueThreads = 32 * kEpilogueWarps;
 constexpr int kThreads = 64 + kEpilogueThreads;  // producer, MMA, epilogue
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxStages = 10;
+constexpr int kMaxSplit = 8;                   // CTAs of a cluster that share a tile's K
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kStaticSmem = 6 * 1024;          // barriers, expert tiles (rounded up)
 
@@ -58,7 +60,9 @@ struct GemmArgs {
     int M, N, K;             // activation rows, weight rows of a matrix, K
     int chunks;              // scale tiles along K per 128-row block
     int weights_once;        // every weight row is read by one tile only
+    int static_weights;      // dense: no earlier kernel in flight writes the weights
     int ks;                  // CTAs of a cluster that share a tile's K (1: none)
+    int xbox;                // activation rows of a copy: as many copies as a tile's rows need
 };
 
 template <bool MX, int BN, int CG>
@@ -206,6 +210,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         }
         mbar_init(finished, 1);
         mbar_fence_init();
+        prefetch_tensor_map(&map_w);
+        prefetch_tensor_map(&map_ws);
+        prefetch_tensor_map(&map_x);
+        prefetch_tensor_map(&map_xs);
     }
     if constexpr (CG == 2) {
         cluster_sync();  // the pair's barriers exist before either CTA signals them
@@ -213,7 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     } else {
         if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), P::kCols);
     }
-    griddep_wait();  // nothing above reads what an earlier kernel wrote
+    // nothing above reads what an earlier kernel wrote; static weights: nor do the first copies below, and their thread
+    // waits after them
+    const bool early = a.static_weights && a.p.experts == 0;
+    if (!early || warp != 0) griddep_wait();
     if (a.p.experts > 0) {
         // tiles before each expert: a block scan, each thread over consecutive experts
         const int E = a.p.experts, nt = (a.N + CG * kRows - 1) / (CG * kRows), per = (E + kThreads - 1) / kThreads;
@@ -257,28 +268,60 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
             bool ok = true;
             int s = 0, issued = 0;
             uint32_t phase = 1;  // the first wait for each free stage passes
+            auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t pol) {
+                if constexpr (CG == 2) tma_load_2d_pair(dst, map, x, y, bar, pol);
+                else tma_load_2d(dst, map, x, y, bar, pol);
+            };
+            // of the tile in turn: coordinates at K = 0, copies and bytes of a stage. All of it outside the loop over K: this
+            // one thread's instructions are a stage's turn where a tile is small.
+            int wrow = 0, wsc = 0, xrow = 0, xsc = 0, xcopies = 0;
+            uint32_t bytes = 0;
+            auto take = [&] {
+                const int n0 = tile.n0 + static_cast<int>(rank) * kRows;
+                wrow = tile.e * a.N + n0;
+                wsc = (tile.e * blocks_w + n0 / 128) * a.chunks;
+                xrow = tile.row0 + static_cast<int>(rank) * (BN / CG);
+                xsc = tile.sblock * a.chunks;
+                // rows past the tile's activations are not copied: their columns are not stored (and a copy's rows past
+                // the end of the matrix, filled with zeros, take longer than rows that are there)
+                xcopies = CG == 2 ? 1 : (tile.rows + a.xbox - 1) / a.xbox;  // a pair's CTAs copy one half each
+                bytes = static_cast<uint32_t>(CG * (P::kStage - P::kCodesB + xcopies * a.xbox * (kStageK / 2)));
+            };
+            auto load_weights = [&](int i, int kt) {
+                const uint32_t st = sbase + static_cast<uint32_t>(i * P::kStage), bar = CG == 2 ? cluster_addr(full(i), 0) : full(i);
+                if (rank == 0) mbar_arrive_expect_tx(full(i), bytes);
+                load(st, &map_w, kt * kStageWords, wrow, bar, pol_w);
+                load(st + kCodesA + P::kCodesB, &map_ws, 0, wsc + kt * P::kTiles, bar, pol_w);
+            };
+            int ahead = 0;  // stages of the first tile whose weights are under way
+            if (early) {
+                Walk<BN, CG> first(a, starts);
+                if (first.next(tile)) {
+                    take();
+                    for (; ahead < min(S, kt1 - kt0); ++ahead) load_weights(ahead, kt0 + ahead);
+                }
+                griddep_wait();
+            }
             while (ok && walk.next(tile)) {
-                const int n0 = tile.n0 + static_cast<int>(rank) * kRows, wrow = tile.e * a.N + n0;
-                const int xrow = tile.row0 + static_cast<int>(rank) * (BN / CG);
-                const int wsc = (tile.e * blocks_w + n0 / 128) * a.chunks, xsc = tile.sblock * a.chunks;
+                take();
                 for (int kt = kt0; kt < kt1; ++kt) {
-                    if (!mbar_wait_cycles(empty(s), phase)) {
-                        ok = false;
-                        break;
+                    if (issued >= ahead) {
+                        if (!mbar_wait_cycles(empty(s), phase)) {
+                            ok = false;
+                            break;
+                        }
+                        load_weights(s, kt);
                     }
-                    const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage), sc = st + kCodesA + P::kCodesB;
-                    if (rank == 0) mbar_arrive_expect_tx(full(s), CG * P::kStage);
-                    const uint32_t bar = CG == 2 ? cluster_addr(full(s), 0) : full(s);
-                    auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t pol) {
-                        if constexpr (CG == 2) tma_load_2d_pair(dst, map, x, y, bar, pol);
-                        else tma_load_2d(dst, map, x, y, bar, pol);
-                    };
-                    load(st, &map_w, kt * kStageWords, wrow, pol_w);
-                    load(sc, &map_ws, 0, wsc + kt * P::kTiles, pol_w);
-                    load(st + kCodesA, &map_x, kt * kStageWords, xrow, pol_x);
+                    const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage), bar = CG == 2 ? cluster_addr(full(s), 0) : full(s);
+                    load(st + kCodesA, &map_x, kt * kStageWords, xrow, bar, pol_x);
+#pragma unroll 1
+                    for (int c = 1; c < xcopies; ++c)
+                        load(st + kCodesA + static_cast<uint32_t>(c * a.xbox * (kStageK / 2)), &map_x, kt * kStageWords,
+                             xrow + c * a.xbox, bar, pol_x);
 #pragma unroll
                     for (int b = 0; b < P::kBlocksB; ++b)
-                        load(sc + P::kScalesA * (1 + b), &map_xs, 0, xsc + b * a.chunks + kt * P::kTiles, pol_x);
+                        load(st + kCodesA + P::kCodesB + P::kScalesA * (1 + b), &map_xs, 0, xsc + b * a.chunks + kt * P::kTiles, bar,
+                             pol_x);
                     ++issued;
                     if (++s == S) s = 0, phase ^= 1;
                 }
@@ -317,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                     const int steps = min(4, (a.K - kt * kStageK + 63) / 64);  // K past the end: no MMA
                     const int now = s;
                     if (++s == S) s = 0, phase ^= 1;
-                    peek = mbar_try_wait(full(s), phase);  // a probe takes some 100 cycles: over before the next stage's turn
+                    peek = mbar_test(full(s), phase);  // a probe takes some 100 cycles: over before the next stage's turn
 #pragma unroll
                     for (int j = 0; j < P::kTiles; ++j) {
                         tmem_copy_scales<CG>(sfa + 4 * j, ds + (j * kScaleTile >> 4));
@@ -423,12 +466,23 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         if (again.next(tile)) {
             T* Y = static_cast<T*>(a.Y);
             const float scale = a.w_global ? a.alpha * __ldg(a.w_global + tile.e) : a.alpha;
+            // a thread sums four rows of a column: its loads from all the CTAs are in flight together
             const int c0 = kz * tile.rows / a.ks, c1 = (kz + 1) * tile.rows / a.ks;
-            for (int e = static_cast<int>(threadIdx.x); e < (c1 - c0) * kRows; e += kThreads) {
-                const int c = c0 + e / kRows, r = e % kRows;
-                float v = 0.0f;
-                for (int z = 0; z < a.ks; ++z) v += ld_dsmem_f32(sbase + 4u * static_cast<uint32_t>(c * kRows + r), static_cast<uint32_t>(z));
-                if (tile.n0 + r < a.N) store_y(Y + static_cast<int64_t>(tile.row0 + c) * a.N + tile.n0 + r, v * scale);
+            for (int e = static_cast<int>(threadIdx.x); e < (c1 - c0) * (kRows / 4); e += kThreads) {
+                const int c = c0 + e / (kRows / 4), r = 4 * (e % (kRows / 4));
+                const uint32_t at = sbase + 4u * static_cast<uint32_t>(c * kRows + r);
+                float4 v[kMaxSplit];
+#pragma unroll
+                for (int z = 0; z < kMaxSplit; ++z)
+                    if (z < a.ks) v[z] = ld_dsmem_f32x4(cluster_addr(at, static_cast<uint32_t>(z)));
+                float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int z = 0; z < kMaxSplit; ++z)
+                    if (z < a.ks) f[0] += v[z].x, f[1] += v[z].y, f[2] += v[z].z, f[3] += v[z].w;
+                T* y = Y + static_cast<int64_t>(tile.row0 + c) * a.N + tile.n0 + r;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (tile.n0 + r + i < a.N) store_y(y + i, f[i] * scale);
             }
         }
         cluster_sync();  // no CTA leaves while another still reads its tile
@@ -440,33 +494,49 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     }
 }
 
-// CTA pairs of a kernel that the current device holds at once (not every group of SMs is even).
-cudaError_t resident_pairs(const void* kernel, cudaLaunchConfig_t lc, int* pairs) {
+// Clusters of x by y CTAs of a kernel that the current device holds at once (not every group of SMs divides evenly).
+cudaError_t resident_clusters(const void* kernel, int smem, int x, int y, int* clusters) {
     static std::mutex mu;
-    static std::map<std::pair<const void*, int>, int> known;
+    static std::map<std::tuple<const void*, int, int, int>, int> known;
     int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
-    int& n = known[{kernel, dev}];
+    int& n = known[{kernel, dev, x, y}];
     if (n == 0) {
-        lc.gridDim = dim3(2 * static_cast<unsigned>(device_sm_count()));
-        lc.numAttrs = 1;  // the cluster alone
-        const cudaError_t q = cudaOccupancyMaxActiveClusters(&n, kernel, &lc);
-        if (q != cudaSuccess) return q;
+        e = opt_in_smem(kernel, smem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t lc{};
+        lc.gridDim = dim3(static_cast<unsigned>(x * device_sm_count()), static_cast<unsigned>(y));
+        lc.blockDim = dim3(kThreads);
+        lc.dynamicSmemBytes = static_cast<size_t>(smem);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(x);
+        attr[0].val.clusterDim.y = static_cast<unsigned>(y);
+        attr[0].val.clusterDim.z = 1;
+        lc.attrs = attr;
+        lc.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &lc);
+        if (e != cudaSuccess) return e;
         n = std::max(n, 1);
     }
-    *pairs = n;
+    *clusters = n;
     return cudaSuccess;
 }
 
+template <bool MX, int BN, int CG>
+constexpr int gemm_smem() {
+    return Plan<MX, BN, CG>::kStages * Plan<MX, BN, CG>::kStage + 1024;
+}
+
 template <bool MX, int BN, int CG, class T>
-cudaError_t run_gemm(const CUtensorMap (&maps)[4], GemmArgs a, int64_t tiles, cudaStream_t stream) {
+cudaError_t run_gemm(const CUtensorMap (&maps)[4], const GemmArgs& a, int64_t tiles, cudaStream_t stream) {
     using P = Plan<MX, BN, CG>;
     static_assert(P::kStages * P::kStage >= BN * kRows * 4, "a partial tile fits the stages");
-    constexpr int smem = P::kStages * P::kStage + 1024;
+    constexpr int smem = gemm_smem<MX, BN, CG>();
     auto kern = fp4_gemm_kernel<MX, BN, CG, T>;
-    const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem);
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc{};
     lc.blockDim = dim3(kThreads);
@@ -488,34 +558,48 @@ cudaError_t run_gemm(const CUtensorMap (&maps)[4], GemmArgs a, int64_t tiles, cu
         lc.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, device_sm_count())));
     } else {
         int pairs = 0;
-        const cudaError_t q = resident_pairs(reinterpret_cast<const void*>(kern), lc, &pairs);
-        if (q != cudaSuccess) return q;
-        lc.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs)));
+        e = resident_clusters(reinterpret_cast<const void*>(kern), smem, CG, 1, &pairs);
+        if (e != cudaSuccess) return e;
+        lc.gridDim = dim3(static_cast<unsigned>(CG * std::min<int64_t>(tiles, pairs)));
     }
     return cudaLaunchKernelEx(&lc, kern, maps[0], maps[1], maps[2], maps[3], a);
 }
 
 template <bool MX, int BN, int CG = 1>
-cudaError_t run_out(bool bf16, const Fp4View& x, const Fp4View& w, int64_t K, const GemmArgs& a, int64_t tiles,
+cudaError_t run_out(bool bf16, const Fp4View& x, const Fp4View& w, int64_t K, GemmArgs a, int64_t tiles,
                     cudaStream_t stream) {
     using P = Plan<MX, BN, CG>;
+    // the tile's rows in one copy; by experts, with few rows each, in copies of 32 (full tiles of 128 in copies of 32 took
+    // 12 percent longer)
+    a.xbox = static_cast<int>(std::min<int64_t>(BN / CG, a.p.experts && x.rows < 32ll * a.p.experts ? 32 : x.rows));
+    if (CG == 2) a.xbox = BN / CG;
     const int64_t nt = (w.rows + kRows - 1) / kRows;  // 128-row scale blocks of a matrix
     // 128-row scale blocks that a copy may touch: by experts the operand has room for any distribution
     const int64_t xblocks = a.p.experts ? (x.rows + 127 * std::min<int64_t>(a.p.experts, x.rows)) / 128 : (x.rows + 127) / 128;
     CUtensorMap maps[4];
     if (!encode_u32_map_pitch(&maps[0], w.codes, w.rows * w.matrices, K / 8, fp4_pitch(K), kStageWords, kRows, true) ||
         !encode_u32_map(&maps[1], w.scales, nt * w.matrices * a.chunks, 128, 128, P::kTiles) ||
-        !encode_u32_map_pitch(&maps[2], x.codes, x.rows, K / 8, fp4_pitch(K), kStageWords, BN / CG, true) ||
+        !encode_u32_map_pitch(&maps[2], x.codes, x.rows, K / 8, fp4_pitch(K), kStageWords, a.xbox, true) ||
         !encode_u32_map(&maps[3], x.scales, xblocks * a.chunks, 128, 128, P::kTiles))
         return cudaErrorInvalidValue;
     return bf16 ? run_gemm<MX, BN, CG, __nv_bfloat16>(maps, a, tiles, stream)
                 : run_gemm<MX, BN, CG, float>(maps, a, tiles, stream);
 }
 
+// A tile shape: columns, CTAs per tile, and what a stage of K, a further tile of a CTA, and the last one cost beyond
+// its stages (us; the first two over long sums and many tiles on products of 17408 rows, the third as the difference
+// of one-tile products; a tile's cost is what its stores and the change of accumulators leave uncovered).
+struct Shape {
+    int bn, cg;
+    double stage, tile, last;
+};
+constexpr Shape kShapes[] = {{32, 1, 0.25, 0.6, 0.0}, {64, 1, 0.25, 0.7, 0.3}, {128, 1, 0.21, 1.0, 0.8}, {256, 2, 0.30, 1.9, 2.4}};
+constexpr Shape kExpertShapes[] = {{64, 1, 0, 0, 0}, {128, 1, 0, 0, 0}, {256, 1, 0, 0, 0}};
+
 }  // namespace
 
 cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t K, const PlanView& p, float alpha,
-                            const float* w_global, bool bf16, void* Y, int* err, bool /*static_weights*/,
+                            const float* w_global, bool bf16, void* Y, int* err, bool static_weights,
                             cudaStream_t stream) {
     GemmArgs a{};
     a.Y = Y;
@@ -527,34 +611,57 @@ cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t
     a.N = static_cast<int>(w.rows);
     a.K = static_cast<int>(K);
     a.chunks = static_cast<int>(fp4_chunks(mx, K));
-    // activation rows of a tile: of the matrix, or of an expert on average
-    const int64_t rows = p.experts ? (x.rows + p.experts - 1) / p.experts : x.rows;
-    int bn = rows <= 32 && !p.experts ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
-    const int64_t nk = (K + kStageK - 1) / kStageK;
-    auto count = [&](int tile_n, int tile_m) {
-        const int64_t mt = p.experts ? std::min<int64_t>(x.rows, x.rows / tile_m + std::min<int64_t>(p.experts, x.rows))
-                                     : (x.rows + tile_m - 1) / tile_m;
-        return (w.rows + tile_n - 1) / tile_n * mt;
-    };
-    int pair = bn == 256;
-    if (const char* s = std::getenv("PNQ_FP4_CFG")) {
-        int b = 0, c = 0;
-        if (std::sscanf(s, "%d,%d", &b, &c) == 2) bn = b, pair = c;
-    }
-    const int64_t tiles = count(pair ? 2 * kRows : kRows, bn);
-    a.weights_once = p.experts ? rows <= bn : x.rows <= bn;
+    a.static_weights = static_weights;
     a.ks = 1;
-    if (!pair && bn <= 128)
-        while (a.ks < 8 && tiles * (a.ks + 1) <= device_sm_count() && nk >= 4 * (a.ks + 1)) ++a.ks;
+    const int64_t nk = (K + kStageK - 1) / kStageK;
+    auto count = [&](const Shape& s) {
+        const int64_t mt = p.experts ? std::min<int64_t>(x.rows, x.rows / s.bn + std::min<int64_t>(p.experts, x.rows))
+                                     : (x.rows + s.bn - 1) / s.bn;
+        return (w.rows + s.cg * kRows - 1) / (s.cg * kRows) * mt;
+    };
+    Shape best{};
+    if (p.experts) {
+        // the experts' loads are not known here: by the rows in all, and by the average. 64 columns where no expert can
+        // have more (one token, 8 of 64 experts of 1408 x 2048: 8.4 us, 10.1 with 128), 256 where most tiles fill
+        // them (512 rows each: 57 us, 59 with 128; 256 rows each: 39 us, 38 with 128)
+        best = kExpertShapes[x.rows <= 64 ? 0 : x.rows < 384ll * p.experts ? 1 : 2];
+        a.weights_once = best.bn < 256;
+    } else {
+        // the shape, and the share of K, whose estimate is least
+        double least = 0.0;
+        for (const Shape& s : kShapes) {
+            if (s.bn == 32 && x.rows > 32) continue;
+            const int64_t tiles = count(s);
+            for (int ks = 1; ks <= (s.cg == 1 ? kMaxSplit : 1) && (ks == 1 || nk >= 3 * ks); ++ks) {
+                int slots = device_sm_count() / s.cg;
+                if (ks > 1) {
+                    // clusters of any shape hold one CTA per SM: the 64-column kernel answers for all
+                    const cudaError_t e = resident_clusters(reinterpret_cast<const void*>(fp4_gemm_kernel<false, 64, 1, float>),
+                                                            gemm_smem<false, 64, 1>(), 1, ks, &slots);
+                    if (e != cudaSuccess) return e;
+                    if (tiles > slots) break;  // one tile per cluster, all at once
+                }
+                const double waves = static_cast<double>((tiles + slots - 1) / slots);
+                const double stages = static_cast<double>((nk + ks - 1) / ks);
+                double t = waves * stages * s.stage + (waves - 1.0) * s.tile + s.last;
+                if (ks > 1) t += 1.6 + 0.01 * static_cast<double>(std::min<int64_t>(s.bn, x.rows));  // the cluster's sum
+                if (least == 0.0 || t < least) least = t, best = s, a.ks = ks;
+            }
+        }
+        a.weights_once = x.rows <= best.bn;
+    }
+    if (const char* s = std::getenv("PNQ_FP4_CFG")) {
+        std::sscanf(s, "%d,%d,%d", &best.bn, &best.cg, &a.ks);
+    }
+    const int64_t tiles = count(best);
     auto go = [&](auto m) {
         constexpr bool MX = decltype(m)::value;
-        switch (bn) {
+        switch (best.bn) {
             case 32: return run_out<MX, 32>(bf16, x, w, K, a, tiles, stream);
             case 64: return run_out<MX, 64>(bf16, x, w, K, a, tiles, stream);
-            case 128: return pair ? run_out<MX, 128, 2>(bf16, x, w, K, a, tiles, stream)
-                                  : run_out<MX, 128>(bf16, x, w, K, a, tiles, stream);
-            default: return pair ? run_out<MX, 256, 2>(bf16, x, w, K, a, tiles, stream)
-                                 : run_out<MX, 256>(bf16, x, w, K, a, tiles, stream);
+            case 128: return run_out<MX, 128>(bf16, x, w, K, a, tiles, stream);
+            default: return best.cg == 2 ? run_out<MX, 256, 2>(bf16, x, w, K, a, tiles, stream)
+                                         : run_out<MX, 256>(bf16, x, w, K, a, tiles, stream);
         }
     };
     return mx ? go(std::true_type{}) : go(std::false_type{});
