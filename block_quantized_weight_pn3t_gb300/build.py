@@ -1,16 +1,19 @@
-"""Builds libpnq.so in-tree: one nvcc process per translation unit, in parallel, for sm_103a."""
+"""Builds libpnq.so in-tree (one nvcc process per translation unit, in parallel, for sm_103a) and _native.so, the torch
+wrappers of the 4-bit operands and the expert layer (g++ against the installed torch), beside it."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpnq.so")
+NATIVE = os.path.join(PKG, "_native.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["pnq_api.cu", "pnq_codec_kernels.cu", "pnq_gemv_simt.cu", "pnq_gemv_pn.cu", "pnq_gemv_nvfp4.cu",
            "pnq_grouped.cu", "pnq_quantize.cu", "pnq_prefill.cu", "pnq_fp4_api.cu", "pnq_fp4_quantize.cu",
@@ -34,6 +37,31 @@ def _deps(src: str) -> list[str]:
         [os.path.join(INCLUDE, "pnq.h"), src]
 
 
+def _torch_dir() -> str:
+    import importlib.util
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found: it is required to build the torch wrappers")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _native_compile(nv: str):
+    """The compile command of pnq_torch.cpp, or None where its object is up to date for this torch and Python."""
+    src, obj, stamp = (os.path.join(CSRC, "pnq_torch.cpp"), os.path.join(BUILD_DIR, "pnq_torch.o"),
+                       os.path.join(BUILD_DIR, "pnq_torch.stamp"))
+    torch_dir = _torch_dir()
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        key = torch_dir + "\n" + f.read() + sysconfig.get_config_var("EXT_SUFFIX")
+    have = open(stamp).read() if os.path.exists(stamp) else None
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "pnq.h")))
+    if have == key and os.path.exists(obj) and os.path.getmtime(obj) >= newest:
+        return None
+    cuda_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nv))), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda_include, "-c", src, "-o", obj]
+    return cmd, stamp, key
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     nv = nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -45,6 +73,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         o = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
         if force or not os.path.exists(o) or os.path.getmtime(o) < max(os.path.getmtime(d) for d in _deps(s)):
             jobs.append([nv, *flags, "-c", s, "-o", o])
+    native = _native_compile(nv)
+    if native is not None:
+        jobs.append(native[0])
     if verbose:
         for j in jobs:
             print(" ".join(j))
@@ -65,6 +96,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         if r.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if jobs or force or not os.path.exists(NATIVE):
+        torch_lib = os.path.join(_torch_dir(), "lib")
+        tmp = NATIVE + f".tmp{os.getpid()}"
+        cmd = ["g++", "-shared", "-o", tmp, os.path.join(BUILD_DIR, "pnq_torch.o"), "-L", PKG, "-l:libpnq.so", "-L", torch_lib, "-lc10",
+               "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, NATIVE)
+        if native is not None:
+            with open(native[1], "w") as f:
+                f.write(native[2])
     return LIB
 
 
