@@ -205,6 +205,12 @@ __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wa
 __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// The first step of a kernel launched by launch_dependent: the kernels before it are done and their writes seen; the
+// next kernel may be launched (it waits in the same place).
+__device__ __forceinline__ void griddep_begin() {
+    griddep_wait();
+    griddep_launch_dependents();
+}
 
 // ---- cluster ------------------------------------------------------------------
 

@@ -62,6 +62,7 @@ template <bool MANY>
 __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int32_t* __restrict__ ids, int n, PlanView p,
                                                                      int C, int per, int bits) {
     extern __shared__ int sort_smem[];
+    griddep_begin();
     const int E = p.experts, W = static_cast<int>(blockDim.x) >> 5;
     int* hist = sort_smem;        // [W][E]
     int* total = hist + W * E;    // [E] counts of this CTA
@@ -175,6 +176,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int3
 
 // order and scale_row from position (many slots).
 __global__ void __launch_bounds__(256) expert_order_kernel(const int32_t* __restrict__ ids, int n, PlanView p) {
+    griddep_begin();
     const int used = __ldg(p.offsets + p.experts);
     for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
         const int at = __ldg(p.position + i);
@@ -279,6 +281,7 @@ template <class T, int V, int TEAM>
 __global__ void __launch_bounds__(kRowThreads) expert_gather_kernel(const typename Vec<T, V>::Raw* __restrict__ X,
                                                                     int64_t vecs, PlanView p,
                                                                     typename Vec<T, V>::Raw* __restrict__ XS) {
+    griddep_begin();
     for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
         for (int j0 = 0; j0 < p.slots; j0 += kSlotBatch) {
             int at[kSlotBatch];
@@ -303,6 +306,7 @@ __global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(const typen
                                                                      typename Vec<T, V>::Raw* __restrict__ Y) {
     using Raw = typename Vec<T, V>::Raw;
     const int k = p.slots;
+    griddep_begin();
     for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
         int at[kSlotBatch];
         float w[kSlotBatch];
@@ -340,6 +344,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) expert_combine_backward_kernel
     using Raw = typename Vec<T, V>::Raw;
     __shared__ float part[kRowThreads / 32][kSlotBatch];
     const int k = p.slots, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    griddep_begin();
     for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
         for (int j0 = 0; j0 < k; j0 += kSlotBatch) {
             int at[kSlotBatch];
@@ -420,22 +425,18 @@ cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const
         std::max<int64_t>(1, std::min<int64_t>((p.tokens + per - 1) / per, int64_t(device_sm_count()) * 32)));
     switch (op) {
         case ExpertOp::Gather:
-            expert_gather_kernel<T, V, TEAM><<<grid, kRowThreads, 0, stream>>>(raw<T, V>(a), vecs, p, raw<T, V>(out));
-            break;
+            return launch_dependent(expert_gather_kernel<T, V, TEAM>, grid, kRowThreads, stream, raw<T, V>(a), vecs, p,
+                                    raw<T, V>(out));
         case ExpertOp::GatherBackward:
-            expert_combine_kernel<T, V, TEAM, false><<<grid, kRowThreads, 0, stream>>>(raw<T, V>(a), vecs, p, nullptr,
-                                                                                       raw<T, V>(out));
-            break;
+            return launch_dependent(expert_combine_kernel<T, V, TEAM, false>, grid, kRowThreads, stream, raw<T, V>(a), vecs, p,
+                                    nullptr, raw<T, V>(out));
         case ExpertOp::Combine:
-            expert_combine_kernel<T, V, TEAM, true><<<grid, kRowThreads, 0, stream>>>(raw<T, V>(a), vecs, p, weights,
-                                                                                      raw<T, V>(out));
-            break;
-        case ExpertOp::CombineBackward:
-            expert_combine_backward_kernel<T, V, TEAM><<<grid, kRowThreads, 0, stream>>>(
-                raw<T, V>(a), raw<T, V>(b), vecs, p, weights, raw<T, V>(out), dw);
-            break;
+            return launch_dependent(expert_combine_kernel<T, V, TEAM, true>, grid, kRowThreads, stream, raw<T, V>(a), vecs, p,
+                                    weights, raw<T, V>(out));
+        default:
+            return launch_dependent(expert_combine_backward_kernel<T, V, TEAM>, grid, kRowThreads, stream, raw<T, V>(a),
+                                    raw<T, V>(b), vecs, p, weights, raw<T, V>(out), dw);
     }
-    return cudaGetLastError();
 }
 
 template <class T, int V>
@@ -479,20 +480,21 @@ cudaError_t launch_expert_sort(const int32_t* ids, const PlanView& p, cudaStream
     lc.blockDim = dim3(32 * warps);
     lc.dynamicSmemBytes = smem;
     lc.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(C);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
-    lc.numAttrs = 1;
+    lc.numAttrs = 2;
     int bits = 1;  // of the numbers 0 .. experts (the last: a dropped slot)
     while ((p.experts >> bits) != 0) ++bits;
     e = cudaLaunchKernelEx(&lc, kern, ids, n, p, C, per, bits);
     if (e != cudaSuccess || C == 1) return e;
     const int grid = std::min((n + 255) / 256, device_sm_count() * 8);
-    expert_order_kernel<<<grid, 256, 0, stream>>>(ids, n, p);
-    return cudaGetLastError();
+    return launch_dependent(expert_order_kernel, grid, 256, stream, ids, n, p);
 }
 
 }  // namespace pnq

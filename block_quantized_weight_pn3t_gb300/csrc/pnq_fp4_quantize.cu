@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const T* __rest
     const int per_row = (K + STEPS * 256 - 1) / (STEPS * 256);
     const int64_t items = rows * matrices * per_row;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kQThreads / 32);
+    griddep_begin();
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
         const int64_t r = items <= INT32_MAX ? static_cast<int32_t>(it) / per_row : it / per_row;
         const int k0 = static_cast<int>(it - r * per_row) * (STEPS * 256) + 8 * lane;
@@ -226,6 +227,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const uint8_t
     const int per_row = (K + STEPS * 256 - 1) / (STEPS * 256);
     const int64_t items = rows * matrices * per_row;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kQThreads / 32);
+    griddep_begin();
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
         const int64_t r = items <= INT32_MAX ? static_cast<int32_t>(it) / per_row : it / per_row;
         const int k0 = static_cast<int>(it - r * per_row) * (STEPS * 256);
@@ -270,6 +272,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_tile_scales_kernel(const uint8_
                                                                     int64_t matrices, int64_t groups, int64_t chunks,
                                                                     uint8_t* __restrict__ out) {
     const int64_t padded = (rows + 127) / 128 * 128, items = matrices * padded * chunks;
+    griddep_begin();
     const int64_t step = static_cast<int64_t>(gridDim.x) * kQThreads;
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x; it < items; it += step) {
         const int64_t r = it / chunks, c = it - r * chunks, m = r / padded, rr = r - m * padded;
@@ -289,6 +292,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_tile_scales_kernel(const uint8_
 __global__ void __launch_bounds__(kQThreads) fp4_pitch_codes_kernel(const uint8_t* __restrict__ in, int64_t rows,
                                                                     int64_t half, int64_t pitch, uint8_t* __restrict__ out) {
     const int64_t words = pitch / 8, items = rows * words;
+    griddep_begin();
     const int64_t step = static_cast<int64_t>(gridDim.x) * kQThreads;
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x; it < items; it += step) {
         const int64_t r = it / words, b = 8 * (it - r * words);
@@ -314,45 +318,45 @@ int item_grid(int64_t items, int per_cta) {
 bool many_items(int64_t rows, int64_t K) { return rows * ((K + 1023) / 1024) >= int64_t(device_sm_count()) * 16; }
 
 template <bool MX, class T, bool VEC, bool PLAN, int STEPS>
-void run_quantize(const T* x, int64_t ldx, int64_t rows, int64_t K, int64_t matrices, float inv_g, const PlanView& p,
+cudaError_t run_quantize(const T* x, int64_t ldx, int64_t rows, int64_t K, int64_t matrices, float inv_g, const PlanView& p,
                   uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
     const int64_t items = rows * matrices * ((K + STEPS * 256 - 1) / (STEPS * 256));
-    fp4_quantize_kernel<MX, T, VEC, PLAN, STEPS><<<item_grid(items, kQThreads / 32), kQThreads, 0, stream>>>(
-        x, ldx, rows, matrices, static_cast<int>(K), inv_g, p, codes, fp4_pitch(K), scales, static_cast<int>(fp4_chunks(MX, K)));
+    return launch_dependent(fp4_quantize_kernel<MX, T, VEC, PLAN, STEPS>, item_grid(items, kQThreads / 32), kQThreads, stream, x,
+                            ldx, rows, matrices, K, inv_g, p, codes, fp4_pitch(K), scales, fp4_chunks(MX, K));
 }
 
 template <bool MX, class T, bool VEC>
-void run_quantize(const void* X, int64_t ldx, int64_t rows, int64_t K, int64_t matrices, float inv_g, const PlanView& p,
+cudaError_t run_quantize(const void* X, int64_t ldx, int64_t rows, int64_t K, int64_t matrices, float inv_g, const PlanView& p,
                   uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
     const T* x = static_cast<const T*>(X);
     const bool many = many_items(rows * matrices, K);
     if (p.experts) {
-        if (many) run_quantize<MX, T, VEC, true, 4>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
-        else run_quantize<MX, T, VEC, true, 1>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+        if (many) return run_quantize<MX, T, VEC, true, 4>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+        else return run_quantize<MX, T, VEC, true, 1>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
     } else {
-        if (many) run_quantize<MX, T, VEC, false, 4>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
-        else run_quantize<MX, T, VEC, false, 1>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+        if (many) return run_quantize<MX, T, VEC, false, 4>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+        else return run_quantize<MX, T, VEC, false, 1>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
     }
 }
 
 template <bool MX, class T, bool VEC, int STEPS>
-void run_dequantize(const Fp4View& v, int64_t K, float g, const PlanView& p, T* out, cudaStream_t stream) {
+cudaError_t run_dequantize(const Fp4View& v, int64_t K, float g, const PlanView& p, T* out, cudaStream_t stream) {
     const int64_t items = v.rows * v.matrices * ((K + STEPS * 256 - 1) / (STEPS * 256));
-    fp4_dequantize_kernel<MX, T, VEC, STEPS><<<item_grid(items, kQThreads / 32), kQThreads, 0, stream>>>(
-        v.codes, fp4_pitch(K), v.scales, static_cast<int>(fp4_chunks(MX, K)), v.rows, v.matrices, static_cast<int>(K), g,
-        p.experts ? p.scale_row : nullptr, out);
+    return launch_dependent(fp4_dequantize_kernel<MX, T, VEC, STEPS>, item_grid(items, kQThreads / 32), kQThreads, stream,
+                            v.codes, fp4_pitch(K), v.scales, fp4_chunks(MX, K), v.rows, v.matrices, K, g,
+                            p.experts ? p.scale_row : nullptr, out);
 }
 
 template <bool MX, class T>
-void run_dequantize(const Fp4View& v, int64_t K, float g, const PlanView& p, void* out, cudaStream_t stream) {
+cudaError_t run_dequantize(const Fp4View& v, int64_t K, float g, const PlanView& p, void* out, cudaStream_t stream) {
     T* o = static_cast<T*>(out);
     const bool many = many_items(v.rows * v.matrices, K);
     // rows of K elements (a multiple of 16) keep the base's 16-byte alignment
     if (reinterpret_cast<uintptr_t>(out) % 16 == 0) {
-        if (many) run_dequantize<MX, T, true, 4>(v, K, g, p, o, stream);
-        else run_dequantize<MX, T, true, 1>(v, K, g, p, o, stream);
+        if (many) return run_dequantize<MX, T, true, 4>(v, K, g, p, o, stream);
+        else return run_dequantize<MX, T, true, 1>(v, K, g, p, o, stream);
     } else {
-        run_dequantize<MX, T, false, 1>(v, K, g, p, o, stream);
+        return run_dequantize<MX, T, false, 1>(v, K, g, p, o, stream);
     }
 }
 
@@ -365,41 +369,32 @@ cudaError_t launch_fp4_quantize(bool mx, bool bf16, const void* X, int64_t ldx, 
     auto go = [&](auto m) {
         constexpr bool MX = decltype(m)::value;
         if (bf16) {
-            if (vec) run_quantize<MX, __nv_bfloat16, true>(X, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
-            else run_quantize<MX, __nv_bfloat16, false>(X, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+            if (vec) return run_quantize<MX, __nv_bfloat16, true>(X, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+            else return run_quantize<MX, __nv_bfloat16, false>(X, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
         } else {
-            if (vec) run_quantize<MX, float, true>(X, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
-            else run_quantize<MX, float, false>(X, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+            if (vec) return run_quantize<MX, float, true>(X, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+            else return run_quantize<MX, float, false>(X, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
         }
     };
-    if (mx) go(std::true_type{});
-    else go(std::false_type{});
-    return cudaGetLastError();
+    return mx ? go(std::true_type{}) : go(std::false_type{});
 }
 
 cudaError_t launch_fp4_dequantize(bool mx, const Fp4View& v, int64_t K, float g, const PlanView& p, bool bf16, void* out,
                                   cudaStream_t stream) {
-    if (mx) {
-        if (bf16) run_dequantize<true, __nv_bfloat16>(v, K, g, p, out, stream);
-        else run_dequantize<true, float>(v, K, g, p, out, stream);
-    } else {
-        if (bf16) run_dequantize<false, __nv_bfloat16>(v, K, g, p, out, stream);
-        else run_dequantize<false, float>(v, K, g, p, out, stream);
-    }
-    return cudaGetLastError();
+    if (mx)
+        return bf16 ? run_dequantize<true, __nv_bfloat16>(v, K, g, p, out, stream) : run_dequantize<true, float>(v, K, g, p, out, stream);
+    return bf16 ? run_dequantize<false, __nv_bfloat16>(v, K, g, p, out, stream) : run_dequantize<false, float>(v, K, g, p, out, stream);
 }
 
 cudaError_t launch_fp4_pack(bool mx, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
                             int64_t matrices, uint8_t* codes_out, uint8_t* scales_out, cudaStream_t stream) {
     const int64_t chunks = fp4_chunks(mx, K), padded = (rows + 127) / 128 * 128;
-    fp4_tile_scales_kernel<<<item_grid(matrices * padded * chunks, kQThreads), kQThreads, 0, stream>>>(
-        scales, rows, matrices, K / (mx ? 32 : 16), chunks, scales_out);
-    if (codes_out != codes) {
-        const int64_t pitch = fp4_pitch(K);
-        fp4_pitch_codes_kernel<<<item_grid(matrices * rows * (pitch / 8), kQThreads), kQThreads, 0, stream>>>(
-            codes, matrices * rows, K / 2, pitch, codes_out);
-    }
-    return cudaGetLastError();
+    cudaError_t e = launch_dependent(fp4_tile_scales_kernel, item_grid(matrices * padded * chunks, kQThreads), kQThreads, stream, scales,
+                                     rows, matrices, K / (mx ? 32 : 16), chunks, scales_out);
+    if (e != cudaSuccess || codes_out == codes) return e;
+    const int64_t pitch = fp4_pitch(K);
+    return launch_dependent(fp4_pitch_codes_kernel, item_grid(matrices * rows * (pitch / 8), kQThreads), kQThreads, stream, codes,
+                            matrices * rows, K / 2, pitch, codes_out);
 }
 
 }  // namespace pnq

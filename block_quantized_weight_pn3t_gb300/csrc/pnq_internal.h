@@ -108,6 +108,22 @@ cudaError_t launch_nvfp4_gemv_mma(const Nvfp4View& w, int64_t N, int64_t K, cons
                                   float* Y, int* err, int cluster, int stages, bool static_weights,
                                   cudaStream_t stream);
 
+// Launches a kernel that begins with griddep_wait() so that its launch and first instructions overlap the end of the
+// kernel before it on the stream (programmatic dependent launch).
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int block, cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(static_cast<unsigned>(grid));
+    lc.blockDim = dim3(static_cast<unsigned>(block));
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, static_cast<Params>(args)...);
+}
+
 // ---- expert layer (pnq_experts.cu) ------------------------------------------------------------
 
 // pnq_expert_plan of the C ABI (all pointers device); no plan: tokens = rows, experts = 0.
