@@ -254,7 +254,8 @@ constexpr int kSlotBatch = 8;  // slots whose rows are in flight together
 
 template <int TEAM>
 struct Team {
-    static constexpr int kPerCta = kRowThreads / TEAM;
+    static constexpr int kThreads = TEAM > kRowThreads ? TEAM : kRowThreads;  // of a CTA
+    static constexpr int kPerCta = kThreads / TEAM;
     static __device__ __forceinline__ int thread() { return static_cast<int>(threadIdx.x) % TEAM; }
     static __device__ __forceinline__ int64_t first() {
         return static_cast<int64_t>(blockIdx.x) * kPerCta + static_cast<int>(threadIdx.x) / TEAM;
@@ -278,7 +279,7 @@ __device__ __forceinline__ void load_slots(const PlanView& p, const float* weigh
 
 // XS[position of each slot of t] = X[t].
 template <class T, int V, int TEAM>
-__global__ void __launch_bounds__(kRowThreads) expert_gather_kernel(const typename Vec<T, V>::Raw* __restrict__ X,
+__global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_gather_kernel(const typename Vec<T, V>::Raw* __restrict__ X,
                                                                     int64_t vecs, PlanView p,
                                                                     typename Vec<T, V>::Raw* __restrict__ XS) {
     griddep_begin();
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kRowThreads) expert_gather_kernel(const typena
 
 // Y[t] = sum over slots of (weights or 1) * YS[position].
 template <class T, int V, int TEAM, bool WEIGHTED>
-__global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(const typename Vec<T, V>::Raw* __restrict__ YS,
+__global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_combine_kernel(const typename Vec<T, V>::Raw* __restrict__ YS,
                                                                      int64_t vecs, PlanView p,
                                                                      const float* __restrict__ weights,
                                                                      typename Vec<T, V>::Raw* __restrict__ Y) {
@@ -337,12 +338,12 @@ __global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(const typen
 
 // dYS[position] = weights * dY[t], dWeights[t][j] = <dY[t], YS[position]>.
 template <class T, int V, int TEAM>
-__global__ void __launch_bounds__(kRowThreads, 2) expert_combine_backward_kernel(
+__global__ void __launch_bounds__(Team<TEAM>::kThreads, TEAM > kRowThreads ? 1 : 2) expert_combine_backward_kernel(
     const typename Vec<T, V>::Raw* __restrict__ dY, const typename Vec<T, V>::Raw* __restrict__ YS, int64_t vecs,
     PlanView p, const float* __restrict__ weights, typename Vec<T, V>::Raw* __restrict__ dYS,
     float* __restrict__ dWeights) {
     using Raw = typename Vec<T, V>::Raw;
-    __shared__ float part[kRowThreads / 32][kSlotBatch];
+    __shared__ float part[Team<TEAM>::kThreads / 32][kSlotBatch];
     const int k = p.slots, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_begin();
     for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) expert_combine_backward_kernel
                     __syncthreads();
                     if (threadIdx.x < kSlotBatch && j0 + static_cast<int>(threadIdx.x) < k) {
                         float s = 0.0f;
-                        for (int q = 0; q < kRowThreads / 32; ++q) s += part[q][threadIdx.x];
+                        for (int q = 0; q < TEAM / 32; ++q) s += part[q][threadIdx.x];
                         dWeights[t * k + j0 + threadIdx.x] = s;
                     }
                     __syncthreads();
@@ -419,22 +420,23 @@ typename Vec<T, V>::Raw* raw(void* p) {
 template <class T, int V, int TEAM>
 cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const PlanView& p, const float* weights,
                      void* out, float* dw, cudaStream_t stream) {
-    const int64_t vecs = D / V, per = kRowThreads / TEAM;
+    const int64_t vecs = D / V, per = Team<TEAM>::kPerCta;
+    constexpr int kBlock = Team<TEAM>::kThreads;
     // enough CTAs to fill the device several times over; each then walks tokens with that stride
     const int grid = static_cast<int>(
         std::max<int64_t>(1, std::min<int64_t>((p.tokens + per - 1) / per, int64_t(device_sm_count()) * 32)));
     switch (op) {
         case ExpertOp::Gather:
-            return launch_dependent(expert_gather_kernel<T, V, TEAM>, grid, kRowThreads, stream, raw<T, V>(a), vecs, p,
+            return launch_dependent(expert_gather_kernel<T, V, TEAM>, grid, kBlock, stream, raw<T, V>(a), vecs, p,
                                     raw<T, V>(out));
         case ExpertOp::GatherBackward:
-            return launch_dependent(expert_combine_kernel<T, V, TEAM, false>, grid, kRowThreads, stream, raw<T, V>(a), vecs, p,
+            return launch_dependent(expert_combine_kernel<T, V, TEAM, false>, grid, kBlock, stream, raw<T, V>(a), vecs, p,
                                     nullptr, raw<T, V>(out));
         case ExpertOp::Combine:
-            return launch_dependent(expert_combine_kernel<T, V, TEAM, true>, grid, kRowThreads, stream, raw<T, V>(a), vecs, p,
+            return launch_dependent(expert_combine_kernel<T, V, TEAM, true>, grid, kBlock, stream, raw<T, V>(a), vecs, p,
                                     weights, raw<T, V>(out));
         default:
-            return launch_dependent(expert_combine_backward_kernel<T, V, TEAM>, grid, kRowThreads, stream, raw<T, V>(a),
+            return launch_dependent(expert_combine_backward_kernel<T, V, TEAM>, grid, kBlock, stream, raw<T, V>(a),
                                     raw<T, V>(b), vecs, p, weights, raw<T, V>(out), dw);
     }
 }
@@ -444,9 +446,13 @@ cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const
                      void* out, float* dw, cudaStream_t stream) {
     // A warp per token where the tokens give every SM 16 warps (16384 tokens of 2048 bf16, 8 slots: combine 97 us against 112
     // with a CTA per token, its gradients 178 against 204; 7 tokens of 1999 fp32 take 28 us by warps and 5 by CTAs). The
-    // gather of a row that a CTA takes in one step or more keeps the CTA (93 us against 96).
-    const bool warps = p.tokens >= int64_t(device_sm_count()) * 16 && (op != ExpertOp::Gather || D / V < kRowThreads);
-    if (warps) return run_rows<T, V, 32>(op, a, b, D, p, weights, out, dw, stream);
+    // gather of a row that a CTA takes in one step or more keeps the CTA (93 us against 96). Few tokens of long rows:
+    // CTAs of 1024 threads.
+    const int64_t vecs = D / V, sms = device_sm_count();
+    if (p.tokens >= sms * 16 && (op != ExpertOp::Gather || vecs < kRowThreads))
+        return run_rows<T, V, 32>(op, a, b, D, p, weights, out, dw, stream);
+    if (p.tokens <= 2 * sms && vecs > 2 * kRowThreads)
+        return run_rows<T, V, 1024>(op, a, b, D, p, weights, out, dw, stream);
     return run_rows<T, V, kRowThreads>(op, a, b, D, p, weights, out, dw, stream);
 }
 

@@ -22,8 +22,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <cstdio>
-#include <cstdlib>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -649,9 +647,6 @@ cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t
             }
         }
         a.weights_once = x.rows <= best.bn;
-    }
-    if (const char* s = std::getenv("PNQ_FP4_CFG")) {
-        std::sscanf(s, "%d,%d,%d", &best.bn, &best.cg, &a.ks);
     }
     const int64_t tiles = count(best);
     auto go = [&](auto m) {

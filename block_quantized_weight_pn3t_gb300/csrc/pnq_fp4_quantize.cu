@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const uint8_t
             w = __ldg(reinterpret_cast<const uint32_t*>(scales + scale_word(sr, chunk, chunks)));
 #pragma unroll
         for (int u = 0; u < STEPS; ++u) {
+            if (k0 + 256 * u >= K) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // lane l: elements 4 l .. 4 l + 3 of this half of the step
                 const uint32_t four = __shfl_sync(0xffffffffu, c[u], 16 * h + (lane >> 1)) >> (16 * (lane & 1));

@@ -218,6 +218,76 @@ def test_gemm_projection_sizes(kind, M, N, K):
     check_product(y[:, torch.from_numpy(rows).cuda()], xv, wv, 1.0, torch.float32)
 
 
+def random_operand(kind, rows, K, seed, matrices=1):
+    """A large random operand (codes of normal values) and its values, both on the GPU in 64 bits."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(matrices * rows, K, generator=gen, device="cuda")
+    m = pnq.fp4_quantize(kind, x.view(matrices, rows, K) if matrices > 1 else x)
+    return m, pnq.fp4_dequantize(m).double()  # bit for bit the definition's values (test_quantize_bits)
+
+
+def check_on_gpu(y, x, w, dtype):
+    want = x @ w.T
+    bound = 1e-5 * (x.abs() @ w.abs().T) + 1e-6
+    if dtype == torch.bfloat16:
+        bound += want.abs() * 2.0 ** -8
+    assert bool(((y.double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("M,N,K", [(700, 9000, 2048), (513, 17408, 1056), (2051, 5121, 1312), (300, 17409, 288), (1000, 1025, 8224),
+                                   (20, 5120, 8192), (50, 3000, 6176), (128, 2049, 4128), (9, 1024, 17408)])
+@pytest.mark.parametrize("dtype", list(FLOATS))
+def test_gemm_every_shape_of_tile(kind, M, N, K, dtype):
+    """Sizes that take CTA pairs, single tiles of every width, and K split over clusters of every size."""
+    x, xv = random_operand(kind, M, K, M + N)
+    w, wv = random_operand(kind, N, K, N + K)
+    y = pnq.fp4_gemm(x, w, dtype=FLOATS[dtype])
+    assert pnq.device_error() == 0
+    check_on_gpu(y, xv, wv, FLOATS[dtype])
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("T,k,E,N,K", [(1700, 2, 8, 300, 544), (900, 4, 7, 1408, 1056), (60, 1, 16, 700, 4128), (513, 8, 64, 200, 288)])
+def test_gemm_experts_large(kind, T, k, E, N, K):
+    """Many rows per expert (256-column tiles), tiles that several experts' loads leave ragged."""
+    ids = route(T, k, E, seed=T, how="skew" if E > 8 else "drop")
+    plan = pnq.expert_sort(torch.from_numpy(ids).cuda(), E)
+    offsets, _, order, _, _ = ref.plan(ids, E)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, K, generator=gen, device="cuda", dtype=torch.bfloat16)
+    xm = pnq.fp4_quantize(kind, x, plan=plan)
+    xv = pnq.fp4_dequantize(xm).double()
+    token = torch.from_numpy(order[:offsets[-1]] // k).cuda()
+    assert torch.equal(xv[:offsets[-1]], pnq.fp4_dequantize(pnq.fp4_quantize(kind, x)).double()[token])
+    w, wv = random_operand(kind, N, K, E, matrices=E)
+    y = pnq.fp4_gemm_experts(xm, w, plan)
+    assert pnq.device_error() == 0 and not y[offsets[-1]:].any()
+    for e in range(E):
+        lo, hi = offsets[e], offsets[e + 1]
+        check_on_gpu(y[lo:hi], xv[lo:hi], wv[e * N:(e + 1) * N], torch.float32)
+
+
+@pytest.mark.parametrize("M", [1, 40, 600])
+def test_static_weights_chain(M):
+    """Products with static weights (copied before the kernel ahead of them ends) in a chain where each encodes the last
+    one's result: bit for bit the chain without the flag."""
+    kind, N = pnq.NVFP4, 2048
+    ws = [random_operand(kind, N, N, i)[0] for i in range(3)]
+    x0 = torch.randn(M, N, device="cuda")
+
+    def chain(flags):
+        x = x0
+        for i in range(12):
+            x = pnq.fp4_gemm(pnq.fp4_quantize(kind, x, 0.25), ws[i % 3], flags=flags) * 0.02
+        return x
+
+    want = chain(0)
+    for _ in range(3):
+        assert torch.equal(chain(pnq.GEMV_STATIC_WEIGHTS), want)
+    assert pnq.device_error() == 0 and bool(want.isfinite().all())
+
+
 def route(T, k, E, seed, how="even"):
     rng = np.random.default_rng(seed)
     if how == "one":
