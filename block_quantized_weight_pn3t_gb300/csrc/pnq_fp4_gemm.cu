@@ -130,37 +130,47 @@ struct Tile {
     int srow;     // row0's row within that block (a multiple of 64)
 };
 
-// Walks the tiles t = first, first + step, ..: all roles of a CTA see the same sequence. By experts: `starts[e]`
-// (shared memory) is the number of tiles before expert e.
+// Walks the tiles number first, first + step, ..: all roles of a CTA see the same sequence. Dense: bands of 16 weight
+// tiles, row tile by row tile (the CTAs at work share a few operand rows in L2). By experts: `starts[e]` (shared memory) is
+// the number of tiles before expert e. Steps by addition: a division or two per tile stood in the way of the threads
+// that issue copies and MMAs.
 template <int BN, int CG>
 struct Walk {
-    static constexpr int kTileN = CG * kRows;
+    static constexpr int kTileN = CG * kRows, kBand = 16;
     const GemmArgs& a;
     const int* starts;
-    int t, step, nt, e;
+    int at, step, nt, mt;   // dense: `at` counts from (m, 0) of the band
+    int m, band, width;     // row tile; first weight tile of the band and its tiles
+    int e;                  // expert
     __device__ Walk(const GemmArgs& args, const int* tile_starts)
-        : a(args), starts(tile_starts), t(static_cast<int>(blockIdx.x) / CG), step(static_cast<int>(gridDim.x) / CG),
-          nt((args.N + kTileN - 1) / kTileN), e(0) {}
+        : a(args), starts(tile_starts), at(static_cast<int>(blockIdx.x) / CG), step(static_cast<int>(gridDim.x) / CG),
+          nt((args.N + kTileN - 1) / kTileN), mt((args.M + BN - 1) / BN), m(0), band(0), width(min(kBand, nt)), e(0) {}
     __device__ bool next(Tile& o) {
-        int m;
         if (a.p.experts == 0) {
-            const int mt = (a.M + BN - 1) / BN;
-            if (t >= nt * mt) return false;
-            // bands of 16 weight tiles: the CTAs at work share a few operand rows in L2
-            const int band = t / (16 * mt), r = t - band * 16 * mt;
-            const int width = min(16, nt - 16 * band);
-            m = r / width;
-            o = Tile{0, m * BN, min(BN, a.M - m * BN), (16 * band + r - m * width) * kTileN, m * BN / 128, m * BN % 128};
+            while (at >= width) {
+                at -= width;
+                if (++m == mt) {
+                    m = 0;
+                    band += kBand;
+                    width = min(kBand, nt - band);
+                    if (width <= 0) {
+                        width = 0x7fffffff;  // past the end: no further tile
+                        band = nt;
+                        mt = 0x7fffffff;
+                    }
+                }
+            }
+            if (band >= nt) return false;
+            o = Tile{0, m * BN, min(BN, a.M - m * BN), (band + at) * kTileN, m * BN / 128, m * BN % 128};
         } else {
-            if (t >= starts[a.p.experts]) return false;
-            while (t >= starts[e + 1]) ++e;
+            if (at >= starts[a.p.experts]) return false;
+            while (at >= starts[e + 1]) ++e;
             const int first = __ldg(a.p.offsets + e), count = __ldg(a.p.offsets + e + 1) - first;
-            const int mt = (count + BN - 1) / BN, r = t - starts[e];
-            m = r % mt;
-            o = Tile{e, first + m * BN, min(BN, count - m * BN), r / mt * kTileN,
-                     __ldg(a.p.block_start + e) + m * BN / 128, m * BN % 128};
+            const int tiles = (count + BN - 1) / BN, r = at - starts[e], n = r / tiles, i = r - n * tiles;
+            o = Tile{e, first + i * BN, min(BN, count - i * BN), n * kTileN, __ldg(a.p.block_start + e) + i * BN / 128,
+                     i * BN % 128};
         }
-        t += step;
+        at += step;
         return true;
     }
 };
