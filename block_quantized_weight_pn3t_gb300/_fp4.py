@@ -9,6 +9,7 @@ compiled (csrc/pnq_torch.cpp): they check tensors, allocate results and make one
     plan = expert_sort(ids, experts)                 # ids [tokens][slots]
     q = fp4_quantize(NVFP4, x, g, plan=plan)         # tokens encoded once, written in expert order
     ys = fp4_gemm_experts(q, w, plan)                # every row times its expert's matrix
+    h = fp4_quantize(NVFP4, hs, g, plan=plan, sorted=True)   # rows in expert order already (between two products)
     y = expert_combine(ys, plan, weights)            # back to tokens, router weights applied
 """
 from __future__ import annotations
@@ -34,7 +35,7 @@ FP4_GROUP = {b.NVFP4: 16, MXFP4: 32}
 _P, _I64, _I, _F, _U = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_uint
 _SIGNATURES = {
     "pnq_fp4_layout": [_I, _I64, _I64, _I64, _I64, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)],
-    "pnq_fp4_quantize": [_I, _I, _P, _I64, _I64, _I64, _I64, _F, _P, _P, _P, _P],
+    "pnq_fp4_quantize": [_I, _I, _P, _I64, _I64, _I64, _I64, _F, _P, _U, _P, _P, _P],
     "pnq_fp4_dequantize": [_I, _P, _P, _I64, _I64, _I64, _F, _P, _I, _P, _P],
     "pnq_fp4_pack": [_I, _P, _P, _I64, _I64, _I64, _P, _P, _P],
     "pnq_fp4_gemm": [_I, _P, _P, _I64, _P, _P, _I64, _I64, _F, _I, _P, _U, _P],

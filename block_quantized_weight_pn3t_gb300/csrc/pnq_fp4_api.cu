@@ -92,11 +92,13 @@ extern "C" int pnq_fp4_layout(int type, int64_t rows, int64_t K, int64_t matrice
 }
 
 extern "C" int pnq_fp4_quantize(int type, int x_type, const void* X, int64_t ldx, int64_t rows, int64_t K,
-                                int64_t matrices, float global_scale, const pnq_expert_plan* plan, uint8_t* codes,
-                                uint8_t* scales, cudaStream_t stream) {
+                                int64_t matrices, float global_scale, const pnq_expert_plan* plan, unsigned int flags,
+                                uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
     int rc = check_shape(type, rows, K, matrices);
     if (rc != PNQ_OK) return rc;
     if (!is_float(x_type)) return PNQ_ERR_TYPE;
+    const bool sorted = (flags & PNQ_FP4_SORTED) != 0;
+    if ((flags & ~static_cast<unsigned int>(PNQ_FP4_SORTED)) != 0 || (sorted && !plan)) return PNQ_ERR_FLAGS;
     if (ldx < K || ldx > INT64_MAX / 8 / (rows * matrices + 1)) return PNQ_ERR_SHAPE;
     const float inv_g = 1.0f / global_scale;
     if (!(global_scale > 0.0f) || !std::isfinite(global_scale) || !std::isfinite(inv_g)) return PNQ_ERR_VALUE;
@@ -104,7 +106,7 @@ extern "C" int pnq_fp4_quantize(int type, int x_type, const void* X, int64_t ldx
     if (plan) {
         rc = check_plan(plan, &p);
         if (rc != PNQ_OK) return rc;
-        if (matrices != 1 || rows != p.tokens) return PNQ_ERR_SHAPE;
+        if (matrices != 1 || rows != (sorted ? p.tokens * p.slots : p.tokens)) return PNQ_ERR_SHAPE;
         rc = check_plan_rows(type, p, K);
         if (rc != PNQ_OK) return rc;
     }
@@ -113,8 +115,8 @@ extern "C" int pnq_fp4_quantize(int type, int x_type, const void* X, int64_t ldx
     if (!aligned(X, x_type == PNQ_BF16 ? 2 : 4)) return PNQ_ERR_ALIGN;
     rc = check_operand(codes, scales);
     if (rc != PNQ_OK) return rc;
-    return map_cuda(launch_fp4_quantize(type == PNQ_MXFP4, x_type == PNQ_BF16, X, ldx, rows, K, matrices, inv_g, p, codes,
-                                        scales, stream));
+    return map_cuda(launch_fp4_quantize(type == PNQ_MXFP4, x_type == PNQ_BF16, X, ldx, rows, K, matrices, inv_g, p, sorted,
+                                        codes, scales, stream));
 }
 
 extern "C" int pnq_fp4_dequantize(int type, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,

@@ -6,13 +6,30 @@
 //   MXFP4: kind::mxf4, scale_vec::2X (one power of two per 32).
 // A product of two codes and two scales is exact; the global multipliers go into the epilogue.
 //
-// Roles. The weight rows are the MMA's M axis (128 lanes), the activation rows its N axis (BN columns): a few
-// activation rows then waste no weight traffic, and a warp's store covers consecutive n of one Y row.
-// Persistent CTAs walk the tiles. Warp 0 (one thread) fills a ring of stages by tensor-map copies: a stage is
-// K = 256 of a tile (128-byte rows of codes, 128-byte swizzle) and its 512-byte scale tiles. Warp 1 (one
-// thread) copies the stage's scale tiles to tensor memory (tcgen05.cp, 32 rows x 16 bytes, repeated over the
-// four lane quarters) and issues one MMA per K = 64. Warps 2..5 read the accumulator back, one weight row per
-// thread, and store. With BN <= 128 two accumulators alternate, so a tile's stores overlap the next tile's MMAs.
+// Layout. The weight rows are the MMA's M axis (128 lanes of tensor memory per CTA), the activation rows its N axis
+// (32 .. 256 columns): a few activation rows then waste no weight traffic, an expert's ragged rows waste columns
+// only, and a warp's store covers consecutive n of one Y row.
+//
+// Roles. Persistent CTAs walk the tiles. One lane of warp 0 fills a ring of stages by tensor-map copies: a stage is
+// K = 256 of a tile (128-byte rows of codes, 128-byte swizzle) and its 512-byte scale tiles. One lane of warp 1 copies
+// the stage's scale tiles to tensor memory (tcgen05.cp, 32 rows x 16 bytes, repeated over the four lane quarters) and
+// issues one MMA per K = 64. Warps 2..9 take the accumulator to registers, one weight row per lane, and store it while
+// the next tile is multiplied. Up to 128 columns two accumulators alternate; 256 columns leave room for one beside
+// the scale columns.
+//
+// What bounds it (GB300, times of 8192 x 17408 x 5120 NVFP4 to bf16 unless said otherwise).
+//   - Many rows: the tensor pipe. 256 x 256 tiles by CTA pairs (cta_group::2: each CTA holds half of the activation
+//     rows, so a stage is 38 KB for the work that takes one CTA 54 KB) 230 us = 6.4 PFLOP/s, single CTAs of 128 x 256
+//     248 us, of 128 x 128 290 us. ncu: the tensor pipe is busy 69 percent of the cycles. A stage in the run of a tile
+//     takes 0.30 us, 0.27 of it the MMAs; a change of tiles costs some 1.9 us, the way from the last MMA through the
+//     accumulator's release to the first (tensor memory has no room for a second one: 2 x 256 columns are all of it)
+//     and the stores. 192 columns with two accumulators took longer a stage than 256 (279 us).
+//   - Few rows: HBM. One row of 17408 x 5120 takes 10.8 us (50.1 MB: 7.4 us at the copy rate; a product of 1/20 of the
+//     bytes takes 3.3). K is split over a cluster where there are fewer tiles than SMs (13 rows of 5120 x 17408:
+//     20.7 -> 12.3 us with three CTAs per tile); the partial tiles meet in distributed shared memory, in CTA order.
+//   - Between them: a stage's turn through one thread's waits and instructions. Waits by one lane (32 lanes probe the
+//     barrier 32 times), bounded by the SM's clock (a read of the global timer costs 0.4 us), one wait per stage (its
+//     scale columns are its own), and the next stage probed ahead brought a 128-column stage from 0.42 to 0.21 us.
 //
 // Every wait is bounded; a wait that gives up records its site in the device error word and ends the role, and
 // tensor memory is released whatever the outcome.
@@ -120,7 +137,7 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
 }
 #undef PNQ_MMA_FP4
 
-// A tile: 128 weight rows (a pair: 256) from n0 of matrix e, up to BN activation rows from m0 of the matrix's rows.
+// A tile: 128 weight rows (a pair: 256) from n0 of matrix e, up to BN activation rows.
 struct Tile {
     int e;        // matrix (0 when dense)
     int row0;     // first activation row (global)

@@ -135,8 +135,11 @@ __device__ __forceinline__ void encode8(float (&x)[8], bool live, float inv_g, u
     if (!live) word = 0;
 }
 
+// Where the encoded rows go: row r to row r; a plan's token to the sorted rows of its slots; a plan's sorted row to its place.
+enum class Rows { Plain, Tokens, Sorted };
+
 // STEPS steps of 256 elements per warp and item.
-template <bool MX, class T, bool VEC, bool PLAN, int STEPS>
+template <bool MX, class T, bool VEC, Rows ROWS, int STEPS>
 __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const T* __restrict__ X, int64_t ldx, int64_t rows,
                                                                  int64_t matrices, int K, float inv_g, PlanView p,
                                                                  uint8_t* __restrict__ codes, int64_t pitch,
@@ -156,7 +159,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const T* __rest
             if (k0 + 256 * u < K) load8<T, VEC>(X + r * ldx + k0 + 256 * u, x[u]);
         // with a plan: where the row goes, lane j holding slot j's places
         int at = -1, srow = 0;
-        if (PLAN && lane < p.slots) {
+        if (ROWS == Rows::Tokens && lane < p.slots) {
             at = __ldg(p.position + r * p.slots + lane);
             if (at >= 0) srow = __ldg(p.scale_row + at);
         }
@@ -179,8 +182,11 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const T* __rest
                 if (lane % (4 * kGroupLanes) == 0 && chunk < chunks) *reinterpret_cast<uint32_t*>(sp + chunk * 512) = word[u];
             }
         };
-        if (!PLAN) {
+        if (ROWS == Rows::Plain) {
             put(r, tiled_row(r, rows, matrices));
+        } else if (ROWS == Rows::Sorted) {
+            const int tiled = __ldg(p.scale_row + r);
+            if (tiled >= 0) put(r, tiled);  // not past the rows in use
         } else {
             for (int j0 = 0; j0 < p.slots; j0 += 32) {
                 if (j0) {
@@ -318,26 +324,26 @@ int item_grid(int64_t items, int per_cta) {
 // Whether the rows fill the device's warps with items of 1024 elements; otherwise items of 256.
 bool many_items(int64_t rows, int64_t K) { return rows * ((K + 1023) / 1024) >= int64_t(device_sm_count()) * 16; }
 
-template <bool MX, class T, bool VEC, bool PLAN, int STEPS>
+template <bool MX, class T, bool VEC, Rows ROWS, int STEPS>
 cudaError_t run_quantize(const T* x, int64_t ldx, int64_t rows, int64_t K, int64_t matrices, float inv_g, const PlanView& p,
                   uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
     const int64_t items = rows * matrices * ((K + STEPS * 256 - 1) / (STEPS * 256));
-    return launch_dependent(fp4_quantize_kernel<MX, T, VEC, PLAN, STEPS>, item_grid(items, kQThreads / 32), kQThreads, stream, x,
+    return launch_dependent(fp4_quantize_kernel<MX, T, VEC, ROWS, STEPS>, item_grid(items, kQThreads / 32), kQThreads, stream, x,
                             ldx, rows, matrices, K, inv_g, p, codes, fp4_pitch(K), scales, fp4_chunks(MX, K));
 }
 
 template <bool MX, class T, bool VEC>
 cudaError_t run_quantize(const void* X, int64_t ldx, int64_t rows, int64_t K, int64_t matrices, float inv_g, const PlanView& p,
-                  uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
+                         bool sorted, uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
     const T* x = static_cast<const T*>(X);
     const bool many = many_items(rows * matrices, K);
-    if (p.experts) {
-        if (many) return run_quantize<MX, T, VEC, true, 4>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
-        else return run_quantize<MX, T, VEC, true, 1>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
-    } else {
-        if (many) return run_quantize<MX, T, VEC, false, 4>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
-        else return run_quantize<MX, T, VEC, false, 1>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
-    }
+    auto go = [&](auto r) {
+        constexpr Rows ROWS = decltype(r)::value;
+        return many ? run_quantize<MX, T, VEC, ROWS, 4>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream)
+                    : run_quantize<MX, T, VEC, ROWS, 1>(x, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+    };
+    if (!p.experts) return go(std::integral_constant<Rows, Rows::Plain>{});
+    return sorted ? go(std::integral_constant<Rows, Rows::Sorted>{}) : go(std::integral_constant<Rows, Rows::Tokens>{});
 }
 
 template <bool MX, class T, bool VEC, int STEPS>
@@ -364,17 +370,17 @@ cudaError_t run_dequantize(const Fp4View& v, int64_t K, float g, const PlanView&
 }  // namespace
 
 cudaError_t launch_fp4_quantize(bool mx, bool bf16, const void* X, int64_t ldx, int64_t rows, int64_t K,
-                                int64_t matrices, float inv_g, const PlanView& p, uint8_t* codes, uint8_t* scales,
-                                cudaStream_t stream) {
+                                int64_t matrices, float inv_g, const PlanView& p, bool sorted, uint8_t* codes,
+                                uint8_t* scales, cudaStream_t stream) {
     const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx * (bf16 ? 2 : 4) % 16 == 0;
     auto go = [&](auto m) {
         constexpr bool MX = decltype(m)::value;
         if (bf16) {
-            if (vec) return run_quantize<MX, __nv_bfloat16, true>(X, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
-            else return run_quantize<MX, __nv_bfloat16, false>(X, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+            if (vec) return run_quantize<MX, __nv_bfloat16, true>(X, ldx, rows, K, matrices, inv_g, p, sorted, codes, scales, stream);
+            else return run_quantize<MX, __nv_bfloat16, false>(X, ldx, rows, K, matrices, inv_g, p, sorted, codes, scales, stream);
         } else {
-            if (vec) return run_quantize<MX, float, true>(X, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
-            else return run_quantize<MX, float, false>(X, ldx, rows, K, matrices, inv_g, p, codes, scales, stream);
+            if (vec) return run_quantize<MX, float, true>(X, ldx, rows, K, matrices, inv_g, p, sorted, codes, scales, stream);
+            else return run_quantize<MX, float, false>(X, ldx, rows, K, matrices, inv_g, p, sorted, codes, scales, stream);
         }
     };
     return mx ? go(std::true_type{}) : go(std::false_type{});

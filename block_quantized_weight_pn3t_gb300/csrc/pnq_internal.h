@@ -158,8 +158,8 @@ inline int64_t fp4_pitch(int64_t K) { return (K / 2 + 15) / 16 * 16; }
 inline int64_t fp4_chunks(bool mx, int64_t K) { return mx ? (K + 127) / 128 : (K + 63) / 64; }
 
 cudaError_t launch_fp4_quantize(bool mx, bool bf16, const void* X, int64_t ldx, int64_t rows, int64_t K,
-                                int64_t matrices, float inv_g, const PlanView& p, uint8_t* codes, uint8_t* scales,
-                                cudaStream_t stream);
+                                int64_t matrices, float inv_g, const PlanView& p, bool sorted, uint8_t* codes,
+                                uint8_t* scales, cudaStream_t stream);
 cudaError_t launch_fp4_dequantize(bool mx, const Fp4View& v, int64_t K, float g, const PlanView& p, bool bf16, void* out,
                                   cudaStream_t stream);
 cudaError_t launch_fp4_pack(bool mx, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,

@@ -475,8 +475,8 @@ PNQ_ENTRY(fp4_layout) {
 
 PNQ_ENTRY(fp4_quantize) {
     return entry([&]() -> PyObject* {
-        static const char* const names[] = {"type_", "x", "global_scale", "plan", "out", "stream"};
-        const Args<6> a("fp4_quantize", names, 2, args, nargs, kwnames);
+        static const char* const names[] = {"type_", "x", "global_scale", "plan", "out", "stream", "sorted"};
+        const Args<7> a("fp4_quantize", names, 2, args, nargs, kwnames);
         const int type = to_type(a[0]), G = type == PNQ_MXFP4 ? 32 : 16;
         const at::Tensor& x = tensor(a[1], "x");
         if (x.dim() != 2 && x.dim() != 3) refuse("x must be a torch.Tensor [rows][K] or [matrices][rows][K]");
@@ -491,9 +491,13 @@ PNQ_ENTRY(fp4_quantize) {
         if (K == 0 || K % G)
             refuse("K = " + std::to_string(K) + " is not a positive multiple of " + std::to_string(G), PNQ_ERR_SHAPE);
         PlanObject* plan = a[3] ? to_plan(a[3]) : nullptr;
+        const int sorted = a[6] ? PyObject_IsTrue(a[6]) : 0;
+        if (sorted < 0) throw PythonError{};
+        if (sorted && !plan) refuse("sorted rows are a plan's: plan is missing", PNQ_ERR_FLAGS);
         if (plan) {
-            if (matrices != 1 || rows != plan->desc.tokens)
-                refuse("x has shape " + shape_text(x.sizes()) + "; the plan has " + std::to_string(plan->desc.tokens) + " tokens");
+            if (matrices != 1 || rows != (sorted ? plan->rows : plan->desc.tokens))
+                refuse("x has shape " + shape_text(x.sizes()) + "; the plan has " + std::to_string(plan->desc.tokens) + " tokens and " +
+                       std::to_string(plan->rows) + " rows");
             require_device(x, "x", plan->device);
         }
         const double g = a[2] ? to_double(a[2]) : 1.0;
@@ -519,7 +523,7 @@ PNQ_ENTRY(fp4_quantize) {
         m->per_matrix = at::Tensor();
         const auto guard = on(device);
         check(pnq_fp4_quantize(type, xt, x.data_ptr(), ldx, rows, K, matrices, static_cast<float>(g), plan ? &plan->desc : nullptr,
-                               m->codes_at, m->scales_at, stream_of(a[5], device)),
+                               sorted ? PNQ_FP4_SORTED : 0u, m->codes_at, m->scales_at, stream_of(a[5], device)),
               "pnq_fp4_quantize");
         return o.release();
     });
@@ -768,10 +772,10 @@ PNQ_ENTRY(expert_combine_backward) {
 PyMethodDef methods[] = {
     PNQ_METHOD(fp4_layout, "fp4_layout(type_, rows, K, matrices=1, plan_experts=0)\n--\n\n"
                            "(pitch of a row of codes, bytes of the tiled scales) of an operand."),
-    PNQ_METHOD(fp4_quantize, "fp4_quantize(type_, x, global_scale=1.0, plan=None, out=None, stream=None)\n--\n\n"
+    PNQ_METHOD(fp4_quantize, "fp4_quantize(type_, x, global_scale=1.0, plan=None, out=None, stream=None, sorted=False)\n--\n\n"
                              "Encode x (CUDA bf16 or fp32, [rows][K], or [matrices][rows][K] contiguous; 2-D rows may be strided)\n"
-                             "for the global multiplier. With a plan, x holds the plan's tokens and the operand its sorted\n"
-                             "rows. out: an operand of the same shape to write into. Returns the Fp4Matrix."),
+                             "for the global multiplier. With a plan, x holds the plan's tokens (sorted: its sorted rows)\n"
+                             "and the operand its sorted rows. out: an operand of the same shape to write into. Returns the Fp4Matrix."),
     PNQ_METHOD(fp4_dequantize, "fp4_dequantize(m, dtype=torch.float32, out=None, stream=None)\n--\n\n"
                                "The values an operand stands for, fp32 or bf16 [matrices * rows][K] (of a plan's operand: its\n"
                                "sorted rows, zeros past the rows in use). Its global_scale must be one float."),

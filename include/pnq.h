@@ -304,6 +304,9 @@ int pnq_selftest_wait(uint32_t limit_us, cudaStream_t stream);
  * scales are at tiled row scale_row[i] (each expert's rows start a new 128-row block).
  */
 
+/* Flags of pnq_fp4_quantize. */
+enum pnq_fp4_flags { PNQ_FP4_SORTED = 1u };
+
 /* Element types of activations, expert rows and products. */
 enum pnq_float { PNQ_F32 = 0, PNQ_BF16 = 1 };
 
@@ -337,14 +340,15 @@ int pnq_fp4_layout(int type, int64_t rows, int64_t K, int64_t matrices, int64_t 
  * zero codes. A group with a NaN or an infinite y gets a NaN scale and zero codes: its values, and every
  * product over it, are NaN. Rows of other groups and matrices are not touched.
  *   plan  NULL, or an expert plan: X holds plan->tokens rows (rows = tokens, matrices = 1), each is
- *         encoded once and written to the sorted rows of its slots.
- * X element-aligned (16-byte aligned rows are faster); codes and scales 16-byte aligned. Errors:
- * PNQ_ERR_TYPE (format or element type), PNQ_ERR_SHAPE, PNQ_ERR_NULL, PNQ_ERR_ALIGN, PNQ_ERR_VALUE (g not
+ *         encoded once and written to the sorted rows of its slots; with PNQ_FP4_SORTED in flags X holds the
+ *         sorted rows themselves (rows = tokens * slots; those past the rows in use are not read).
+ * X element-aligned (16-byte aligned rows are faster); codes and scales 16-byte aligned. Errors: PNQ_ERR_FLAGS
+ * (an unknown flag, or PNQ_FP4_SORTED without a plan), PNQ_ERR_TYPE (format or element type), PNQ_ERR_SHAPE, PNQ_ERR_NULL, PNQ_ERR_ALIGN, PNQ_ERR_VALUE (g not
  * finite and > 0, or 1 / g not finite), PNQ_ERR_CUDA.
  */
 int pnq_fp4_quantize(int type, int x_type, const void* X, int64_t ldx, int64_t rows, int64_t K, int64_t matrices,
-                     float global_scale, const pnq_expert_plan* plan, uint8_t* codes, uint8_t* scales,
-                     cudaStream_t stream);
+                     float global_scale, const pnq_expert_plan* plan, unsigned int flags, uint8_t* codes,
+                     uint8_t* scales, cudaStream_t stream);
 
 /*
  * pnq_fp4_dequantize -- out[r][k] = fp32(e2m1 * scale * g) (the first product is exact), rounded once more

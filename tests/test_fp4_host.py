@@ -58,8 +58,9 @@ def test_layout(lib):
 
 
 def test_quantize_refusals(lib):
-    def call(type_=pnq.NVFP4, xt=F32, X=FAKE, ldx=64, rows=4, K=64, matrices=1, g=1.0, p=None, codes=FAKE, scales=FAKE):
-        return lib.pnq_fp4_quantize(type_, xt, X, ldx, rows, K, matrices, g, ctypes.byref(p) if p else None, codes, scales, None)
+    def call(type_=pnq.NVFP4, xt=F32, X=FAKE, ldx=64, rows=4, K=64, matrices=1, g=1.0, p=None, flags=0, codes=FAKE, scales=FAKE):
+        return lib.pnq_fp4_quantize(type_, xt, X, ldx, rows, K, matrices, g, ctypes.byref(p) if p else None, flags, codes, scales,
+                                    None)
 
     assert call(type_=pnq.PN4T) == Status.ERR_TYPE
     assert call(xt=2) == Status.ERR_TYPE
@@ -72,6 +73,9 @@ def test_quantize_refusals(lib):
     assert call(codes=FAKE + 8) == Status.ERR_ALIGN and call(scales=FAKE + 4) == Status.ERR_ALIGN
     assert call(rows=0) == Status.OK
     assert call(p=plan(tokens=5)) == Status.ERR_SHAPE and call(p=plan(), matrices=2) == Status.ERR_SHAPE
+    assert call(flags=2) == Status.ERR_FLAGS and call(flags=1) == Status.ERR_FLAGS  # sorted rows need a plan
+    assert call(p=plan(), flags=1) == Status.ERR_SHAPE                              # 4 rows, the plan has 8
+    assert call(p=plan(tokens=0), rows=0, flags=1) == Status.OK
     assert call(p=plan(slots=0)) == Status.ERR_SHAPE and call(p=plan(slots=65)) == Status.ERR_SHAPE
     assert call(p=plan(experts=0)) == Status.ERR_SHAPE and call(p=plan(experts=1025)) == Status.ERR_SHAPE
     assert call(p=plan(position=0)) == Status.ERR_NULL and call(p=plan(offsets=0)) == Status.ERR_NULL

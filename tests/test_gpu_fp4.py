@@ -324,6 +324,12 @@ def test_gemm_experts(kind, T, k, E, N, K, how, dtype):
     token = order[:used] // k
     assert np.array_equal(codes[:used], want_codes[token]) and np.array_equal(words[:used], want_words[token])
     xv = ref.values(want_codes, want_words, kind)
+    # the same rows, sorted already (NaN past the rows in use: they are not read)
+    xs = np.full((T * k, K), np.nan, np.float32)
+    xs[:used] = x[token]
+    sm = pnq.fp4_quantize(kind, torch.from_numpy(xs).cuda(), 0.5, plan=plan, sorted=True)
+    codes, words = read_operand(sm, np.maximum(scale_row, 0))
+    assert np.array_equal(codes[:used], want_codes[token]) and np.array_equal(words[:used], want_words[token])
     back = pnq.fp4_dequantize(xm).cpu().numpy()
     assert np.array_equal(back[:used], (xv[token] * 0.5).astype(np.float32)) and not back[used:].any()
 
