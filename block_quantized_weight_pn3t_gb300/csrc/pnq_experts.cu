@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int3
 #pragma unroll
         for (int j = 0; j < kSortAhead; ++j) {
             const int i = 32 * (b + j) + lane;
-            e[j] = b + j < b1 && i < n ? __ldg(ids + i) : -1;
+            e[j] = b + j < b1 && i < n ? ld_l2(ids + i) : -1;
         }
 #pragma unroll
         for (int j = 0; j < kSortAhead; ++j)
@@ -176,14 +176,17 @@ __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int3
 
 // order and scale_row from position (many slots).
 __global__ void __launch_bounds__(256) expert_order_kernel(const int32_t* __restrict__ ids, int n, PlanView p) {
+    __shared__ int shift[1024];  // of each expert: from sorted row to row in the tiled scales
     griddep_begin();
-    const int used = __ldg(p.offsets + p.experts);
+    for (int e = threadIdx.x; e < p.experts; e += 256) shift[e] = 128 * ld_l2(p.block_start + e) - ld_l2(p.offsets + e);
+    __syncthreads();
+    const int used = ld_l2(p.offsets + p.experts);
     for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
-        const int at = __ldg(p.position + i);
+        const int at = ld_l2(p.position + i);
         if (at >= 0) {
-            const int e = __ldg(ids + i);
+            const int e = ld_l2(ids + i);
             p.order[at] = i;
-            p.scale_row[at] = 128 * __ldg(p.block_start + e) + at - __ldg(p.offsets + e);
+            p.scale_row[at] = at + shift[e];
         }
         if (i >= used) {
             p.order[i] = -1;
@@ -240,7 +243,7 @@ template <> struct Vec<__nv_bfloat16, 1> {
 // Zero rows [used, n) of out, shared by all CTAs.
 template <class Raw>
 __device__ __forceinline__ void zero_tail(Raw* out, const PlanView& p, int64_t n, int64_t vecs) {
-    const int64_t used = __ldg(p.offsets + p.experts);
+    const int64_t used = ld_l2(p.offsets + p.experts);
     const int64_t count = (n - used) * vecs;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < count;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x)
@@ -263,17 +266,21 @@ struct Team {
     static __device__ __forceinline__ int64_t step() { return static_cast<int64_t>(gridDim.x) * kPerCta; }
 };
 
-// Sorted rows (and weights) of slots j0 .. j0 + kSlotBatch - 1 of token t; -1 where there is none.
-template <bool WEIGHTED>
+// Sorted rows and weights (or ones) of slots j0 .. j0 + kSlotBatch - 1 of token t, in every lane of the warp; -1 where there is
+// none. Lane j loads slot j's: one request for all of them.
 __device__ __forceinline__ void load_slots(const PlanView& p, const float* weights, int64_t t, int j0, int (&at)[kSlotBatch],
                                            float (&w)[kSlotBatch]) {
-    const int k = p.slots;
+    const int k = p.slots, j = j0 + (static_cast<int>(threadIdx.x) & 31);
+    int mine = -1;
+    float weight = 1.0f;
+    if (j < min(k, j0 + kSlotBatch)) {
+        mine = ld_l2(p.position + t * k + j);
+        if (weights) weight = ld_l2(weights + t * k + j);
+    }
 #pragma unroll
-    for (int j = 0; j < kSlotBatch; ++j) at[j] = j0 + j < k ? __ldg(p.position + t * k + j0 + j) : -1;
-#pragma unroll
-    for (int j = 0; j < kSlotBatch; ++j) {
-        w[j] = 0.0f;
-        if (WEIGHTED && j0 + j < k) w[j] = __ldg(weights + t * k + j0 + j);
+    for (int i = 0; i < kSlotBatch; ++i) {
+        at[i] = __shfl_sync(0xffffffffu, mine, i);
+        w[i] = __shfl_sync(0xffffffffu, weight, i);
     }
 }
 
@@ -287,9 +294,9 @@ __global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_gather_kernel(con
         for (int j0 = 0; j0 < p.slots; j0 += kSlotBatch) {
             int at[kSlotBatch];
             float w[kSlotBatch];
-            load_slots<false>(p, nullptr, t, j0, at, w);
+            load_slots(p, nullptr, t, j0, at, w);
             for (int64_t c = Team<TEAM>::thread(); c < vecs; c += TEAM) {
-                const auto v = __ldg(X + t * vecs + c);
+                const auto v = ld_l2(X + t * vecs + c);
 #pragma unroll
                 for (int j = 0; j < kSlotBatch; ++j)
                     if (at[j] >= 0) XS[at[j] * vecs + c] = v;
@@ -299,8 +306,8 @@ __global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_gather_kernel(con
     zero_tail(XS, p, p.tokens * p.slots, vecs);
 }
 
-// Y[t] = sum over slots of (weights or 1) * YS[position].
-template <class T, int V, int TEAM, bool WEIGHTED>
+// Y[t] = sum over slots of (weights, or 1 where they are null) * YS[position].
+template <class T, int V, int TEAM>
 __global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_combine_kernel(const typename Vec<T, V>::Raw* __restrict__ YS,
                                                                      int64_t vecs, PlanView p,
                                                                      const float* __restrict__ weights,
@@ -311,27 +318,30 @@ __global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_combine_kernel(co
     for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
         int at[kSlotBatch];
         float w[kSlotBatch];
-        load_slots<WEIGHTED>(p, weights, t, 0, at, w);
-        for (int64_t c = Team<TEAM>::thread(); c < vecs; c += TEAM) {
+        load_slots(p, weights, t, 0, at, w);
+        // whole warps take the columns' steps together (the slots are loaded again in each where there are over kSlotBatch)
+        for (int64_t c0 = Team<TEAM>::thread() & ~31; c0 < vecs; c0 += TEAM) {
+            const int64_t c = c0 + (static_cast<int>(threadIdx.x) & 31);
+            const bool live = c < vecs;
             float acc[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] = 0.0f;
             for (int j0 = 0; j0 < k; j0 += kSlotBatch) {
-                if (k > kSlotBatch) load_slots<WEIGHTED>(p, weights, t, j0, at, w);
+                if (k > kSlotBatch) load_slots(p, weights, t, j0, at, w);
                 Raw r[kSlotBatch];
 #pragma unroll
                 for (int j = 0; j < kSlotBatch; ++j)
-                    if (at[j] >= 0) r[j] = __ldg(YS + at[j] * vecs + c);
+                    if (at[j] >= 0 && live) r[j] = ld_l2(YS + at[j] * vecs + c);
 #pragma unroll
                 for (int j = 0; j < kSlotBatch; ++j) {
-                    if (at[j] < 0) continue;
+                    if (at[j] < 0 || !live) continue;
                     float f[V];
                     Vec<T, V>::to_f32(r[j], f);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) acc[i] = WEIGHTED ? fmaf(w[j], f[i], acc[i]) : acc[i] + f[i];
+                    for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
                 }
             }
-            Y[t * vecs + c] = Vec<T, V>::from_f32(acc);
+            if (live) Y[t * vecs + c] = Vec<T, V>::from_f32(acc);
         }
     }
 }
@@ -350,16 +360,16 @@ __global__ void __launch_bounds__(Team<TEAM>::kThreads, TEAM > kRowThreads ? 1 :
         for (int j0 = 0; j0 < k; j0 += kSlotBatch) {
             int at[kSlotBatch];
             float w[kSlotBatch], dot[kSlotBatch];
-            load_slots<true>(p, weights, t, j0, at, w);
+            load_slots(p, weights, t, j0, at, w);
 #pragma unroll
             for (int j = 0; j < kSlotBatch; ++j) dot[j] = 0.0f;
             for (int64_t c = Team<TEAM>::thread(); c < vecs; c += TEAM) {
-                const Raw gr = __ldg(dY + t * vecs + c);
+                const Raw gr = ld_l2(dY + t * vecs + c);
                 Raw r[kSlotBatch];
                 if (dWeights) {
 #pragma unroll
                     for (int j = 0; j < kSlotBatch; ++j)
-                        if (at[j] >= 0) r[j] = __ldg(YS + at[j] * vecs + c);
+                        if (at[j] >= 0) r[j] = ld_l2(YS + at[j] * vecs + c);
                 }
                 float g[V];
                 Vec<T, V>::to_f32(gr, g);
@@ -425,20 +435,17 @@ cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const
     // enough CTAs to fill the device several times over; each then walks tokens with that stride
     const int grid = static_cast<int>(
         std::max<int64_t>(1, std::min<int64_t>((p.tokens + per - 1) / per, int64_t(device_sm_count()) * 32)));
-    switch (op) {
-        case ExpertOp::Gather:
-            return launch_dependent(expert_gather_kernel<T, V, TEAM>, grid, kBlock, stream, raw<T, V>(a), vecs, p,
+    if constexpr (TEAM != 512) {
+        if (op == ExpertOp::Gather)
+            return launch_dependent(expert_gather_kernel<T, V, TEAM>, grid, kBlock, stream, raw<T, V>(a), vecs, p, raw<T, V>(out));
+        if (op != ExpertOp::CombineBackward)
+            return launch_dependent(expert_combine_kernel<T, V, TEAM>, grid, kBlock, stream, raw<T, V>(a), vecs, p, weights,
                                     raw<T, V>(out));
-        case ExpertOp::GatherBackward:
-            return launch_dependent(expert_combine_kernel<T, V, TEAM, false>, grid, kBlock, stream, raw<T, V>(a), vecs, p,
-                                    nullptr, raw<T, V>(out));
-        case ExpertOp::Combine:
-            return launch_dependent(expert_combine_kernel<T, V, TEAM, true>, grid, kBlock, stream, raw<T, V>(a), vecs, p,
-                                    weights, raw<T, V>(out));
-        default:
-            return launch_dependent(expert_combine_backward_kernel<T, V, TEAM>, grid, kBlock, stream, raw<T, V>(a),
-                                    raw<T, V>(b), vecs, p, weights, raw<T, V>(out), dw);
     }
+    if constexpr (TEAM != 1024)
+        return launch_dependent(expert_combine_backward_kernel<T, V, TEAM>, grid, kBlock, stream, raw<T, V>(a), raw<T, V>(b), vecs, p,
+                                weights, raw<T, V>(out), dw);
+    return cudaErrorInvalidValue;  // no such pair is asked for
 }
 
 template <class T, int V>
@@ -447,12 +454,14 @@ cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const
     // A warp per token where the tokens give every SM 16 warps (16384 tokens of 2048 bf16, 8 slots: combine 97 us against 112
     // with a CTA per token, its gradients 178 against 204; 7 tokens of 1999 fp32 take 28 us by warps and 5 by CTAs). The
     // gather of a row that a CTA takes in one step or more keeps the CTA (93 us against 96). Few tokens of long rows:
-    // CTAs of 1024 threads.
+    // CTAs of 1024 threads (7 tokens of 1999 fp32, 6 slots: combine 4.4 -> 2.7 us), 512 for the gradients, which need twice
+    // the registers.
     const int64_t vecs = D / V, sms = device_sm_count();
     if (p.tokens >= sms * 16 && (op != ExpertOp::Gather || vecs < kRowThreads))
         return run_rows<T, V, 32>(op, a, b, D, p, weights, out, dw, stream);
     if (p.tokens <= 2 * sms && vecs > 2 * kRowThreads)
-        return run_rows<T, V, 1024>(op, a, b, D, p, weights, out, dw, stream);
+        return op == ExpertOp::CombineBackward ? run_rows<T, V, 512>(op, a, b, D, p, weights, out, dw, stream)
+                                               : run_rows<T, V, 1024>(op, a, b, D, p, weights, out, dw, stream);
     return run_rows<T, V, kRowThreads>(op, a, b, D, p, weights, out, dw, stream);
 }
 

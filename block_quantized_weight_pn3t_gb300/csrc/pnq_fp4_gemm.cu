@@ -182,9 +182,9 @@ struct Walk {
         } else {
             if (at >= starts[a.p.experts]) return false;
             while (at >= starts[e + 1]) ++e;
-            const int first = __ldg(a.p.offsets + e), count = __ldg(a.p.offsets + e + 1) - first;
+            const int first = ld_l2(a.p.offsets + e), count = ld_l2(a.p.offsets + e + 1) - first;
             const int tiles = (count + BN - 1) / BN, r = at - starts[e], n = r / tiles, i = r - n * tiles;
-            o = Tile{e, first + i * BN, min(BN, count - i * BN), n * kTileN, __ldg(a.p.block_start + e) + i * BN / 128,
+            o = Tile{e, first + i * BN, min(BN, count - i * BN), n * kTileN, ld_l2(a.p.block_start + e) + i * BN / 128,
                      i * BN % 128};
         }
         at += step;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         const int E = a.p.experts, nt = (a.N + CG * kRows - 1) / (CG * kRows), per = (E + kThreads - 1) / kThreads;
         const int e0 = min(E, static_cast<int>(threadIdx.x) * per), e1 = min(E, e0 + per);
         int sum = 0;
-        for (int e = e0; e < e1; ++e) sum += (__ldg(a.p.offsets + e + 1) - __ldg(a.p.offsets + e) + BN - 1) / BN * nt;
+        for (int e = e0; e < e1; ++e) sum += (ld_l2(a.p.offsets + e + 1) - ld_l2(a.p.offsets + e) + BN - 1) / BN * nt;
         int incl = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         for (int w = 0; w < warp; ++w) at += warp_sums[w];
         for (int e = e0; e < e1; ++e) {
             starts[e] = at;
-            at += (__ldg(a.p.offsets + e + 1) - __ldg(a.p.offsets + e) + BN - 1) / BN * nt;
+            at += (ld_l2(a.p.offsets + e + 1) - ld_l2(a.p.offsets + e) + BN - 1) / BN * nt;
         }
         if (e1 == E && e0 < E) starts[E] = at;
     }
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                         if (c * kChunk + j < cols)
                             red[(half * kHalf + c * kChunk + j) * kRows + 32 * q + lane] = __uint_as_float(v[c][j]);
             } else if (r < a.N) {
-                const float scale = a.w_global ? a.alpha * __ldg(a.w_global + tile.e) : a.alpha;
+                const float scale = a.w_global ? a.alpha * ld_l2(a.w_global + tile.e) : a.alpha;
                 T* y = Y + static_cast<int64_t>(tile.row0 + half * kHalf) * a.N + r;
 #pragma unroll
                 for (int c = 0; c < kHalf / kChunk; ++c)
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         }
         if (!ok && lane == 0) record_error(a.err, kErrFullWait);
         if (a.p.experts > 0) {  // rows past the rows in use
-            const int64_t used = __ldg(a.p.offsets + a.p.experts), count = (static_cast<int64_t>(a.M) - used) * a.N;
+            const int64_t used = ld_l2(a.p.offsets + a.p.experts), count = (static_cast<int64_t>(a.M) - used) * a.N;
             const int64_t cta = blockIdx.y * static_cast<int64_t>(gridDim.x) + blockIdx.x;
             const int64_t step = static_cast<int64_t>(gridDim.x) * gridDim.y * kEpilogueThreads;
             for (int64_t j = cta * kEpilogueThreads + static_cast<int>(threadIdx.x) - 64; j < count; j += step)
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         Walk<BN, CG> again(a, starts);
         if (again.next(tile)) {
             T* Y = static_cast<T*>(a.Y);
-            const float scale = a.w_global ? a.alpha * __ldg(a.w_global + tile.e) : a.alpha;
+            const float scale = a.w_global ? a.alpha * ld_l2(a.w_global + tile.e) : a.alpha;
             // a thread sums four rows of a column: its loads from all the CTAs are in flight together
             const int c0 = kz * tile.rows / a.ks, c1 = (kz + 1) * tile.rows / a.ks;
             for (int e = static_cast<int>(threadIdx.x); e < (c1 - c0) * (kRows / 4); e += kThreads) {

@@ -64,25 +64,25 @@ __device__ __forceinline__ float e4m3_bits_to_f32(uint32_t word) {
     return __low2float(u32_as_half2(e4m3x2_to_f16x2(word)));
 }
 
+// Eight consecutive elements. VEC: by one load, 8 * sizeof(T) bytes aligned.
 template <class T, bool VEC>
 __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
     if constexpr (sizeof(T) == 4) {
         if constexpr (VEC) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+            ld_l2_f32x8(p, x);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __ldg(p + i);
+            for (int i = 0; i < 8; ++i) x[i] = ld_l2(p + i);
         }
     } else {
         uint32_t w[4];
         if constexpr (VEC) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+            const uint4 a = ld_l2(reinterpret_cast<const uint4*>(p));
             w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
         } else {
             const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __ldg(h + 2 * i) | (static_cast<uint32_t>(__ldg(h + 2 * i + 1)) << 16);
+            for (int i = 0; i < 4; ++i) w[i] = ld_l2(h + 2 * i) | (static_cast<uint32_t>(ld_l2(h + 2 * i + 1)) << 16);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const T* __rest
         // with a plan: where the row goes, lane j holding slot j's places
         int at = -1, srow = 0;
         if (ROWS == Rows::Tokens && lane < p.slots) {
-            at = __ldg(p.position + r * p.slots + lane);
-            if (at >= 0) srow = __ldg(p.scale_row + at);
+            at = ld_l2(p.position + r * p.slots + lane);
+            if (at >= 0) srow = ld_l2(p.scale_row + at);
         }
         uint32_t word[STEPS], c[STEPS];
 #pragma unroll
@@ -185,14 +185,14 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const T* __rest
         if (ROWS == Rows::Plain) {
             put(r, tiled_row(r, rows, matrices));
         } else if (ROWS == Rows::Sorted) {
-            const int tiled = __ldg(p.scale_row + r);
+            const int tiled = ld_l2(p.scale_row + r);
             if (tiled >= 0) put(r, tiled);  // not past the rows in use
         } else {
             for (int j0 = 0; j0 < p.slots; j0 += 32) {
                 if (j0) {
                     at = -1;
-                    if (j0 + lane < p.slots) at = __ldg(p.position + r * p.slots + j0 + lane);
-                    if (at >= 0) srow = __ldg(p.scale_row + at);
+                    if (j0 + lane < p.slots) at = ld_l2(p.position + r * p.slots + j0 + lane);
+                    if (at >= 0) srow = ld_l2(p.scale_row + at);
                 }
                 for (int j = 0; j < min(32, p.slots - j0); ++j) {
                     const int row = __shfl_sync(0xffffffffu, at, j), tiled = __shfl_sync(0xffffffffu, srow, j);
@@ -237,17 +237,17 @@ __global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const uint8_t
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
         const int64_t r = items <= INT32_MAX ? static_cast<int32_t>(it) / per_row : it / per_row;
         const int k0 = static_cast<int>(it - r * per_row) * (STEPS * 256);
-        const int64_t sr = scale_row ? __ldg(scale_row + r) : tiled_row(r, rows, matrices);  // -1: a row not in use
+        const int64_t sr = scale_row ? ld_l2(scale_row + r) : tiled_row(r, rows, matrices);  // -1: a row not in use
         uint32_t c[STEPS], w = 0;
 #pragma unroll
         for (int u = 0; u < STEPS; ++u) {
             const int k = k0 + 256 * u + 8 * lane;
-            c[u] = sr >= 0 && k < K ? __ldg(reinterpret_cast<const uint32_t*>(codes + r * pitch + k / 2)) : 0u;
+            c[u] = sr >= 0 && k < K ? ld_l2(reinterpret_cast<const uint32_t*>(codes + r * pitch + k / 2)) : 0u;
         }
         // lane j holds the scale words of the item's chunk j
         const int chunk = k0 / kChunkElems + lane;
         if (sr >= 0 && lane < STEPS * kChunksStep && chunk < chunks)
-            w = __ldg(reinterpret_cast<const uint32_t*>(scales + scale_word(sr, chunk, chunks)));
+            w = ld_l2(reinterpret_cast<const uint32_t*>(scales + scale_word(sr, chunk, chunks)));
 #pragma unroll
         for (int u = 0; u < STEPS; ++u) {
             if (k0 + 256 * u >= K) break;
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_tile_scales_kernel(const uint8_
             const uint8_t* src = in + (m * rows + rr) * groups + 4 * c;
             const int64_t left = groups - 4 * c;
             for (int j = 0; j < 4; ++j)
-                if (j < left) word |= static_cast<uint32_t>(__ldg(src + j)) << (8 * j);
+                if (j < left) word |= static_cast<uint32_t>(ld_l2(src + j)) << (8 * j);
         }
         *reinterpret_cast<uint32_t*>(out + scale_word(r, c, chunks)) = word;
     }
@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(kQThreads) fp4_pitch_codes_kernel(const uint8_
             const uint8_t* src = in + r * half + b;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                lo |= static_cast<uint32_t>(__ldg(src + j)) << (8 * j);
-                hi |= static_cast<uint32_t>(__ldg(src + 4 + j)) << (8 * j);
+                lo |= static_cast<uint32_t>(ld_l2(src + j)) << (8 * j);
+                hi |= static_cast<uint32_t>(ld_l2(src + 4 + j)) << (8 * j);
             }
         }
         *reinterpret_cast<uint2*>(out + r * pitch + b) = make_uint2(lo, hi);
@@ -372,7 +372,8 @@ cudaError_t run_dequantize(const Fp4View& v, int64_t K, float g, const PlanView&
 cudaError_t launch_fp4_quantize(bool mx, bool bf16, const void* X, int64_t ldx, int64_t rows, int64_t K,
                                 int64_t matrices, float inv_g, const PlanView& p, bool sorted, uint8_t* codes,
                                 uint8_t* scales, cudaStream_t stream) {
-    const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx * (bf16 ? 2 : 4) % 16 == 0;
+    const int64_t bytes = bf16 ? 16 : 32;  // of eight elements
+    const bool vec = reinterpret_cast<uintptr_t>(X) % bytes == 0 && ldx * (bytes / 8) % bytes == 0;
     auto go = [&](auto m) {
         constexpr bool MX = decltype(m)::value;
         if (bf16) {

@@ -342,7 +342,7 @@ int pnq_fp4_layout(int type, int64_t rows, int64_t K, int64_t matrices, int64_t 
  *   plan  NULL, or an expert plan: X holds plan->tokens rows (rows = tokens, matrices = 1), each is
  *         encoded once and written to the sorted rows of its slots; with PNQ_FP4_SORTED in flags X holds the
  *         sorted rows themselves (rows = tokens * slots; those past the rows in use are not read).
- * X element-aligned (16-byte aligned rows are faster); codes and scales 16-byte aligned. Errors: PNQ_ERR_FLAGS
+ * X element-aligned (rows on 16 bytes, fp32 on 32, are faster); codes and scales 16-byte aligned. Errors: PNQ_ERR_FLAGS
  * (an unknown flag, or PNQ_FP4_SORTED without a plan), PNQ_ERR_TYPE (format or element type), PNQ_ERR_SHAPE, PNQ_ERR_NULL, PNQ_ERR_ALIGN, PNQ_ERR_VALUE (g not
  * finite and > 0, or 1 / g not finite), PNQ_ERR_CUDA.
  */
