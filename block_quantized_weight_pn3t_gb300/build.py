@@ -100,7 +100,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         torch_lib = os.path.join(_torch_dir(), "lib")
         tmp = NATIVE + f".tmp{os.getpid()}"
         cmd = ["g++", "-shared", "-o", tmp, os.path.join(BUILD_DIR, "pnq_torch.o"), "-L", PKG, "-l:libpnq.so", "-L", torch_lib, "-lc10",
-               "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
+               "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
