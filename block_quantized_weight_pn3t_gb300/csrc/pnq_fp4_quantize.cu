@@ -168,25 +168,54 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const T* __rest
         for (int u = 0; u < STEPS; ++u) {
             encode8<MX>(x[u], k0 + 256 * u < K, inv_g, word[u], c[u]);
             // the words of four groups in one, in every lane of the four
-            word[u] = lane % kGroupLanes == 0 ? word[u] << (8 * (lane / kGroupLanes % 4)) : 0u;
+            word[u] <<= 8 * (lane / kGroupLanes % 4);
             word[u] |= __shfl_xor_sync(0xffffffffu, word[u], kGroupLanes);
             word[u] |= __shfl_xor_sync(0xffffffffu, word[u], 2 * kGroupLanes);
         }
-        auto put = [&](int64_t row, int64_t tiled) {
-            uint8_t* cp = codes + row * pitch + k0 / 2;
-            uint8_t* sp = scales + scale_word(tiled, 0, chunks);
+        // Codes of row `row`: where there are four steps the lanes of a four exchange them so that each writes 16 bytes of
+        // one step (a store instruction per row instead of four).
+        const int quad = lane & 3;
+        if constexpr (STEPS == 4) {
 #pragma unroll
-            for (int u = 0; u < STEPS; ++u) {
-                const int k = k0 + 256 * u, chunk = k / kChunkElems;
-                if (k < K) *reinterpret_cast<uint32_t*>(cp + 128 * u) = c[u];
-                if (lane % (4 * kGroupLanes) == 0 && chunk < chunks) *reinterpret_cast<uint32_t*>(sp + chunk * 512) = word[u];
+            for (int d = 1; d < 4; d <<= 1) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (u & d) continue;
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, quad & d ? c[u] : c[u + d], d);
+                    if (quad & d) c[u] = got;
+                    else c[u + d] = got;
+                }
+            }
+        }
+        auto put_codes = [&](int64_t row) {
+            uint8_t* cp = codes + row * pitch + (k0 - 8 * lane) / 2;
+            if constexpr (STEPS == 4) {
+                const int k = 256 * quad + 32 * (lane >> 2);  // within the item; the bytes up to the pitch are the row's own
+                if (k0 - 8 * lane + k < K) *reinterpret_cast<uint4*>(cp + k / 2) = make_uint4(c[0], c[1], c[2], c[3]);
+            } else {
+                if (k0 < K) *reinterpret_cast<uint32_t*>(cp + 4 * lane) = c[0];
             }
         };
+        // Scale words: lane l writes the word of step l % 4 of its chunk, and with a plan the lanes of a chunk's kSub fours
+        // write for kSub slots at once.
+        constexpr int kChunkLanes = 4 * kGroupLanes, kSub = kChunkLanes / 4, kChunksStep = 32 / kChunkLanes;
+        const int sub = lane % kChunkLanes / 4, step_of = STEPS == 4 ? quad : 0;
+        const int chunk = (k0 - 8 * lane) / kChunkElems + step_of * kChunksStep + lane / kChunkLanes;
+        const bool has = chunk < chunks && (STEPS == 4 || quad == 0);
+        const uint32_t mine = STEPS == 4 ? (quad == 0 ? word[0] : quad == 1 ? word[1 % STEPS] : quad == 2 ? word[2 % STEPS] : word[3 % STEPS])
+                                         : word[0];
+        auto put_scales = [&](int64_t tiled) {
+            *reinterpret_cast<uint32_t*>(scales + scale_word(tiled, chunk, chunks)) = mine;
+        };
         if (ROWS == Rows::Plain) {
-            put(r, tiled_row(r, rows, matrices));
+            put_codes(r);
+            if (has && sub == 0) put_scales(tiled_row(r, rows, matrices));
         } else if (ROWS == Rows::Sorted) {
             const int tiled = ld_l2(p.scale_row + r);
-            if (tiled >= 0) put(r, tiled);  // not past the rows in use
+            if (tiled >= 0) {  // not past the rows in use
+                put_codes(r);
+                if (has && sub == 0) put_scales(tiled);
+            }
         } else {
             for (int j0 = 0; j0 < p.slots; j0 += 32) {
                 if (j0) {
@@ -194,9 +223,14 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const T* __rest
                     if (j0 + lane < p.slots) at = ld_l2(p.position + r * p.slots + j0 + lane);
                     if (at >= 0) srow = ld_l2(p.scale_row + at);
                 }
-                for (int j = 0; j < min(32, p.slots - j0); ++j) {
-                    const int row = __shfl_sync(0xffffffffu, at, j), tiled = __shfl_sync(0xffffffffu, srow, j);
-                    if (row >= 0) put(row, tiled);
+                const int most = min(32, p.slots - j0);
+                for (int j = 0; j < most; ++j) {
+                    const int row = __shfl_sync(0xffffffffu, at, j);
+                    if (row >= 0) put_codes(row);
+                }
+                for (int j = 0; j < most; j += kSub) {  // lanes past the slots hold -1
+                    const int row = __shfl_sync(0xffffffffu, at, (j + sub) & 31), tiled = __shfl_sync(0xffffffffu, srow, (j + sub) & 31);
+                    if (has && row >= 0 && j + sub < most) put_scales(tiled);
                 }
             }
         }

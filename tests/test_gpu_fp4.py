@@ -76,6 +76,51 @@ def test_quantize_bits(kind, dtype, rows, K, g):
 
 
 @pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("dtype", list(FLOATS))
+@pytest.mark.parametrize("rows,K", [(2600, 1040), (1301, 2080), (900, 4128), (3000, 96)])
+def test_quantize_bits_many_rows(kind, dtype, rows, K):
+    """Enough rows that a warp takes 1024 elements at a time, K that ends inside them; plain, and through a plan both from
+    tokens and from sorted rows."""
+    if K % ref.GROUP[kind]:
+        K = K // 32 * 32 + 32
+    x = values_like(rows, K, seed=K)
+    xd = torch.from_numpy(x).cuda().to(FLOATS[dtype])
+    want_codes, want_words = ref.quantize(x, kind, 0.31)
+    codes, words = read_operand(pnq.fp4_quantize(kind, xd, 0.31))
+    assert np.array_equal(codes, want_codes) and np.array_equal(words, want_words)
+    E, k = 5, 3
+    ids = route(rows, k, E, seed=K, how="drop")
+    plan = pnq.expert_sort(torch.from_numpy(ids).cuda(), E)
+    offsets, _, order, _, scale_row = ref.plan(ids, E)
+    used = int(offsets[-1])
+    token = order[:used] // k
+    xs = torch.full((rows * k, K), float("nan"), dtype=FLOATS[dtype], device="cuda")
+    xs[:used] = xd[torch.from_numpy(token).cuda()]
+    for m in (pnq.fp4_quantize(kind, xd, 0.31, plan=plan), pnq.fp4_quantize(kind, xs, 0.31, plan=plan, sorted=True)):
+        codes, words = read_operand(m, np.maximum(scale_row, 0))
+        assert np.array_equal(codes[:used], want_codes[token]) and np.array_equal(words[:used], want_words[token])
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("slots", [1, 7, 33, 64])
+@pytest.mark.parametrize("tokens", [3, 2500])
+def test_quantize_every_slot(kind, slots, tokens):
+    """Any number of slots, over 32 too, few tokens and many."""
+    K, E = 160, 70
+    x = values_like(tokens, K, seed=slots)
+    ids = route(tokens, slots, E, seed=slots, how="even")
+    ids[0] = -1
+    plan = pnq.expert_sort(torch.from_numpy(ids).cuda(), E)
+    offsets, _, order, _, scale_row = ref.plan(ids, E)
+    used = int(offsets[-1])
+    m = pnq.fp4_quantize(kind, torch.from_numpy(x).cuda(), 1.0, plan=plan)
+    want_codes, want_words = ref.quantize(x, kind, 1.0)
+    codes, words = read_operand(m, np.maximum(scale_row, 0))
+    token = order[:used] // slots
+    assert np.array_equal(codes[:used], want_codes[token]) and np.array_equal(words[:used], want_words[token])
+
+
+@pytest.mark.parametrize("kind", TYPES)
 def test_quantize_edges(kind):
     """Ties of every scale and code, subnormal and huge magnitudes, saturation, infinities and NaN."""
     G = ref.GROUP[kind]
