@@ -9,6 +9,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -157,15 +158,39 @@ void require_matrix(const at::Tensor& t, const char* what, at::ScalarType dtype,
     require_device(t, what, device);
 }
 
-cudaStream_t stream_of(PyObject* stream, int device) {
-    if (!stream) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
-    PyObject* h = PyObject_GetAttrString(stream, "cuda_stream");
-    if (!h) throw PythonError{};
-    void* p = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (!p && PyErr_Occurred()) throw PythonError{};
-    return static_cast<cudaStream_t>(p);
-}
+// The device and stream of a call: the tensors' device, and the given stream or that device's current one. On a stream
+// other than the current one, results are allocated there, and the tensors named by record() are kept from
+// reuse until the work on it is done (they belong to another stream's pool).
+class Place {
+public:
+    Place(PyObject* stream, int device) : guard_(static_cast<c10::DeviceIndex>(device)) {
+        const auto current = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device));
+        stream_ = current.stream();
+        if (!stream) return;
+        PyObject* h = PyObject_GetAttrString(stream, "cuda_stream");
+        if (!h) throw PythonError{};
+        void* p = PyLong_AsVoidPtr(h);
+        Py_DECREF(h);
+        if (!p && PyErr_Occurred()) throw PythonError{};
+        if (p == stream_) return;
+        stream_ = static_cast<cudaStream_t>(p);
+        const auto other = c10::cuda::getStreamFromExternal(stream_, static_cast<c10::DeviceIndex>(device));
+        other_.emplace(other);
+    }
+    cudaStream_t stream() const { return stream_; }
+    template <class... Tensors>
+    void record(const Tensors&... t) const {
+        if (other_) (record_one(t), ...);
+    }
+
+private:
+    void record_one(const at::Tensor& t) const {
+        if (t.defined()) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), other_->current_stream());
+    }
+    c10::cuda::CUDAGuard guard_;
+    cudaStream_t stream_;
+    std::optional<c10::cuda::CUDAStreamGuard> other_;
+};
 
 // A new CUDA tensor (from torch's caching allocator, without the dispatcher on the way).
 at::Tensor new_tensor(at::IntArrayRef sizes, at::ScalarType dtype, int device) {
@@ -188,8 +213,6 @@ at::Tensor view_of(const at::Tensor& buffer, int64_t first, at::IntArrayRef size
 }
 
 PyObject* wrap(at::Tensor t) { return THPVariable_Wrap(std::move(t)); }
-
-c10::cuda::CUDAGuard on(int device) { return c10::cuda::CUDAGuard(static_cast<c10::DeviceIndex>(device)); }
 
 // ---- ExpertPlan ---------------------------------------------------------------------------------------
 
@@ -516,6 +539,7 @@ PNQ_ENTRY(fp4_quantize) {
         }
         const double g = a[2] ? to_double(a[2]) : 1.0;
         const int64_t out_rows = plan ? plan->rows : rows;
+        const Place place(a[5], device);
         Owned o{nullptr};
         if (a[4]) {
             MatrixObject* m = to_matrix(a[4], "out");
@@ -535,9 +559,10 @@ PNQ_ENTRY(fp4_quantize) {
         MatrixObject* m = reinterpret_cast<MatrixObject*>(o.o);
         m->scale = g;
         m->per_matrix = at::Tensor();
-        const auto guard = on(device);
+        place.record(x, m->scales, m->codes);
+        if (plan) place.record(plan->buffer);
         check(pnq_fp4_quantize(type, xt, x.data_ptr(), ldx, rows, K, matrices, static_cast<float>(g), plan ? &plan->desc : nullptr,
-                               sorted ? PNQ_FP4_SORTED : 0u, m->codes_at, m->scales_at, stream_of(a[5], device)),
+                               sorted ? PNQ_FP4_SORTED : 0u, m->codes_at, m->scales_at, place.stream()),
               "pnq_fp4_quantize");
         return o.release();
     });
@@ -564,12 +589,14 @@ PNQ_ENTRY(fp4_dequantize) {
         const Args<4> a("fp4_dequantize", names, 1, args, nargs, kwnames);
         MatrixObject* m = to_matrix(a[0], "m");
         if (m->per_matrix.defined()) refuse("an operand with a global scale per matrix is read back matrix by matrix");
+        const Place place(a[3], m->device);
         int type = 0;
         at::Tensor t = result(a[2], m->matrices * m->rows, m->K, dtype_of(a[1], at::kFloat), m->device, &type);
-        const auto guard = on(m->device);
+        place.record(m->codes, m->scales, t);
+        if (m->plan) place.record(reinterpret_cast<PlanObject*>(m->plan)->buffer);
         check(pnq_fp4_dequantize(m->type, m->codes_at, m->scales_at, m->rows, m->K, m->matrices, static_cast<float>(m->scale),
                                  m->plan ? &reinterpret_cast<PlanObject*>(m->plan)->desc : nullptr, type, t.data_ptr(),
-                                 stream_of(a[3], m->device)),
+                                 place.stream()),
               "pnq_fp4_dequantize");
         return returned(a[2], t);
     });
@@ -590,14 +617,15 @@ PNQ_ENTRY(fp4_pack) {
         m->device = codes.get_device();
         require_device(scales, "scales", m->device);
         set_scale(m, a[5]);
+        const Place place(a[7], m->device);
         const bool keep = K % 32 == 0 && reinterpret_cast<uintptr_t>(codes.data_ptr()) % 16 == 0;
         m->codes = keep ? codes : new_tensor({n, m->pitch}, at::kByte, m->device);
         m->scales = new_tensor({m->scale_bytes}, at::kByte, m->device);
         m->codes_at = m->codes.data_ptr<uint8_t>();
         m->scales_at = m->scales.data_ptr<uint8_t>();
-        const auto guard = on(m->device);
+        place.record(codes, scales);
         check(pnq_fp4_pack(type, codes.data_ptr<uint8_t>(), scales.data_ptr<uint8_t>(), rows, K, matrices, m->codes_at, m->scales_at,
-                           stream_of(a[7], m->device)),
+                           place.stream()),
               "pnq_fp4_pack");
         return o.release();
     });
@@ -623,11 +651,12 @@ PNQ_ENTRY(fp4_gemm) {
         check_operands(x, w);
         if (w->matrices != 1 || w->per_matrix.defined() || x->plan || w->plan)
             refuse("fp4_gemm takes one matrix each; expert layers go through fp4_gemm_experts");
+        const Place place(a[5], x->device);
         int type = 0;
         at::Tensor t = result(a[3], x->rows, w->rows, dtype_of(a[2], at::kFloat), x->device, &type);
-        const auto guard = on(x->device);
+        place.record(x->codes, x->scales, w->codes, w->scales, t);
         check(pnq_fp4_gemm(x->type, x->codes_at, x->scales_at, x->rows, w->codes_at, w->scales_at, w->rows, x->K,
-                           static_cast<float>(x->scale * w->scale), type, t.data_ptr(), to_flags(a[4]), stream_of(a[5], x->device)),
+                           static_cast<float>(x->scale * w->scale), type, t.data_ptr(), to_flags(a[4]), place.stream()),
               "pnq_fp4_gemm");
         return returned(a[3], t);
     });
@@ -648,14 +677,15 @@ PNQ_ENTRY(fp4_gemm_experts) {
             refuse("w has " + std::to_string(w->matrices) + " matrices; one for each of the plan's experts is wanted");
         if (plan->device != x->device)
             refuse("the operands are on cuda:" + std::to_string(x->device) + ", the plan on cuda:" + std::to_string(plan->device));
+        const Place place(a[6], x->device);
         int type = 0;
         at::Tensor t = result(a[4], plan->rows, w->rows, dtype_of(a[3], at::kFloat), x->device, &type);
         const bool per = w->per_matrix.defined();
-        const auto guard = on(x->device);
+        place.record(x->codes, x->scales, w->codes, w->scales, w->per_matrix, plan->buffer, t);
         check(pnq_fp4_gemm_experts(x->type, x->codes_at, x->scales_at, &plan->desc, w->codes_at, w->scales_at, w->rows, x->K,
                                    static_cast<float>(per ? x->scale : x->scale * w->scale),
                                    per ? w->per_matrix.data_ptr<float>() : nullptr, type, t.data_ptr(), to_flags(a[5]),
-                                   stream_of(a[6], x->device)),
+                                   place.stream()),
               "pnq_fp4_gemm_experts");
         return returned(a[4], t);
     });
@@ -673,6 +703,7 @@ PNQ_ENTRY(expert_sort) {
         const int64_t tokens = ids.size(0), slots = ids.size(1), experts = to_int(a[1]);
         check_plan_shape(tokens, slots, experts);
         const int device = ids.get_device();
+        const Place place(a[3], device);
         Owned o{nullptr};
         if (a[2]) {
             const PlanObject* p = to_plan(a[2]);
@@ -682,8 +713,8 @@ PNQ_ENTRY(expert_sort) {
         } else {
             o.o = reinterpret_cast<PyObject*>(new_plan(tokens, slots, experts, device));
         }
-        const auto guard = on(device);
-        check(pnq_expert_sort(ids.data_ptr<int32_t>(), &reinterpret_cast<PlanObject*>(o.o)->desc, stream_of(a[3], device)),
+        place.record(ids, reinterpret_cast<PlanObject*>(o.o)->buffer);
+        check(pnq_expert_sort(ids.data_ptr<int32_t>(), &reinterpret_cast<PlanObject*>(o.o)->desc, place.stream()),
               "pnq_expert_sort");
         return o.release();
     });
@@ -717,9 +748,10 @@ PNQ_ENTRY(expert_gather) {
         PlanObject* plan = to_plan(a[1]);
         const at::Tensor& x = tensor(a[0], "x");
         const int type = rows_of(x, "x", plan->desc.tokens, plan);
+        const Place place(a[3], plan->device);
         at::Tensor t = rows_out(a[2], x, plan->rows, plan);
-        const auto guard = on(plan->device);
-        check(pnq_expert_gather(type, x.data_ptr(), x.size(1), &plan->desc, t.data_ptr(), stream_of(a[3], plan->device)),
+        place.record(x, plan->buffer, t);
+        check(pnq_expert_gather(type, x.data_ptr(), x.size(1), &plan->desc, t.data_ptr(), place.stream()),
               "pnq_expert_gather");
         return returned(a[2], t);
     });
@@ -732,9 +764,10 @@ PNQ_ENTRY(expert_gather_backward) {
         PlanObject* plan = to_plan(a[1]);
         const at::Tensor& dxs = tensor(a[0], "dxs");
         const int type = rows_of(dxs, "dxs", plan->rows, plan);
+        const Place place(a[3], plan->device);
         at::Tensor t = rows_out(a[2], dxs, plan->desc.tokens, plan);
-        const auto guard = on(plan->device);
-        check(pnq_expert_gather_backward(type, dxs.data_ptr(), dxs.size(1), &plan->desc, t.data_ptr(), stream_of(a[3], plan->device)),
+        place.record(dxs, plan->buffer, t);
+        check(pnq_expert_gather_backward(type, dxs.data_ptr(), dxs.size(1), &plan->desc, t.data_ptr(), place.stream()),
               "pnq_expert_gather_backward");
         return returned(a[2], t);
     });
@@ -748,10 +781,11 @@ PNQ_ENTRY(expert_combine) {
         const at::Tensor& ys = tensor(a[0], "ys");
         const int type = rows_of(ys, "ys", plan->rows, plan);
         const at::Tensor& w = weights_of(a[2], plan, "weights");
+        const Place place(a[4], plan->device);
         at::Tensor t = rows_out(a[3], ys, plan->desc.tokens, plan);
-        const auto guard = on(plan->device);
+        place.record(ys, w, plan->buffer, t);
         check(pnq_expert_combine(type, ys.data_ptr(), ys.size(1), &plan->desc, w.data_ptr<float>(), t.data_ptr(),
-                                 stream_of(a[4], plan->device)),
+                                 place.stream()),
               "pnq_expert_combine");
         return returned(a[3], t);
     });
@@ -766,12 +800,13 @@ PNQ_ENTRY(expert_combine_backward) {
         const int type = rows_of(ys, "ys", plan->rows, plan);
         require_matrix(dy, "dy", ys.scalar_type(), plan->desc.tokens, ys.size(1), plan->device);
         const at::Tensor& w = weights_of(a[3], plan, "weights");
+        const Place place(a[6], plan->device);
         at::Tensor t = rows_out(a[4], ys, plan->rows, plan);
         at::Tensor dw = a[5] ? weights_of(a[5], plan, "dweights")
                              : new_matrix(plan->desc.tokens, plan->desc.slots, at::kFloat, plan->device);
-        const auto guard = on(plan->device);
+        place.record(dy, ys, w, plan->buffer, t, dw);
         check(pnq_expert_combine_backward(type, dy.data_ptr(), ys.data_ptr(), ys.size(1), &plan->desc, w.data_ptr<float>(),
-                                          t.data_ptr(), dw.data_ptr<float>(), stream_of(a[6], plan->device)),
+                                          t.data_ptr(), dw.data_ptr<float>(), place.stream()),
               "pnq_expert_combine_backward");
         Owned first{returned(a[4], t)}, second{returned(a[5], dw)};
         return PyTuple_Pack(2, first.o, second.o);

@@ -297,8 +297,8 @@ int pnq_selftest_wait(uint32_t limit_us, cudaStream_t stream);
  *   scales  tiles of 128 rows x 4 groups, 512 bytes each: the word of row r (0..127), group j
  *           (0..3) at byte 16 (r % 32) + 4 (r / 32) + j. Tiles of one 128-row block follow each
  *           other along K (ceil(K / (4 G)) of them); every matrix starts a new block; words of
- *           groups past K are zero. 16-byte aligned. NVFP4 words are E4M3FN, MXFP4 words biased
- *           exponents.
+ *           groups past K are zero. 16-byte aligned. NVFP4 words are E4M3FN (sign bit clear), MXFP4 words
+ *           biased exponents.
  *   global  one fp32 multiplier g: a value is e2m1 * scale * g.
  * Operands made with an expert plan hold the plan's sorted rows: codes row i is sorted row i, its
  * scales are at tiled row scale_row[i] (each expert's rows start a new 128-row block).
@@ -412,7 +412,7 @@ int pnq_expert_gather_backward(int type, const void* dXS, int64_t D, const pnq_e
 /*
  * pnq_expert_combine -- Y[t] = sum over t's slots j of weights[t][j] * YS[position] (weights device fp32
  * [tokens][slots]; YS [tokens * slots][D], Y [tokens][D]), in fp32, in slot order, rounded once. The rows
- * and weights of dropped slots are not read.
+ * and weights of dropped slots are not used.
  * pnq_expert_combine_backward -- its gradients: dYS[i] = weights * dY[token] for every sorted row (rows past the
  * rows in use are zeros), dWeights[t][j] = <dY[t], YS[position]> in fp32 (0 for a dropped slot). dWeights
  * may be NULL.

@@ -200,7 +200,7 @@ def check_product(y, x, w, alpha, dtype, what=""):
     assert np.all(err <= bound), (what, float((err / bound).max()))
 
 
-GEMMS = [(1, 1, 32), (1, 128, 64), (2, 129, 96), (3, 127, 272), (17, 64, 1056), (33, 300, 4128), (64, 256, 512),
+GEMMS = [(5, 7, 16), (1, 1, 32), (1, 128, 64), (2, 129, 96), (3, 127, 272), (17, 64, 1056), (33, 300, 4128), (64, 256, 512),
          (65, 257, 544), (100, 130, 288), (129, 500, 320), (200, 33, 64), (256, 256, 256), (300, 1001, 2080), (513, 384, 800)]
 
 
@@ -433,6 +433,30 @@ def test_streams_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, 2.0 * want)
+
+
+def test_another_stream_keeps_its_tensors():
+    """Calls on a stream that is behind: inputs freed after the call, and results made on that stream, are not handed to
+    the current stream's allocations while the work is still to come."""
+    kind, rows, K = pnq.NVFP4, 700, 2048
+    w = pnq.fp4_quantize(kind, torch.randn(256, K, device="cuda"))
+    x0 = torch.randn(rows, K, device="cuda")
+    want = pnq.fp4_gemm(pnq.fp4_quantize(kind, x0), w)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        x = x0.clone()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)  # about 10 ms
+        q = pnq.fp4_quantize(kind, x, stream=s)
+        y = pnq.fp4_gemm(q, w, stream=s)
+        del x, q
+        junk = [torch.full((rows, K), 3.0, device="cuda") for _ in range(4)] + \
+               [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (rows * K // 2, rows * K // 16) * 4]
+        s.synchronize()
+        assert torch.equal(y, want)
+        del junk
 
 
 def test_empty():
