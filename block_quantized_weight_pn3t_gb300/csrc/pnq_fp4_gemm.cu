@@ -62,7 +62,7 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxStages = 10;
 constexpr int kMaxSplit = 8;                   // CTAs of a cluster that share a tile's K
 constexpr int kSmemLimit = 227 * 1024;
-constexpr int kStaticSmem = 6 * 1024;          // barriers, expert tiles (rounded up)
+constexpr int kStaticSmem = 9 * 1024;          // barriers, first rows and tiles of the experts (rounded up)
 
 constexpr int imin(int a, int b) { return a < b ? a : b; }
 
@@ -143,24 +143,24 @@ struct Tile {
     int row0;     // first activation row (global)
     int rows;     // activation rows in the tile
     int n0;       // first weight row within the matrix
-    int sblock;   // 128-row scale block of row0
+    int sblock;   // 128-row scale block of row0 within the matrix
     int srow;     // row0's row within that block (a multiple of 64)
 };
 
 // Walks the tiles number first, first + step, ..: all roles of a CTA see the same sequence. Dense: bands of 16 weight
-// tiles, row tile by row tile (the CTAs at work share a few operand rows in L2). By experts: `starts[e]` (shared memory) is
-// the number of tiles before expert e. Steps by addition: a division or two per tile stood in the way of the threads
+// tiles, row tile by row tile (the CTAs at work share a few operand rows in L2). By experts: `starts[e]` and `firsts[e]`
+// (shared memory) are the tiles and the rows before expert e. Steps by addition: a division or two per tile stood in the way of the threads
 // that issue copies and MMAs.
 template <int BN, int CG>
 struct Walk {
     static constexpr int kTileN = CG * kRows, kBand = 16;
     const GemmArgs& a;
-    const int* starts;
+    const int *starts, *firsts;
     int at, step, nt, mt;   // dense: `at` counts from (m, 0) of the band
     int m, band, width;     // row tile; first weight tile of the band and its tiles
     int e;                  // expert
-    __device__ Walk(const GemmArgs& args, const int* tile_starts)
-        : a(args), starts(tile_starts), at(static_cast<int>(blockIdx.x) / CG), step(static_cast<int>(gridDim.x) / CG),
+    __device__ Walk(const GemmArgs& args, const int* tile_starts, const int* first_rows)
+        : a(args), starts(tile_starts), firsts(first_rows), at(static_cast<int>(blockIdx.x) / CG), step(static_cast<int>(gridDim.x) / CG),
           nt((args.N + kTileN - 1) / kTileN), mt((args.M + BN - 1) / BN), m(0), band(0), width(min(kBand, nt)), e(0) {}
     __device__ bool next(Tile& o) {
         if (a.p.experts == 0) {
@@ -182,10 +182,9 @@ struct Walk {
         } else {
             if (at >= starts[a.p.experts]) return false;
             while (at >= starts[e + 1]) ++e;
-            const int first = ld_l2(a.p.offsets + e), count = ld_l2(a.p.offsets + e + 1) - first;
+            const int first = firsts[e], count = firsts[e + 1] - first;
             const int tiles = (count + BN - 1) / BN, r = at - starts[e], n = r / tiles, i = r - n * tiles;
-            o = Tile{e, first + i * BN, min(BN, count - i * BN), n * kTileN, ld_l2(a.p.block_start + e) + i * BN / 128,
-                     i * BN % 128};
+            o = Tile{e, first + i * BN, min(BN, count - i * BN), n * kTileN, i * BN / 128, i * BN % 128};
         }
         at += step;
         return true;
@@ -210,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
     __shared__ uint32_t tmem_slot;
-    __shared__ int starts[kMaxExperts + 1];
+    __shared__ int starts[kMaxExperts + 1], firsts[kMaxExperts + 1];
     __shared__ int warp_sums[kThreads / 32];
     const uint32_t b0 = smem_addr(bars);
     auto full = [&](int s) { return b0 + 8u * s; };
@@ -254,8 +253,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         // tiles before each expert: a block scan, each thread over consecutive experts
         const int E = a.p.experts, nt = (a.N + CG * kRows - 1) / (CG * kRows), per = (E + kThreads - 1) / kThreads;
         const int e0 = min(E, static_cast<int>(threadIdx.x) * per), e1 = min(E, e0 + per);
-        int sum = 0;
-        for (int e = e0; e < e1; ++e) sum += (ld_l2(a.p.offsets + e + 1) - ld_l2(a.p.offsets + e) + BN - 1) / BN * nt;
+        int sum = 0, first = ld_l2(a.p.offsets + e0);
+        for (int e = e0; e < e1; ++e) {
+            const int next = ld_l2(a.p.offsets + e + 1);
+            firsts[e] = first;
+            starts[e] = (next - first + BN - 1) / BN * nt;
+            sum += starts[e];
+            first = next;
+        }
+        if (e1 == E) firsts[E] = first;
         int incl = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -267,8 +273,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         int at = incl - sum;
         for (int w = 0; w < warp; ++w) at += warp_sums[w];
         for (int e = e0; e < e1; ++e) {
+            const int tiles = starts[e];
             starts[e] = at;
-            at += (ld_l2(a.p.offsets + e + 1) - ld_l2(a.p.offsets + e) + BN - 1) / BN * nt;
+            at += tiles;
         }
         if (e1 == E && e0 < E) starts[E] = at;
     }
@@ -280,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     // this CTA's share of the stages along K: [kt0, kt1)
     const int nk = (a.K + kStageK - 1) / kStageK, kz = static_cast<int>(blockIdx.y);
     const int kt0 = kz * nk / a.ks, kt1 = (kz + 1) * nk / a.ks;
-    Walk<BN, CG> walk(a, starts);
+    Walk<BN, CG> walk(a, starts, firsts);
     Tile tile{};
 
     // Warps 0 and 1 run their loops in one elected lane: a wait by 32 lanes is 32 probes of the barrier, one after
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                 wrow = tile.e * a.N + n0;
                 wsc = (tile.e * blocks_w + n0 / 128) * a.chunks;
                 xrow = tile.row0 + static_cast<int>(rank) * (BN / CG);
-                xsc = tile.sblock * a.chunks;
+                xsc = ((a.p.experts ? ld_l2(a.p.block_start + tile.e) : 0) + tile.sblock) * a.chunks;
                 // rows past the tile's activations are not copied: their columns are not stored (and a copy's rows past
                 // the end of the matrix, filled with zeros, take longer than rows that are there)
                 xcopies = CG == 2 ? 1 : (tile.rows + a.xbox - 1) / a.xbox;  // a pair's CTAs copy one half each
@@ -320,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
             };
             int ahead = 0;  // stages of the first tile whose weights are under way
             if (early) {
-                Walk<BN, CG> first(a, starts);
+                Walk<BN, CG> first(a, starts, firsts);
                 if (first.next(tile)) {
                     take();
                     for (; ahead < min(S, kt1 - kt0); ++ahead) load_weights(ahead, kt0 + ahead);
@@ -487,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         // CTA kz of the cluster sums its share of the tile's columns over the ks partial tiles, in CTA order
         // (distributed shared memory), and writes them
         cluster_sync();
-        Walk<BN, CG> again(a, starts);
+        Walk<BN, CG> again(a, starts, firsts);
         if (again.next(tile)) {
             T* Y = static_cast<T*>(a.Y);
             const float scale = a.w_global ? a.alpha * ld_l2(a.w_global + tile.e) : a.alpha;
