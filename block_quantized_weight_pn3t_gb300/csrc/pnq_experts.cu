@@ -197,46 +197,47 @@ __global__ void __launch_bounds__(256) expert_order_kernel(const int32_t* __rest
 
 // ---- rows ---------------------------------------------------------------------------------------
 
-// V consecutive elements of T: 16 bytes (or one element, for rows that are not 16-byte aligned).
-template <class T, int V> struct Vec;
-template <> struct Vec<float, 4> {
-    using Raw = uint4;
-    static __device__ __forceinline__ void to_f32(const uint4& r, float (&f)[4]) {
-        f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y), f[2] = __uint_as_float(r.z), f[3] = __uint_as_float(r.w);
+// V consecutive elements of T in one access of 16 bytes, or of the 8, 4 or 2 that the rows' alignment allows; kSteps
+// such accesses a thread are in flight together, so that rows of any length keep the loads' bytes up.
+template <int BYTES> struct RawOf;
+template <> struct RawOf<16> { using type = uint4; };
+template <> struct RawOf<8> { using type = uint2; };
+template <> struct RawOf<4> { using type = uint32_t; };
+template <> struct RawOf<2> { using type = uint16_t; };
+
+template <class T, int V>
+struct Vec {
+    static constexpr int kBytes = V * static_cast<int>(sizeof(T)), kWords = kBytes < 4 ? 1 : kBytes / 4;
+    static constexpr int kSteps = kBytes == 16 ? 1 : kBytes == 8 ? 2 : 4;
+    using Raw = typename RawOf<kBytes>::type;
+    static __device__ __forceinline__ void words(const Raw& r, uint32_t (&w)[kWords]) {
+        if constexpr (kBytes == 16) w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
+        else if constexpr (kBytes == 8) w[0] = r.x, w[1] = r.y;
+        else w[0] = r;
     }
-    static __device__ __forceinline__ uint4 from_f32(const float (&f)[4]) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    }
-};
-template <> struct Vec<float, 1> {
-    using Raw = uint32_t;
-    static __device__ __forceinline__ void to_f32(const uint32_t& r, float (&f)[1]) { f[0] = __uint_as_float(r); }
-    static __device__ __forceinline__ uint32_t from_f32(const float (&f)[1]) { return __float_as_uint(f[0]); }
-};
-template <> struct Vec<__nv_bfloat16, 8> {
-    using Raw = uint4;
-    static __device__ __forceinline__ void to_f32(const uint4& r, float (&f)[8]) {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    static __device__ __forceinline__ void to_f32(const Raw& r, float (&f)[V]) {
+        uint32_t w[kWords];
+        words(r, w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int i = 0; i < V; ++i) {
+            if constexpr (sizeof(T) == 4) f[i] = __uint_as_float(w[i]);
+            else f[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
         }
     }
-    static __device__ __forceinline__ uint4 from_f32(const float (&f)[8]) {
-        uint32_t w[4];
+    static __device__ __forceinline__ Raw from_f32(const float (&f)[V]) {
+        uint32_t w[kWords];
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = f32x2_to_bf16x2(f[2 * i], f[2 * i + 1]);
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-template <> struct Vec<__nv_bfloat16, 1> {
-    using Raw = uint16_t;
-    static __device__ __forceinline__ void to_f32(const uint16_t& r, float (&f)[1]) {
-        f[0] = __uint_as_float(static_cast<uint32_t>(r) << 16);
-    }
-    static __device__ __forceinline__ uint16_t from_f32(const float (&f)[1]) {
-        return static_cast<uint16_t>(f32x2_to_bf16x2(f[0], 0.0f));
+            for (int i = 0; i < V; ++i) w[i] = __float_as_uint(f[i]);
+        } else if constexpr (V == 1) {
+            w[0] = f32x2_to_bf16x2(f[0], 0.0f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) w[i] = f32x2_to_bf16x2(f[2 * i], f[2 * i + 1]);
+        }
+        if constexpr (kBytes == 16) return make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (kBytes == 8) return make_uint2(w[0], w[1]);
+        else return static_cast<Raw>(w[0]);
     }
 };
 
@@ -259,6 +260,8 @@ template <int TEAM>
 struct Team {
     static constexpr int kThreads = TEAM > kRowThreads ? TEAM : kRowThreads;  // of a CTA
     static constexpr int kPerCta = kThreads / TEAM;
+    // accesses a thread has in flight: one in the largest teams, which take few tokens' rows in a step or two
+    static constexpr __host__ __device__ int steps(int most) { return TEAM > kRowThreads ? 1 : most; }
     static __device__ __forceinline__ int thread() { return static_cast<int>(threadIdx.x) % TEAM; }
     static __device__ __forceinline__ int64_t first() {
         return static_cast<int64_t>(blockIdx.x) * kPerCta + static_cast<int>(threadIdx.x) / TEAM;
@@ -289,17 +292,25 @@ template <class T, int V, int TEAM>
 __global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_gather_kernel(const typename Vec<T, V>::Raw* __restrict__ X,
                                                                     int64_t vecs, PlanView p,
                                                                     typename Vec<T, V>::Raw* __restrict__ XS) {
+    constexpr int U = Team<TEAM>::steps(Vec<T, V>::kSteps);
     griddep_begin();
     for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
         for (int j0 = 0; j0 < p.slots; j0 += kSlotBatch) {
             int at[kSlotBatch];
             float w[kSlotBatch];
             load_slots(p, nullptr, t, j0, at, w);
-            for (int64_t c = Team<TEAM>::thread(); c < vecs; c += TEAM) {
-                const auto v = ld_l2(X + t * vecs + c);
+            for (int64_t c = Team<TEAM>::thread(); c < vecs; c += TEAM * U) {
+                typename Vec<T, V>::Raw v[U];
 #pragma unroll
-                for (int j = 0; j < kSlotBatch; ++j)
-                    if (at[j] >= 0) XS[at[j] * vecs + c] = v;
+                for (int u = 0; u < U; ++u)
+                    if (c + u * TEAM < vecs) v[u] = ld_l2(X + t * vecs + c + u * TEAM);
+#pragma unroll
+                for (int j = 0; j < kSlotBatch; ++j) {
+                    if (at[j] < 0) continue;
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (c + u * TEAM < vecs) XS[at[j] * vecs + c + u * TEAM] = v[u];
+                }
             }
         }
     }
@@ -313,6 +324,7 @@ __global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_combine_kernel(co
                                                                      const float* __restrict__ weights,
                                                                      typename Vec<T, V>::Raw* __restrict__ Y) {
     using Raw = typename Vec<T, V>::Raw;
+    constexpr int U = Team<TEAM>::steps(Vec<T, V>::kSteps);
     const int k = p.slots;
     griddep_begin();
     for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
@@ -320,28 +332,37 @@ __global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_combine_kernel(co
         float w[kSlotBatch];
         load_slots(p, weights, t, 0, at, w);
         // whole warps take the columns' steps together (the slots are loaded again in each where there are over kSlotBatch)
-        for (int64_t c0 = Team<TEAM>::thread() & ~31; c0 < vecs; c0 += TEAM) {
+        for (int64_t c0 = Team<TEAM>::thread() & ~31; c0 < vecs; c0 += TEAM * U) {
             const int64_t c = c0 + (static_cast<int>(threadIdx.x) & 31);
-            const bool live = c < vecs;
-            float acc[V];
+            float acc[U][V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[u][i] = 0.0f;
             for (int j0 = 0; j0 < k; j0 += kSlotBatch) {
                 if (k > kSlotBatch) load_slots(p, weights, t, j0, at, w);
-                Raw r[kSlotBatch];
+                Raw r[kSlotBatch][U];
 #pragma unroll
                 for (int j = 0; j < kSlotBatch; ++j)
-                    if (at[j] >= 0 && live) r[j] = ld_l2(YS + at[j] * vecs + c);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (at[j] >= 0 && c + u * TEAM < vecs) r[j][u] = ld_l2(YS + at[j] * vecs + c + u * TEAM);
 #pragma unroll
                 for (int j = 0; j < kSlotBatch; ++j) {
-                    if (at[j] < 0 || !live) continue;
-                    float f[V];
-                    Vec<T, V>::to_f32(r[j], f);
+                    if (at[j] < 0) continue;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+                    for (int u = 0; u < U; ++u) {
+                        if (c + u * TEAM >= vecs) continue;
+                        float f[V];
+                        Vec<T, V>::to_f32(r[j][u], f);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) acc[u][i] = fmaf(w[j], f[i], acc[u][i]);
+                    }
                 }
             }
-            if (live) Y[t * vecs + c] = Vec<T, V>::from_f32(acc);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c + u * TEAM < vecs) Y[t * vecs + c + u * TEAM] = Vec<T, V>::from_f32(acc[u]);
         }
     }
 }
@@ -353,6 +374,7 @@ __global__ void __launch_bounds__(Team<TEAM>::kThreads, TEAM > kRowThreads ? 1 :
     PlanView p, const float* __restrict__ weights, typename Vec<T, V>::Raw* __restrict__ dYS,
     float* __restrict__ dWeights) {
     using Raw = typename Vec<T, V>::Raw;
+    constexpr int U = Team<TEAM>::steps(Vec<T, V>::kSteps);
     __shared__ float part[Team<TEAM>::kThreads / 32][kSlotBatch];
     const int k = p.slots, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_begin();
@@ -363,27 +385,35 @@ __global__ void __launch_bounds__(Team<TEAM>::kThreads, TEAM > kRowThreads ? 1 :
             load_slots(p, weights, t, j0, at, w);
 #pragma unroll
             for (int j = 0; j < kSlotBatch; ++j) dot[j] = 0.0f;
-            for (int64_t c = Team<TEAM>::thread(); c < vecs; c += TEAM) {
-                const Raw gr = ld_l2(dY + t * vecs + c);
-                Raw r[kSlotBatch];
+            for (int64_t c = Team<TEAM>::thread(); c < vecs; c += TEAM * U) {
+                Raw gr[U], r[kSlotBatch][U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c + u * TEAM < vecs) gr[u] = ld_l2(dY + t * vecs + c + u * TEAM);
                 if (dWeights) {
 #pragma unroll
                     for (int j = 0; j < kSlotBatch; ++j)
-                        if (at[j] >= 0) r[j] = ld_l2(YS + at[j] * vecs + c);
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+                            if (at[j] >= 0 && c + u * TEAM < vecs) r[j][u] = ld_l2(YS + at[j] * vecs + c + u * TEAM);
                 }
-                float g[V];
-                Vec<T, V>::to_f32(gr, g);
 #pragma unroll
-                for (int j = 0; j < kSlotBatch; ++j) {
-                    if (at[j] < 0) continue;
-                    float f[V];
+                for (int u = 0; u < U; ++u) {
+                    if (c + u * TEAM >= vecs) continue;
+                    float g[V];
+                    Vec<T, V>::to_f32(gr[u], g);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) f[i] = w[j] * g[i];
-                    dYS[at[j] * vecs + c] = Vec<T, V>::from_f32(f);
-                    if (dWeights) {
-                        Vec<T, V>::to_f32(r[j], f);
+                    for (int j = 0; j < kSlotBatch; ++j) {
+                        if (at[j] < 0) continue;
+                        float f[V];
 #pragma unroll
-                        for (int i = 0; i < V; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
+                        for (int i = 0; i < V; ++i) f[i] = w[j] * g[i];
+                        dYS[at[j] * vecs + c + u * TEAM] = Vec<T, V>::from_f32(f);
+                        if (dWeights) {
+                            Vec<T, V>::to_f32(r[j][u], f);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
+                        }
                     }
                 }
             }
@@ -413,9 +443,11 @@ __global__ void __launch_bounds__(Team<TEAM>::kThreads, TEAM > kRowThreads ? 1 :
     zero_tail(dYS, p, p.tokens * k, vecs);
 }
 
-bool vectorised(const void* a, const void* b, const void* c, int64_t row_bytes) {
-    return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c)) % 16 == 0) &&
-           row_bytes % 16 == 0;
+// Bytes of the widest access that the tensors' addresses and the rows' length allow (16 at most).
+int access_bytes(const void* a, const void* b, const void* c, int64_t row_bytes) {
+    const uintptr_t all = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c) |
+                          static_cast<uintptr_t>(row_bytes) | 16u;
+    return static_cast<int>(all & (~all + 1));
 }
 
 template <class T, int V>
@@ -451,11 +483,13 @@ cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const
 template <class T, int V>
 cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const PlanView& p, const float* weights,
                      void* out, float* dw, cudaStream_t stream) {
-    // A warp per token where the tokens give every SM 16 warps (16384 tokens of 2048 bf16, 8 slots: combine 97 us against 112
-    // with a CTA per token, its gradients 178 against 204; 7 tokens of 1999 fp32 take 28 us by warps and 5 by CTAs). The
-    // gather of a row that a CTA takes in one step or more keeps the CTA (93 us against 96). Few tokens of long rows:
-    // CTAs of 1024 threads (7 tokens of 1999 fp32, 6 slots: combine 4.4 -> 2.7 us), 512 for the gradients, which need twice
-    // the registers.
+    // A warp per token where the tokens give every SM 16 warps (16384 tokens of 2048 bf16, 8 slots: combine 92 us = 6.5 TB/s,
+    // its gradients 182 = 6.3 TB/s; a CTA per token took 13 to 15 percent longer; 7 tokens of 1999 fp32 took 28 us by warps
+    // and 5 by CTAs of 256). The gather of a row that a CTA takes in one step or more keeps the CTA (93 us against 96).
+    // Few tokens of long rows: CTAs of 1024 threads (those 7 tokens: combine 4.4 -> 2.9 us), 512 for the gradients, which
+    // need twice the registers.
+    // Rows that are not on 16 bytes (D = 3924 bf16, 3194 tokens, 4 slots): gather 25.6 us, combine 40; 34 and 77 where D
+    // is odd and an access two bytes; 7 times as long with one access of an element a thread.
     const int64_t vecs = D / V, sms = device_sm_count();
     if (p.tokens >= sms * 16 && (op != ExpertOp::Gather || vecs < kRowThreads))
         return run_rows<T, V, 32>(op, a, b, D, p, weights, out, dw, stream);
@@ -469,12 +503,19 @@ cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const
 
 cudaError_t launch_expert_rows(ExpertOp op, bool bf16, const void* a, const void* b, int64_t D, const PlanView& p,
                                const float* weights, void* out, float* dweights, cudaStream_t stream) {
-    if (bf16) {
-        if (vectorised(a, b, out, D * 2)) return run_rows<__nv_bfloat16, 8>(op, a, b, D, p, weights, out, dweights, stream);
-        return run_rows<__nv_bfloat16, 1>(op, a, b, D, p, weights, out, dweights, stream);
+    switch (access_bytes(a, b, out, D * (bf16 ? 2 : 4))) {
+        case 16:
+            return bf16 ? run_rows<__nv_bfloat16, 8>(op, a, b, D, p, weights, out, dweights, stream)
+                        : run_rows<float, 4>(op, a, b, D, p, weights, out, dweights, stream);
+        case 8:
+            return bf16 ? run_rows<__nv_bfloat16, 4>(op, a, b, D, p, weights, out, dweights, stream)
+                        : run_rows<float, 2>(op, a, b, D, p, weights, out, dweights, stream);
+        case 4:
+            return bf16 ? run_rows<__nv_bfloat16, 2>(op, a, b, D, p, weights, out, dweights, stream)
+                        : run_rows<float, 1>(op, a, b, D, p, weights, out, dweights, stream);
+        default:
+            return run_rows<__nv_bfloat16, 1>(op, a, b, D, p, weights, out, dweights, stream);
     }
-    if (vectorised(a, b, out, D * 4)) return run_rows<float, 4>(op, a, b, D, p, weights, out, dweights, stream);
-    return run_rows<float, 1>(op, a, b, D, p, weights, out, dweights, stream);
 }
 
 cudaError_t launch_expert_sort(const int32_t* ids, const PlanView& p, cudaStream_t stream) {

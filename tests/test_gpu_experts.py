@@ -32,7 +32,8 @@ def test_sort(T, k, E, how):
 
 
 ROWS = [(1, 1, 1, "even", 1), (1, 8, 64, "even", 5120), (7, 3, 5, "drop", 33), (40, 9, 12, "drop", 264), (20, 17, 30, "even", 100),
-        (100, 2, 3, "one", 1999), (50, 4, 6, "none", 64), (700, 8, 128, "skew", 520)]
+        (100, 2, 3, "one", 1999), (50, 4, 6, "none", 64), (700, 8, 128, "skew", 520), (5, 3, 4, "even", 2052), (3000, 3, 9, "drop", 300),
+        (2600, 9, 20, "drop", 67), (4, 2, 3, "even", 12290), (300, 2, 5, "drop", 1030)]
 
 
 def rows_on_gpu(a, dtype, offset):
