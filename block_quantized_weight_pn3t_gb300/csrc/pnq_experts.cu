@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int3
     int* total = hist + W * E;    // [E] counts of this CTA
     int* first = total + E;       // [E] first sorted row of the expert
     int* block0 = first + E;      // [E] first scale block of the expert
+    int* base = block0 + E;       // [E] first sorted row of the expert's slots in this CTA
     __shared__ unsigned long long warp_sums[32];
     __shared__ int used_rows;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = static_cast<int>(blockDim.x);
@@ -113,20 +114,23 @@ __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int3
         cluster_sync();
         if (tid < E) {
             all = 0;
-            for (int c = 0; c < C; ++c) {
-                const int v = ld_dsmem_s32(smem_addr(total + tid), static_cast<uint32_t>(c));
-                if (c < rank) before += v;
-                all += v;
+            int v[kSortCluster];  // all the loads in flight together: one takes some 0.25 us
+#pragma unroll
+            for (int c = 0; c < kSortCluster; ++c) v[c] = c < C ? ld_dsmem_s32(smem_addr(total + tid), static_cast<uint32_t>(c)) : 0;
+#pragma unroll
+            for (int c = 0; c < kSortCluster; ++c) {
+                if (c < rank) before += v[c];
+                all += v[c];
             }
         }
     }
-    if (MANY) cluster_sync();  // every CTA has read the counts: they may be written over, and the CTAs may leave
+    if (MANY) cluster_arrive();  // this CTA has read the counts (cluster_wait at the end: no CTA leaves before all have)
     // rows and 128-row blocks before expert tid, in one scan
     const unsigned long long pre =
         block_exclusive_scan((static_cast<unsigned long long>((all + 127) / 128) << 32) | static_cast<unsigned>(all), warp_sums);
     const int off = static_cast<int>(pre & 0xffffffffu), blk = static_cast<int>(pre >> 32);
     if (tid < E) {
-        total[tid] = off + before;  // this CTA's first sorted row of the expert (no one reads the counts any more, below)
+        base[tid] = off + before;  // this CTA's first sorted row of the expert
         first[tid] = off;
         block0[tid] = blk;
         if (rank == 0) {
@@ -156,7 +160,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int3
                 same &= one ? ones : ~ones;
             }
             const int r = __popc(same & ((1u << lane) - 1u));
-            const int at = e[j] >= 0 ? mine[e[j]] + total[e[j]] + r : -1;
+            const int at = e[j] >= 0 ? mine[e[j]] + base[e[j]] + r : -1;
             __syncwarp();
             if (e[j] >= 0 && r == 0) mine[e[j]] += __popc(same);
             __syncwarp();
@@ -172,6 +176,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const int3
             p.order[i] = -1;
             p.scale_row[i] = -1;
         }
+    if (MANY) cluster_wait();
 }
 
 // order and scale_row from position (many slots).
@@ -489,7 +494,7 @@ cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const
     // Few tokens of long rows: CTAs of 1024 threads (those 7 tokens: combine 4.4 -> 2.9 us), 512 for the gradients, which
     // need twice the registers.
     // Rows that are not on 16 bytes (D = 3924 bf16, 3194 tokens, 4 slots): gather 25.6 us, combine 40; 34 and 77 where D
-    // is odd and an access two bytes; 7 times as long with one access of an element a thread.
+    // is odd and an access two bytes; with one access of one element a thread the two took some three times as long.
     const int64_t vecs = D / V, sms = device_sm_count();
     if (p.tokens >= sms * 16 && (op != ExpertOp::Gather || vecs < kRowThreads))
         return run_rows<T, V, 32>(op, a, b, D, p, weights, out, dw, stream);
@@ -525,10 +530,10 @@ cudaError_t launch_expert_sort(const int32_t* ids, const PlanView& p, cudaStream
     const int C = std::max(1, std::min(kSortCluster, (batches + 31) / 32));
     const int warps = C > 1 ? 32 : std::max({1, batches, (p.experts + 31) / 32});
     const int per = std::max(1, (batches + C * warps - 1) / (C * warps));
-    const int smem = (warps + 3) * p.experts * static_cast<int>(sizeof(int));
+    const int smem = (warps + 4) * p.experts * static_cast<int>(sizeof(int));
     const auto kern = C > 1 ? expert_sort_kernel<true> : expert_sort_kernel<false>;
-    // opt in to the most any number of experts needs (1024: 143,360 bytes), once per device
-    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), (kSortThreads / 32 + 3) * 1024 * 4);
+    // opt in to the most any number of experts needs (1024: 147,456 bytes), once per device
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), (kSortThreads / 32 + 4) * 1024 * 4);
     if (e == cudaSuccess && C > 8) e = opt_in_cluster(reinterpret_cast<const void*>(kern));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc{};
