@@ -626,7 +626,7 @@ struct Shape {
     double stage, tile, last;
 };
 constexpr Shape kShapes[] = {{32, 1, 0.25, 0.6, 0.0}, {64, 1, 0.25, 0.7, 0.3}, {128, 1, 0.21, 1.0, 0.8}, {256, 2, 0.30, 1.9, 2.4}};
-constexpr Shape kExpertShapes[] = {{64, 1, 0, 0, 0}, {128, 1, 0, 0, 0}, {256, 1, 0, 0, 0}};
+constexpr Shape kExpertShapes[] = {{64, 1, 0, 0, 0}, {128, 1, 0, 0, 0}, {256, 1, 0, 0, 0}, {256, 2, 0, 0, 0}};
 
 }  // namespace
 
@@ -654,9 +654,11 @@ cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t
     Shape best{};
     if (p.experts) {
         // the experts' loads are not known here: by the rows in all, and by the average. 64 columns where no expert can
-        // have more (one token, 8 of 64 experts of 1408 x 2048: 8.4 us, 10.1 with 128), 256 where most tiles fill
-        // them (512 rows each: 57 us, 59 with 128; 256 rows each: 39 us, 38 with 128)
-        best = kExpertShapes[x.rows <= 64 ? 0 : x.rows < 384ll * p.experts ? 1 : 2];
+        // have more (one token, 8 of 64 experts of 1408 x 2048: 8.2 us, 8.5 with 128); 256 where tiles fill well enough
+        // (64 experts of 1408 x 2048, 100 rows each: 24.1 us with 128, 27.4 with 256; 192 each: 34.7 and 29.5), by pairs
+        // where K outweighs their dearer change of tiles (8 experts of 4096 x 4096, 1000 rows each: 58.7 us and 54.9 by
+        // pairs; 64 of 1408 x 2048: 87.3 and 95.4)
+        best = kExpertShapes[x.rows <= 64 ? 0 : x.rows < 160ll * p.experts ? 1 : K < 4096 ? 2 : 3];
         a.weights_once = best.bn < 256;
     } else {
         // the shape, and the share of K, whose estimate is least

@@ -293,7 +293,8 @@ def test_gemm_every_shape_of_tile(kind, M, N, K, dtype):
 
 
 @pytest.mark.parametrize("kind", TYPES)
-@pytest.mark.parametrize("T,k,E,N,K", [(1700, 2, 8, 300, 544), (900, 4, 7, 1408, 1056), (60, 1, 16, 700, 4128), (513, 8, 64, 200, 288)])
+@pytest.mark.parametrize("T,k,E,N,K", [(1700, 2, 8, 300, 544), (900, 4, 7, 1408, 1056), (60, 1, 16, 700, 4128), (513, 8, 64, 200, 288),
+                                       (900, 2, 5, 385, 4128), (2000, 3, 3, 1000, 4352)])
 def test_gemm_experts_large(kind, T, k, E, N, K):
     """Many rows per expert (256-column tiles), tiles that several experts' loads leave ragged."""
     ids = route(T, k, E, seed=T, how="skew" if E > 8 else "drop")
