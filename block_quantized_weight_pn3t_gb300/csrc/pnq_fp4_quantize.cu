@@ -64,75 +64,126 @@ __device__ __forceinline__ float e4m3_bits_to_f32(uint32_t word) {
     return __low2float(u32_as_half2(e4m3x2_to_f16x2(word)));
 }
 
-// Eight consecutive elements. VEC: by one load, 8 * sizeof(T) bytes aligned.
+// Eight consecutive elements as loaded: four words of two bf16, or eight floats. VEC: by one load, 8 * sizeof(T) bytes
+// aligned.
+template <class T>
+struct Eight {
+    static constexpr int kWords = 2 * static_cast<int>(sizeof(T));
+    uint32_t w[kWords];
+};
+
 template <class T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+__device__ __forceinline__ void load8(const T* p, Eight<T>& x) {
     if constexpr (sizeof(T) == 4) {
         if constexpr (VEC) {
-            ld_l2_f32x8(p, x);
+            float f[8];
+            ld_l2_f32x8(p, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x.w[i] = __float_as_uint(f[i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = ld_l2(p + i);
+            for (int i = 0; i < 8; ++i) x.w[i] = __float_as_uint(ld_l2(p + i));
         }
     } else {
-        uint32_t w[4];
         if constexpr (VEC) {
             const uint4 a = ld_l2(reinterpret_cast<const uint4*>(p));
-            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+            x.w[0] = a.x, x.w[1] = a.y, x.w[2] = a.z, x.w[3] = a.w;
         } else {
             const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = ld_l2(h + 2 * i) | (static_cast<uint32_t>(ld_l2(h + 2 * i + 1)) << 16);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            for (int i = 0; i < 4; ++i) x.w[i] = ld_l2(h + 2 * i) | (static_cast<uint32_t>(ld_l2(h + 2 * i + 1)) << 16);
         }
     }
 }
 
-// x / s rounded to nearest, for s > 0 and r = 1 / s rounded to nearest: two fused steps after the first estimate
-// give the correctly rounded quotient (P. W. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990). Where the remainder underflows the quotient is far below the least nonzero
-// code's threshold. The sign is x's, of a zero too (the fused steps would make -0 a +0).
-__device__ __forceinline__ float divide(float x, float s, float r) {
-    const float q = x * r;
-    return copysignf(fmaf(fmaf(-q, s, x), r, q), x);
+// Largest magnitude of the eight; NaN where one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+template <class T>
+__device__ __forceinline__ float magnitude(const Eight<T>& x) {
+    if constexpr (sizeof(T) == 4) {
+        float m = fabsf(__uint_as_float(x.w[0]));
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(__uint_as_float(x.w[i])));
+        return m;
+    } else {
+        uint32_t m = x.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) m = max_nan_bf16x2(m, x.w[i] & 0x7FFF7FFFu);
+        m = max_nan_bf16x2(m, m >> 16);  // the low half: both halves' largest
+        return __uint_as_float(m << 16);
+    }
+}
+// Elements 2 i and 2 i + 1 as packed floats.
+template <class T>
+__device__ __forceinline__ uint64_t pair_of(const Eight<T>& x, int i) {
+    if constexpr (sizeof(T) == 4) return f32x2_pack(__uint_as_float(x.w[2 * i]), __uint_as_float(x.w[2 * i + 1]));
+    else return f32x2_pack(__uint_as_float(x.w[i] << 16), __uint_as_float(x.w[i] & 0xFFFF0000u));
 }
 
-// Encodes this lane's 8 elements (live: the lane is inside the row): its scale word and its 8 codes. The
-// group's lanes (2 for NVFP4, 4 for MXFP4) are neighbours.
-template <bool MX>
-__device__ __forceinline__ void encode8(float (&x)[8], bool live, float inv_g, uint32_t& word, uint32_t& codes) {
-    uint32_t top = 0;  // largest |y| as bits: infinities and NaN sort above every finite value
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = live ? __fmul_rn(x[i], inv_g) : 0.0f;
-        top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    if (MX) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const bool finite = top < 0x7F800000u;
-    const float amax = __uint_as_float(top);
-    float t[8];
+// v / 6 rounded to nearest (see encode8).
+__device__ __forceinline__ float sixth(float v) {
+    const float q = v * (1.0f / 6.0f);
+    return fmaf(fmaf(-q, 6.0f, v), 1.0f / 6.0f, q);
+}
+
+// 1 / s rounded to nearest for an E4M3 value s > 0: an approximation one unit off at most, and one Newton step (the same
+// paper), which leaves 2^-46 of 1 / s before its own rounding. s is 8 .. 15 or 1 .. 7 times a power of two: 1 / s is such a
+// power itself or has binary digits of a period of 12 at most, so no midpoint of two floats is that near. All 126 values are
+// tested through the codes on both sides of every threshold.
+__device__ __forceinline__ float reciprocal(float s) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return fmaf(fmaf(-r, s, 1.0f), r, r);
+}
+
+// Encodes this lane's 8 elements (zeros where the lane is past the row): its scale word and its 8 codes. The group's lanes
+// (2 for NVFP4, 4 for MXFP4) are neighbours. Instructions, not HBM, bounded the encode of bf16, so two elements go through
+// each packed one, and the largest |y| is made from the largest |x| (the product's rounding keeps their order): 8191 x 5152
+// to NVFP4 36.0 -> 27.0 us from bf16, 36.3 -> 30.8 from fp32; to MXFP4 30.7 -> 22.2 and 30.8 -> 29.5.
+//
+// y / s is rounded to nearest, from r = 1 / s rounded to nearest, by two fused steps after the first estimate (P. W.
+// Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990):
+// q = y r, y / s = q - (q s - y) r. Written with -y and -r the signs of zeros come out right. Where the remainder
+// underflows the quotient is far below the least nonzero code's threshold.
+template <bool MX, class T>
+__device__ __forceinline__ void encode8(const Eight<T>& x, float inv_g, uint32_t& word, uint32_t& codes) {
+    float amax = magnitude(x);
+    amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    if (MX) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    amax = __fmul_rn(amax, inv_g);
+    const bool finite = __float_as_uint(amax) < 0x7F800000u;
     bool zero = !finite;
+    const uint64_t ng = f32x2_pack(-inv_g, -inv_g);
+    float t[8];
     if (MX) {
         // floor(log2 amax) - 2 in the biased exponent; amax below 2^-125 (zero too) takes the least, 2^-127
-        const int b = max(static_cast<int>(top >> 23) - 2, 0);
+        const int b = max(static_cast<int>(__float_as_uint(amax) >> 23) - 2, 0);
         word = finite ? static_cast<uint32_t>(b) : 255u;
         const float inv = __uint_as_float(static_cast<uint32_t>(254 - b) << 23);  // 2^(127 - b), exact
+        const uint64_t ni = f32x2_pack(-inv, -inv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = x[i] * inv;
+        for (int i = 0; i < 4; ++i) f32x2_unpack(f32x2_mul(f32x2_mul(pair_of(x, i), ng), ni), t[2 * i], t[2 * i + 1]);
     } else {
-        word = finite ? f32_to_e4m3(divide(amax, 6.0f, 1.0f / 6.0f)) : 0x7Fu;
+        word = finite ? f32_to_e4m3(sixth(amax)) : 0x7Fu;
         zero |= word == 0;
-        const float s = zero ? 1.0f : e4m3_bits_to_f32(word), r = __frcp_rn(s);
+        const float s = zero ? 1.0f : e4m3_bits_to_f32(word), r = reciprocal(s);
+        const uint64_t ss = f32x2_pack(s, s), nr = f32x2_pack(-r, -r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = divide(x[i], s, r);
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t ny = f32x2_mul(pair_of(x, i), ng), q = f32x2_mul(ny, nr);
+            f32x2_unpack(f32x2_fma(f32x2_fma(q, ss, ny), nr, q), t[2 * i], t[2 * i + 1]);
+        }
     }
     codes = zero ? 0u : f32x8_to_e2m1(t);
-    if (!live) word = 0;
 }
 
 // Where the encoded rows go: row r to row r; a plan's token to the sorted rows of its slots; a plan's sorted row to its place.
@@ -154,24 +205,37 @@ __global__ void __launch_bounds__(kQThreads, 8) fp4_quantize_kernel(const T* __r
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
         const int64_t r = items <= INT32_MAX ? static_cast<int32_t>(it) / per_row : it / per_row;
         const int k0 = static_cast<int>(it - r * per_row) * (STEPS * 256) + 8 * lane;
-        float x[STEPS][8];
+        Eight<T> x[STEPS];
 #pragma unroll
-        for (int u = 0; u < STEPS; ++u)
+        for (int u = 0; u < STEPS; ++u) {
+            x[u] = Eight<T>{};
             if (k0 + 256 * u < K) load8<T, VEC>(X + r * ldx + k0 + 256 * u, x[u]);
+        }
         // with a plan: where the row goes, lane j holding slot j's places
         int at = -1, srow = 0;
         if (ROWS == Rows::Tokens && lane < p.slots) {
             at = ld_l2(p.position + r * p.slots + lane);
             if (at >= 0) srow = ld_l2(p.scale_row + at);
         }
-        uint32_t word[STEPS], c[STEPS];
+        uint32_t c[STEPS], words = 0;  // words: a byte of each step, the same in a group's lanes; groups past K: zero
 #pragma unroll
         for (int u = 0; u < STEPS; ++u) {
-            encode8<MX>(x[u], k0 + 256 * u < K, inv_g, word[u], c[u]);
-            // the words of four groups in one, in every lane of the four
-            word[u] <<= 8 * (lane / kGroupLanes % 4);
-            word[u] |= __shfl_xor_sync(0xffffffffu, word[u], kGroupLanes);
-            word[u] |= __shfl_xor_sync(0xffffffffu, word[u], 2 * kGroupLanes);
+            uint32_t word;
+            encode8<MX>(x[u], inv_g, word, c[u]);
+            if (k0 + 256 * u < K) words |= word << (8 * u);
+        }
+        // Four groups are a scale word. Four steps: the groups transpose their four bytes, so that group i holds the word of
+        // step i; one step: every group gathers the word.
+        const int group = lane / kGroupLanes % 4;  // within the four
+        if constexpr (STEPS == 4) {
+            uint32_t got = __shfl_xor_sync(0xffffffffu, words, kGroupLanes);
+            words = group & 1 ? prmt(words, got, 0x3715) : prmt(words, got, 0x6240);
+            got = __shfl_xor_sync(0xffffffffu, words, 2 * kGroupLanes);
+            words = group & 2 ? prmt(words, got, 0x3276) : prmt(words, got, 0x5410);
+        } else {
+            words <<= 8 * group;
+            words |= __shfl_xor_sync(0xffffffffu, words, kGroupLanes);
+            words |= __shfl_xor_sync(0xffffffffu, words, 2 * kGroupLanes);
         }
         // Codes of row `row`: where there are four steps the lanes of a four exchange them so that each writes 16 bytes of
         // one step (a store instruction per row instead of four).
@@ -197,16 +261,14 @@ __global__ void __launch_bounds__(kQThreads, 8) fp4_quantize_kernel(const T* __r
                 if (k0 < K) *reinterpret_cast<uint32_t*>(cp + 4 * lane) = c[0];
             }
         };
-        // Scale words: lane l writes the word of step l % 4 of its chunk, and with a plan the lanes of a chunk's kSub fours
-        // write for kSub slots at once.
-        constexpr int kChunkLanes = 4 * kGroupLanes, kSub = kChunkLanes / 4, kChunksStep = 32 / kChunkLanes;
-        const int sub = lane % kChunkLanes / 4, step_of = STEPS == 4 ? quad : 0;
-        const int chunk = (k0 - 8 * lane) / kChunkElems + step_of * kChunksStep + lane / kChunkLanes;
-        const bool has = chunk < chunks && (STEPS == 4 || quad == 0);
-        const uint32_t mine = STEPS == 4 ? (quad == 0 ? word[0] : quad == 1 ? word[1 % STEPS] : quad == 2 ? word[2 % STEPS] : word[3 % STEPS])
-                                         : word[0];
+        // Scale words: a lane of each group writes the group's step (one step: of the first group); with a plan the group's
+        // kSub lanes write for kSub slots at once.
+        constexpr int kSub = kGroupLanes, kChunkLanes = 4 * kGroupLanes, kChunksStep = 32 / kChunkLanes;
+        const int sub = lane % kGroupLanes;
+        const int chunk = (k0 - 8 * lane) / kChunkElems + (STEPS == 4 ? group * kChunksStep : 0) + lane / kChunkLanes;
+        const bool has = chunk < chunks && (STEPS == 4 || group == 0);
         auto put_scales = [&](int64_t tiled) {
-            *reinterpret_cast<uint32_t*>(scales + scale_word(tiled, chunk, chunks)) = mine;
+            *reinterpret_cast<uint32_t*>(scales + scale_word(tiled, chunk, chunks)) = words;
         };
         if (ROWS == Rows::Plain) {
             put_codes(r);

@@ -101,6 +101,34 @@ def test_quantize_bits_many_rows(kind, dtype, rows, K):
         assert np.array_equal(codes[:used], want_codes[token]) and np.array_equal(words[:used], want_words[token])
 
 
+def neighbours(x, dtype):
+    """Exact values x > 0 of a type and their neighbours: [..., 3] as fp32."""
+    bits = np.asarray(x, np.float32).view(np.int32)[..., None]
+    step = 1 if dtype == "fp32" else 1 << 16
+    return (bits + np.array([-step, 0, step], np.int32)).view(np.float32)
+
+
+@pytest.mark.parametrize("dtype", list(FLOATS))
+@pytest.mark.parametrize("copies", [1, 13])
+def test_quantize_at_thresholds(dtype, copies):
+    """Every E4M3 scale with elements at, just below and just above every threshold between two codes, of both signs; and
+    group maxima at, below and above every threshold between two scales."""
+    scales = ref.E4M3[1:127]
+    t = neighbours(scales[:, None] * np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]), dtype).reshape(126, 21)
+    x = np.zeros((126, 32), np.float32)
+    x[:, 0] = x[:, 16] = 6 * scales
+    x[:, 1:16], x[:, 17:23] = t[:, :15], t[:, 15:]
+    x = np.concatenate((x, -x))
+    top = neighbours(6 * (ref.E4M3[:126] + ref.E4M3[1:127]) / 2, dtype).reshape(-1)
+    y = np.zeros((top.size, 32), np.float32)
+    y[:, 5], y[:, 31] = top, -top
+    x = np.tile(np.concatenate((x, y)), (copies, 1))
+    codes, words = read_operand(pnq.fp4_quantize(pnq.NVFP4, on_gpu(x, FLOATS[dtype]), 1.0))
+    want_codes, want_words = ref.quantize(x, pnq.NVFP4, 1.0)
+    assert np.array_equal(words, want_words)
+    assert np.array_equal(codes, want_codes)
+
+
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("slots", [1, 7, 33, 64])
 @pytest.mark.parametrize("tokens", [3, 2500])
