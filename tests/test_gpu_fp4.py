@@ -130,6 +130,30 @@ def test_quantize_at_thresholds(dtype, copies):
 
 
 @pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("dtype", list(FLOATS))
+@pytest.mark.parametrize("rows,K", [(3, 96), (70, 1312), (2600, 1056), (900, 4128)])
+@pytest.mark.parametrize("offset,pad", [(1, 1), (2, 2), (4, 4), (3, 0)])
+def test_quantize_unaligned_rows(kind, dtype, rows, K, offset, pad):
+    """Rows on any of the type's own boundaries, few and many, K that ends inside a warp's elements; non-finite values lie
+    between the rows and are not read into them."""
+    x = values_like(rows, K, seed=K + pad)
+    buf = torch.full((offset + rows * (K + pad) + 64,), float("nan"), dtype=FLOATS[dtype], device="cuda")
+    xd = torch.as_strided(buf, (rows, K), (K + pad, 1), offset)
+    xd.copy_(torch.from_numpy(x))
+    codes, words = read_operand(pnq.fp4_quantize(kind, xd, 0.31))
+    want_codes, want_words = ref.quantize(x, kind, 0.31)
+    assert np.array_equal(words, want_words)
+    assert np.array_equal(codes, want_codes)
+    ids = route(rows, 2, 5, seed=K, how="drop")
+    plan = pnq.expert_sort(torch.from_numpy(ids).cuda(), 5)
+    offsets, _, order, _, scale_row = ref.plan(ids, 5)
+    used = int(offsets[-1])
+    codes, words = read_operand(pnq.fp4_quantize(kind, xd, 0.31, plan=plan), np.maximum(scale_row, 0))
+    token = order[:used] // 2
+    assert np.array_equal(codes[:used], want_codes[token]) and np.array_equal(words[:used], want_words[token])
+
+
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("slots", [1, 7, 33, 64])
 @pytest.mark.parametrize("tokens", [3, 2500])
 def test_quantize_every_slot(kind, slots, tokens):
