@@ -490,13 +490,24 @@ cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const
                      void* out, float* dw, cudaStream_t stream) {
     // A warp per token where the tokens give every SM 16 warps (16384 tokens of 2048 bf16, 8 slots: combine 92 us = 6.5 TB/s,
     // its gradients 182 = 6.3 TB/s; a CTA per token took 13 to 15 percent longer; 7 tokens of 1999 fp32 took 28 us by warps
-    // and 5 by CTAs of 256). The gather of a row that a CTA takes in one step or more keeps the CTA (93 us against 96).
+    // and 5 by CTAs of 256). The gather of rows of 4096 bytes or more keeps the CTA (93 us against 96).
+    // Between them, rounds of the device times the steps of a token in each (a step is about half of what a round costs
+    // besides), with the 2 CTAs of 256 per SM that the gradients have room for and the 3 of the others. By warps and by CTAs,
+    // 2300 tokens of 101 bf16, 4 slots: gather 2.4 and 6.5 us, combine 2.2 and 11.5, gradients 3.7 and 17.8; 400 of 2048,
+    // 8 slots: 5.9 and 3.9, 7.1 and 2.8, 11.9 and 7.4.
     // Few tokens of long rows: CTAs of 1024 threads (those 7 tokens: combine 4.4 -> 2.9 us), 512 for the gradients, which
     // need twice the registers.
     // Rows that are not on 16 bytes (D = 3924 bf16, 3194 tokens, 4 slots): gather 25.6 us, combine 40; 34 and 77 where D
-    // is odd and an access two bytes; with one access of one element a thread the two took some three times as long.
+    // is odd and an access two bytes; with one access of one element a thread the two took some three times as long. Accesses
+    // of 16 bytes shifted into place by shuffles and funnel shifts are no better: 73 and 76 us at any D.
     const int64_t vecs = D / V, sms = device_sm_count();
-    if (p.tokens >= sms * 16 && (op != ExpertOp::Gather || vecs < kRowThreads))
+    const int64_t round = sms * (op == ExpertOp::CombineBackward ? 2 : 3);  // CTAs that run at a time
+    auto rounds = [&](int64_t per_cta, int64_t threads) {
+        const int64_t step = threads * Vec<T, V>::kSteps;
+        return (p.tokens + round * per_cta - 1) / (round * per_cta) * (2 + (vecs + step - 1) / step);
+    };
+    const bool warps = p.tokens >= sms * 16 || (p.tokens > sms * 2 && rounds(kRowThreads / 32, 32) <= rounds(1, kRowThreads));
+    if (warps && (op != ExpertOp::Gather || vecs * Vec<T, V>::kBytes < 4096))
         return run_rows<T, V, 32>(op, a, b, D, p, weights, out, dw, stream);
     if (p.tokens <= 2 * sms && vecs > 2 * kRowThreads)
         return op == ExpertOp::CombineBackward ? run_rows<T, V, 512>(op, a, b, D, p, weights, out, dw, stream)
