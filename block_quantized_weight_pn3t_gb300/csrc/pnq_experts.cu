@@ -263,10 +263,7 @@ constexpr int kSlotBatch = 8;  // slots whose rows are in flight together
 
 template <int TEAM>
 struct Team {
-    static constexpr int kThreads = TEAM > kRowThreads ? TEAM : kRowThreads;  // of a CTA
-    static constexpr int kPerCta = kThreads / TEAM;
-    // accesses a thread has in flight: one in the largest teams, which take few tokens' rows in a step or two
-    static constexpr __host__ __device__ int steps(int most) { return TEAM > kRowThreads ? 1 : most; }
+    static constexpr int kPerCta = kRowThreads / TEAM;
     static __device__ __forceinline__ int thread() { return static_cast<int>(threadIdx.x) % TEAM; }
     static __device__ __forceinline__ int64_t first() {
         return static_cast<int64_t>(blockIdx.x) * kPerCta + static_cast<int>(threadIdx.x) / TEAM;
@@ -294,10 +291,10 @@ __device__ __forceinline__ void load_slots(const PlanView& p, const float* weigh
 
 // XS[position of each slot of t] = X[t].
 template <class T, int V, int TEAM>
-__global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_gather_kernel(const typename Vec<T, V>::Raw* __restrict__ X,
+__global__ void __launch_bounds__(kRowThreads) expert_gather_kernel(const typename Vec<T, V>::Raw* __restrict__ X,
                                                                     int64_t vecs, PlanView p,
                                                                     typename Vec<T, V>::Raw* __restrict__ XS) {
-    constexpr int U = Team<TEAM>::steps(Vec<T, V>::kSteps);
+    constexpr int U = Vec<T, V>::kSteps;
     griddep_begin();
     for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
         for (int j0 = 0; j0 < p.slots; j0 += kSlotBatch) {
@@ -324,12 +321,12 @@ __global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_gather_kernel(con
 
 // Y[t] = sum over slots of (weights, or 1 where they are null) * YS[position].
 template <class T, int V, int TEAM>
-__global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_combine_kernel(const typename Vec<T, V>::Raw* __restrict__ YS,
+__global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(const typename Vec<T, V>::Raw* __restrict__ YS,
                                                                      int64_t vecs, PlanView p,
                                                                      const float* __restrict__ weights,
                                                                      typename Vec<T, V>::Raw* __restrict__ Y) {
     using Raw = typename Vec<T, V>::Raw;
-    constexpr int U = Team<TEAM>::steps(Vec<T, V>::kSteps);
+    constexpr int U = Vec<T, V>::kSteps;
     const int k = p.slots;
     griddep_begin();
     for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
@@ -374,13 +371,13 @@ __global__ void __launch_bounds__(Team<TEAM>::kThreads) expert_combine_kernel(co
 
 // dYS[position] = weights * dY[t], dWeights[t][j] = <dY[t], YS[position]>.
 template <class T, int V, int TEAM>
-__global__ void __launch_bounds__(Team<TEAM>::kThreads, TEAM > kRowThreads ? 1 : 2) expert_combine_backward_kernel(
+__global__ void __launch_bounds__(kRowThreads, 2) expert_combine_backward_kernel(
     const typename Vec<T, V>::Raw* __restrict__ dY, const typename Vec<T, V>::Raw* __restrict__ YS, int64_t vecs,
     PlanView p, const float* __restrict__ weights, typename Vec<T, V>::Raw* __restrict__ dYS,
     float* __restrict__ dWeights) {
     using Raw = typename Vec<T, V>::Raw;
-    constexpr int U = Team<TEAM>::steps(Vec<T, V>::kSteps);
-    __shared__ float part[Team<TEAM>::kThreads / 32][kSlotBatch];
+    constexpr int U = Vec<T, V>::kSteps;
+    __shared__ float part[kRowThreads / 32][kSlotBatch];
     const int k = p.slots, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_begin();
     for (int64_t t = Team<TEAM>::first(); t < p.tokens; t += Team<TEAM>::step()) {
@@ -468,35 +465,31 @@ template <class T, int V, int TEAM>
 cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const PlanView& p, const float* weights,
                      void* out, float* dw, cudaStream_t stream) {
     const int64_t vecs = D / V, per = Team<TEAM>::kPerCta;
-    constexpr int kBlock = Team<TEAM>::kThreads;
     // enough CTAs to fill the device several times over; each then walks tokens with that stride
     const int grid = static_cast<int>(
         std::max<int64_t>(1, std::min<int64_t>((p.tokens + per - 1) / per, int64_t(device_sm_count()) * 32)));
-    if constexpr (TEAM != 512) {
-        if (op == ExpertOp::Gather)
-            return launch_dependent(expert_gather_kernel<T, V, TEAM>, grid, kBlock, stream, raw<T, V>(a), vecs, p, raw<T, V>(out));
-        if (op != ExpertOp::CombineBackward)
-            return launch_dependent(expert_combine_kernel<T, V, TEAM>, grid, kBlock, stream, raw<T, V>(a), vecs, p, weights,
-                                    raw<T, V>(out));
-    }
-    if constexpr (TEAM != 1024)
-        return launch_dependent(expert_combine_backward_kernel<T, V, TEAM>, grid, kBlock, stream, raw<T, V>(a), raw<T, V>(b), vecs, p,
-                                weights, raw<T, V>(out), dw);
-    return cudaErrorInvalidValue;  // no such pair is asked for
+    if (op == ExpertOp::CombineBackward)
+        return launch_dependent(expert_combine_backward_kernel<T, V, TEAM>, grid, kRowThreads, stream, raw<T, V>(a), raw<T, V>(b), vecs,
+                                p, weights, raw<T, V>(out), dw);
+    if (op == ExpertOp::Gather)
+        return launch_dependent(expert_gather_kernel<T, V, TEAM>, grid, kRowThreads, stream, raw<T, V>(a), vecs, p, raw<T, V>(out));
+    return launch_dependent(expert_combine_kernel<T, V, TEAM>, grid, kRowThreads, stream, raw<T, V>(a), vecs, p, weights,
+                            raw<T, V>(out));
 }
 
 template <class T, int V>
 cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const PlanView& p, const float* weights,
                      void* out, float* dw, cudaStream_t stream) {
     // A warp per token where the tokens give every SM 16 warps (16384 tokens of 2048 bf16, 8 slots: combine 92 us = 6.5 TB/s,
-    // its gradients 182 = 6.3 TB/s; a CTA per token took 13 to 15 percent longer; 7 tokens of 1999 fp32 took 28 us by warps
-    // and 5 by CTAs of 256). The gather of rows of 4096 bytes or more keeps the CTA (93 us against 96).
+    // its gradients 182 = 6.3 TB/s; a CTA per token took 13 to 15 percent longer), a CTA where they are few (5 tokens of 2048
+    // fp32, 4 slots: combine 8.1 us by warps and 2.0 by CTAs). The gather of rows of 4096 bytes or more keeps the CTA (93 us
+    // against 96).
     // Between them, rounds of the device times the steps of a token in each (a step is about half of what a round costs
     // besides), with the 2 CTAs of 256 per SM that the gradients have room for and the 3 of the others. By warps and by CTAs,
     // 2300 tokens of 101 bf16, 4 slots: gather 2.4 and 6.5 us, combine 2.2 and 11.5, gradients 3.7 and 17.8; 400 of 2048,
     // 8 slots: 5.9 and 3.9, 7.1 and 2.8, 11.9 and 7.4.
-    // Few tokens of long rows: CTAs of 1024 threads (those 7 tokens: combine 4.4 -> 2.9 us), 512 for the gradients, which
-    // need twice the registers.
+    // Larger CTAs for few tokens give nothing now that a thread has several narrow accesses in flight (7 tokens of 1999 fp32 by
+    // 256 threads: combine 2.8 us, gradients 3.9; by 1024 and 512: 2.9 and 3.8; 300 of 5120 bf16: 5.5 and 11, 9 and 14).
     // Rows that are not on 16 bytes (D = 3924 bf16, 3194 tokens, 4 slots): gather 25.6 us, combine 40; 34 and 77 where D
     // is odd and an access two bytes; with one access of one element a thread the two took some three times as long. Accesses
     // of 16 bytes shifted into place by shuffles and funnel shifts are no better: 73 and 76 us at any D.
@@ -509,9 +502,6 @@ cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const
     const bool warps = p.tokens >= sms * 16 || (p.tokens > sms * 2 && rounds(kRowThreads / 32, 32) <= rounds(1, kRowThreads));
     if (warps && (op != ExpertOp::Gather || vecs * Vec<T, V>::kBytes < 4096))
         return run_rows<T, V, 32>(op, a, b, D, p, weights, out, dw, stream);
-    if (p.tokens <= 2 * sms && vecs > 2 * kRowThreads)
-        return op == ExpertOp::CombineBackward ? run_rows<T, V, 512>(op, a, b, D, p, weights, out, dw, stream)
-                                               : run_rows<T, V, 1024>(op, a, b, D, p, weights, out, dw, stream);
     return run_rows<T, V, kRowThreads>(op, a, b, D, p, weights, out, dw, stream);
 }
 
