@@ -8,8 +8,9 @@
 //   encode: 8 elements per lane (one 16-byte load of bf16); the lanes of a group take its maximum by shuffles; with four
 //           steps the lanes of a four exchange their codes and write 16 bytes each; the scale words of four groups are
 //           neighbours in the tiled layout and leave as one word.
-//   decode: a lane loads the words of 8 codes and the warp exchanges them so that lane l writes elements 4 l ..
-//           4 l + 3 of 128: every store covers 512 contiguous bytes of fp32.
+//   decode: a lane loads the word of 8 codes, which is a store of 16 bytes of bf16. For fp32 the warp exchanges the words so
+//           that lane l writes elements 4 l .. 4 l + 3 of 128: every store covers 512 contiguous bytes (8191 x 5152: 34 us;
+//           lanes that write 32 bytes each 36), and for a bf16 output that is not on 16 bytes too.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -335,20 +336,22 @@ __global__ void __launch_bounds__(kQThreads, 8) fp4_quantize_kernel(const T* __r
     }
 }
 
-// Four elements -> out at o.
-template <class T, bool VEC>
-__device__ __forceinline__ void store4(T* o, float a, float b, float c, float d) {
-    if constexpr (sizeof(T) == 4) {
-        if constexpr (VEC) *reinterpret_cast<float4*>(o) = make_float4(a, b, c, d);
-        else o[0] = a, o[1] = b, o[2] = c, o[3] = d;
+// E consecutive elements -> out at o: by one store of 16 bytes, or of an element each.
+template <class T, bool VEC, int E>
+__device__ __forceinline__ void store(T* o, const float (&v)[E]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4 && i < E; ++i) {
+        if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
+        else if (2 * i < E) w[i] = f32x2_to_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+    if constexpr (VEC) {
+        *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
-        const uint32_t lo = f32x2_to_bf16x2(a, b), hi = f32x2_to_bf16x2(c, d);
-        if constexpr (VEC) {
-            *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
-        } else {
-            uint16_t* h = reinterpret_cast<uint16_t*>(o);
-            h[0] = static_cast<uint16_t>(lo), h[1] = static_cast<uint16_t>(lo >> 16);
-            h[2] = static_cast<uint16_t>(hi), h[3] = static_cast<uint16_t>(hi >> 16);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if constexpr (sizeof(T) == 4) o[i] = v[i];
+            else reinterpret_cast<uint16_t*>(o)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i % 2)));
         }
     }
 }
@@ -361,6 +364,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const uint8_t
                                                                    const int32_t* __restrict__ scale_row,
                                                                    T* __restrict__ out) {
     constexpr int kChunkElems = MX ? 128 : 64, kChunksStep = 256 / kChunkElems;
+    constexpr int E = VEC && sizeof(T) == 2 ? 8 : 4;  // elements a lane writes at a time
     const int lane = threadIdx.x & 31;
     const int per_row = (K + STEPS * 256 - 1) / (STEPS * 256);
     const int64_t items = rows * matrices * per_row;
@@ -384,22 +388,24 @@ __global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const uint8_t
         for (int u = 0; u < STEPS; ++u) {
             if (k0 + 256 * u >= K) break;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // lane l: elements 4 l .. 4 l + 3 of this half of the step
-                const uint32_t four = __shfl_sync(0xffffffffu, c[u], 16 * h + (lane >> 1)) >> (16 * (lane & 1));
-                const int group = (128 * h + 4 * lane) / (kChunkElems / 4);  // within the step
+            for (int h = 0; h < 8 / E; ++h) {  // lane l: elements E l .. E l + E - 1 of this part of the step
+                const int at = 32 * E * h + E * lane;
+                const uint32_t mine = E == 8 ? c[u] : __shfl_sync(0xffffffffu, c[u], 16 * h + (lane >> 1)) >> (16 * (lane & 1));
+                const int group = at / (kChunkElems / 4);  // within the step
                 const uint32_t word = __shfl_sync(0xffffffffu, w, u * kChunksStep + (group >> 2)) >> (8 * (group & 3)) & 255u;
                 float s = MX ? (word == 255u ? __uint_as_float(0x7FC00000u)
                                 : word == 0u ? __uint_as_float(0x00400000u)  // 2^-127
                                              : __uint_as_float(word << 23))
                              : e4m3_bits_to_f32(word);
                 if (sr < 0) s = 0.0f;
-                const float2 a = __half22float2(u32_as_half2(e2m1x2_to_f16x2<0>(four)));
-                const float2 b = __half22float2(u32_as_half2(e2m1x2_to_f16x2<1>(four)));
-                const int k = k0 + 256 * u + 128 * h + 4 * lane;
-                if (k < K)
-                    store4<T, VEC>(out + r * static_cast<int64_t>(K) + k, __fmul_rn(__fmul_rn(a.x, s), g),
-                                   __fmul_rn(__fmul_rn(a.y, s), g), __fmul_rn(__fmul_rn(b.x, s), g),
-                                   __fmul_rn(__fmul_rn(b.y, s), g));
+                float v[E];
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    const float2 e = __half22float2(u32_as_half2(e2m1x2_to_f16x2<0>(mine >> (8 * i))));
+                    f32x2_unpack(f32x2_mul(f32x2_mul(f32x2_pack(e.x, e.y), f32x2_pack(s, s)), f32x2_pack(g, g)), v[2 * i], v[2 * i + 1]);
+                }
+                const int k = k0 + 256 * u + at;
+                if (k < K) store<T, VEC, E>(out + r * static_cast<int64_t>(K) + k, v);
             }
         }
     }

@@ -154,6 +154,23 @@ def test_quantize_unaligned_rows(kind, dtype, rows, K, offset, pad):
 
 
 @pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("dtype", list(FLOATS))
+@pytest.mark.parametrize("rows,K", [(3, 96), (70, 1312), (2600, 1056)])
+@pytest.mark.parametrize("offset", [0, 1, 2, 4, 8])
+def test_dequantize_into_any_alignment(kind, dtype, rows, K, offset):
+    """Outputs on every boundary of their type, few rows and many, groups of NaN among them; nothing is written beside them."""
+    x = values_like(rows, K, seed=rows)
+    x[rows // 2, 40] = np.inf
+    codes, words = ref.quantize(x, kind, 0.31)
+    want = torch.from_numpy((ref.values(codes, words, kind).astype(np.float32) * np.float32(0.31)).astype(np.float32)).to(FLOATS[dtype])
+    buf = torch.full((offset + rows * K + 16,), 77.0, dtype=FLOATS[dtype], device="cuda")
+    out = buf[offset:offset + rows * K].view(rows, K)
+    pnq.fp4_dequantize(pnq.fp4_quantize(kind, on_gpu(x, torch.float32), 0.31), out=out)
+    assert torch.equal(out.cpu().nan_to_num(nan=99.0), want.nan_to_num(nan=99.0)) and out.isnan().sum() == ref.GROUP[kind]
+    assert bool((buf[:offset] == 77).all()) and bool((buf[offset + rows * K:] == 77).all())
+
+
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("slots", [1, 7, 33, 64])
 @pytest.mark.parametrize("tokens", [3, 2500])
 def test_quantize_every_slot(kind, slots, tokens):
