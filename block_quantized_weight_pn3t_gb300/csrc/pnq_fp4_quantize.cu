@@ -9,8 +9,8 @@
 //           steps the lanes of a four exchange their codes and write 16 bytes each; the scale words of four groups are
 //           neighbours in the tiled layout and leave as one word.
 //   decode: a lane loads the word of 8 codes, which is a store of 16 bytes of bf16. For fp32 the warp exchanges the words so
-//           that lane l writes elements 4 l .. 4 l + 3 of 128: every store covers 512 contiguous bytes (8191 x 5152: 34 us;
-//           lanes that write 32 bytes each 36), and for a bf16 output that is not on 16 bytes too.
+//           that lane l writes elements 4 l .. 4 l + 3 of 128: every store covers 512 contiguous bytes (8191 x 5152: 34.3 us;
+//           lanes that wrote 32 bytes each took 36.7), and for a bf16 output that is not on 16 bytes too.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -210,10 +210,11 @@ __device__ __forceinline__ void encode8(const Eight<T>& x, float inv_g, uint32_t
 // Where the encoded rows go: row r to row r; a plan's token to the sorted rows of its slots; a plan's sorted row to its place.
 enum class Rows { Plain, Tokens, Sorted };
 
-// STEPS steps of 256 elements per warp and item. 64 registers: 8191 x 5152 fp32 33.2 -> 30.7 us; CTAs of 128
-// threads rather than 256: 4096 tokens x 8 slots of 2048 13.8 -> 13.2 us (1.7 rounds of CTAs, the second not full).
+// STEPS steps of 256 elements per warp and item. 64 registers: 8191 x 5152 fp32 33.2 -> 30.7 us; 48 for bf16, which holds half
+// as many words: 27.0 -> 25.4 (MXFP4 23.1 -> 21.5). CTAs of 128 threads rather than 256: 4096 tokens x 8 slots of 2048
+// 13.8 -> 13.2 us (1.7 rounds of CTAs, the second not full).
 template <bool MX, class T, bool VEC, Rows ROWS, int STEPS>
-__global__ void __launch_bounds__(kQThreads, 8) fp4_quantize_kernel(const T* __restrict__ X, int64_t ldx, int64_t rows,
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 10 : 8) fp4_quantize_kernel(const T* __restrict__ X, int64_t ldx, int64_t rows,
                                                                  int64_t matrices, int K, float inv_g, PlanView p,
                                                                  uint8_t* __restrict__ codes, int64_t pitch,
                                                                  uint8_t* __restrict__ scales, int chunks) {
@@ -454,9 +455,12 @@ __global__ void __launch_bounds__(kQThreads) fp4_pitch_codes_kernel(const uint8_
     }
 }
 
+// CTAs of a grid, each of which walks its items with that stride. Several rounds of them: a CTA that comes in loads while its
+// neighbours compute (8191 x 5152 with 64 per SM rather than 16: decode 34.1 -> 29.8 us, 19.8 -> 18.2 to bf16, encode of fp32 30.6
+// -> 29.6; with 256 the unaligned outputs take a fifth longer).
 int item_grid(int64_t items, int per_cta) {
     return static_cast<int>(
-        std::max<int64_t>(1, std::min<int64_t>((items + per_cta - 1) / per_cta, int64_t(device_sm_count()) * 16)));
+        std::max<int64_t>(1, std::min<int64_t>((items + per_cta - 1) / per_cta, int64_t(device_sm_count()) * 64)));
 }
 
 // Whether the rows fill the device's warps with items of 1024 elements; otherwise items of 256.
