@@ -411,15 +411,20 @@ PyObject* matrix_vectorcall(PyObject*, PyObject* const* args, size_t nargsf, PyO
     return entry([&]() -> PyObject* {
         static const char* const names[] = {"type_", "rows", "K", "codes", "scales", "global_scale", "matrices", "plan"};
         const Args<8> a("Fp4Matrix", names, 5, args, PyVectorcall_NARGS(nargsf), kwnames);
-        if (a[7]) to_plan(a[7]);
+        const PlanObject* plan = a[7] ? to_plan(a[7]) : nullptr;
         const at::Tensor &codes = tensor(a[3], "codes"), &scales = tensor(a[4], "scales");
         Owned o{reinterpret_cast<PyObject*>(
             alloc_matrix(to_type(a[0]), to_int(a[1]), to_int(a[2]), a[6] ? to_int(a[6]) : 1, a[7]))};
         MatrixObject* m = reinterpret_cast<MatrixObject*>(o.o);
+        // the product by experts reads as many rows as the plan has
+        if (plan && m->rows != plan->rows)
+            refuse("an operand of " + std::to_string(m->rows) + " rows; the plan has " + std::to_string(plan->rows) + " sorted rows");
         require(codes, "codes", at::kByte, m->matrices * m->rows * m->pitch);
         require(scales, "scales", at::kByte, m->scale_bytes);
         m->device = codes.get_device();
         require_device(scales, "scales", m->device);
+        if (plan && plan->device != m->device)
+            refuse("codes are on cuda:" + std::to_string(m->device) + ", the plan on cuda:" + std::to_string(plan->device));
         m->codes = codes;
         m->scales = scales;
         m->codes_at = codes.data_ptr<uint8_t>();
