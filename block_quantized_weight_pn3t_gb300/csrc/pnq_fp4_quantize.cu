@@ -221,14 +221,18 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 10 : 8) fp4_quanti
     constexpr int kGroupLanes = MX ? 4 : 2, kChunkElems = MX ? 128 : 64;
     const int lane = threadIdx.x & 31;
     const int per_row = (K + STEPS * 256 - 1) / (STEPS * 256);
-    const int64_t items = rows * matrices * per_row;
+    int64_t items = rows * matrices * per_row;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kQThreads / 32);
     using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
     __shared__ alignas(16) Bits turned[VEC ? 1 : kQThreads / 32][256];  // unaligned rows: a step of each warp's
     griddep_begin();
+    // sorted rows: those past the rows in use are not read (the caller's buffer may end before them)
+    if constexpr (ROWS == Rows::Sorted) items = min(items, static_cast<int64_t>(ld_l2(p.offsets + p.experts)) * per_row);
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
         const int64_t r = items <= INT32_MAX ? static_cast<int32_t>(it) / per_row : it / per_row;
         const int k0 = static_cast<int>(it - r * per_row) * (STEPS * 256) + 8 * lane;
+        int tiled = -1;
+        if constexpr (ROWS == Rows::Sorted) tiled = ld_l2(p.scale_row + r);
         Eight<T> x[STEPS];
 #pragma unroll
         for (int u = 0; u < STEPS; ++u) {
@@ -311,8 +315,7 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 10 : 8) fp4_quanti
             put_codes(r);
             if (has && sub == 0) put_scales(tiled_row(r, rows, matrices));
         } else if (ROWS == Rows::Sorted) {
-            const int tiled = ld_l2(p.scale_row + r);
-            if (tiled >= 0) {  // not past the rows in use
+            if (tiled >= 0) {
                 put_codes(r);
                 if (has && sub == 0) put_scales(tiled);
             }
