@@ -674,9 +674,10 @@ PNQ_ENTRY(fp4_gemm_experts) {
         const MatrixObject *x = to_matrix(a[0], "x"), *w = to_matrix(a[1], "w");
         PlanObject* plan = to_plan(a[2]);
         check_operands(x, w);
+        // the same plan, or another view of its memory: a plan of the same sizes sorts other rows (another layer's, say)
         const PlanObject* made = reinterpret_cast<PlanObject*>(x->plan);
         if (!made || (made != plan && (made->desc.tokens != plan->desc.tokens || made->desc.slots != plan->desc.slots ||
-                                       made->desc.experts != plan->desc.experts)))
+                                       made->desc.experts != plan->desc.experts || made->desc.offsets != plan->desc.offsets)))
             refuse("x is not an operand of this plan's sorted rows");
         if (w->matrices != plan->desc.experts || w->plan)
             refuse("w has " + std::to_string(w->matrices) + " matrices; one for each of the plan's experts is wanted");

@@ -28,3 +28,22 @@ def test_an_operand_has_its_plans_rows(kind, rows):
         pnq.Fp4Matrix(kind, rows, 64, *raw(kind, rows, 64, 3), plan=plan)
     m = pnq.Fp4Matrix(kind, 1000, 64, *raw(kind, 1000, 64, 3), plan=plan)
     assert m.rows == plan.rows and m.plan is plan
+
+
+def test_products_refuse_another_plan():
+    """Two layers of one model have plans of the same sizes: an operand sorted by one is not multiplied by the other. The
+    same memory as another ExpertPlan is the same plan."""
+    K, E = 64, 3
+    first, second = plan_of(8, 2, E), plan_of(8, 2, E, shift=1)
+    x = torch.randn(8, K, device="cuda")
+    w = pnq.fp4_quantize(pnq.NVFP4, torch.randn(E, 40, K, device="cuda"))
+    q = pnq.fp4_quantize(pnq.NVFP4, x, plan=first)
+    for other in (second, plan_of(8, 2, E + 1), plan_of(16, 1, E), plan_of(4, 2, E)):
+        with pytest.raises(pnq.PnqError, match="not an operand of this plan"):
+            pnq.fp4_gemm_experts(q, w, other)
+    want = pnq.fp4_gemm_experts(q, w, first)
+    assert torch.equal(pnq.fp4_gemm_experts(q, w, pnq.ExpertPlan(8, 2, E, first.buffer)), want)
+    pnq.fp4_quantize(pnq.NVFP4, x, plan=second, out=q)  # the operand is the second plan's from here on
+    with pytest.raises(pnq.PnqError, match="not an operand of this plan"):
+        pnq.fp4_gemm_experts(q, w, first)
+    pnq.fp4_gemm_experts(q, w, second)
