@@ -552,23 +552,24 @@ PNQ_ENTRY(fp4_quantize) {
             if (m->type != type || m->rows != out_rows || m->K != K || m->matrices != matrices || m->device != device ||
                 have != (plan ? plan->desc.experts : 0))
                 refuse("out is an operand of another type, shape or device");
-            if (plan && m->plan != reinterpret_cast<PyObject*>(plan)) {
-                Py_INCREF(plan);
-                Py_SETREF(m->plan, reinterpret_cast<PyObject*>(plan));
-            }
             o.o = Py_NewRef(a[4]);
         } else {
             o.o = reinterpret_cast<PyObject*>(alloc_matrix(type, out_rows, K, matrices, a[3]));
             allocate(reinterpret_cast<MatrixObject*>(o.o), device);
         }
         MatrixObject* m = reinterpret_cast<MatrixObject*>(o.o);
-        m->scale = g;
-        m->per_matrix = at::Tensor();
         place.record(x, m->scales, m->codes);
         if (plan) place.record(plan->buffer);
         check(pnq_fp4_quantize(type, xt, x.data_ptr(), ldx, rows, K, matrices, static_cast<float>(g), plan ? &plan->desc : nullptr,
                                sorted ? PNQ_FP4_SORTED : 0u, m->codes_at, m->scales_at, place.stream()),
               "pnq_fp4_quantize");
+        // only now: a refused call leaves `out` as it was
+        m->scale = g;
+        m->per_matrix = at::Tensor();
+        if (plan && m->plan != a[3]) {
+            Py_INCREF(a[3]);
+            Py_XSETREF(m->plan, a[3]);
+        }
         return o.release();
     });
 }

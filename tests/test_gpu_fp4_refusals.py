@@ -47,3 +47,23 @@ def test_products_refuse_another_plan():
     with pytest.raises(pnq.PnqError, match="not an operand of this plan"):
         pnq.fp4_gemm_experts(q, w, first)
     pnq.fp4_gemm_experts(q, w, second)
+
+
+@pytest.mark.parametrize("g", [0.0, -1.0, float("nan"), float("inf"), 1e-45])
+def test_a_refused_encode_leaves_out_as_it_was(g):
+    """Codes, multiplier (one, or one per matrix) and plan of `out` stay those of the operand it was."""
+    x = torch.randn(8, 64, device="cuda")
+    first, second = plan_of(8, 2, 3), plan_of(8, 2, 3, shift=1)
+    q = pnq.fp4_quantize(pnq.NVFP4, x, 0.25, plan=first)
+    before = q.codes.clone()
+    with pytest.raises(pnq.PnqError) as e:
+        pnq.fp4_quantize(pnq.NVFP4, 2 * x, g, plan=second, out=q)
+    assert e.value.status == pnq.Status.ERR_VALUE
+    assert q.global_scale == 0.25 and q.plan is first and torch.equal(q.codes, before)
+    m = pnq.fp4_quantize(pnq.NVFP4, x.view(2, 4, 64))
+    m.global_scale = torch.tensor([0.5, 2.0], device="cuda")
+    with pytest.raises(pnq.PnqError):
+        pnq.fp4_quantize(pnq.NVFP4, x.view(2, 4, 64), g, out=m)
+    assert torch.equal(m.global_scale, torch.tensor([0.5, 2.0], device="cuda"))
+    pnq.fp4_quantize(pnq.NVFP4, x, 0.5, plan=second, out=q)
+    assert q.global_scale == 0.5 and q.plan is second
