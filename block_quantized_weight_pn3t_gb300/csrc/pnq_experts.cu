@@ -249,7 +249,7 @@ struct Vec {
 // Zero rows [used, n) of out, shared by all CTAs.
 template <class Raw>
 __device__ __forceinline__ void zero_tail(Raw* out, const PlanView& p, int64_t n, int64_t vecs) {
-    const int64_t used = ld_l2(p.offsets + p.experts);
+    const int64_t used = max(0, ld_l2(p.offsets + p.experts));
     const int64_t count = (n - used) * vecs;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < count;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x)
@@ -279,7 +279,7 @@ __device__ __forceinline__ void load_slots(const PlanView& p, const float* weigh
     int mine = -1;
     float weight = 1.0f;
     if (j < min(k, j0 + kSlotBatch)) {
-        mine = ld_l2(p.position + t * k + j);
+        mine = plan_index(ld_l2(p.position + t * k + j), p.rows);
         if (weights) weight = ld_l2(weights + t * k + j);
     }
 #pragma unroll
@@ -320,8 +320,9 @@ __global__ void __launch_bounds__(kRowThreads) expert_gather_kernel(const typena
 }
 
 // Y[t] = sum over slots of (weights, or 1 where they are null) * YS[position].
+// bf16 by 16 bytes: 3 CTAs an SM, which its 80 registers give and 85 would not.
 template <class T, int V, int TEAM>
-__global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(const typename Vec<T, V>::Raw* __restrict__ YS,
+__global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 && V == 8 ? 3 : 0) expert_combine_kernel(const typename Vec<T, V>::Raw* __restrict__ YS,
                                                                      int64_t vecs, PlanView p,
                                                                      const float* __restrict__ weights,
                                                                      typename Vec<T, V>::Raw* __restrict__ Y) {

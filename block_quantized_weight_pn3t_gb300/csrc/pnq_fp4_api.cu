@@ -48,6 +48,8 @@ int check_plan(const pnq_expert_plan* d, PlanView* p) {
     p->tokens = d->tokens;
     p->slots = d->slots;
     p->experts = d->experts;
+    p->rows = static_cast<int>(d->tokens * d->slots);
+    p->tiled = static_cast<int>(128 * plan_blocks(p->rows, d->experts));
     return PNQ_OK;
 }
 

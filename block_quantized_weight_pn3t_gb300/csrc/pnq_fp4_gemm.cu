@@ -254,12 +254,18 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         const int E = a.p.experts, nt = (a.N + CG * kRows - 1) / (CG * kRows), per = (E + kThreads - 1) / kThreads;
         const int e0 = min(E, static_cast<int>(threadIdx.x) * per), e1 = min(E, e0 + per);
         int sum = 0, first = ld_l2(a.p.offsets + e0);
+        bool wrong = first < 0 || first > a.M;  // not the offsets of a sorted plan of these sizes
         for (int e = e0; e < e1; ++e) {
             const int next = ld_l2(a.p.offsets + e + 1);
+            wrong |= next < first || next > a.M;
             firsts[e] = first;
-            starts[e] = (next - first + BN - 1) / BN * nt;
+            starts[e] = wrong ? 0 : (next - first + BN - 1) / BN * nt;
             sum += starts[e];
             first = next;
+        }
+        if (__syncthreads_or(wrong)) {  // no tile and no row in use
+            sum = first = 0;
+            for (int e = e0; e < e1; ++e) starts[e] = 0;
         }
         if (e1 == E) firsts[E] = first;
         int incl = sum;
@@ -313,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                 wrow = tile.e * a.N + n0;
                 wsc = (tile.e * blocks_w + n0 / 128) * a.chunks;
                 xrow = tile.row0 + static_cast<int>(rank) * (BN / CG);
-                xsc = ((a.p.experts ? ld_l2(a.p.block_start + tile.e) : 0) + tile.sblock) * a.chunks;
+                xsc = ((a.p.experts ? max(0, plan_index(ld_l2(a.p.block_start + tile.e), a.p.tiled)) : 0) + tile.sblock) * a.chunks;
                 // rows past the tile's activations are not copied: their columns are not stored (and a copy's rows past
                 // the end of the matrix, filled with zeros, take longer than rows that are there)
                 xcopies = CG == 2 ? 1 : (tile.rows + a.xbox - 1) / a.xbox;  // a pair's CTAs copy one half each
@@ -480,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         }
         if (!ok && lane == 0) record_error(a.err, kErrFullWait);
         if (a.p.experts > 0) {  // rows past the rows in use
-            const int64_t used = ld_l2(a.p.offsets + a.p.experts), count = (static_cast<int64_t>(a.M) - used) * a.N;
+            const int64_t used = firsts[a.p.experts], count = (static_cast<int64_t>(a.M) - used) * a.N;
             const int64_t cta = blockIdx.y * static_cast<int64_t>(gridDim.x) + blockIdx.x;
             const int64_t step = static_cast<int64_t>(gridDim.x) * gridDim.y * kEpilogueThreads;
             for (int64_t j = cta * kEpilogueThreads + static_cast<int>(threadIdx.x) - 64; j < count; j += step)

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 10 : 8) fp4_quanti
         const int64_t r = items <= INT32_MAX ? static_cast<int32_t>(it) / per_row : it / per_row;
         const int k0 = static_cast<int>(it - r * per_row) * (STEPS * 256) + 8 * lane;
         int tiled = -1;
-        if constexpr (ROWS == Rows::Sorted) tiled = ld_l2(p.scale_row + r);
+        if constexpr (ROWS == Rows::Sorted) tiled = plan_index(ld_l2(p.scale_row + r), p.tiled);
         Eight<T> x[STEPS];
 #pragma unroll
         for (int u = 0; u < STEPS; ++u) {
@@ -255,8 +255,9 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 10 : 8) fp4_quanti
         // with a plan: where the row goes, lane j holding slot j's places
         int at = -1, srow = 0;
         if (ROWS == Rows::Tokens && lane < p.slots) {
-            at = ld_l2(p.position + r * p.slots + lane);
+            at = plan_index(ld_l2(p.position + r * p.slots + lane), p.rows);
             if (at >= 0) srow = ld_l2(p.scale_row + at);
+            if (plan_index(srow, p.tiled) < 0) at = -1;
         }
         uint32_t c[STEPS], words = 0;  // words: a byte of each step, the same in a group's lanes; groups past K: zero
 #pragma unroll
@@ -323,8 +324,9 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 10 : 8) fp4_quanti
             for (int j0 = 0; j0 < p.slots; j0 += 32) {
                 if (j0) {
                     at = -1;
-                    if (j0 + lane < p.slots) at = ld_l2(p.position + r * p.slots + j0 + lane);
+                    if (j0 + lane < p.slots) at = plan_index(ld_l2(p.position + r * p.slots + j0 + lane), p.rows);
                     if (at >= 0) srow = ld_l2(p.scale_row + at);
+                    if (plan_index(srow, p.tiled) < 0) at = -1;
                 }
                 const int most = min(32, p.slots - j0);
                 for (int j = 0; j < most; ++j) {
@@ -360,12 +362,13 @@ __device__ __forceinline__ void store(T* o, const float (&v)[E]) {
     }
 }
 
-// out = fp32(e2m1 * s * g), the first product exact.
-template <bool MX, class T, bool VEC, int STEPS>
+// out = fp32(e2m1 * s * g), the first product exact. A kernel of its own for a plan's rows: the check of scale_row in one for
+// both cost 1000 x 5120 of no plan a tenth (3.8 -> 4.2 us to bf16).
+template <bool MX, class T, bool VEC, int STEPS, bool PLAN>
 __global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const uint8_t* __restrict__ codes, int64_t pitch,
                                                                    const uint8_t* __restrict__ scales, int chunks,
                                                                    int64_t rows, int64_t matrices, int K, float g,
-                                                                   const int32_t* __restrict__ scale_row,
+                                                                   const int32_t* __restrict__ scale_row, int tiled,
                                                                    T* __restrict__ out) {
     constexpr int kChunkElems = MX ? 128 : 64, kChunksStep = 256 / kChunkElems;
     constexpr int E = VEC && sizeof(T) == 2 ? 8 : 4;  // elements a lane writes at a time
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const uint8_t
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
         const int64_t r = items <= INT32_MAX ? static_cast<int32_t>(it) / per_row : it / per_row;
         const int k0 = static_cast<int>(it - r * per_row) * (STEPS * 256);
-        const int64_t sr = scale_row ? ld_l2(scale_row + r) : tiled_row(r, rows, matrices);  // -1: a row not in use
+        const int64_t sr = PLAN ? plan_index(ld_l2(scale_row + r), tiled) : tiled_row(r, rows, matrices);  // -1: a row not in use
         uint32_t c[STEPS], w = 0;
 #pragma unroll
         for (int u = 0; u < STEPS; ++u) {
@@ -494,9 +497,9 @@ cudaError_t run_quantize(const void* X, int64_t ldx, int64_t rows, int64_t K, in
 template <bool MX, class T, bool VEC, int STEPS>
 cudaError_t run_dequantize(const Fp4View& v, int64_t K, float g, const PlanView& p, T* out, cudaStream_t stream) {
     const int64_t items = v.rows * v.matrices * ((K + STEPS * 256 - 1) / (STEPS * 256));
-    return launch_dependent(fp4_dequantize_kernel<MX, T, VEC, STEPS>, item_grid(items, kQThreads / 32), kQThreads, stream,
-                            v.codes, fp4_pitch(K), v.scales, fp4_chunks(MX, K), v.rows, v.matrices, K, g,
-                            p.experts ? p.scale_row : nullptr, out);
+    const auto kern = p.experts ? fp4_dequantize_kernel<MX, T, VEC, STEPS, true> : fp4_dequantize_kernel<MX, T, VEC, STEPS, false>;
+    return launch_dependent(kern, item_grid(items, kQThreads / 32), kQThreads, stream, v.codes, fp4_pitch(K), v.scales,
+                            fp4_chunks(MX, K), v.rows, v.matrices, K, g, p.scale_row, p.tiled, out);
 }
 
 template <bool MX, class T>

@@ -136,7 +136,15 @@ struct PlanView {
     int64_t tokens = 0;
     int slots = 1;
     int experts = 0;
+    int rows = 0;   // tokens * slots
+    int tiled = 0;  // rows that the tiled scales of an operand of the plan's rows have
 };
+
+// Entry v of a plan's arrays as an index below `limit`, or -1. The arrays are the caller's memory: one that was never sorted, or
+// sorted for other sizes, leads to no access outside the buffers of a call.
+__host__ __device__ inline int plan_index(int v, int limit) {
+    return static_cast<unsigned>(v) < static_cast<unsigned>(limit) ? v : -1;
+}
 
 enum class ExpertOp { Gather, GatherBackward, Combine, CombineBackward };
 

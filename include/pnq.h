@@ -312,7 +312,9 @@ enum pnq_float { PNQ_F32 = 0, PNQ_BF16 = 1 };
 
 /* How the rows of an expert layer are sorted: device int32 arrays, filled by pnq_expert_sort. Passed
  * by HOST pointer. n = tokens * slots is the number of (token, slot) choices; slot number t * slots
- * + j is token t's j-th choice. */
+ * + j is token t's j-th choice. The arrays are checked where they are used: a position or a scale row outside its range
+ * counts as -1, and offsets that do not rise within 0 .. n leave the product no rows (zeros), so that arrays that
+ * were never sorted, or were overwritten, lead to no access outside a call's buffers. */
 typedef struct pnq_expert_plan {
     int32_t* offsets;      /* [experts + 1] first sorted row of each expert; the last: rows in use */
     int32_t* block_start;  /* [experts + 1] first 128-row scale block of each expert */
