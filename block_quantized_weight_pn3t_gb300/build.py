@@ -1,5 +1,5 @@
-"""Builds libpnq.so in-tree (one nvcc process per translation unit, in parallel, for sm_103a) and _native.so, the torch
-wrappers of the 4-bit operands and the expert layer (g++ against the installed torch), beside it."""
+"""Builds libpnq.so in-tree (one nvcc process per translation unit, in parallel, for sm_103a) and, where torch and g++ are
+there, _native.so beside it, the torch wrappers of the 4-bit operands and the expert layer. The C library needs nvcc alone."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -37,19 +37,19 @@ def _deps(src: str) -> list[str]:
         [os.path.join(INCLUDE, "pnq.h"), src]
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
+    """Where the installed torch is, None where there is none."""
     import importlib.util
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found: it is required to build the torch wrappers")
+        return None
     return list(spec.submodule_search_locations)[0]
 
 
-def _native_compile(nv: str):
+def _native_compile(nv: str, torch_dir: str):
     """The compile command of pnq_torch.cpp, or None where its object is up to date for this torch and Python."""
     src, obj, stamp = (os.path.join(CSRC, "pnq_torch.cpp"), os.path.join(BUILD_DIR, "pnq_torch.o"),
                        os.path.join(BUILD_DIR, "pnq_torch.stamp"))
-    torch_dir = _torch_dir()
     with open(os.path.join(torch_dir, "version.py")) as f:
         key = torch_dir + "\n" + f.read() + sysconfig.get_config_var("EXT_SUFFIX")
     have = open(stamp).read() if os.path.exists(stamp) else None
@@ -73,7 +73,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         o = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
         if force or not os.path.exists(o) or os.path.getmtime(o) < max(os.path.getmtime(d) for d in _deps(s)):
             jobs.append([nv, *flags, "-c", s, "-o", o])
-    native = _native_compile(nv)
+    torch_dir = _torch_dir()
+    wrappers = torch_dir is not None and shutil.which("g++") is not None
+    if not wrappers:
+        print(f"{'torch' if torch_dir is None else 'g++'} not found: building {os.path.basename(LIB)} without the torch wrappers of "
+              "the 4-bit operands and the expert layer")
+    native = _native_compile(nv, torch_dir) if wrappers else None
     if native is not None:
         jobs.append(native[0])
     if verbose:
@@ -81,9 +86,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(" ".join(j))
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         results = list(ex.map(lambda cmd: subprocess.run(cmd, capture_output=True, text=True), jobs))
+    failed = None  # of the wrappers' compile: raised once the C library is there
     for cmd, r in zip(jobs, results):
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            failed = RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            if native is None or cmd is not native[0]:
+                raise failed
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr)
     objs = [os.path.join(BUILD_DIR, s.replace(".cu", ".o")) for s in SOURCES]
@@ -96,8 +104,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         if r.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    if jobs or force or not os.path.exists(NATIVE):
-        torch_lib = os.path.join(_torch_dir(), "lib")
+    if failed is not None:
+        raise failed
+    if wrappers and (jobs or force or not os.path.exists(NATIVE)):
+        torch_lib = os.path.join(torch_dir, "lib")
         tmp = NATIVE + f".tmp{os.getpid()}"
         cmd = ["g++", "-shared", "-o", tmp, os.path.join(BUILD_DIR, "pnq_torch.o"), "-L", PKG, "-l:libpnq.so", "-L", torch_lib, "-lc10",
                "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
