@@ -39,6 +39,7 @@ _SIGNATURES = {
     "pnq_fp4_dequantize": [_I, _P, _P, _I64, _I64, _I64, _F, _P, _I, _P, _P],
     "pnq_fp4_pack": [_I, _P, _P, _I64, _I64, _I64, _P, _P, _P],
     "pnq_fp4_gemm": [_I, _P, _P, _I64, _P, _P, _I64, _I64, _F, _I, _P, _U, _P],
+    "pnq_fp4_gemm_shape": [_I, _I64, _I64, _I64, *[ctypes.POINTER(ctypes.c_int32)] * 3],
     "pnq_fp4_gemm_experts": [_I, _P, _P, _P, _P, _P, _I64, _I64, _F, _P, _I, _P, _U, _P],
     "pnq_expert_sort": [_P, _P, _P],
     "pnq_expert_gather": [_I, _P, _I64, _P, _P, _P],

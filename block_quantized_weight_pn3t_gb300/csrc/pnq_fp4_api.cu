@@ -179,6 +179,16 @@ extern "C" int pnq_fp4_gemm(int type, const uint8_t* x_codes, const uint8_t* x_s
                                     (flags & PNQ_GEMV_STATIC_WEIGHTS) != 0, stream));
 }
 
+extern "C" int pnq_fp4_gemm_shape(int type, int64_t M, int64_t N, int64_t K, int32_t* columns, int32_t* ctas, int32_t* split) {
+    int rc = check_shape(type, M, K, 1);
+    if (rc != PNQ_OK) return rc;
+    rc = check_shape(type, N, K, 1);
+    if (rc != PNQ_OK) return rc;
+    if (M == 0 || N == 0 || ((M + 63) / 64) * ((N + 127) / 128) > kMaxRows) return PNQ_ERR_SHAPE;
+    if (!columns || !ctas || !split) return PNQ_ERR_NULL;
+    return map_cuda(fp4_gemm_shape(M, N, K, columns, ctas, split));
+}
+
 extern "C" int pnq_fp4_gemm_experts(int type, const uint8_t* x_codes, const uint8_t* x_scales,
                                     const pnq_expert_plan* plan, const uint8_t* w_codes, const uint8_t* w_scales,
                                     int64_t N, int64_t K, float alpha, const float* w_global, int y_type, void* Y,

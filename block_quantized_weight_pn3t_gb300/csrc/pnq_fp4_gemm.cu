@@ -634,7 +634,46 @@ struct Shape {
 constexpr Shape kShapes[] = {{32, 1, 0.25, 0.6, 0.0}, {64, 1, 0.25, 0.7, 0.3}, {128, 1, 0.21, 1.0, 0.8}, {256, 2, 0.30, 1.9, 2.4}};
 constexpr Shape kExpertShapes[] = {{64, 1, 0, 0, 0}, {128, 1, 0, 0, 0}, {256, 1, 0, 0, 0}, {256, 2, 0, 0, 0}};
 
+// Tiles of a dense product of M by N rows.
+int64_t dense_tiles(const Shape& s, int64_t M, int64_t N) {
+    return (N + s.cg * kRows - 1) / (s.cg * kRows) * ((M + s.bn - 1) / s.bn);
+}
+
+// The shape of a dense product's tiles, and the CTAs that share a tile's K, whose estimate is least.
+cudaError_t choose_dense(int64_t M, int64_t N, int64_t K, Shape* best, int* split) {
+    const int64_t nk = (K + kStageK - 1) / kStageK;
+    double least = 0.0;
+    for (const Shape& s : kShapes) {
+        if (s.bn == 32 && M > 32) continue;
+        const int64_t tiles = dense_tiles(s, M, N);
+        for (int ks = 1; ks <= (s.cg == 1 ? kMaxSplit : 1) && (ks == 1 || nk >= 3 * ks); ++ks) {
+            int slots = device_sm_count() / s.cg;
+            if (ks > 1) {
+                // clusters of any shape hold one CTA per SM: the 64-column kernel answers for all
+                const cudaError_t e = resident_clusters(reinterpret_cast<const void*>(fp4_gemm_kernel<false, 64, 1, float>),
+                                                        gemm_smem<false, 64, 1>(), 1, ks, &slots);
+                if (e != cudaSuccess) return e;
+                if (tiles > slots) break;  // one tile per cluster, all at once
+            }
+            const double waves = static_cast<double>((tiles + slots - 1) / slots);
+            const double stages = static_cast<double>((nk + ks - 1) / ks);
+            double t = waves * stages * s.stage + (waves - 1.0) * s.tile + s.last;
+            if (ks > 1) t += 1.6 + 0.01 * static_cast<double>(std::min<int64_t>(s.bn, M));  // the cluster's sum
+            if (least == 0.0 || t < least) least = t, *best = s, *split = ks;
+        }
+    }
+    return cudaSuccess;
+}
+
 }  // namespace
+
+cudaError_t fp4_gemm_shape(int64_t M, int64_t N, int64_t K, int* columns, int* ctas, int* split) {
+    Shape s{};
+    const cudaError_t e = choose_dense(M, N, K, &s, split);
+    *columns = s.bn;
+    *ctas = s.cg;
+    return e;
+}
 
 cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t K, const PlanView& p, float alpha,
                             const float* w_global, bool bf16, void* Y, int* err, bool static_weights,
@@ -651,13 +690,8 @@ cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t
     a.chunks = static_cast<int>(fp4_chunks(mx, K));
     a.static_weights = static_weights;
     a.ks = 1;
-    const int64_t nk = (K + kStageK - 1) / kStageK;
-    auto count = [&](const Shape& s) {
-        const int64_t mt = p.experts ? std::min<int64_t>(x.rows, x.rows / s.bn + std::min<int64_t>(p.experts, x.rows))
-                                     : (x.rows + s.bn - 1) / s.bn;
-        return (w.rows + s.cg * kRows - 1) / (s.cg * kRows) * mt;
-    };
     Shape best{};
+    int64_t tiles = 0;
     if (p.experts) {
         // the experts' loads are not known here: by the rows in all, and by the average. 64 columns where no expert can
         // have more (one token, 8 of 64 experts of 1408 x 2048: 8.2 us, 8.5 with 128); 256 where tiles fill well enough
@@ -666,31 +700,15 @@ cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t
         // pairs; 64 of 1408 x 2048: 87.3 and 95.4)
         best = kExpertShapes[x.rows <= 64 ? 0 : x.rows < 160ll * p.experts ? 1 : K < 4096 ? 2 : 3];
         a.weights_once = best.bn < 256;
+        // the most that any distribution of the rows makes
+        tiles = (w.rows + best.cg * kRows - 1) / (best.cg * kRows) *
+                std::min<int64_t>(x.rows, x.rows / best.bn + std::min<int64_t>(p.experts, x.rows));
     } else {
-        // the shape, and the share of K, whose estimate is least
-        double least = 0.0;
-        for (const Shape& s : kShapes) {
-            if (s.bn == 32 && x.rows > 32) continue;
-            const int64_t tiles = count(s);
-            for (int ks = 1; ks <= (s.cg == 1 ? kMaxSplit : 1) && (ks == 1 || nk >= 3 * ks); ++ks) {
-                int slots = device_sm_count() / s.cg;
-                if (ks > 1) {
-                    // clusters of any shape hold one CTA per SM: the 64-column kernel answers for all
-                    const cudaError_t e = resident_clusters(reinterpret_cast<const void*>(fp4_gemm_kernel<false, 64, 1, float>),
-                                                            gemm_smem<false, 64, 1>(), 1, ks, &slots);
-                    if (e != cudaSuccess) return e;
-                    if (tiles > slots) break;  // one tile per cluster, all at once
-                }
-                const double waves = static_cast<double>((tiles + slots - 1) / slots);
-                const double stages = static_cast<double>((nk + ks - 1) / ks);
-                double t = waves * stages * s.stage + (waves - 1.0) * s.tile + s.last;
-                if (ks > 1) t += 1.6 + 0.01 * static_cast<double>(std::min<int64_t>(s.bn, x.rows));  // the cluster's sum
-                if (least == 0.0 || t < least) least = t, best = s, a.ks = ks;
-            }
-        }
+        const cudaError_t e = choose_dense(x.rows, w.rows, K, &best, &a.ks);
+        if (e != cudaSuccess) return e;
+        tiles = dense_tiles(best, x.rows, w.rows);
         a.weights_once = x.rows <= best.bn;
     }
-    const int64_t tiles = count(best);
     auto go = [&](auto m) {
         constexpr bool MX = decltype(m)::value;
         switch (best.bn) {

@@ -173,6 +173,9 @@ cudaError_t launch_fp4_dequantize(bool mx, const Fp4View& v, int64_t K, float g,
 cudaError_t launch_fp4_pack(bool mx, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
                             int64_t matrices, uint8_t* codes_out, uint8_t* scales_out, cudaStream_t stream);
 
+// How launch_fp4_gemm tiles a dense product: activation rows of a tile, CTAs of a tile, CTAs that share a tile's K.
+cudaError_t fp4_gemm_shape(int64_t M, int64_t N, int64_t K, int* columns, int* ctas, int* split);
+
 // Y = alpha X W^T (p.experts == 0), or by experts with p (x: its sorted rows).
 cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t K, const PlanView& p, float alpha,
                             const float* w_global, bool bf16, void* Y, int* err, bool static_weights,

@@ -382,6 +382,13 @@ int pnq_fp4_gemm(int type, const uint8_t* x_codes, const uint8_t* x_scales, int6
                  cudaStream_t stream);
 
 /*
+ * pnq_fp4_gemm_shape -- which kernel pnq_fp4_gemm takes for these sizes on the current device (host only, nothing is
+ * launched; for tests and measurements): the activation rows of a tile (columns), its CTAs (ctas: 2 for a pair) and
+ * the CTAs that share the sum over K (split). M, N >= 1.
+ */
+int pnq_fp4_gemm_shape(int type, int64_t M, int64_t N, int64_t K, int32_t* columns, int32_t* ctas, int32_t* split);
+
+/*
  * pnq_fp4_gemm_experts -- the product of an expert layer: Y[i] = alpha * w_global[e] * X[i] W_e^T for every
  * sorted row i of expert e. X: the operand pnq_fp4_quantize made with the same plan; W: experts
  * matrices of N x K; w_global: device fp32 [experts], or NULL (all 1). Y: [tokens * slots][N]; rows past
