@@ -3,8 +3,11 @@
 //
 // Every row kernel runs token by token: a token's row is read once and written to (or summed from) the
 // sorted rows of its slots, so the bytes moved are the least possible: T rows on one side, T * k on
-// the other. All of them are bound by HBM. Sums run in slot order in fp32: results do not depend on
-// the launch.
+// the other. All of them are bound by HBM. Sums over slots run in slot order in fp32: rows do not depend on
+// the launch. The weights' gradients are sums over D in fp32, split over a warp's or a CTA's threads: in which pieces goes by the
+// number of tokens and the alignment of the rows, so the same token's may differ in the last bits between batches
+// (never between two calls with the same tensors). A thread adds D / 32 (a warp per token) or D / 256 terms (a CTA), then the
+// threads' sums meet in 5 or 13 additions.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -424,8 +424,8 @@ int pnq_expert_gather_backward(int type, const void* dXS, int64_t D, const pnq_e
  * [tokens][slots]; YS [tokens * slots][D], Y [tokens][D]), in fp32, in slot order, rounded once. The rows
  * and weights of dropped slots are not used.
  * pnq_expert_combine_backward -- its gradients: dYS[i] = weights * dY[token] for every sorted row (rows past the
- * rows in use are zeros), dWeights[t][j] = <dY[t], YS[position]> in fp32 (0 for a dropped slot). dWeights
- * may be NULL.
+ * rows in use are zeros), dWeights[t][j] = <dY[t], YS[position]> in fp32 (0 for a dropped slot): how its D terms are
+ * grouped goes by the number of tokens and the rows' alignment, not by the call. dWeights may be NULL.
  */
 int pnq_expert_combine(int type, const void* YS, int64_t D, const pnq_expert_plan* plan, const float* weights, void* Y,
                        cudaStream_t stream);
