@@ -13,7 +13,18 @@ namespace {
 constexpr int64_t kMaxRows = int64_t(1) << 30;  // rows, expert rows and scale tiles are 32-bit in the kernels
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-int map_cuda(cudaError_t e) { return e == cudaSuccess ? PNQ_OK : PNQ_ERR_CUDA; }
+
+// The status of a launch. The launches keep what they asked of the device in maps under a mutex, which may throw where the host has
+// no memory left: no exception leaves a C entry.
+template <class F>
+int launched(F&& launch) {
+    try {
+        return launch() == cudaSuccess ? PNQ_OK : PNQ_ERR_CUDA;
+    } catch (...) {
+        return PNQ_ERR_CUDA;
+    }
+}
+
 bool is_fp4(int type) { return type == PNQ_NVFP4 || type == PNQ_MXFP4; }
 bool is_float(int type) { return type == PNQ_F32 || type == PNQ_BF16; }
 int group(int type) { return type == PNQ_MXFP4 ? 32 : 16; }
@@ -117,8 +128,10 @@ extern "C" int pnq_fp4_quantize(int type, int x_type, const void* X, int64_t ldx
     if (!aligned(X, x_type == PNQ_BF16 ? 2 : 4)) return PNQ_ERR_ALIGN;
     rc = check_operand(codes, scales);
     if (rc != PNQ_OK) return rc;
-    return map_cuda(launch_fp4_quantize(type == PNQ_MXFP4, x_type == PNQ_BF16, X, ldx, rows, K, matrices, inv_g, p, sorted,
-                                        codes, scales, stream));
+    return launched([&] {
+        return launch_fp4_quantize(type == PNQ_MXFP4, x_type == PNQ_BF16, X, ldx, rows, K, matrices, inv_g, p, sorted, codes,
+                                   scales, stream);
+    });
 }
 
 extern "C" int pnq_fp4_dequantize(int type, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
@@ -140,8 +153,10 @@ extern "C" int pnq_fp4_dequantize(int type, const uint8_t* codes, const uint8_t*
     if (rc != PNQ_OK) return rc;
     if (!out) return PNQ_ERR_NULL;
     if (!aligned(out, out_type == PNQ_BF16 ? 2 : 4)) return PNQ_ERR_ALIGN;
-    return map_cuda(launch_fp4_dequantize(type == PNQ_MXFP4, Fp4View{codes, scales, rows, matrices}, K, global_scale, p,
-                                          out_type == PNQ_BF16, out, stream));
+    return launched([&] {
+        return launch_fp4_dequantize(type == PNQ_MXFP4, Fp4View{codes, scales, rows, matrices}, K, global_scale, p,
+                                     out_type == PNQ_BF16, out, stream);
+    });
 }
 
 extern "C" int pnq_fp4_pack(int type, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
@@ -153,7 +168,9 @@ extern "C" int pnq_fp4_pack(int type, const uint8_t* codes, const uint8_t* scale
     if (codes_out == codes && K % 32 != 0) return PNQ_ERR_SHAPE;  // the rows' pitch changes: not in place
     rc = check_operand(codes_out, scales_out);
     if (rc != PNQ_OK) return rc;
-    return map_cuda(launch_fp4_pack(type == PNQ_MXFP4, codes, scales, rows, K, matrices, codes_out, scales_out, stream));
+    return launched([&] {
+        return launch_fp4_pack(type == PNQ_MXFP4, codes, scales, rows, K, matrices, codes_out, scales_out, stream);
+    });
 }
 
 extern "C" int pnq_fp4_gemm(int type, const uint8_t* x_codes, const uint8_t* x_scales, int64_t M, const uint8_t* w_codes,
@@ -174,9 +191,11 @@ extern "C" int pnq_fp4_gemm(int type, const uint8_t* x_codes, const uint8_t* x_s
     if (rc != PNQ_OK) return rc;
     if (!Y) return PNQ_ERR_NULL;
     if (!aligned(Y, y_type == PNQ_BF16 ? 2 : 4)) return PNQ_ERR_ALIGN;
-    return map_cuda(launch_fp4_gemm(type == PNQ_MXFP4, Fp4View{x_codes, x_scales, M, 1}, Fp4View{w_codes, w_scales, N, 1}, K,
-                                    PlanView{}, alpha, nullptr, y_type == PNQ_BF16, Y, device_error_word(),
-                                    (flags & PNQ_GEMV_STATIC_WEIGHTS) != 0, stream));
+    return launched([&] {
+        return launch_fp4_gemm(type == PNQ_MXFP4, Fp4View{x_codes, x_scales, M, 1}, Fp4View{w_codes, w_scales, N, 1}, K,
+                               PlanView{}, alpha, nullptr, y_type == PNQ_BF16, Y, device_error_word(),
+                               (flags & PNQ_GEMV_STATIC_WEIGHTS) != 0, stream);
+    });
 }
 
 extern "C" int pnq_fp4_gemm_shape(int type, int64_t M, int64_t N, int64_t K, int32_t* columns, int32_t* ctas, int32_t* split) {
@@ -186,7 +205,7 @@ extern "C" int pnq_fp4_gemm_shape(int type, int64_t M, int64_t N, int64_t K, int
     if (rc != PNQ_OK) return rc;
     if (M == 0 || N == 0 || ((M + 63) / 64) * ((N + 127) / 128) > kMaxRows) return PNQ_ERR_SHAPE;
     if (!columns || !ctas || !split) return PNQ_ERR_NULL;
-    return map_cuda(fp4_gemm_shape(M, N, K, columns, ctas, split));
+    return launched([&] { return fp4_gemm_shape(M, N, K, columns, ctas, split); });
 }
 
 extern "C" int pnq_fp4_gemm_experts(int type, const uint8_t* x_codes, const uint8_t* x_scales,
@@ -212,9 +231,11 @@ extern "C" int pnq_fp4_gemm_experts(int type, const uint8_t* x_codes, const uint
     if (rc != PNQ_OK) return rc;
     if (!Y) return PNQ_ERR_NULL;
     if (!aligned(Y, y_type == PNQ_BF16 ? 2 : 4) || !aligned(w_global, 4)) return PNQ_ERR_ALIGN;
-    return map_cuda(launch_fp4_gemm(type == PNQ_MXFP4, Fp4View{x_codes, x_scales, n, 1},
-                                    Fp4View{w_codes, w_scales, N, p.experts}, K, p, alpha, w_global, y_type == PNQ_BF16, Y,
-                                    device_error_word(), (flags & PNQ_GEMV_STATIC_WEIGHTS) != 0, stream));
+    return launched([&] {
+        return launch_fp4_gemm(type == PNQ_MXFP4, Fp4View{x_codes, x_scales, n, 1}, Fp4View{w_codes, w_scales, N, p.experts},
+                               K, p, alpha, w_global, y_type == PNQ_BF16, Y, device_error_word(),
+                               (flags & PNQ_GEMV_STATIC_WEIGHTS) != 0, stream);
+    });
 }
 
 extern "C" int pnq_expert_sort(const int32_t* ids, const pnq_expert_plan* plan, cudaStream_t stream) {
@@ -223,7 +244,7 @@ extern "C" int pnq_expert_sort(const int32_t* ids, const pnq_expert_plan* plan, 
     if (rc != PNQ_OK) return rc;
     if (p.tokens > 0 && !ids) return PNQ_ERR_NULL;
     if (!aligned(ids, 4)) return PNQ_ERR_ALIGN;
-    return map_cuda(launch_expert_sort(ids, p, stream));
+    return launched([&] { return launch_expert_sort(ids, p, stream); });
 }
 
 extern "C" int pnq_expert_gather(int type, const void* X, int64_t D, const pnq_expert_plan* plan, void* XS,
@@ -233,7 +254,9 @@ extern "C" int pnq_expert_gather(int type, const void* X, int64_t D, const pnq_e
     if (rc != PNQ_OK || p.tokens == 0) return rc;
     rc = check_elements(type, {X, XS});
     if (rc != PNQ_OK) return rc;
-    return map_cuda(launch_expert_rows(ExpertOp::Gather, type == PNQ_BF16, X, nullptr, D, p, nullptr, XS, nullptr, stream));
+    return launched([&] {
+        return launch_expert_rows(ExpertOp::Gather, type == PNQ_BF16, X, nullptr, D, p, nullptr, XS, nullptr, stream);
+    });
 }
 
 extern "C" int pnq_expert_gather_backward(int type, const void* dXS, int64_t D, const pnq_expert_plan* plan, void* dX,
@@ -243,8 +266,10 @@ extern "C" int pnq_expert_gather_backward(int type, const void* dXS, int64_t D, 
     if (rc != PNQ_OK || p.tokens == 0) return rc;
     rc = check_elements(type, {dXS, dX});
     if (rc != PNQ_OK) return rc;
-    return map_cuda(
-        launch_expert_rows(ExpertOp::GatherBackward, type == PNQ_BF16, dXS, nullptr, D, p, nullptr, dX, nullptr, stream));
+    return launched([&] {
+        return launch_expert_rows(ExpertOp::GatherBackward, type == PNQ_BF16, dXS, nullptr, D, p, nullptr, dX, nullptr,
+                                  stream);
+    });
 }
 
 extern "C" int pnq_expert_combine(int type, const void* YS, int64_t D, const pnq_expert_plan* plan, const float* weights,
@@ -255,7 +280,9 @@ extern "C" int pnq_expert_combine(int type, const void* YS, int64_t D, const pnq
     rc = check_elements(type, {YS, Y, weights});
     if (rc != PNQ_OK) return rc;
     if (!aligned(weights, 4)) return PNQ_ERR_ALIGN;
-    return map_cuda(launch_expert_rows(ExpertOp::Combine, type == PNQ_BF16, YS, nullptr, D, p, weights, Y, nullptr, stream));
+    return launched([&] {
+        return launch_expert_rows(ExpertOp::Combine, type == PNQ_BF16, YS, nullptr, D, p, weights, Y, nullptr, stream);
+    });
 }
 
 extern "C" int pnq_expert_combine_backward(int type, const void* dY, const void* YS, int64_t D,
@@ -267,6 +294,8 @@ extern "C" int pnq_expert_combine_backward(int type, const void* dY, const void*
     rc = check_elements(type, {dY, YS, dYS, weights});
     if (rc != PNQ_OK) return rc;
     if (!aligned(weights, 4) || !aligned(dWeights, 4)) return PNQ_ERR_ALIGN;
-    return map_cuda(launch_expert_rows(ExpertOp::CombineBackward, type == PNQ_BF16, dY, YS, D, p, weights, dYS, dWeights,
-                                       stream));
+    return launched([&] {
+        return launch_expert_rows(ExpertOp::CombineBackward, type == PNQ_BF16, dY, YS, D, p, weights, dYS, dWeights,
+                                  stream);
+    });
 }
