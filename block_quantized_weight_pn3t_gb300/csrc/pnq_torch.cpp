@@ -647,7 +647,11 @@ void check_operands(const MatrixObject* x, const MatrixObject* w) {
         refuse("operands are on cuda:" + std::to_string(x->device) + " and cuda:" + std::to_string(w->device));
 }
 
-unsigned to_flags(PyObject* o) { return o ? static_cast<unsigned>(to_int(o)) : 0u; }
+unsigned to_flags(PyObject* o) {
+    const int64_t v = o ? to_int(o) : 0;
+    if (v < 0 || v > UINT32_MAX) refuse("flags = " + std::to_string(v) + " are not known", PNQ_ERR_FLAGS);
+    return static_cast<unsigned>(v);
+}
 
 PNQ_ENTRY(fp4_gemm) {
     return entry([&]() -> PyObject* {

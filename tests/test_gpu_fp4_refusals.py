@@ -67,3 +67,16 @@ def test_a_refused_encode_leaves_out_as_it_was(g):
     assert torch.equal(m.global_scale, torch.tensor([0.5, 2.0], device="cuda"))
     pnq.fp4_quantize(pnq.NVFP4, x, 0.5, plan=second, out=q)
     assert q.global_scale == 0.5 and q.plan is second
+
+
+@pytest.mark.parametrize("flags", [2, 3, -1, 1 << 32, (1 << 32) + 1, -(1 << 32)])
+def test_unknown_flags(flags):
+    """Flags past 32 bits too: their low bits are not taken for the whole."""
+    q, w = pnq.fp4_quantize(pnq.NVFP4, torch.randn(8, 64, device="cuda")), pnq.fp4_quantize(pnq.NVFP4, torch.randn(3, 5, 64, device="cuda"))
+    with pytest.raises(pnq.PnqError) as e:
+        pnq.fp4_gemm(q, q, flags=flags)
+    assert e.value.status == pnq.Status.ERR_FLAGS
+    plan = plan_of(8, 2, 3)
+    with pytest.raises(pnq.PnqError) as e:
+        pnq.fp4_gemm_experts(pnq.fp4_quantize(pnq.NVFP4, torch.randn(8, 64, device="cuda"), plan=plan), w, plan, flags=flags)
+    assert e.value.status == pnq.Status.ERR_FLAGS
