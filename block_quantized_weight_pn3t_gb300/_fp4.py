@@ -11,6 +11,10 @@ compiled (csrc/pnq_torch.cpp): they check tensors, allocate results and make one
     ys = fp4_gemm_experts(q, w, plan)                # every row times its expert's matrix
     h = fp4_quantize(NVFP4, hs, g, plan=plan, sorted=True)   # rows in expert order already (between two products)
     y = expert_combine(ys, plan, weights)            # back to tokens, router weights applied
+
+They stand outside autograd: results require no gradient. The gather and the combine have theirs as calls,
+    dys, dweights = expert_combine_backward(dy, ys, plan, weights)
+    dx = expert_gather_backward(dxs, plan)
 """
 from __future__ import annotations
 

@@ -1,5 +1,6 @@
 // pnq_torch.cpp -- the torch wrappers of the 4-bit operands and the expert layer (module _native): checks of the tensors,
-// allocation of the results, and one call of the C ABI. No arithmetic happens here.
+// allocation of the results, and one call of the C ABI. No arithmetic happens here, and no autograd: results require no
+// gradient whatever the inputs do; expert_gather and expert_combine have their gradients as calls of their own.
 //
 // These calls run several times per layer of a decode step, each a few microseconds of GPU work. Through ctypes and
 // Python an encode cost the host some 8 us, of which the launch is two; here the checks read the tensors' fields
@@ -833,7 +834,7 @@ PyMethodDef methods[] = {
                            "(pitch of a row of codes, bytes of the tiled scales) of an operand."),
     PNQ_METHOD(fp4_quantize, "fp4_quantize(type_, x, global_scale=1.0, plan=None, out=None, stream=None, sorted=False)\n--\n\n"
                              "Encode x (CUDA bf16 or fp32, [rows][K], or [matrices][rows][K] contiguous; 2-D rows may be strided)\n"
-                             "for the global multiplier. With a plan, x holds the plan's tokens (sorted: its sorted rows)\n"
+                             "for the global multiplier (a number on the host: one computed on the device has to be read back). With a plan, x holds the plan's tokens (sorted: its sorted rows)\n"
                              "and the operand its sorted rows. out: an operand of the same shape to write into. Returns the Fp4Matrix."),
     PNQ_METHOD(fp4_dequantize, "fp4_dequantize(m, dtype=torch.float32, out=None, stream=None)\n--\n\n"
                                "The values an operand stands for, fp32 or bf16 [matrices * rows][K] (of a plan's operand: its\n"
@@ -843,20 +844,23 @@ PyMethodDef methods[] = {
                          "as an operand, once, when they are loaded. Where K is a multiple of 32 and the codes are 16-byte\n"
                          "aligned they are kept as they are, not copied."),
     PNQ_METHOD(fp4_gemm, "fp4_gemm(x, w, dtype=torch.float32, out=None, flags=0, stream=None)\n--\n\n"
-                         "Y[m][n] = sum_k X[m][k] W[n][k] of two operands of one type; fp32 or bf16 [M][N]."),
+                         "Y[m][n] = sum_k X[m][k] W[n][k] of two operands of one type; fp32 or bf16 [M][N]. There is no\n"
+                         "gradient of it: operands are codes."),
     PNQ_METHOD(fp4_gemm_experts, "fp4_gemm_experts(x, w, plan, dtype=torch.float32, out=None, flags=0, stream=None)\n--\n\n"
                                  "Every sorted row of x (made with `plan`) times its expert's matrix of w (matrices = the plan's\n"
-                                 "experts): fp32 or bf16 [tokens * slots][N], zeros past the rows in use."),
+                                 "experts): fp32 or bf16 [tokens * slots][N], zeros past the rows in use. No gradient, as fp4_gemm."),
     PNQ_METHOD(expert_sort, "expert_sort(ids, experts, plan=None, stream=None)\n--\n\n"
                             "The plan of ids (CUDA int32 [tokens][slots]: the expert of each choice; one outside 0 .. experts - 1\n"
                             "is dropped): stable, so equal experts keep the order of their slots."),
     PNQ_METHOD(expert_gather, "expert_gather(x, plan, out=None, stream=None)\n--\n\n"
-                              "Sorted rows of x (fp32 or bf16 [tokens][D]): [tokens * slots][D], zeros past the rows in use."),
+                              "Sorted rows of x (fp32 or bf16 [tokens][D]): [tokens * slots][D], zeros past the rows in use. Outside\n"
+                              "autograd: the result requires no gradient; expert_gather_backward gives x's."),
     PNQ_METHOD(expert_gather_backward, "expert_gather_backward(dxs, plan, out=None, stream=None)\n--\n\n"
                                        "Gradient of expert_gather: dx [tokens][D], each token's rows summed in fp32 in slot order."),
     PNQ_METHOD(expert_combine, "expert_combine(ys, plan, weights, out=None, stream=None)\n--\n\n"
                                "y[t] = sum over t's slots of weights[t][j] * its row of ys ([tokens * slots][D]; weights fp32\n"
-                               "[tokens][slots])."),
+                               "[tokens][slots]). Outside autograd: the result requires no gradient; expert_combine_backward gives\n"
+                               "those of ys and weights."),
     PNQ_METHOD(expert_combine_backward, "expert_combine_backward(dy, ys, plan, weights, out=None, dweights=None, stream=None)\n--\n\n"
                                         "Gradients of expert_combine: (dys [tokens * slots][D], dweights fp32 [tokens][slots])."),
     {nullptr, nullptr, 0, nullptr}};
