@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 && V == 8 ? 3 : 0)
     }
 }
 
-// dYS[position] = weights * dY[t], dWeights[t][j] = <dY[t], YS[position]>.
+// dYS[position] = weights * dY[t], dWeights[t][j] = <dY[t], YS[position]>. 2 CTAs an SM: 128 registers, and 28 to 68 bytes a
+// thread spilled (16384 x 8 rows of 2048 bf16, 40 bytes: 183 us = 6.2 TB/s all the same).
 template <class T, int V, int TEAM>
 __global__ void __launch_bounds__(kRowThreads, 2) expert_combine_backward_kernel(
     const typename Vec<T, V>::Raw* __restrict__ dY, const typename Vec<T, V>::Raw* __restrict__ YS, int64_t vecs,
@@ -484,8 +485,8 @@ cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const
 template <class T, int V>
 cudaError_t run_rows(ExpertOp op, const void* a, const void* b, int64_t D, const PlanView& p, const float* weights,
                      void* out, float* dw, cudaStream_t stream) {
-    // A warp per token where the tokens give every SM 16 warps (16384 tokens of 2048 bf16, 8 slots: combine 92 us = 6.5 TB/s,
-    // its gradients 182 = 6.3 TB/s; a CTA per token took 13 to 15 percent longer), a CTA where they are few (5 tokens of 2048
+    // A warp per token where the tokens give every SM 16 warps (16384 tokens of 2048 bf16, 8 slots: combine 94 us = 6.4 TB/s,
+    // its gradients 183 = 6.2 TB/s; a CTA per token took 13 to 15 percent longer), a CTA where they are few (5 tokens of 2048
     // fp32, 4 slots: combine 8.1 us by warps and 2.0 by CTAs). The gather of rows of 4096 bytes or more keeps the CTA (93 us
     // against 96).
     // Between them, rounds of the device times the steps of a token in each (a step is about half of what a round costs

@@ -17,15 +17,16 @@
 // the next tile is multiplied. Up to 128 columns two accumulators alternate; 256 columns leave room for one beside
 // the scale columns.
 //
-// What bounds it (GB300, times of 8192 x 17408 x 5120 NVFP4 to bf16 unless said otherwise).
+// What bounds it (GB300, times of 8192 x 17408 x 5120 NVFP4 to bf16 unless said otherwise; in short runs, in runs of
+// seconds the power limit holds it at 250 us).
 //   - Many rows: the tensor pipe. 256 x 256 tiles by CTA pairs (cta_group::2: each CTA holds half of the activation
 //     rows, so a stage is 38 KB for the work that takes one CTA 54 KB) 230 us = 6.4 PFLOP/s, single CTAs of 128 x 256
-//     248 us, of 128 x 128 290 us. ncu: the tensor pipe is busy 69 percent of the cycles. A stage in the run of a tile
+//     248 us, of 128 x 128 290 us. ncu: the tensor pipe is busy 68 percent of the cycles. A stage in the run of a tile
 //     takes 0.30 us, 0.27 of it the MMAs; a change of tiles costs some 1.9 us, the way from the last MMA through the
-//     accumulator's release to the first (tensor memory has no room for a second one: 2 x 256 columns are all of it)
-//     and the stores. 192 columns with two accumulators took longer a stage than 256 (279 us).
-//   - Few rows: HBM. One row of 17408 x 5120 takes 10.8 us (50.1 MB: 7.4 us at the copy rate; a product of 1/20 of the
-//     bytes takes 3.3). K is split over a cluster where there are fewer tiles than SMs (13 rows of 5120 x 17408:
+//     accumulator's release to the first (beside the scale columns that each stage has for itself there is no room for a
+//     second one) and the stores. 192 columns with two accumulators took longer a stage than 256 (279 us).
+//   - Few rows: HBM. One row of 17408 x 5120 takes 11.0 us (50.1 MB: 7.4 us at the copy rate; a product of 1/20 of the
+//     bytes, 17408 x 256, takes 3.4). K is split over a cluster where there are fewer tiles than SMs (13 rows of 5120 x 17408:
 //     20.7 -> 12.3 us with three CTAs per tile); the partial tiles meet in distributed shared memory, in CTA order.
 //   - Between them: a stage's turn through one thread's waits and instructions. Waits by one lane (32 lanes probe the
 //     barrier 32 times), bounded by the SM's clock (a read of the global timer costs 0.4 us), one wait per stage (its
@@ -694,10 +695,12 @@ cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t
     int64_t tiles = 0;
     if (p.experts) {
         // the experts' loads are not known here: by the rows in all, and by the average. 64 columns where no expert can
-        // have more (one token, 8 of 64 experts of 1408 x 2048: 8.2 us, 8.5 with 128); 256 where tiles fill well enough
-        // (64 experts of 1408 x 2048, 100 rows each: 24.1 us with 128, 27.4 with 256; 192 each: 34.7 and 29.5), by pairs
-        // where K outweighs their dearer change of tiles (8 experts of 4096 x 4096, 1000 rows each: 58.7 us and 54.9 by
-        // pairs; 64 of 1408 x 2048: 87.3 and 95.4)
+        // have more (one token, 8 of 64 experts of 1408 x 2048: 8.2 us, 8.5 with 128); 256 from 160 rows an expert on
+        // (64 experts of 1408 x 2048, 100 rows each: 23.1 us with 128, 27.4 with 256; 192 each: 34.6 and 29.2), by pairs
+        // where K outweighs their dearer change of tiles (8 experts of 4096 x 4096, 1000 rows each: 54.6 us and 51.3 by
+        // pairs; 64 of 1408 x 2048: 87.3 and 95.4). The rule looks at neither N nor the number of SMs: few experts with few
+        // weight rows leave SMs without a tile (8 experts of 512 x 2048, 200 rows each: 7.9 us, 6.6 with 128 columns; of
+        // 512 x 4096: 10.6 by pairs, 8.3 with 128)
         best = kExpertShapes[x.rows <= 64 ? 0 : x.rows < 160ll * p.experts ? 1 : K < 4096 ? 2 : 3];
         a.weights_once = best.bn < 256;
         // the most that any distribution of the rows makes

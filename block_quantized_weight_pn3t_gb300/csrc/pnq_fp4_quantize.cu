@@ -9,8 +9,9 @@
 //           steps the lanes of a four exchange their codes and write 16 bytes each; the scale words of four groups are
 //           neighbours in the tiled layout and leave as one word.
 //   decode: a lane loads the word of 8 codes, which is a store of 16 bytes of bf16. For fp32 the warp exchanges the words so
-//           that lane l writes elements 4 l .. 4 l + 3 of 128: every store covers 512 contiguous bytes (8191 x 5152: 34.3 us;
-//           lanes that wrote 32 bytes each took 36.7), and for a bf16 output that is not on 16 bytes too.
+//           that lane l writes elements 4 l .. 4 l + 3 of 128: every store covers 512 contiguous bytes (with a quarter of the CTAs
+//           that a launch has now, 8191 x 5152 took 34.3 us so and 36.7 by lanes that wrote 32 bytes each; now 29.9), and
+//           for a bf16 output that is not on 16 bytes too.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -87,7 +88,8 @@ __device__ __forceinline__ void load8(const T* p, Eight<T>& x) {
 }
 
 // Rows of any other alignment: a lane loads elements lane + 32 i, so that a load of the warp reads one run of addresses and
-// not 32 (8191 x 5152 fp32, row stride 5153: 72.5 -> 36.6 us; bf16 41.1 -> 33.2), and the warp turns them through shared memory.
+// not 32 (8191 x 5152 fp32 to NVFP4, row stride 5153: 72.5 us by lanes of eight elements each, 35.4 so; bf16 41.1 and 34.2), and
+// the warp turns them through shared memory.
 __device__ __forceinline__ void pack8(const uint32_t (&e)[8], Eight<float>& x) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x.w[i] = e[i];
@@ -167,9 +169,10 @@ __device__ __forceinline__ float reciprocal(float s) {
 }
 
 // Encodes this lane's 8 elements (zeros where the lane is past the row): its scale word and its 8 codes. The group's lanes
-// (2 for NVFP4, 4 for MXFP4) are neighbours. Instructions, not HBM, bounded the encode of bf16, so two elements go through
-// each packed one, and the largest |y| is made from the largest |x| (the product's rounding keeps their order): 8191 x 5152
-// to NVFP4 36.0 -> 27.0 us from bf16, 36.3 -> 30.8 from fp32; to MXFP4 30.7 -> 22.2 and 30.8 -> 29.5.
+// (2 for NVFP4, 4 for MXFP4) are neighbours. Instructions, not HBM, bound the encode of bf16 (of NVFP4 the issue slots are
+// busy 79 percent of the cycles, DRAM 39), so two elements go through each packed one, and the largest |y| is made from
+// the largest |x| (the product's rounding keeps their order). 8191 x 5152 with an instruction an element took 36 us to
+// NVFP4 from either type and 31 to MXFP4; now 25.4 from bf16 and 29.6 from fp32, and 21.6 and 28.4.
 //
 // y / s is rounded to nearest, from r = 1 / s rounded to nearest, by two fused steps after the first estimate (P. W.
 // Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990):
@@ -210,9 +213,10 @@ __device__ __forceinline__ void encode8(const Eight<T>& x, float inv_g, uint32_t
 // Where the encoded rows go: row r to row r; a plan's token to the sorted rows of its slots; a plan's sorted row to its place.
 enum class Rows { Plain, Tokens, Sorted };
 
-// STEPS steps of 256 elements per warp and item. 64 registers: 8191 x 5152 fp32 33.2 -> 30.7 us; 48 for bf16, which holds half
-// as many words: 27.0 -> 25.4 (MXFP4 23.1 -> 21.5). CTAs of 128 threads rather than 256: 4096 tokens x 8 slots of 2048
-// 13.8 -> 13.2 us (1.7 rounds of CTAs, the second not full).
+// STEPS steps of 256 elements per warp and item. 64 registers, and 48 for bf16, which holds half as many words: without the
+// bounds 8191 x 5152 took 8 percent longer from fp32 and 6 from bf16. CTAs of 128 threads rather than 256: 4096 tokens x 8 slots
+// of 2048 to MXFP4 13.8 -> 12.6 us (1.7 rounds of CTAs, the second not full; its issue slots are busy 42 percent of
+// the cycles and DRAM 15: latency bounds it, not either of them).
 template <bool MX, class T, bool VEC, Rows ROWS, int STEPS>
 __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 10 : 8) fp4_quantize_kernel(const T* __restrict__ X, int64_t ldx, int64_t rows,
                                                                  int64_t matrices, int K, float inv_g, PlanView p,
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_pitch_codes_kernel(const uint8_
 }
 
 // CTAs of a grid, each of which walks its items with that stride. Several rounds of them: a CTA that comes in loads while its
-// neighbours compute (8191 x 5152 with 64 per SM rather than 16: decode 34.1 -> 29.8 us, 19.8 -> 18.2 to bf16, encode of fp32 30.6
+// neighbours compute (8191 x 5152 with 64 per SM rather than 16: decode 34.1 -> 29.9 us, 19.8 -> 18.2 to bf16, encode of fp32 30.6
 // -> 29.6; with 256 the unaligned outputs take a fifth longer).
 int item_grid(int64_t items, int per_cta) {
     return static_cast<int>(
