@@ -256,12 +256,12 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 10 : 8) fp4_quanti
 #pragma unroll
             for (int u = 0; u < STEPS; ++u) turn8(x[u], turned[threadIdx.x >> 5], lane);
         }
-        // with a plan: where the row goes, lane j holding slot j's places
-        int at = -1, srow = 0;
+        // with a plan: where the row goes, lane j holding slot j's places (checked where they are used: a check here, in the way of
+        // the loads, cost 96 rows of 2048 a tenth, 2.4 -> 2.6 us)
+        int at = -1, srow = -1;
         if (ROWS == Rows::Tokens && lane < p.slots) {
-            at = plan_index(ld_l2(p.position + r * p.slots + lane), p.rows);
-            if (at >= 0) srow = ld_l2(p.scale_row + at);
-            if (plan_index(srow, p.tiled) < 0) at = -1;
+            at = ld_l2(p.position + r * p.slots + lane);
+            if (plan_index(at, p.rows) >= 0) srow = ld_l2(p.scale_row + at);
         }
         uint32_t c[STEPS], words = 0;  // words: a byte of each step, the same in a group's lanes; groups past K: zero
 #pragma unroll
@@ -327,19 +327,18 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 10 : 8) fp4_quanti
         } else {
             for (int j0 = 0; j0 < p.slots; j0 += 32) {
                 if (j0) {
-                    at = -1;
-                    if (j0 + lane < p.slots) at = plan_index(ld_l2(p.position + r * p.slots + j0 + lane), p.rows);
-                    if (at >= 0) srow = ld_l2(p.scale_row + at);
-                    if (plan_index(srow, p.tiled) < 0) at = -1;
+                    at = srow = -1;
+                    if (j0 + lane < p.slots) at = ld_l2(p.position + r * p.slots + j0 + lane);
+                    if (plan_index(at, p.rows) >= 0) srow = ld_l2(p.scale_row + at);
                 }
                 const int most = min(32, p.slots - j0);
                 for (int j = 0; j < most; ++j) {
-                    const int row = __shfl_sync(0xffffffffu, at, j);
+                    const int row = plan_index(__shfl_sync(0xffffffffu, at, j), p.rows);
                     if (row >= 0) put_codes(row);
                 }
                 for (int j = 0; j < most; j += kSub) {  // lanes past the slots hold -1
-                    const int row = __shfl_sync(0xffffffffu, at, (j + sub) & 31), tiled = __shfl_sync(0xffffffffu, srow, (j + sub) & 31);
-                    if (has && row >= 0 && j + sub < most) put_scales(tiled);
+                    const int tiled = plan_index(__shfl_sync(0xffffffffu, srow, (j + sub) & 31), p.tiled);
+                    if (has && tiled >= 0 && j + sub < most) put_scales(tiled);
                 }
             }
         }
