@@ -15,7 +15,9 @@ from ._binding import (PN3T, PN4T, NVFP4, NVFP4_DIV, Q4G64_F16S, Q5G64_F16S, Q6G
 # libraries) is imported at the first use of one of its names, and `import *`, which would use them all, leaves them out
 _FP4_NAMES = ("MXFP4", "FP4_GROUP", "Fp4Matrix", "ExpertPlan", "fp4_lib", "fp4_layout", "fp4_quantize",
               "fp4_dequantize", "fp4_pack", "fp4_gemm", "fp4_gemm_experts", "expert_sort", "expert_gather",
-              "expert_gather_backward", "expert_combine", "expert_combine_backward")
+              "expert_gather_backward", "expert_combine", "expert_combine_backward", "SOFTMAX", "SIGMOID", "RouteRule",
+              "expert_route", "expert_route_backward", "rms_norm", "rms_norm_int8", "rms_norm_backward", "int8_quantize",
+              "int8_dequantize", "int8_gemm")
 
 
 def __getattr__(name):

@@ -31,10 +31,19 @@ if not os.path.exists(_NATIVE):
 
 from ._native import (Fp4Matrix, ExpertPlan, fp4_layout, fp4_quantize, fp4_dequantize, fp4_pack, fp4_gemm,  # noqa: E402,F401
                       fp4_gemm_experts, expert_sort, expert_gather, expert_gather_backward, expert_combine,
-                      expert_combine_backward)
+                      expert_combine_backward, expert_route, expert_route_backward, rms_norm, rms_norm_int8, rms_norm_backward,
+                      int8_quantize, int8_dequantize, int8_gemm)
 
 MXFP4 = 1006
+SOFTMAX, SIGMOID = 0, 1  # scores of expert_route
 FP4_GROUP = {b.NVFP4: 16, MXFP4: 32}
+
+
+class RouteRule(ctypes.Structure):
+    """pnq_route_rule of ``include/pnq.h``, for calls of the library itself."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("experts", "slots", "score", "groups", "top_groups", "best", "renormalize")] + \
+        [("scale", ctypes.c_float)]
+
 
 _P, _I64, _I, _F, _U = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_uint
 _SIGNATURES = {
@@ -50,6 +59,15 @@ _SIGNATURES = {
     "pnq_expert_gather_backward": [_I, _P, _I64, _P, _P, _P],
     "pnq_expert_combine": [_I, _P, _I64, _P, _P, _P, _P],
     "pnq_expert_combine_backward": [_I, _P, _P, _I64, _P, _P, _P, _P, _P],
+    "pnq_expert_route": [_I, _P, _I64, _I64, _P, _P, _P, _P, _P],
+    "pnq_expert_route_backward": [_I, _P, _P, _I64, _P, _I64, _P, _P, _P],
+    "pnq_rms_norm": [_I, _P, _I64, _P, _I64, _I64, _I64, _I, _P, _F, _P, _P, _P, _P, _I64, _P, _P],
+    "pnq_rms_norm_backward": [_I, _P, _I64, _P, _I64, _I, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, ctypes.c_uint64, _P],
+    "pnq_rms_norm_backward_scratch_bytes": [_I64, _I64, ctypes.POINTER(ctypes.c_uint64)],
+    "pnq_int8_quantize": [_I, _P, _I64, _I64, _I64, _P, _I64, _P, _P],
+    "pnq_int8_dequantize": [_P, _I64, _P, _I64, _I64, _I, _P, _P],
+    "pnq_int8_gemm": [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I, _P, _P, ctypes.c_uint64, _P],
+    "pnq_int8_gemm_scratch_bytes": [_I64, _P, _I64, _I64, _I64, ctypes.POINTER(ctypes.c_uint64)],
 }
 _lib = None
 

@@ -1,0 +1,164 @@
+// pnq_int8_gemm.cu -- products of 8-bit integer matrices with a scale per activation row and per weight row, sm_103a:
+//   Y[m][n] = (sum_k X[m][k] W[n][k]) x_scale[m] w_scale[n]
+// The sum is exact (32-bit integers), whatever kernel takes a call: results do not hang on the number of rows.
+//
+// Few rows (int8_rows_kernel): the weights stream from HBM through registers and are multiplied by __dp4a; x waits in shared memory.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "pnq_device.cuh"
+#include "pnq_internal.h"
+
+namespace pnq {
+namespace {
+
+constexpr int kRowThreads = 512;
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kGroup = 4;                 // weight rows that a warp takes together: a piece of x serves them all
+constexpr int kBlockRows = 256;           // weight rows of a CTA whose sums are in shared memory at a time
+constexpr int kRowSmem = 200 * 1024;      // x
+
+struct RowArgs {
+    const int8_t *X, *W;
+    const float *x_scales, *w_scales;
+    void* Y;
+    int64_t ldx, ldw;
+    int M, N, K, tile, segment;  // tile: activation rows of a CTA; segment: bytes of a row that a warp takes at a time
+};
+
+__device__ __forceinline__ void store_product(float* y, float f) { *y = f; }
+__device__ __forceinline__ void store_product(__nv_bfloat16* y, float f) { *y = __float2bfloat16_rn(f); }
+
+// The sum as fp32 (one rounding), times both scales in turn.
+__device__ __forceinline__ float scaled(int sum, float x_scale, float w_scale) {
+    return __fmul_rn(__fmul_rn(__int2float_rn(sum), x_scale), w_scale);
+}
+
+// 16 bytes of a row from `at` on, bytes from K on as zeros. ALIGNED: rows start on 16 bytes.
+template <bool ALIGNED>
+__device__ __forceinline__ uint4 load16(const int8_t* row, int at, int K) {
+    if (ALIGNED && at + 16 <= K) return ld_l2(reinterpret_cast<const uint4*>(row + at));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (at + i < K) w[i / 4] |= ld_l2(reinterpret_cast<const uint8_t*>(row + at + i)) << (8 * (i % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ int dot16(uint4 a, uint4 b, int c) {
+    c = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), c);
+    c = __dp4a(static_cast<int>(a.y), static_cast<int>(b.y), c);
+    c = __dp4a(static_cast<int>(a.z), static_cast<int>(b.z), c);
+    return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), c);
+}
+
+// CTA (b, t): weight rows [N b / grid, N (b + 1) / grid), activation rows [t tile, ..). Its warps take pieces of kGroup weight rows x `segment`
+// bytes in turn; a piece's sums go into the CTA's by integer additions in shared memory.
+template <int MT, bool ALIGNED, class T>
+__global__ void __launch_bounds__(kRowThreads, 1) int8_rows_kernel(const RowArgs a) {
+    extern __shared__ __align__(16) uint8_t xs[];
+    __shared__ int sums[kBlockRows][MT];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int m0 = static_cast<int>(blockIdx.y) * a.tile, mt = min(a.tile, a.M - m0), K = a.K, pitch = (K + 15) / 16 * 16;
+    const int64_t N = a.N, b = blockIdx.x, g = gridDim.x;
+    const int first = static_cast<int>(N * b / g), last = static_cast<int>(N * (b + 1) / g);
+    griddep_begin();
+    for (int m = 0; m < MT; ++m)
+        for (int at = static_cast<int>(threadIdx.x) * 16; at < pitch; at += kRowThreads * 16)
+            *reinterpret_cast<uint4*>(xs + static_cast<int64_t>(m) * pitch + at) =
+                m < mt ? load16<false>(a.X + (m0 + m) * a.ldx, at, K) : make_uint4(0, 0, 0, 0);
+    const int segments = (K + a.segment - 1) / a.segment;
+    for (int r0 = first; r0 < last; r0 += kBlockRows) {
+        const int rows = min(kBlockRows, last - r0), groups = (rows + kGroup - 1) / kGroup;
+        for (int i = threadIdx.x; i < rows * MT; i += kRowThreads) (&sums[0][0])[i] = 0;
+        __syncthreads();
+        for (int u = warp; u < groups * segments; u += kRowWarps) {
+            const int group = u / segments, s = u - group * segments;
+            const int end = min(K, (s + 1) * a.segment);
+            const int8_t* w[kGroup];
+#pragma unroll
+            for (int r = 0; r < kGroup; ++r) w[r] = a.W + min(r0 + group * kGroup + r, last - 1) * a.ldw;
+            int acc[kGroup][MT] = {};
+#pragma unroll 2
+            for (int at = s * a.segment + lane * 16; at < end; at += 512) {
+                uint4 v[kGroup];
+#pragma unroll
+                for (int r = 0; r < kGroup; ++r) v[r] = load16<ALIGNED>(w[r], at, K);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(xs + static_cast<int64_t>(m) * pitch + at);
+#pragma unroll
+                    for (int r = 0; r < kGroup; ++r) acc[r][m] = dot16(v[r], x, acc[r][m]);
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < kGroup; ++r)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const int sum = __reduce_add_sync(0xffffffffu, acc[r][m]);
+                    if (lane == 0 && group * kGroup + r < rows) atomicAdd(&sums[group * kGroup + r][m], sum);
+                }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * mt; i += kRowThreads) {
+            const int m = i / rows, r = i - m * rows, n = r0 + r;
+            store_product(static_cast<T*>(a.Y) + static_cast<int64_t>(m0 + m) * a.N + n,
+                          scaled(sums[r][m], ld_l2(a.x_scales + m0 + m), ld_l2(a.w_scales + n)));
+        }
+        __syncthreads();
+    }
+}
+
+template <int MT, class T>
+cudaError_t run_rows(const RowArgs& a, cudaStream_t stream) {
+    const bool aligned = reinterpret_cast<uintptr_t>(a.W) % 16 == 0 && a.ldw % 16 == 0;
+    auto kernel = aligned ? int8_rows_kernel<MT, true, T> : int8_rows_kernel<MT, false, T>;
+    const int smem = MT * ((a.K + 15) / 16 * 16);
+    const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(static_cast<unsigned>(std::min(device_sm_count(), (a.N + kGroup - 1) / kGroup)), static_cast<unsigned>((a.M + a.tile - 1) / a.tile));
+    lc.blockDim = dim3(kRowThreads);
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, a);
+}
+
+template <class T>
+cudaError_t run_rows(RowArgs a, cudaStream_t stream) {
+    const int pitch = (a.K + 15) / 16 * 16;
+    int mt = 8;
+    while (mt > 1 && (mt * pitch > kRowSmem || mt / 2 >= a.M)) mt /= 2;
+    a.tile = mt;
+    a.segment = 2048;
+    switch (mt) {
+        case 8: return run_rows<8, T>(a, stream);
+        case 4: return run_rows<4, T>(a, stream);
+        case 2: return run_rows<2, T>(a, stream);
+        default: return run_rows<1, T>(a, stream);
+    }
+}
+
+}  // namespace
+
+uint64_t int8_gemm_scratch(int64_t, const Int8View&, int64_t) { return 0; }
+
+cudaError_t launch_int8_gemm(const Int8View& x, const Int8View& w, int64_t K, bool bf16, void* Y, void*, int*, cudaStream_t stream) {
+    RowArgs a{};
+    a.X = x.codes, a.ldx = x.ld, a.x_scales = x.scales;
+    a.W = w.codes, a.ldw = w.ld, a.w_scales = w.scales;
+    a.Y = Y;
+    a.M = static_cast<int>(x.rows), a.N = static_cast<int>(w.rows), a.K = static_cast<int>(K);
+    return bf16 ? run_rows<__nv_bfloat16>(a, stream) : run_rows<float>(a, stream);
+}
+
+}  // namespace pnq

@@ -181,4 +181,50 @@ cudaError_t launch_fp4_gemm(bool mx, const Fp4View& x, const Fp4View& w, int64_t
                             const float* w_global, bool bf16, void* Y, int* err, bool static_weights,
                             cudaStream_t stream);
 
+// ---- norms, 8-bit rows and their products, routing (layouts and definitions: include/pnq.h) ---------
+
+// Rows of elements, `ld` elements apart.
+struct RowsView {
+    const void* p;
+    int64_t ld;
+};
+
+// Rows of 8-bit codes, `ld` bytes apart, with a scale each.
+struct Int8View {
+    const int8_t* codes;
+    int64_t ld;
+    const float* scales;
+    int64_t rows;
+};
+
+// total, y, rstd: null where not wanted; codes and scales: both or neither.
+cudaError_t launch_rms_norm(bool bf16, const RowsView& x, const RowsView& residual, bool weight_bf16, const void* weight, float eps,
+                            int64_t rows, int64_t D, void* total, void* y, float* rstd, int8_t* codes, int64_t pitch, float* scales,
+                            cudaStream_t stream);
+// Rows of D partial sums that the weight's gradient goes through.
+int64_t rms_norm_backward_rows(int64_t rows, int64_t D);
+cudaError_t launch_rms_norm_backward(bool bf16, const RowsView& dy, const RowsView& total, bool weight_bf16, const void* weight,
+                                     const float* rstd, const RowsView& dtotal, int64_t rows, int64_t D, void* dx, float* dweight,
+                                     float* partial, cudaStream_t stream);
+
+cudaError_t launch_int8_quantize(bool bf16, const RowsView& x, int64_t rows, int64_t K, int8_t* codes, int64_t pitch, float* scales,
+                                 cudaStream_t stream);
+cudaError_t launch_int8_dequantize(const int8_t* codes, int64_t pitch, const float* scales, int64_t rows, int64_t K, bool bf16, void* out,
+                                   cudaStream_t stream);
+// Bytes of scratch that a product of M rows takes (w: its weights' layout).
+uint64_t int8_gemm_scratch(int64_t M, const Int8View& w, int64_t K);
+cudaError_t launch_int8_gemm(const Int8View& x, const Int8View& w, int64_t K, bool bf16, void* Y, void* scratch, int* err,
+                             cudaStream_t stream);
+
+// How experts are chosen and weighted.
+struct RouteRule {
+    int experts, slots, groups, top_groups, best;
+    bool sigmoid, renormalize;
+    float scale;
+};
+cudaError_t launch_expert_route(bool bf16, const RowsView& logits, int64_t tokens, const RouteRule& rule, const float* bias, int32_t* ids,
+                                float* weights, cudaStream_t stream);
+cudaError_t launch_expert_route_backward(bool bf16, const float* dweights, const RowsView& logits, const int32_t* ids, int64_t tokens,
+                                         const RouteRule& rule, void* dlogits, cudaStream_t stream);
+
 }  // namespace pnq

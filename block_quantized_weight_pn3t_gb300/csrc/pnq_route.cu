@@ -1,0 +1,540 @@
+// pnq_route.cu -- routing to experts: scores of a token's logits, its experts in order, their weights, and the gradient of the
+// logits (definitions in include/pnq.h). A warp takes a token; its scores stay in registers.
+//
+//   s = softmax(x) or 1 / (1 + exp(-x)), c = s + bias; of groups of experts the best by the sum of their largest c; then the
+//   largest c in turn, ties to the lowest index; weights s, over their sum where renormalised, times a scale.
+//
+// Which of two scores is the larger must not hang on a rounding. Without bias and groups the logits themselves are compared. Otherwise
+// c is computed in fp32 with a bound on its error (route_kernel), and a row in which two scores that decide anything are nearer than that,
+// and are not of equal logits and equal biases, is done again in 64 bits (a few rows in a thousand).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "pnq_device.cuh"
+#include "pnq_internal.h"
+
+namespace pnq {
+namespace {
+
+constexpr int kWarps = 4;          // tokens of a CTA
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kNone = -INFINITY;  // the score of an expert that is out
+
+struct RouteArgs {
+    const void* logits;
+    const float* bias;  // null: none
+    int32_t* ids;
+    float* weights;
+    int64_t ld, tokens;
+    int E, k, groups, per, top_groups, best;
+    uint32_t per_magic;  // e / per = e * per_magic >> 20 for e < 1024
+    float scale;
+    bool sigmoid, renormalize;
+};
+
+// Elements e(i) of a lane: V consecutive ones of every run of 32 V.
+template <int V>
+__device__ __forceinline__ int element(int i, int lane) {
+    return i / V * 32 * V + lane * V + i % V;
+}
+
+template <class T>
+__device__ __forceinline__ float load_one(const T* p);
+template <>
+__device__ __forceinline__ float load_one(const float* p) { return ld_l2(p); }
+template <>
+__device__ __forceinline__ float load_one(const __nv_bfloat16* p) {
+    return __uint_as_float(static_cast<uint32_t>(ld_l2(reinterpret_cast<const uint16_t*>(p))) << 16);
+}
+
+// Row x of E logits: what lies past E counts as -infinity.
+template <class T, int NE, int V>
+__device__ __forceinline__ void load_row(const T* row, int E, int lane, float (&x)[NE]) {
+#pragma unroll
+    for (int i = 0; i < NE; i += V) {
+        const int e = element<V>(i, lane);
+        if constexpr (V == 1) {
+            x[i] = e < E ? load_one(row + e) : kNone;
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[i + j] = kNone;
+            if (e < E) {
+                if constexpr (sizeof(T) == 4) {
+                    const uint4 w = ld_l2(reinterpret_cast<const uint4*>(row + e));
+                    x[i] = __uint_as_float(w.x), x[i + 1] = __uint_as_float(w.y), x[i + 2] = __uint_as_float(w.z), x[i + 3] = __uint_as_float(w.w);
+                } else {
+                    const uint2 w = ld_l2(reinterpret_cast<const uint2*>(row + e));
+                    x[i] = __uint_as_float(w.x << 16), x[i + 1] = __uint_as_float(w.x & 0xffff0000u);
+                    x[i + 2] = __uint_as_float(w.y << 16), x[i + 3] = __uint_as_float(w.y & 0xffff0000u);
+                }
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+    return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+    return v;
+}
+
+// Whole numbers in the order of the values (-0 as +0); 0 is below them all: an expert that is out.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return v == kNone ? 0u : b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return key == 0 ? kNone : __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// The row again in 64 bits. c: E doubles of shared memory of this warp; x: the row's logits there. Returns slots lane and lane + 32 of the
+// token's experts.
+__device__ __noinline__ int2 route_exact(const RouteArgs& a, const float* x, double* c, int lane) {
+    int2 id = make_int2(-1, -1);
+    double top = -INFINITY, sum = 0.0;
+    for (int e = lane; e < a.E; e += 32) top = fmax(top, static_cast<double>(x[e]));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, d));
+    for (int e = lane; e < a.E; e += 32) {
+        const double v = x[e];
+        c[e] = a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - top);
+        sum += c[e];
+    }
+    sum = a.sigmoid ? 1.0 : warp_sum(sum);
+    for (int e = lane; e < a.E; e += 32) {
+        const double b = a.bias ? static_cast<double>(ld_l2(a.bias + e)) : 0.0;
+        c[e] = x[e] == kNone ? -INFINITY : c[e] / sum + b;
+    }
+    __syncwarp();
+    if (a.groups > 1) {
+        double b1 = -INFINITY, b2 = -INFINITY;
+        if (lane < a.groups) {
+            for (int j = 0; j < a.per; ++j) {
+                const double v = c[lane * a.per + j];
+                if (v > b1) b2 = b1, b1 = v;
+                else if (v > b2) b2 = v;
+            }
+        }
+        const double score = a.best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+        int rank = 0;
+        for (int h = 0; h < a.groups; ++h) {
+            const double other = __shfl_sync(kAll, score, h);
+            rank += other > score || (other == score && h < lane);
+        }
+        const uint32_t kept = __ballot_sync(kAll, lane < a.groups && rank < a.top_groups);
+        for (int e = lane; e < a.E; e += 32)
+            if (!(kept >> (e / a.per) & 1)) c[e] = -INFINITY;
+        __syncwarp();
+    }
+    for (int j = 0; j < a.k; ++j) {
+        double v = -INFINITY;
+        int at = a.E;
+        for (int e = lane; e < a.E; e += 32)
+            if (c[e] > v) v = c[e], at = e;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            const double ov = __shfl_xor_sync(kAll, v, d);
+            const int oat = __shfl_xor_sync(kAll, at, d);
+            if (ov > v || (ov == v && oat < at)) v = ov, at = oat;
+        }
+        if (lane == (j & 31)) (j < 32 ? id.x : id.y) = at < a.E ? at : -1;
+        if (at < a.E && lane == (at & 31)) c[at] = -INFINITY;
+        __syncwarp();
+    }
+    return id;
+}
+
+// Shared memory of a warp: the row's logits, and behind them the groups' scores (each group on an odd pitch) or 64-bit scores.
+__host__ __device__ inline int route_floats(int E) { return E + (E & 1) + 2 * E + 32; }
+
+template <class T, int NE, int V>
+__global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
+    extern __shared__ __align__(16) float shared[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    float* xs = shared + warp * route_floats(a.E);
+    float* cs = xs + a.E + (a.E & 1);
+    griddep_begin();
+    if (t >= a.tokens) return;
+    float x[NE];
+    load_row<T, NE, V>(static_cast<const T*>(a.logits) + t * a.ld, a.E, lane, x);
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+        if (element<V>(i, lane) < a.E) xs[element<V>(i, lane)] = x[i];
+
+    // scores; a NaN, or an infinity that is not an expert taken out, makes the whole row NaN
+    float m = kNone, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) m = fmaxf(m, x[i]);
+    m = warp_max(m);
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) bad |= isnan(x[i]);
+    const bool by_logit = !a.bias && a.groups == 1;
+    float s[NE];
+    if (!a.sigmoid) {
+        bad |= m == INFINITY;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            s[i] = x[i] == kNone ? 0.0f : expf(x[i] - m);
+            sum += s[i];
+        }
+        sum = warp_sum(sum);
+        if (!by_logit) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) s[i] = s[i] / sum;
+        }
+    } else if (!by_logit) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) s[i] = sigmoid(x[i]);
+    }
+    uint32_t key[NE];
+    float cmax = 0.0f;
+    if (by_logit) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) key[i] = order_key(x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const int e = element<V>(i, lane);
+            float c = x[i] == kNone ? kNone : a.bias ? s[i] + ld_l2(a.bias + e) : s[i];
+            bad |= isnan(c) || c == INFINITY;
+            if (c != kNone) cmax = fmaxf(cmax, fabsf(c));
+            key[i] = order_key(c);
+        }
+        cmax = warp_max(cmax);
+    }
+    bad = __any_sync(kAll, bad);
+
+    int id[2] = {-1, -1};
+    if (bad) {
+        id[0] = lane, id[1] = lane + 32;
+    } else {
+        // How far two computed scores of different order may be apart. Sigmoid: expf is within 2 ulp and s (1 - s) <= 1/4, so s is within
+        // 3 * 2^-24, twice that for two. Softmax: an exponential is within 2^-22 of itself and its argument's rounding adds (m - x) 2^-24; the
+        // sum, E / 32 + 5 additions of such, is within 1.5 * 2^-19 and moves a difference by that times the larger score. The addition
+        // of the bias rounds by half an ulp of c.
+        const float smax = 1.0f / sum;  // softmax: the score of the largest logit
+        const float tol = (a.sigmoid ? 0x1p-21f : 0x1p-18f * smax + 0x1p-24f) + 0x1p-23f * cmax;
+        bool near = false;
+        if (a.groups > 1) {
+            const int pitch = a.per | 1;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                const int e = element<V>(i, lane), g = static_cast<int>(e * a.per_magic >> 20);
+                if (e < a.E) cs[g * pitch + e - g * a.per] = key_value(key[i]);
+            }
+            __syncwarp();
+            // the largest power of two of lanes that a group can have: its best two by them
+            const int lanes = 1 << (31 - __clz(32 / a.groups)), g = lane / lanes;
+            float b1 = kNone, b2 = kNone;
+            if (g < a.groups) {
+                for (int j = lane & (lanes - 1); j < a.per; j += lanes) {
+                    const float v = cs[g * pitch + j];
+                    b2 = fmaxf(b2, fminf(b1, v));
+                    b1 = fmaxf(b1, v);
+                }
+            }
+            for (int d = lanes >> 1; d; d >>= 1) {
+                const float o1 = __shfl_xor_sync(kAll, b1, d), o2 = __shfl_xor_sync(kAll, b2, d);
+                b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+                b1 = fmaxf(b1, o1);
+            }
+            const float score = a.best == 2 && b2 != kNone ? b1 + b2 : b1;
+            int rank = 0;
+            for (int h = 0; h < a.groups; ++h) {
+                const float other = __shfl_sync(kAll, score, h * lanes);
+                rank += other > score || (other == score && h < g);
+            }
+            const bool stays = g < a.groups && rank < a.top_groups;
+            const uint32_t kept = __ballot_sync(kAll, stays);
+            const float least = -warp_max(stays ? -score : kNone), most = warp_max(g < a.groups && !stays ? score : kNone);
+            near |= most != kNone && least - most <= 2.0f * tol + 0x1p-22f * cmax;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                const int e = element<V>(i, lane), of = static_cast<int>(e * a.per_magic >> 20);
+                if (e < a.E && !(kept >> (of * lanes) & 1)) key[i] = 0;
+            }
+        }
+        uint32_t mine = 0, won[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < NE; ++i) mine = max(mine, key[i]);
+        for (int j = 0; j < a.k; ++j) {
+            const uint32_t most = __reduce_max_sync(kAll, mine);
+            if (most == 0) break;  // no expert is left
+            int at = a.E;
+            if (mine == most) {
+#pragma unroll
+                for (int i = NE - 1; i >= 0; --i)
+                    if (key[i] == most) at = element<V>(i, lane);
+            }
+            const int e = static_cast<int>(__reduce_min_sync(kAll, static_cast<uint32_t>(at)));
+            if (at == e) {
+                mine = 0;
+#pragma unroll
+                for (int i = 0; i < NE; ++i) {
+                    if (element<V>(i, lane) == e) key[i] = 0;
+                    mine = max(mine, key[i]);
+                }
+            }
+            if (lane == j) id[0] = e, won[0] = most;
+            if (lane + 32 == j) id[1] = e, won[1] = most;
+        }
+        if (!by_logit) {
+            // neighbours in order, and the last against what is left: near, and not the same logit with the same bias
+            const uint32_t left = __reduce_max_sync(kAll, mine);
+            auto same = [&](int e, int f) { return xs[e] == xs[f] && (!a.bias || ld_l2(a.bias + e) == ld_l2(a.bias + f)); };
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = 32 * h + lane;
+                const uint32_t next = __shfl_sync(kAll, h == 0 && lane == 0 ? won[1] : won[h], (lane + 1) & 31);
+                const int next_id = __shfl_sync(kAll, h == 0 && lane == 0 ? id[1] : id[h], (lane + 1) & 31);
+                if (j + 1 < a.k && won[h] && next && key_value(won[h]) - key_value(next) <= tol) near |= !same(id[h], next_id);
+            }
+            const int last = a.k - 1;
+            const uint32_t final_key = __shfl_sync(kAll, last < 32 ? won[0] : won[1], last & 31);
+            const int final_id = __shfl_sync(kAll, last < 32 ? id[0] : id[1], last & 31);
+            if (final_key && left && key_value(final_key) - key_value(left) <= tol) {
+#pragma unroll
+                for (int i = 0; i < NE; ++i)
+                    if (key[i] && key_value(final_key) - key_value(key[i]) <= tol) near |= !same(element<V>(i, lane), final_id);
+            }
+        }
+        __syncwarp();
+        if (__any_sync(kAll, near)) {
+            const int2 again = route_exact(a, xs, reinterpret_cast<double*>(cs), lane);
+            id[0] = again.x, id[1] = again.y;
+        }
+    }
+
+    // weights: of chosen experts alone where renormalised, by their largest logit (so that no sum of theirs is too small to divide by)
+    __syncwarp();
+    float w[2], z[2], mc = kNone;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const bool has = 32 * h + lane < a.k && id[h] >= 0;
+        if (!has) id[h] = -1;
+        z[h] = has ? xs[id[h]] : kNone;
+        mc = fmaxf(mc, z[h]);
+    }
+    mc = warp_max(mc);
+    float total = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        w[h] = 0.0f;
+        if (id[h] >= 0) {
+            if (a.sigmoid) w[h] = a.renormalize && mc < -60.0f ? expf(z[h] - mc) : sigmoid(z[h]);
+            else w[h] = a.renormalize ? expf(z[h] - mc) : expf(z[h] - m) / sum;
+        }
+        total += w[h];
+    }
+    if (a.renormalize) total = warp_sum(total);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (32 * h + lane >= a.k) continue;
+        const int64_t at = t * a.k + 32 * h + lane;
+        float v = a.scale * w[h];
+        if (a.renormalize && id[h] >= 0) v /= total;
+        a.ids[at] = id[h];
+        a.weights[at] = bad ? __uint_as_float(0x7fc00000u) : v;
+    }
+}
+
+// ---- gradient -------------------------------------------------------------------------------------------
+
+struct RouteBackwardArgs {
+    const float* dweights;
+    const void* logits;
+    const int32_t* ids;
+    void* dlogits;
+    int64_t ld, tokens;
+    int E, k;
+    float scale;
+    bool sigmoid, renormalize;
+};
+
+// dlogits of a token by a warp. Renormalised weights hang on the chosen logits alone: r = their shares, softmax scale r (dw - <dw, r>),
+// sigmoid times 1 - s besides; the rest is zeros. Sigmoid: scale dw s (1 - s). Softmax: s (g - <g, s>) over the row, g = scale dw at the
+// chosen. An expert named twice gets both, in slot order.
+template <class T, int NE, int V>
+__global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const RouteBackwardArgs a) {
+    extern __shared__ __align__(16) float shared[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    float* g = shared + warp * a.E;
+    griddep_begin();
+    if (t >= a.tokens) return;
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    const bool whole = !a.sigmoid && !a.renormalize;
+    float x[NE];
+    if (whole) load_row<T, NE, V>(row, a.E, lane, x);
+    int id[2];
+    float dw[2], z[2], q[2], mc = kNone;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int j = 32 * h + lane;
+        id[h] = j < a.k ? plan_index(ld_l2(a.ids + t * a.k + j), a.E) : -1;
+        dw[h] = id[h] >= 0 ? ld_l2(a.dweights + t * a.k + j) : 0.0f;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        z[h] = id[h] >= 0 ? load_one(row + id[h]) : kNone;
+        mc = fmaxf(mc, z[h]);
+    }
+    for (int e = lane; e < a.E; e += 32) g[e] = 0.0f;
+    __syncwarp();
+    if (a.renormalize) {
+        mc = warp_max(mc);
+        float total = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            q[h] = 0.0f;
+            if (id[h] >= 0) q[h] = a.sigmoid && !(mc < -60.0f) ? sigmoid(z[h]) : expf(z[h] - mc);
+            total += q[h];
+        }
+        total = warp_sum(total);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (id[h] >= 0) q[h] /= total;
+            dot = fmaf(q[h], dw[h], dot);
+        }
+        dot = warp_sum(dot);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            q[h] = a.scale * q[h] * (dw[h] - dot);
+            if (a.sigmoid && id[h] >= 0) q[h] *= sigmoid(-z[h]);
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            q[h] = a.scale * dw[h];
+            if (a.sigmoid && id[h] >= 0) q[h] *= sigmoid(z[h]) * sigmoid(-z[h]);
+        }
+    }
+    for (int j = 0; j < a.k; ++j) {
+        const int e = __shfl_sync(kAll, j < 32 ? id[0] : id[1], j & 31);
+        const float v = __shfl_sync(kAll, j < 32 ? q[0] : q[1], j & 31);
+        if (e >= 0 && lane == (e & 31)) g[e] += v;
+    }
+    __syncwarp();
+    float out[NE];
+    if (whole) {
+        float m = kNone, sum = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) m = fmaxf(m, x[i]);
+        m = warp_max(m);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            x[i] = x[i] == kNone ? 0.0f : expf(x[i] - m);
+            sum += x[i];
+        }
+        sum = warp_sum(sum);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const int e = element<V>(i, lane);
+            x[i] = m == kNone ? 0.0f : x[i] / sum;  // no expert at all: zeros
+            out[i] = e < a.E ? g[e] : 0.0f;
+            dot = fmaf(x[i], out[i], dot);
+        }
+        dot = warp_sum(dot);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) out[i] = x[i] * (out[i] - dot);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) out[i] = element<V>(i, lane) < a.E ? g[element<V>(i, lane)] : 0.0f;
+    }
+    T* to = static_cast<T*>(a.dlogits) + t * a.E;
+#pragma unroll
+    for (int i = 0; i < NE; i += V) {
+        const int e = element<V>(i, lane);
+        if (e >= a.E) continue;
+        if constexpr (V == 1) to[e] = T(out[i]);
+        else if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(to + e) = make_float4(out[i], out[i + 1], out[i + 2], out[i + 3]);
+        else *reinterpret_cast<uint2*>(to + e) = make_uint2(f32x2_to_bf16x2(out[i], out[i + 1]), f32x2_to_bf16x2(out[i + 2], out[i + 3]));
+    }
+}
+
+template <class Kernel, class Args>
+cudaError_t launch_rows(Kernel kernel, const Args& a, int floats, cudaStream_t stream) {
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(static_cast<unsigned>((a.tokens + kWarps - 1) / kWarps));
+    lc.blockDim = dim3(32 * kWarps);
+    lc.dynamicSmemBytes = static_cast<size_t>(kWarps) * floats * 4;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    if (lc.dynamicSmemBytes > 48 * 1024) {
+        const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(lc.dynamicSmemBytes));
+        if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&lc, kernel, a);
+}
+
+// go(elements a lane, elements an access) with both as types: the fewest registers that hold a row.
+template <class F>
+cudaError_t by_experts(int E, bool wide, F&& go) {
+    auto with = [&](auto v) {
+        if (E <= 128) return go(std::integral_constant<int, 4>{}, v);
+        if (E <= 256) return go(std::integral_constant<int, 8>{}, v);
+        if (E <= 512) return go(std::integral_constant<int, 16>{}, v);
+        return go(std::integral_constant<int, 32>{}, v);
+    };
+    return wide ? with(std::integral_constant<int, 4>{}) : with(std::integral_constant<int, 1>{});
+}
+
+bool aligned4(const void* p, int64_t ld, int E, bool bf16) {
+    return E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (bf16 ? 8 : 16) == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_expert_route(bool bf16, const RowsView& logits, int64_t tokens, const RouteRule& rule, const float* bias, int32_t* ids,
+                                float* weights, cudaStream_t stream) {
+    RouteArgs a{};
+    a.logits = logits.p, a.ld = logits.ld, a.tokens = tokens;
+    a.bias = bias, a.ids = ids, a.weights = weights;
+    a.E = rule.experts, a.k = rule.slots, a.groups = rule.groups, a.per = rule.experts / rule.groups;
+    a.top_groups = rule.top_groups, a.best = rule.best;
+    a.per_magic = static_cast<uint32_t>(((1 << 20) + a.per - 1) / a.per);
+    a.scale = rule.scale, a.sigmoid = rule.sigmoid, a.renormalize = rule.renormalize;
+    return by_experts(a.E, aligned4(logits.p, logits.ld, a.E, bf16), [&](auto n, auto v) {
+        constexpr int NE = decltype(n)::value, V = decltype(v)::value;
+        return bf16 ? launch_rows(route_kernel<__nv_bfloat16, NE, V>, a, route_floats(a.E), stream)
+                    : launch_rows(route_kernel<float, NE, V>, a, route_floats(a.E), stream);
+    });
+}
+
+cudaError_t launch_expert_route_backward(bool bf16, const float* dweights, const RowsView& logits, const int32_t* ids, int64_t tokens,
+                                         const RouteRule& rule, void* dlogits, cudaStream_t stream) {
+    RouteBackwardArgs a{};
+    a.dweights = dweights, a.logits = logits.p, a.ld = logits.ld, a.ids = ids, a.dlogits = dlogits, a.tokens = tokens;
+    a.E = rule.experts, a.k = rule.slots;
+    a.scale = rule.scale, a.sigmoid = rule.sigmoid, a.renormalize = rule.renormalize;
+    const bool wide = aligned4(logits.p, logits.ld, a.E, bf16) && aligned4(dlogits, a.E, a.E, bf16);
+    return by_experts(a.E, wide, [&](auto n, auto v) {
+        constexpr int NE = decltype(n)::value, V = decltype(v)::value;
+        return bf16 ? launch_rows(route_backward_kernel<__nv_bfloat16, NE, V>, a, a.E, stream)
+                    : launch_rows(route_backward_kernel<float, NE, V>, a, a.E, stream);
+    });
+}
+
+}  // namespace pnq

@@ -825,6 +825,344 @@ PNQ_ENTRY(expert_combine_backward) {
     });
 }
 
+// ---- routing ------------------------------------------------------------------------------------------------
+
+// Rows of a CUDA matrix whose elements are consecutive: its row stride (rows of one or none: its columns).
+int64_t row_stride(const at::Tensor& t, const char* what) {
+    if (t.dim() != 2) refuse(std::string(what) + " must be a torch.Tensor [rows][columns]");
+    if (!t.is_cuda()) refuse(std::string(what) + " must be a CUDA tensor");
+    if (t.size(1) > 1 && t.size(0) > 0 && t.stride(1) != 1) refuse("the elements of a row of " + std::string(what) + " must be consecutive");
+    const int64_t ld = t.size(0) <= 1 ? t.size(1) : t.stride(0);
+    if (ld < t.size(1))
+        refuse("rows of " + std::string(what) + " are " + std::to_string(ld) + " elements apart; at least " + std::to_string(t.size(1)) + " is wanted");
+    return ld;
+}
+
+bool to_bool(PyObject* o, bool otherwise) {
+    if (!o) return otherwise;
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw PythonError{};
+    return v != 0;
+}
+
+int32_t to_int32(PyObject* o, int32_t otherwise, const char* what) {
+    if (!o) return otherwise;
+    const int64_t v = to_int(o);
+    if (v < INT32_MIN || v > INT32_MAX) refuse(std::string(what) + " = " + std::to_string(v) + " is out of range", PNQ_ERR_SHAPE);
+    return static_cast<int32_t>(v);
+}
+
+// The rule of a call; refuses what the library would, with the numbers in the text.
+pnq_route_rule route_rule(int64_t experts, int64_t slots, PyObject* score, PyObject* groups, PyObject* top_groups, PyObject* best,
+                          PyObject* renormalize, PyObject* scale) {
+    if (experts < 1 || experts > 1024) refuse(std::to_string(experts) + " experts; 1..1024 are wanted", PNQ_ERR_SHAPE);
+    pnq_route_rule r{};
+    r.experts = static_cast<int32_t>(experts);
+    r.score = to_int32(score, PNQ_SOFTMAX, "score");
+    if (r.score != PNQ_SOFTMAX && r.score != PNQ_SIGMOID) refuse("score is neither SOFTMAX nor SIGMOID", PNQ_ERR_TYPE);
+    r.groups = to_int32(groups, 1, "groups");
+    if (r.groups < 1 || r.groups > 32 || r.experts % r.groups)
+        refuse(std::to_string(r.groups) + " groups of " + std::to_string(experts) + " experts; 1..32 equal ones are wanted", PNQ_ERR_SHAPE);
+    r.top_groups = to_int32(top_groups, r.groups, "top_groups");
+    if (r.top_groups < 1 || r.top_groups > r.groups)
+        refuse("top_groups = " + std::to_string(r.top_groups) + " of " + std::to_string(r.groups) + " groups", PNQ_ERR_SHAPE);
+    r.best = to_int32(best, 1, "best");
+    if (r.best < 1 || r.best > 2) refuse("best = " + std::to_string(r.best) + "; 1 or 2 is wanted", PNQ_ERR_SHAPE);
+    if (slots < 1 || slots > 64 || slots > r.experts / r.groups * r.top_groups)
+        refuse(std::to_string(slots) + " slots; 1..64 and at most the " + std::to_string(r.experts / r.groups * r.top_groups) +
+                   " experts of the groups that stay are wanted",
+               PNQ_ERR_SHAPE);
+    r.slots = static_cast<int32_t>(slots);
+    r.renormalize = to_bool(renormalize, false);
+    r.scale = scale ? static_cast<float>(to_double(scale)) : 1.0f;
+    return r;
+}
+
+// `out` as a contiguous CUDA matrix of that dtype and shape, or a new one.
+at::Tensor matrix_out(PyObject* out, const char* what, int64_t rows, int64_t cols, at::ScalarType dtype, int device) {
+    if (!out) return new_matrix(rows, cols, dtype, device);
+    const at::Tensor& t = tensor(out, what);
+    require_matrix(t, what, dtype, rows, cols, device);
+    return t;
+}
+
+// The same of one dimension.
+void require_vector(const at::Tensor& t, const char* what, at::ScalarType dtype, int64_t n, int device) {
+    if (t.dim() != 1 || t.size(0) != n)
+        refuse(std::string(what) + " has shape " + shape_text(t.sizes()) + "; expected (" + std::to_string(n) + ",)");
+    require(t, what, dtype, 0);
+    require_device(t, what, device);
+}
+at::Tensor vector_out(PyObject* out, const char* what, int64_t n, at::ScalarType dtype, int device) {
+    if (!out) return new_tensor({n}, dtype, device);
+    const at::Tensor& t = tensor(out, what);
+    require_vector(t, what, dtype, n, device);
+    return t;
+}
+
+PNQ_ENTRY(expert_route) {
+    return entry([&]() -> PyObject* {
+        static const char* const names[] = {"logits", "slots", "score", "bias", "groups", "top_groups", "best", "renormalize", "scale",
+                                            "ids", "weights", "stream"};
+        const Args<12> a("expert_route", names, 2, args, nargs, kwnames);
+        const at::Tensor& logits = tensor(a[0], "logits");
+        const int type = float_type(logits.scalar_type(), "logits");
+        const int64_t ld = row_stride(logits, "logits"), tokens = logits.size(0), experts = logits.size(1);
+        const pnq_route_rule rule = route_rule(experts, to_int(a[1]), a[2], a[4], a[5], a[6], a[7], a[8]);
+        const int device = logits.get_device();
+        at::Tensor bias;
+        if (a[3]) {
+            bias = tensor(a[3], "bias");
+            require_vector(bias, "bias", at::kFloat, experts, device);
+        }
+        const Place place(a[11], device);
+        at::Tensor ids = matrix_out(a[9], "ids", tokens, rule.slots, at::kInt, device);
+        at::Tensor weights = matrix_out(a[10], "weights", tokens, rule.slots, at::kFloat, device);
+        place.record(logits, bias, ids, weights);
+        check(pnq_expert_route(type, logits.data_ptr(), ld, tokens, &rule, bias.defined() ? bias.data_ptr<float>() : nullptr,
+                               ids.data_ptr<int32_t>(), weights.data_ptr<float>(), place.stream()),
+              "pnq_expert_route");
+        Owned first{returned(a[9], ids)}, second{returned(a[10], weights)};
+        return PyTuple_Pack(2, first.o, second.o);
+    });
+}
+
+PNQ_ENTRY(expert_route_backward) {
+    return entry([&]() -> PyObject* {
+        static const char* const names[] = {"dweights", "logits", "ids", "score", "renormalize", "scale", "out", "stream"};
+        const Args<8> a("expert_route_backward", names, 3, args, nargs, kwnames);
+        const at::Tensor &dweights = tensor(a[0], "dweights"), &logits = tensor(a[1], "logits"), &ids = tensor(a[2], "ids");
+        const int type = float_type(logits.scalar_type(), "logits");
+        const int64_t ld = row_stride(logits, "logits"), tokens = logits.size(0), experts = logits.size(1);
+        if (ids.dim() != 2) refuse("ids must be a torch.Tensor [tokens][slots]");
+        const pnq_route_rule rule = route_rule(experts, ids.size(1), a[3], nullptr, nullptr, nullptr, a[4], a[5]);
+        const int device = logits.get_device();
+        require_matrix(ids, "ids", at::kInt, tokens, rule.slots, device);
+        require_matrix(dweights, "dweights", at::kFloat, tokens, rule.slots, device);
+        const Place place(a[7], device);
+        at::Tensor t = matrix_out(a[6], "out", tokens, experts, logits.scalar_type(), device);
+        place.record(dweights, logits, ids, t);
+        check(pnq_expert_route_backward(type, dweights.data_ptr<float>(), logits.data_ptr(), ld, ids.data_ptr<int32_t>(), tokens, &rule,
+                                        t.data_ptr(), place.stream()),
+              "pnq_expert_route_backward");
+        return returned(a[6], t);
+    });
+}
+
+// ---- norms and 8-bit rows -----------------------------------------------------------------------------------
+
+// Rows of 8-bit codes: a CUDA int8 matrix whose rows have consecutive elements.
+int64_t code_rows(const at::Tensor& t, const char* what) {
+    if (t.scalar_type() != at::kChar)
+        refuse(std::string(what) + " has dtype " + at::toString(t.scalar_type()) + "; expected " + at::toString(at::kChar));
+    return row_stride(t, what);
+}
+
+// Where a call writes codes: `out`, whose rows are on 16 bytes, or a new [rows][K] view of rows padded to 16 bytes.
+struct Codes {
+    at::Tensor t;
+    int64_t pitch;
+};
+Codes codes_out(PyObject* out, int64_t rows, int64_t K, int device) {
+    if (!out) {
+        const int64_t pitch = (K + 15) / 16 * 16;
+        if (pitch == K) return {new_matrix(rows, K, at::kChar, device), pitch};
+        at::Tensor whole = new_matrix(rows, pitch, at::kChar, device);
+        auto impl = c10::make_intrusive<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+        const int64_t sizes[] = {rows, K}, strides[] = {pitch, 1};
+        impl->set_sizes_and_strides(sizes, strides);
+        return {at::Tensor(std::move(impl)), pitch};
+    }
+    const at::Tensor& t = tensor(out, "codes");
+    if (t.dim() != 2 || t.size(0) != rows || t.size(1) != K)
+        refuse("codes have shape " + shape_text(t.sizes()) + "; expected (" + std::to_string(rows) + ", " + std::to_string(K) + ")");
+    int64_t pitch = code_rows(t, "codes");
+    require_device(t, "codes", device);
+    if (rows <= 1) pitch = (K + 15) / 16 * 16;  // the one row's pitch is not used
+    if (pitch % 16 || reinterpret_cast<uintptr_t>(t.data_ptr()) % 16) refuse("rows of codes must start on 16 bytes", PNQ_ERR_ALIGN);
+    return {t, pitch};
+}
+
+// x, weight, eps, residual of a norm.
+struct NormInputs {
+    at::Tensor x, weight, residual;
+    int type, weight_type, device;
+    int64_t ldx, ldr, rows, D;
+    float eps;
+};
+NormInputs norm_inputs(PyObject* x, PyObject* weight, PyObject* eps, PyObject* residual) {
+    NormInputs n{tensor(x, "x"), tensor(weight, "weight"), {}, 0, 0, 0, 0, 0, 0, 0, 1e-6f};
+    n.type = float_type(n.x.scalar_type(), "x");
+    n.weight_type = float_type(n.weight.scalar_type(), "weight");
+    n.ldx = row_stride(n.x, "x");
+    n.rows = n.x.size(0), n.D = n.x.size(1);
+    if (n.D < 1) refuse("rows of no elements have no norm", PNQ_ERR_SHAPE);
+    n.device = n.x.get_device();
+    require_vector(n.weight, "weight", n.weight.scalar_type(), n.D, n.device);
+    if (eps) n.eps = static_cast<float>(to_double(eps));
+    if (residual) {
+        n.residual = tensor(residual, "residual");
+        if (n.residual.scalar_type() != n.x.scalar_type() || n.residual.sizes() != n.x.sizes())
+            refuse("residual has another shape or dtype than x");
+        n.ldr = row_stride(n.residual, "residual");
+        require_device(n.residual, "residual", n.device);
+    }
+    return n;
+}
+
+// The total of a norm: x itself where there is no residual, else `out` (which may be the residual itself) or a new tensor.
+at::Tensor total_of(const NormInputs& n, PyObject* out) {
+    if (!n.residual.defined()) {
+        if (out) refuse("total is x where there is no residual");
+        return n.x;
+    }
+    return matrix_out(out, "total", n.rows, n.D, n.x.scalar_type(), n.device);
+}
+
+PNQ_ENTRY(rms_norm) {
+    return entry([&]() -> PyObject* {
+        static const char* const names[] = {"x", "weight", "eps", "residual", "out", "total", "stream"};
+        const Args<7> a("rms_norm", names, 2, args, nargs, kwnames);
+        const NormInputs n = norm_inputs(a[0], a[1], a[2], a[3]);
+        const Place place(a[6], n.device);
+        at::Tensor total = total_of(n, a[5]);
+        at::Tensor y = matrix_out(a[4], "out", n.rows, n.D, n.x.scalar_type(), n.device);
+        at::Tensor rstd = new_tensor({n.rows}, at::kFloat, n.device);
+        place.record(n.x, n.weight, n.residual, total, y, rstd);
+        const bool added = n.residual.defined();
+        check(pnq_rms_norm(n.type, n.x.data_ptr(), n.ldx, added ? n.residual.data_ptr() : nullptr, n.ldr, n.rows, n.D, n.weight_type,
+                           n.weight.data_ptr(), n.eps, added ? total.data_ptr() : nullptr, y.data_ptr(), rstd.data_ptr<float>(), nullptr, 0,
+                           nullptr, place.stream()),
+              "pnq_rms_norm");
+        Owned first{returned(a[4], y)}, second{added ? returned(a[5], total) : Py_NewRef(a[0])}, third{wrap(std::move(rstd))};
+        return PyTuple_Pack(3, first.o, second.o, third.o);
+    });
+}
+
+PNQ_ENTRY(rms_norm_int8) {
+    return entry([&]() -> PyObject* {
+        static const char* const names[] = {"x", "weight", "eps", "residual", "y", "codes", "scales", "total", "stream"};
+        const Args<9> a("rms_norm_int8", names, 2, args, nargs, kwnames);
+        const NormInputs n = norm_inputs(a[0], a[1], a[2], a[3]);
+        const Place place(a[8], n.device);
+        at::Tensor total = total_of(n, a[7]), y;
+        if (a[4]) y = matrix_out(a[4], "y", n.rows, n.D, n.x.scalar_type(), n.device);
+        Codes codes = codes_out(a[5], n.rows, n.D, n.device);
+        at::Tensor scales = vector_out(a[6], "scales", n.rows, at::kFloat, n.device);
+        place.record(n.x, n.weight, n.residual, total, y, codes.t, scales);
+        const bool added = n.residual.defined();
+        check(pnq_rms_norm(n.type, n.x.data_ptr(), n.ldx, added ? n.residual.data_ptr() : nullptr, n.ldr, n.rows, n.D, n.weight_type,
+                           n.weight.data_ptr(), n.eps, added ? total.data_ptr() : nullptr, y.defined() ? y.data_ptr() : nullptr, nullptr,
+                           codes.t.data_ptr<int8_t>(), codes.pitch, scales.data_ptr<float>(), place.stream()),
+              "pnq_rms_norm");
+        Owned first{returned(a[5], codes.t)}, second{returned(a[6], scales)}, third{added ? returned(a[7], total) : Py_NewRef(a[0])};
+        return PyTuple_Pack(3, first.o, second.o, third.o);
+    });
+}
+
+PNQ_ENTRY(rms_norm_backward) {
+    return entry([&]() -> PyObject* {
+        static const char* const names[] = {"dy", "total", "weight", "rstd", "dtotal", "out", "dweight", "stream"};
+        const Args<8> a("rms_norm_backward", names, 4, args, nargs, kwnames);
+        const NormInputs n = norm_inputs(a[1], a[2], nullptr, nullptr);
+        const at::Tensor &dy = tensor(a[0], "dy"), &rstd = tensor(a[3], "rstd");
+        auto like = [&](const at::Tensor& t, const char* what) {
+            if (t.scalar_type() != n.x.scalar_type() || t.sizes() != n.x.sizes()) refuse(std::string(what) + " has another shape or dtype than total");
+            const int64_t ld = row_stride(t, what);
+            require_device(t, what, n.device);
+            return ld;
+        };
+        const int64_t ldy = like(dy, "dy");
+        require_vector(rstd, "rstd", at::kFloat, n.rows, n.device);
+        at::Tensor dtotal;
+        int64_t ldd = 0;
+        if (a[4]) {
+            dtotal = tensor(a[4], "dtotal");
+            ldd = like(dtotal, "dtotal");
+        }
+        const Place place(a[7], n.device);
+        at::Tensor dx = matrix_out(a[5], "out", n.rows, n.D, n.x.scalar_type(), n.device);
+        at::Tensor dweight = vector_out(a[6], "dweight", n.D, at::kFloat, n.device);
+        uint64_t bytes = 0;
+        check(pnq_rms_norm_backward_scratch_bytes(n.rows, n.D, &bytes), "pnq_rms_norm_backward_scratch_bytes");
+        at::Tensor scratch = new_tensor({static_cast<int64_t>(bytes)}, at::kByte, n.device);
+        place.record(dy, n.x, n.weight, rstd, dtotal, dx, dweight);
+        check(pnq_rms_norm_backward(n.type, dy.data_ptr(), ldy, n.x.data_ptr(), n.ldx, n.weight_type, n.weight.data_ptr(),
+                                    rstd.data_ptr<float>(), dtotal.defined() ? dtotal.data_ptr() : nullptr, ldd, n.rows, n.D, dx.data_ptr(),
+                                    dweight.data_ptr<float>(), scratch.data_ptr(), bytes, place.stream()),
+              "pnq_rms_norm_backward");
+        Owned first{returned(a[5], dx)}, second{returned(a[6], dweight)};
+        return PyTuple_Pack(2, first.o, second.o);
+    });
+}
+
+PNQ_ENTRY(int8_quantize) {
+    return entry([&]() -> PyObject* {
+        static const char* const names[] = {"x", "codes", "scales", "stream"};
+        const Args<4> a("int8_quantize", names, 1, args, nargs, kwnames);
+        const at::Tensor& x = tensor(a[0], "x");
+        const int type = float_type(x.scalar_type(), "x");
+        const int64_t ldx = row_stride(x, "x"), rows = x.size(0), K = x.size(1);
+        if (K < 1) refuse("rows of no elements have no scale", PNQ_ERR_SHAPE);
+        const int device = x.get_device();
+        const Place place(a[3], device);
+        Codes codes = codes_out(a[1], rows, K, device);
+        at::Tensor scales = vector_out(a[2], "scales", rows, at::kFloat, device);
+        place.record(x, codes.t, scales);
+        check(pnq_int8_quantize(type, x.data_ptr(), ldx, rows, K, codes.t.data_ptr<int8_t>(), codes.pitch, scales.data_ptr<float>(),
+                                place.stream()),
+              "pnq_int8_quantize");
+        Owned first{returned(a[1], codes.t)}, second{returned(a[2], scales)};
+        return PyTuple_Pack(2, first.o, second.o);
+    });
+}
+
+PNQ_ENTRY(int8_dequantize) {
+    return entry([&]() -> PyObject* {
+        static const char* const names[] = {"codes", "scales", "dtype", "out", "stream"};
+        const Args<5> a("int8_dequantize", names, 2, args, nargs, kwnames);
+        const at::Tensor &codes = tensor(a[0], "codes"), &scales = tensor(a[1], "scales");
+        const int64_t pitch = code_rows(codes, "codes"), rows = codes.size(0), K = codes.size(1);
+        if (K < 1) refuse("rows of no codes", PNQ_ERR_SHAPE);
+        const int device = codes.get_device();
+        require_vector(scales, "scales", at::kFloat, rows, device);
+        const Place place(a[4], device);
+        int type = 0;
+        at::Tensor t = result(a[3], rows, K, dtype_of(a[2], at::kFloat), device, &type);
+        place.record(codes, scales, t);
+        check(pnq_int8_dequantize(codes.data_ptr<int8_t>(), pitch, scales.data_ptr<float>(), rows, K, type, t.data_ptr(), place.stream()),
+              "pnq_int8_dequantize");
+        return returned(a[3], t);
+    });
+}
+
+PNQ_ENTRY(int8_gemm) {
+    return entry([&]() -> PyObject* {
+        static const char* const names[] = {"x", "x_scales", "w", "w_scales", "dtype", "out", "stream"};
+        const Args<7> a("int8_gemm", names, 4, args, nargs, kwnames);
+        const at::Tensor &x = tensor(a[0], "x"), &xs = tensor(a[1], "x_scales"), &w = tensor(a[2], "w"), &ws = tensor(a[3], "w_scales");
+        const int64_t ldx = code_rows(x, "x"), ldw = code_rows(w, "w"), M = x.size(0), N = w.size(0), K = x.size(1);
+        if (w.size(1) != K)
+            refuse("operands differ: K = " + std::to_string(K) + " and K = " + std::to_string(w.size(1)));
+        if (K < 1 || K > 131071) refuse("K = " + std::to_string(K) + "; 1..131071 is wanted (sums of 32 bits)", PNQ_ERR_SHAPE);
+        const int device = x.get_device();
+        require_device(w, "w", device);
+        require_vector(xs, "x_scales", at::kFloat, M, device);
+        require_vector(ws, "w_scales", at::kFloat, N, device);
+        const Place place(a[6], device);
+        int type = 0;
+        at::Tensor t = result(a[5], M, N, dtype_of(a[4], at::kFloat), device, &type), scratch;
+        uint64_t bytes = 0;
+        check(pnq_int8_gemm_scratch_bytes(M, w.data_ptr<int8_t>(), ldw, N, K, &bytes), "pnq_int8_gemm_scratch_bytes");
+        if (bytes) scratch = new_tensor({static_cast<int64_t>(bytes)}, at::kByte, device);
+        place.record(x, xs, w, ws, t);
+        check(pnq_int8_gemm(x.data_ptr<int8_t>(), ldx, xs.data_ptr<float>(), M, w.data_ptr<int8_t>(), ldw, ws.data_ptr<float>(), N, K, type,
+                            t.data_ptr(), bytes ? scratch.data_ptr() : nullptr, bytes, place.stream()),
+              "pnq_int8_gemm");
+        return returned(a[5], t);
+    });
+}
+
 // ---- the module -------------------------------------------------------------------------------------------------
 
 #define PNQ_METHOD(name, doc) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL | METH_KEYWORDS, doc}
@@ -863,6 +1201,36 @@ PyMethodDef methods[] = {
                                "those of ys and weights."),
     PNQ_METHOD(expert_combine_backward, "expert_combine_backward(dy, ys, plan, weights, out=None, dweights=None, stream=None)\n--\n\n"
                                         "Gradients of expert_combine: (dys [tokens * slots][D], dweights fp32 [tokens][slots])."),
+    PNQ_METHOD(expert_route, "expert_route(logits, slots, score=SOFTMAX, bias=None, groups=1, top_groups=groups, best=1, renormalize=False,\n"
+                             "             scale=1.0, ids=None, weights=None, stream=None)\n--\n\n"
+                             "Each token's experts (int32 [tokens][slots], for expert_sort) and their weights (fp32, for expert_combine) from\n"
+                             "its logits (fp32 or bf16 [tokens][experts]): scores by SOFTMAX or SIGMOID, choice by score + bias (fp32\n"
+                             "[experts]) among the top_groups of `groups` equal groups (a group's score: the sum of its `best` largest),\n"
+                             "ties to the lowest index; weights scale * score, over their sum with renormalize. An expert of logit\n"
+                             "-infinity is out; a slot without an expert is -1 with the weight 0; a NaN makes its token's weights NaN.\n"
+                             "Outside autograd: expert_route_backward gives the logits' gradient."),
+    PNQ_METHOD(expert_route_backward, "expert_route_backward(dweights, logits, ids, score=SOFTMAX, renormalize=False, scale=1.0, out=None,\n"
+                                      "                      stream=None)\n--\n\n"
+                                      "Gradient of expert_route's weights: dlogits [tokens][experts] in the logits' type. The choice has none."),
+    PNQ_METHOD(rms_norm, "rms_norm(x, weight, eps=1e-6, residual=None, out=None, total=None, stream=None)\n--\n\n"
+                         "(y, total, rstd): total = x + residual (x itself without a residual), rstd = 1 / sqrt(mean(total^2) + eps),\n"
+                         "y = total * rstd * weight. x, residual: fp32 or bf16 [rows][D], rows may be strided; weight: fp32 or bf16 [D].\n"
+                         "total=residual adds in place, out=x overwrites x. Outside autograd: rms_norm_backward gives the gradients."),
+    PNQ_METHOD(rms_norm_int8, "rms_norm_int8(x, weight, eps=1e-6, residual=None, y=None, codes=None, scales=None, total=None, stream=None)\n--\n\n"
+                              "(codes, scales, total): the norm as 8-bit codes (int8 [rows][D], rows padded to 16 bytes) with a scale per\n"
+                              "row, for int8_gemm. y: a [rows][D] tensor that takes the norm itself too (for a router, say)."),
+    PNQ_METHOD(rms_norm_backward, "rms_norm_backward(dy, total, weight, rstd, dtotal=None, out=None, dweight=None, stream=None)\n--\n\n"
+                                  "Gradients of rms_norm: (dx, dweight); dx is the residual's gradient too. dtotal: the gradient that\n"
+                                  "reaches the total from elsewhere, added to dx. dweight is fp32."),
+    PNQ_METHOD(int8_quantize, "int8_quantize(x, codes=None, scales=None, stream=None)\n--\n\n"
+                              "(codes, scales) of rows (fp32 or bf16 [rows][K], rows may be strided): scale = max |x| / 127, code = the whole\n"
+                              "number nearest to 127 x / max |x|. Activations, and weights once (a scale per output channel)."),
+    PNQ_METHOD(int8_dequantize, "int8_dequantize(codes, scales, dtype=torch.float32, out=None, stream=None)\n--\n\n"
+                                "codes * scales, fp32 or bf16 [rows][K]."),
+    PNQ_METHOD(int8_gemm, "int8_gemm(x, x_scales, w, w_scales, dtype=torch.float32, out=None, stream=None)\n--\n\n"
+                          "Y[m][n] = (sum_k x[m][k] w[n][k]) x_scales[m] w_scales[n] of int8 matrices [M][K] and [N][K] (rows may be\n"
+                          "strided; those of w on 16 bytes, as int8_quantize makes them, are faster), the sum exact; fp32 or bf16\n"
+                          "[M][N]. There is no gradient of it: operands are codes."),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "Torch wrappers of the 4-bit operands and the expert layer.", -1, methods};

@@ -432,6 +432,107 @@ int pnq_expert_combine(int type, const void* YS, int64_t D, const pnq_expert_pla
 int pnq_expert_combine_backward(int type, const void* dY, const void* YS, int64_t D, const pnq_expert_plan* plan,
                                 const float* weights, void* dYS, float* dWeights, cudaStream_t stream);
 
+/* ---- routing: logits to experts and weights -------------------------------------------------------- */
+
+enum pnq_score { PNQ_SOFTMAX = 0, PNQ_SIGMOID = 1 };
+
+/* How experts are chosen and weighted, passed by HOST pointer. */
+typedef struct pnq_route_rule {
+    int32_t experts;      /* 1..1024 */
+    int32_t slots;        /* choices per token: 1..64, at most the experts of top_groups groups */
+    int32_t score;        /* pnq_score */
+    int32_t groups;       /* equal runs of experts: 1..32, a divisor of experts (1: no groups) */
+    int32_t top_groups;   /* groups that stay: 1..groups */
+    int32_t best;         /* 1 or 2: a group's score is the sum of so many of its largest choice scores */
+    int32_t renormalize;  /* not 0: weights are divided by their sum */
+    float scale;          /* multiplies the weights; finite */
+} pnq_route_rule;
+
+/*
+ * pnq_expert_route -- the experts of each token and their weights, as pnq_expert_sort and pnq_expert_combine take them.
+ * logits: device, fp32 or bf16 [tokens][experts], row t at t * ld elements. bias: device fp32 [experts], or NULL.
+ *   s = softmax(logits) or 1 / (1 + exp(-logits)); choice score c = s + bias (the bias takes part in the choice, not in the weights).
+ *   With groups, the top_groups groups of the largest scores stay (ties to the lowest group). ids[t] = the `slots` largest c
+ *   of what stays, in that order, ties to the lowest expert. weights[t][j] = scale * s, over the sum of the token's chosen s
+ *   if renormalize.
+ * Scores are compared as they are, not as they round: without bias and groups by the logits, otherwise in 64 bits where fp32 does not decide.
+ * An expert whose logit or bias is -infinity is out: it is not chosen and adds nothing to its group. A slot for which no expert is left
+ * has the id -1 and the weight 0 (pnq_expert_sort drops it): a row of -infinities, a padded token, takes part in nothing. A token
+ * with a NaN logit, with a softmax logit of +infinity, or for whose choice scores the bias is a NaN or +infinity, has the ids 0 .. slots
+ * - 1 and weights of NaN, so that the NaN stays in the token's row and is seen there.
+ * ids: device int32 [tokens][slots]; weights: device fp32 [tokens][slots]. Errors: PNQ_ERR_TYPE (element type, score), PNQ_ERR_SHAPE,
+ * PNQ_ERR_VALUE (scale), PNQ_ERR_NULL, PNQ_ERR_ALIGN (elements), PNQ_ERR_CUDA.
+ */
+int pnq_expert_route(int type, const void* logits, int64_t ld, int64_t tokens, const pnq_route_rule* rule, const float* bias,
+                     int32_t* ids, float* weights, cudaStream_t stream);
+
+/*
+ * pnq_expert_route_backward -- dlogits ([tokens][experts] contiguous, the logits' type, overwritten) from dweights (device fp32
+ * [tokens][slots]), the logits and the ids of the forward call, in fp32, rounded once. The choice itself has no gradient
+ * (nor has the bias). ids outside 0 .. experts - 1 take part in nothing; an expert named twice gets both gradients, in slot
+ * order. Of the rule, groups, top_groups and best are not used. dlogits may be the logits' own buffer where ld = experts.
+ */
+int pnq_expert_route_backward(int type, const float* dweights, const void* logits, int64_t ld, const int32_t* ids, int64_t tokens,
+                              const pnq_route_rule* rule, void* dlogits, cudaStream_t stream);
+
+/* ---- norms, 8-bit rows and their products ------------------------------------------------------------
+ *
+ * Rows of 8-bit codes: int8 [rows][pitch], a scale per row (device fp32 [rows]); a value is code * scale. The calls that write codes
+ * want them on 16 bytes and a pitch that is a multiple of 16 (bytes past a row's codes are not written).
+ */
+
+/*
+ * pnq_rms_norm -- with t = X + residual (rounded to the rows' type; t = X where residual is NULL), r = 1 / sqrt(mean(t^2) + eps):
+ *   total   t, contiguous [rows][D], the type of X (NULL: not written; it may be the residual's own buffer where ldr = D);
+ *   y       t r w, contiguous [rows][D], the type of X (NULL: not written; it may be X's own buffer where ldx = D);
+ *   rstd    r, device fp32 [rows] (NULL: not written), for the backward pass;
+ *   codes, scales  (NULL together: not written) of p = fp32(t w): scale = max|p| r / 127, code = the whole number nearest to
+ *           127 p / max|p|, ties to even. A row of zeros has the scale 0; a row with a NaN or an infinity (of t, w or p) has the scale NaN and codes of
+ *           zero, so that what is computed from it is NaN.
+ * type: PNQ_F32 or PNQ_BF16, of X, residual, total and y (row strides in elements); weight: device [D], PNQ_F32 or PNQ_BF16 of its own.
+ * Sums of squares are fp32 (|t| up to about 1e18); rows on 16 bytes with D a multiple of 8 are faster. Errors: PNQ_ERR_TYPE,
+ * PNQ_ERR_SHAPE (D < 1, a stride below D, a pitch that is not a multiple of 16), PNQ_ERR_VALUE (eps negative or not finite),
+ * PNQ_ERR_NULL (codes without scales, or nothing to write), PNQ_ERR_ALIGN, PNQ_ERR_CUDA.
+ */
+int pnq_rms_norm(int type, const void* X, int64_t ldx, const void* residual, int64_t ldr, int64_t rows, int64_t D, int weight_type,
+                 const void* weight, float eps, void* total, void* y, float* rstd, int8_t* codes, int64_t pitch, float* scales,
+                 cudaStream_t stream);
+
+/*
+ * pnq_rms_norm_backward -- the gradients of y: with n = total rstd and g = dY w,
+ *   dX = rstd (g - n mean(g n)) + dtotal   (contiguous [rows][D]; the residual's gradient too; dtotal, the gradient that
+ *                                           reaches the total itself, may be NULL),
+ *   dweight[c] = sum over rows of dY n     (device fp32 [D]; NULL: not computed).
+ * scratch (with dweight): device fp32, 4-byte aligned, pnq_rms_norm_backward_scratch_bytes long; the order of the sums goes by the
+ * sizes and the device alone. Types as in the forward call. dX is a buffer of its own.
+ */
+int pnq_rms_norm_backward(int type, const void* dY, int64_t ldy, const void* total, int64_t ldt, int weight_type, const void* weight,
+                          const float* rstd, const void* dtotal, int64_t ldd, int64_t rows, int64_t D, void* dX, float* dweight,
+                          void* scratch, uint64_t scratch_bytes, cudaStream_t stream);
+int pnq_rms_norm_backward_scratch_bytes(int64_t rows, int64_t D, uint64_t* bytes);
+
+/*
+ * pnq_int8_quantize -- codes and scales of rows as they are (X: fp32 or bf16, row r at X + r * ldx elements): p = x and r = 1 in
+ * pnq_rms_norm's definition. Activations between two products, and weights once (a scale per output channel).
+ * pnq_int8_dequantize -- out[r][k] = fp32(code * scale), rounded once more for bf16; contiguous [rows][K]; codes of any alignment and pitch.
+ */
+int pnq_int8_quantize(int type, const void* X, int64_t ldx, int64_t rows, int64_t K, int8_t* codes, int64_t pitch, float* scales,
+                      cudaStream_t stream);
+int pnq_int8_dequantize(const int8_t* codes, int64_t pitch, const float* scales, int64_t rows, int64_t K, int out_type, void* out,
+                        cudaStream_t stream);
+
+/*
+ * pnq_int8_gemm -- Y[m][n] = fp32(fp32(sum_k X[m][k] W[n][k]) * x_scales[m]) * w_scales[n] (each step one rounding; bf16 Y one more).
+ * The sum is exact: Y is the same bit for bit whatever M is and whichever kernel takes the call. X: int8, row m at m * ldx bytes;
+ * W: int8, row n at n * ldw bytes (-128 .. 127 all count); 1 <= K <= 131071 (sums within 32 bits). M, N >= 0; a zero one launches nothing.
+ * Y: [M][N] contiguous, fp32 or bf16. scratch: device, 16-byte aligned, as many bytes as pnq_int8_gemm_scratch_bytes gives for
+ * the same arguments (NULL where that is 0: few rows of X); overwritten. Rows of W on 16 bytes with ldw a multiple of 16 are faster.
+ * Errors: PNQ_ERR_TYPE, PNQ_ERR_SHAPE, PNQ_ERR_NULL, PNQ_ERR_ALIGN (scales, Y, scratch), PNQ_ERR_SCRATCH, PNQ_ERR_CUDA.
+ */
+int pnq_int8_gemm(const int8_t* X, int64_t ldx, const float* x_scales, int64_t M, const int8_t* W, int64_t ldw, const float* w_scales,
+                  int64_t N, int64_t K, int y_type, void* Y, void* scratch, uint64_t scratch_bytes, cudaStream_t stream);
+int pnq_int8_gemm_scratch_bytes(int64_t M, const int8_t* W, int64_t ldw, int64_t N, int64_t K, uint64_t* bytes);
+
 /* Library version string (static storage). */
 const char* pnq_version(void);
 
