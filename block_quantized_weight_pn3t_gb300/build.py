@@ -17,7 +17,7 @@ NATIVE = os.path.join(PKG, "_native.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["pnq_api.cu", "pnq_codec_kernels.cu", "pnq_gemv_simt.cu", "pnq_gemv_pn.cu", "pnq_gemv_nvfp4.cu",
            "pnq_grouped.cu", "pnq_quantize.cu", "pnq_prefill.cu", "pnq_fp4_api.cu", "pnq_fp4_quantize.cu",
-           "pnq_fp4_gemm.cu", "pnq_experts.cu", "pnq_norm.cu", "pnq_route.cu", "pnq_int8_gemm.cu", "pnq_int8_api.cu"]
+           "pnq_fp4_gemm.cu", "pnq_experts.cu", "pnq_norm.cu", "pnq_route.cu", "pnq_int8_gemm.cu", "pnq_int8_mma.cu", "pnq_int8_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

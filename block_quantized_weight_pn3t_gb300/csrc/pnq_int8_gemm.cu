@@ -26,7 +26,7 @@ struct RowArgs {
     const float *x_scales, *w_scales;
     void* Y;
     int64_t ldx, ldw;
-    int M, N, K, tile, segment;  // tile: activation rows of a CTA; segment: bytes of a row that a warp takes at a time
+    int M, N, K, segment;  // segment: bytes of a row that a warp takes at a time
 };
 
 __device__ __forceinline__ void store_product(float* y, float f) { *y = f; }
@@ -55,21 +55,21 @@ __device__ __forceinline__ int dot16(uint4 a, uint4 b, int c) {
     return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), c);
 }
 
-// CTA (b, t): weight rows [N b / grid, N (b + 1) / grid), activation rows [t tile, ..). Its warps take pieces of kGroup weight rows x `segment`
+// CTA b: weight rows [N b / grid, N (b + 1) / grid), all of x (MT rows at most). Its warps take pieces of kGroup weight rows x `segment`
 // bytes in turn; a piece's sums go into the CTA's by integer additions in shared memory.
 template <int MT, bool ALIGNED, class T>
 __global__ void __launch_bounds__(kRowThreads, 1) int8_rows_kernel(const RowArgs a) {
     extern __shared__ __align__(16) uint8_t xs[];
     __shared__ int sums[kBlockRows][MT];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int m0 = static_cast<int>(blockIdx.y) * a.tile, mt = min(a.tile, a.M - m0), K = a.K, pitch = (K + 15) / 16 * 16;
+    const int K = a.K, pitch = (K + 15) / 16 * 16;
     const int64_t N = a.N, b = blockIdx.x, g = gridDim.x;
     const int first = static_cast<int>(N * b / g), last = static_cast<int>(N * (b + 1) / g);
     griddep_begin();
     for (int m = 0; m < MT; ++m)
         for (int at = static_cast<int>(threadIdx.x) * 16; at < pitch; at += kRowThreads * 16)
             *reinterpret_cast<uint4*>(xs + static_cast<int64_t>(m) * pitch + at) =
-                m < mt ? load16<false>(a.X + (m0 + m) * a.ldx, at, K) : make_uint4(0, 0, 0, 0);
+                m < a.M ? load16<false>(a.X + m * a.ldx, at, K) : make_uint4(0, 0, 0, 0);
     const int segments = (K + a.segment - 1) / a.segment;
     for (int r0 = first; r0 < last; r0 += kBlockRows) {
         const int rows = min(kBlockRows, last - r0), groups = (rows + kGroup - 1) / kGroup;
@@ -104,10 +104,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) int8_rows_kernel(const RowArgs
                 }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < rows * mt; i += kRowThreads) {
+        for (int i = threadIdx.x; i < rows * a.M; i += kRowThreads) {
             const int m = i / rows, r = i - m * rows, n = r0 + r;
-            store_product(static_cast<T*>(a.Y) + static_cast<int64_t>(m0 + m) * a.N + n,
-                          scaled(sums[r][m], ld_l2(a.x_scales + m0 + m), ld_l2(a.w_scales + n)));
+            store_product(static_cast<T*>(a.Y) + static_cast<int64_t>(m) * a.N + n,
+                          scaled(sums[r][m], ld_l2(a.x_scales + m), ld_l2(a.w_scales + n)));
         }
         __syncthreads();
     }
@@ -121,7 +121,7 @@ cudaError_t run_rows(const RowArgs& a, cudaStream_t stream) {
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3(static_cast<unsigned>(std::min(device_sm_count(), (a.N + kGroup - 1) / kGroup)), static_cast<unsigned>((a.M + a.tile - 1) / a.tile));
+    lc.gridDim = dim3(static_cast<unsigned>(std::min(device_sm_count(), (a.N + kGroup - 1) / kGroup)));
     lc.blockDim = dim3(kRowThreads);
     lc.dynamicSmemBytes = static_cast<size_t>(smem);
     lc.stream = stream;
@@ -134,11 +134,7 @@ cudaError_t run_rows(const RowArgs& a, cudaStream_t stream) {
 }
 
 template <class T>
-cudaError_t run_rows(RowArgs a, cudaStream_t stream) {
-    const int pitch = (a.K + 15) / 16 * 16;
-    int mt = 8;
-    while (mt > 1 && (mt * pitch > kRowSmem || mt / 2 >= a.M)) mt /= 2;
-    a.tile = mt;
+cudaError_t run_rows(RowArgs a, int mt, cudaStream_t stream) {
     a.segment = 2048;
     switch (mt) {
         case 8: return run_rows<8, T>(a, stream);
@@ -148,17 +144,27 @@ cudaError_t run_rows(RowArgs a, cudaStream_t stream) {
     }
 }
 
+// The activation rows (1, 2, 4 or 8) of the kernel that takes M of them with its x in shared memory; 0 where none does.
+int row_tile(int64_t M, int64_t K) {
+    for (int mt = 1; mt <= 8; mt *= 2)
+        if (M <= mt) return mt * ((K + 15) / 16 * 16) <= kRowSmem ? mt : 0;
+    return 0;
+}
+
 }  // namespace
 
-uint64_t int8_gemm_scratch(int64_t, const Int8View&, int64_t) { return 0; }
+uint64_t int8_gemm_scratch(int64_t M, const Int8View& w, int64_t K) { return M == 0 || row_tile(M, K) > 0 ? 0 : int8_mma_scratch(M, w, K); }
 
-cudaError_t launch_int8_gemm(const Int8View& x, const Int8View& w, int64_t K, bool bf16, void* Y, void*, int*, cudaStream_t stream) {
+cudaError_t launch_int8_gemm(const Int8View& x, const Int8View& w, int64_t K, bool bf16, void* Y, void* scratch, int* err,
+                             cudaStream_t stream) {
+    const int mt = row_tile(x.rows, K);
+    if (mt == 0) return launch_int8_mma(x, w, K, bf16, Y, scratch, err, stream);
     RowArgs a{};
     a.X = x.codes, a.ldx = x.ld, a.x_scales = x.scales;
     a.W = w.codes, a.ldw = w.ld, a.w_scales = w.scales;
     a.Y = Y;
     a.M = static_cast<int>(x.rows), a.N = static_cast<int>(w.rows), a.K = static_cast<int>(K);
-    return bf16 ? run_rows<__nv_bfloat16>(a, stream) : run_rows<float>(a, stream);
+    return bf16 ? run_rows<__nv_bfloat16>(a, mt, stream) : run_rows<float>(a, mt, stream);
 }
 
 }  // namespace pnq

@@ -1,0 +1,573 @@
+// pnq_int8_mma.cu -- products of 8-bit integer matrices on the fifth-generation tensor cores (tcgen05), sm_103a, for more rows than
+// pnq_int8_gemm.cu takes through registers.
+//
+// The chip has no fast 8-bit integer MMA. Every code is exact in fp16 (11 significant bits) and a product of two is a whole number up to 2^14, so
+// the 16-bit MMA with fp32 accumulators sums 1024 of them exactly: no partial sum passes 2^24. After each 1024 of K the accumulator is
+// taken out, turned into whole numbers and added to 32-bit sums in registers, while the next 1024 go to a second accumulator.
+// That makes the result independent of tile shapes and of how K is split.
+//
+// Layout. The weight rows are the MMA's M axis (128 lanes of tensor memory per CTA), the activation rows its N axis. x is widened to
+// fp16 once, in a pass of its own, to scratch. The weights stay 8-bit until they are on the SM: four warps read a stage's codes from shared
+// memory, one row a thread, widen them (a byte b xor 128 beside the byte 0x64 is the fp16 number 1024 + 128 + b, less 1152) and write
+// them to tensor memory, where the MMA takes its A operand from. Weight bytes cross HBM, L2 and shared memory as they are.
+//
+// Roles of the warps of a CTA: 0..3 widen, 4..11 take accumulators out (two per lane quarter, half of the columns each), 12 copies
+// (one lane), 13 issues MMAs (one lane). Pairs (CG = 2): two CTAs work on one tile of 256 weight rows (cta_group::2), each with its own
+// 128 and half of the activation rows; the first one's thread issues for both.
+//
+// Every wait is bounded; a wait that gives up records its site in the device error word and ends the role, and tensor memory is
+// released whatever the outcome.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "pnq_device.cuh"
+#include "pnq_internal.h"
+
+namespace pnq {
+namespace {
+
+constexpr int kRows = 128;          // weight rows per CTA and tile (MMA M)
+constexpr int kChunkK = 1024;       // K of an accumulator: 1024 * 2^14 = 2^24
+constexpr int kWidenWarps = 4;
+constexpr int kDrainWarps = 8;
+constexpr int kCopyWarp = kWidenWarps + kDrainWarps, kMmaWarp = kCopyWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kMaxStages = 8;
+constexpr int kMaxSplit = 8;        // CTAs of a cluster that share a tile's K
+constexpr int kSmemLimit = 227 * 1024;
+
+constexpr int imin(int a, int b) { return a < b ? a : b; }
+
+struct MmaArgs {
+    const float *x_scales, *w_scales;
+    void* Y;
+    int* err;
+    int M, N, K;
+    int ks;            // CTAs of a cluster that share a tile's K (1: none)
+    int xbox;          // activation rows of a copy
+    int weights_once;  // every weight row is read by one tile only
+};
+
+// BN activation rows a tile, KS of K a stage, CG CTAs a tile.
+template <int BN, int KS, int CG>
+struct Plan {
+    static constexpr int kCtas = BN <= 64 ? 2 : 1;               // CTAs of an SM
+    static constexpr int kCodes = kRows * KS;                    // bytes of a stage's weights
+    static constexpr int kBox = BN / CG;                         // activation rows that a CTA holds
+    static constexpr int kX = kBox * KS * 2;
+    static constexpr int kStage = kCodes + kX;
+    static constexpr int kStages = imin(kMaxStages, (kSmemLimit / kCtas - 3072) / kStage);
+    static constexpr int kSlotCols = KS / 2;                     // tensor-memory columns of a widened stage
+    static constexpr int kCols = BN <= 64 ? 256 : 512;
+    static constexpr int kSlots = imin(4, imin(kStages, (kCols - 2 * BN) / kSlotCols));
+    static_assert(kStages >= 3 && kSlots >= 2, "stages");
+    static constexpr int kChunkStages = kChunkK / KS;
+    // fp32 accumulators, fp16 operands, N, M = 128 per CTA
+    static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(CG * kRows >> 4) << 24);
+};
+
+// Shared-memory descriptor: K-major rows of 128 bytes, 128-byte swizzle, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// D += A B^T, A (M x 16, fp16) in tensor memory, B (N x 16) in shared memory.
+template <int CG>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// Four codes -> two fp16 pairs in order.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t b = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    uint32_t p = prmt(b, 0x64646464u, 0x4140), q = prmt(b, 0x64646464u, 0x4342);
+    const __half2 u = __hsub2(*reinterpret_cast<__half2*>(&p), off), v = __hsub2(*reinterpret_cast<__half2*>(&q), off);
+    lo = *reinterpret_cast<const uint32_t*>(&u);
+    hi = *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The sum as fp32 (one rounding), times both scales in turn.
+__device__ __forceinline__ float scaled(int sum, float x_scale, float w_scale) {
+    return __fmul_rn(__fmul_rn(__int2float_rn(sum), x_scale), w_scale);
+}
+__device__ __forceinline__ void store_product(float* y, float f) { *y = f; }
+__device__ __forceinline__ void store_product(__nv_bfloat16* y, float f) { *y = __float2bfloat16_rn(f); }
+
+// Walks the tiles number first, first + step, ..: all roles of a CTA see the same sequence. Bands of 16 weight tiles, row tile by
+// row tile: the CTAs at work share a few operand rows in L2.
+struct Tile {
+    int row0, rows, n0;
+};
+template <int BN, int CG>
+struct Walk {
+    static constexpr int kTileN = CG * kRows, kBand = 16;
+    const MmaArgs& a;
+    int at, step, nt, mt, m, band, width;
+    __device__ explicit Walk(const MmaArgs& args)
+        : a(args), at(static_cast<int>(blockIdx.x) / CG), step(static_cast<int>(gridDim.x) / CG), nt((args.N + kTileN - 1) / kTileN),
+          mt((args.M + BN - 1) / BN), m(0), band(0), width(min(kBand, nt)) {}
+    __device__ bool next(Tile& o) {
+        while (band < nt && at >= width) {
+            at -= width;
+            if (++m == mt) m = 0, band += kBand, width = min(kBand, nt - band);
+        }
+        if (band >= nt) return false;
+        o = Tile{m * BN, min(BN, a.M - m * BN), (band + at) * kTileN};
+        at += step;
+        return true;
+    }
+};
+
+template <int BN, int KS, int CG, class T>
+__global__ void __launch_bounds__(kThreads, Plan<BN, KS, CG>::kCtas) int8_mma_kernel(const __grid_constant__ CUtensorMap map_w,
+                                                                                     const __grid_constant__ CUtensorMap map_x,
+                                                                                     const MmaArgs a) {
+    using P = Plan<BN, KS, CG>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    __shared__ __align__(8) uint64_t bars[4 * kMaxStages + 5];
+    __shared__ uint32_t tmem_slot;
+    const uint32_t b0 = smem_addr(bars), sbase = smem_addr(base);
+    auto full_w = [&](int s) { return b0 + 8u * s; };                                // the weights of a stage, this CTA's
+    auto full_x = [&](int s) { return b0 + 8u * (kMaxStages + s); };                 // the activations, both CTAs', at the first
+    auto empty = [&](int s) { return b0 + 8u * (2 * kMaxStages + s); };              // the stage's MMAs are done
+    auto wide = [&](int i) { return b0 + 8u * (3 * kMaxStages + i); };               // a slot is written, by both CTAs, at the first
+    auto acc_full = [&](int i) { return b0 + 8u * (4 * kMaxStages + i); };
+    auto acc_empty = [&](int i) { return b0 + 8u * (4 * kMaxStages + 2 + i); };
+    const uint32_t finished = b0 + 8u * (4 * kMaxStages + 4);
+    constexpr int S = P::kStages, A = P::kSlots;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? blockIdx.x & 1u : 0u;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_w(s), 1);
+            mbar_init(full_x(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int i = 0; i < A; ++i) mbar_init(wide(i), CG * kWidenWarps);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full(i), 1);
+            mbar_init(acc_empty(i), CG * kDrainWarps);
+        }
+        mbar_init(finished, 1);
+        mbar_fence_init();
+        prefetch_tensor_map(&map_w);
+        prefetch_tensor_map(&map_x);
+    }
+    if constexpr (CG == 2) {
+        cluster_sync();  // the pair's barriers exist before either CTA signals them
+        if (warp == kMmaWarp) tmem_alloc_pair(smem_addr(&tmem_slot), P::kCols);
+    } else {
+        if (warp == kMmaWarp) tmem_alloc(smem_addr(&tmem_slot), P::kCols);
+    }
+    griddep_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_launch_dependents();
+    const uint32_t tmem = tmem_slot, slots = tmem + 2 * BN;
+    const int nk = (a.K + KS - 1) / KS, kz = static_cast<int>(blockIdx.y);
+    const int kt0 = kz * nk / a.ks, kt1 = (kz + 1) * nk / a.ks, chunks = (kt1 - kt0 + P::kChunkStages - 1) / P::kChunkStages;
+    Walk<BN, CG> walk(a);
+    Tile tile{};
+
+    if (warp == kCopyWarp) {
+        if (elect_one()) {
+            const uint64_t pol_x = l2_policy_evict_last(), pol_w = a.weights_once ? l2_policy_evict_first() : pol_x;
+            bool ok = true;
+            int s = 0, issued = 0;
+            uint32_t phase = 1;  // the first wait for each free stage passes
+            while (ok && walk.next(tile)) {
+                const int wrow = tile.n0 + static_cast<int>(rank) * kRows, xrow = tile.row0 + static_cast<int>(rank) * P::kBox;
+                for (int kt = kt0; kt < kt1; ++kt) {
+                    if (!mbar_wait_cycles(empty(s), phase)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage);
+                    mbar_arrive_expect_tx(full_w(s), P::kCodes);
+                    if (rank == 0) mbar_arrive_expect_tx(full_x(s), static_cast<uint32_t>(CG * a.xbox * KS * 2));
+                    const uint32_t bar = CG == 2 ? cluster_addr(full_x(s), 0) : full_x(s);
+                    tma_load_2d(st + P::kX, &map_w, kt * KS, wrow, full_w(s), pol_w);
+#pragma unroll
+                    for (int h = 0; h < KS / 64; ++h) {
+                        if constexpr (CG == 2) tma_load_2d_pair(st + h * P::kBox * 128, &map_x, kt * KS + 64 * h, xrow, bar, pol_x);
+                        else tma_load_2d(st + h * P::kBox * 128, &map_x, kt * KS + 64 * h, xrow, bar, pol_x);
+                    }
+                    ++issued;
+                    if (++s == S) s = 0, phase ^= 1;
+                }
+            }
+            if (!ok) record_error(a.err, kErrEmptyWait);
+            // every copy issued has landed before the CTA may exit; a pair's activations are all counted in CTA 0, and CTA 1 waits until
+            // its last stages are reported free (no signal to its barriers is under way when it exits)
+            bool drained = true;
+            for (int g = max(0, issued - S); drained && g < issued; ++g) {
+                drained = mbar_wait_cycles(full_w(g % S), (g / S) & 1);
+                drained = drained && mbar_wait_cycles(rank == 0 ? full_x(g % S) : empty(g % S), (g / S) & 1);
+            }
+            if (!drained) record_error(a.err, kErrDrainWait);
+        }
+    } else if (warp == kMmaWarp) {
+        if (rank == 0 && elect_one()) {
+            auto commit = [](uint32_t bar) {
+                if constexpr (CG == 2) tc_commit_pair(bar);
+                else tc_commit(bar);
+            };
+            bool ok = true;
+            int s = 0, slot = 0, buf = 0;
+            uint32_t phase = 0, slot_phase = 0, acc_phase = 1;
+            while (ok && walk.next(tile)) {
+                for (int kt = kt0, in_chunk = 0; kt < kt1; ++kt) {
+                    if (in_chunk == 0 && !mbar_wait_cycles(acc_empty(buf), acc_phase)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!mbar_wait_cycles(full_x(s), phase) || !mbar_wait_cycles(wide(slot), slot_phase)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN), from = slots + static_cast<uint32_t>(slot * P::kSlotCols);
+                    const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage);
+#pragma unroll
+                    for (int j = 0; j < KS / 16; ++j)
+                        mma_f16<CG>(acc, from + 8 * j, desc_rows(st + (j / 4) * P::kBox * 128) + 2 * (j % 4), P::kIdesc,
+                                    (in_chunk > 0 || j > 0) ? 1u : 0u);
+                    commit(empty(s));  // the stage and its slot are free
+                    if (++s == S) s = 0, phase ^= 1;
+                    if (++slot == A) slot = 0, slot_phase ^= 1;
+                    if (++in_chunk == P::kChunkStages || kt == kt1 - 1) {
+                        commit(acc_full(buf));
+                        in_chunk = 0;
+                        if (++buf == 2) buf = 0, acc_phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) record_error(a.err, kErrFullWait);
+            // no MMA is in flight when tensor memory is released
+            if constexpr (CG == 2) tc_commit_pair_own(finished);
+            else tc_commit(finished);
+            if (!mbar_wait_cycles(finished, 0)) record_error(a.err, kErrDrainWait);
+        }
+    } else if (warp < kWidenWarps) {
+        const int row = 32 * warp + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+        bool ok = true;
+        int i = 0, s = 0, slot = 0;
+        uint32_t phase = 0;
+        while (ok && walk.next(tile)) {
+            for (int kt = kt0; kt < kt1; ++kt, ++i) {
+                if (lane == 0) {
+                    ok = mbar_wait_cycles(full_w(s), phase);
+                    // the slot's last MMAs are those of A stages before
+                    if (ok && i >= A) ok = mbar_wait_cycles(empty((i - A) % S), ((i - A) / S) & 1);
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                __syncwarp();
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t src = sbase + static_cast<uint32_t>(s * P::kStage + P::kX + row * KS);
+#pragma unroll
+                for (int h = 0; h < KS / 32; ++h) {
+                    uint32_t v[16];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        // 16-byte chunk 2 h + c of the row, where the swizzle put it
+                        const uint32_t at = (2 * h + c) ^ (KS == 64 ? (row >> 1) & 3 : row & 7);
+                        const uint4 w = ld_shared_v4<0>(src + 16 * at);
+                        widen4(w.x, v[8 * c], v[8 * c + 1]);
+                        widen4(w.y, v[8 * c + 2], v[8 * c + 3]);
+                        widen4(w.z, v[8 * c + 4], v[8 * c + 5]);
+                        widen4(w.w, v[8 * c + 6], v[8 * c + 7]);
+                    }
+                    tmem_st16(slots + static_cast<uint32_t>(slot * P::kSlotCols + 16 * h) + lanes, v);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(wide(slot), 0));
+                    else mbar_arrive(wide(slot));
+                }
+                if (++s == S) s = 0, phase ^= 1;
+                if (++slot == A) slot = 0;
+            }
+        }
+        if (!ok && lane == 0) record_error(a.err, kErrOperandWait);
+        tc_fence_before();
+    } else {
+        const int q = warp & 3, half = (warp - kWidenWarps) >> 2;  // lanes 32 q .. of tensor memory, half of the columns
+        constexpr int kHalf = BN / 2, kLoad = kHalf < 16 ? kHalf : 16;
+        T* Y = static_cast<T*>(a.Y);
+        int* red = reinterpret_cast<int*>(base);
+        bool ok = true;
+        int buf = 0;
+        uint32_t acc_phase = 0;
+        while (walk.next(tile)) {
+            const int cols = tile.rows - half * kHalf;
+            int sum[kHalf];
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) sum[j] = 0;
+            for (int c = 0; c < chunks; ++c) {
+                if (lane == 0) ok = mbar_wait_cycles(acc_full(buf), acc_phase);
+                ok = __shfl_sync(0xffffffffu, ok, 0);  // tcgen05.ld is .aligned: the warp goes on or stops as one
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN + half * kHalf) + (static_cast<uint32_t>(32 * q) << 16);
+#pragma unroll
+                for (int p = 0; p < kHalf / kLoad; ++p) {
+                    if (p * kLoad >= cols) continue;
+                    uint32_t v[kLoad];
+                    tmem_ld<kLoad>(acc + p * kLoad, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < kLoad; ++j) sum[p * kLoad + j] += __float2int_rn(__uint_as_float(v[j]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(acc_empty(buf), 0));
+                    else mbar_arrive(acc_empty(buf));
+                }
+                if (++buf == 2) buf = 0, acc_phase ^= 1;
+            }
+            if (!ok) break;
+            const int n = tile.n0 + static_cast<int>(rank) * kRows + 32 * q + lane;
+            if (a.ks > 1) {
+                // the partial sums to shared memory, [column][128 rows]; every copy and MMA of the one tile is done
+#pragma unroll
+                for (int j = 0; j < kHalf; ++j)
+                    if (j < cols) red[(half * kHalf + j) * kRows + 32 * q + lane] = sum[j];
+            } else {
+                const float ws = n < a.N ? ld_l2(a.w_scales + n) : 0.0f;
+                const int m0 = tile.row0 + half * kHalf;
+                T* y = Y + static_cast<int64_t>(m0) * a.N + n;
+#pragma unroll
+                for (int p = 0; p < (kHalf + 31) / 32; ++p) {
+                    const float xs = 32 * p + lane < cols ? ld_l2(a.x_scales + m0 + 32 * p + lane) : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < (kHalf < 32 ? kHalf : 32); ++j) {
+                        const float x_scale = __shfl_sync(0xffffffffu, xs, j);
+                        if (32 * p + j < cols && n < a.N) store_product(y, scaled(sum[32 * p + j], x_scale, ws));
+                        y += a.N;
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) record_error(a.err, kErrFullWait);
+        tc_fence_before();
+    }
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();  // both CTAs' copies have landed, both accumulators are read
+    if (CG == 1 && a.ks > 1) {
+        // CTA kz of the cluster adds up its share of the tile's columns over the ks partial tiles (distributed shared memory), and writes them
+        cluster_sync();
+        Walk<BN, CG> again(a);
+        if (again.next(tile)) {
+            T* Y = static_cast<T*>(a.Y);
+            const int c0 = kz * tile.rows / a.ks, c1 = (kz + 1) * tile.rows / a.ks;
+            for (int e = static_cast<int>(threadIdx.x); e < (c1 - c0) * (kRows / 4); e += kThreads) {
+                const int c = c0 + e / (kRows / 4), r = 4 * (e % (kRows / 4)), m = tile.row0 + c, n = tile.n0 + r;
+                const uint32_t at = sbase + 4u * static_cast<uint32_t>(c * kRows + r);
+                float4 v[kMaxSplit];
+#pragma unroll
+                for (int z = 0; z < kMaxSplit; ++z)
+                    if (z < a.ks) v[z] = ld_dsmem_f32x4(cluster_addr(at, static_cast<uint32_t>(z)));
+                int f[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int z = 0; z < kMaxSplit; ++z)
+                    if (z < a.ks) {
+                        f[0] += __float_as_int(v[z].x), f[1] += __float_as_int(v[z].y);
+                        f[2] += __float_as_int(v[z].z), f[3] += __float_as_int(v[z].w);
+                    }
+                const float xs = ld_l2(a.x_scales + m);
+                T* y = Y + static_cast<int64_t>(m) * a.N + n;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n + i < a.N) store_product(y + i, scaled(f[i], xs, ld_l2(a.w_scales + n + i)));
+            }
+        }
+        cluster_sync();  // no CTA leaves while another still reads its tile
+    }
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        if constexpr (CG == 2) tmem_dealloc_pair(tmem, P::kCols);
+        else tmem_dealloc(tmem, P::kCols);
+    }
+}
+
+// ---- x widened, and rows of weights laid out on 16 bytes -------------------------------------------------
+
+// 16 bytes of a row from `at` on, bytes from K on as zeros.
+template <bool ALIGNED>
+__device__ __forceinline__ uint4 load16(const int8_t* row, int at, int K) {
+    if (ALIGNED && at + 16 <= K) return ld_l2(reinterpret_cast<const uint4*>(row + at));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (at + i < K) w[i / 4] |= ld_l2(reinterpret_cast<const uint8_t*>(row + at + i)) << (8 * (i % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Rows of K codes -> rows of `per` pieces of 16: as fp16, or as they are.
+template <bool ALIGNED, bool WIDEN>
+__global__ void __launch_bounds__(256) int8_rows_copy_kernel(const int8_t* X, int64_t ld, int64_t rows, int K, int per, uint4* out) {
+    griddep_begin();
+    const int64_t total = rows * per;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; u < total; u += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t r = u / per;
+        const int c = static_cast<int>(u - r * per);
+        const uint4 w = load16<ALIGNED>(X + r * ld, 16 * c, K);
+        if constexpr (WIDEN) {
+            uint4 a, b;
+            widen4(w.x, a.x, a.y);
+            widen4(w.y, a.z, a.w);
+            widen4(w.z, b.x, b.y);
+            widen4(w.w, b.z, b.w);
+            out[2 * u] = a;
+            out[2 * u + 1] = b;
+        } else {
+            out[u] = w;
+        }
+    }
+}
+
+template <bool WIDEN>
+cudaError_t copy_rows(const int8_t* X, int64_t ld, int64_t rows, int64_t K, void* out, cudaStream_t stream) {
+    const bool aligned = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ld % 16 == 0;
+    const int64_t per = (K + 15) / 16;
+    const int grid = static_cast<int>(std::min<int64_t>((rows * per + 255) / 256, static_cast<int64_t>(device_sm_count()) * 32));
+    return launch_dependent(aligned ? int8_rows_copy_kernel<true, WIDEN> : int8_rows_copy_kernel<false, WIDEN>, grid, 256, stream, X, ld, rows,
+                            static_cast<int>(K), static_cast<int>(per), static_cast<uint4*>(out));
+}
+
+// ---- launches ------------------------------------------------------------------------------------------
+
+template <int BN, int KS, int CG>
+constexpr int mma_smem() {
+    return Plan<BN, KS, CG>::kStages * Plan<BN, KS, CG>::kStage + 1024;
+}
+
+template <int BN, int KS, int CG, class T>
+cudaError_t run_mma(const CUtensorMap& map_w, const CUtensorMap& map_x, const MmaArgs& a, int64_t tiles, cudaStream_t stream) {
+    using P = Plan<BN, KS, CG>;
+    static_assert(P::kStages * P::kStage >= BN * kRows * 4, "a partial tile fits the stages");
+    constexpr int smem = mma_smem<BN, KS, CG>();
+    auto kern = int8_mma_kernel<BN, KS, CG, T>;
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t lc{};
+    lc.blockDim = dim3(kThreads);
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = static_cast<unsigned>(a.ks);
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    if (a.ks > 1) {
+        lc.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.ks));
+    } else if (CG == 1) {
+        lc.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, P::kCtas * device_sm_count())));
+    } else {
+        int pairs = 0;
+        e = resident_clusters(reinterpret_cast<const void*>(kern), kThreads, smem, CG, 1, &pairs);
+        if (e != cudaSuccess) return e;
+        lc.gridDim = dim3(static_cast<unsigned>(CG * std::min<int64_t>(tiles, pairs)));
+    }
+    return cudaLaunchKernelEx(&lc, kern, map_w, map_x, a);
+}
+
+// x: fp16 rows of pitch_x bytes; w: codes on 16 bytes.
+template <int BN, int KS, int CG>
+cudaError_t run_shape(bool bf16, const void* x, int64_t pitch_x, const int8_t* w, int64_t ldw, MmaArgs a, cudaStream_t stream) {
+    using P = Plan<BN, KS, CG>;
+    const int64_t M = a.M, N = a.N, K = a.K;
+    a.xbox = CG == 2 ? P::kBox : static_cast<int>(std::min<int64_t>(BN, M));
+    a.weights_once = M <= BN;
+    const int64_t tiles = (N + CG * kRows - 1) / (CG * kRows) * ((M + BN - 1) / BN);
+    if constexpr (CG == 1) {
+        // K is split over clusters of CTAs where there are fewer tiles than CTAs that the device holds: the fewest stages one after
+        // the other, counting a cluster's sum as two stages
+        const int64_t nk = (K + KS - 1) / KS;
+        int64_t least = 0;
+        for (int ks = 1; ks <= kMaxSplit && (ks == 1 || nk >= 3 * ks); ++ks) {
+            int64_t at_once = static_cast<int64_t>(P::kCtas) * device_sm_count();
+            if (ks > 1) {
+                int clusters = 0;
+                const cudaError_t e = resident_clusters(reinterpret_cast<const void*>(int8_mma_kernel<BN, KS, CG, float>), kThreads,
+                                                        mma_smem<BN, KS, CG>(), 1, ks, &clusters);
+                if (e != cudaSuccess) return e;
+                at_once = clusters;
+                if (tiles > at_once) break;
+            }
+            const int64_t cost = (tiles + at_once - 1) / at_once * ((nk + ks - 1) / ks) + (ks > 1 ? 2 : 0);
+            if (least == 0 || cost < least) least = cost, a.ks = ks;
+        }
+    }
+    CUtensorMap map_w, map_x;
+    if (!encode_rows_map(&map_w, w, N, K, 1, ldw, KS, kRows) || !encode_rows_map(&map_x, x, M, K, 2, pitch_x, 64, a.xbox))
+        return cudaErrorInvalidValue;
+    return bf16 ? run_mma<BN, KS, CG, __nv_bfloat16>(map_w, map_x, a, tiles, stream)
+                : run_mma<BN, KS, CG, float>(map_w, map_x, a, tiles, stream);
+}
+
+bool on_16(const Int8View& w) { return reinterpret_cast<uintptr_t>(w.codes) % 16 == 0 && w.ld % 16 == 0; }
+
+}  // namespace
+
+// x as fp16, and the weights' codes where their rows are not on 16 bytes.
+uint64_t int8_mma_scratch(int64_t M, const Int8View& w, int64_t K) {
+    const uint64_t per = static_cast<uint64_t>((K + 15) / 16);
+    return static_cast<uint64_t>(M) * per * 32 + (on_16(w) ? 0 : static_cast<uint64_t>(w.rows) * per * 16);
+}
+
+cudaError_t launch_int8_mma(const Int8View& x, const Int8View& w, int64_t K, bool bf16, void* Y, void* scratch, int* err,
+                            cudaStream_t stream) {
+    const int64_t per = (K + 15) / 16;
+    cudaError_t e = copy_rows<true>(x.codes, x.ld, x.rows, K, scratch, stream);
+    if (e != cudaSuccess) return e;
+    const int8_t* codes = w.codes;
+    int64_t ldw = w.ld;
+    if (!on_16(w)) {
+        int8_t* copy = static_cast<int8_t*>(scratch) + x.rows * per * 32;
+        e = copy_rows<false>(w.codes, w.ld, w.rows, K, copy, stream);
+        if (e != cudaSuccess) return e;
+        codes = copy, ldw = per * 16;
+    }
+    MmaArgs a{};
+    a.x_scales = x.scales, a.w_scales = w.scales, a.Y = Y, a.err = err;
+    a.M = static_cast<int>(x.rows), a.N = static_cast<int>(w.rows), a.K = static_cast<int>(K), a.ks = 1;
+    const int64_t pitch = per * 32;
+    if (a.M <= 16) return run_shape<16, 128, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
+    if (a.M <= 32) return run_shape<32, 128, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
+    if (a.M <= 64) return run_shape<64, 128, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
+    if (a.M <= 128 || static_cast<int64_t>(a.M + 191) / 192 * ((a.N + 255) / 256) < device_sm_count() / 2)
+        return run_shape<128, 64, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
+    return run_shape<192, 64, 2>(bf16, scratch, pitch, codes, ldw, a, stream);
+}
+
+}  // namespace pnq

@@ -49,6 +49,15 @@ bool encode_u32_map(CUtensorMap* map, const void* base, int64_t rows, int64_t ro
 bool encode_u32_map_pitch(CUtensorMap* map, const void* base, int64_t rows, int64_t row_u32, int64_t pitch_bytes,
                           int box_x, int box_y, bool swizzle_128b);
 
+// 2-D tensor map over rows of `cols` elements of elem_bytes (1 or 2), pitch_bytes apart (a multiple of 16), box {box_x, box_y}, the box's
+// rows of 64 or 128 bytes swizzled over as many: what lies past a row's end or past the last row reads as zeros.
+bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int elem_bytes, int64_t pitch_bytes, int box_x,
+                     int box_y);
+
+// Clusters of x by y CTAs of a kernel (threads and dynamic shared memory given) that the current device holds at once: not every group
+// of SMs divides evenly. Asked once per (kernel, device, x, y).
+cudaError_t resident_clusters(const void* kernel, int threads, int smem, int x, int y, int* clusters);
+
 cudaError_t launch_pn_dequant(int type, const uint8_t* W, int64_t n_rows, int64_t K, float* out,
                               cudaStream_t stream);
 cudaError_t launch_nvfp4_dequant(const Nvfp4View& w, int64_t n_rows, int64_t K, float* out,
@@ -215,6 +224,11 @@ cudaError_t launch_int8_dequantize(const int8_t* codes, int64_t pitch, const flo
 uint64_t int8_gemm_scratch(int64_t M, const Int8View& w, int64_t K);
 cudaError_t launch_int8_gemm(const Int8View& x, const Int8View& w, int64_t K, bool bf16, void* Y, void* scratch, int* err,
                              cudaStream_t stream);
+
+// The same on the tensor cores (pnq_int8_mma.cu), any number of rows.
+uint64_t int8_mma_scratch(int64_t M, const Int8View& w, int64_t K);
+cudaError_t launch_int8_mma(const Int8View& x, const Int8View& w, int64_t K, bool bf16, void* Y, void* scratch, int* err,
+                            cudaStream_t stream);
 
 // How experts are chosen and weighted.
 struct RouteRule {
