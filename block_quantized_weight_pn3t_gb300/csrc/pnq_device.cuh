@@ -119,6 +119,17 @@ __device__ __forceinline__ bool mbar_wait_cycles(uint32_t bar, uint32_t parity) 
     return false;
 }
 
+// The same by a whole warp, the answer the same in every lane: one probe and one vote where the phase has completed. (A wait by lane 0 that
+// the others learn of by a shuffle costs the warp several times that, for the branch around it.)
+__device__ __forceinline__ bool mbar_wait_cycles_warp(uint32_t bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const long long t0 = clock64();
+    do {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    } while (__all_sync(0xffffffffu, clock64() - t0 < (1ll << 32)));
+    return false;
+}
+
 // True in one lane of a converged warp (the same one every time). Branches on it tell the compiler that one
 // thread runs them, as the operands of the asynchronous instructions (uniform registers) want.
 __device__ __forceinline__ bool elect_one() {
@@ -194,6 +205,12 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap,
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// The same without the release, for signals that pass no ordinary memory (tensor memory, ordered by tcgen05.wait and tcgen05.fence, and
+// values already read): a release at cluster scope holds the thread up for half a microsecond.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 // Fetch a tensor map (a __grid_constant__ parameter) ahead of its first copy.

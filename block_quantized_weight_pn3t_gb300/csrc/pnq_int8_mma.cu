@@ -32,6 +32,7 @@ namespace pnq {
 namespace {
 
 constexpr int kRows = 128;          // weight rows per CTA and tile (MMA M)
+constexpr int KS = 128;             // K of a stage: one row of shared memory for the weights, two for the activations
 constexpr int kChunkK = 1024;       // K of an accumulator: 1024 * 2^14 = 2^24
 constexpr int kWidenWarps = 4;
 constexpr int kDrainWarps = 8;
@@ -51,10 +52,11 @@ struct MmaArgs {
     int ks;            // CTAs of a cluster that share a tile's K (1: none)
     int xbox;          // activation rows of a copy
     int weights_once;  // every weight row is read by one tile only
+    int early;         // the weights are the caller's: no kernel in flight writes them
 };
 
-// BN activation rows a tile, KS of K a stage, CG CTAs a tile.
-template <int BN, int KS, int CG>
+// BN activation rows a tile, CG CTAs a tile.
+template <int BN, int CG>
 struct Plan {
     static constexpr int kCtas = BN <= 64 ? 2 : 1;               // CTAs of an SM
     static constexpr int kCodes = kRows * KS;                    // bytes of a stage's weights
@@ -135,11 +137,11 @@ struct Walk {
     }
 };
 
-template <int BN, int KS, int CG, class T>
-__global__ void __launch_bounds__(kThreads, Plan<BN, KS, CG>::kCtas) int8_mma_kernel(const __grid_constant__ CUtensorMap map_w,
+template <int BN, int CG, class T>
+__global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel(const __grid_constant__ CUtensorMap map_w,
                                                                                      const __grid_constant__ CUtensorMap map_x,
                                                                                      const MmaArgs a) {
-    using P = Plan<BN, KS, CG>;
+    using P = Plan<BN, CG>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     __shared__ __align__(8) uint64_t bars[4 * kMaxStages + 5];
@@ -178,7 +180,9 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, KS, CG>::kCtas) int8_mma_ke
     } else {
         if (warp == kMmaWarp) tmem_alloc(smem_addr(&tmem_slot), P::kCols);
     }
-    griddep_wait();
+    // nothing above reads what an earlier kernel wrote. Nor do the first copies of the weights below, where they are the caller's own: the
+    // pass that widened x has waited for all that came before it, and this kernel begins after that
+    if (!a.early || warp != kCopyWarp) griddep_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -193,20 +197,32 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, KS, CG>::kCtas) int8_mma_ke
         if (elect_one()) {
             const uint64_t pol_x = l2_policy_evict_last(), pol_w = a.weights_once ? l2_policy_evict_first() : pol_x;
             bool ok = true;
-            int s = 0, issued = 0;
-            uint32_t phase = 1;  // the first wait for each free stage passes
+            int s = 0, issued = 0, ahead = 0;  // ahead: stages of the first tile whose weights are under way
+            uint32_t phase = 1;                // the first wait for each free stage passes
+            auto load_weights = [&](int i, int kt) {
+                mbar_arrive_expect_tx(full_w(i), P::kCodes);
+                tma_load_2d(sbase + static_cast<uint32_t>(i * P::kStage + P::kX), &map_w, kt * KS,
+                            tile.n0 + static_cast<int>(rank) * kRows, full_w(i), pol_w);
+            };
+            if (a.early) {
+                Walk<BN, CG> first(a);
+                if (first.next(tile))
+                    for (; ahead < min(S, kt1 - kt0); ++ahead) load_weights(ahead, kt0 + ahead);
+                griddep_wait();
+            }
             while (ok && walk.next(tile)) {
-                const int wrow = tile.n0 + static_cast<int>(rank) * kRows, xrow = tile.row0 + static_cast<int>(rank) * P::kBox;
+                const int xrow = tile.row0 + static_cast<int>(rank) * P::kBox;
                 for (int kt = kt0; kt < kt1; ++kt) {
-                    if (!mbar_wait_cycles(empty(s), phase)) {
-                        ok = false;
-                        break;
+                    if (issued >= ahead) {
+                        if (!mbar_wait_cycles(empty(s), phase)) {
+                            ok = false;
+                            break;
+                        }
+                        load_weights(s, kt);
                     }
                     const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage);
-                    mbar_arrive_expect_tx(full_w(s), P::kCodes);
                     if (rank == 0) mbar_arrive_expect_tx(full_x(s), static_cast<uint32_t>(CG * a.xbox * KS * 2));
                     const uint32_t bar = CG == 2 ? cluster_addr(full_x(s), 0) : full_x(s);
-                    tma_load_2d(st + P::kX, &map_w, kt * KS, wrow, full_w(s), pol_w);
 #pragma unroll
                     for (int h = 0; h < KS / 64; ++h) {
                         if constexpr (CG == 2) tma_load_2d_pair(st + h * P::kBox * 128, &map_x, kt * KS + 64 * h, xrow, bar, pol_x);
@@ -276,36 +292,47 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, KS, CG>::kCtas) int8_mma_ke
         uint32_t phase = 0;
         while (ok && walk.next(tile)) {
             for (int kt = kt0; kt < kt1; ++kt, ++i) {
-                if (lane == 0) {
-                    ok = mbar_wait_cycles(full_w(s), phase);
-                    // the slot's last MMAs are those of A stages before
-                    if (ok && i >= A) ok = mbar_wait_cycles(empty((i - A) % S), ((i - A) / S) & 1);
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                __syncwarp();
+                ok = mbar_wait_cycles_warp(full_w(s), phase);
                 if (!ok) break;
-                tc_fence_after();
                 const uint32_t src = sbase + static_cast<uint32_t>(s * P::kStage + P::kX + row * KS);
-#pragma unroll
-                for (int h = 0; h < KS / 32; ++h) {
-                    uint32_t v[16];
+                auto widen = [&](int h, uint32_t (&v)[16]) {  // 32 codes of the row: 16-byte chunks 2 h and 2 h + 1, where the swizzle put them
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        // 16-byte chunk 2 h + c of the row, where the swizzle put it
-                        const uint32_t at = (2 * h + c) ^ (KS == 64 ? (row >> 1) & 3 : row & 7);
-                        const uint4 w = ld_shared_v4<0>(src + 16 * at);
+                        const uint4 w = ld_shared_v4<0>(src + 16 * ((2 * h + c) ^ (row & 7)));
                         widen4(w.x, v[8 * c], v[8 * c + 1]);
                         widen4(w.y, v[8 * c + 2], v[8 * c + 3]);
                         widen4(w.z, v[8 * c + 4], v[8 * c + 5]);
                         widen4(w.w, v[8 * c + 6], v[8 * c + 7]);
                     }
-                    tmem_st16(slots + static_cast<uint32_t>(slot * P::kSlotCols + 16 * h) + lanes, v);
+                };
+                // the slot's last MMAs are those of A stages before
+                auto slot_free = [&] { return i < A || mbar_wait_cycles_warp(empty((i - A) % S), ((i - A) / S) & 1); };
+                auto slot_at = [&](int h) { return slots + static_cast<uint32_t>(slot * P::kSlotCols + 16 * h) + lanes; };
+                if constexpr (P::kCtas == 1) {  // the whole row in registers while the slot is waited for
+                    uint32_t v[KS / 32][16];
+#pragma unroll
+                    for (int h = 0; h < KS / 32; ++h) widen(h, v[h]);
+                    ok = slot_free();
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < KS / 32; ++h) tmem_st16(slot_at(h), v[h]);
+                } else {
+                    ok = slot_free();
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < KS / 32; ++h) {
+                        uint32_t v[16];
+                        widen(h, v);
+                        tmem_st16(slot_at(h), v);
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(wide(slot), 0));
+                    if constexpr (CG == 2) mbar_arrive_cluster_relaxed(cluster_addr(wide(slot), 0));
                     else mbar_arrive(wide(slot));
                 }
                 if (++s == S) s = 0, phase ^= 1;
@@ -328,8 +355,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, KS, CG>::kCtas) int8_mma_ke
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) sum[j] = 0;
             for (int c = 0; c < chunks; ++c) {
-                if (lane == 0) ok = mbar_wait_cycles(acc_full(buf), acc_phase);
-                ok = __shfl_sync(0xffffffffu, ok, 0);  // tcgen05.ld is .aligned: the warp goes on or stops as one
+                ok = mbar_wait_cycles_warp(acc_full(buf), acc_phase);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN + half * kHalf) + (static_cast<uint32_t>(32 * q) << 16);
@@ -345,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, KS, CG>::kCtas) int8_mma_ke
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (CG == 2) mbar_arrive_cluster(cluster_addr(acc_empty(buf), 0));
+                    if constexpr (CG == 2) mbar_arrive_cluster_relaxed(cluster_addr(acc_empty(buf), 0));
                     else mbar_arrive(acc_empty(buf));
                 }
                 if (++buf == 2) buf = 0, acc_phase ^= 1;
@@ -462,17 +488,17 @@ cudaError_t copy_rows(const int8_t* X, int64_t ld, int64_t rows, int64_t K, void
 
 // ---- launches ------------------------------------------------------------------------------------------
 
-template <int BN, int KS, int CG>
+template <int BN, int CG>
 constexpr int mma_smem() {
-    return Plan<BN, KS, CG>::kStages * Plan<BN, KS, CG>::kStage + 1024;
+    return Plan<BN, CG>::kStages * Plan<BN, CG>::kStage + 1024;
 }
 
-template <int BN, int KS, int CG, class T>
+template <int BN, int CG, class T>
 cudaError_t run_mma(const CUtensorMap& map_w, const CUtensorMap& map_x, const MmaArgs& a, int64_t tiles, cudaStream_t stream) {
-    using P = Plan<BN, KS, CG>;
-    static_assert(P::kStages * P::kStage >= BN * kRows * 4, "a partial tile fits the stages");
-    constexpr int smem = mma_smem<BN, KS, CG>();
-    auto kern = int8_mma_kernel<BN, KS, CG, T>;
+    using P = Plan<BN, CG>;
+    static_assert(CG == 2 || P::kStages * P::kStage >= BN * kRows * 4, "a partial tile fits the stages");
+    constexpr int smem = mma_smem<BN, CG>();
+    auto kern = int8_mma_kernel<BN, CG, T>;
     cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc{};
@@ -502,9 +528,9 @@ cudaError_t run_mma(const CUtensorMap& map_w, const CUtensorMap& map_x, const Mm
 }
 
 // x: fp16 rows of pitch_x bytes; w: codes on 16 bytes.
-template <int BN, int KS, int CG>
+template <int BN, int CG>
 cudaError_t run_shape(bool bf16, const void* x, int64_t pitch_x, const int8_t* w, int64_t ldw, MmaArgs a, cudaStream_t stream) {
-    using P = Plan<BN, KS, CG>;
+    using P = Plan<BN, CG>;
     const int64_t M = a.M, N = a.N, K = a.K;
     a.xbox = CG == 2 ? P::kBox : static_cast<int>(std::min<int64_t>(BN, M));
     a.weights_once = M <= BN;
@@ -518,8 +544,8 @@ cudaError_t run_shape(bool bf16, const void* x, int64_t pitch_x, const int8_t* w
             int64_t at_once = static_cast<int64_t>(P::kCtas) * device_sm_count();
             if (ks > 1) {
                 int clusters = 0;
-                const cudaError_t e = resident_clusters(reinterpret_cast<const void*>(int8_mma_kernel<BN, KS, CG, float>), kThreads,
-                                                        mma_smem<BN, KS, CG>(), 1, ks, &clusters);
+                const cudaError_t e = resident_clusters(reinterpret_cast<const void*>(int8_mma_kernel<BN, CG, float>), kThreads,
+                                                        mma_smem<BN, CG>(), 1, ks, &clusters);
                 if (e != cudaSuccess) return e;
                 at_once = clusters;
                 if (tiles > at_once) break;
@@ -531,8 +557,8 @@ cudaError_t run_shape(bool bf16, const void* x, int64_t pitch_x, const int8_t* w
     CUtensorMap map_w, map_x;
     if (!encode_rows_map(&map_w, w, N, K, 1, ldw, KS, kRows) || !encode_rows_map(&map_x, x, M, K, 2, pitch_x, 64, a.xbox))
         return cudaErrorInvalidValue;
-    return bf16 ? run_mma<BN, KS, CG, __nv_bfloat16>(map_w, map_x, a, tiles, stream)
-                : run_mma<BN, KS, CG, float>(map_w, map_x, a, tiles, stream);
+    return bf16 ? run_mma<BN, CG, __nv_bfloat16>(map_w, map_x, a, tiles, stream)
+                : run_mma<BN, CG, float>(map_w, map_x, a, tiles, stream);
 }
 
 bool on_16(const Int8View& w) { return reinterpret_cast<uintptr_t>(w.codes) % 16 == 0 && w.ld % 16 == 0; }
@@ -552,7 +578,8 @@ cudaError_t launch_int8_mma(const Int8View& x, const Int8View& w, int64_t K, boo
     if (e != cudaSuccess) return e;
     const int8_t* codes = w.codes;
     int64_t ldw = w.ld;
-    if (!on_16(w)) {
+    const bool own = on_16(w);
+    if (!own) {
         int8_t* copy = static_cast<int8_t*>(scratch) + x.rows * per * 32;
         e = copy_rows<false>(w.codes, w.ld, w.rows, K, copy, stream);
         if (e != cudaSuccess) return e;
@@ -560,14 +587,14 @@ cudaError_t launch_int8_mma(const Int8View& x, const Int8View& w, int64_t K, boo
     }
     MmaArgs a{};
     a.x_scales = x.scales, a.w_scales = w.scales, a.Y = Y, a.err = err;
-    a.M = static_cast<int>(x.rows), a.N = static_cast<int>(w.rows), a.K = static_cast<int>(K), a.ks = 1;
+    a.M = static_cast<int>(x.rows), a.N = static_cast<int>(w.rows), a.K = static_cast<int>(K), a.ks = 1, a.early = own;
     const int64_t pitch = per * 32;
-    if (a.M <= 16) return run_shape<16, 128, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
-    if (a.M <= 32) return run_shape<32, 128, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
-    if (a.M <= 64) return run_shape<64, 128, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
+    if (a.M <= 16) return run_shape<16, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
+    if (a.M <= 32) return run_shape<32, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
+    if (a.M <= 64) return run_shape<64, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
     if (a.M <= 128 || static_cast<int64_t>(a.M + 191) / 192 * ((a.N + 255) / 256) < device_sm_count() / 2)
-        return run_shape<128, 64, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
-    return run_shape<192, 64, 2>(bf16, scratch, pitch, codes, ldw, a, stream);
+        return run_shape<128, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
+    return run_shape<192, 2>(bf16, scratch, pitch, codes, ldw, a, stream);
 }
 
 }  // namespace pnq

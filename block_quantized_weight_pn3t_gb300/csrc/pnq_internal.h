@@ -50,7 +50,7 @@ bool encode_u32_map_pitch(CUtensorMap* map, const void* base, int64_t rows, int6
                           int box_x, int box_y, bool swizzle_128b);
 
 // 2-D tensor map over rows of `cols` elements of elem_bytes (1 or 2), pitch_bytes apart (a multiple of 16), box {box_x, box_y}, the box's
-// rows of 64 or 128 bytes swizzled over as many: what lies past a row's end or past the last row reads as zeros.
+// rows of 128 bytes swizzled as above: what lies past a row's end or past the last row reads as zeros.
 bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int elem_bytes, int64_t pitch_bytes, int box_x,
                      int box_y);
 
