@@ -11,7 +11,6 @@
 #include <cstring>
 #include <map>
 #include <mutex>
-#include <tuple>
 #include <utility>
 #include <vector>
 
@@ -217,36 +216,6 @@ bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t c
     return enc(map, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims,
                strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-cudaError_t resident_clusters(const void* kernel, int threads, int smem, int x, int y, int* clusters) {
-    static std::mutex mu;
-    static std::map<std::tuple<const void*, int, int, int>, int> known;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    int& n = known[{kernel, dev, x, y}];
-    if (n == 0) {
-        e = opt_in_smem(kernel, smem);
-        if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t lc{};
-        lc.gridDim = dim3(static_cast<unsigned>(x * device_sm_count()), static_cast<unsigned>(y));
-        lc.blockDim = dim3(static_cast<unsigned>(threads));
-        lc.dynamicSmemBytes = static_cast<size_t>(smem);
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = static_cast<unsigned>(x);
-        attr[0].val.clusterDim.y = static_cast<unsigned>(y);
-        attr[0].val.clusterDim.z = 1;
-        lc.attrs = attr;
-        lc.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&n, kernel, &lc);
-        if (e != cudaSuccess) return e;
-        n = std::max(n, 1);
-    }
-    *clusters = n;
-    return cudaSuccess;
 }
 
 }  // namespace pnq

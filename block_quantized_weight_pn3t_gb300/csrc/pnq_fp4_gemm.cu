@@ -40,6 +40,9 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <map>
+#include <mutex>
+#include <tuple>
 #include <utility>
 
 #include "pnq_device.cuh"
@@ -530,6 +533,37 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     }
 }
 
+// Clusters of x by y CTAs of a kernel that the current device holds at once (not every group of SMs divides evenly).
+cudaError_t resident_clusters(const void* kernel, int smem, int x, int y, int* clusters) {
+    static std::mutex mu;
+    static std::map<std::tuple<const void*, int, int, int>, int> known;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    int& n = known[{kernel, dev, x, y}];
+    if (n == 0) {
+        e = opt_in_smem(kernel, smem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t lc{};
+        lc.gridDim = dim3(static_cast<unsigned>(x * device_sm_count()), static_cast<unsigned>(y));
+        lc.blockDim = dim3(kThreads);
+        lc.dynamicSmemBytes = static_cast<size_t>(smem);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(x);
+        attr[0].val.clusterDim.y = static_cast<unsigned>(y);
+        attr[0].val.clusterDim.z = 1;
+        lc.attrs = attr;
+        lc.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &lc);
+        if (e != cudaSuccess) return e;
+        n = std::max(n, 1);
+    }
+    *clusters = n;
+    return cudaSuccess;
+}
+
 template <bool MX, int BN, int CG>
 constexpr int gemm_smem() {
     return Plan<MX, BN, CG>::kStages * Plan<MX, BN, CG>::kStage + 1024;
@@ -563,7 +597,7 @@ cudaError_t run_gemm(const CUtensorMap (&maps)[4], const GemmArgs& a, int64_t ti
         lc.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, device_sm_count())));
     } else {
         int pairs = 0;
-        e = resident_clusters(reinterpret_cast<const void*>(kern), kThreads, smem, CG, 1, &pairs);
+        e = resident_clusters(reinterpret_cast<const void*>(kern), smem, CG, 1, &pairs);
         if (e != cudaSuccess) return e;
         lc.gridDim = dim3(static_cast<unsigned>(CG * std::min<int64_t>(tiles, pairs)));
     }
@@ -617,7 +651,7 @@ cudaError_t choose_dense(int64_t M, int64_t N, int64_t K, Shape* best, int* spli
             int slots = device_sm_count() / s.cg;
             if (ks > 1) {
                 // clusters of any shape hold one CTA per SM: the 64-column kernel answers for all
-                const cudaError_t e = resident_clusters(reinterpret_cast<const void*>(fp4_gemm_kernel<false, 64, 1, float>), kThreads,
+                const cudaError_t e = resident_clusters(reinterpret_cast<const void*>(fp4_gemm_kernel<false, 64, 1, float>),
                                                         gemm_smem<false, 64, 1>(), 1, ks, &slots);
                 if (e != cudaSuccess) return e;
                 if (tiles > slots) break;  // one tile per cluster, all at once

@@ -19,6 +19,7 @@ constexpr int kRowThreads = 512;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kGroup = 4;                 // weight rows that a warp takes together: a piece of x serves them all
 constexpr int kBlockRows = 256;           // weight rows of a CTA whose sums are in shared memory at a time
+constexpr int kStepsAhead = 4;            // steps of a warp in flight
 constexpr int kRowSmem = 200 * 1024;      // x
 
 struct RowArgs {
@@ -26,7 +27,7 @@ struct RowArgs {
     const float *x_scales, *w_scales;
     void* Y;
     int64_t ldx, ldw;
-    int M, N, K, segment;  // segment: bytes of a row that a warp takes at a time
+    int M, N, K;
 };
 
 __device__ __forceinline__ void store_product(float* y, float f) { *y = f; }
@@ -41,6 +42,7 @@ __device__ __forceinline__ float scaled(int sum, float x_scale, float w_scale) {
 template <bool ALIGNED>
 __device__ __forceinline__ uint4 load16(const int8_t* row, int at, int K) {
     if (ALIGNED && at + 16 <= K) return ld_l2(reinterpret_cast<const uint4*>(row + at));
+    if (at >= K) return make_uint4(0, 0, 0, 0);
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -55,53 +57,70 @@ __device__ __forceinline__ int dot16(uint4 a, uint4 b, int c) {
     return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), c);
 }
 
-// CTA b: weight rows [N b / grid, N (b + 1) / grid), all of x (MT rows at most). Its warps take pieces of kGroup weight rows x `segment`
-// bytes in turn; a piece's sums go into the CTA's by integer additions in shared memory.
+// CTA b: weight rows [N b / grid, N (b + 1) / grid) in groups of kGroup, all of x (MT rows at most). A step is 512 bytes of a group's rows, 16 a
+// lane; the steps of all groups, one after the other, are dealt to the warps in equal runs, and a warp has kAhead of its steps in
+// flight, across the groups' ends. A group's sums go into the CTA's by integer additions in shared memory.
 template <int MT, bool ALIGNED, class T>
 __global__ void __launch_bounds__(kRowThreads, 1) int8_rows_kernel(const RowArgs a) {
     extern __shared__ __align__(16) uint8_t xs[];
     __shared__ int sums[kBlockRows][MT];
+    constexpr int kAhead = kStepsAhead;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int K = a.K, pitch = (K + 15) / 16 * 16;
+    const int K = a.K, per = (K + 511) / 512, pitch = per * 512;
     const int64_t N = a.N, b = blockIdx.x, g = gridDim.x;
     const int first = static_cast<int>(N * b / g), last = static_cast<int>(N * (b + 1) / g);
     griddep_begin();
-    for (int m = 0; m < MT; ++m)
-        for (int at = static_cast<int>(threadIdx.x) * 16; at < pitch; at += kRowThreads * 16)
-            *reinterpret_cast<uint4*>(xs + static_cast<int64_t>(m) * pitch + at) =
-                m < a.M ? load16<false>(a.X + m * a.ldx, at, K) : make_uint4(0, 0, 0, 0);
-    const int segments = (K + a.segment - 1) / a.segment;
     for (int r0 = first; r0 < last; r0 += kBlockRows) {
-        const int rows = min(kBlockRows, last - r0), groups = (rows + kGroup - 1) / kGroup;
+        const int rows = min(kBlockRows, last - r0), groups = (rows + kGroup - 1) / kGroup, steps = groups * per;
+        const int s0 = steps * warp / kRowWarps, s1 = steps * (warp + 1) / kRowWarps;
+        uint4 v[kAhead][kGroup];
+        int next = s0, next_group = s0 / per, next_at = (s0 - next_group * per) * 512 + lane * 16;  // of the step to load
+        auto load = [&](uint4 (&to)[kGroup]) {
+            if (next < s1) {
+#pragma unroll
+                for (int r = 0; r < kGroup; ++r)
+                    to[r] = load16<ALIGNED>(a.W + min(r0 + next_group * kGroup + r, last - 1) * a.ldw, next_at, K);
+                ++next;
+                next_at += 512;
+                if (next_at >= pitch) next_at -= pitch, ++next_group;
+            }
+        };
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) load(v[p]);
+        if (r0 == first) {
+            for (int m = 0; m < MT; ++m)
+                for (int at = static_cast<int>(threadIdx.x) * 16; at < pitch; at += kRowThreads * 16)
+                    *reinterpret_cast<uint4*>(xs + static_cast<int64_t>(m) * pitch + at) =
+                        m < a.M ? load16<false>(a.X + m * a.ldx, at, K) : make_uint4(0, 0, 0, 0);
+        }
         for (int i = threadIdx.x; i < rows * MT; i += kRowThreads) (&sums[0][0])[i] = 0;
         __syncthreads();
-        for (int u = warp; u < groups * segments; u += kRowWarps) {
-            const int group = u / segments, s = u - group * segments;
-            const int end = min(K, (s + 1) * a.segment);
-            const int8_t* w[kGroup];
+        int group = s0 / per, at = (s0 - group * per) * 512 + lane * 16;
+        int acc[kGroup][MT] = {};
+        for (int s = s0; s < s1; s += kAhead) {
 #pragma unroll
-            for (int r = 0; r < kGroup; ++r) w[r] = a.W + min(r0 + group * kGroup + r, last - 1) * a.ldw;
-            int acc[kGroup][MT] = {};
-#pragma unroll 2
-            for (int at = s * a.segment + lane * 16; at < end; at += 512) {
-                uint4 v[kGroup];
-#pragma unroll
-                for (int r = 0; r < kGroup; ++r) v[r] = load16<ALIGNED>(w[r], at, K);
+            for (int p = 0; p < kAhead; ++p) {
+                if (s + p >= s1) break;
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     const uint4 x = *reinterpret_cast<const uint4*>(xs + static_cast<int64_t>(m) * pitch + at);
 #pragma unroll
-                    for (int r = 0; r < kGroup; ++r) acc[r][m] = dot16(v[r], x, acc[r][m]);
+                    for (int r = 0; r < kGroup; ++r) acc[r][m] = dot16(v[p][r], x, acc[r][m]);
+                }
+                load(v[p]);
+                at += 512;
+                if (at >= pitch || s + p + 1 == s1) {
+#pragma unroll
+                    for (int r = 0; r < kGroup; ++r)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const int sum = __reduce_add_sync(0xffffffffu, acc[r][m]);
+                            acc[r][m] = 0;
+                            if (lane == 0 && group * kGroup + r < rows) atomicAdd(&sums[group * kGroup + r][m], sum);
+                        }
+                    if (at >= pitch) at -= pitch, ++group;
                 }
             }
-            __syncwarp();
-#pragma unroll
-            for (int r = 0; r < kGroup; ++r)
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const int sum = __reduce_add_sync(0xffffffffu, acc[r][m]);
-                    if (lane == 0 && group * kGroup + r < rows) atomicAdd(&sums[group * kGroup + r][m], sum);
-                }
         }
         __syncthreads();
         for (int i = threadIdx.x; i < rows * a.M; i += kRowThreads) {
@@ -117,7 +136,7 @@ template <int MT, class T>
 cudaError_t run_rows(const RowArgs& a, cudaStream_t stream) {
     const bool aligned = reinterpret_cast<uintptr_t>(a.W) % 16 == 0 && a.ldw % 16 == 0;
     auto kernel = aligned ? int8_rows_kernel<MT, true, T> : int8_rows_kernel<MT, false, T>;
-    const int smem = MT * ((a.K + 15) / 16 * 16);
+    const int smem = MT * ((a.K + 511) / 512 * 512);
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc{};
@@ -135,7 +154,6 @@ cudaError_t run_rows(const RowArgs& a, cudaStream_t stream) {
 
 template <class T>
 cudaError_t run_rows(RowArgs a, int mt, cudaStream_t stream) {
-    a.segment = 2048;
     switch (mt) {
         case 8: return run_rows<8, T>(a, stream);
         case 4: return run_rows<4, T>(a, stream);
@@ -147,7 +165,7 @@ cudaError_t run_rows(RowArgs a, int mt, cudaStream_t stream) {
 // The activation rows (1, 2, 4 or 8) of the kernel that takes M of them with its x in shared memory; 0 where none does.
 int row_tile(int64_t M, int64_t K) {
     for (int mt = 1; mt <= 8; mt *= 2)
-        if (M <= mt) return mt * ((K + 15) / 16 * 16) <= kRowSmem ? mt : 0;
+        if (M <= mt) return mt * ((K + 511) / 512 * 512) <= kRowSmem ? mt : 0;
     return 0;
 }
 

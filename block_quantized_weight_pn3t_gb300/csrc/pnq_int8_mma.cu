@@ -39,38 +39,41 @@ constexpr int kDrainWarps = 8;
 constexpr int kCopyWarp = kWidenWarps + kDrainWarps, kMmaWarp = kCopyWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kMaxStages = 8;
-constexpr int kMaxSplit = 8;        // CTAs of a cluster that share a tile's K
+constexpr int kMaxSlots = 4;
+constexpr int kBand = 16;           // weight tiles of a band
 constexpr int kSmemLimit = 227 * 1024;
-
-constexpr int imin(int a, int b) { return a < b ? a : b; }
+constexpr int kCodes = kRows * KS;  // bytes of a stage's weights
+constexpr int kSlotCols = KS / 2;   // tensor-memory columns of a widened stage
+constexpr int kChunkStages = kChunkK / KS;
 
 struct MmaArgs {
     const float *x_scales, *w_scales;
     void* Y;
     int* err;
     int M, N, K;
-    int ks;            // CTAs of a cluster that share a tile's K (1: none)
+    int bn;            // activation rows of a tile
+    int ks;            // CTAs (pairs) of a cluster that share a tile's K (1: none)
+    int stages, slots; // of the rings in shared and in tensor memory
     int xbox;          // activation rows of a copy
     int weights_once;  // every weight row is read by one tile only
     int early;         // the weights are the caller's: no kernel in flight writes them
 };
 
-// BN activation rows a tile, CG CTAs a tile.
+// Tiles of at most BN activation rows, by CG CTAs.
 template <int BN, int CG>
 struct Plan {
-    static constexpr int kCtas = BN <= 64 ? 2 : 1;               // CTAs of an SM
-    static constexpr int kCodes = kRows * KS;                    // bytes of a stage's weights
-    static constexpr int kBox = BN / CG;                         // activation rows that a CTA holds
-    static constexpr int kX = kBox * KS * 2;
-    static constexpr int kStage = kCodes + kX;
-    static constexpr int kStages = imin(kMaxStages, (kSmemLimit / kCtas - 3072) / kStage);
-    static constexpr int kSlotCols = KS / 2;                     // tensor-memory columns of a widened stage
-    static constexpr int kCols = BN <= 64 ? 256 : 512;
-    static constexpr int kSlots = imin(4, imin(kStages, (kCols - 2 * BN) / kSlotCols));
-    static_assert(kStages >= 3 && kSlots >= 2, "stages");
-    static constexpr int kChunkStages = kChunkK / KS;
+    static constexpr int kCtas = BN <= 64 ? 2 : 1;             // CTAs of an SM
+    static constexpr int kBound = kCtas == 2 ? 512 : kThreads; // two CTAs of 14 warps share an SM's four register files as two of 16 do
+    static constexpr int kStep = 16 * CG;                      // a tile's activation rows are a multiple of it
+    static constexpr int kCols = kCtas == 2 ? 256 : 512;       // tensor-memory columns: two accumulators, and the slots
+    static constexpr int kSplit = 8 / CG;                      // the most that share a tile's K: clusters of 8 CTAs
+    static int stage(int bn) { return kCodes + bn / CG * KS * 2; }
+    static int stages(int bn) { return std::min(kMaxStages, (kSmemLimit / kCtas - 3072) / stage(bn)); }
+    static int slots(int bn) { return std::min({kMaxSlots, stages(bn), (kCols - 2 * bn) / kSlotCols}); }
     // fp32 accumulators, fp16 operands, N, M = 128 per CTA
-    static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(CG * kRows >> 4) << 24);
+    static __device__ uint32_t idesc(int bn) {
+        return (1u << 4) | (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(CG * kRows >> 4) << 24);
+    }
 };
 
 // Shared-memory descriptor: K-major rows of 128 bytes, 128-byte swizzle, 8-row groups 1024 bytes apart.
@@ -95,6 +98,17 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint
             : "memory");
 }
 
+// The first CTA of this CTA's pair, by its rank in the cluster (pairs lie along x, the parts of a tile's K along y).
+__device__ __forceinline__ uint32_t pair_leader() { return 2u * blockIdx.y; }
+
+// Arrives on the barrier at this offset in both CTAs of the pair whose first has the given rank, when the pair's MMAs are done.
+__device__ __forceinline__ void tc_commit_pair_of(uint32_t bar, uint32_t leader) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3u << leader))
+        : "memory");
+}
+
 // Four codes -> two fp16 pairs in order.
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     const uint32_t b = w ^ 0x80808080u;
@@ -112,49 +126,51 @@ __device__ __forceinline__ float scaled(int sum, float x_scale, float w_scale) {
 __device__ __forceinline__ void store_product(float* y, float f) { *y = f; }
 __device__ __forceinline__ void store_product(__nv_bfloat16* y, float f) { *y = __float2bfloat16_rn(f); }
 
-// Walks the tiles number first, first + step, ..: all roles of a CTA see the same sequence. Bands of 16 weight tiles, row tile by
-// row tile: the CTAs at work share a few operand rows in L2.
+// Walks the tiles number first, first + step, ..: all roles of a CTA see the same sequence. Bands of 16 weight tiles, row tile by row
+// tile: the CTAs at work share a few operand rows in L2.
 struct Tile {
     int row0, rows, n0;
 };
-template <int BN, int CG>
+template <int CG>
 struct Walk {
-    static constexpr int kTileN = CG * kRows, kBand = 16;
+    static constexpr int kTileN = CG * kRows;
     const MmaArgs& a;
     int at, step, nt, mt, m, band, width;
     __device__ explicit Walk(const MmaArgs& args)
         : a(args), at(static_cast<int>(blockIdx.x) / CG), step(static_cast<int>(gridDim.x) / CG), nt((args.N + kTileN - 1) / kTileN),
-          mt((args.M + BN - 1) / BN), m(0), band(0), width(min(kBand, nt)) {}
+          mt((args.M + args.bn - 1) / args.bn), m(0), band(0), width(min(kBand, nt)) {}
     __device__ bool next(Tile& o) {
         while (band < nt && at >= width) {
             at -= width;
             if (++m == mt) m = 0, band += kBand, width = min(kBand, nt - band);
         }
         if (band >= nt) return false;
-        o = Tile{m * BN, min(BN, a.M - m * BN), (band + at) * kTileN};
+        o = Tile{m * a.bn, min(a.bn, a.M - m * a.bn), (band + at) * kTileN};
         at += step;
         return true;
     }
 };
 
 template <int BN, int CG, class T>
-__global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel(const __grid_constant__ CUtensorMap map_w,
-                                                                                     const __grid_constant__ CUtensorMap map_x,
-                                                                                     const MmaArgs a) {
+__global__ void __launch_bounds__(Plan<BN, CG>::kBound, Plan<BN, CG>::kCtas) int8_mma_kernel(const __grid_constant__ CUtensorMap map_w,
+                                                                                             const __grid_constant__ CUtensorMap map_x,
+                                                                                             const MmaArgs a) {
     using P = Plan<BN, CG>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    __shared__ __align__(8) uint64_t bars[4 * kMaxStages + 5];
+    __shared__ __align__(8) uint64_t bars[3 * kMaxStages + kMaxSlots + 5];
     __shared__ uint32_t tmem_slot;
     const uint32_t b0 = smem_addr(bars), sbase = smem_addr(base);
     auto full_w = [&](int s) { return b0 + 8u * s; };                                // the weights of a stage, this CTA's
     auto full_x = [&](int s) { return b0 + 8u * (kMaxStages + s); };                 // the activations, both CTAs', at the first
     auto empty = [&](int s) { return b0 + 8u * (2 * kMaxStages + s); };              // the stage's MMAs are done
     auto wide = [&](int i) { return b0 + 8u * (3 * kMaxStages + i); };               // a slot is written, by both CTAs, at the first
-    auto acc_full = [&](int i) { return b0 + 8u * (4 * kMaxStages + i); };
-    auto acc_empty = [&](int i) { return b0 + 8u * (4 * kMaxStages + 2 + i); };
-    const uint32_t finished = b0 + 8u * (4 * kMaxStages + 4);
-    constexpr int S = P::kStages, A = P::kSlots;
+    auto acc_full = [&](int i) { return b0 + 8u * (3 * kMaxStages + kMaxSlots + i); };
+    auto acc_empty = [&](int i) { return b0 + 8u * (3 * kMaxStages + kMaxSlots + 2 + i); };
+    const uint32_t finished = b0 + 8u * (3 * kMaxStages + kMaxSlots + 4);
+    const int S = a.stages, A = a.slots, bn = a.bn;
+    const uint32_t box = static_cast<uint32_t>(bn / CG) * 128;  // bytes of 64 of K of this CTA's activations
+    const uint32_t x_bytes = 2 * box, stage = kCodes + x_bytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? blockIdx.x & 1u : 0u;
 
@@ -187,10 +203,10 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
     __syncthreads();
     tc_fence_after();
     griddep_launch_dependents();
-    const uint32_t tmem = tmem_slot, slots = tmem + 2 * BN;
+    const uint32_t tmem = tmem_slot, slots = tmem + static_cast<uint32_t>(2 * bn);
     const int nk = (a.K + KS - 1) / KS, kz = static_cast<int>(blockIdx.y);
-    const int kt0 = kz * nk / a.ks, kt1 = (kz + 1) * nk / a.ks, chunks = (kt1 - kt0 + P::kChunkStages - 1) / P::kChunkStages;
-    Walk<BN, CG> walk(a);
+    const int kt0 = kz * nk / a.ks, kt1 = (kz + 1) * nk / a.ks, chunks = (kt1 - kt0 + kChunkStages - 1) / kChunkStages;
+    Walk<CG> walk(a);
     Tile tile{};
 
     if (warp == kCopyWarp) {
@@ -200,18 +216,18 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
             int s = 0, issued = 0, ahead = 0;  // ahead: stages of the first tile whose weights are under way
             uint32_t phase = 1;                // the first wait for each free stage passes
             auto load_weights = [&](int i, int kt) {
-                mbar_arrive_expect_tx(full_w(i), P::kCodes);
-                tma_load_2d(sbase + static_cast<uint32_t>(i * P::kStage + P::kX), &map_w, kt * KS,
-                            tile.n0 + static_cast<int>(rank) * kRows, full_w(i), pol_w);
+                mbar_arrive_expect_tx(full_w(i), kCodes);
+                tma_load_2d(sbase + static_cast<uint32_t>(i) * stage + x_bytes, &map_w, kt * KS, tile.n0 + static_cast<int>(rank) * kRows,
+                            full_w(i), pol_w);
             };
             if (a.early) {
-                Walk<BN, CG> first(a);
+                Walk<CG> first(a);
                 if (first.next(tile))
                     for (; ahead < min(S, kt1 - kt0); ++ahead) load_weights(ahead, kt0 + ahead);
                 griddep_wait();
             }
             while (ok && walk.next(tile)) {
-                const int xrow = tile.row0 + static_cast<int>(rank) * P::kBox;
+                const int xrow = tile.row0 + static_cast<int>(rank) * (bn / CG);
                 for (int kt = kt0; kt < kt1; ++kt) {
                     if (issued >= ahead) {
                         if (!mbar_wait_cycles(empty(s), phase)) {
@@ -220,20 +236,20 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
                         }
                         load_weights(s, kt);
                     }
-                    const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage);
+                    const uint32_t st = sbase + static_cast<uint32_t>(s) * stage;
                     if (rank == 0) mbar_arrive_expect_tx(full_x(s), static_cast<uint32_t>(CG * a.xbox * KS * 2));
-                    const uint32_t bar = CG == 2 ? cluster_addr(full_x(s), 0) : full_x(s);
+                    const uint32_t bar = CG == 2 ? cluster_addr(full_x(s), pair_leader()) : full_x(s);
 #pragma unroll
                     for (int h = 0; h < KS / 64; ++h) {
-                        if constexpr (CG == 2) tma_load_2d_pair(st + h * P::kBox * 128, &map_x, kt * KS + 64 * h, xrow, bar, pol_x);
-                        else tma_load_2d(st + h * P::kBox * 128, &map_x, kt * KS + 64 * h, xrow, bar, pol_x);
+                        if constexpr (CG == 2) tma_load_2d_pair(st + h * box, &map_x, kt * KS + 64 * h, xrow, bar, pol_x);
+                        else tma_load_2d(st + h * box, &map_x, kt * KS + 64 * h, xrow, bar, pol_x);
                     }
                     ++issued;
                     if (++s == S) s = 0, phase ^= 1;
                 }
             }
             if (!ok) record_error(a.err, kErrEmptyWait);
-            // every copy issued has landed before the CTA may exit; a pair's activations are all counted in CTA 0, and CTA 1 waits until
+            // every copy issued has landed before the CTA may exit; a pair's activations are all counted in its first CTA, and the second waits until
             // its last stages are reported free (no signal to its barriers is under way when it exits)
             bool drained = true;
             for (int g = max(0, issued - S); drained && g < issued; ++g) {
@@ -244,10 +260,11 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
         }
     } else if (warp == kMmaWarp) {
         if (rank == 0 && elect_one()) {
-            auto commit = [](uint32_t bar) {
-                if constexpr (CG == 2) tc_commit_pair(bar);
+            auto commit = [&](uint32_t bar) {
+                if constexpr (CG == 2) tc_commit_pair_of(bar, pair_leader());
                 else tc_commit(bar);
             };
+            const uint32_t idesc = P::idesc(bn);
             bool ok = true;
             int s = 0, slot = 0, buf = 0;
             uint32_t phase = 0, slot_phase = 0, acc_phase = 1;
@@ -262,16 +279,16 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN), from = slots + static_cast<uint32_t>(slot * P::kSlotCols);
-                    const uint32_t st = sbase + static_cast<uint32_t>(s * P::kStage);
+                    const uint32_t acc = tmem + static_cast<uint32_t>(buf * bn), from = slots + static_cast<uint32_t>(slot * kSlotCols);
+                    const uint32_t st = sbase + static_cast<uint32_t>(s) * stage;
+                    const uint64_t x0 = desc_rows(st), x1 = desc_rows(st + box);
 #pragma unroll
                     for (int j = 0; j < KS / 16; ++j)
-                        mma_f16<CG>(acc, from + 8 * j, desc_rows(st + (j / 4) * P::kBox * 128) + 2 * (j % 4), P::kIdesc,
-                                    (in_chunk > 0 || j > 0) ? 1u : 0u);
+                        mma_f16<CG>(acc, from + 8 * j, (j < 4 ? x0 : x1) + 2 * (j % 4), idesc, (in_chunk > 0 || j > 0) ? 1u : 0u);
                     commit(empty(s));  // the stage and its slot are free
                     if (++s == S) s = 0, phase ^= 1;
                     if (++slot == A) slot = 0, slot_phase ^= 1;
-                    if (++in_chunk == P::kChunkStages || kt == kt1 - 1) {
+                    if (++in_chunk == kChunkStages || kt == kt1 - 1) {
                         commit(acc_full(buf));
                         in_chunk = 0;
                         if (++buf == 2) buf = 0, acc_phase ^= 1;
@@ -288,13 +305,13 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
         const int row = 32 * warp + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
         bool ok = true;
-        int i = 0, s = 0, slot = 0;
-        uint32_t phase = 0;
+        int i = 0, s = 0, slot = 0, es = 0;   // es, ephase: the stage whose MMAs were the slot's last, A stages before
+        uint32_t phase = 0, ephase = 0;
         while (ok && walk.next(tile)) {
             for (int kt = kt0; kt < kt1; ++kt, ++i) {
                 ok = mbar_wait_cycles_warp(full_w(s), phase);
                 if (!ok) break;
-                const uint32_t src = sbase + static_cast<uint32_t>(s * P::kStage + P::kX + row * KS);
+                const uint32_t src = sbase + static_cast<uint32_t>(s) * stage + x_bytes + static_cast<uint32_t>(row * KS);
                 auto widen = [&](int h, uint32_t (&v)[16]) {  // 32 codes of the row: 16-byte chunks 2 h and 2 h + 1, where the swizzle put them
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
@@ -305,9 +322,13 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
                         widen4(w.w, v[8 * c + 6], v[8 * c + 7]);
                     }
                 };
-                // the slot's last MMAs are those of A stages before
-                auto slot_free = [&] { return i < A || mbar_wait_cycles_warp(empty((i - A) % S), ((i - A) / S) & 1); };
-                auto slot_at = [&](int h) { return slots + static_cast<uint32_t>(slot * P::kSlotCols + 16 * h) + lanes; };
+                auto slot_free = [&] {
+                    if (i < A) return true;
+                    const bool free = mbar_wait_cycles_warp(empty(es), ephase);
+                    if (++es == S) es = 0, ephase ^= 1;
+                    return free;
+                };
+                auto slot_at = [&](int h) { return slots + static_cast<uint32_t>(slot * kSlotCols + 16 * h) + lanes; };
                 if constexpr (P::kCtas == 1) {  // the whole row in registers while the slot is waited for
                     uint32_t v[KS / 32][16];
 #pragma unroll
@@ -332,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (CG == 2) mbar_arrive_cluster_relaxed(cluster_addr(wide(slot), 0));
+                    if constexpr (CG == 2) mbar_arrive_cluster_relaxed(cluster_addr(wide(slot), pair_leader()));
                     else mbar_arrive(wide(slot));
                 }
                 if (++s == S) s = 0, phase ^= 1;
@@ -343,14 +364,15 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
         tc_fence_before();
     } else {
         const int q = warp & 3, half = (warp - kWidenWarps) >> 2;  // lanes 32 q .. of tensor memory, half of the columns
-        constexpr int kHalf = BN / 2, kLoad = kHalf < 16 ? kHalf : 16;
+        constexpr int kHalf = BN / 2, kLoad = P::kStep / 2;
+        const int columns = bn / 2;  // a multiple of kLoad
         T* Y = static_cast<T*>(a.Y);
         int* red = reinterpret_cast<int*>(base);
         bool ok = true;
         int buf = 0;
         uint32_t acc_phase = 0;
         while (walk.next(tile)) {
-            const int cols = tile.rows - half * kHalf;
+            const int cols = min(columns, tile.rows - half * columns);
             int sum[kHalf];
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) sum[j] = 0;
@@ -358,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
                 ok = mbar_wait_cycles_warp(acc_full(buf), acc_phase);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + static_cast<uint32_t>(buf * BN + half * kHalf) + (static_cast<uint32_t>(32 * q) << 16);
+                const uint32_t acc = tmem + static_cast<uint32_t>(buf * bn + half * columns) + (static_cast<uint32_t>(32 * q) << 16);
 #pragma unroll
                 for (int p = 0; p < kHalf / kLoad; ++p) {
                     if (p * kLoad >= cols) continue;
@@ -371,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (CG == 2) mbar_arrive_cluster_relaxed(cluster_addr(acc_empty(buf), 0));
+                    if constexpr (CG == 2) mbar_arrive_cluster_relaxed(cluster_addr(acc_empty(buf), pair_leader()));
                     else mbar_arrive(acc_empty(buf));
                 }
                 if (++buf == 2) buf = 0, acc_phase ^= 1;
@@ -382,16 +404,16 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
                 // the partial sums to shared memory, [column][128 rows]; every copy and MMA of the one tile is done
 #pragma unroll
                 for (int j = 0; j < kHalf; ++j)
-                    if (j < cols) red[(half * kHalf + j) * kRows + 32 * q + lane] = sum[j];
+                    if (j < cols) red[(half * columns + j) * kRows + 32 * q + lane] = sum[j];
             } else {
                 const float ws = n < a.N ? ld_l2(a.w_scales + n) : 0.0f;
-                const int m0 = tile.row0 + half * kHalf;
+                const int m0 = tile.row0 + half * columns;
                 T* y = Y + static_cast<int64_t>(m0) * a.N + n;
 #pragma unroll
                 for (int p = 0; p < (kHalf + 31) / 32; ++p) {
                     const float xs = 32 * p + lane < cols ? ld_l2(a.x_scales + m0 + 32 * p + lane) : 0.0f;
 #pragma unroll
-                    for (int j = 0; j < (kHalf < 32 ? kHalf : 32); ++j) {
+                    for (int j = 0; j < 32; ++j) {
                         const float x_scale = __shfl_sync(0xffffffffu, xs, j);
                         if (32 * p + j < cols && n < a.N) store_product(y, scaled(sum[32 * p + j], x_scale, ws));
                         y += a.N;
@@ -404,23 +426,23 @@ __global__ void __launch_bounds__(kThreads, Plan<BN, CG>::kCtas) int8_mma_kernel
     }
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();  // both CTAs' copies have landed, both accumulators are read
-    if (CG == 1 && a.ks > 1) {
+    if (a.ks > 1) {
         // CTA kz of the cluster adds up its share of the tile's columns over the ks partial tiles (distributed shared memory), and writes them
-        cluster_sync();
-        Walk<BN, CG> again(a);
+        if constexpr (CG == 1) cluster_sync();
+        Walk<CG> again(a);
         if (again.next(tile)) {
             T* Y = static_cast<T*>(a.Y);
             const int c0 = kz * tile.rows / a.ks, c1 = (kz + 1) * tile.rows / a.ks;
             for (int e = static_cast<int>(threadIdx.x); e < (c1 - c0) * (kRows / 4); e += kThreads) {
-                const int c = c0 + e / (kRows / 4), r = 4 * (e % (kRows / 4)), m = tile.row0 + c, n = tile.n0 + r;
+                const int c = c0 + e / (kRows / 4), r = 4 * (e % (kRows / 4)), m = tile.row0 + c, n = tile.n0 + static_cast<int>(rank) * kRows + r;
                 const uint32_t at = sbase + 4u * static_cast<uint32_t>(c * kRows + r);
-                float4 v[kMaxSplit];
+                float4 v[P::kSplit];
 #pragma unroll
-                for (int z = 0; z < kMaxSplit; ++z)
-                    if (z < a.ks) v[z] = ld_dsmem_f32x4(cluster_addr(at, static_cast<uint32_t>(z)));
+                for (int z = 0; z < P::kSplit; ++z)
+                    if (z < a.ks) v[z] = ld_dsmem_f32x4(cluster_addr(at, rank + static_cast<uint32_t>(CG * z)));
                 int f[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int z = 0; z < kMaxSplit; ++z)
+                for (int z = 0; z < P::kSplit; ++z)
                     if (z < a.ks) {
                         f[0] += __float_as_int(v[z].x), f[1] += __float_as_int(v[z].y);
                         f[2] += __float_as_int(v[z].z), f[3] += __float_as_int(v[z].w);
@@ -488,20 +510,39 @@ cudaError_t copy_rows(const int8_t* X, int64_t ld, int64_t rows, int64_t K, void
 
 // ---- launches ------------------------------------------------------------------------------------------
 
+// How a product is cut: tiles of bn activation rows and cg * 128 weight rows, and the CTAs (pairs) that share a tile's K.
+struct Cut {
+    int bn, cg, ks;
+    int64_t tiles;
+};
+
 template <int BN, int CG>
-constexpr int mma_smem() {
-    return Plan<BN, CG>::kStages * Plan<BN, CG>::kStage + 1024;
+Cut cut_by(int64_t M, int64_t N, int64_t K) {
+    using P = Plan<BN, CG>;
+    const int64_t mt = (M + BN - 1) / BN, nk = (K + KS - 1) / KS, units = static_cast<int64_t>(P::kCtas) * device_sm_count() / CG;
+    Cut c{};
+    c.bn = static_cast<int>(((M + mt - 1) / mt + P::kStep - 1) / P::kStep * P::kStep);
+    c.cg = CG;
+    c.tiles = (N + CG * kRows - 1) / (CG * kRows) * mt;
+    double least = 0.0;
+    for (int ks = 1; ks <= P::kSplit && (ks == 1 || nk >= 2 * ks); ++ks) {
+        const double cost = static_cast<double>((c.tiles * ks + units - 1) / units * ((nk + ks - 1) / ks)) + (ks > 1 ? 3.0 : 0.0);
+        if (ks == 1 || cost < least) least = cost, c.ks = ks;
+    }
+    return c;
 }
 
 template <int BN, int CG, class T>
 cudaError_t run_mma(const CUtensorMap& map_w, const CUtensorMap& map_x, const MmaArgs& a, int64_t tiles, cudaStream_t stream) {
     using P = Plan<BN, CG>;
-    static_assert(CG == 2 || P::kStages * P::kStage >= BN * kRows * 4, "a partial tile fits the stages");
-    constexpr int smem = mma_smem<BN, CG>();
+    const int smem = a.stages * P::stage(a.bn) + 1024;
     auto kern = int8_mma_kernel<BN, CG, T>;
-    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem);
+    const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc{};
+    // K split: one tile a cluster; otherwise as many CTAs as the device holds at once, each over its tiles
+    const int64_t units = static_cast<int64_t>(P::kCtas) * device_sm_count() / CG;
+    lc.gridDim = dim3(static_cast<unsigned>(CG * (a.ks > 1 ? tiles : std::min(tiles, units))), static_cast<unsigned>(a.ks));
     lc.blockDim = dim3(kThreads);
     lc.dynamicSmemBytes = static_cast<size_t>(smem);
     lc.stream = stream;
@@ -514,51 +555,22 @@ cudaError_t run_mma(const CUtensorMap& map_w, const CUtensorMap& map_x, const Mm
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 2;
-    if (a.ks > 1) {
-        lc.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.ks));
-    } else if (CG == 1) {
-        lc.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, P::kCtas * device_sm_count())));
-    } else {
-        int pairs = 0;
-        e = resident_clusters(reinterpret_cast<const void*>(kern), kThreads, smem, CG, 1, &pairs);
-        if (e != cudaSuccess) return e;
-        lc.gridDim = dim3(static_cast<unsigned>(CG * std::min<int64_t>(tiles, pairs)));
-    }
     return cudaLaunchKernelEx(&lc, kern, map_w, map_x, a);
 }
 
-// x: fp16 rows of pitch_x bytes; w: codes on 16 bytes.
 template <int BN, int CG>
-cudaError_t run_shape(bool bf16, const void* x, int64_t pitch_x, const int8_t* w, int64_t ldw, MmaArgs a, cudaStream_t stream) {
+cudaError_t run_cut(const Cut& c, bool bf16, const void* x, const int8_t* w, int64_t ldw, MmaArgs a, cudaStream_t stream) {
     using P = Plan<BN, CG>;
     const int64_t M = a.M, N = a.N, K = a.K;
-    a.xbox = CG == 2 ? P::kBox : static_cast<int>(std::min<int64_t>(BN, M));
-    a.weights_once = M <= BN;
-    const int64_t tiles = (N + CG * kRows - 1) / (CG * kRows) * ((M + BN - 1) / BN);
-    if constexpr (CG == 1) {
-        // K is split over clusters of CTAs where there are fewer tiles than CTAs that the device holds: the fewest stages one after
-        // the other, counting a cluster's sum as two stages
-        const int64_t nk = (K + KS - 1) / KS;
-        int64_t least = 0;
-        for (int ks = 1; ks <= kMaxSplit && (ks == 1 || nk >= 3 * ks); ++ks) {
-            int64_t at_once = static_cast<int64_t>(P::kCtas) * device_sm_count();
-            if (ks > 1) {
-                int clusters = 0;
-                const cudaError_t e = resident_clusters(reinterpret_cast<const void*>(int8_mma_kernel<BN, CG, float>), kThreads,
-                                                        mma_smem<BN, CG>(), 1, ks, &clusters);
-                if (e != cudaSuccess) return e;
-                at_once = clusters;
-                if (tiles > at_once) break;
-            }
-            const int64_t cost = (tiles + at_once - 1) / at_once * ((nk + ks - 1) / ks) + (ks > 1 ? 2 : 0);
-            if (least == 0 || cost < least) least = cost, a.ks = ks;
-        }
-    }
+    a.bn = c.bn, a.ks = c.ks;
+    a.stages = P::stages(c.bn), a.slots = P::slots(c.bn);
+    a.xbox = CG == 2 ? c.bn / CG : static_cast<int>(std::min<int64_t>(c.bn, M));
+    a.weights_once = M <= c.bn;
     CUtensorMap map_w, map_x;
-    if (!encode_rows_map(&map_w, w, N, K, 1, ldw, KS, kRows) || !encode_rows_map(&map_x, x, M, K, 2, pitch_x, 64, a.xbox))
+    if (!encode_rows_map(&map_w, w, N, K, 1, ldw, KS, kRows) || !encode_rows_map(&map_x, x, M, K, 2, (K + 15) / 16 * 32, 64, a.xbox))
         return cudaErrorInvalidValue;
-    return bf16 ? run_mma<BN, CG, __nv_bfloat16>(map_w, map_x, a, tiles, stream)
-                : run_mma<BN, CG, float>(map_w, map_x, a, tiles, stream);
+    return bf16 ? run_mma<BN, CG, __nv_bfloat16>(map_w, map_x, a, c.tiles, stream)
+                : run_mma<BN, CG, float>(map_w, map_x, a, c.tiles, stream);
 }
 
 bool on_16(const Int8View& w) { return reinterpret_cast<uintptr_t>(w.codes) % 16 == 0 && w.ld % 16 == 0; }
@@ -587,14 +599,9 @@ cudaError_t launch_int8_mma(const Int8View& x, const Int8View& w, int64_t K, boo
     }
     MmaArgs a{};
     a.x_scales = x.scales, a.w_scales = w.scales, a.Y = Y, a.err = err;
-    a.M = static_cast<int>(x.rows), a.N = static_cast<int>(w.rows), a.K = static_cast<int>(K), a.ks = 1, a.early = own;
-    const int64_t pitch = per * 32;
-    if (a.M <= 16) return run_shape<16, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
-    if (a.M <= 32) return run_shape<32, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
-    if (a.M <= 64) return run_shape<64, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
-    if (a.M <= 128 || static_cast<int64_t>(a.M + 191) / 192 * ((a.N + 255) / 256) < device_sm_count() / 2)
-        return run_shape<128, 1>(bf16, scratch, pitch, codes, ldw, a, stream);
-    return run_shape<192, 2>(bf16, scratch, pitch, codes, ldw, a, stream);
+    a.M = static_cast<int>(x.rows), a.N = static_cast<int>(w.rows), a.K = static_cast<int>(K), a.early = own;
+    if (a.M <= 64) return run_cut<64, 1>(cut_by<64, 1>(a.M, a.N, a.K), bf16, scratch, codes, ldw, a, stream);
+    return run_cut<192, 2>(cut_by<192, 2>(a.M, a.N, a.K), bf16, scratch, codes, ldw, a, stream);
 }
 
 }  // namespace pnq

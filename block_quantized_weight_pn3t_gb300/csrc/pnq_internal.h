@@ -54,10 +54,6 @@ bool encode_u32_map_pitch(CUtensorMap* map, const void* base, int64_t rows, int6
 bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int elem_bytes, int64_t pitch_bytes, int box_x,
                      int box_y);
 
-// Clusters of x by y CTAs of a kernel (threads and dynamic shared memory given) that the current device holds at once: not every group
-// of SMs divides evenly. Asked once per (kernel, device, x, y).
-cudaError_t resident_clusters(const void* kernel, int threads, int smem, int x, int y, int* clusters);
-
 cudaError_t launch_pn_dequant(int type, const uint8_t* W, int64_t n_rows, int64_t K, float* out,
                               cudaStream_t stream);
 cudaError_t launch_nvfp4_dequant(const Nvfp4View& w, int64_t n_rows, int64_t K, float* out,
