@@ -455,6 +455,15 @@ __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
     return d;
 }
 
+// Four int8 codes -> two f16x2 in order, exact: a code c xor 128 beside the byte 0x64 is the f16 number 1024 + 128 + c, less 1152.
+__device__ __forceinline__ void int8x4_to_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t b = w ^ 0x80808080u;
+    lo = prmt(b, 0x64646464u, 0x4140);
+    hi = prmt(b, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(lo), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(hi), "r"(0x64806480u));
+}
+
 // Two floats -> f16x2 (low half = a), rounded to nearest even, in one conversion instruction.
 __device__ __forceinline__ uint32_t f32x2_to_f16x2(float a, float b) {
     uint32_t d;

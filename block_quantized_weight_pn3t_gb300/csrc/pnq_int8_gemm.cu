@@ -2,7 +2,13 @@
 //   Y[m][n] = (sum_k X[m][k] W[n][k]) x_scale[m] w_scale[n]
 // The sum is exact (32-bit integers), whatever kernel takes a call: results do not hang on the number of rows.
 //
-// Few rows (int8_rows_kernel): the weights stream from HBM through registers and are multiplied by __dp4a; x waits in shared memory.
+// pnq_int8_mma.cu takes more than eight activation rows; here are the fewer ones.
+//
+// Few rows (int8_rows_kernel): bound by HBM. The weights stream through registers, 512 contiguous bytes of a row at a time, and are multiplied by
+// __dp4a (two multiply-adds of 2 x 16 bits or four of 8 are what the CUDA cores do on integers in one instruction); x waits in shared memory. One row
+// of 17408 x 5120 takes 16.3 us (89 MB: 13.1 us at the copy rate), of 5120 x 17408 16.2 us; eight rows 22.8 and 24.8, where the
+// multiplications begin to count. (Through mma.sync on codes widened to fp16, whose fragments want 16 rows of 64 bytes an
+// access: 20.7 and 25.7 us for one row. Through the tensor cores of pnq_int8_mma.cu: 20.8 and 29.9.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -15,11 +21,10 @@
 namespace pnq {
 namespace {
 
-constexpr int kRowThreads = 512;
+constexpr int kRowThreads = 1024;
 constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kGroup = 4;                 // weight rows that a warp takes together: a piece of x serves them all
+constexpr int kGroup = 2;                 // weight rows that a warp takes together: a piece of x serves them all
 constexpr int kBlockRows = 256;           // weight rows of a CTA whose sums are in shared memory at a time
-constexpr int kStepsAhead = 4;            // steps of a warp in flight
 constexpr int kRowSmem = 200 * 1024;      // x
 
 struct RowArgs {
@@ -64,7 +69,7 @@ template <int MT, bool ALIGNED, class T>
 __global__ void __launch_bounds__(kRowThreads, 1) int8_rows_kernel(const RowArgs a) {
     extern __shared__ __align__(16) uint8_t xs[];
     __shared__ int sums[kBlockRows][MT];
-    constexpr int kAhead = kStepsAhead;
+    constexpr int kAhead = MT == 8 ? 2 : 4;  // 64 registers a thread: with eight rows' sums, fewer steps
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int K = a.K, per = (K + 511) / 512, pitch = per * 512;
     const int64_t N = a.N, b = blockIdx.x, g = gridDim.x;
@@ -88,10 +93,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) int8_rows_kernel(const RowArgs
 #pragma unroll
         for (int p = 0; p < kAhead; ++p) load(v[p]);
         if (r0 == first) {
-            for (int m = 0; m < MT; ++m)
-                for (int at = static_cast<int>(threadIdx.x) * 16; at < pitch; at += kRowThreads * 16)
-                    *reinterpret_cast<uint4*>(xs + static_cast<int64_t>(m) * pitch + at) =
-                        m < a.M ? load16<false>(a.X + m * a.ldx, at, K) : make_uint4(0, 0, 0, 0);
+            const bool on16 = (reinterpret_cast<uintptr_t>(a.X) | static_cast<uintptr_t>(a.ldx)) % 16 == 0;
+            for (int i = threadIdx.x; i < MT * (pitch / 16); i += kRowThreads) {
+                const int m = i / (pitch / 16), at = (i - m * (pitch / 16)) * 16;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (m < a.M) v = on16 ? load16<true>(a.X + m * a.ldx, at, K) : load16<false>(a.X + m * a.ldx, at, K);
+                *reinterpret_cast<uint4*>(xs + static_cast<int64_t>(m) * pitch + at) = v;
+            }
         }
         for (int i = threadIdx.x; i < rows * MT; i += kRowThreads) (&sums[0][0])[i] = 0;
         __syncthreads();
@@ -140,7 +148,7 @@ cudaError_t run_rows(const RowArgs& a, cudaStream_t stream) {
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3(static_cast<unsigned>(std::min(device_sm_count(), (a.N + kGroup - 1) / kGroup)));
+    lc.gridDim = dim3(static_cast<unsigned>(std::min(device_sm_count(), (a.N + 3) / 4)));
     lc.blockDim = dim3(kRowThreads);
     lc.dynamicSmemBytes = static_cast<size_t>(smem);
     lc.stream = stream;

@@ -19,11 +19,13 @@
 // released whatever the outcome.
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "pnq_device.cuh"
 #include "pnq_internal.h"
@@ -34,10 +36,7 @@ namespace {
 constexpr int kRows = 128;          // weight rows per CTA and tile (MMA M)
 constexpr int KS = 128;             // K of a stage: one row of shared memory for the weights, two for the activations
 constexpr int kChunkK = 1024;       // K of an accumulator: 1024 * 2^14 = 2^24
-constexpr int kWidenWarps = 4;
 constexpr int kDrainWarps = 8;
-constexpr int kCopyWarp = kWidenWarps + kDrainWarps, kMmaWarp = kCopyWarp + 1;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kMaxStages = 8;
 constexpr int kMaxSlots = 4;
 constexpr int kBand = 16;           // weight tiles of a band
@@ -59,10 +58,11 @@ struct MmaArgs {
     int early;         // the weights are the caller's: no kernel in flight writes them
 };
 
-// Tiles of at most BN activation rows, by CG CTAs.
-template <int BN, int CG>
+// Tiles of at most BN activation rows, by CG CTAs with SETS sets of four warps that widen.
+template <int BN, int CG, int SETS>
 struct Plan {
     static constexpr int kCtas = BN <= 64 ? 2 : 1;             // CTAs of an SM
+    static constexpr int kCopyWarp = 4 * SETS + kDrainWarps, kMmaWarp = kCopyWarp + 1, kThreads = 32 * (kMmaWarp + 1);
     static constexpr int kBound = kCtas == 2 ? 512 : kThreads; // two CTAs of 14 warps share an SM's four register files as two of 16 do
     static constexpr int kStep = 16 * CG;                      // a tile's activation rows are a multiple of it
     static constexpr int kCols = kCtas == 2 ? 256 : 512;       // tensor-memory columns: two accumulators, and the slots
@@ -109,16 +109,6 @@ __device__ __forceinline__ void tc_commit_pair_of(uint32_t bar, uint32_t leader)
         : "memory");
 }
 
-// Four codes -> two fp16 pairs in order.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    const uint32_t b = w ^ 0x80808080u;
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
-    uint32_t p = prmt(b, 0x64646464u, 0x4140), q = prmt(b, 0x64646464u, 0x4342);
-    const __half2 u = __hsub2(*reinterpret_cast<__half2*>(&p), off), v = __hsub2(*reinterpret_cast<__half2*>(&q), off);
-    lo = *reinterpret_cast<const uint32_t*>(&u);
-    hi = *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // The sum as fp32 (one rounding), times both scales in turn.
 __device__ __forceinline__ float scaled(int sum, float x_scale, float w_scale) {
     return __fmul_rn(__fmul_rn(__int2float_rn(sum), x_scale), w_scale);
@@ -151,11 +141,11 @@ struct Walk {
     }
 };
 
-template <int BN, int CG, class T>
-__global__ void __launch_bounds__(Plan<BN, CG>::kBound, Plan<BN, CG>::kCtas) int8_mma_kernel(const __grid_constant__ CUtensorMap map_w,
+template <int BN, int CG, int SETS, class T>
+__global__ void __launch_bounds__(Plan<BN, CG, SETS>::kBound, Plan<BN, CG, SETS>::kCtas) int8_mma_kernel(const __grid_constant__ CUtensorMap map_w,
                                                                                              const __grid_constant__ CUtensorMap map_x,
                                                                                              const MmaArgs a) {
-    using P = Plan<BN, CG>;
+    using P = Plan<BN, CG, SETS>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     __shared__ __align__(8) uint64_t bars[3 * kMaxStages + kMaxSlots + 5];
@@ -180,7 +170,7 @@ __global__ void __launch_bounds__(Plan<BN, CG>::kBound, Plan<BN, CG>::kCtas) int
             mbar_init(full_x(s), 1);
             mbar_init(empty(s), 1);
         }
-        for (int i = 0; i < A; ++i) mbar_init(wide(i), CG * kWidenWarps);
+        for (int i = 0; i < A; ++i) mbar_init(wide(i), CG * 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full(i), 1);
             mbar_init(acc_empty(i), CG * kDrainWarps);
@@ -192,13 +182,13 @@ __global__ void __launch_bounds__(Plan<BN, CG>::kBound, Plan<BN, CG>::kCtas) int
     }
     if constexpr (CG == 2) {
         cluster_sync();  // the pair's barriers exist before either CTA signals them
-        if (warp == kMmaWarp) tmem_alloc_pair(smem_addr(&tmem_slot), P::kCols);
+        if (warp == P::kMmaWarp) tmem_alloc_pair(smem_addr(&tmem_slot), P::kCols);
     } else {
-        if (warp == kMmaWarp) tmem_alloc(smem_addr(&tmem_slot), P::kCols);
+        if (warp == P::kMmaWarp) tmem_alloc(smem_addr(&tmem_slot), P::kCols);
     }
     // nothing above reads what an earlier kernel wrote. Nor do the first copies of the weights below, where they are the caller's own: the
     // pass that widened x has waited for all that came before it, and this kernel begins after that
-    if (!a.early || warp != kCopyWarp) griddep_wait();
+    if (!a.early || warp != P::kCopyWarp) griddep_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -209,7 +199,7 @@ __global__ void __launch_bounds__(Plan<BN, CG>::kBound, Plan<BN, CG>::kCtas) int
     Walk<CG> walk(a);
     Tile tile{};
 
-    if (warp == kCopyWarp) {
+    if (warp == P::kCopyWarp) {
         if (elect_one()) {
             const uint64_t pol_x = l2_policy_evict_last(), pol_w = a.weights_once ? l2_policy_evict_first() : pol_x;
             bool ok = true;
@@ -258,7 +248,7 @@ __global__ void __launch_bounds__(Plan<BN, CG>::kBound, Plan<BN, CG>::kCtas) int
             }
             if (!drained) record_error(a.err, kErrDrainWait);
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == P::kMmaWarp) {
         if (rank == 0 && elect_one()) {
             auto commit = [&](uint32_t bar) {
                 if constexpr (CG == 2) tc_commit_pair_of(bar, pair_leader());
@@ -301,14 +291,20 @@ __global__ void __launch_bounds__(Plan<BN, CG>::kBound, Plan<BN, CG>::kCtas) int
             else tc_commit(finished);
             if (!mbar_wait_cycles(finished, 0)) record_error(a.err, kErrDrainWait);
         }
-    } else if (warp < kWidenWarps) {
-        const int row = 32 * warp + lane;
-        const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+    } else if (warp < 4 * SETS) {
+        const int row = 32 * (warp & 3) + lane, set = warp >> 2;  // the sets take the stages in turn
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         bool ok = true;
         int i = 0, s = 0, slot = 0, es = 0;   // es, ephase: the stage whose MMAs were the slot's last, A stages before
         uint32_t phase = 0, ephase = 0;
+        auto step = [&] {
+            if (++s == S) s = 0, phase ^= 1;
+            if (++slot == A) slot = 0;
+            if (i++ >= A && ++es == S) es = 0, ephase ^= 1;
+        };
         while (ok && walk.next(tile)) {
-            for (int kt = kt0; kt < kt1; ++kt, ++i) {
+            for (int kt = kt0; kt < kt1; ++kt, step()) {
+                if (SETS == 2 && (i & 1) != set) continue;
                 ok = mbar_wait_cycles_warp(full_w(s), phase);
                 if (!ok) break;
                 const uint32_t src = sbase + static_cast<uint32_t>(s) * stage + x_bytes + static_cast<uint32_t>(row * KS);
@@ -316,18 +312,13 @@ __global__ void __launch_bounds__(Plan<BN, CG>::kBound, Plan<BN, CG>::kCtas) int
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const uint4 w = ld_shared_v4<0>(src + 16 * ((2 * h + c) ^ (row & 7)));
-                        widen4(w.x, v[8 * c], v[8 * c + 1]);
-                        widen4(w.y, v[8 * c + 2], v[8 * c + 3]);
-                        widen4(w.z, v[8 * c + 4], v[8 * c + 5]);
-                        widen4(w.w, v[8 * c + 6], v[8 * c + 7]);
+                        int8x4_to_f16x2(w.x, v[8 * c], v[8 * c + 1]);
+                        int8x4_to_f16x2(w.y, v[8 * c + 2], v[8 * c + 3]);
+                        int8x4_to_f16x2(w.z, v[8 * c + 4], v[8 * c + 5]);
+                        int8x4_to_f16x2(w.w, v[8 * c + 6], v[8 * c + 7]);
                     }
                 };
-                auto slot_free = [&] {
-                    if (i < A) return true;
-                    const bool free = mbar_wait_cycles_warp(empty(es), ephase);
-                    if (++es == S) es = 0, ephase ^= 1;
-                    return free;
-                };
+                auto slot_free = [&] { return i < A || mbar_wait_cycles_warp(empty(es), ephase); };
                 auto slot_at = [&](int h) { return slots + static_cast<uint32_t>(slot * kSlotCols + 16 * h) + lanes; };
                 if constexpr (P::kCtas == 1) {  // the whole row in registers while the slot is waited for
                     uint32_t v[KS / 32][16];
@@ -356,14 +347,12 @@ __global__ void __launch_bounds__(Plan<BN, CG>::kBound, Plan<BN, CG>::kCtas) int
                     if constexpr (CG == 2) mbar_arrive_cluster_relaxed(cluster_addr(wide(slot), pair_leader()));
                     else mbar_arrive(wide(slot));
                 }
-                if (++s == S) s = 0, phase ^= 1;
-                if (++slot == A) slot = 0;
             }
         }
         if (!ok && lane == 0) record_error(a.err, kErrOperandWait);
         tc_fence_before();
     } else {
-        const int q = warp & 3, half = (warp - kWidenWarps) >> 2;  // lanes 32 q .. of tensor memory, half of the columns
+        const int q = warp & 3, half = (warp - 4 * SETS) >> 2;  // lanes 32 q .. of tensor memory, half of the columns
         constexpr int kHalf = BN / 2, kLoad = P::kStep / 2;
         const int columns = bn / 2;  // a multiple of kLoad
         T* Y = static_cast<T*>(a.Y);
@@ -433,7 +422,7 @@ __global__ void __launch_bounds__(Plan<BN, CG>::kBound, Plan<BN, CG>::kCtas) int
         if (again.next(tile)) {
             T* Y = static_cast<T*>(a.Y);
             const int c0 = kz * tile.rows / a.ks, c1 = (kz + 1) * tile.rows / a.ks;
-            for (int e = static_cast<int>(threadIdx.x); e < (c1 - c0) * (kRows / 4); e += kThreads) {
+            for (int e = static_cast<int>(threadIdx.x); e < (c1 - c0) * (kRows / 4); e += P::kThreads) {
                 const int c = c0 + e / (kRows / 4), r = 4 * (e % (kRows / 4)), m = tile.row0 + c, n = tile.n0 + static_cast<int>(rank) * kRows + r;
                 const uint32_t at = sbase + 4u * static_cast<uint32_t>(c * kRows + r);
                 float4 v[P::kSplit];
@@ -456,7 +445,7 @@ __global__ void __launch_bounds__(Plan<BN, CG>::kBound, Plan<BN, CG>::kCtas) int
         }
         cluster_sync();  // no CTA leaves while another still reads its tile
     }
-    if (warp == kMmaWarp) {
+    if (warp == P::kMmaWarp) {
         tc_fence_after();
         if constexpr (CG == 2) tmem_dealloc_pair(tmem, P::kCols);
         else tmem_dealloc(tmem, P::kCols);
@@ -487,10 +476,10 @@ __global__ void __launch_bounds__(256) int8_rows_copy_kernel(const int8_t* X, in
         const uint4 w = load16<ALIGNED>(X + r * ld, 16 * c, K);
         if constexpr (WIDEN) {
             uint4 a, b;
-            widen4(w.x, a.x, a.y);
-            widen4(w.y, a.z, a.w);
-            widen4(w.z, b.x, b.y);
-            widen4(w.w, b.z, b.w);
+            int8x4_to_f16x2(w.x, a.x, a.y);
+            int8x4_to_f16x2(w.y, a.z, a.w);
+            int8x4_to_f16x2(w.z, b.x, b.y);
+            int8x4_to_f16x2(w.w, b.z, b.w);
             out[2 * u] = a;
             out[2 * u + 1] = b;
         } else {
@@ -510,40 +499,79 @@ cudaError_t copy_rows(const int8_t* X, int64_t ld, int64_t rows, int64_t K, void
 
 // ---- launches ------------------------------------------------------------------------------------------
 
-// How a product is cut: tiles of bn activation rows and cg * 128 weight rows, and the CTAs (pairs) that share a tile's K.
+// How a product is cut: tiles of bn activation rows, and the CTAs (pairs) that share a tile's K.
 struct Cut {
-    int bn, cg, ks;
-    int64_t tiles;
+    int bn, ks;
+    int64_t tiles, stages;  // stages: one after the other
 };
 
-template <int BN, int CG>
-Cut cut_by(int64_t M, int64_t N, int64_t K) {
-    using P = Plan<BN, CG>;
-    const int64_t mt = (M + BN - 1) / BN, nk = (K + KS - 1) / KS, units = static_cast<int64_t>(P::kCtas) * device_sm_count() / CG;
-    Cut c{};
-    c.bn = static_cast<int>(((M + mt - 1) / mt + P::kStep - 1) / P::kStep * P::kStep);
-    c.cg = CG;
-    c.tiles = (N + CG * kRows - 1) / (CG * kRows) * mt;
-    double least = 0.0;
-    for (int ks = 1; ks <= P::kSplit && (ks == 1 || nk >= 2 * ks); ++ks) {
-        const double cost = static_cast<double>((c.tiles * ks + units - 1) / units * ((nk + ks - 1) / ks)) + (ks > 1 ? 3.0 : 0.0);
-        if (ks == 1 || cost < least) least = cost, c.ks = ks;
+// Clusters of CG by ks CTAs of a kernel that the current device holds at once (not every group of SMs divides evenly). The runtime counts one CTA
+// an SM for kernels that allocate tensor memory; two fit where theirs is half of it.
+template <int BN, int CG, int SETS>
+cudaError_t resident(int ks, int smem, int* clusters) {
+    using P = Plan<BN, CG, SETS>;
+    static std::mutex mu;
+    static std::map<std::pair<int, int>, int> known;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    int& n = known[{dev, ks}];
+    if (n == 0) {
+        const void* kernel = reinterpret_cast<const void*>(int8_mma_kernel<BN, CG, SETS, float>);
+        e = opt_in_smem(kernel, smem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t lc{};
+        lc.gridDim = dim3(static_cast<unsigned>(CG * device_sm_count()), static_cast<unsigned>(ks));
+        lc.blockDim = dim3(P::kThreads);
+        lc.dynamicSmemBytes = static_cast<size_t>(smem);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = CG;
+        attr[0].val.clusterDim.y = static_cast<unsigned>(ks);
+        attr[0].val.clusterDim.z = 1;
+        lc.attrs = attr;
+        lc.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &lc);
+        if (e != cudaSuccess) return e;
+        n = std::max(n, 1);
     }
-    return c;
+    *clusters = n * P::kCtas;
+    return cudaSuccess;
 }
 
-template <int BN, int CG, class T>
+// The tiles of a product, and over how many CTAs (pairs) K is split: so that the fewest stages come one after the other, with a cluster's sum
+// counted as three. K is split only where all clusters run at once: a second round of them costs more than a split gains.
+template <int BN, int CG, int SETS>
+cudaError_t cut_by(int64_t M, int64_t N, int64_t K, Cut* c) {
+    using P = Plan<BN, CG, SETS>;
+    const int64_t mt = (M + BN - 1) / BN, nk = (K + KS - 1) / KS;
+    c->bn = static_cast<int>(((M + mt - 1) / mt + P::kStep - 1) / P::kStep * P::kStep);
+    c->tiles = (N + CG * kRows - 1) / (CG * kRows) * mt;
+    c->ks = 1;
+    c->stages = (c->tiles * CG + P::kCtas * device_sm_count() - 1) / (P::kCtas * device_sm_count()) * nk;
+    for (int ks = 2; ks <= P::kSplit && nk >= 2 * ks; ++ks) {
+        int clusters = 0;
+        const cudaError_t e = resident<BN, CG, SETS>(ks, P::stages(c->bn) * P::stage(c->bn) + 1024, &clusters);
+        if (e != cudaSuccess) return e;
+        const int64_t stages = (nk + ks - 1) / ks + 3;
+        if (c->tiles <= clusters && stages < c->stages) c->stages = stages, c->ks = ks;
+    }
+    return cudaSuccess;
+}
+
+template <int BN, int CG, int SETS, class T>
 cudaError_t run_mma(const CUtensorMap& map_w, const CUtensorMap& map_x, const MmaArgs& a, int64_t tiles, cudaStream_t stream) {
-    using P = Plan<BN, CG>;
+    using P = Plan<BN, CG, SETS>;
     const int smem = a.stages * P::stage(a.bn) + 1024;
-    auto kern = int8_mma_kernel<BN, CG, T>;
+    auto kern = int8_mma_kernel<BN, CG, SETS, T>;
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc{};
     // K split: one tile a cluster; otherwise as many CTAs as the device holds at once, each over its tiles
     const int64_t units = static_cast<int64_t>(P::kCtas) * device_sm_count() / CG;
     lc.gridDim = dim3(static_cast<unsigned>(CG * (a.ks > 1 ? tiles : std::min(tiles, units))), static_cast<unsigned>(a.ks));
-    lc.blockDim = dim3(kThreads);
+    lc.blockDim = dim3(P::kThreads);
     lc.dynamicSmemBytes = static_cast<size_t>(smem);
     lc.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -558,10 +586,13 @@ cudaError_t run_mma(const CUtensorMap& map_w, const CUtensorMap& map_x, const Mm
     return cudaLaunchKernelEx(&lc, kern, map_w, map_x, a);
 }
 
-template <int BN, int CG>
-cudaError_t run_cut(const Cut& c, bool bf16, const void* x, const int8_t* w, int64_t ldw, MmaArgs a, cudaStream_t stream) {
-    using P = Plan<BN, CG>;
+template <int BN, int CG, int SETS>
+cudaError_t run_cut(bool bf16, const void* x, const int8_t* w, int64_t ldw, MmaArgs a, cudaStream_t stream) {
+    using P = Plan<BN, CG, SETS>;
     const int64_t M = a.M, N = a.N, K = a.K;
+    Cut c{};
+    const cudaError_t e = cut_by<BN, CG, SETS>(M, N, K, &c);
+    if (e != cudaSuccess) return e;
     a.bn = c.bn, a.ks = c.ks;
     a.stages = P::stages(c.bn), a.slots = P::slots(c.bn);
     a.xbox = CG == 2 ? c.bn / CG : static_cast<int>(std::min<int64_t>(c.bn, M));
@@ -569,8 +600,8 @@ cudaError_t run_cut(const Cut& c, bool bf16, const void* x, const int8_t* w, int
     CUtensorMap map_w, map_x;
     if (!encode_rows_map(&map_w, w, N, K, 1, ldw, KS, kRows) || !encode_rows_map(&map_x, x, M, K, 2, (K + 15) / 16 * 32, 64, a.xbox))
         return cudaErrorInvalidValue;
-    return bf16 ? run_mma<BN, CG, __nv_bfloat16>(map_w, map_x, a, c.tiles, stream)
-                : run_mma<BN, CG, float>(map_w, map_x, a, c.tiles, stream);
+    return bf16 ? run_mma<BN, CG, SETS, __nv_bfloat16>(map_w, map_x, a, c.tiles, stream)
+                : run_mma<BN, CG, SETS, float>(map_w, map_x, a, c.tiles, stream);
 }
 
 bool on_16(const Int8View& w) { return reinterpret_cast<uintptr_t>(w.codes) % 16 == 0 && w.ld % 16 == 0; }
@@ -600,8 +631,9 @@ cudaError_t launch_int8_mma(const Int8View& x, const Int8View& w, int64_t K, boo
     MmaArgs a{};
     a.x_scales = x.scales, a.w_scales = w.scales, a.Y = Y, a.err = err;
     a.M = static_cast<int>(x.rows), a.N = static_cast<int>(w.rows), a.K = static_cast<int>(K), a.early = own;
-    if (a.M <= 64) return run_cut<64, 1>(cut_by<64, 1>(a.M, a.N, a.K), bf16, scratch, codes, ldw, a, stream);
-    return run_cut<192, 2>(cut_by<192, 2>(a.M, a.N, a.K), bf16, scratch, codes, ldw, a, stream);
+    if (a.M <= 64) return run_cut<64, 1, 1>(bf16, scratch, codes, ldw, a, stream);
+    if (a.M <= 128) return run_cut<128, 2, 2>(bf16, scratch, codes, ldw, a, stream);
+    return run_cut<192, 2, 1>(bf16, scratch, codes, ldw, a, stream);
 }
 
 }  // namespace pnq
