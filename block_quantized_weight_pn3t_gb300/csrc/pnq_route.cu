@@ -6,7 +6,7 @@
 //
 // Which of two scores is the larger must not hang on a rounding. Without bias and groups the logits themselves are compared. Otherwise
 // c is computed in fp32 with a bound on its error (route_kernel), and a row in which two scores that decide anything are nearer than that,
-// and are not of equal logits and equal biases, is done again in 64 bits (a few rows in a thousand).
+// and are not of equal logits and equal biases, is done again with scores of some 2^-44 (a few rows in a thousand).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -20,7 +20,8 @@
 namespace pnq {
 namespace {
 
-constexpr int kWarps = 4;          // tokens of a CTA
+constexpr int kWarps = 4;          // of a CTA
+constexpr int kCtas = 8;           // of an SM at most
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kNone = -INFINITY;  // the score of an expert that is out
 
@@ -86,273 +87,356 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
     return v;
 }
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
-    return v;
-}
-
-// Whole numbers in the order of the values (-0 as +0); 0 is below them all: an expert that is out.
-__device__ __forceinline__ uint32_t order_key(float v) {
-    const uint32_t b = __float_as_uint(v + 0.0f);
-    return v == kNone ? 0u : b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t key) {
-    return key == 0 ? kNone : __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+// The largest of a warp's values in one instruction (no NaN among them).
+__device__ __forceinline__ float redux_max(float v) {
+    float d;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+    return d;
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// The row again in 64 bits. c: E doubles of shared memory of this warp; x: the row's logits there. Returns slots lane and lane + 32 of the
-// token's experts.
-__device__ __noinline__ int2 route_exact(const RouteArgs& a, const float* x, double* c, int lane) {
-    int2 id = make_int2(-1, -1);
-    double top = -INFINITY, sum = 0.0;
-    for (int e = lane; e < a.E; e += 32) top = fmax(top, static_cast<double>(x[e]));
+// ---- scores to some 2^-44, as unevaluated sums of two floats (T. J. Dekker 1971, D. E. Knuth) ---------------
+// (64-bit arithmetic runs at 1/64 of the rate of 32-bit here: the same row took 15 us in doubles.)
+
+struct Two {
+    float hi, lo;  // |lo| <= half an ulp of hi
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two fast_sum(float a, float b) {  // |a| >= |b|
+    const float s = __fadd_rn(a, b);
+    return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    const Two s = two_sum(a.hi, b.hi), t = two_sum(a.lo, b.lo), u = fast_sum(s.hi, __fadd_rn(s.lo, t.hi));
+    return fast_sum(u.hi, __fadd_rn(u.lo, t.lo));
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    const float p = __fmul_rn(a.hi, b.hi);
+    return fast_sum(p, fmaf(a.hi, b.lo, fmaf(a.lo, b.hi, fmaf(a.hi, b.hi, -p))));
+}
+__device__ __forceinline__ Two inverse(Two a) {  // Newton's step, 2 - a q, from the fp32 quotient
+    const float q = __fdiv_rn(1.0f, a.hi), e = fmaf(-a.lo, q, fmaf(-a.hi, q, 1.0f));
+    return fast_sum(q, __fmul_rn(q, e));
+}
+
+// exp(d) for d <= 0: d = n log 2 + r, the series of exp(r) (|r| <= 0.35; terms from r^8 / 8! on weigh below 2^-27, in fp32), times 2^n. Below
+// 2^-125: zero.
+__device__ Two exp_two(Two d) {
+    if (!(d.hi > -86.6f)) return {0.0f, 0.0f};
+    const float n = rintf(d.hi * 1.44269504f);
+    // log 2 = 0x1.62e4p-1 + 0x1.7f7d1cp-20 + ..: n times the first part is exact
+    const Two t = two_sum(d.hi, -n * 0x1.62e4p-1f);
+    const float p = __fmul_rn(n, 0x1.7f7d1cp-20f), e = fmaf(n, 0x1.7f7d1cp-20f, -p);
+    const Two r = t + Two{-p, -e} + Two{d.lo, n * -0x1.ef357ap-45f};
+    constexpr double kInverse[] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040};  // 1 / k!
+    const float x = r.hi;
+    float high = 1.0f / 479001600;  // r^8 (1 / 8! + r / 9! + r^2 / 10! + r^3 / 11! + r^4 / 12!)
+    high = fmaf(high, x, 1.0f / 39916800);
+    high = fmaf(high, x, 1.0f / 3628800);
+    high = fmaf(high, x, 1.0f / 362880);
+    high = fmaf(high, x, 1.0f / 40320);
+    Two sum{__fmul_rn(high, x), 0.0f};
 #pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, d));
-    for (int e = lane; e < a.E; e += 32) {
-        const double v = x[e];
-        c[e] = a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - top);
-        sum += c[e];
+    for (int k = 7; k >= 0; --k) {
+        const float c = static_cast<float>(kInverse[k]), l = static_cast<float>(kInverse[k] - static_cast<double>(c));
+        sum = sum + Two{c, l};
+        if (k > 0) sum = sum * r;
     }
-    sum = a.sigmoid ? 1.0 : warp_sum(sum);
+    const float scale = __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23);  // n >= -125
+    return {sum.hi * scale, sum.lo * scale};
+}
+
+// Whole numbers in the order of the values (-0 as +0).
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ uint64_t order_key(Two v) { return static_cast<uint64_t>(order_key(v.hi)) << 32 | order_key(v.lo); }
+__device__ __forceinline__ Two key_value(uint64_t key) {
+    auto value = [](uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); };
+    return {value(static_cast<uint32_t>(key >> 32)), value(static_cast<uint32_t>(key))};
+}
+
+// The row again with such scores. c: E keys of shared memory of this warp (0: an expert that is out); x: the row's logits there. Equal scores
+// go by the logits, then by the index. Returns slots lane and lane + 32 of the token's experts.
+__device__ __noinline__ int2 route_exact(const RouteArgs& a, const float* x, const float* bias, uint64_t* c, int lane) {
+    int2 id = make_int2(-1, -1);
+    Two scale{1.0f, 0.0f};
+    float top = kNone;
+    if (!a.sigmoid) {
+        for (int e = lane; e < a.E; e += 32) top = fmaxf(top, x[e]);
+        top = redux_max(top);
+        Two sum{0.0f, 0.0f};
+        for (int e = lane; e < a.E; e += 32)
+            if (x[e] != kNone) sum = sum + exp_two(two_sum(x[e], -top));
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum = sum + Two{__shfl_xor_sync(kAll, sum.hi, d), __shfl_xor_sync(kAll, sum.lo, d)};
+        scale = inverse(sum);
+    }
     for (int e = lane; e < a.E; e += 32) {
-        const double b = a.bias ? static_cast<double>(ld_l2(a.bias + e)) : 0.0;
-        c[e] = x[e] == kNone ? -INFINITY : c[e] / sum + b;
+        uint64_t key = 0;
+        const float b = a.bias ? bias[e] : 0.0f;
+        if (x[e] != kNone && b != kNone) {
+            Two s;
+            if (a.sigmoid) {
+                const Two z = exp_two({-fabsf(x[e]), 0.0f}), w = inverse(z + Two{1.0f, 0.0f});
+                s = x[e] >= 0.0f ? w : w * z;
+            } else {
+                s = exp_two(two_sum(x[e], -top)) * scale;
+            }
+            key = order_key(s + Two{b, 0.0f});
+        }
+        c[e] = key;
     }
     __syncwarp();
     if (a.groups > 1) {
-        double b1 = -INFINITY, b2 = -INFINITY;
+        uint64_t b1 = 0, b2 = 0;
         if (lane < a.groups) {
             for (int j = 0; j < a.per; ++j) {
-                const double v = c[lane * a.per + j];
+                const uint64_t v = c[lane * a.per + j];
                 if (v > b1) b2 = b1, b1 = v;
                 else if (v > b2) b2 = v;
             }
         }
-        const double score = a.best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+        const uint64_t score = a.best == 2 && b2 ? order_key(key_value(b1) + key_value(b2)) : b1;
         int rank = 0;
         for (int h = 0; h < a.groups; ++h) {
-            const double other = __shfl_sync(kAll, score, h);
+            const uint64_t other = __shfl_sync(kAll, score, h);
             rank += other > score || (other == score && h < lane);
         }
         const uint32_t kept = __ballot_sync(kAll, lane < a.groups && rank < a.top_groups);
         for (int e = lane; e < a.E; e += 32)
-            if (!(kept >> (e / a.per) & 1)) c[e] = -INFINITY;
+            if (!(kept >> (e / a.per) & 1)) c[e] = 0;
         __syncwarp();
     }
     for (int j = 0; j < a.k; ++j) {
-        double v = -INFINITY;
+        uint64_t v = 0;
+        uint32_t tie = 0;  // the logit, in order
         int at = a.E;
-        for (int e = lane; e < a.E; e += 32)
-            if (c[e] > v) v = c[e], at = e;
+        for (int e = lane; e < a.E; e += 32) {
+            const uint64_t key = c[e];
+            const uint32_t logit = order_key(x[e]);
+            if (key > v || (key == v && key && logit > tie)) v = key, tie = logit, at = e;
+        }
 #pragma unroll
         for (int d = 16; d; d >>= 1) {
-            const double ov = __shfl_xor_sync(kAll, v, d);
+            const uint64_t ov = __shfl_xor_sync(kAll, v, d);
+            const uint32_t otie = __shfl_xor_sync(kAll, tie, d);
             const int oat = __shfl_xor_sync(kAll, at, d);
-            if (ov > v || (ov == v && oat < at)) v = ov, at = oat;
+            if (ov > v || (ov == v && (otie > tie || (otie == tie && oat < at)))) v = ov, tie = otie, at = oat;
         }
-        if (lane == (j & 31)) (j < 32 ? id.x : id.y) = at < a.E ? at : -1;
-        if (at < a.E && lane == (at & 31)) c[at] = -INFINITY;
+        if (v == 0) break;  // no expert is left
+        if (lane == (j & 31)) (j < 32 ? id.x : id.y) = at;
+        if (lane == (at & 31)) c[at] = 0;
         __syncwarp();
     }
     return id;
 }
 
-// Shared memory of a warp: the row's logits, and behind them the groups' scores (each group on an odd pitch) or 64-bit scores.
+// Shared memory of a warp: the row's logits, and behind them the groups' scores (each group on an odd pitch) or the keys above.
 __host__ __device__ inline int route_floats(int E) { return E + (E & 1) + 2 * E + 32; }
 
+// A warp takes token after token, the next one's logits on their way meanwhile. The bias is read once a CTA: by every warp for every token, out
+// of the same few lines of L2, it took more time than all the rest (16384 tokens of 256 experts: 25 of 45 us).
 template <class T, int NE, int V>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
     extern __shared__ __align__(16) float shared[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    float* xs = shared + warp * route_floats(a.E);
+    float* bs = shared;  // [E] bias, in whole 16 bytes
+    float* xs = shared + (a.E + 3) / 4 * 4 + warp * route_floats(a.E);
     float* cs = xs + a.E + (a.E & 1);
     griddep_begin();
-    if (t >= a.tokens) return;
-    float x[NE];
-    load_row<T, NE, V>(static_cast<const T*>(a.logits) + t * a.ld, a.E, lane, x);
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-        if (element<V>(i, lane) < a.E) xs[element<V>(i, lane)] = x[i];
-
-    // scores; a NaN, or an infinity that is not an expert taken out, makes the whole row NaN
-    float m = kNone, sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) m = fmaxf(m, x[i]);
-    m = warp_max(m);
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) bad |= isnan(x[i]);
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+    const T* logits = static_cast<const T*>(a.logits);
+    float coming[NE];
+    if (t < a.tokens) load_row<T, NE, V>(logits + t * a.ld, a.E, lane, coming);
+    if (a.bias) {
+        for (int e = threadIdx.x; e < a.E; e += 32 * kWarps) bs[e] = ld_l2(a.bias + e);
+    }
+    __syncthreads();
     const bool by_logit = !a.bias && a.groups == 1;
-    float s[NE];
-    if (!a.sigmoid) {
-        bad |= m == INFINITY;
+    for (; t < a.tokens; t += step) {
+        float x[NE];
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            s[i] = x[i] == kNone ? 0.0f : expf(x[i] - m);
-            sum += s[i];
-        }
-        sum = warp_sum(sum);
-        if (!by_logit) {
+        for (int i = 0; i < NE; ++i) x[i] = coming[i];
+        if (t + step < a.tokens) load_row<T, NE, V>(logits + (t + step) * a.ld, a.E, lane, coming);
+        __syncwarp();  // the last token's scores have been read
 #pragma unroll
-            for (int i = 0; i < NE; ++i) s[i] = s[i] / sum;
-        }
-    } else if (!by_logit) {
-#pragma unroll
-        for (int i = 0; i < NE; ++i) s[i] = sigmoid(x[i]);
-    }
-    uint32_t key[NE];
-    float cmax = 0.0f;
-    if (by_logit) {
-#pragma unroll
-        for (int i = 0; i < NE; ++i) key[i] = order_key(x[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int e = element<V>(i, lane);
-            float c = x[i] == kNone ? kNone : a.bias ? s[i] + ld_l2(a.bias + e) : s[i];
-            bad |= isnan(c) || c == INFINITY;
-            if (c != kNone) cmax = fmaxf(cmax, fabsf(c));
-            key[i] = order_key(c);
-        }
-        cmax = warp_max(cmax);
-    }
-    bad = __any_sync(kAll, bad);
+        for (int i = 0; i < NE; ++i)
+            if (element<V>(i, lane) < a.E) xs[element<V>(i, lane)] = x[i];
 
-    int id[2] = {-1, -1};
-    if (bad) {
-        id[0] = lane, id[1] = lane + 32;
-    } else {
-        // How far two computed scores of different order may be apart. Sigmoid: expf is within 2 ulp and s (1 - s) <= 1/4, so s is within
-        // 3 * 2^-24, twice that for two. Softmax: an exponential is within 2^-22 of itself and its argument's rounding adds (m - x) 2^-24; the
-        // sum, E / 32 + 5 additions of such, is within 1.5 * 2^-19 and moves a difference by that times the larger score. The addition
-        // of the bias rounds by half an ulp of c.
-        const float smax = 1.0f / sum;  // softmax: the score of the largest logit
-        const float tol = (a.sigmoid ? 0x1p-21f : 0x1p-18f * smax + 0x1p-24f) + 0x1p-23f * cmax;
-        bool near = false;
-        if (a.groups > 1) {
-            const int pitch = a.per | 1;
+        // scores c; a NaN, or an infinity that is not an expert taken out, makes the whole row NaN
+        float m = kNone, sum = 0.0f, smax = 1.0f, cmax = 0.0f, c[NE];
+        bool bad = false;
+        if (!a.sigmoid) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) m = fmaxf(m, x[i]);
+            m = redux_max(m);
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
-                const int e = element<V>(i, lane), g = static_cast<int>(e * a.per_magic >> 20);
-                if (e < a.E) cs[g * pitch + e - g * a.per] = key_value(key[i]);
+                bad |= !(x[i] < INFINITY);
+                c[i] = x[i] == kNone ? 0.0f : expf(x[i] - m);
+                sum += c[i];
             }
-            __syncwarp();
-            // the largest power of two of lanes that a group can have: its best two by them
-            const int lanes = 1 << (31 - __clz(32 / a.groups)), g = lane / lanes;
-            float b1 = kNone, b2 = kNone;
-            if (g < a.groups) {
-                for (int j = lane & (lanes - 1); j < a.per; j += lanes) {
-                    const float v = cs[g * pitch + j];
-                    b2 = fmaxf(b2, fminf(b1, v));
-                    b1 = fmaxf(b1, v);
-                }
-            }
-            for (int d = lanes >> 1; d; d >>= 1) {
-                const float o1 = __shfl_xor_sync(kAll, b1, d), o2 = __shfl_xor_sync(kAll, b2, d);
-                b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
-                b1 = fmaxf(b1, o1);
-            }
-            const float score = a.best == 2 && b2 != kNone ? b1 + b2 : b1;
-            int rank = 0;
-            for (int h = 0; h < a.groups; ++h) {
-                const float other = __shfl_sync(kAll, score, h * lanes);
-                rank += other > score || (other == score && h < g);
-            }
-            const bool stays = g < a.groups && rank < a.top_groups;
-            const uint32_t kept = __ballot_sync(kAll, stays);
-            const float least = -warp_max(stays ? -score : kNone), most = warp_max(g < a.groups && !stays ? score : kNone);
-            near |= most != kNone && least - most <= 2.0f * tol + 0x1p-22f * cmax;
+            sum = warp_sum(sum);
+            smax = 1.0f / sum;  // the score of the largest logit
+        } else {
 #pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                const int e = element<V>(i, lane), of = static_cast<int>(e * a.per_magic >> 20);
-                if (e < a.E && !(kept >> (of * lanes) & 1)) key[i] = 0;
-            }
+            for (int i = 0; i < NE; ++i) bad |= isnan(x[i]);
         }
-        uint32_t mine = 0, won[2] = {0, 0};
+        if (by_logit) {
 #pragma unroll
-        for (int i = 0; i < NE; ++i) mine = max(mine, key[i]);
-        for (int j = 0; j < a.k; ++j) {
-            const uint32_t most = __reduce_max_sync(kAll, mine);
-            if (most == 0) break;  // no expert is left
-            int at = a.E;
-            if (mine == most) {
+            for (int i = 0; i < NE; ++i) c[i] = x[i];
+        } else {
 #pragma unroll
-                for (int i = NE - 1; i >= 0; --i)
-                    if (key[i] == most) at = element<V>(i, lane);
+            for (int i = 0; i < NE; ++i) {
+                const int e = element<V>(i, lane);
+                float s = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-x[i])) : c[i] * smax;
+                if (x[i] < -87.0f) s = 0.0f;
+                if (a.bias && e < a.E) s += bs[e];
+                bad |= !(s < INFINITY);
+                c[i] = x[i] == kNone ? kNone : s;
+                if (c[i] != kNone) cmax = fmaxf(cmax, fabsf(c[i]));
             }
-            const int e = static_cast<int>(__reduce_min_sync(kAll, static_cast<uint32_t>(at)));
-            if (at == e) {
-                mine = 0;
+            cmax = redux_max(cmax);
+        }
+        bad = __any_sync(kAll, bad);
+
+        int id[2] = {-1, -1};
+        if (bad) {
+            id[0] = lane, id[1] = lane + 32;
+        } else {
+            // How far two computed scores of different order may be apart. Sigmoid: __expf is within (2 + 1.18 |x|) ulp and s (1 - s) (2 + 1.18 |x|) <= 0.58;
+            // the quotient is within 2 ulp: s within 2.6 * 2^-23, twice that for two. Softmax: an exponential is within 2^-22 of itself
+            // and its argument's rounding adds (m - x) 2^-24; the sum, E / 32 + 5 additions of such, is within 1.5 * 2^-19 and moves a difference by
+            // that times the larger score. The addition of the bias rounds by half an ulp of c.
+            const float tol = (a.sigmoid ? 0x1.6p-21f : 0x1p-18f * smax + 0x1p-24f) + 0x1p-23f * cmax;
+            bool near = false;
+            if (a.groups > 1) {
+                const int pitch = a.per | 1;
 #pragma unroll
                 for (int i = 0; i < NE; ++i) {
-                    if (element<V>(i, lane) == e) key[i] = 0;
-                    mine = max(mine, key[i]);
+                    const int e = element<V>(i, lane), g = static_cast<int>(e * a.per_magic >> 20);
+                    if (e < a.E) cs[g * pitch + e - g * a.per] = c[i];
+                }
+                __syncwarp();
+                // the largest power of two of lanes that a group can have: its best two by them
+                const int lanes = 1 << (31 - __clz(32 / a.groups)), g = lane / lanes;
+                float b1 = kNone, b2 = kNone;
+                if (g < a.groups) {
+                    for (int j = lane & (lanes - 1); j < a.per; j += lanes) {
+                        const float v = cs[g * pitch + j];
+                        b2 = fmaxf(b2, fminf(b1, v));
+                        b1 = fmaxf(b1, v);
+                    }
+                }
+                for (int d = lanes >> 1; d; d >>= 1) {
+                    const float o1 = __shfl_xor_sync(kAll, b1, d), o2 = __shfl_xor_sync(kAll, b2, d);
+                    b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+                    b1 = fmaxf(b1, o1);
+                }
+                const float score = a.best == 2 && b2 != kNone ? b1 + b2 : b1;
+                int rank = 0;
+                for (int h = 0; h < a.groups; ++h) {
+                    const float other = __shfl_sync(kAll, score, h * lanes);
+                    rank += other > score || (other == score && h < g);
+                }
+                const bool stays = g < a.groups && rank < a.top_groups;
+                const uint32_t kept = __ballot_sync(kAll, stays);
+                const float least = -redux_max(stays ? -score : kNone), most = redux_max(g < a.groups && !stays ? score : kNone);
+                near |= most != kNone && least - most <= 2.0f * tol + 0x1p-22f * cmax;
+#pragma unroll
+                for (int i = 0; i < NE; ++i) {
+                    const int e = element<V>(i, lane), of = static_cast<int>(e * a.per_magic >> 20);
+                    if (e < a.E && !(kept >> (of * lanes) & 1)) c[i] = kNone;
                 }
             }
-            if (lane == j) id[0] = e, won[0] = most;
-            if (lane + 32 == j) id[1] = e, won[1] = most;
-        }
-        if (!by_logit) {
-            // neighbours in order, and the last against what is left: near, and not the same logit with the same bias
-            const uint32_t left = __reduce_max_sync(kAll, mine);
-            auto same = [&](int e, int f) { return xs[e] == xs[f] && (!a.bias || ld_l2(a.bias + e) == ld_l2(a.bias + f)); };
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int j = 32 * h + lane;
-                const uint32_t next = __shfl_sync(kAll, h == 0 && lane == 0 ? won[1] : won[h], (lane + 1) & 31);
-                const int next_id = __shfl_sync(kAll, h == 0 && lane == 0 ? id[1] : id[h], (lane + 1) & 31);
-                if (j + 1 < a.k && won[h] && next && key_value(won[h]) - key_value(next) <= tol) near |= !same(id[h], next_id);
-            }
-            const int last = a.k - 1;
-            const uint32_t final_key = __shfl_sync(kAll, last < 32 ? won[0] : won[1], last & 31);
-            const int final_id = __shfl_sync(kAll, last < 32 ? id[0] : id[1], last & 31);
-            if (final_key && left && key_value(final_key) - key_value(left) <= tol) {
+            // the lane's best and where it is; the winner's lane looks for its next
+            float mine = kNone, won[2] = {kNone, kNone};
+            int mine_at = a.E;
+            auto best = [&] {
+                mine = kNone, mine_at = a.E;
 #pragma unroll
                 for (int i = 0; i < NE; ++i)
-                    if (key[i] && key_value(final_key) - key_value(key[i]) <= tol) near |= !same(element<V>(i, lane), final_id);
+                    if (c[i] > mine) mine = c[i], mine_at = element<V>(i, lane);
+            };
+            best();
+            for (int j = 0; j < a.k; ++j) {
+                const float most = redux_max(mine);
+                if (most == kNone) break;  // no expert is left
+                const int e = static_cast<int>(__reduce_min_sync(kAll, mine == most ? static_cast<uint32_t>(mine_at) : 0xffffffffu));
+                if (mine_at == e) {
+#pragma unroll
+                    for (int i = 0; i < NE; ++i)
+                        if (element<V>(i, lane) == e) c[i] = kNone;
+                    best();
+                }
+                if (lane == j) id[0] = e, won[0] = most;
+                if (lane + 32 == j) id[1] = e, won[1] = most;
+            }
+            if (!by_logit) {
+                // neighbours in order, and the last against what is left: near, and not the same logit with the same bias
+                const float left = redux_max(mine);
+                auto same = [&](int e, int f) { return xs[e] == xs[f] && (!a.bias || bs[e] == bs[f]); };
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int j = 32 * h + lane;
+                    const float next = __shfl_sync(kAll, h == 0 && lane == 0 ? won[1] : won[h], (lane + 1) & 31);
+                    const int next_id = __shfl_sync(kAll, h == 0 && lane == 0 ? id[1] : id[h], (lane + 1) & 31);
+                    if (j + 1 < a.k && next != kNone && won[h] - next <= tol) near |= !same(id[h], next_id);
+                }
+                const int last = a.k - 1;
+                const float final_won = __shfl_sync(kAll, last < 32 ? won[0] : won[1], last & 31);
+                const int final_id = __shfl_sync(kAll, last < 32 ? id[0] : id[1], last & 31);
+                if (final_won != kNone && left != kNone && final_won - left <= tol) {
+#pragma unroll
+                    for (int i = 0; i < NE; ++i)
+                        if (c[i] != kNone && final_won - c[i] <= tol) near |= !same(element<V>(i, lane), final_id);
+                }
+                __syncwarp();
+                if (__any_sync(kAll, near)) {
+                    const int2 again = route_exact(a, xs, bs, reinterpret_cast<uint64_t*>(cs), lane);
+                    id[0] = again.x, id[1] = again.y;
+                }
             }
         }
-        __syncwarp();
-        if (__any_sync(kAll, near)) {
-            const int2 again = route_exact(a, xs, reinterpret_cast<double*>(cs), lane);
-            id[0] = again.x, id[1] = again.y;
-        }
-    }
 
-    // weights: of chosen experts alone where renormalised, by their largest logit (so that no sum of theirs is too small to divide by)
-    __syncwarp();
-    float w[2], z[2], mc = kNone;
+        // weights: of chosen experts alone where renormalised, by their largest logit (so that no sum of theirs is too small to divide by)
+        __syncwarp();
+        float w[2], z[2], mc = kNone;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const bool has = 32 * h + lane < a.k && id[h] >= 0;
-        if (!has) id[h] = -1;
-        z[h] = has ? xs[id[h]] : kNone;
-        mc = fmaxf(mc, z[h]);
-    }
-    mc = warp_max(mc);
-    float total = 0.0f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        w[h] = 0.0f;
-        if (id[h] >= 0) {
-            if (a.sigmoid) w[h] = a.renormalize && mc < -60.0f ? expf(z[h] - mc) : sigmoid(z[h]);
-            else w[h] = a.renormalize ? expf(z[h] - mc) : expf(z[h] - m) / sum;
+        for (int h = 0; h < 2; ++h) {
+            const bool has = 32 * h + lane < a.k && id[h] >= 0;
+            if (!has) id[h] = -1;
+            z[h] = has ? xs[id[h]] : kNone;
+            mc = fmaxf(mc, z[h]);
         }
-        total += w[h];
-    }
-    if (a.renormalize) total = warp_sum(total);
+        if (a.renormalize) mc = redux_max(mc);
+        float total = 0.0f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (32 * h + lane >= a.k) continue;
-        const int64_t at = t * a.k + 32 * h + lane;
-        float v = a.scale * w[h];
-        if (a.renormalize && id[h] >= 0) v /= total;
-        a.ids[at] = id[h];
-        a.weights[at] = bad ? __uint_as_float(0x7fc00000u) : v;
+        for (int h = 0; h < 2; ++h) {
+            w[h] = 0.0f;
+            if (id[h] >= 0) {
+                if (a.sigmoid) w[h] = a.renormalize && mc < -60.0f ? expf(z[h] - mc) : sigmoid(z[h]);
+                else w[h] = a.renormalize ? expf(z[h] - mc) : expf(z[h] - m) / sum;
+            }
+            total += w[h];
+        }
+        if (a.renormalize) total = warp_sum(total);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (32 * h + lane >= a.k) continue;
+            const int64_t at = t * a.k + 32 * h + lane;
+            float v = a.scale * w[h];
+            if (a.renormalize && id[h] >= 0) v /= total;
+            a.ids[at] = id[h];
+            a.weights[at] = bad ? __uint_as_float(0x7fc00000u) : v;
+        }
     }
 }
 
@@ -376,106 +460,108 @@ template <class T, int NE, int V>
 __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const RouteBackwardArgs a) {
     extern __shared__ __align__(16) float shared[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     float* g = shared + warp * a.E;
     griddep_begin();
-    if (t >= a.tokens) return;
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
     const bool whole = !a.sigmoid && !a.renormalize;
-    float x[NE];
-    if (whole) load_row<T, NE, V>(row, a.E, lane, x);
-    int id[2];
-    float dw[2], z[2], q[2], mc = kNone;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int j = 32 * h + lane;
-        id[h] = j < a.k ? plan_index(ld_l2(a.ids + t * a.k + j), a.E) : -1;
-        dw[h] = id[h] >= 0 ? ld_l2(a.dweights + t * a.k + j) : 0.0f;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        z[h] = id[h] >= 0 ? load_one(row + id[h]) : kNone;
-        mc = fmaxf(mc, z[h]);
-    }
-    for (int e = lane; e < a.E; e += 32) g[e] = 0.0f;
-    __syncwarp();
-    if (a.renormalize) {
-        mc = warp_max(mc);
-        float total = 0.0f, dot = 0.0f;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.tokens; t += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+        float x[NE];
+        if (whole) load_row<T, NE, V>(row, a.E, lane, x);
+        int id[2];
+        float dw[2], z[2], q[2], mc = kNone;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            q[h] = 0.0f;
-            if (id[h] >= 0) q[h] = a.sigmoid && !(mc < -60.0f) ? sigmoid(z[h]) : expf(z[h] - mc);
-            total += q[h];
+            const int j = 32 * h + lane;
+            id[h] = j < a.k ? plan_index(ld_l2(a.ids + t * a.k + j), a.E) : -1;
+            dw[h] = id[h] >= 0 ? ld_l2(a.dweights + t * a.k + j) : 0.0f;
         }
-        total = warp_sum(total);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if (id[h] >= 0) q[h] /= total;
-            dot = fmaf(q[h], dw[h], dot);
+            z[h] = id[h] >= 0 ? load_one(row + id[h]) : kNone;
+            mc = fmaxf(mc, z[h]);
         }
-        dot = warp_sum(dot);
+        for (int e = lane; e < a.E; e += 32) g[e] = 0.0f;
+        __syncwarp();
+        if (a.renormalize) {
+            mc = warp_max(mc);
+            float total = 0.0f, dot = 0.0f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            q[h] = a.scale * q[h] * (dw[h] - dot);
-            if (a.sigmoid && id[h] >= 0) q[h] *= sigmoid(-z[h]);
+            for (int h = 0; h < 2; ++h) {
+                q[h] = 0.0f;
+                if (id[h] >= 0) q[h] = a.sigmoid && !(mc < -60.0f) ? sigmoid(z[h]) : expf(z[h] - mc);
+                total += q[h];
+            }
+            total = warp_sum(total);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (id[h] >= 0) q[h] /= total;
+                dot = fmaf(q[h], dw[h], dot);
+            }
+            dot = warp_sum(dot);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                q[h] = a.scale * q[h] * (dw[h] - dot);
+                if (a.sigmoid && id[h] >= 0) q[h] *= sigmoid(-z[h]);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                q[h] = a.scale * dw[h];
+                if (a.sigmoid && id[h] >= 0) q[h] *= sigmoid(z[h]) * sigmoid(-z[h]);
+            }
         }
-    } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            q[h] = a.scale * dw[h];
-            if (a.sigmoid && id[h] >= 0) q[h] *= sigmoid(z[h]) * sigmoid(-z[h]);
+        for (int j = 0; j < a.k; ++j) {
+            const int e = __shfl_sync(kAll, j < 32 ? id[0] : id[1], j & 31);
+            const float v = __shfl_sync(kAll, j < 32 ? q[0] : q[1], j & 31);
+            if (e >= 0 && lane == (e & 31)) g[e] += v;
         }
-    }
-    for (int j = 0; j < a.k; ++j) {
-        const int e = __shfl_sync(kAll, j < 32 ? id[0] : id[1], j & 31);
-        const float v = __shfl_sync(kAll, j < 32 ? q[0] : q[1], j & 31);
-        if (e >= 0 && lane == (e & 31)) g[e] += v;
-    }
-    __syncwarp();
-    float out[NE];
-    if (whole) {
-        float m = kNone, sum = 0.0f, dot = 0.0f;
+        __syncwarp();
+        float out[NE];
+        if (whole) {
+            float m = kNone, sum = 0.0f, dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) m = fmaxf(m, x[i]);
-        m = warp_max(m);
+            for (int i = 0; i < NE; ++i) m = fmaxf(m, x[i]);
+            m = warp_max(m);
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            x[i] = x[i] == kNone ? 0.0f : expf(x[i] - m);
-            sum += x[i];
+            for (int i = 0; i < NE; ++i) {
+                x[i] = x[i] == kNone ? 0.0f : expf(x[i] - m);
+                sum += x[i];
+            }
+            sum = warp_sum(sum);
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                const int e = element<V>(i, lane);
+                x[i] = m == kNone ? 0.0f : x[i] / sum;  // no expert at all: zeros
+                out[i] = e < a.E ? g[e] : 0.0f;
+                dot = fmaf(x[i], out[i], dot);
+            }
+            dot = warp_sum(dot);
+#pragma unroll
+            for (int i = 0; i < NE; ++i) out[i] = x[i] * (out[i] - dot);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) out[i] = element<V>(i, lane) < a.E ? g[element<V>(i, lane)] : 0.0f;
         }
-        sum = warp_sum(sum);
+        T* to = static_cast<T*>(a.dlogits) + t * a.E;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
+        for (int i = 0; i < NE; i += V) {
             const int e = element<V>(i, lane);
-            x[i] = m == kNone ? 0.0f : x[i] / sum;  // no expert at all: zeros
-            out[i] = e < a.E ? g[e] : 0.0f;
-            dot = fmaf(x[i], out[i], dot);
+            if (e >= a.E) continue;
+            if constexpr (V == 1) to[e] = T(out[i]);
+            else if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(to + e) = make_float4(out[i], out[i + 1], out[i + 2], out[i + 3]);
+            else *reinterpret_cast<uint2*>(to + e) = make_uint2(f32x2_to_bf16x2(out[i], out[i + 1]), f32x2_to_bf16x2(out[i + 2], out[i + 3]));
         }
-        dot = warp_sum(dot);
-#pragma unroll
-        for (int i = 0; i < NE; ++i) out[i] = x[i] * (out[i] - dot);
-    } else {
-#pragma unroll
-        for (int i = 0; i < NE; ++i) out[i] = element<V>(i, lane) < a.E ? g[element<V>(i, lane)] : 0.0f;
-    }
-    T* to = static_cast<T*>(a.dlogits) + t * a.E;
-#pragma unroll
-    for (int i = 0; i < NE; i += V) {
-        const int e = element<V>(i, lane);
-        if (e >= a.E) continue;
-        if constexpr (V == 1) to[e] = T(out[i]);
-        else if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(to + e) = make_float4(out[i], out[i + 1], out[i + 2], out[i + 3]);
-        else *reinterpret_cast<uint2*>(to + e) = make_uint2(f32x2_to_bf16x2(out[i], out[i + 1]), f32x2_to_bf16x2(out[i + 2], out[i + 3]));
+        __syncwarp();  // the row's sums have been read
     }
 }
 
+// Shared memory: `whole` floats of a CTA and `floats` of each of its warps. As many CTAs as keep the SMs full (and no more than there are tokens for).
 template <class Kernel, class Args>
-cudaError_t launch_rows(Kernel kernel, const Args& a, int floats, cudaStream_t stream) {
+cudaError_t launch_rows(Kernel kernel, const Args& a, int whole, int floats, cudaStream_t stream) {
     cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3(static_cast<unsigned>((a.tokens + kWarps - 1) / kWarps));
+    lc.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((a.tokens + kWarps - 1) / kWarps, static_cast<int64_t>(device_sm_count()) * kCtas)));
     lc.blockDim = dim3(32 * kWarps);
-    lc.dynamicSmemBytes = static_cast<size_t>(kWarps) * floats * 4;
+    lc.dynamicSmemBytes = (static_cast<size_t>(whole) + static_cast<size_t>(kWarps) * floats) * 4;
     lc.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -518,8 +604,8 @@ cudaError_t launch_expert_route(bool bf16, const RowsView& logits, int64_t token
     a.scale = rule.scale, a.sigmoid = rule.sigmoid, a.renormalize = rule.renormalize;
     return by_experts(a.E, aligned4(logits.p, logits.ld, a.E, bf16), [&](auto n, auto v) {
         constexpr int NE = decltype(n)::value, V = decltype(v)::value;
-        return bf16 ? launch_rows(route_kernel<__nv_bfloat16, NE, V>, a, route_floats(a.E), stream)
-                    : launch_rows(route_kernel<float, NE, V>, a, route_floats(a.E), stream);
+        return bf16 ? launch_rows(route_kernel<__nv_bfloat16, NE, V>, a, (a.E + 3) / 4 * 4, route_floats(a.E), stream)
+                    : launch_rows(route_kernel<float, NE, V>, a, (a.E + 3) / 4 * 4, route_floats(a.E), stream);
     });
 }
 
@@ -532,8 +618,8 @@ cudaError_t launch_expert_route_backward(bool bf16, const float* dweights, const
     const bool wide = aligned4(logits.p, logits.ld, a.E, bf16) && aligned4(dlogits, a.E, a.E, bf16);
     return by_experts(a.E, wide, [&](auto n, auto v) {
         constexpr int NE = decltype(n)::value, V = decltype(v)::value;
-        return bf16 ? launch_rows(route_backward_kernel<__nv_bfloat16, NE, V>, a, a.E, stream)
-                    : launch_rows(route_backward_kernel<float, NE, V>, a, a.E, stream);
+        return bf16 ? launch_rows(route_backward_kernel<__nv_bfloat16, NE, V>, a, 0, a.E, stream)
+                    : launch_rows(route_backward_kernel<float, NE, V>, a, 0, a.E, stream);
     });
 }
 
