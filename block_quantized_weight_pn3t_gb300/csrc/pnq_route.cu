@@ -21,7 +21,7 @@ namespace pnq {
 namespace {
 
 constexpr int kWarps = 4;          // of a CTA
-constexpr int kCtas = 8;           // of an SM at most
+constexpr int kCtas = 16;          // of an SM at most
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kNone = -INFINITY;  // the score of an expert that is out
 
@@ -125,8 +125,9 @@ __device__ __forceinline__ Two inverse(Two a) {  // Newton's step, 2 - a q, from
 
 // exp(d) for d <= 0: d = n log 2 + r, the series of exp(r) (|r| <= 0.35; terms from r^8 / 8! on weigh below 2^-27, in fp32), times 2^n. Below
 // 2^-125: zero.
-__device__ Two exp_two(Two d) {
-    if (!(d.hi > -86.6f)) return {0.0f, 0.0f};
+__device__ __forceinline__ Two exp_two(Two d) {
+    const bool none = !(d.hi > -86.6f);
+    if (none) d = {0.0f, 0.0f};
     const float n = rintf(d.hi * 1.44269504f);
     // log 2 = 0x1.62e4p-1 + 0x1.7f7d1cp-20 + ..: n times the first part is exact
     const Two t = two_sum(d.hi, -n * 0x1.62e4p-1f);
@@ -146,8 +147,8 @@ __device__ Two exp_two(Two d) {
         sum = sum + Two{c, l};
         if (k > 0) sum = sum * r;
     }
-    const float scale = __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23);  // n >= -125
-    return {sum.hi * scale, sum.lo * scale};
+    const float scale = exp2i(static_cast<int>(n));  // n >= -125
+    return {none ? 0.0f : sum.hi * scale, none ? 0.0f : sum.lo * scale};
 }
 
 // Whole numbers in the order of the values (-0 as +0).
@@ -171,26 +172,23 @@ __device__ __noinline__ int2 route_exact(const RouteArgs& a, const float* x, con
         for (int e = lane; e < a.E; e += 32) top = fmaxf(top, x[e]);
         top = redux_max(top);
         Two sum{0.0f, 0.0f};
-        for (int e = lane; e < a.E; e += 32)
-            if (x[e] != kNone) sum = sum + exp_two(two_sum(x[e], -top));
+#pragma unroll 4
+        for (int e = lane; e < a.E; e += 32) sum = sum + exp_two(two_sum(fmaxf(x[e], -3e38f), -top));
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum = sum + Two{__shfl_xor_sync(kAll, sum.hi, d), __shfl_xor_sync(kAll, sum.lo, d)};
         scale = inverse(sum);
     }
-    for (int e = lane; e < a.E; e += 32) {
-        uint64_t key = 0;
-        const float b = a.bias ? bias[e] : 0.0f;
-        if (x[e] != kNone && b != kNone) {
-            Two s;
-            if (a.sigmoid) {
-                const Two z = exp_two({-fabsf(x[e]), 0.0f}), w = inverse(z + Two{1.0f, 0.0f});
-                s = x[e] >= 0.0f ? w : w * z;
-            } else {
-                s = exp_two(two_sum(x[e], -top)) * scale;
-            }
-            key = order_key(s + Two{b, 0.0f});
+#pragma unroll 4
+    for (int e = lane; e < a.E; e += 32) {  // several at a time, without branches: a score is some 200 instructions, one after the other
+        const float v = fmaxf(x[e], -3e38f), b = a.bias ? bias[e] : 0.0f;
+        Two s;
+        if (a.sigmoid) {
+            const Two z = exp_two({-fabsf(v), 0.0f}), w = inverse(z + Two{1.0f, 0.0f}), u = w * z;
+            s = {v >= 0.0f ? w.hi : u.hi, v >= 0.0f ? w.lo : u.lo};
+        } else {
+            s = exp_two(two_sum(v, -top)) * scale;
         }
-        c[e] = key;
+        c[e] = x[e] == kNone || b == kNone ? 0 : order_key(s + Two{b, 0.0f});
     }
     __syncwarp();
     if (a.groups > 1) {
@@ -240,7 +238,7 @@ __device__ __noinline__ int2 route_exact(const RouteArgs& a, const float* x, con
 // Shared memory of a warp: the row's logits, and behind them the groups' scores (each group on an odd pitch) or the keys above.
 __host__ __device__ inline int route_floats(int E) { return E + (E & 1) + 2 * E + 32; }
 
-// A warp takes token after token, the next one's logits on their way meanwhile. The bias is read once a CTA: by every warp for every token, out
+// A warp takes token after token. The bias is read once a CTA: by every warp for every token, out
 // of the same few lines of L2, it took more time than all the rest (16384 tokens of 256 experts: 25 of 45 us).
 template <class T, int NE, int V>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
@@ -253,25 +251,31 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
     int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
     const T* logits = static_cast<const T*>(a.logits);
-    float coming[NE];
-    if (t < a.tokens) load_row<T, NE, V>(logits + t * a.ld, a.E, lane, coming);
     if (a.bias) {
         for (int e = threadIdx.x; e < a.E; e += 32 * kWarps) bs[e] = ld_l2(a.bias + e);
     }
     __syncthreads();
     const bool by_logit = !a.bias && a.groups == 1;
+    float bmax = 0.0f;  // the largest finite |bias|
+    if (a.bias) {
+        for (int e = lane; e < a.E; e += 32)
+            if (fabsf(bs[e]) < INFINITY) bmax = fmaxf(bmax, fabsf(bs[e]));
+        bmax = redux_max(bmax);
+    }
+    const int pitch = a.per | 1;  // of a group in shared memory
+    int group[NE];                // of each of the lane's experts
+#pragma unroll
+    for (int i = 0; i < NE; ++i) group[i] = min(a.groups - 1, static_cast<int>(element<V>(i, lane) * a.per_magic >> 20));
     for (; t < a.tokens; t += step) {
         float x[NE];
-#pragma unroll
-        for (int i = 0; i < NE; ++i) x[i] = coming[i];
-        if (t + step < a.tokens) load_row<T, NE, V>(logits + (t + step) * a.ld, a.E, lane, coming);
+        load_row<T, NE, V>(logits + t * a.ld, a.E, lane, x);
         __syncwarp();  // the last token's scores have been read
 #pragma unroll
         for (int i = 0; i < NE; ++i)
             if (element<V>(i, lane) < a.E) xs[element<V>(i, lane)] = x[i];
 
         // scores c; a NaN, or an infinity that is not an expert taken out, makes the whole row NaN
-        float m = kNone, sum = 0.0f, smax = 1.0f, cmax = 0.0f, c[NE];
+        float m = kNone, sum = 0.0f, smax = 1.0f, c[NE];
         bool bad = false;
         if (!a.sigmoid) {
 #pragma unroll
@@ -301,9 +305,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
                 if (a.bias && e < a.E) s += bs[e];
                 bad |= !(s < INFINITY);
                 c[i] = x[i] == kNone ? kNone : s;
-                if (c[i] != kNone) cmax = fmaxf(cmax, fabsf(c[i]));
             }
-            cmax = redux_max(cmax);
         }
         bad = __any_sync(kAll, bad);
 
@@ -315,14 +317,14 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
             // the quotient is within 2 ulp: s within 2.6 * 2^-23, twice that for two. Softmax: an exponential is within 2^-22 of itself
             // and its argument's rounding adds (m - x) 2^-24; the sum, E / 32 + 5 additions of such, is within 1.5 * 2^-19 and moves a difference by
             // that times the larger score. The addition of the bias rounds by half an ulp of c.
+            const float cmax = smax + bmax;
             const float tol = (a.sigmoid ? 0x1.6p-21f : 0x1p-18f * smax + 0x1p-24f) + 0x1p-23f * cmax;
             bool near = false;
             if (a.groups > 1) {
-                const int pitch = a.per | 1;
 #pragma unroll
                 for (int i = 0; i < NE; ++i) {
-                    const int e = element<V>(i, lane), g = static_cast<int>(e * a.per_magic >> 20);
-                    if (e < a.E) cs[g * pitch + e - g * a.per] = c[i];
+                    const int e = element<V>(i, lane);
+                    if (e < a.E) cs[group[i] * (pitch - a.per) + e] = c[i];
                 }
                 __syncwarp();
                 // the largest power of two of lanes that a group can have: its best two by them
@@ -352,8 +354,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
                 near |= most != kNone && least - most <= 2.0f * tol + 0x1p-22f * cmax;
 #pragma unroll
                 for (int i = 0; i < NE; ++i) {
-                    const int e = element<V>(i, lane), of = static_cast<int>(e * a.per_magic >> 20);
-                    if (e < a.E && !(kept >> (of * lanes) & 1)) c[i] = kNone;
+                    if (!(kept >> (group[i] * lanes) & 1)) c[i] = kNone;
                 }
             }
             // the lane's best and where it is; the winner's lane looks for its next
