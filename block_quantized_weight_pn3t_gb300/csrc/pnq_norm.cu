@@ -24,23 +24,28 @@ constexpr int kMaxThreads = 1024;
 constexpr int kWarpRows = 4;      // rows (warps) of a CTA where a warp takes a row
 constexpr uint32_t kInf = 0x7f800000u;
 
-// V consecutive elements <-> fp32. V = 8: 16-byte accesses; V = 2: one access of two elements.
+// V consecutive elements as they are in memory (`Raw` words) and as fp32. V = 8: 16-byte accesses; V = 2: one access of two elements.
 template <class T, int V>
 struct Io;
 template <int V>
 struct Io<float, V> {
-    static __device__ __forceinline__ void load(const float* p, float (&f)[V]) {
+    struct Raw {
+        uint32_t w[V];
+    };
+    static __device__ __forceinline__ Raw raw(const float* p) {
         if constexpr (V == 8) {
             const uint4 a = ld_l2(reinterpret_cast<const uint4*>(p)), b = ld_l2(reinterpret_cast<const uint4*>(p) + 1);
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+            return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
         } else if constexpr (V == 2) {
             const uint2 a = ld_l2(reinterpret_cast<const uint2*>(p));
-            f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y);
+            return {{a.x, a.y}};
         } else {
-            f[0] = ld_l2(p);
+            return {{__float_as_uint(ld_l2(p))}};
         }
+    }
+    static __device__ __forceinline__ void value(const Raw& r, float (&f)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = __uint_as_float(r.w[i]);
     }
     static __device__ __forceinline__ void store(float* p, const float (&f)[V]) {
         if constexpr (V == 8) {
@@ -56,18 +61,22 @@ struct Io<float, V> {
 };
 template <int V>
 struct Io<__nv_bfloat16, V> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&f)[V]) {
+    struct Raw {
+        uint32_t w[(V + 1) / 2];
+    };
+    static __device__ __forceinline__ Raw raw(const __nv_bfloat16* p) {
         if constexpr (V == 8) {
             const uint4 a = ld_l2(reinterpret_cast<const uint4*>(p));
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            return {{a.x, a.y, a.z, a.w}};
         } else if constexpr (V == 2) {
-            const uint32_t a = ld_l2(reinterpret_cast<const uint32_t*>(p));
-            f[0] = __uint_as_float(a << 16), f[1] = __uint_as_float(a & 0xffff0000u);
+            return {{ld_l2(reinterpret_cast<const uint32_t*>(p))}};
         } else {
-            f[0] = __uint_as_float(static_cast<uint32_t>(ld_l2(reinterpret_cast<const uint16_t*>(p))) << 16);
+            return {{static_cast<uint32_t>(ld_l2(reinterpret_cast<const uint16_t*>(p)))}};
         }
+    }
+    static __device__ __forceinline__ void value(const Raw& r, float (&f)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = __uint_as_float(i % 2 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
     }
     static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[V]) {
         if constexpr (V == 8) {
@@ -81,47 +90,60 @@ struct Io<__nv_bfloat16, V> {
     }
     static __device__ __forceinline__ float round(float f) { return __bfloat162float(__float2bfloat16_rn(f)); }
 };
+template <class T, int V>
+__device__ __forceinline__ void load(const T* p, float (&f)[V]) {
+    Io<T, V>::value(Io<T, V>::raw(p), f);
+}
 
 template <int V>
 __device__ __forceinline__ void load_weight(const void* w, bool bf16, int at, float (&f)[V]) {
-    if (bf16) Io<__nv_bfloat16, V>::load(static_cast<const __nv_bfloat16*>(w) + at, f);
-    else Io<float, V>::load(static_cast<const float*>(w) + at, f);
+    if (bf16) load<__nv_bfloat16, V>(static_cast<const __nv_bfloat16*>(w) + at, f);
+    else load<float, V>(static_cast<const float*>(w) + at, f);
 }
 
 // The codes of p against inv = 127 / top: t = p inv is within 127 * 2^-23 of 127 p / top (two roundings), so the whole number
-// nearest to it is the code unless t is near a border; there the two sides of the border are compared exactly (254 |p| and an odd
-// number up to 253 times top have 32 bits each), ties to even.
+// nearest to it is the code unless t is near the middle of two. There the sign of 127 |p| - (low + 1/2) top decides, ties to even: both products as
+// unevaluated sums of two floats (T. J. Dekker 1971), whose difference is exact (31 and 33 bits, near to each other). One branch for V elements; bf16
+// rows, whose quotients often are ties, take it in every second warp. (In doubles, which run at 1/64 of the rate, the same took 70 of 100 us.)
 struct Encoder {
-    float f, inv;   // p f inv: f lifts rows whose 127 / top would not be finite
-    double top;
+    float f, inv, top;  // f lifts rows of tiny values, and lowers rows of huge ones, so that no step leaves the normal numbers
     __device__ __forceinline__ explicit Encoder(float t) {
-        f = t < 0x1p-60f ? 0x1p100f : 1.0f;
-        inv = t > 0.0f ? 127.0f / (t * f) : 0.0f;
-        top = static_cast<double>(t);
+        f = t < 0x1p-60f ? 0x1p100f : t > 0x1p100f ? 0x1p-100f : 1.0f;
+        top = t * f;
+        inv = t > 0.0f ? 127.0f / top : 0.0f;
     }
-    __device__ __forceinline__ uint32_t operator()(float p) const {
+    template <int V>
+    __device__ __forceinline__ void operator()(const float (&p)[V], uint32_t (&c)[V]) const {
         constexpr float kWhole = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are the whole number
-        const float t = p * f * inv, s = __fadd_rn(t, kWhole), away = __fsub_rn(t, __fsub_rn(s, kWhole));
-        uint32_t code = __float_as_uint(s);
-        if (fabsf(away) > 0.5f - 0x1p-14f) {
-            const int low = static_cast<int>(floorf(fabsf(t)));
-            const double twice = 254.0 * fabs(static_cast<double>(p)), middle = (2 * low + 1) * top;
-            const int q = low + ((twice > middle || (twice == middle && (low & 1))) ? 1 : 0);
-            code = static_cast<uint32_t>(p < 0.0f ? -q : q);
+        bool near = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float t = __fmul_rn(__fmul_rn(p[i], f), inv), s = __fadd_rn(t, kWhole);
+            near |= fabsf(__fsub_rn(t, __fsub_rn(s, kWhole))) > 0.5f - 0x1p-14f;
+            c[i] = __float_as_uint(s);
         }
-        return code & 0xffu;
+        if (near) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float q = fabsf(__fmul_rn(p[i], f)), low = floorf(__fmul_rn(q, inv)), middle = low + 0.5f;
+                const float a = __fmul_rn(127.0f, q), b = __fmul_rn(middle, top);
+                const float d = __fadd_rn(__fsub_rn(a, b), __fsub_rn(fmaf(127.0f, q, -a), fmaf(middle, top, -b)));
+                const int l = static_cast<int>(low), n = l + ((d > 0.0f || (d == 0.0f && (l & 1))) ? 1 : 0);
+                c[i] = static_cast<uint32_t>(p[i] < 0.0f ? -n : n);
+            }
+        }
     }
 };
 
 template <int V>
 __device__ __forceinline__ void store_codes(int8_t* at, const Encoder& e, const float (&p)[V]) {
     uint32_t c[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) c[i] = e(p[i]);
+    e(p, c);
     if constexpr (V == 8) {
-        *reinterpret_cast<uint2*>(at) = make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+        *reinterpret_cast<uint2*>(at) = make_uint2(prmt(prmt(c[0], c[1], 0x0040), prmt(c[2], c[3], 0x0040), 0x5410),
+                                                   prmt(prmt(c[4], c[5], 0x0040), prmt(c[6], c[7], 0x0040), 0x5410));
     } else if constexpr (V == 2) {
-        *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(c[0] | c[1] << 8);
+        *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(prmt(c[0], c[1], 0x0040));
     } else {
         *at = static_cast<int8_t>(c[0]);
     }
@@ -169,92 +191,116 @@ __device__ __forceinline__ float row_scale(uint32_t top, float rstd) {
 
 template <class T, int V>
 __device__ __forceinline__ void load_total(const NormArgs& a, int64_t row, int at, float (&f)[V]) {
-    Io<T, V>::load(static_cast<const T*>(a.x) + row * a.ldx + at, f);
+    load<T, V>(static_cast<const T*>(a.x) + row * a.ldx + at, f);
     if (a.residual) {
         float r[V];
-        Io<T, V>::load(static_cast<const T*>(a.residual) + row * a.ldr + at, r);
+        load<T, V>(static_cast<const T*>(a.residual) + row * a.ldr + at, r);
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = Io<T, V>::round(f[i] + r[i]);
     }
 }
 
-// A row by a warp or a CTA, N accesses of V elements a thread, all in flight at once.
+// A row by a warp or a CTA, N accesses of V elements a thread, all in flight at once; row after row. With eight elements a thread the weight
+// stays in registers and the next row is loaded before the present one's sum is known: one CTA an SM then keeps HBM busy.
 template <class T, int V, int N, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads) norm_kernel(const NormArgs a) {
-    __shared__ float2 part[32];
+    constexpr bool kAhead = V * N == 8;
+    using X = Io<T, V>;
+    __shared__ float2 part[2][32];
     const int team = WARP ? 32 : static_cast<int>(blockDim.x), tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);
+    int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
     griddep_begin();
-    if (WARP && row >= a.rows) return;
     const int D = a.D;
-    float p[N][V];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int at = (tid + i * team) * V;
-        if (at < D) load_total<T, V>(a, row, at, p[i]);
-        else
-#pragma unroll
-            for (int j = 0; j < V; ++j) p[i][j] = 0.0f;
-    }
-    float sum = 0.0f;
-    if (a.norm) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) sum = fmaf(p[i][j], p[i][j], sum);
-        if (a.total) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int at = (tid + i * team) * V;
-                if (at < D) Io<T, V>::store(static_cast<T*>(a.total) + row * D + at, p[i]);
-            }
-        }
+    const bool added = a.residual != nullptr;
+    typename X::Raw x[N] = {}, r[N] = {};
+    auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int at = (tid + i * team) * V;
             if (at < D) {
-                float w[V];
-                load_weight<V>(a.weight, a.weight_bf16, at, w);
-#pragma unroll
-                for (int j = 0; j < V; ++j) p[i][j] = __fmul_rn(p[i][j], w[j]);
+                x[i] = X::raw(static_cast<const T*>(a.x) + row * a.ldx + at);
+                if (added) r[i] = X::raw(static_cast<const T*>(a.residual) + row * a.ldr + at);
             }
         }
-    }
-    uint32_t top = 0;
-    if (a.codes) {
+    };
+    float w[kAhead ? N : 1][V];
+    if (row < a.rows) fetch(row);
+    if (kAhead && a.norm) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(p[i][j]) & 0x7fffffffu);
+            if ((tid + i * team) * V < D) load_weight<V>(a.weight, a.weight_bf16, (tid + i * team) * V, w[kAhead ? i : 0]);
     }
-    reduce<WARP>(sum, top, part);
-    const float rstd = row_rstd(a, sum);
-    if (tid == 0) {
-        if (a.rstd) a.rstd[row] = rstd;
-        if (a.codes) a.scales[row] = row_scale(top, rstd);
-    }
-    if (a.codes) {
-        const Encoder e(top >= kInf ? 0.0f : __uint_as_float(top));
+    for (int turn = 0; row < a.rows; turn ^= 1) {
+        float p[N][V], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int at = (tid + i * team) * V;
-            if (at >= D) continue;
-            if (top >= kInf) {
-                const float none[V] = {};
-                store_codes<V>(a.codes + row * a.pitch + at, e, none);
-            } else {
-                store_codes<V>(a.codes + row * a.pitch + at, e, p[i]);
+            X::value(x[i], p[i]);
+            if (added) {
+                float e[V];
+                X::value(r[i], e);
+#pragma unroll
+                for (int j = 0; j < V; ++j) p[i][j] = X::round(p[i][j] + e[j]);
             }
         }
-    }
-    if (a.y) {
+        const int64_t now = row;
+        row += step;
+        if (kAhead && row < a.rows) fetch(row);
+        if (a.norm) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = (tid + i * team) * V;
-            if (at >= D) continue;
+            for (int i = 0; i < N; ++i) {
+                const int at = (tid + i * team) * V;
 #pragma unroll
-            for (int j = 0; j < V; ++j) p[i][j] *= rstd;
-            Io<T, V>::store(static_cast<T*>(a.y) + row * D + at, p[i]);
+                for (int j = 0; j < V; ++j) sum = fmaf(p[i][j], p[i][j], sum);
+                if (at < D) {
+                    if (a.total) X::store(static_cast<T*>(a.total) + now * D + at, p[i]);
+                    if constexpr (!kAhead) load_weight<V>(a.weight, a.weight_bf16, at, w[0]);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) p[i][j] = __fmul_rn(p[i][j], w[kAhead ? i : 0][j]);
+                }
+            }
+        }
+        uint32_t top = 0;
+        if (a.codes) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(p[i][j]) & 0x7fffffffu);
+        }
+        reduce<WARP>(sum, top, part[turn]);
+        const float rstd = row_rstd(a, sum);
+        if (tid == 0) {
+            if (a.rstd) a.rstd[now] = rstd;
+            if (a.codes) a.scales[now] = row_scale(top, rstd);
+        }
+        if (a.codes) {
+            const Encoder e(top >= kInf ? 0.0f : __uint_as_float(top));
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = (tid + i * team) * V;
+                if (at >= D) continue;
+                if (top >= kInf) {
+                    const float none[V] = {};
+                    store_codes<V>(a.codes + now * a.pitch + at, e, none);
+                } else {
+                    store_codes<V>(a.codes + now * a.pitch + at, e, p[i]);
+                }
+            }
+        }
+        if (a.y) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = (tid + i * team) * V;
+                if (at >= D) continue;
+#pragma unroll
+                for (int j = 0; j < V; ++j) p[i][j] *= rstd;
+                X::store(static_cast<T*>(a.y) + now * D + at, p[i]);
+            }
+        }
+        if (!kAhead && row < a.rows) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = r[i] = {};
+            fetch(row);
         }
     }
 }
@@ -290,7 +336,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a
     }
     const Encoder e(top >= kInf ? 0.0f : __uint_as_float(top));
     for (int64_t at = first; at < D; at += step) {
-        if (a.norm && a.total) Io<T, V>::load(static_cast<const T*>(a.total) + row * D + at, p);
+        if (a.norm && a.total) load<T, V>(static_cast<const T*>(a.total) + row * D + at, p);
         else load_total<T, V>(a, row, static_cast<int>(at), p);
         if (a.norm) {
             load_weight<V>(a.weight, a.weight_bf16, static_cast<int>(at), w);
@@ -332,22 +378,23 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormBa
     __shared__ float part[2][32];
     const int tid = threadIdx.x, team = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = team >> 5, D = a.D;
     griddep_begin();
-    float w[N][V], dw[N][V], t[N][V], g[N][V];
-    auto load = [&](int64_t row) {
+    float w[N][V], dw[N][V];
+    typename Io<T, V>::Raw t[N], g[N], d[N] = {};
+    auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int at = (tid + i * team) * V;
             if (at < D) {
-                Io<T, V>::load(static_cast<const T*>(a.total) + row * a.ldt + at, t[i]);
-                Io<T, V>::load(static_cast<const T*>(a.dy) + row * a.ldy + at, g[i]);
+                t[i] = Io<T, V>::raw(static_cast<const T*>(a.total) + row * a.ldt + at);
+                g[i] = Io<T, V>::raw(static_cast<const T*>(a.dy) + row * a.ldy + at);
+                if (a.dtotal) d[i] = Io<T, V>::raw(static_cast<const T*>(a.dtotal) + row * a.ldd + at);
             } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) t[i][j] = g[i][j] = 0.0f;
+                t[i] = g[i] = {};
             }
         }
     };
     int64_t row = blockIdx.x;
-    load(row);
+    fetch(row);
     float rstd = ld_l2(a.rstd + row);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -358,20 +405,25 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormBa
     }
     for (int turn = 0; row < a.rows; turn ^= 1) {
         float dot = 0.0f, n[N][V], h[N][V];
+        typename Io<T, V>::Raw more[N];
         const float r = rstd;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i) {
+            Io<T, V>::value(t[i], n[i]);
+            Io<T, V>::value(g[i], h[i]);
+            more[i] = d[i];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                n[i][j] = t[i][j] * r;
-                dw[i][j] = fmaf(g[i][j], n[i][j], dw[i][j]);
-                h[i][j] = g[i][j] * w[i][j];
+                n[i][j] *= r;
+                dw[i][j] = fmaf(h[i][j], n[i][j], dw[i][j]);
+                h[i][j] *= w[i][j];
                 dot = fmaf(h[i][j], n[i][j], dot);
             }
+        }
         const int64_t now = row;
         row += gridDim.x;
         if (row < a.rows) {
-            load(row);
+            fetch(row);
             rstd = ld_l2(a.rstd + row);
         }
 #pragma unroll
@@ -391,10 +443,10 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormBa
 #pragma unroll
             for (int j = 0; j < V; ++j) h[i][j] = r * (h[i][j] - n[i][j] * mean);
             if (a.dtotal) {
-                float d[V];
-                Io<T, V>::load(static_cast<const T*>(a.dtotal) + now * a.ldd + at, d);
+                float e[V];
+                Io<T, V>::value(more[i], e);
 #pragma unroll
-                for (int j = 0; j < V; ++j) h[i][j] += d[j];
+                for (int j = 0; j < V; ++j) h[i][j] += e[j];
             }
             Io<T, V>::store(static_cast<T*>(a.dx) + now * D + at, h[i]);
         }
@@ -423,8 +475,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_long_kernel(const N
         float dot = 0.0f, w[V], n[V], g[V];
         uint32_t none = 0;
         for (int64_t at = first; at < D; at += step) {
-            Io<T, V>::load(t + at, n);
-            Io<T, V>::load(dy + at, g);
+            load<T, V>(t + at, n);
+            load<T, V>(dy + at, g);
             load_weight<V>(a.weight, a.weight_bf16, static_cast<int>(at), w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -437,13 +489,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_long_kernel(const N
         reduce<false>(dot, none, part);
         const float mean = dot / static_cast<float>(D);
         for (int64_t at = first; at < D; at += step) {
-            Io<T, V>::load(t + at, n);
-            Io<T, V>::load(dy + at, g);
+            load<T, V>(t + at, n);
+            load<T, V>(dy + at, g);
             load_weight<V>(a.weight, a.weight_bf16, static_cast<int>(at), w);
 #pragma unroll
             for (int j = 0; j < V; ++j) n[j] = r * (g[j] * w[j] - n[j] * r * mean);
             if (a.dtotal) {
-                Io<T, V>::load(static_cast<const T*>(a.dtotal) + row * a.ldd + at, g);
+                load<T, V>(static_cast<const T*>(a.dtotal) + row * a.ldd + at, g);
 #pragma unroll
                 for (int j = 0; j < V; ++j) n[j] += g[j];
             }
@@ -475,38 +527,41 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* partial,
 
 // ---- codes back to values -----------------------------------------------------------------------------
 
-// out[r][k] = codes[r][k] * scales[r]: V consecutive elements a thread and step.
+// out[r][k] = codes[r][k] * scales[r]: V consecutive elements a thread and step; the rows' pieces of V (`per` a row) one after the other, so that
+// short rows fill CTAs too.
+constexpr int kDecodeSteps = 4, kDecodeThreads = 256;
 template <class T, int V>
-__global__ void __launch_bounds__(256) int8_dequantize_kernel(const int8_t* codes, int64_t pitch, const float* scales, int64_t rows,
-                                                              int K, T* out) {
-    constexpr int kSteps = 4;
+__global__ void __launch_bounds__(kDecodeThreads) int8_dequantize_kernel(const int8_t* codes, int64_t pitch, const float* scales, int64_t rows,
+                                                                         int per, T* out) {
     griddep_begin();
-    const int first = (static_cast<int>(blockIdx.x) * kSteps * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
-    const int step = static_cast<int>(blockDim.x) * V;
-    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
-        const uint8_t* c = reinterpret_cast<const uint8_t*>(codes) + row * pitch;
-        uint32_t word[kSteps];
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kDecodeSteps * kDecodeThreads), row0 = first / per;
+    const int in0 = static_cast<int>(first - row0 * per);  // of the CTA's first piece within its row
+    uint32_t word[kDecodeSteps];
+    float scale[kDecodeSteps];
+    int64_t row[kDecodeSteps];
+    int at[kDecodeSteps];
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int at = first + i * step;
-            if (at < K) {
-                if constexpr (V == 4) word[i] = ld_l2(reinterpret_cast<const uint32_t*>(c + at));
-                else word[i] = ld_l2(c + at);
-            }
+    for (int i = 0; i < kDecodeSteps; ++i) {
+        const uint32_t u = static_cast<uint32_t>(in0) + i * kDecodeThreads + threadIdx.x, r = u / static_cast<uint32_t>(per);
+        row[i] = row0 + r;
+        at[i] = static_cast<int>(u - r * per);
+        if (row[i] < rows) {
+            const uint8_t* c = reinterpret_cast<const uint8_t*>(codes) + row[i] * pitch + static_cast<int64_t>(at[i]) * V;
+            if constexpr (V == 4) word[i] = ld_l2(reinterpret_cast<const uint32_t*>(c));
+            else word[i] = ld_l2(c);
+            scale[i] = ld_l2(scales + row[i]);
         }
-        const float scale = ld_l2(scales + row);
+    }
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int at = first + i * step;
-            if (at >= K) continue;
-            float f[4];
+    for (int i = 0; i < kDecodeSteps; ++i) {
+        if (row[i] >= rows) continue;
+        float f[4];
 #pragma unroll
-            for (int j = 0; j < V; ++j) f[j] = static_cast<float>(static_cast<int8_t>(word[i] >> (8 * j))) * scale;
-            T* o = out + row * K + at;
-            if constexpr (V == 4 && sizeof(T) == 4) *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
-            else if constexpr (V == 4) *reinterpret_cast<uint2*>(o) = make_uint2(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]));
-            else *o = T(f[0]);
-        }
+        for (int j = 0; j < V; ++j) f[j] = static_cast<float>(static_cast<int8_t>(word[i] >> (8 * j))) * scale[i];
+        T* o = out + (row[i] * per + at[i]) * V;
+        if constexpr (V == 4 && sizeof(T) == 4) *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+        else if constexpr (V == 4) *reinterpret_cast<uint2*>(o) = make_uint2(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]));
+        else *o = T(f[0]);
     }
 }
 
@@ -537,14 +592,19 @@ int threads_for(int64_t D, int per) {
 
 template <class T, int V>
 cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
-    const int64_t D = a.D;
+    const int64_t D = a.D, sms = device_sm_count();
     auto block = [&](auto n) {
         constexpr int N = decltype(n)::value;
-        return launch_dependent(norm_kernel<T, V, N, false>, static_cast<int>(a.rows), threads_for(D, V * N), stream, a);
+        const int threads = threads_for(D, V * N);
+        const int64_t ctas = std::min(a.rows, sms * std::max(1, 1536 / threads));
+        return launch_dependent(norm_kernel<T, V, N, false>, static_cast<int>(ctas), threads, stream, a);
     };
-    if (D <= 256)
-        return launch_dependent(norm_kernel<T, V, 8 / V, true>, static_cast<int>((a.rows + kWarpRows - 1) / kWarpRows), 32 * kWarpRows, stream, a);
+    if (D <= 256) {
+        const int64_t ctas = std::min((a.rows + kWarpRows - 1) / kWarpRows, sms * 12);
+        return launch_dependent(norm_kernel<T, V, 8 / V, true>, static_cast<int>(ctas), 32 * kWarpRows, stream, a);
+    }
     if (D <= 8 * kMaxThreads) return block(std::integral_constant<int, 8 / V>{});
+    if (D <= 16 * kMaxThreads) return block(std::integral_constant<int, 16 / V>{});
     if (D <= 32 * kMaxThreads) return block(std::integral_constant<int, 32 / V>{});
     return launch_dependent(norm_long_kernel<T, V>, static_cast<int>(a.rows), kMaxThreads, stream, a);
 }
@@ -630,26 +690,17 @@ cudaError_t launch_int8_dequantize(const int8_t* codes, int64_t pitch, const flo
                                    cudaStream_t stream) {
     const bool wide = K % 4 == 0 && pitch % 4 == 0 && reinterpret_cast<uintptr_t>(codes) % 4 == 0 &&
                       reinterpret_cast<uintptr_t>(out) % (bf16 ? 8 : 16) == 0;
-    const int V = wide ? 4 : 1;
-    const int threads = std::min(256, threads_for(K, V));
-    cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3(static_cast<unsigned>((K + 4ll * threads * V - 1) / (4ll * threads * V)), static_cast<unsigned>(std::min<int64_t>(rows, 65535)));
-    lc.blockDim = dim3(static_cast<unsigned>(threads));
-    lc.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
-    const int k = static_cast<int>(K);
+    const int64_t per = K / (wide ? 4 : 1), ctas = (rows * per + kDecodeSteps * kDecodeThreads - 1) / (kDecodeSteps * kDecodeThreads);
+    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+    auto go = [&](auto kernel, auto* o) {
+        return launch_dependent(kernel, static_cast<int>(ctas), kDecodeThreads, stream, codes, pitch, scales, rows, static_cast<int>(per), o);
+    };
     if (bf16) {
         auto* o = static_cast<__nv_bfloat16*>(out);
-        return wide ? cudaLaunchKernelEx(&lc, int8_dequantize_kernel<__nv_bfloat16, 4>, codes, pitch, scales, rows, k, o)
-                    : cudaLaunchKernelEx(&lc, int8_dequantize_kernel<__nv_bfloat16, 1>, codes, pitch, scales, rows, k, o);
+        return wide ? go(int8_dequantize_kernel<__nv_bfloat16, 4>, o) : go(int8_dequantize_kernel<__nv_bfloat16, 1>, o);
     }
     auto* o = static_cast<float*>(out);
-    return wide ? cudaLaunchKernelEx(&lc, int8_dequantize_kernel<float, 4>, codes, pitch, scales, rows, k, o)
-                : cudaLaunchKernelEx(&lc, int8_dequantize_kernel<float, 1>, codes, pitch, scales, rows, k, o);
+    return wide ? go(int8_dequantize_kernel<float, 4>, o) : go(int8_dequantize_kernel<float, 1>, o);
 }
 
 }  // namespace pnq

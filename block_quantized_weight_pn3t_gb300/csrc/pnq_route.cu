@@ -211,42 +211,55 @@ __device__ __noinline__ int2 route_exact(const RouteArgs& a, const float* x, con
             if (!(kept >> (e / a.per) & 1)) c[e] = 0;
         __syncwarp();
     }
+    // each lane's best of its own (lane, lane + 32, ..); the winner's next is found by all lanes together, one of its experts each
+    struct Best {
+        uint32_t hi, lo, tie;  // the score in order, and the logit
+        int at;
+    };
+    auto of = [&](int e) -> Best {
+        const uint64_t key = e < a.E ? c[e] : 0;
+        return {static_cast<uint32_t>(key >> 32), static_cast<uint32_t>(key), key ? order_key(x[e]) : 0, key ? e : 1 << 30};
+    };
+    auto largest = [&](Best b) -> Best {  // of the warp; at = 1 << 30 where none is left
+        const uint32_t hi = __reduce_max_sync(kAll, b.hi);
+        bool in = b.hi == hi;
+        const uint32_t lo = __reduce_max_sync(kAll, in ? b.lo : 0);
+        in = in && b.lo == lo;
+        const uint32_t tie = __reduce_max_sync(kAll, in ? b.tie : 0);
+        in = in && b.tie == tie;
+        return {hi, lo, tie, static_cast<int>(__reduce_min_sync(kAll, in ? static_cast<uint32_t>(b.at) : 1u << 30))};
+    };
+    Best mine = of(lane);
+    for (int e = lane + 32; e < a.E; e += 32) {
+        const Best b = of(e);
+        if (b.hi > mine.hi || (b.hi == mine.hi && (b.lo > mine.lo || (b.lo == mine.lo && b.tie > mine.tie)))) mine = b;
+    }
     for (int j = 0; j < a.k; ++j) {
-        uint64_t v = 0;
-        uint32_t tie = 0;  // the logit, in order
-        int at = a.E;
-        for (int e = lane; e < a.E; e += 32) {
-            const uint64_t key = c[e];
-            const uint32_t logit = order_key(x[e]);
-            if (key > v || (key == v && key && logit > tie)) v = key, tie = logit, at = e;
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const uint64_t ov = __shfl_xor_sync(kAll, v, d);
-            const uint32_t otie = __shfl_xor_sync(kAll, tie, d);
-            const int oat = __shfl_xor_sync(kAll, at, d);
-            if (ov > v || (ov == v && (otie > tie || (otie == tie && oat < at)))) v = ov, tie = otie, at = oat;
-        }
-        if (v == 0) break;  // no expert is left
-        if (lane == (j & 31)) (j < 32 ? id.x : id.y) = at;
-        if (lane == (at & 31)) c[at] = 0;
+        const Best won = largest(mine);
+        if (won.at >= a.E) break;  // no expert is left
+        if (lane == (j & 31)) (j < 32 ? id.x : id.y) = won.at;
+        const int w = won.at & 31;
+        if (lane == w) c[won.at] = 0;
         __syncwarp();
+        const Best next = largest(of(w + 32 * lane));
+        if (lane == w) mine = next;
     }
     return id;
 }
 
 // Shared memory of a warp: the row's logits, and behind them the groups' scores (each group on an odd pitch) or the keys above.
-__host__ __device__ inline int route_floats(int E) { return E + (E & 1) + 2 * E + 32; }
+__host__ __device__ inline int route_floats(int E) { return (E + 3) / 4 * 4 * 3 + 32; }
 
 // A warp takes token after token. The bias is read once a CTA: by every warp for every token, out
 // of the same few lines of L2, it took more time than all the rest (16384 tokens of 256 experts: 25 of 45 us).
+// (Registers for eight CTAs an SM up to 256 experts: a token is a chain of some 3 us. With four CTAs fewer it took 4 to 12 percent longer.)
 template <class T, int NE, int V>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, NE <= 8 ? 8 : 4) route_kernel(const RouteArgs a) {
     extern __shared__ __align__(16) float shared[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float* bs = shared;  // [E] bias, in whole 16 bytes
     float* xs = shared + (a.E + 3) / 4 * 4 + warp * route_floats(a.E);
-    float* cs = xs + a.E + (a.E & 1);
+    float* cs = xs + (a.E + 3) / 4 * 4;
     griddep_begin();
     int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -263,16 +276,22 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
         bmax = redux_max(bmax);
     }
     const int pitch = a.per | 1;  // of a group in shared memory
-    int group[NE];                // of each of the lane's experts
+    auto group = [&](int e) { return static_cast<int>(e * a.per_magic >> 20); };
+    // a row's values to shared memory, in the experts' order
+    auto keep = [&](float* to, const float (&v)[NE]) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) group[i] = min(a.groups - 1, static_cast<int>(element<V>(i, lane) * a.per_magic >> 20));
+        for (int i = 0; i < NE; i += V) {
+            const int e = element<V>(i, lane);
+            if (e >= a.E) continue;
+            if constexpr (V == 4) *reinterpret_cast<float4*>(to + e) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            else to[e] = v[i];
+        }
+    };
     for (; t < a.tokens; t += step) {
         float x[NE];
         load_row<T, NE, V>(logits + t * a.ld, a.E, lane, x);
         __syncwarp();  // the last token's scores have been read
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (element<V>(i, lane) < a.E) xs[element<V>(i, lane)] = x[i];
+        keep(xs, x);
 
         // scores c; a NaN, or an infinity that is not an expert taken out, makes the whole row NaN
         float m = kNone, sum = 0.0f, smax = 1.0f, c[NE];
@@ -288,7 +307,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
                 sum += c[i];
             }
             sum = warp_sum(sum);
-            smax = 1.0f / sum;  // the score of the largest logit
+            smax = sum > 0.0f ? 1.0f / sum : 0.0f;  // the score of the largest logit, if any expert is in
         } else {
 #pragma unroll
             for (int i = 0; i < NE; ++i) bad |= isnan(x[i]);
@@ -300,8 +319,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
                 const int e = element<V>(i, lane);
-                float s = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-x[i])) : c[i] * smax;
-                if (x[i] < -87.0f) s = 0.0f;
+                float s = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-x[i])) : c[i] * smax;  // 0 from a divisor of 2^126 on
                 if (a.bias && e < a.E) s += bs[e];
                 bad |= !(s < INFINITY);
                 c[i] = x[i] == kNone ? kNone : s;
@@ -324,7 +342,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
 #pragma unroll
                 for (int i = 0; i < NE; ++i) {
                     const int e = element<V>(i, lane);
-                    if (e < a.E) cs[group[i] * (pitch - a.per) + e] = c[i];
+                    if (e < a.E) cs[group(e) * (pitch - a.per) + e] = c[i];
                 }
                 __syncwarp();
                 // the largest power of two of lanes that a group can have: its best two by them
@@ -354,29 +372,32 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
                 near |= most != kNone && least - most <= 2.0f * tol + 0x1p-22f * cmax;
 #pragma unroll
                 for (int i = 0; i < NE; ++i) {
-                    if (!(kept >> (group[i] * lanes) & 1)) c[i] = kNone;
+                    const int e = element<V>(i, lane);
+                    if (e < a.E && !(kept >> (group(e) * lanes) & 1)) c[i] = kNone;
                 }
+                __syncwarp();  // the groups' scores have been read
             }
-            // the lane's best and where it is; the winner's lane looks for its next
+            // each lane's best and where it is. The winner's lane loses it, and its next is found by all lanes together, one of its experts each (by
+            // that lane alone, the others waiting, selection took twice the instructions)
+            keep(cs, c);
             float mine = kNone, won[2] = {kNone, kNone};
             int mine_at = a.E;
-            auto best = [&] {
-                mine = kNone, mine_at = a.E;
 #pragma unroll
-                for (int i = 0; i < NE; ++i)
-                    if (c[i] > mine) mine = c[i], mine_at = element<V>(i, lane);
-            };
-            best();
+            for (int i = 0; i < NE; ++i)
+                if (c[i] > mine) mine = c[i], mine_at = element<V>(i, lane);
+            __syncwarp();
             for (int j = 0; j < a.k; ++j) {
                 const float most = redux_max(mine);
-                if (most == kNone) break;  // no expert is left
-                const int e = static_cast<int>(__reduce_min_sync(kAll, mine == most ? static_cast<uint32_t>(mine_at) : 0xffffffffu));
-                if (mine_at == e) {
-#pragma unroll
-                    for (int i = 0; i < NE; ++i)
-                        if (element<V>(i, lane) == e) c[i] = kNone;
-                    best();
-                }
+                if (!(most > kNone)) break;  // no expert is left
+                const uint32_t ties = __ballot_sync(kAll, mine == most);
+                int e = __shfl_sync(kAll, mine_at, __ffs(ties) - 1);
+                if (ties & (ties - 1)) e = static_cast<int>(__reduce_min_sync(kAll, mine == most ? static_cast<uint32_t>(mine_at) : 0xffffffffu));
+                const int owner = e / V & 31, own = element<V>(lane, owner);
+                if (lane == owner) cs[e] = kNone;
+                __syncwarp();
+                const float v = lane < NE && own < a.E ? cs[own] : kNone, next = redux_max(v);
+                const int next_at = element<V>(__ffs(__ballot_sync(kAll, v == next)) - 1, owner);
+                if (lane == owner) mine = next, mine_at = next_at;
                 if (lane == j) id[0] = e, won[0] = most;
                 if (lane + 32 == j) id[1] = e, won[1] = most;
             }
@@ -395,9 +416,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
                 const float final_won = __shfl_sync(kAll, last < 32 ? won[0] : won[1], last & 31);
                 const int final_id = __shfl_sync(kAll, last < 32 ? id[0] : id[1], last & 31);
                 if (final_won != kNone && left != kNone && final_won - left <= tol) {
-#pragma unroll
-                    for (int i = 0; i < NE; ++i)
-                        if (c[i] != kNone && final_won - c[i] <= tol) near |= !same(element<V>(i, lane), final_id);
+                    for (int e = lane; e < a.E; e += 32)
+                        if (cs[e] != kNone && final_won - cs[e] <= tol) near |= !same(e, final_id);
                 }
                 __syncwarp();
                 if (__any_sync(kAll, near)) {
@@ -409,19 +429,19 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
 
         // weights: of chosen experts alone where renormalised, by their largest logit (so that no sum of theirs is too small to divide by)
         __syncwarp();
-        float w[2], z[2], mc = kNone;
+        const int halves = a.k > 32 ? 2 : 1;
+        float w[2] = {0.0f, 0.0f}, z[2], mc = kNone, total = 0.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const bool has = 32 * h + lane < a.k && id[h] >= 0;
-            if (!has) id[h] = -1;
-            z[h] = has ? xs[id[h]] : kNone;
+            if (h >= halves) break;
+            if (32 * h + lane >= a.k) id[h] = -1;
+            z[h] = id[h] >= 0 ? xs[id[h]] : kNone;
             mc = fmaxf(mc, z[h]);
         }
         if (a.renormalize) mc = redux_max(mc);
-        float total = 0.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            w[h] = 0.0f;
+            if (h >= halves) break;
             if (id[h] >= 0) {
                 if (a.sigmoid) w[h] = a.renormalize && mc < -60.0f ? expf(z[h] - mc) : sigmoid(z[h]);
                 else w[h] = a.renormalize ? expf(z[h] - mc) : expf(z[h] - m) / sum;
