@@ -57,7 +57,17 @@ struct Io<float, V> {
             *p = f[0];
         }
     }
-    static __device__ __forceinline__ float round(float f) { return f; }
+    static __device__ __forceinline__ void store(float* p, const Raw& r) {
+        float f[V];
+        value(r, f);
+        store(p, f);
+    }
+    static __device__ __forceinline__ Raw sum(const Raw& a, const Raw& b) {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.w[i] = __float_as_uint(__fadd_rn(__uint_as_float(a.w[i]), __uint_as_float(b.w[i])));
+        return r;
+    }
 };
 template <int V>
 struct Io<__nv_bfloat16, V> {
@@ -88,7 +98,19 @@ struct Io<__nv_bfloat16, V> {
             *p = __float2bfloat16_rn(f[0]);
         }
     }
-    static __device__ __forceinline__ float round(float f) { return __bfloat162float(__float2bfloat16_rn(f)); }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const Raw& r) {
+        if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(p) = r.w[0];
+        else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(r.w[0]);
+    }
+    // Rounded once, which is what the fp32 sum rounded again is: where two numbers of 8 bits have no exact sum of 24, one is below 2^-16 of the other,
+    // and the sum is not near the middle of two bf16 numbers.
+    static __device__ __forceinline__ Raw sum(const Raw& a, const Raw& b) {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < (V + 1) / 2; ++i) asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r.w[i]) : "r"(a.w[i]), "r"(b.w[i]));
+        return r;
+    }
 };
 template <class T, int V>
 __device__ __forceinline__ void load(const T* p, float (&f)[V]) {
@@ -101,10 +123,10 @@ __device__ __forceinline__ void load_weight(const void* w, bool bf16, int at, fl
     else load<float, V>(static_cast<const float*>(w) + at, f);
 }
 
-// The codes of p against inv = 127 / top: t = p inv is within 127 * 2^-23 of 127 p / top (two roundings), so the whole number
-// nearest to it is the code unless t is near the middle of two. There the sign of 127 |p| - (low + 1/2) top decides, ties to even: both products as
-// unevaluated sums of two floats (T. J. Dekker 1971), whose difference is exact (31 and 33 bits, near to each other). One branch for V elements; bf16
-// rows, whose quotients often are ties, take it in every second warp. (In doubles, which run at 1/64 of the rate, the same took 70 of 100 us.)
+// The codes of p against inv = 127 / top: p inv, rounded once to a whole number, is the code unless it is near the middle of two (inv's
+// rounding moves it by 127 * 2^-24 at most, and what is left of it is computed to 2^-25). There the sign of 127 p - middle top decides, ties to
+// even: both products as unevaluated sums of two floats (T. J. Dekker 1971), whose difference is exact (31 and 33 bits, near to each other). bf16 rows, whose
+// quotients often are ties, need that for one element in a hundred. (In doubles, which run at 1/64 of the rate, it took 70 of 100 us.)
 struct Encoder {
     float f, inv, top;  // f lifts rows of tiny values, and lowers rows of huge ones, so that no step leaves the normal numbers
     __device__ __forceinline__ explicit Encoder(float t) {
@@ -112,26 +134,36 @@ struct Encoder {
         top = t * f;
         inv = t > 0.0f ? 127.0f / top : 0.0f;
     }
+    static constexpr float kWhole = 12582912.0f;  // 1.5 * 2^23: a sum's low bits are the whole number
     template <int V>
-    __device__ __forceinline__ void operator()(const float (&p)[V], uint32_t (&c)[V]) const {
-        constexpr float kWhole = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are the whole number
+    __device__ __forceinline__ void operator()(const float (&v)[V], uint32_t (&c)[V]) const {
+        float p[V], away[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = v[i];
+        if (f != 1.0f) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] *= f;
+        }
         bool near = false;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float t = __fmul_rn(__fmul_rn(p[i], f), inv), s = __fadd_rn(t, kWhole);
-            near |= fabsf(__fsub_rn(t, __fsub_rn(s, kWhole))) > 0.5f - 0x1p-14f;
+            const float s = fmaf(p[i], inv, kWhole);
+            away[i] = fmaf(p[i], inv, -__fsub_rn(s, kWhole));
+            near |= fabsf(away[i]) > 0.5f - 0x1p-16f;
             c[i] = __float_as_uint(s);
         }
         if (near) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float q = fabsf(__fmul_rn(p[i], f)), low = floorf(__fmul_rn(q, inv)), middle = low + 0.5f;
-                const float a = __fmul_rn(127.0f, q), b = __fmul_rn(middle, top);
-                const float d = __fadd_rn(__fsub_rn(a, b), __fsub_rn(fmaf(127.0f, q, -a), fmaf(middle, top, -b)));
-                const int l = static_cast<int>(low), n = l + ((d > 0.0f || (d == 0.0f && (l & 1))) ? 1 : 0);
-                c[i] = static_cast<uint32_t>(p[i] < 0.0f ? -n : n);
-            }
+            for (int i = 0; i < V; ++i)
+                if (fabsf(away[i]) > 0.5f - 0x1p-16f) c[i] = decide(p[i], c[i], away[i] > 0.0f ? 1.0f : -1.0f);
         }
+    }
+    // The code of p, which lies near the middle of the whole number (in c's low bits) and the next to `side`.
+    __device__ __forceinline__ uint32_t decide(float p, uint32_t c, float side) const {
+        const float middle = fmaf(0.5f, side, __fsub_rn(__uint_as_float(c), kWhole)), a = __fmul_rn(127.0f, p), b = __fmul_rn(middle, top);
+        const float d = side * __fadd_rn(__fsub_rn(a, b), __fsub_rn(fmaf(127.0f, p, -a), fmaf(middle, top, -b)));
+        // beyond the middle, or on it with an odd whole number (its lowest bit is the sum's)
+        return d > 0.0f || (d == 0.0f && (c & 1)) ? c + (side > 0.0f ? 1u : ~0u) : c;
     }
 };
 
@@ -147,6 +179,24 @@ __device__ __forceinline__ void store_codes(int8_t* at, const Encoder& e, const 
     } else {
         *at = static_cast<int8_t>(c[0]);
     }
+}
+
+// The larger of top and the magnitudes of a row's values, NaN if there is one.
+template <int V>
+__device__ __forceinline__ float largest(float top, const float (&p)[V]) {
+    if constexpr (V == 1) {
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(p[0])));
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(p[j]), "f"(p[j + 1]));
+    }
+    return top;
+}
+
+__device__ __forceinline__ float warp_total(float v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
 }
 
 // Sum and largest word over a team (a warp, or the CTA through `part`), the same in every thread and from call to call.
@@ -190,20 +240,15 @@ __device__ __forceinline__ float row_scale(uint32_t top, float rstd) {
 }
 
 template <class T, int V>
-__device__ __forceinline__ void load_total(const NormArgs& a, int64_t row, int at, float (&f)[V]) {
-    load<T, V>(static_cast<const T*>(a.x) + row * a.ldx + at, f);
-    if (a.residual) {
-        float r[V];
-        load<T, V>(static_cast<const T*>(a.residual) + row * a.ldr + at, r);
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = Io<T, V>::round(f[i] + r[i]);
-    }
+__device__ __forceinline__ typename Io<T, V>::Raw load_total(const NormArgs& a, int64_t row, int at) {
+    const auto x = Io<T, V>::raw(static_cast<const T*>(a.x) + row * a.ldx + at);
+    return a.residual ? Io<T, V>::sum(x, Io<T, V>::raw(static_cast<const T*>(a.residual) + row * a.ldr + at)) : x;
 }
 
 // A row by a warp or a CTA, N accesses of V elements a thread, all in flight at once; row after row. With eight elements a thread the weight
-// stays in registers and the next row is loaded before the present one's sum is known: one CTA an SM then keeps HBM busy.
-template <class T, int V, int N, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads) norm_kernel(const NormArgs a) {
+// stays in registers and the next row is loaded before the present one's sum is known. Few rows, and rows not on 16 bytes, go here.
+template <class T, int V, int N, bool WARP, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) norm_kernel(const NormArgs a) {
     constexpr bool kAhead = V * N == 8;
     using X = Io<T, V>;
     __shared__ float2 part[2][32];
@@ -235,13 +280,11 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads) norm_kern
         float p[N][V], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            X::value(x[i], p[i]);
             if (added) {
-                float e[V];
-                X::value(r[i], e);
-#pragma unroll
-                for (int j = 0; j < V; ++j) p[i][j] = X::round(p[i][j] + e[j]);
+                x[i] = X::sum(x[i], r[i]);
+                if (a.total && (tid + i * team) * V < D) X::store(static_cast<T*>(a.total) + row * D + (tid + i * team) * V, x[i]);
             }
+            X::value(x[i], p[i]);
         }
         const int64_t now = row;
         row += step;
@@ -253,20 +296,19 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads) norm_kern
 #pragma unroll
                 for (int j = 0; j < V; ++j) sum = fmaf(p[i][j], p[i][j], sum);
                 if (at < D) {
-                    if (a.total) X::store(static_cast<T*>(a.total) + now * D + at, p[i]);
+                    if (a.total && !added) X::store(static_cast<T*>(a.total) + now * D + at, p[i]);
                     if constexpr (!kAhead) load_weight<V>(a.weight, a.weight_bf16, at, w[0]);
 #pragma unroll
                     for (int j = 0; j < V; ++j) p[i][j] = __fmul_rn(p[i][j], w[kAhead ? i : 0][j]);
                 }
             }
         }
-        uint32_t top = 0;
+        float most = 0.0f;
         if (a.codes) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-#pragma unroll
-                for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(p[i][j]) & 0x7fffffffu);
+            for (int i = 0; i < N; ++i) most = largest(most, p[i]);
         }
+        uint32_t top = __float_as_uint(most) & 0x7fffffffu;
         reduce<WARP>(sum, top, part[turn]);
         const float rstd = row_rstd(a, sum);
         if (tid == 0) {
@@ -305,6 +347,102 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxThreads) norm_kern
     }
 }
 
+// The same for many rows on 16 bytes: `teams` rows at a time in a CTA, each by `warps` warps, N accesses of eight elements a lane. What a row costs
+// besides its elements (sums through the warps, two divisions, addresses) is some 150 instructions a thread, more than eight elements do: 8192 x 5120
+// bf16 with eight a thread executed 35 instructions an element and took 64 us (74 to codes); this takes 55 (55), 6.1 (5.3) TB/s. The weight waits
+// in shared memory.
+template <class T, int N, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) norm_teams_kernel(const NormArgs a, int warps, int teams) {
+    using X = Io<T, 8>;
+    extern __shared__ __align__(16) float weight[];  // [D] fp32
+    __shared__ float2 part[2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp / warps, first = mine * warps, team = 32 * warps;
+    const int tid = static_cast<int>(threadIdx.x) - 32 * first, D = a.D;
+    griddep_begin();
+    if (a.norm) {
+        for (int at = static_cast<int>(threadIdx.x) * 8; at < D; at += static_cast<int>(blockDim.x) * 8) {
+            float w[8];
+            load_weight<8>(a.weight, a.weight_bf16, at, w);
+            Io<float, 8>::store(weight + at, w);
+        }
+        __syncthreads();
+    }
+    const bool added = a.residual != nullptr;
+    int turn = 0;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * teams + mine; row < a.rows; row += static_cast<int64_t>(gridDim.x) * teams, turn ^= 1) {
+        typename X::Raw x[N] = {};
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if ((tid + i * team) * 8 < D) x[i] = X::raw(static_cast<const T*>(a.x) + row * a.ldx + (tid + i * team) * 8);
+        if (added) {
+            typename X::Raw r[N] = {};
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if ((tid + i * team) * 8 < D) r[i] = X::raw(static_cast<const T*>(a.residual) + row * a.ldr + (tid + i * team) * 8);
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = X::sum(x[i], r[i]);
+        }
+        float p[N][8], sum = 0.0f, most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = (tid + i * team) * 8;
+            X::value(x[i], p[i]);
+            if (at >= D) continue;
+            if (a.norm) {
+                if (a.total) X::store(static_cast<T*>(a.total) + row * D + at, x[i]);
+                float w[8];
+                const float4 u = *reinterpret_cast<const float4*>(weight + at), v = *reinterpret_cast<const float4*>(weight + at + 4);
+                w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sum = fmaf(p[i][j], p[i][j], sum);
+                    p[i][j] = __fmul_rn(p[i][j], w[j]);
+                }
+            }
+            if (a.codes) most = largest(most, p[i]);
+        }
+        uint32_t top = __float_as_uint(most) & 0x7fffffffu;
+        sum = warp_total(sum);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (warps > 1) {
+            if (lane == 0) part[turn][warp] = make_float2(sum, __uint_as_float(top));
+            named_sync(static_cast<uint32_t>(1 + mine), static_cast<uint32_t>(team));
+            sum = 0.0f, top = 0;
+            for (int w = first; w < first + warps; ++w) {
+                const float2 v = part[turn][w];
+                sum += v.x;
+                top = max(top, __float_as_uint(v.y));
+            }
+        }
+        const float rstd = row_rstd(a, sum);
+        if (tid == 0) {
+            if (a.rstd) a.rstd[row] = rstd;
+            if (a.codes) a.scales[row] = row_scale(top, rstd);
+        }
+        if (a.codes) {
+            const Encoder e(top >= kInf ? 0.0f : __uint_as_float(top));
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = (tid + i * team) * 8;
+                if (at >= D) continue;
+                int8_t* to = a.codes + row * a.pitch + at;
+                if (top >= kInf) *reinterpret_cast<uint2*>(to) = make_uint2(0, 0);
+                else store_codes<8>(to, e, p[i]);
+            }
+        }
+        if (a.y) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = (tid + i * team) * 8;
+                if (at >= D) continue;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) p[i][j] *= rstd;
+                X::store(static_cast<T*>(a.y) + row * D + at, p[i]);
+            }
+        }
+    }
+}
+
 // Rows too long for registers: read twice, the second time from L2 as far as it goes. A thread reads and writes the same
 // elements in both passes, so that y or total may be x or residual here too.
 template <class T, int V>
@@ -313,21 +451,21 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a
     const int64_t row = blockIdx.x;
     const int64_t D = a.D, step = static_cast<int64_t>(kMaxThreads) * V, first = static_cast<int64_t>(threadIdx.x) * V;
     griddep_begin();
-    float sum = 0.0f, p[V], w[V];
-    uint32_t top = 0;
+    float sum = 0.0f, most = 0.0f, p[V], w[V];
     for (int64_t at = first; at < D; at += step) {
-        load_total<T, V>(a, row, static_cast<int>(at), p);
+        const auto t = load_total<T, V>(a, row, static_cast<int>(at));
+        Io<T, V>::value(t, p);
         if (a.norm) {
 #pragma unroll
             for (int j = 0; j < V; ++j) sum = fmaf(p[j], p[j], sum);
-            if (a.total) Io<T, V>::store(static_cast<T*>(a.total) + row * D + at, p);
+            if (a.total) Io<T, V>::store(static_cast<T*>(a.total) + row * D + at, t);
             load_weight<V>(a.weight, a.weight_bf16, static_cast<int>(at), w);
 #pragma unroll
             for (int j = 0; j < V; ++j) p[j] = __fmul_rn(p[j], w[j]);
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(p[j]) & 0x7fffffffu);
+        most = largest(most, p);
     }
+    uint32_t top = __float_as_uint(most) & 0x7fffffffu;
     reduce<false>(sum, top, part);
     const float rstd = row_rstd(a, sum);
     if (threadIdx.x == 0) {
@@ -337,7 +475,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a
     const Encoder e(top >= kInf ? 0.0f : __uint_as_float(top));
     for (int64_t at = first; at < D; at += step) {
         if (a.norm && a.total) load<T, V>(static_cast<const T*>(a.total) + row * D + at, p);
-        else load_total<T, V>(a, row, static_cast<int>(at), p);
+        else Io<T, V>::value(load_total<T, V>(a, row, static_cast<int>(at)), p);
         if (a.norm) {
             load_weight<V>(a.weight, a.weight_bf16, static_cast<int>(at), w);
 #pragma unroll
@@ -590,22 +728,54 @@ int threads_for(int64_t D, int per) {
     return static_cast<int>(std::max<int64_t>(32, ((D + per - 1) / per + 31) / 32 * 32));
 }
 
+template <class T, int N, int THREADS, int CTAS>
+cudaError_t run_teams(const NormArgs& a, cudaStream_t stream) {
+    const int warps = static_cast<int>((a.D + 256 * N - 1) / (256 * N)), teams = std::max(1, THREADS / 32 / warps), smem = a.norm ? 4 * a.D : 0;
+    auto kernel = norm_teams_kernel<T, N, THREADS, CTAS>;
+    const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((a.rows + teams - 1) / teams, CTAS * device_sm_count())));
+    lc.blockDim = dim3(static_cast<unsigned>(32 * warps * teams));
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, a, warps, teams);
+}
+
 template <class T, int V>
 cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
     const int64_t D = a.D, sms = device_sm_count();
-    auto block = [&](auto n) {
+    if constexpr (V == 8) {
+        // Many rows: rows together in a CTA, 32 elements a lane (16: 67 us for 8192 x 5120 bf16, 64: 63, 32: 55), by few warps a row
+        if (a.rows > 4 * sms && D <= 20 * kMaxThreads) {
+            if (D <= 256) return run_teams<T, 1, 320, 4>(a, stream);
+            if (D <= 512) return run_teams<T, 2, 320, 3>(a, stream);
+            if (D <= 10 * kMaxThreads) return run_teams<T, 4, 320, 2>(a, stream);
+            return run_teams<T, 4, 640, 1>(a, stream);
+        }
+    }
+    auto block = [&](auto n, auto most, auto per_sm) {
         constexpr int N = decltype(n)::value;
         const int threads = threads_for(D, V * N);
         const int64_t ctas = std::min(a.rows, sms * std::max(1, 1536 / threads));
-        return launch_dependent(norm_kernel<T, V, N, false>, static_cast<int>(ctas), threads, stream, a);
+        return launch_dependent(norm_kernel<T, V, N, false, decltype(most)::value, decltype(per_sm)::value>, static_cast<int>(ctas), threads, stream, a);
     };
     if (D <= 256) {
         const int64_t ctas = std::min((a.rows + kWarpRows - 1) / kWarpRows, sms * 12);
-        return launch_dependent(norm_kernel<T, V, 8 / V, true>, static_cast<int>(ctas), 32 * kWarpRows, stream, a);
+        return launch_dependent(norm_kernel<T, V, 8 / V, true, 32 * kWarpRows, 1>, static_cast<int>(ctas), 32 * kWarpRows, stream, a);
     }
-    if (D <= 8 * kMaxThreads) return block(std::integral_constant<int, 8 / V>{});
-    if (D <= 16 * kMaxThreads) return block(std::integral_constant<int, 16 / V>{});
-    if (D <= 32 * kMaxThreads) return block(std::integral_constant<int, 32 / V>{});
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    using All = std::integral_constant<int, kMaxThreads>;
+    if (D <= 5120) return block(std::integral_constant<int, 8 / V>{}, std::integral_constant<int, 640>{}, Two{});
+    if (D <= 8 * kMaxThreads) return block(std::integral_constant<int, 8 / V>{}, All{}, One{});
+    if (D <= 16 * kMaxThreads) return block(std::integral_constant<int, 16 / V>{}, All{}, One{});
+    if (D <= 32 * kMaxThreads) return block(std::integral_constant<int, 32 / V>{}, All{}, One{});
     return launch_dependent(norm_long_kernel<T, V>, static_cast<int>(a.rows), kMaxThreads, stream, a);
 }
 
