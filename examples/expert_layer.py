@@ -1,6 +1,7 @@
-"""A gated expert layer on 4-bit weights and activations: tokens sorted by expert, encoded once, multiplied by their experts'
-matrices, gated, encoded again, multiplied back, and combined with the router's weights. Then, at the same sizes, the
-gradients that a trained router and what lies before the layer need of the gather and the combine.
+"""A gated expert layer on 4-bit weights and activations: the residual stream normalised, tokens routed by an 8-bit router, sorted by
+expert, encoded once, multiplied by their experts' matrices, gated, encoded again, multiplied back, and combined with the
+router's weights. Then, at the same sizes, the gradients that a trained router and what lies before the layer need: of the combine,
+the routing, the gather and the norm.
 
     python examples/expert_layer.py [--tokens 64] [--experts 32] [--slots 4] [--hidden 1024] [--inner 768] [--mx]
 
@@ -66,19 +67,26 @@ def run(tokens=64, experts=32, slots=4, hidden=1024, inner=768, kind=None, seed=
     r = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
     layer = ExpertLayer(kind, r(experts, 2 * inner, hidden) * hidden ** -0.5, r(experts, hidden, inner) * inner ** -0.5,
                         6.0 / (6 * 448) if kind == pnq.NVFP4 else 1.0, 8.0 / (6 * 448) if kind == pnq.NVFP4 else 1.0)
-    x = r(tokens, hidden).to(torch.bfloat16)
-    probs, ids = torch.softmax(r(tokens, experts), -1).topk(slots, -1)
-    weights, ids = (probs / probs.sum(-1, keepdim=True)).contiguous(), ids.to(torch.int32).contiguous()
+    # what comes in and the residual stream, added and normalised: as they are for the experts, in 8 bits for the router
+    norm, router = 1 + 0.1 * r(hidden), pnq.int8_quantize(r(experts, hidden) * hidden ** -0.5)
+    x, stream = torch.empty(tokens, hidden, dtype=torch.bfloat16, device="cuda"), r(tokens, hidden).to(torch.bfloat16)
+    codes, scales, total = pnq.rms_norm_int8(r(tokens, hidden).to(torch.bfloat16), norm, residual=stream, y=x)
+    logits = pnq.int8_gemm(codes, scales, *router)
+    ids, weights = pnq.expert_route(logits, slots, renormalize=True)
     y, plan = layer(x, ids, weights)
     want = reference(layer, x, plan, weights)
     err = float((y.double() - want).norm() / want.norm())
 
-    # training around frozen experts: the gradient of the combine reaches the experts' rows and the router, that of
-    # the gather the tokens (here through experts that pass their rows on)
+    # training around frozen experts: the gradient of the combine reaches the experts' rows and the router's logits, that of
+    # the gather the tokens (here through experts that pass their rows on), and that of the norm the residual stream
     xs = pnq.expert_gather(x, plan)
     dy = r(tokens, hidden).to(torch.bfloat16)
     dys, dweights = pnq.expert_combine_backward(dy, xs, plan, weights)
     dx = pnq.expert_gather_backward(dys, plan)
+    dlogits = pnq.expert_route_backward(dweights, logits, ids, renormalize=True)
+    _, _, rstd = pnq.rms_norm(total, norm)
+    dstream, dnorm = pnq.rms_norm_backward(dx, total, norm, rstd, dtotal=dy)
+    assert all(bool(g.isfinite().all()) for g in (dlogits, dstream, dnorm))
     whole = float((dx.double() - dy.double() * weights.sum(-1, keepdim=True).double()).norm() / dx.double().norm())
     assert pnq.device_error() == 0
     return err, whole, dweights
