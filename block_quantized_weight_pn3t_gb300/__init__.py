@@ -1,5 +1,5 @@
 """pnq: block-quantized weight GEMV (pn3t, pn4t, NVFP4 W4A16, grouped signed-integer formats)
-and 4-bit microscaled products (NVFP4, MXFP4) with the expert layer around them, for sm_103a.
+and 4-bit microscaled products (NVFP4, MXFP4) with the expert layer around them, norms and 8-bit products, for sm_103a.
 
 The compute path is the C-ABI library ``libpnq.so`` built from ``csrc/``; this
 package only marshals arguments to it (see ``_binding``). Importing the package

@@ -1,5 +1,5 @@
-"""4-bit microscaled operands (NVFP4, MXFP4) and the expert layer around their product: the torch wrappers of
-the pnq_fp4_* and pnq_expert_* entry points (formats, layouts and rounding steps are stated in ``include/pnq.h``). They are
+"""4-bit microscaled operands (NVFP4, MXFP4) and the expert layer around their product, norms, 8-bit rows and products: the torch wrappers
+of the pnq_fp4_*, pnq_expert_*, pnq_rms_norm* and pnq_int8_* entry points (formats, layouts and rounding steps are stated in ``include/pnq.h``). They are
 compiled (csrc/pnq_torch.cpp): they check tensors, allocate results and make one call of the library.
 
     q = fp4_quantize(NVFP4, x, g)                    # activations -> operand
@@ -12,9 +12,15 @@ compiled (csrc/pnq_torch.cpp): they check tensors, allocate results and make one
     h = fp4_quantize(NVFP4, hs, g, plan=plan, sorted=True)   # rows in expert order already (between two products)
     y = expert_combine(ys, plan, weights)            # back to tokens, router weights applied
 
-They stand outside autograd: results require no gradient. The gather and the combine have theirs as calls,
+    codes, scales, total = rms_norm_int8(x, norm, residual=stream)   # the norm of x + stream in 8 bits, a scale per row
+    y = int8_gemm(codes, scales, *int8_quantize(w))  # Y = X W^T, the sums exact
+    ids, weights = expert_route(logits, slots, renormalize=True)
+
+They stand outside autograd: results require no gradient. The gather, the combine, the routing and the norm have theirs as calls,
     dys, dweights = expert_combine_backward(dy, ys, plan, weights)
+    dlogits = expert_route_backward(dweights, logits, ids, renormalize=True)
     dx = expert_gather_backward(dxs, plan)
+    dx, dnorm = rms_norm_backward(dy, total, norm, rstd)
 """
 from __future__ import annotations
 

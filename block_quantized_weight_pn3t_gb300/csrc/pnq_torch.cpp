@@ -1,6 +1,6 @@
-// pnq_torch.cpp -- the torch wrappers of the 4-bit operands and the expert layer (module _native): checks of the tensors,
-// allocation of the results, and one call of the C ABI. No arithmetic happens here, and no autograd: results require no
-// gradient whatever the inputs do; expert_gather and expert_combine have their gradients as calls of their own.
+// pnq_torch.cpp -- the torch wrappers of the 4-bit operands, the expert layer, the norms and the 8-bit rows and product (module _native):
+// checks of the tensors, allocation of the results, and one call of the C ABI. No arithmetic happens here, and no autograd: results require
+// no gradient whatever the inputs do; expert_gather, expert_combine, expert_route and rms_norm have their gradients as calls of their own.
 //
 // These calls run several times per layer of a decode step, each a few microseconds of GPU work. Through ctypes and
 // Python an encode cost the host some 8 us, of which the launch is two; here the checks read the tensors' fields

@@ -5,7 +5,8 @@
  * Conventions shared by every entry point
  *   - Returns PNQ_OK (0) or a negative pnq_status. Nothing aborts; no kernel traps.
  *   - Device pointers are plain CUDA device addresses owned by the caller. The library
- *     allocates no device memory in any entry point: the fast GEMV paths sum their partial
+ *     allocates no device memory in any entry point (those that need scratch say how much and take the caller's, one for each call
+ *     that may be under way): the fast GEMV paths sum their partial
  *     results on chip (shared memory, and distributed shared memory between the two CTAs of
  *     a thread-block cluster), so calls may be made from any stream, during stream capture,
  *     and from several host threads at once.
