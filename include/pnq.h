@@ -456,7 +456,8 @@ typedef struct pnq_route_rule {
  *   With groups, the top_groups groups of the largest scores stay (ties to the lowest group). ids[t] = the `slots` largest c
  *   of what stays, in that order, ties to the lowest expert. weights[t][j] = scale * s, over the sum of the token's chosen s
  *   if renormalize.
- * Scores are compared as they are, not as they round: without bias and groups by the logits, otherwise in 64 bits where fp32 does not decide.
+ * Scores are compared as they are, not as they round: without bias and groups by the logits, otherwise to some 2^-44 of themselves where fp32 does not
+ * decide (exponentials below 2^-125 count as 0). Equal ones go by the logit, then by the index. Finite biases: |bias| up to about 1e38.
  * An expert whose logit or bias is -infinity is out: it is not chosen and adds nothing to its group. A slot for which no expert is left
  * has the id -1 and the weight 0 (pnq_expert_sort drops it): a row of -infinities, a padded token, takes part in nothing. A token
  * with a NaN logit, with a softmax logit of +infinity, or for whose choice scores the bias is a NaN or +infinity, has the ids 0 .. slots
@@ -488,7 +489,7 @@ int pnq_expert_route_backward(int type, const float* dweights, const void* logit
  *   y       t r w, contiguous [rows][D], the type of X (NULL: not written; it may be X's own buffer where ldx = D);
  *   rstd    r, device fp32 [rows] (NULL: not written), for the backward pass;
  *   codes, scales  (NULL together: not written) of p = fp32(t w): scale = max|p| r / 127, code = the whole number nearest to
- *           127 p / max|p|, ties to even. A row of zeros has the scale 0; a row with a NaN or an infinity (of t, w or p) has the scale NaN and codes of
+ *           127 p / max|p|, ties to even. A row of zeros has the scale 0 (NaN where eps is 0, as y is); a row with a NaN or an infinity (of t, w or p) has the scale NaN and codes of
  *           zero, so that what is computed from it is NaN.
  * type: PNQ_F32 or PNQ_BF16, of X, residual, total and y (row strides in elements); weight: device [D], PNQ_F32 or PNQ_BF16 of its own.
  * Sums of squares are fp32 (|t| up to about 1e18); rows on 16 bytes with D a multiple of 8 are faster. Errors: PNQ_ERR_TYPE,

@@ -141,6 +141,18 @@ def test_rows_without_values():
     assert bool(scales.isnan().all()) and bool((codes == 0).all())
 
 
+def test_rows_of_zeros_without_eps():
+    """r is infinite there: y and the scale are NaN, the codes zero, and other rows do not see it."""
+    x, w = torch.randn(3, 96, device="cuda"), torch.ones(96, device="cuda")
+    x[1] = 0
+    for rows in (x, x.repeat(400, 1)):
+        y, _, rstd = pnq.rms_norm(rows, w, 0.0)
+        codes, scales, _ = pnq.rms_norm_int8(rows, w, 0.0)
+        assert bool(y[1].isnan().all()) and bool(rstd[1].isinf()) and bool(scales[1].isnan()) and not bool(codes[1].any())
+        assert bool(y[[0, 2]].isfinite().all()) and bool(scales[[0, 2]].isfinite().all())
+    assert float(pnq.int8_quantize(x)[1][1]) == 0.0
+
+
 @pytest.mark.parametrize("rows,D", [(6, 2048), (6, 1999), (6, 40000), (2000, 2048), (1500, 5120), (2001, 264), (900, 17408), (1300, 999)])
 def test_in_place_and_given_buffers(rows, D):
     x, w, res = inputs(rows, D, torch.bfloat16, torch.float32, True)
