@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "pnq_device.cuh"
 #include "pnq_internal.h"
@@ -665,41 +666,69 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* partial,
 
 // ---- codes back to values -----------------------------------------------------------------------------
 
-// out[r][k] = codes[r][k] * scales[r]: V consecutive elements a thread and step; the rows' pieces of V (`per` a row) one after the other, so that
-// short rows fill CTAs too.
-constexpr int kDecodeSteps = 4, kDecodeThreads = 256;
-template <class T, int V>
+// out[r][k] = codes[r][k] * scales[r]: four consecutive elements a thread and step; the rows' pieces of four (`per` a row) one after the other, so
+// that short rows fill CTAs too. Many pieces: eight steps, all loads under way at once (17408 x 5120 to fp32 72.6 us, to bf16 57.7; four 75.3 and
+// 61.3, sixteen 79.9 and 68.0). Fewer than some sixteen such CTAs an SM: four, for more CTAs (13 x 17408 1.9 us, with eight 2.3).
+constexpr int kDecodeThreads = 128;
+template <class T, int STEPS>
 __global__ void __launch_bounds__(kDecodeThreads) int8_dequantize_kernel(const int8_t* codes, int64_t pitch, const float* scales, int64_t rows,
                                                                          int per, T* out) {
     griddep_begin();
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kDecodeSteps * kDecodeThreads), row0 = first / per;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (STEPS * kDecodeThreads), row0 = first / per;
     const int in0 = static_cast<int>(first - row0 * per);  // of the CTA's first piece within its row
-    uint32_t word[kDecodeSteps];
-    float scale[kDecodeSteps];
-    int64_t row[kDecodeSteps];
-    int at[kDecodeSteps];
+    uint32_t word[STEPS];
+    float scale[STEPS];
+    int64_t row[STEPS];
+    int at[STEPS];
 #pragma unroll
-    for (int i = 0; i < kDecodeSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
         const uint32_t u = static_cast<uint32_t>(in0) + i * kDecodeThreads + threadIdx.x, r = u / static_cast<uint32_t>(per);
         row[i] = row0 + r;
         at[i] = static_cast<int>(u - r * per);
         if (row[i] < rows) {
-            const uint8_t* c = reinterpret_cast<const uint8_t*>(codes) + row[i] * pitch + static_cast<int64_t>(at[i]) * V;
-            if constexpr (V == 4) word[i] = ld_l2(reinterpret_cast<const uint32_t*>(c));
-            else word[i] = ld_l2(c);
+            word[i] = ld_l2(reinterpret_cast<const uint32_t*>(codes + row[i] * pitch) + at[i]);
             scale[i] = ld_l2(scales + row[i]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < kDecodeSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
         if (row[i] >= rows) continue;
         float f[4];
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = static_cast<float>(static_cast<int8_t>(word[i] >> (8 * j))) * scale[i];
-        T* o = out + (row[i] * per + at[i]) * V;
-        if constexpr (V == 4 && sizeof(T) == 4) *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
-        else if constexpr (V == 4) *reinterpret_cast<uint2*>(o) = make_uint2(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]));
-        else *o = T(f[0]);
+        for (int j = 0; j < 4; ++j) f[j] = static_cast<float>(static_cast<int8_t>(word[i] >> (8 * j))) * scale[i];
+        T* o = out + (row[i] * per + at[i]) * 4;
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+        else *reinterpret_cast<uint2*>(o) = make_uint2(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]));
+    }
+}
+
+// The same for rows of any length and alignment: pieces of 128 elements of a row (`per` a row), two a warp, of each four elements a lane, 32 apart.
+template <class T>
+__global__ void __launch_bounds__(kDecodeThreads) int8_dequantize_any_kernel(const int8_t* codes, int64_t pitch, const float* scales, int64_t rows,
+                                                                             int K, int per, T* out) {
+    griddep_begin();
+    const int lane = threadIdx.x & 31;
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * (kDecodeThreads / 32) + (threadIdx.x >> 5)) * 2;
+    uint8_t code[2][4];
+    float scale[2];
+    int64_t row[2];
+    int at[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        row[i] = (first + i) / per;
+        at[i] = static_cast<int>(first + i - row[i] * per) * 128 + lane;
+        if (row[i] >= rows) continue;
+        scale[i] = ld_l2(scales + row[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (at[i] + 32 * j < K) code[i][j] = ld_l2(reinterpret_cast<const uint8_t*>(codes + row[i] * pitch + at[i] + 32 * j));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (row[i] >= rows) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (at[i] + 32 * j < K) out[row[i] * K + at[i] + 32 * j] = T(static_cast<float>(static_cast<int8_t>(code[i][j])) * scale[i]);
     }
 }
 
@@ -860,17 +889,22 @@ cudaError_t launch_int8_dequantize(const int8_t* codes, int64_t pitch, const flo
                                    cudaStream_t stream) {
     const bool wide = K % 4 == 0 && pitch % 4 == 0 && reinterpret_cast<uintptr_t>(codes) % 4 == 0 &&
                       reinterpret_cast<uintptr_t>(out) % (bf16 ? 8 : 16) == 0;
-    const int64_t per = K / (wide ? 4 : 1), ctas = (rows * per + kDecodeSteps * kDecodeThreads - 1) / (kDecodeSteps * kDecodeThreads);
+    // threads of the kernels' first kind and warps of the second, at one step each
+    const int64_t per = wide ? K / 4 : (K + 127) / 128, each = wide ? kDecodeThreads : kDecodeThreads / 32, ctas = (rows * per + each - 1) / each;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    auto go = [&](auto kernel, auto* o) {
-        return launch_dependent(kernel, static_cast<int>(ctas), kDecodeThreads, stream, codes, pitch, scales, rows, static_cast<int>(per), o);
+    auto go = [&](auto* o) {
+        using T = std::remove_pointer_t<decltype(o)>;
+        auto steps = [&](auto s) {
+            constexpr int S = decltype(s)::value;
+            return launch_dependent(int8_dequantize_kernel<T, S>, static_cast<int>((ctas + S - 1) / S), kDecodeThreads, stream, codes, pitch, scales,
+                                    rows, static_cast<int>(per), o);
+        };
+        if (!wide)
+            return launch_dependent(int8_dequantize_any_kernel<T>, static_cast<int>((ctas + 1) / 2), kDecodeThreads, stream, codes, pitch, scales, rows,
+                                    static_cast<int>(K), static_cast<int>(per), o);
+        return ctas > 8 * 16 * static_cast<int64_t>(device_sm_count()) ? steps(std::integral_constant<int, 8>{}) : steps(std::integral_constant<int, 4>{});
     };
-    if (bf16) {
-        auto* o = static_cast<__nv_bfloat16*>(out);
-        return wide ? go(int8_dequantize_kernel<__nv_bfloat16, 4>, o) : go(int8_dequantize_kernel<__nv_bfloat16, 1>, o);
-    }
-    auto* o = static_cast<float*>(out);
-    return wide ? go(int8_dequantize_kernel<float, 4>, o) : go(int8_dequantize_kernel<float, 1>, o);
+    return bf16 ? go(static_cast<__nv_bfloat16*>(out)) : go(static_cast<float*>(out));
 }
 
 }  // namespace pnq

@@ -102,6 +102,18 @@ def test_quantize(rows, K, dtype, extra):
     assert torch.equal(scales, by_127(top))
 
 
+@pytest.mark.parametrize("rows,K", [(1, 1), (5, 127), (3, 128), (700, 129), (333, 2063), (2100, 1000), (9000, 1024), (40, 30001)])
+@pytest.mark.parametrize("at,extra", [(0, 0), (0, 1), (1, 3), (4, 8)])
+def test_decode_of_any_rows(rows, K, at, extra):
+    """Codes `at` bytes into a buffer, rows K + extra bytes apart: code * scale in fp32, rounded once more for bf16; bytes behind a row are not read."""
+    gen = torch.Generator(device="cuda").manual_seed(rows + K)
+    buf = torch.randint(-128, 128, (at + rows * (K + extra) + 16,), generator=gen, device="cuda", dtype=torch.int8)
+    codes, scales = buf[at: at + rows * (K + extra)].view(rows, K + extra)[:, :K], torch.rand(rows, generator=gen, device="cuda")
+    want = codes.float() * scales[:, None]
+    assert torch.equal(pnq.int8_dequantize(codes, scales), want)
+    assert torch.equal(pnq.int8_dequantize(codes, scales, dtype=torch.bfloat16), want.to(torch.bfloat16))
+
+
 def test_codes_on_the_borders():
     """Rows whose values lie on borders between codes, one step of fp32 to either side of them, and rows of every magnitude."""
     k = torch.arange(-127, 127, device="cuda", dtype=torch.float32) + 0.5
