@@ -608,6 +608,9 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
                  : "memory");
     return v;
 }
+__device__ __forceinline__ void st_shared_v4(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 
 // f(std::integral_constant<int, I>) for I = 0 .. N - 1, unrolled at compile time.
 template <class F, int... I>

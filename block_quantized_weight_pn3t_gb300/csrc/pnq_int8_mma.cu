@@ -6,14 +6,23 @@
 // taken out, turned into whole numbers and added to 32-bit sums in registers, while the next 1024 go to a second accumulator.
 // That makes the result independent of tile shapes and of how K is split.
 //
-// Layout. The weight rows are the MMA's M axis (128 lanes of tensor memory per CTA), the activation rows its N axis. x is widened to
-// fp16 once, in a pass of its own, to scratch. The weights stay 8-bit until they are on the SM: four warps read a stage's codes from shared
-// memory, one row a thread, widen them (a byte b xor 128 beside the byte 0x64 is the fp16 number 1024 + 128 + b, less 1152) and write
-// them to tensor memory, where the MMA takes its A operand from. Weight bytes cross HBM, L2 and shared memory as they are.
+// Layout. The weight rows are the MMA's M axis (128 lanes of tensor memory per CTA), the activation rows its N axis. The weights stay 8-bit until
+// they are on the SM: four warps (or eight, in turn) read a stage's codes from shared memory, one row a thread, widen them (a byte b xor 128
+// beside the byte 0x64 is the fp16 number 1024 + 128 + b, less 1152) and write them to tensor memory, where the MMA takes its A operand
+// from. Weight bytes cross HBM, L2 and shared memory as they are. x is widened once, in a pass of its own, to scratch (1.2 to 2.8 us), or, for
+// products of few stages, by the same warps from a stage's codes to shared memory.
 //
-// Roles of the warps of a CTA: 0..3 widen, 4..11 take accumulators out (two per lane quarter, half of the columns each), 12 copies
-// (one lane), 13 issues MMAs (one lane). Pairs (CG = 2): two CTAs work on one tile of 256 weight rows (cta_group::2), each with its own
-// 128 and half of the activation rows; the first one's thread issues for both.
+// What bounds it. Many rows: the tensor pipe (8192 x 17408 x 5120 745 us in short runs, 1.96 PFLOP/s; 842 in long ones, at the power limit;
+// counters of 2048 rows: 85 % busy). A stage of 128 of K with 192 rows moves 137 bytes of shared memory a cycle of its MMAs, where 128 is
+// the limit: so activations are not widened there. Few rows: HBM for the weights' bytes (16 x 17408 x 5120 20.7 us for 89 MB), and what
+// stands before and after it: launch, the first copies, the sum over a cluster (100 x 256 with 64 rows: 4.8 us).
+// What it took (8192 x 17408 x 5120): signals within a pair that do not release memory (2718 us to 1125: a release at cluster scope held each warp up
+// by 0.5 us a stage), stages of 128 of K (943), waits by whole warps (792), a row widened before its slot is waited for (781), accumulators of a tile's
+// end taken out under the next (745).
+//
+// Roles of the warps of a CTA: 0..3 (0..7) widen, the next 8 take accumulators out (two per lane quarter, half of the columns each), then one that
+// copies (one lane) and one that issues MMAs (one lane). Pairs (CG = 2): two CTAs work on one tile of 256 weight rows (cta_group::2), each with
+// its own 128 and half of the activation rows; the first one's thread issues for both.
 //
 // Every wait is bounded; a wait that gives up records its site in the device error word and ends the role, and tensor memory is
 // released whatever the outcome.
@@ -58,8 +67,8 @@ struct MmaArgs {
     int early;         // the weights are the caller's: no kernel in flight writes them
 };
 
-// Tiles of at most BN activation rows, by CG CTAs with SETS sets of four warps that widen.
-template <int BN, int CG, int SETS>
+// Tiles of at most BN activation rows, by CG CTAs with SETS sets of four warps that widen the weights, and with WX the activations too.
+template <int BN, int CG, int SETS, bool WX>
 struct Plan {
     static constexpr int kCtas = BN <= 64 ? 2 : 1;             // CTAs of an SM
     static constexpr int kCopyWarp = 4 * SETS + kDrainWarps, kMmaWarp = kCopyWarp + 1, kThreads = 32 * (kMmaWarp + 1);
@@ -67,9 +76,12 @@ struct Plan {
     static constexpr int kStep = 16 * CG;                      // a tile's activation rows are a multiple of it
     static constexpr int kCols = kCtas == 2 ? 256 : 512;       // tensor-memory columns: two accumulators, and the slots
     static constexpr int kSplit = 8 / CG;                      // the most that share a tile's K: clusters of 8 CTAs
-    static int stage(int bn) { return kCodes + bn / CG * KS * 2; }
-    static int stages(int bn) { return std::min(kMaxStages, (kSmemLimit / kCtas - 3072) / stage(bn)); }
-    static int slots(int bn) { return std::min({kMaxSlots, stages(bn), (kCols - 2 * bn) / kSlotCols}); }
+    static constexpr bool kWidenX = WX;                        // a stage holds x's codes; beside every slot of tensor memory there is one of x
+    static int slot(int bn) { return kWidenX ? bn * KS * 2 : 0; }
+    static int stage(int bn) { return kCodes + (kWidenX ? bn * KS : bn / CG * KS * 2); }
+    static int slots(int bn) { return std::min(kMaxSlots, (kCols - 2 * bn) / kSlotCols); }
+    static int stages(int bn) { return std::min(kMaxStages, (kSmemLimit / kCtas - 3072 - slots(bn) * slot(bn)) / stage(bn)); }
+    static int smem(int bn) { return stages(bn) * stage(bn) + slots(bn) * slot(bn) + 1024; }
     // fp32 accumulators, fp16 operands, N, M = 128 per CTA
     static __device__ uint32_t idesc(int bn) {
         return (1u << 4) | (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(CG * kRows >> 4) << 24);
@@ -141,11 +153,11 @@ struct Walk {
     }
 };
 
-template <int BN, int CG, int SETS, class T>
-__global__ void __launch_bounds__(Plan<BN, CG, SETS>::kBound, Plan<BN, CG, SETS>::kCtas) int8_mma_kernel(const __grid_constant__ CUtensorMap map_w,
+template <int BN, int CG, int SETS, bool WX, class T>
+__global__ void __launch_bounds__(Plan<BN, CG, SETS, WX>::kBound, Plan<BN, CG, SETS, WX>::kCtas) int8_mma_kernel(const __grid_constant__ CUtensorMap map_w,
                                                                                              const __grid_constant__ CUtensorMap map_x,
                                                                                              const MmaArgs a) {
-    using P = Plan<BN, CG, SETS>;
+    using P = Plan<BN, CG, SETS, WX>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     __shared__ __align__(8) uint64_t bars[3 * kMaxStages + kMaxSlots + 5];
@@ -153,14 +165,16 @@ __global__ void __launch_bounds__(Plan<BN, CG, SETS>::kBound, Plan<BN, CG, SETS>
     const uint32_t b0 = smem_addr(bars), sbase = smem_addr(base);
     auto full_w = [&](int s) { return b0 + 8u * s; };                                // the weights of a stage, this CTA's
     auto full_x = [&](int s) { return b0 + 8u * (kMaxStages + s); };                 // the activations, both CTAs', at the first
-    auto empty = [&](int s) { return b0 + 8u * (2 * kMaxStages + s); };              // the stage's MMAs are done
+    auto slot_done = full_x;                                                          // widened here: a slot's MMAs are done
+    auto empty = [&](int s) { return b0 + 8u * (2 * kMaxStages + s); };              // the stage's MMAs are done; widened here: its codes are read
     auto wide = [&](int i) { return b0 + 8u * (3 * kMaxStages + i); };               // a slot is written, by both CTAs, at the first
     auto acc_full = [&](int i) { return b0 + 8u * (3 * kMaxStages + kMaxSlots + i); };
     auto acc_empty = [&](int i) { return b0 + 8u * (3 * kMaxStages + kMaxSlots + 2 + i); };
     const uint32_t finished = b0 + 8u * (3 * kMaxStages + kMaxSlots + 4);
     const int S = a.stages, A = a.slots, bn = a.bn;
-    const uint32_t box = static_cast<uint32_t>(bn / CG) * 128;  // bytes of 64 of K of this CTA's activations
-    const uint32_t x_bytes = 2 * box, stage = kCodes + x_bytes;
+    const uint32_t box = static_cast<uint32_t>(bn / CG) * 128;  // bytes of 64 of K of this CTA's activations as fp16, of 128 as codes
+    const uint32_t x_bytes = P::kWidenX ? box : 2 * box, stage = kCodes + x_bytes;
+    const uint32_t xslots = sbase + static_cast<uint32_t>(S) * stage;  // widened here: activations beside the slots of tensor memory
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? blockIdx.x & 1u : 0u;
 
@@ -168,7 +182,7 @@ __global__ void __launch_bounds__(Plan<BN, CG, SETS>::kBound, Plan<BN, CG, SETS>
         for (int s = 0; s < S; ++s) {
             mbar_init(full_w(s), 1);
             mbar_init(full_x(s), 1);
-            mbar_init(empty(s), 1);
+            mbar_init(empty(s), P::kWidenX ? 4 : 1);
         }
         for (int i = 0; i < A; ++i) mbar_init(wide(i), CG * 4);
         for (int i = 0; i < 2; ++i) {
@@ -205,8 +219,9 @@ __global__ void __launch_bounds__(Plan<BN, CG, SETS>::kBound, Plan<BN, CG, SETS>
             bool ok = true;
             int s = 0, issued = 0, ahead = 0;  // ahead: stages of the first tile whose weights are under way
             uint32_t phase = 1;                // the first wait for each free stage passes
+            const uint32_t x_box = static_cast<uint32_t>(a.xbox * KS);
             auto load_weights = [&](int i, int kt) {
-                mbar_arrive_expect_tx(full_w(i), kCodes);
+                mbar_arrive_expect_tx(full_w(i), kCodes + (P::kWidenX ? x_box : 0u));
                 tma_load_2d(sbase + static_cast<uint32_t>(i) * stage + x_bytes, &map_w, kt * KS, tile.n0 + static_cast<int>(rank) * kRows,
                             full_w(i), pol_w);
             };
@@ -227,12 +242,16 @@ __global__ void __launch_bounds__(Plan<BN, CG, SETS>::kBound, Plan<BN, CG, SETS>
                         load_weights(s, kt);
                     }
                     const uint32_t st = sbase + static_cast<uint32_t>(s) * stage;
-                    if (rank == 0) mbar_arrive_expect_tx(full_x(s), static_cast<uint32_t>(CG * a.xbox * KS * 2));
-                    const uint32_t bar = CG == 2 ? cluster_addr(full_x(s), pair_leader()) : full_x(s);
+                    if constexpr (P::kWidenX) {
+                        tma_load_2d(st, &map_x, kt * KS, xrow, full_w(s), pol_x);
+                    } else {
+                        if (rank == 0) mbar_arrive_expect_tx(full_x(s), CG * 2 * x_box);
+                        const uint32_t bar = CG == 2 ? cluster_addr(full_x(s), pair_leader()) : full_x(s);
 #pragma unroll
-                    for (int h = 0; h < KS / 64; ++h) {
-                        if constexpr (CG == 2) tma_load_2d_pair(st + h * box, &map_x, kt * KS + 64 * h, xrow, bar, pol_x);
-                        else tma_load_2d(st + h * box, &map_x, kt * KS + 64 * h, xrow, bar, pol_x);
+                        for (int h = 0; h < KS / 64; ++h) {
+                            if constexpr (CG == 2) tma_load_2d_pair(st + h * box, &map_x, kt * KS + 64 * h, xrow, bar, pol_x);
+                            else tma_load_2d(st + h * box, &map_x, kt * KS + 64 * h, xrow, bar, pol_x);
+                        }
                     }
                     ++issued;
                     if (++s == S) s = 0, phase ^= 1;
@@ -244,7 +263,7 @@ __global__ void __launch_bounds__(Plan<BN, CG, SETS>::kBound, Plan<BN, CG, SETS>
             bool drained = true;
             for (int g = max(0, issued - S); drained && g < issued; ++g) {
                 drained = mbar_wait_cycles(full_w(g % S), (g / S) & 1);
-                drained = drained && mbar_wait_cycles(rank == 0 ? full_x(g % S) : empty(g % S), (g / S) & 1);
+                if constexpr (!P::kWidenX) drained = drained && mbar_wait_cycles(rank == 0 ? full_x(g % S) : empty(g % S), (g / S) & 1);
             }
             if (!drained) record_error(a.err, kErrDrainWait);
         }
@@ -264,18 +283,18 @@ __global__ void __launch_bounds__(Plan<BN, CG, SETS>::kBound, Plan<BN, CG, SETS>
                         ok = false;
                         break;
                     }
-                    if (!mbar_wait_cycles(full_x(s), phase) || !mbar_wait_cycles(wide(slot), slot_phase)) {
+                    if ((!P::kWidenX && !mbar_wait_cycles(full_x(s), phase)) || !mbar_wait_cycles(wide(slot), slot_phase)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t acc = tmem + static_cast<uint32_t>(buf * bn), from = slots + static_cast<uint32_t>(slot * kSlotCols);
-                    const uint32_t st = sbase + static_cast<uint32_t>(s) * stage;
+                    const uint32_t st = P::kWidenX ? xslots + static_cast<uint32_t>(slot) * 2 * box : sbase + static_cast<uint32_t>(s) * stage;
                     const uint64_t x0 = desc_rows(st), x1 = desc_rows(st + box);
 #pragma unroll
                     for (int j = 0; j < KS / 16; ++j)
                         mma_f16<CG>(acc, from + 8 * j, (j < 4 ? x0 : x1) + 2 * (j % 4), idesc, (in_chunk > 0 || j > 0) ? 1u : 0u);
-                    commit(empty(s));  // the stage and its slot are free
+                    commit(P::kWidenX ? slot_done(slot) : empty(s));  // the slot is free, and where it holds activations the stage
                     if (++s == S) s = 0, phase ^= 1;
                     if (++slot == A) slot = 0, slot_phase ^= 1;
                     if (++in_chunk == kChunkStages || kt == kt1 - 1) {
@@ -296,10 +315,10 @@ __global__ void __launch_bounds__(Plan<BN, CG, SETS>::kBound, Plan<BN, CG, SETS>
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         bool ok = true;
         int i = 0, s = 0, slot = 0, es = 0;   // es, ephase: the stage whose MMAs were the slot's last, A stages before
-        uint32_t phase = 0, ephase = 0;
+        uint32_t phase = 0, ephase = 0, sphase = 1;
         auto step = [&] {
             if (++s == S) s = 0, phase ^= 1;
-            if (++slot == A) slot = 0;
+            if (++slot == A) slot = 0, sphase ^= 1;
             if (i++ >= A && ++es == S) es = 0, ephase ^= 1;
         };
         while (ok && walk.next(tile)) {
@@ -330,7 +349,7 @@ __global__ void __launch_bounds__(Plan<BN, CG, SETS>::kBound, Plan<BN, CG, SETS>
 #pragma unroll
                     for (int h = 0; h < KS / 32; ++h) tmem_st16(slot_at(h), v[h]);
                 } else {
-                    ok = slot_free();
+                    ok = P::kWidenX ? mbar_wait_cycles_warp(slot_done(slot), sphase) : slot_free();
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -339,6 +358,26 @@ __global__ void __launch_bounds__(Plan<BN, CG, SETS>::kBound, Plan<BN, CG, SETS>
                         widen(h, v);
                         tmem_st16(slot_at(h), v);
                     }
+                }
+                if constexpr (P::kWidenX) {
+                    // the activations, 16 codes a thread and turn: 32 bytes in the row's half of K, where the swizzle of 128 bytes puts them (lanes
+                    // of the two halves write theirs in opposite orders, so that they do not meet in a bank)
+                    const uint32_t from = sbase + static_cast<uint32_t>(s) * stage, to = xslots + static_cast<uint32_t>(slot) * 2 * box;
+                    const int c = row & 7, first = 2 * (c & 3) + (c >> 2);
+                    for (int r = row >> 3; r < bn; r += 16) {
+                        const uint4 w = ld_shared_v4<0>(from + static_cast<uint32_t>(r * KS + 16 * (c ^ (r & 7))));
+                        uint4 u, v;
+                        int8x4_to_f16x2(w.x, u.x, u.y);
+                        int8x4_to_f16x2(w.y, u.z, u.w);
+                        int8x4_to_f16x2(w.z, v.x, v.y);
+                        int8x4_to_f16x2(w.w, v.z, v.w);
+                        const uint32_t row_at = to + static_cast<uint32_t>(c >> 2) * box + static_cast<uint32_t>(r * 128);
+                        st_shared_v4(row_at + 16 * (first ^ (r & 7)), c < 4 ? u : v);
+                        st_shared_v4(row_at + 16 * (first ^ 1 ^ (r & 7)), c < 4 ? v : u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty(s));
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -514,9 +553,9 @@ struct Cut {
 
 // Clusters of CG by ks CTAs of a kernel that the current device holds at once (not every group of SMs divides evenly). The runtime counts one CTA
 // an SM for kernels that allocate tensor memory; two fit where theirs is half of it.
-template <int BN, int CG, int SETS>
+template <int BN, int CG, int SETS, bool WX>
 cudaError_t resident(int ks, int smem, int* clusters) {
-    using P = Plan<BN, CG, SETS>;
+    using P = Plan<BN, CG, SETS, WX>;
     static std::mutex mu;
     static std::map<std::pair<int, int>, int> known;
     int dev = 0;
@@ -525,7 +564,7 @@ cudaError_t resident(int ks, int smem, int* clusters) {
     std::lock_guard<std::mutex> lock(mu);
     int& n = known[{dev, ks}];
     if (n == 0) {
-        const void* kernel = reinterpret_cast<const void*>(int8_mma_kernel<BN, CG, SETS, float>);
+        const void* kernel = reinterpret_cast<const void*>(int8_mma_kernel<BN, CG, SETS, WX, float>);
         e = opt_in_smem(kernel, smem);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t lc{};
@@ -549,9 +588,9 @@ cudaError_t resident(int ks, int smem, int* clusters) {
 
 // The tiles of a product, and over how many CTAs (pairs) K is split: so that the fewest stages come one after the other, with a cluster's sum
 // counted as three. K is split only where all clusters run at once: a second round of them costs more than a split gains.
-template <int BN, int CG, int SETS>
+template <int BN, int CG, int SETS, bool WX>
 cudaError_t cut_by(int64_t M, int64_t N, int64_t K, Cut* c) {
-    using P = Plan<BN, CG, SETS>;
+    using P = Plan<BN, CG, SETS, WX>;
     const int64_t mt = (M + BN - 1) / BN, nk = (K + KS - 1) / KS;
     c->bn = static_cast<int>(((M + mt - 1) / mt + P::kStep - 1) / P::kStep * P::kStep);
     c->tiles = (N + CG * kRows - 1) / (CG * kRows) * mt;
@@ -559,7 +598,7 @@ cudaError_t cut_by(int64_t M, int64_t N, int64_t K, Cut* c) {
     c->stages = (c->tiles * CG + P::kCtas * device_sm_count() - 1) / (P::kCtas * device_sm_count()) * nk;
     for (int ks = 2; ks <= P::kSplit && nk >= 2 * ks; ++ks) {
         int clusters = 0;
-        const cudaError_t e = resident<BN, CG, SETS>(ks, P::stages(c->bn) * P::stage(c->bn) + 1024, &clusters);
+        const cudaError_t e = resident<BN, CG, SETS, WX>(ks, P::smem(c->bn), &clusters);
         if (e != cudaSuccess) return e;
         const int64_t stages = (nk + ks - 1) / ks + 3;
         if (c->tiles <= clusters && stages < c->stages) c->stages = stages, c->ks = ks;
@@ -567,11 +606,11 @@ cudaError_t cut_by(int64_t M, int64_t N, int64_t K, Cut* c) {
     return cudaSuccess;
 }
 
-template <int BN, int CG, int SETS, class T>
+template <int BN, int CG, int SETS, bool WX, class T>
 cudaError_t run_mma(const CUtensorMap& map_w, const CUtensorMap& map_x, const MmaArgs& a, int64_t tiles, cudaStream_t stream) {
-    using P = Plan<BN, CG, SETS>;
-    const int smem = a.stages * P::stage(a.bn) + 1024;
-    auto kern = int8_mma_kernel<BN, CG, SETS, T>;
+    using P = Plan<BN, CG, SETS, WX>;
+    const int smem = P::smem(a.bn);
+    auto kern = int8_mma_kernel<BN, CG, SETS, WX, T>;
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc{};
@@ -593,26 +632,27 @@ cudaError_t run_mma(const CUtensorMap& map_w, const CUtensorMap& map_x, const Mm
     return cudaLaunchKernelEx(&lc, kern, map_w, map_x, a);
 }
 
-template <int BN, int CG, int SETS>
-cudaError_t run_cut(const Cut& c, bool bf16, const void* x, const int8_t* w, int64_t ldw, MmaArgs a, cudaStream_t stream) {
-    using P = Plan<BN, CG, SETS>;
+template <int BN, int CG, int SETS, bool WX>
+cudaError_t run_cut(const Cut& c, bool bf16, const void* x, int64_t ldx, const int8_t* w, int64_t ldw, MmaArgs a, cudaStream_t stream) {
+    using P = Plan<BN, CG, SETS, WX>;
     const int64_t M = a.M, N = a.N, K = a.K;
     a.bn = c.bn, a.ks = c.ks;
     a.stages = P::stages(c.bn), a.slots = P::slots(c.bn);
     a.xbox = CG == 2 ? c.bn / CG : static_cast<int>(std::min<int64_t>(c.bn, M));
     a.weights_once = M <= c.bn;
     CUtensorMap map_w, map_x;
-    if (!encode_rows_map(&map_w, w, N, K, 1, ldw, KS, kRows) || !encode_rows_map(&map_x, x, M, K, 2, (K + 15) / 16 * 32, 64, a.xbox))
-        return cudaErrorInvalidValue;
-    return bf16 ? run_mma<BN, CG, SETS, __nv_bfloat16>(map_w, map_x, a, c.tiles, stream)
-                : run_mma<BN, CG, SETS, float>(map_w, map_x, a, c.tiles, stream);
+    const bool mapped = P::kWidenX ? encode_rows_map(&map_x, x, M, K, 1, ldx, KS, a.xbox)
+                                   : encode_rows_map(&map_x, x, M, K, 2, (K + 15) / 16 * 32, 64, a.xbox);
+    if (!mapped || !encode_rows_map(&map_w, w, N, K, 1, ldw, KS, kRows)) return cudaErrorInvalidValue;
+    return bf16 ? run_mma<BN, CG, SETS, WX, __nv_bfloat16>(map_w, map_x, a, c.tiles, stream)
+                : run_mma<BN, CG, SETS, WX, float>(map_w, map_x, a, c.tiles, stream);
 }
 
 bool on_16(const Int8View& w) { return reinterpret_cast<uintptr_t>(w.codes) % 16 == 0 && w.ld % 16 == 0; }
 
 }  // namespace
 
-// x as fp16, and the weights' codes where their rows are not on 16 bytes.
+// x as fp16 (or its codes where their rows are not on 16 bytes), and the weights' codes where their rows are not on 16 bytes.
 uint64_t int8_mma_scratch(int64_t M, const Int8View& w, int64_t K) {
     const uint64_t per = static_cast<uint64_t>((K + 15) / 16);
     return static_cast<uint64_t>(M) * per * 32 + (on_16(w) ? 0 : static_cast<uint64_t>(w.rows) * per * 16);
@@ -621,34 +661,44 @@ uint64_t int8_mma_scratch(int64_t M, const Int8View& w, int64_t K) {
 cudaError_t launch_int8_mma(const Int8View& x, const Int8View& w, int64_t K, bool bf16, void* Y, void* scratch, int* err,
                             cudaStream_t stream) {
     const int64_t per = (K + 15) / 16;
-    cudaError_t e = copy_rows<true>(x.codes, x.ld, x.rows, K, scratch, stream);
+    MmaArgs a{};
+    a.x_scales = x.scales, a.w_scales = w.scales, a.Y = Y, a.err = err;
+    a.M = static_cast<int>(x.rows), a.N = static_cast<int>(w.rows), a.K = static_cast<int>(K);
+    // up to 64 rows a CTA a tile; above, pairs: tiles of at most 128 rows, widened by eight warps, or of at most 192 by four (more would not leave
+    // registers for 192 rows' sums), by the stages that come one after the other and what one takes, 0.22 us and 0.00122 for each row
+    // (fitted on 17408 x 5120, 5120 x 17408 and 4096 x 4096, 65 to 2048 rows)
+    Cut small{}, few{}, many{};
+    cudaError_t e = cut_by<64, 1, 1, false>(a.M, a.N, a.K, &small);
+    if (e == cudaSuccess && a.M > 64) e = cut_by<128, 2, 2, false>(a.M, a.N, a.K, &few);
+    if (e == cudaSuccess && a.M > 64) e = cut_by<192, 2, 1, false>(a.M, a.N, a.K, &many);
     if (e != cudaSuccess) return e;
+    auto time = [](const Cut& c) { return static_cast<double>(c.stages) * (0.22 + 0.00122 * c.bn); };
+    // A kernel that widens x itself saves the pass that does it, some 1.2 us, and takes 0.0028 us more for each row of each stage: for few stages (64 x
+    // 1001 x 2063 7.9 us instead of 8.4, 64 x 4096 x 4096 13.6 and 14.2, but 33 x 17408 x 5120 23.8 and 22.7). Of few tiles a CTA an SM, each with
+    // few stages, is then faster than pairs are, too (128 x 1001 x 2063 8.1 and 10.7, 333 x 384 x 7168 13.4 and 14.9; two CTAs an SM lose: 192 x 1001 x
+    // 2063 10.6 and 10.2).
+    const int64_t work = (small.ks == 1 ? small.stages : ((K + KS - 1) / KS + small.ks - 1) / small.ks) * small.bn;
+    const bool wide_x = a.M <= 64 ? work <= 300 : small.tiles * small.ks <= device_sm_count() && work <= 512;
+    const bool own_x = wide_x && on_16(x), own = on_16(w);
+    const void* xs = own_x ? static_cast<const void*>(x.codes) : scratch;
+    const int64_t ldx = own_x ? x.ld : per * 16;
+    if (!own_x) {
+        e = wide_x ? copy_rows<false>(x.codes, x.ld, x.rows, K, scratch, stream) : copy_rows<true>(x.codes, x.ld, x.rows, K, scratch, stream);
+        if (e != cudaSuccess) return e;
+    }
     const int8_t* codes = w.codes;
     int64_t ldw = w.ld;
-    const bool own = on_16(w);
     if (!own) {
         int8_t* copy = static_cast<int8_t*>(scratch) + x.rows * per * 32;
         e = copy_rows<false>(w.codes, w.ld, w.rows, K, copy, stream);
         if (e != cudaSuccess) return e;
         codes = copy, ldw = per * 16;
     }
-    MmaArgs a{};
-    a.x_scales = x.scales, a.w_scales = w.scales, a.Y = Y, a.err = err;
-    a.M = static_cast<int>(x.rows), a.N = static_cast<int>(w.rows), a.K = static_cast<int>(K), a.early = own;
-    Cut few{}, many{};
-    if (a.M <= 64) {
-        e = cut_by<64, 1, 1>(a.M, a.N, a.K, &few);
-        return e == cudaSuccess ? run_cut<64, 1, 1>(few, bf16, scratch, codes, ldw, a, stream) : e;
-    }
-    // tiles of at most 128 rows, widened by eight warps, or of at most 192 by four (more would not leave registers for 192 rows' sums): by the
-    // stages that come one after the other and what one takes, 0.22 us and 0.00122 for each row (fitted on 17408 x 5120, 5120 x 17408
-    // and 4096 x 4096, 65 to 2048 rows)
-    e = cut_by<128, 2, 2>(a.M, a.N, a.K, &few);
-    if (e == cudaSuccess) e = cut_by<192, 2, 1>(a.M, a.N, a.K, &many);
-    if (e != cudaSuccess) return e;
-    auto time = [](const Cut& c) { return static_cast<double>(c.stages) * (0.22 + 0.00122 * c.bn); };
-    return time(few) <= time(many) ? run_cut<128, 2, 2>(few, bf16, scratch, codes, ldw, a, stream)
-                                   : run_cut<192, 2, 1>(many, bf16, scratch, codes, ldw, a, stream);
+    a.early = own && !own_x;
+    if (wide_x) return run_cut<64, 1, 1, true>(small, bf16, xs, ldx, codes, ldw, a, stream);
+    if (a.M <= 64) return run_cut<64, 1, 1, false>(small, bf16, xs, ldx, codes, ldw, a, stream);
+    return time(few) <= time(many) ? run_cut<128, 2, 2, false>(few, bf16, xs, ldx, codes, ldw, a, stream)
+                                   : run_cut<192, 2, 1, false>(many, bf16, xs, ldx, codes, ldw, a, stream);
 }
 
 }  // namespace pnq

@@ -59,6 +59,14 @@ def test_strides_and_alignment(M, K, x_pitch, w_pitch, x_at, w_at):
     check(M, 270, K, x_pitch=x_pitch, w_pitch=w_pitch, x_at=x_at, w_at=w_at)
 
 
+@pytest.mark.parametrize("M,N,K", [(65, 1001, 2063), (128, 640, 1024), (333, 384, 7168), (512, 100, 256), (64, 4096, 4096), (20, 151936, 128), (40, 151936, 640),
+                                   (300, 130, 512)])
+@pytest.mark.parametrize("x_at,x_extra", [(0, 0), (5, 0), (0, 16)])
+def test_small_products(M, N, K, x_at, x_extra):
+    """Few tiles or few stages each: kernels that widen x themselves, from its own rows or from a copy of them on 16 bytes."""
+    check(M, N, K, x_at=x_at, x_pitch=-(-K // 16) * 16 + x_extra, dtypes=(torch.float32, torch.bfloat16))
+
+
 @pytest.mark.parametrize("M", [1, 5, 20, 70, 300])
 @pytest.mark.parametrize("K", [1024, 1040, 4096, 131071])
 def test_largest_sums(M, K):
