@@ -351,16 +351,19 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_kernel(const NormArgs a) {
 // The same for many rows on 16 bytes: `teams` rows at a time in a CTA, each by `warps` warps, N accesses of eight elements a lane. What a row costs
 // besides its elements (sums through the warps, two divisions, addresses) is some 150 instructions a thread, more than eight elements do: 8192 x 5120
 // bf16 with eight a thread executed 35 instructions an element and took 64 us (74 to codes); this takes 55 (55), 6.1 (5.3) TB/s. The weight waits
-// in shared memory.
-template <class T, int N, int THREADS, int CTAS>
+// in shared memory. Encoding rows as they are (not NORM) leaves registers: bf16 rows are loaded one ahead (65536 x 256 21.0 us, 26.9 without; fp32 rows of 5120
+// spill, 99 and 81).
+template <class T, bool NORM, int N, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) norm_teams_kernel(const NormArgs a, int warps, int teams) {
     using X = Io<T, 8>;
+    constexpr bool kAhead = !NORM && sizeof(T) == 2;
+    const bool norm = NORM && (sizeof(T) == 2 || a.norm);  // always NORM: taken as known, it makes fp32 rows spill (17408 x 5120 with residual 236 us, 225)
     extern __shared__ __align__(16) float weight[];  // [D] fp32
     __shared__ float2 part[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp / warps, first = mine * warps, team = 32 * warps;
     const int tid = static_cast<int>(threadIdx.x) - 32 * first, D = a.D;
     griddep_begin();
-    if (a.norm) {
+    if (norm) {
         for (int at = static_cast<int>(threadIdx.x) * 8; at < D; at += static_cast<int>(blockDim.x) * 8) {
             float w[8];
             load_weight<8>(a.weight, a.weight_bf16, at, w);
@@ -369,13 +372,26 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_teams_kernel(const NormArg
         __syncthreads();
     }
     const bool added = a.residual != nullptr;
-    int turn = 0;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * teams + mine; row < a.rows; row += static_cast<int64_t>(gridDim.x) * teams, turn ^= 1) {
-        typename X::Raw x[N] = {};
+    const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * teams + mine;
+    auto fetch = [&](int64_t row, typename X::Raw(&x)[N]) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i) {
+            x[i] = {};
             if ((tid + i * team) * 8 < D) x[i] = X::raw(static_cast<const T*>(a.x) + row * a.ldx + (tid + i * team) * 8);
-        if (added) {
+        }
+    };
+    typename X::Raw ahead[N];
+    if (kAhead && row < a.rows) fetch(row, ahead);
+    for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+        typename X::Raw x[N];
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = ahead[i];
+        } else {
+            fetch(row, x);
+        }
+        if (NORM && added) {
             typename X::Raw r[N] = {};
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -389,7 +405,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_teams_kernel(const NormArg
             const int at = (tid + i * team) * 8;
             X::value(x[i], p[i]);
             if (at >= D) continue;
-            if (a.norm) {
+            if (norm) {
                 if (a.total) X::store(static_cast<T*>(a.total) + row * D + at, x[i]);
                 float w[8];
                 const float4 u = *reinterpret_cast<const float4*>(weight + at), v = *reinterpret_cast<const float4*>(weight + at + 4);
@@ -402,6 +418,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_teams_kernel(const NormArg
             }
             if (a.codes) most = largest(most, p[i]);
         }
+        if (kAhead && row + step < a.rows) fetch(row + step, ahead);
         uint32_t top = __float_as_uint(most) & 0x7fffffffu;
         sum = warp_total(sum);
         top = __reduce_max_sync(0xffffffffu, top);
@@ -760,7 +777,7 @@ int threads_for(int64_t D, int per) {
 template <class T, int N, int THREADS, int CTAS>
 cudaError_t run_teams(const NormArgs& a, cudaStream_t stream) {
     const int warps = static_cast<int>((a.D + 256 * N - 1) / (256 * N)), teams = std::max(1, THREADS / 32 / warps), smem = a.norm ? 4 * a.D : 0;
-    auto kernel = norm_teams_kernel<T, N, THREADS, CTAS>;
+    auto kernel = a.norm ? norm_teams_kernel<T, true, N, THREADS, CTAS> : norm_teams_kernel<T, false, N, THREADS, CTAS>;
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc{};
