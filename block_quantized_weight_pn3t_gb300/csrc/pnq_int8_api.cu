@@ -114,6 +114,7 @@ extern "C" int pnq_rms_norm_backward(int type, const void* dY, int64_t ldy, cons
     const int rc = pnq_rms_norm_backward_scratch_bytes(rows, D, &need);
     if (rc != PNQ_OK) return rc;
     if (dweight && scratch_bytes < need) return PNQ_ERR_SCRATCH;
+    if (rows > 0 && (dX == dY || dX == total)) return PNQ_ERR_VALUE;  // the weight's gradient may be summed from rows whose dX is written
     return launched([&] {
         return launch_rms_norm_backward(type == PNQ_BF16, RowsView{dY, ldy}, RowsView{total, ldt}, weight_type == PNQ_BF16, weight, rstd,
                                         RowsView{dtotal, ldd}, rows, D, dX, dweight, static_cast<float*>(scratch), stream);

@@ -1221,7 +1221,7 @@ PyMethodDef methods[] = {
                               "row, for int8_gemm. y: a [rows][D] tensor that takes the norm itself too (for a router, say)."),
     PNQ_METHOD(rms_norm_backward, "rms_norm_backward(dy, total, weight, rstd, dtotal=None, out=None, dweight=None, stream=None)\n--\n\n"
                                   "Gradients of rms_norm: (dx, dweight); dx is the residual's gradient too. dtotal: the gradient that\n"
-                                  "reaches the total from elsewhere, added to dx. dweight is fp32."),
+                                  "reaches the total from elsewhere, added to dx (out=dtotal adds in place; dy and total stay). dweight is fp32."),
     PNQ_METHOD(int8_quantize, "int8_quantize(x, codes=None, scales=None, stream=None)\n--\n\n"
                               "(codes, scales) of rows (fp32 or bf16 [rows][K], rows may be strided): scale = max |x| / 127, code = the whole\n"
                               "number nearest to 127 x / max |x|. Activations, and weights once (a scale per output channel)."),

@@ -506,7 +506,7 @@ int pnq_rms_norm(int type, const void* X, int64_t ldx, const void* residual, int
  *                                           reaches the total itself, may be NULL),
  *   dweight[c] = sum over rows of dY n     (device fp32 [D]; NULL: not computed).
  * scratch (with dweight): device fp32, 4-byte aligned, pnq_rms_norm_backward_scratch_bytes long; the order of the sums goes by the
- * sizes and the device alone. Types as in the forward call. dX is a buffer of its own.
+ * sizes and the device alone. Types as in the forward call. dX may be dtotal's own buffer where ldd = D, not dY's or the total's (PNQ_ERR_VALUE).
  */
 int pnq_rms_norm_backward(int type, const void* dY, int64_t ldy, const void* total, int64_t ldt, int weight_type, const void* weight,
                           const float* rstd, const void* dtotal, int64_t ldd, int64_t rows, int64_t D, void* dX, float* dweight,

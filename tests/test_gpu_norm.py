@@ -181,7 +181,7 @@ def test_in_place_and_given_buffers(rows, D):
     assert yy is xx and tt is held and torch.equal(xx, y) and torch.equal(held, total) and torch.equal(rr, rstd)
 
 
-@pytest.mark.parametrize("rows,D", SHAPES + [(0, 40), (700, 512), (5000, 136)])
+@pytest.mark.parametrize("rows,D", SHAPES + [(0, 40), (700, 512), (5000, 136), (64, 4096), (200, 999), (24, 130), (120, 8191)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_backward(rows, D, dtype):
     """Against the formula in 64 bits; the bound of dx counts the terms that cancel, that of dweight every term of its sum."""
@@ -226,6 +226,19 @@ def test_backward_against_differences():
         step = torch.zeros_like(ww)
         step[j] = h
         assert float(dw[j]) == pytest.approx(float((loss(t, ww + step) - loss(t, ww - step)) / (2 * h)), rel=1e-5, abs=1e-6)
+
+
+def test_backward_in_place():
+    """dx may take dtotal's buffer, not dy's or the total's: those may be read for the weight's gradient after it is written."""
+    for rows, D in ((40, 512), (3000, 512)):
+        dy, t, dt = (torch.randn(rows, D, device="cuda") for _ in range(3))
+        w, rstd = torch.randn(D, device="cuda"), torch.rand(rows, device="cuda")
+        want = pnq.rms_norm_backward(dy, t, w, rstd, dt)
+        got = pnq.rms_norm_backward(dy, t, w, rstd, dt, out=dt)
+        assert got[0] is dt and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        for out in (dy, t):
+            with pytest.raises(RuntimeError):
+                pnq.rms_norm_backward(dy, t, w, rstd, out=out)
 
 
 def test_capture_and_another_stream():
