@@ -22,6 +22,8 @@ namespace {
 
 constexpr int kWarps = 4;          // of a CTA
 constexpr int kCtas = 16;          // of an SM at most
+constexpr int kScan = 32;          // tokens that a CTA of the second kernel looks through, one a lane of its first warp
+constexpr int32_t kAgain = INT32_MIN;  // the first id of a token that the second kernel is to do
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kNone = -INFINITY;  // the score of an expert that is out
 
@@ -162,53 +164,103 @@ __device__ __forceinline__ Two key_value(uint64_t key) {
     return {value(static_cast<uint32_t>(key >> 32)), value(static_cast<uint32_t>(key))};
 }
 
-// The row again with such scores. c: E keys of shared memory of this warp (0: an expert that is out); x: the row's logits there. Equal scores
-// go by the logits, then by the index. Returns slots lane and lane + 32 of the token's experts.
-__device__ __noinline__ int2 route_exact(const RouteArgs& a, const float* x, const float* bias, uint64_t* c, int lane) {
-    int2 id = make_int2(-1, -1);
-    Two scale{1.0f, 0.0f};
+// The weights of token t's experts, slots lane and lane + 32 of them in id, from its logits x in shared memory; m, sum: softmax's largest logit and
+// divisor. Renormalised by the chosen experts alone, by their largest logit (so that no sum of theirs is too small to divide by).
+__device__ __forceinline__ void write_weights(const RouteArgs& a, int64_t t, int (&id)[2], const float* x, float m, float sum, bool bad, int lane) {
+    const int halves = a.k > 32 ? 2 : 1;
+    float w[2] = {0.0f, 0.0f}, z[2], mc = kNone, total = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h >= halves) break;
+        if (32 * h + lane >= a.k) id[h] = -1;
+        z[h] = id[h] >= 0 ? x[id[h]] : kNone;
+        mc = fmaxf(mc, z[h]);
+    }
+    if (a.renormalize) mc = redux_max(mc);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h >= halves) break;
+        if (id[h] >= 0) {
+            if (a.sigmoid) w[h] = a.renormalize && mc < -60.0f ? expf(z[h] - mc) : sigmoid(z[h]);
+            else w[h] = a.renormalize ? expf(z[h] - mc) : expf(z[h] - m) / sum;
+        }
+        total += w[h];
+    }
+    if (a.renormalize) total = warp_sum(total);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (32 * h + lane >= a.k) continue;
+        const int64_t at = t * a.k + 32 * h + lane;
+        float v = a.scale * w[h];
+        if (a.renormalize && id[h] >= 0) v /= total;
+        a.ids[at] = id[h];
+        a.weights[at] = bad ? __uint_as_float(0x7fc00000u) : v;
+    }
+}
+
+// Token t with such scores, by a whole CTA. c: E keys of shared memory (0: an expert that is out); x: the row's logits there. Equal
+// scores go by the logits, then by the index.
+__device__ __noinline__ void route_exact(const RouteArgs& a, int64_t t, const float* x, const float* bias, uint64_t* c) {
+    __shared__ Two part[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Two scale{1.0f, 0.0f}, sum{1.0f, 0.0f};
     float top = kNone;
     if (!a.sigmoid) {
         for (int e = lane; e < a.E; e += 32) top = fmaxf(top, x[e]);
         top = redux_max(top);
-        Two sum{0.0f, 0.0f};
-#pragma unroll 4
-        for (int e = lane; e < a.E; e += 32) sum = sum + exp_two(two_sum(fmaxf(x[e], -3e38f), -top));
+        Two mine{0.0f, 0.0f};
+        for (int e = tid; e < a.E; e += 32 * kWarps) {
+            const Two z = exp_two(two_sum(fmaxf(x[e], -3e38f), -top));
+            c[e] = static_cast<uint64_t>(__float_as_uint(z.hi)) << 32 | __float_as_uint(z.lo);
+            mine = mine + z;
+        }
 #pragma unroll
-        for (int d = 16; d; d >>= 1) sum = sum + Two{__shfl_xor_sync(kAll, sum.hi, d), __shfl_xor_sync(kAll, sum.lo, d)};
+        for (int d = 16; d; d >>= 1) mine = mine + Two{__shfl_xor_sync(kAll, mine.hi, d), __shfl_xor_sync(kAll, mine.lo, d)};
+        if (lane == 0) part[warp] = mine;
+        __syncthreads();
+        sum = (part[0] + part[1]) + (part[2] + part[3]);
         scale = inverse(sum);
     }
-#pragma unroll 4
-    for (int e = lane; e < a.E; e += 32) {  // several at a time, without branches: a score is some 200 instructions, one after the other
-        const float v = fmaxf(x[e], -3e38f), b = a.bias ? bias[e] : 0.0f;
+#pragma unroll 2
+    for (int e = tid; e < a.E; e += 32 * kWarps) {  // two at a time, without branches: a score is some 200 instructions, one after the other
+        const float b = a.bias ? bias[e] : 0.0f;
         Two s;
         if (a.sigmoid) {
+            const float v = fmaxf(x[e], -3e38f);
             const Two z = exp_two({-fabsf(v), 0.0f}), w = inverse(z + Two{1.0f, 0.0f}), u = w * z;
             s = {v >= 0.0f ? w.hi : u.hi, v >= 0.0f ? w.lo : u.lo};
         } else {
-            s = exp_two(two_sum(v, -top)) * scale;
+            s = Two{__uint_as_float(static_cast<uint32_t>(c[e] >> 32)), __uint_as_float(static_cast<uint32_t>(c[e]))} * scale;
         }
         c[e] = x[e] == kNone || b == kNone ? 0 : order_key(s + Two{b, 0.0f});
     }
-    __syncwarp();
+    __syncthreads();
+    if (warp > 0) return;
     if (a.groups > 1) {
+        // the largest power of two of lanes that a group can have: its best two by them
+        const int lanes = 1 << (31 - __clz(32 / a.groups)), g = lane / lanes;
         uint64_t b1 = 0, b2 = 0;
-        if (lane < a.groups) {
-            for (int j = 0; j < a.per; ++j) {
-                const uint64_t v = c[lane * a.per + j];
-                if (v > b1) b2 = b1, b1 = v;
-                else if (v > b2) b2 = v;
-            }
+        auto take = [&](uint64_t v) {
+            if (v > b1) b2 = b1, b1 = v;
+            else if (v > b2) b2 = v;
+        };
+        if (g < a.groups) {
+            for (int j = lane & (lanes - 1); j < a.per; j += lanes) take(c[g * a.per + j]);
+        }
+        for (int d = lanes >> 1; d; d >>= 1) {
+            const uint64_t o1 = __shfl_xor_sync(kAll, b1, d), o2 = __shfl_xor_sync(kAll, b2, d);
+            take(o1);
+            take(o2);
         }
         const uint64_t score = a.best == 2 && b2 ? order_key(key_value(b1) + key_value(b2)) : b1;
         int rank = 0;
         for (int h = 0; h < a.groups; ++h) {
-            const uint64_t other = __shfl_sync(kAll, score, h);
-            rank += other > score || (other == score && h < lane);
+            const uint64_t other = __shfl_sync(kAll, score, h * lanes);
+            rank += other > score || (other == score && h < g);
         }
-        const uint32_t kept = __ballot_sync(kAll, lane < a.groups && rank < a.top_groups);
+        const uint32_t kept = __ballot_sync(kAll, g < a.groups && rank < a.top_groups);
         for (int e = lane; e < a.E; e += 32)
-            if (!(kept >> (e / a.per) & 1)) c[e] = 0;
+            if (!(kept >> (e / a.per * lanes) & 1)) c[e] = 0;
         __syncwarp();
     }
     // each lane's best of its own (lane, lane + 32, ..); the winner's next is found by all lanes together, one of its experts each
@@ -221,7 +273,11 @@ __device__ __noinline__ int2 route_exact(const RouteArgs& a, const float* x, con
         return {static_cast<uint32_t>(key >> 32), static_cast<uint32_t>(key), key ? order_key(x[e]) : 0, key ? e : 1 << 30};
     };
     auto largest = [&](Best b) -> Best {  // of the warp; at = 1 << 30 where none is left
-        const uint32_t hi = __reduce_max_sync(kAll, b.hi);
+        const uint32_t hi = __reduce_max_sync(kAll, b.hi), first = __ballot_sync(kAll, b.hi == hi);
+        if ((first & (first - 1)) == 0) {
+            const int from = __ffs(first) - 1;
+            return {hi, __shfl_sync(kAll, b.lo, from), __shfl_sync(kAll, b.tie, from), __shfl_sync(kAll, b.at, from)};
+        }
         bool in = b.hi == hi;
         const uint32_t lo = __reduce_max_sync(kAll, in ? b.lo : 0);
         in = in && b.lo == lo;
@@ -234,28 +290,44 @@ __device__ __noinline__ int2 route_exact(const RouteArgs& a, const float* x, con
         const Best b = of(e);
         if (b.hi > mine.hi || (b.hi == mine.hi && (b.lo > mine.lo || (b.lo == mine.lo && b.tie > mine.tie)))) mine = b;
     }
+    int id[2] = {-1, -1};
     for (int j = 0; j < a.k; ++j) {
         const Best won = largest(mine);
         if (won.at >= a.E) break;  // no expert is left
-        if (lane == (j & 31)) (j < 32 ? id.x : id.y) = won.at;
+        if (lane == j) id[0] = won.at;
+        if (lane + 32 == j) id[1] = won.at;
         const int w = won.at & 31;
         if (lane == w) c[won.at] = 0;
         __syncwarp();
         const Best next = largest(of(w + 32 * lane));
         if (lane == w) mine = next;
     }
-    return id;
+    write_weights(a, t, id, x, top, sum.hi, false, lane);
+}
+
+// The same with the row's logits loaded; x: shared memory of route_floats(E).
+template <class T>
+__device__ __forceinline__ void route_again(const RouteArgs& a, int64_t t, const float* bias, float* x) {
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    for (int e = threadIdx.x; e < a.E; e += 32 * kWarps) x[e] = load_one(row + e);
+    __syncthreads();
+    route_exact(a, t, x, bias, reinterpret_cast<uint64_t*>(x + (a.E + 3) / 4 * 4));
+    __syncthreads();
 }
 
 // Shared memory of a warp: the row's logits, and behind them the groups' scores (each group on an odd pitch) or the keys above.
 __host__ __device__ inline int route_floats(int E) { return (E + 3) / 4 * 4 * 3 + 32; }
 
-// A warp takes token after token. The bias is read once a CTA: by every warp for every token, out
-// of the same few lines of L2, it took more time than all the rest (16384 tokens of 256 experts: 25 of 45 us).
+// A warp takes token after token. Tokens with near scores (a few in 16384) are done again by a whole CTA: HERE, where a warp has one token at
+// most, at this kernel's end, otherwise by the kernel below. In the loop, by the warp that met them, the code for it alone cost every call 2 to 4
+// us: 16384 x 256 sigmoid by the logits 18.1 us, now 15.6, 4096 x 256 with bias and 8 groups 16.2 and 13.6; 16384 of those 36.9 and 35.0, of which
+// the second kernel is 9 (with 64 experts it takes 1.7 more than it saves). The bias is read once a CTA: by every warp for every token, out of the
+// same few lines of L2, it took more time than all the rest (25 of 45 us then).
 // (Registers for eight CTAs an SM up to 256 experts: a token is a chain of some 3 us. With four CTAs fewer it took 4 to 12 percent longer.)
-template <class T, int NE, int V>
+template <class T, int NE, int V, bool HERE>
 __global__ void __launch_bounds__(32 * kWarps, NE <= 8 ? 8 : 4) route_kernel(const RouteArgs a) {
     extern __shared__ __align__(16) float shared[];
+    __shared__ int64_t again[kWarps];  // HERE: a warp's token if it is to be done again, else -1
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float* bs = shared;  // [E] bias, in whole 16 bytes
     float* xs = shared + (a.E + 3) / 4 * 4 + warp * route_floats(a.E);
@@ -287,6 +359,7 @@ __global__ void __launch_bounds__(32 * kWarps, NE <= 8 ? 8 : 4) route_kernel(con
             else to[e] = v[i];
         }
     };
+    if (HERE && lane == 0) again[warp] = -1;
     for (; t < a.tokens; t += step) {
         float x[NE];
         load_row<T, NE, V>(logits + t * a.ld, a.E, lane, x);
@@ -419,45 +492,47 @@ __global__ void __launch_bounds__(32 * kWarps, NE <= 8 ? 8 : 4) route_kernel(con
                     for (int e = lane; e < a.E; e += 32)
                         if (cs[e] != kNone && final_won - cs[e] <= tol) near |= !same(e, final_id);
                 }
-                __syncwarp();
                 if (__any_sync(kAll, near)) {
-                    const int2 again = route_exact(a, xs, bs, reinterpret_cast<uint64_t*>(cs), lane);
-                    id[0] = again.x, id[1] = again.y;
+                    if (lane == 0) {
+                        if constexpr (HERE) again[warp] = t;
+                        else a.ids[t * a.k] = kAgain;
+                    }
+                    continue;
                 }
             }
         }
 
-        // weights: of chosen experts alone where renormalised, by their largest logit (so that no sum of theirs is too small to divide by)
         __syncwarp();
-        const int halves = a.k > 32 ? 2 : 1;
-        float w[2] = {0.0f, 0.0f}, z[2], mc = kNone, total = 0.0f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (h >= halves) break;
-            if (32 * h + lane >= a.k) id[h] = -1;
-            z[h] = id[h] >= 0 ? xs[id[h]] : kNone;
-            mc = fmaxf(mc, z[h]);
+        write_weights(a, t, id, xs, m, sum, bad, lane);
+    }
+    if constexpr (HERE) {
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w)
+            if (again[w] >= 0) route_again<T>(a, again[w], bs, shared + (a.E + 3) / 4 * 4);
+    }
+}
+
+// The tokens that the kernel above left: a CTA looks through kScan of them at a time.
+template <class T>
+__global__ void __launch_bounds__(32 * kWarps) route_again_kernel(const RouteArgs a) {
+    extern __shared__ __align__(16) float shared[];
+    __shared__ uint32_t marked;
+    bool bias = false;
+    griddep_begin();
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kScan; t0 < a.tokens; t0 += static_cast<int64_t>(gridDim.x) * kScan) {
+        if (threadIdx.x < 32) {
+            const int64_t t = t0 + threadIdx.x;
+            const uint32_t mask = __ballot_sync(kAll, t < a.tokens && ld_l2(a.ids + t * a.k) == kAgain);
+            if (threadIdx.x == 0) marked = mask;
         }
-        if (a.renormalize) mc = redux_max(mc);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (h >= halves) break;
-            if (id[h] >= 0) {
-                if (a.sigmoid) w[h] = a.renormalize && mc < -60.0f ? expf(z[h] - mc) : sigmoid(z[h]);
-                else w[h] = a.renormalize ? expf(z[h] - mc) : expf(z[h] - m) / sum;
-            }
-            total += w[h];
+        __syncthreads();
+        uint32_t mask = marked;
+        if (mask && a.bias && !bias) {
+            for (int e = threadIdx.x; e < a.E; e += 32 * kWarps) shared[e] = ld_l2(a.bias + e);
+            bias = true;
         }
-        if (a.renormalize) total = warp_sum(total);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (32 * h + lane >= a.k) continue;
-            const int64_t at = t * a.k + 32 * h + lane;
-            float v = a.scale * w[h];
-            if (a.renormalize && id[h] >= 0) v /= total;
-            a.ids[at] = id[h];
-            a.weights[at] = bad ? __uint_as_float(0x7fc00000u) : v;
-        }
+        for (; mask; mask &= mask - 1) route_again<T>(a, t0 + __ffs(mask) - 1, shared, shared + (a.E + 3) / 4 * 4);
+        __syncthreads();  // marked has been read
     }
 }
 
@@ -576,13 +651,13 @@ __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const Route
     }
 }
 
-// Shared memory: `whole` floats of a CTA and `floats` of each of its warps. As many CTAs as keep the SMs full (and no more than there are tokens for).
+// `floats` of shared memory, `tokens` to a CTA at a time. As many CTAs as keep the SMs full (and no more than there are tokens for).
 template <class Kernel, class Args>
-cudaError_t launch_rows(Kernel kernel, const Args& a, int whole, int floats, cudaStream_t stream) {
+cudaError_t launch_rows(Kernel kernel, const Args& a, int floats, int tokens, cudaStream_t stream) {
     cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((a.tokens + kWarps - 1) / kWarps, static_cast<int64_t>(device_sm_count()) * kCtas)));
+    lc.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((a.tokens + tokens - 1) / tokens, static_cast<int64_t>(device_sm_count()) * kCtas)));
     lc.blockDim = dim3(32 * kWarps);
-    lc.dynamicSmemBytes = (static_cast<size_t>(whole) + static_cast<size_t>(kWarps) * floats) * 4;
+    lc.dynamicSmemBytes = static_cast<size_t>(floats) * 4;
     lc.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -623,11 +698,17 @@ cudaError_t launch_expert_route(bool bf16, const RowsView& logits, int64_t token
     a.top_groups = rule.top_groups, a.best = rule.best;
     a.per_magic = static_cast<uint32_t>(((1 << 20) + a.per - 1) / a.per);
     a.scale = rule.scale, a.sigmoid = rule.sigmoid, a.renormalize = rule.renormalize;
-    return by_experts(a.E, aligned4(logits.p, logits.ld, a.E, bf16), [&](auto n, auto v) {
+    // by the logits alone no token is done again; few tokens, one a warp, end in one launch
+    const bool by_logit = !bias && rule.groups == 1, here = !by_logit && tokens <= std::min(4096, kWarps * kCtas * device_sm_count());
+    const int whole = (a.E + 3) / 4 * 4;
+    const cudaError_t e = by_experts(a.E, aligned4(logits.p, logits.ld, a.E, bf16), [&](auto n, auto v) {
         constexpr int NE = decltype(n)::value, V = decltype(v)::value;
-        return bf16 ? launch_rows(route_kernel<__nv_bfloat16, NE, V>, a, (a.E + 3) / 4 * 4, route_floats(a.E), stream)
-                    : launch_rows(route_kernel<float, NE, V>, a, (a.E + 3) / 4 * 4, route_floats(a.E), stream);
+        const int floats = whole + kWarps * route_floats(a.E);
+        if (here) return launch_rows(bf16 ? route_kernel<__nv_bfloat16, NE, V, true> : route_kernel<float, NE, V, true>, a, floats, kWarps, stream);
+        return launch_rows(bf16 ? route_kernel<__nv_bfloat16, NE, V, false> : route_kernel<float, NE, V, false>, a, floats, kWarps, stream);
     });
+    if (e != cudaSuccess || here || by_logit) return e;
+    return launch_rows(bf16 ? route_again_kernel<__nv_bfloat16> : route_again_kernel<float>, a, whole + route_floats(a.E), kScan, stream);
 }
 
 cudaError_t launch_expert_route_backward(bool bf16, const float* dweights, const RowsView& logits, const int32_t* ids, int64_t tokens,
@@ -639,8 +720,7 @@ cudaError_t launch_expert_route_backward(bool bf16, const float* dweights, const
     const bool wide = aligned4(logits.p, logits.ld, a.E, bf16) && aligned4(dlogits, a.E, a.E, bf16);
     return by_experts(a.E, wide, [&](auto n, auto v) {
         constexpr int NE = decltype(n)::value, V = decltype(v)::value;
-        return bf16 ? launch_rows(route_backward_kernel<__nv_bfloat16, NE, V>, a, 0, a.E, stream)
-                    : launch_rows(route_backward_kernel<float, NE, V>, a, 0, a.E, stream);
+        return launch_rows(bf16 ? route_backward_kernel<__nv_bfloat16, NE, V> : route_backward_kernel<float, NE, V>, a, kWarps * a.E, kWarps, stream);
     });
 }
 

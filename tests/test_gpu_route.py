@@ -104,6 +104,20 @@ def test_scores_nearer_than_fp32_tells(score, groups):
         check(rows, 20, score=score, bias=bias, groups=groups, top_groups=min(2, groups), best=2)
 
 
+@pytest.mark.parametrize("T", [3, 130, 4096, 4097, 10001])
+@pytest.mark.parametrize("score", [pnq.SOFTMAX, pnq.SIGMOID])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_many_tokens_of_near_scores(T, score, groups):
+    """The same among many tokens: one in three, and all of a CTA's at the end, need more than fp32."""
+    x, _ = make(1, 64, torch.float32, 11)
+    bias = (0.7 - scores(x, score)[0]).float()
+    rows, _ = make(T, 64, torch.float32, 12)
+    rows[::3] = x
+    rows[-40:] = x
+    for dtype in (torch.float32, torch.bfloat16):
+        check(rows.to(dtype), 7, score=score, bias=bias, groups=groups, top_groups=min(2, groups), best=2, renormalize=True)
+
+
 def test_ties_go_to_the_lowest():
     for dtype in (torch.float32, torch.bfloat16):
         x = torch.zeros(5, 100, dtype=dtype, device="cuda")
