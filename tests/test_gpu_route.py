@@ -275,3 +275,28 @@ def test_routing_into_the_layer():
     torch.cuda.synchronize()
     for a, b in zip(out, step()):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [100, 6000])
+def test_captured_with_near_scores(T):
+    """Captured, and replayed on other logits, at once with a second call on another stream: the same as called."""
+    x, _ = make(1, 64, torch.float32, 11)
+    bias = (0.7 - scores(x, pnq.SIGMOID)[0]).float()
+    rows = make(T, 64, torch.float32, 5)[0].clone()
+    other = make(T, 64, torch.float32, 6)[0].clone()
+    other[::7] = x
+    rule = dict(score=pnq.SIGMOID, bias=bias, groups=4, top_groups=2, best=2, renormalize=True)
+    pnq.expert_route(rows, 6, **rule)
+    torch.cuda.synchronize()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        out = pnq.expert_route(rows, 6, **rule)
+    rows.copy_(other)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        graph.replay()
+        second = pnq.expert_route(other, 6, stream=stream, **rule)
+        torch.cuda.synchronize()
+        want_ids, _ = reference(other, 6, **rule)
+        for ids, w in (out, second):
+            assert torch.equal(ids, want_ids) and torch.equal(w, second[1])
