@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 using namespace pnq;
 
@@ -30,6 +31,18 @@ int launched(F&& launch) {
 // rows x D elements, rows `ld` apart: offsets stay within 64 bits.
 bool fits(int64_t rows, int64_t D, int64_t ld) {
     return rows >= 0 && rows <= kMaxRows && D >= 1 && D <= kMaxRows && ld >= D && ld <= INT64_MAX / 8 / (rows + 1);
+}
+
+// Whether a contiguous [rows][D] result may stand where rows of an operand do: in their own place, row for row, or apart from them.
+bool apart(const void* out, const RowsView& in, int64_t rows, int64_t D, uintptr_t bytes) {
+    if (!out || !in.p) return true;
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in.p);
+    const uintptr_t length = static_cast<uintptr_t>(D) * bytes, step = static_cast<uintptr_t>(in.ld) * bytes, n = static_cast<uintptr_t>(rows);
+    const uintptr_t r = i + length > o ? 0 : (o - i - length) / step + 1;  // the operand's first row that ends behind the result's start
+    return r >= n || i + r * step >= o + n * length;
+}
+bool in_place_or_apart(const void* out, const RowsView& in, int64_t rows, int64_t D, uintptr_t bytes) {
+    return (out == in.p && (in.ld == D || rows == 1)) || apart(out, in, rows, D, bytes);
 }
 
 int check_rule(const pnq_route_rule* r, int64_t tokens, RouteRule* out) {
@@ -69,6 +82,7 @@ extern "C" int pnq_expert_route_backward(int type, const float* dweights, const 
     if (tokens == 0) return PNQ_OK;
     if (!dweights || !logits || !ids || !dlogits) return PNQ_ERR_NULL;
     if (!aligned(logits, size_of(type)) || !aligned(dlogits, size_of(type)) || !aligned(ids, 4) || !aligned(dweights, 4)) return PNQ_ERR_ALIGN;
+    if (!in_place_or_apart(dlogits, RowsView{logits, ld}, tokens, r.experts, size_of(type))) return PNQ_ERR_VALUE;
     return launched(
         [&] { return launch_expert_route_backward(type == PNQ_BF16, dweights, RowsView{logits, ld}, ids, tokens, r, dlogits, stream); });
 }
@@ -86,6 +100,9 @@ extern "C" int pnq_rms_norm(int type, const void* X, int64_t ldx, const void* re
     if (!aligned(X, b) || !aligned(residual, b) || !aligned(total, b) || !aligned(y, b) || !aligned(weight, size_of(weight_type)) ||
         !aligned(rstd, 4) || !aligned(scales, 4) || !aligned(codes, 16))
         return PNQ_ERR_ALIGN;
+    for (const void* out : {total, y})
+        if (!in_place_or_apart(out, RowsView{X, ldx}, rows, D, b) || !in_place_or_apart(out, RowsView{residual, ldr}, rows, D, b)) return PNQ_ERR_VALUE;
+    if (!apart(total, RowsView{y, D}, rows, D, b)) return PNQ_ERR_VALUE;
     return launched([&] {
         return launch_rms_norm(type == PNQ_BF16, RowsView{X, ldx}, RowsView{residual, ldr}, weight_type == PNQ_BF16, weight, eps, rows, D,
                                total, y, rstd, codes, pitch, scales, stream);
@@ -114,7 +131,10 @@ extern "C" int pnq_rms_norm_backward(int type, const void* dY, int64_t ldy, cons
     const int rc = pnq_rms_norm_backward_scratch_bytes(rows, D, &need);
     if (rc != PNQ_OK) return rc;
     if (dweight && scratch_bytes < need) return PNQ_ERR_SCRATCH;
-    if (rows > 0 && (dX == dY || dX == total)) return PNQ_ERR_VALUE;  // the weight's gradient may be summed from rows whose dX is written
+    // the weight's gradient may be summed from rows whose dX is written
+    if (rows > 0 && (!apart(dX, RowsView{dY, ldy}, rows, D, b) || !apart(dX, RowsView{total, ldt}, rows, D, b) ||
+                     !in_place_or_apart(dX, RowsView{dtotal, ldd}, rows, D, b)))
+        return PNQ_ERR_VALUE;
     return launched([&] {
         return launch_rms_norm_backward(type == PNQ_BF16, RowsView{dY, ldy}, RowsView{total, ldt}, weight_type == PNQ_BF16, weight, rstd,
                                         RowsView{dtotal, ldd}, rows, D, dX, dweight, static_cast<float*>(scratch), stream);

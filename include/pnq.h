@@ -472,7 +472,8 @@ int pnq_expert_route(int type, const void* logits, int64_t ld, int64_t tokens, c
  * pnq_expert_route_backward -- dlogits ([tokens][experts] contiguous, the logits' type, overwritten) from dweights (device fp32
  * [tokens][slots]), the logits and the ids of the forward call, in fp32, rounded once. The choice itself has no gradient
  * (nor has the bias). ids outside 0 .. experts - 1 take part in nothing; an expert named twice gets both gradients, in slot
- * order. Of the rule, groups, top_groups and best are not used. dlogits may be the logits' own buffer where ld = experts.
+ * order. Of the rule, groups, top_groups and best are not used. dlogits may be the logits' own buffer where ld = experts, and is otherwise apart
+ * from them (PNQ_ERR_VALUE).
  */
 int pnq_expert_route_backward(int type, const float* dweights, const void* logits, int64_t ld, const int32_t* ids, int64_t tokens,
                               const pnq_route_rule* rule, void* dlogits, cudaStream_t stream);
@@ -485,15 +486,17 @@ int pnq_expert_route_backward(int type, const float* dweights, const void* logit
 
 /*
  * pnq_rms_norm -- with t = X + residual (rounded to the rows' type; t = X where residual is NULL), r = 1 / sqrt(mean(t^2) + eps):
- *   total   t, contiguous [rows][D], the type of X (NULL: not written; it may be the residual's own buffer where ldr = D);
- *   y       t r w, contiguous [rows][D], the type of X (NULL: not written; it may be X's own buffer where ldx = D);
+ *   total   t, contiguous [rows][D], the type of X (NULL: not written);
+ *   y       t r w, contiguous [rows][D], the type of X (NULL: not written);
+ *           each of these two may be X's or the residual's own buffer where its rows are D apart; otherwise they are apart from both, and always
+ *           from each other (PNQ_ERR_VALUE);
  *   rstd    r, device fp32 [rows] (NULL: not written), for the backward pass;
  *   codes, scales  (NULL together: not written) of p = fp32(t w): scale = max|p| r / 127, code = the whole number nearest to
  *           127 p / max|p|, ties to even. A row of zeros has the scale 0 (NaN where eps is 0, as y is); a row with a NaN or an infinity (of t, w or p) has the scale NaN and codes of
  *           zero, so that what is computed from it is NaN.
  * type: PNQ_F32 or PNQ_BF16, of X, residual, total and y (row strides in elements); weight: device [D], PNQ_F32 or PNQ_BF16 of its own.
  * Sums of squares are fp32 (|t| up to about 1e18); rows on 16 bytes with D a multiple of 8 are faster. Errors: PNQ_ERR_TYPE,
- * PNQ_ERR_SHAPE (D < 1, a stride below D, a pitch that is not a multiple of 16), PNQ_ERR_VALUE (eps negative or not finite),
+ * PNQ_ERR_SHAPE (D < 1, a stride below D, a pitch that is not a multiple of 16), PNQ_ERR_VALUE (eps negative or not finite, buffers that overlap),
  * PNQ_ERR_NULL (codes without scales, or nothing to write), PNQ_ERR_ALIGN, PNQ_ERR_CUDA.
  */
 int pnq_rms_norm(int type, const void* X, int64_t ldx, const void* residual, int64_t ldr, int64_t rows, int64_t D, int weight_type,
@@ -506,7 +509,8 @@ int pnq_rms_norm(int type, const void* X, int64_t ldx, const void* residual, int
  *                                           reaches the total itself, may be NULL),
  *   dweight[c] = sum over rows of dY n     (device fp32 [D]; NULL: not computed).
  * scratch (with dweight): device fp32, 4-byte aligned, pnq_rms_norm_backward_scratch_bytes long; the order of the sums goes by the
- * sizes and the device alone. Types as in the forward call. dX may be dtotal's own buffer where ldd = D, not dY's or the total's (PNQ_ERR_VALUE).
+ * sizes and the device alone. Types as in the forward call. dX may be dtotal's own buffer where ldd = D, and is
+ * otherwise apart from it, and always from dY and the total (PNQ_ERR_VALUE).
  */
 int pnq_rms_norm_backward(int type, const void* dY, int64_t ldy, const void* total, int64_t ldt, int weight_type, const void* weight,
                           const float* rstd, const void* dtotal, int64_t ldd, int64_t rows, int64_t D, void* dX, float* dweight,
