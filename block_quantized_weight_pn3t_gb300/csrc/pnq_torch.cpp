@@ -1019,6 +1019,12 @@ at::Tensor total_of(const NormInputs& n, PyObject* out) {
     return matrix_out(out, "total", n.rows, n.D, n.x.scalar_type(), n.device);
 }
 
+// The total as it is returned: of a norm without a residual x itself, or None where y took x's place (the total is gone then).
+PyObject* returned_total(PyObject* x, const NormInputs& n, PyObject* out, at::Tensor& total, const at::Tensor& y) {
+    if (n.residual.defined()) return returned(out, total);
+    return Py_NewRef(n.rows > 0 && y.defined() && y.data_ptr() == n.x.data_ptr() ? Py_None : x);
+}
+
 PNQ_ENTRY(rms_norm) {
     return entry([&]() -> PyObject* {
         static const char* const names[] = {"x", "weight", "eps", "residual", "out", "total", "stream"};
@@ -1034,7 +1040,7 @@ PNQ_ENTRY(rms_norm) {
                            n.weight.data_ptr(), n.eps, added ? total.data_ptr() : nullptr, y.data_ptr(), rstd.data_ptr<float>(), nullptr, 0,
                            nullptr, place.stream()),
               "pnq_rms_norm");
-        Owned first{returned(a[4], y)}, second{added ? returned(a[5], total) : Py_NewRef(a[0])}, third{wrap(std::move(rstd))};
+        Owned second{returned_total(a[0], n, a[5], total, y)}, first{returned(a[4], y)}, third{wrap(std::move(rstd))};
         return PyTuple_Pack(3, first.o, second.o, third.o);
     });
 }
@@ -1055,7 +1061,7 @@ PNQ_ENTRY(rms_norm_int8) {
                            n.weight.data_ptr(), n.eps, added ? total.data_ptr() : nullptr, y.defined() ? y.data_ptr() : nullptr, nullptr,
                            codes.t.data_ptr<int8_t>(), codes.pitch, scales.data_ptr<float>(), place.stream()),
               "pnq_rms_norm");
-        Owned first{returned(a[5], codes.t)}, second{returned(a[6], scales)}, third{added ? returned(a[7], total) : Py_NewRef(a[0])};
+        Owned first{returned(a[5], codes.t)}, second{returned(a[6], scales)}, third{returned_total(a[0], n, a[7], total, y)};
         return PyTuple_Pack(3, first.o, second.o, third.o);
     });
 }
@@ -1215,10 +1221,12 @@ PyMethodDef methods[] = {
     PNQ_METHOD(rms_norm, "rms_norm(x, weight, eps=1e-6, residual=None, out=None, total=None, stream=None)\n--\n\n"
                          "(y, total, rstd): total = x + residual (x itself without a residual), rstd = 1 / sqrt(mean(total^2) + eps),\n"
                          "y = total * rstd * weight. x, residual: fp32 or bf16 [rows][D], rows may be strided; weight: fp32 or bf16 [D].\n"
-                         "total=residual adds in place, out=x overwrites x. Outside autograd: rms_norm_backward gives the gradients."),
+                         "total=residual adds in place. out=x overwrites x: without a residual the total is gone then, and None is returned for it\n"
+                         "(such a call has no backward pass). Outside autograd: rms_norm_backward gives the gradients."),
     PNQ_METHOD(rms_norm_int8, "rms_norm_int8(x, weight, eps=1e-6, residual=None, y=None, codes=None, scales=None, total=None, stream=None)\n--\n\n"
                               "(codes, scales, total): the norm as 8-bit codes (int8 [rows][D], rows padded to 16 bytes) with a scale per\n"
-                              "row, for int8_gemm. y: a [rows][D] tensor that takes the norm itself too (for a router, say)."),
+                              "row, for int8_gemm. y: a [rows][D] tensor that takes the norm itself too (for a router, say); y=x without a residual\n"
+                              "leaves no total: None."),
     PNQ_METHOD(rms_norm_backward, "rms_norm_backward(dy, total, weight, rstd, dtotal=None, out=None, dweight=None, stream=None)\n--\n\n"
                                   "Gradients of rms_norm: (dx, dweight); dx is the residual's gradient too. dtotal: the gradient that\n"
                                   "reaches the total from elsewhere, added to dx (out=dtotal adds in place; dy and total stay). dweight is fp32."),
