@@ -77,11 +77,18 @@ struct Plan {
     static constexpr int kCols = kCtas == 2 ? 256 : 512;       // tensor-memory columns: two accumulators, and the slots
     static constexpr int kSplit = 8 / CG;                      // the most that share a tile's K: clusters of 8 CTAs
     static constexpr bool kWidenX = WX;                        // a stage holds x's codes; beside every slot of tensor memory there is one of x
-    static int slot(int bn) { return kWidenX ? bn * KS * 2 : 0; }
-    static int stage(int bn) { return kCodes + (kWidenX ? bn * KS : bn / CG * KS * 2); }
-    static int slots(int bn) { return std::min(kMaxSlots, (kCols - 2 * bn) / kSlotCols); }
-    static int stages(int bn) { return std::min(kMaxStages, (kSmemLimit / kCtas - 3072 - slots(bn) * slot(bn)) / stage(bn)); }
-    static int smem(int bn) { return stages(bn) * stage(bn) + slots(bn) * slot(bn) + 1024; }
+    static constexpr int slot(int bn) { return kWidenX ? bn * KS * 2 : 0; }
+    static constexpr int stage(int bn) { return kCodes + (kWidenX ? bn * KS : bn / CG * KS * 2); }
+    static constexpr int slots(int bn) { return std::min(kMaxSlots, (kCols - 2 * bn) / kSlotCols); }
+    static constexpr int stages(int bn) { return std::min(kMaxStages, (kSmemLimit / kCtas - 3072 - slots(bn) * slot(bn)) / stage(bn)); }
+    static constexpr int smem(int bn) { return stages(bn) * stage(bn) + slots(bn) * slot(bn) + 1024; }
+    static constexpr int largest_smem() {
+        int most = 0;
+        for (int bn = kStep; bn <= BN; bn += kStep) most = std::max(most, smem(bn));
+        return most;
+    }
+    // kCtas of them share an SM whatever bn is (1 KB of each CTA is the system's, and the barriers are static)
+    static_assert(kCtas * (largest_smem() + 2048) <= 228 * 1024, "the rings leave no room for the CTAs of an SM");
     // fp32 accumulators, fp16 operands, N, M = 128 per CTA
     static __device__ uint32_t idesc(int bn) {
         return (1u << 4) | (static_cast<uint32_t>(bn >> 3) << 17) | (static_cast<uint32_t>(CG * kRows >> 4) << 24);
@@ -551,11 +558,13 @@ struct Cut {
     int64_t tiles, stages;  // stages: one after the other
 };
 
-// Clusters of CG by ks CTAs of a kernel that the current device holds at once (not every group of SMs divides evenly). The runtime counts one CTA
-// an SM for kernels that allocate tensor memory; two fit where theirs is half of it.
+// Clusters of CG by ks CTAs of a kernel that the current device holds at once (not every group of SMs divides evenly), asked for with the largest
+// tile's shared memory, so that the answer is one for all of them. The runtime counts one CTA an SM for kernels that allocate tensor memory; two fit where
+// theirs is half of it. The kernel that widens x too has the same threads, tensor memory and CTAs an SM, and goes by the same count.
 template <int BN, int CG, int SETS, bool WX>
-cudaError_t resident(int ks, int smem, int* clusters) {
+cudaError_t resident(int ks, int* clusters) {
     using P = Plan<BN, CG, SETS, WX>;
+    constexpr int smem = P::largest_smem();
     static std::mutex mu;
     static std::map<std::pair<int, int>, int> known;
     int dev = 0;
@@ -598,7 +607,7 @@ cudaError_t cut_by(int64_t M, int64_t N, int64_t K, Cut* c) {
     c->stages = (c->tiles * CG + P::kCtas * device_sm_count() - 1) / (P::kCtas * device_sm_count()) * nk;
     for (int ks = 2; ks <= P::kSplit && nk >= 2 * ks; ++ks) {
         int clusters = 0;
-        const cudaError_t e = resident<BN, CG, SETS, WX>(ks, P::smem(c->bn), &clusters);
+        const cudaError_t e = resident<BN, CG, SETS, WX>(ks, &clusters);
         if (e != cudaSuccess) return e;
         const int64_t stages = (nk + ks - 1) / ks + 3;
         if (c->tiles <= clusters && stages < c->stages) c->stages = stages, c->ks = ks;
