@@ -89,10 +89,10 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
     return v;
 }
-// The largest of a warp's values in one instruction (no NaN among them).
+// The largest of a warp's values in one instruction (no NaN among them). Volatile: all lanes have to meet in it where it stands.
 __device__ __forceinline__ float redux_max(float v) {
     float d;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
     return d;
 }
 
