@@ -125,16 +125,22 @@ __device__ __forceinline__ Two inverse(Two a) {  // Newton's step, 2 - a q, from
     return fast_sum(q, __fmul_rn(q, e));
 }
 
+// log 2 in three parts (the reduction of W. J. Cody and W. Waite 1980): its first 17 bits, of which n times (7 bits) is exact, and what is left
+// of it in two floats. kLog2Rest: log 2 less the double kLog2.
+constexpr double kLog2 = 0.6931471805599453094, kLog2Rest = 2.3190468138462996e-17;
+constexpr float kLog2High = static_cast<float>(static_cast<int>(kLog2 * 131072.0) / 131072.0);
+constexpr float kLog2Middle = static_cast<float>(kLog2 - static_cast<double>(kLog2High));
+constexpr float kLog2Low = static_cast<float>(kLog2 - static_cast<double>(kLog2High) - static_cast<double>(kLog2Middle) + kLog2Rest);
+
 // exp(d) for d <= 0: d = n log 2 + r, the series of exp(r) (|r| <= 0.35; terms from r^8 / 8! on weigh below 2^-27, in fp32), times 2^n. Below
 // 2^-125: zero.
 __device__ __forceinline__ Two exp_two(Two d) {
     const bool none = !(d.hi > -86.6f);
     if (none) d = {0.0f, 0.0f};
     const float n = rintf(d.hi * 1.44269504f);
-    // log 2 = 0x1.62e4p-1 + 0x1.7f7d1cp-20 + ..: n times the first part is exact
-    const Two t = two_sum(d.hi, -n * 0x1.62e4p-1f);
-    const float p = __fmul_rn(n, 0x1.7f7d1cp-20f), e = fmaf(n, 0x1.7f7d1cp-20f, -p);
-    const Two r = t + Two{-p, -e} + Two{d.lo, n * -0x1.ef357ap-45f};
+    const Two t = two_sum(d.hi, -n * kLog2High);
+    const float p = __fmul_rn(n, kLog2Middle), e = fmaf(n, kLog2Middle, -p);
+    const Two r = t + Two{-p, -e} + Two{d.lo, n * -kLog2Low};
     constexpr double kInverse[] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040};  // 1 / k!
     const float x = r.hi;
     float high = 1.0f / 479001600;  // r^8 (1 / 8! + r / 9! + r^2 / 10! + r^3 / 11! + r^4 / 12!)
