@@ -77,7 +77,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     wrappers = torch_dir is not None and shutil.which("g++") is not None
     if not wrappers:
         print(f"{'torch' if torch_dir is None else 'g++'} not found: building {os.path.basename(LIB)} without the torch wrappers of "
-              "the 4-bit operands and the expert layer")
+              "the 4-bit operands, the expert layer, the norms and the 8-bit rows and product")
     native = _native_compile(nv, torch_dir) if wrappers else None
     if native is not None:
         jobs.append(native[0])

@@ -6,7 +6,8 @@
 //
 // Which of two scores is the larger must not hang on a rounding. Without bias and groups the logits themselves are compared. Otherwise
 // c is computed in fp32 with a bound on its error (route_kernel), and a row in which two scores that decide anything are nearer than that,
-// and are not of equal logits and equal biases, is done again with scores of some 2^-44 (a few rows in a thousand).
+// and are not of equal logits and equal biases, is done again with scores of some 2^-44 (four tokens in ten thousand of 256 experts with normal logits).
+// Groups near each other are done again even where they are equal: a batch whose logits are all the same, with groups, goes there whole (route_kernel).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -324,10 +325,11 @@ __device__ __forceinline__ void route_again(const RouteArgs& a, int64_t t, const
 // Shared memory of a warp: the row's logits, and behind them the groups' scores (each group on an odd pitch) or the keys above.
 __host__ __device__ inline int route_floats(int E) { return (E + 3) / 4 * 4 * 3 + 32; }
 
-// A warp takes token after token. Tokens with near scores (a few in 16384) are done again by a whole CTA: HERE, where a warp has one token at
+// A warp takes token after token. Tokens with near scores (six of 16384 with normal logits) are done again by a whole CTA: HERE, where a warp has one token at
 // most, at this kernel's end, otherwise by the kernel below. In the loop, by the warp that met them, the code for it alone cost every call 2 to 4
 // us: 16384 x 256 sigmoid by the logits 18.1 us, now 15.6, 4096 x 256 with bias and 8 groups 16.2 and 13.6; 16384 of those 36.9 and 35.0, of which
-// the second kernel is 9 (with 64 experts it takes 1.7 more than it saves). The bias is read once a CTA: by every warp for every token, out of the
+// the second kernel is 9 (with 64 experts it takes 1.7 more than it saves). Where every token is near it takes most of the time: 16384 x 256 equal logits in 8
+// groups 266 us, 4096 of them 46, 12 of 128 experts 28 (random ones 34, 16 and 5; equal logits without groups are ties, not near: 24, 10 and 5). The bias is read once a CTA: by every warp for every token, out of the
 // same few lines of L2, it took more time than all the rest (25 of 45 us then).
 // (Registers for eight CTAs an SM up to 256 experts: a token is a chain of some 3 us. With four CTAs fewer it took 4 to 12 percent longer.)
 template <class T, int NE, int V, bool HERE>
@@ -410,8 +412,9 @@ __global__ void __launch_bounds__(32 * kWarps, NE <= 8 ? 8 : 4) route_kernel(con
         if (bad) {
             id[0] = lane, id[1] = lane + 32;
         } else {
-            // How far two computed scores of different order may be apart. Sigmoid: __expf is within (2 + 1.18 |x|) ulp and s (1 - s) (2 + 1.18 |x|) <= 0.58;
-            // the quotient is within 2 ulp: s within 2.6 * 2^-23, twice that for two. Softmax: an exponential is within 2^-22 of itself
+            // How far two computed scores of different order may be apart. Sigmoid, in units of 2^-23: __expf is within (2 + 1.18 |x|) ulp, which moves s by
+            // s (1 - s) (2 + 1.18 |x|) <= 0.63 (largest at |x| = 0.84); the sum with 1 rounds by half an ulp, 0.5 at most; the quotient is within 2 ulp, 1 where it is
+            // below 1: s within 2.13, two of them 4.26, and the tolerance is 5.5. Softmax: an exponential is within 2^-22 of itself
             // and its argument's rounding adds (m - x) 2^-24; the sum, E / 32 + 5 additions of such, is within 1.5 * 2^-19 and moves a difference by
             // that times the larger score. The addition of the bias rounds by half an ulp of c.
             const float cmax = smax + bmax;

@@ -1237,11 +1237,11 @@ PyMethodDef methods[] = {
                                 "codes * scales, fp32 or bf16 [rows][K]."),
     PNQ_METHOD(int8_gemm, "int8_gemm(x, x_scales, w, w_scales, dtype=torch.float32, out=None, stream=None)\n--\n\n"
                           "Y[m][n] = (sum_k x[m][k] w[n][k]) x_scales[m] w_scales[n] of int8 matrices [M][K] and [N][K] (rows may be\n"
-                          "strided; those of w on 16 bytes, as int8_quantize makes them, are faster), the sum exact; fp32 or bf16\n"
-                          "[M][N]. There is no gradient of it: operands are codes."),
+                          "strided; those of w are wanted on 16 bytes, as int8_quantize makes them: others take several times as long for few rows of x, and\n"
+                          "a copy of w as scratch for more than eight), the sum exact; fp32 or bf16 [M][N]. There is no gradient of it: operands are codes."),
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "Torch wrappers of the 4-bit operands and the expert layer.", -1, methods};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "Torch wrappers of the 4-bit operands, the expert layer, the norms, and the 8-bit rows and product.", -1, methods};
 
 // type(args) goes through vectorcall; tp_new is what a type needs for it.
 PyObject* no_new(PyTypeObject* type, PyObject* args, PyObject* kwargs) {

@@ -93,7 +93,7 @@ enum pnq_status {
     PNQ_ERR_FLAGS = -7,  /* unknown bit in a flags argument */
     PNQ_ERR_SCRATCH = -8, /* the caller's scratch holds less than the call needs (pnq_gemm) */
     PNQ_ERR_VALUE = -9    /* an argument value outside its domain (a global scale that is not finite
-                             and > 0) */
+                             and > 0), or buffers that overlap where they may not */
 };
 
 /* Flags of pnq_gemv_ex. */
@@ -456,8 +456,10 @@ typedef struct pnq_route_rule {
  *   With groups, the top_groups groups of the largest scores stay (ties to the lowest group). ids[t] = the `slots` largest c
  *   of what stays, in that order, ties to the lowest expert. weights[t][j] = scale * s, over the sum of the token's chosen s
  *   if renormalize.
- * Scores are compared as they are, not as they round: without bias and groups by the logits, otherwise to some 2^-44 of themselves where fp32 does not
- * decide (exponentials below 2^-125 count as 0). Equal ones go by the logit, then by the index. Finite biases: |bias| up to about 1e38.
+ * Scores are compared as they are, not as they round: without bias and groups by the logits, otherwise, where fp32 does not decide, by s to some 2^-44 of
+ * itself (exponentials below 2^-125 count as 0) and c to 2^-46 of itself besides: where the bias cancels s, c is known to 2^-44 of s, not of
+ * itself. Equal ones go by the logit, then by the index. Finite biases: |bias| up to about 1e38. Tokens that fp32 does not
+ * decide, and those whose last group in and first group out tie (equal logits, as in padding), take some 5 us each more, many at a time.
  * An expert whose logit or bias is -infinity is out: it is not chosen and adds nothing to its group. A slot for which no expert is left
  * has the id -1 and the weight 0 (pnq_expert_sort drops it): a row of -infinities, a padded token, takes part in nothing. A token
  * with a NaN logit, with a softmax logit of +infinity, or for whose choice scores the bias is a NaN or +infinity, has the ids 0 .. slots
@@ -495,7 +497,7 @@ int pnq_expert_route_backward(int type, const float* dweights, const void* logit
  *           127 p / max|p|, ties to even. A row of zeros has the scale 0 (NaN where eps is 0, as y is); a row with a NaN or an infinity (of t, w or p) has the scale NaN and codes of
  *           zero, so that what is computed from it is NaN.
  * type: PNQ_F32 or PNQ_BF16, of X, residual, total and y (row strides in elements); weight: device [D], PNQ_F32 or PNQ_BF16 of its own.
- * Sums of squares are fp32 (|t| up to about 1e18); rows on 16 bytes with D a multiple of 8 are faster. Errors: PNQ_ERR_TYPE,
+ * Sums of squares are fp32 (|t| up to about 1e18; with eps = 0 a root mean square from about 1e-18 on); t w is formed before r. Rows on 16 bytes with D a multiple of 8 are faster. Errors: PNQ_ERR_TYPE,
  * PNQ_ERR_SHAPE (D < 1, a stride below D, a pitch that is not a multiple of 16), PNQ_ERR_VALUE (eps negative or not finite, buffers that overlap),
  * PNQ_ERR_NULL (codes without scales, or nothing to write), PNQ_ERR_ALIGN, PNQ_ERR_CUDA.
  */
@@ -532,7 +534,9 @@ int pnq_int8_dequantize(const int8_t* codes, int64_t pitch, const float* scales,
  * The sum is exact: Y is the same bit for bit whatever M is and whichever kernel takes the call. X: int8, row m at m * ldx bytes;
  * W: int8, row n at n * ldw bytes (-128 .. 127 all count); 1 <= K <= 131071 (sums within 32 bits). M, N >= 0; a zero one launches nothing.
  * Y: [M][N] contiguous, fp32 or bf16. scratch: device, 16-byte aligned, as many bytes as pnq_int8_gemm_scratch_bytes gives for
- * the same arguments (NULL where that is 0: few rows of X); overwritten. Rows of W on 16 bytes with ldw a multiple of 16 are faster.
+ * the same arguments (NULL where that is 0: few rows of X); overwritten. Rows of W are wanted on 16 bytes, ldw a multiple of 16: others are read
+ * byte by byte, and for more than eight rows of X copied to scratch (N K bytes) in every call (17408 x 5121: one row 97 us, 21 on 16 bytes; 33 rows 105
+ * and 26).
  * Errors: PNQ_ERR_TYPE, PNQ_ERR_SHAPE, PNQ_ERR_NULL, PNQ_ERR_ALIGN (scales, Y, scratch), PNQ_ERR_SCRATCH, PNQ_ERR_CUDA.
  */
 int pnq_int8_gemm(const int8_t* X, int64_t ldx, const float* x_scales, int64_t M, const int8_t* W, int64_t ldw, const float* w_scales,
