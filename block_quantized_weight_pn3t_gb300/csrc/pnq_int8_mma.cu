@@ -80,7 +80,7 @@ struct Plan {
     static constexpr int slot(int bn) { return kWidenX ? bn * KS * 2 : 0; }
     static constexpr int stage(int bn) { return kCodes + (kWidenX ? bn * KS : bn / CG * KS * 2); }
     static constexpr int slots(int bn) { return std::min(kMaxSlots, (kCols - 2 * bn) / kSlotCols); }
-    static constexpr int stages(int bn) { return std::min(kMaxStages, (kSmemLimit / kCtas - 3072 - slots(bn) * slot(bn)) / stage(bn)); }
+    static constexpr int stages(int bn) { return std::min(kMaxStages, (kSmemLimit / kCtas - 3 * 1024 - slots(bn) * slot(bn)) / stage(bn)); }
     static constexpr int smem(int bn) { return stages(bn) * stage(bn) + slots(bn) * slot(bn) + 1024; }
     static constexpr int largest_smem() {
         int most = 0;
